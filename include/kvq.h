@@ -304,6 +304,173 @@ kvq_status kvq_set_row_slices(kvq_cache* cache, int slices);
  * evenly. */
 kvq_status kvq_set_split_rows(kvq_cache* cache, int rows);
 
+/* ------------------------------------------------------------------------
+ * Paged cache.  No passage: the pages describe rows of one sequence side by
+ * side; these calls hold the same block formats in pages that tables share
+ * out, for a server whose sequences grow, share prefixes and come and go.
+ *
+ * The caller owns the page pool, the tables and the lengths.  A sequence is a
+ * row of page numbers (its table) and a length; logical row r lies in page
+ * table[r / page_rows].  Tables (int32 [n_seq][max_pages]), lengths (int32
+ * [n_seq]) and every other index array are DEVICE arrays, read when the
+ * kernels run, so a captured graph follows what they then hold.  A length
+ * counts the rows including those the call itself appends or whose queries it
+ * takes: an append of T rows writes logical rows [len - T, len), and the T
+ * query rows of a decode sit at positions len - T .. len - 1.  Rollback is a
+ * smaller length.  Nothing but the named rows is written.
+ *
+ * Layout.  Pool: [n_pages][n_kv_heads][page_rows / 16] cells; a cell holds 16
+ * rows of one KV head in the order in which tensor-core fragments take them.
+ * NB = head_dim / 32; row t of a cell: h = t / 8, j = (t % 8) / 2, s = t % 2;
+ * element e: b = e / 32, g = (e % 32) / 4, r = e % 4, c = (e % 32) / 8;
+ * n = h * NB + b, lane = 4 g + j.  Byte offsets in a cell:
+ *   K code      (b/2)*1024 + t*64 + c*16 + (b%2)*8 + e%8
+ *               (q8_0: the int8 code + 128; E4M3: the byte)
+ *   q8_0 d      512 NB + (j*NB + b)*8 + (2h + s)*2                     fp16
+ *   q5_1 codes  u16 at 544 NB + (n/4)*512 + lane*16 + (n%4)*4 + s*2: bits
+ *               5r..5r+4 the code of r = 0, 1, 2, bit 15 bit 4 of r = 3; bits
+ *               0..3 of r = 3 in nibble n%2 of byte
+ *               800 NB + (n/4)*128 + lane*4 + s*2 + (n%4)/2
+ *   q5_1 d, m   864 NB + (j*NB + b)*16 + (2h + s)*2, and + 8           fp16
+ *   E4M3 V      512 NB + (n/2)*512 + lane*16 + (n%2)*8 + r*2 + s
+ * A cell is 928 NB bytes (58 per 32 elements, as in the flat cache) or 1024 NB.
+ *
+ * Errors.  A page number outside the pool or a length above max_pages *
+ * page_rows sets the device error word to 1: appends skip the row, decodes
+ * take a bad page's rows as masked and a bad sequence as empty.  A query row
+ * that sees no row (a sequence of length 0, a position below 0) gives zeros,
+ * with or without a sink.  Calls on one cache share its workspace: order them
+ * on one stream (captured graphs that share a cache included). */
+typedef struct kvq_paged_config {
+    int n_pages;         /* pages in the pool                                     */
+    int page_rows;       /* rows per page: 16, 32, 64, 128 or 256                 */
+    int n_kv_heads;      /* Hkv: 1..128                                           */
+    int head_dim;        /* D: 64, 128 or 256                                     */
+    int max_q_heads;     /* largest Hq (a multiple of Hkv, at most 128 x Hkv)     */
+    int max_seqs;        /* most sequences one call takes (1..1024)               */
+    int max_pages;       /* entries of a sequence's table; max_pages * page_rows  */
+                         /* at most 2^24                                          */
+    int max_t;           /* largest T of a decode (1..64); appends have no limit  */
+    kvq_fmt k_fmt;       /* KVQ_Q8_0 with KVQ_Q5_1, or KVQ_FP8_E4M3 twice         */
+    kvq_fmt v_fmt;
+    int bounds;          /* 1: appends keep key bounds per page (kvq_paged_select) */
+    int rope_dim;        /* leading elements of a head that the append rotates: 0 */
+                         /* or a multiple of 16 up to head_dim                    */
+    int rope_interleaved;/* 0: pairs (i, i + rope_dim/2); 1: pairs (2i, 2i+1)     */
+    double rope_base;    /* angle of pair i at position p: p * base^(-2i/rope_dim) */
+} kvq_paged_config;
+
+/* Device bytes the caller provides (each 16-byte aligned): pool, bounds (0
+ * without cfg.bounds), workspace (the error word, decode partials, page
+ * scores).  Pool bytes need no initial value. */
+typedef struct kvq_paged_sizes {
+    size_t pool, bounds, workspace;
+    size_t page_bytes, cell_bytes;
+} kvq_paged_sizes;
+
+typedef struct kvq_paged kvq_paged;
+
+kvq_status kvq_paged_required_bytes(const kvq_paged_config* cfg, kvq_paged_sizes* out);
+
+/* Build a paged cache over caller buffers and enqueue on `stream` the clearing
+ * of the workspace's error word.  rope_freq: HOST array of rope_dim / 2
+ * radians per position that replaces base^(-2i/rope_dim) (scaled or stretched
+ * rotations), or NULL; copied.  bounds may be NULL without cfg.bounds. */
+kvq_status kvq_paged_alloc(const kvq_paged_config* cfg, void* pool, void* bounds, void* workspace,
+                           const double* rope_freq, void* stream, kvq_paged** out);
+void kvq_paged_free(kvq_paged* cache);
+
+/* Append with the rotation applied on the way.  k, v: device [rows][Hkv][D]
+ * of dtype, consecutive rows k_stride / v_stride elements apart (a multiple of
+ * 8; Hkv * D when dense; a fused projection's slices are taken as they lie).
+ * Without `starts` entry i of n has T rows, rows = n * T.  With `starts`
+ * (device int32 [n + 1], non-decreasing) entry i has rows starts[i] ..
+ * starts[i+1] - 1 of the `rows` there are; rows outside [starts[0], starts[n])
+ * are neither read nor written.  Keys are rotated by their position in fp32
+ * (angles kept to 2^-24 of a turn) and quantised from fp32; values only
+ * quantised.  q (or NULL): device [rows][Hq][D] of dtype, q_stride apart,
+ * rotated likewise into q_out, dense [rows][Hq][D]; q_out may be q when q is
+ * dense.  With cfg.bounds the bounds of the pages that got rows are renewed
+ * from all rows below the length. */
+kvq_status kvq_paged_append(kvq_paged* cache, const void* k, long long k_stride, const void* v, long long v_stride,
+                            const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,
+                            const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,
+                            void* stream);
+
+/* Rows back as values: entry i's last T rows (or its rows by `starts`, as in
+ * the append) into k_out, v_out, dense [rows][Hkv][D] of dtype, rounded once.
+ * A row below 0 or in a bad page gives zeros (the latter sets the error
+ * word). */
+kvq_status kvq_paged_read(kvq_paged* cache, void* k_out, void* v_out, kvq_dtype dtype, const int* tables,
+                          const int* lens, int n_seq, int T, const int* starts, int rows, void* stream);
+
+/* Arguments that the decodes share.  q: device dense [n_seq][T][Hq][D] of
+ * dtype; out the same shape and type (bf16 queries give bf16 outputs).  Row t
+ * sees logical rows [max(0, p + 1 - window), p + 1), p = len - T + t (window
+ * 0: all).  scale <= 0 selects 1/sqrt(D); softcap > 0 caps scaled scores to
+ * softcap * tanh(s / softcap); sinks: device f32 [Hq] or NULL, logits that
+ * join max and denominator without a value. */
+typedef struct kvq_paged_query {
+    const void* q;
+    void* out;
+    kvq_dtype dtype;
+    int n_seq, T, n_q_heads;
+    const int* tables;
+    const int* lens;
+    const float* sinks;
+    float scale, softcap;
+    int window;
+} kvq_paged_query;
+
+/* Decode attention over the pages.  f32 queries keep f32 accuracy (products
+ * split in two parts); bf16 queries round probabilities and values to fp16
+ * inside, sums are f32 throughout. */
+kvq_status kvq_paged_decode(kvq_paged* cache, const kvq_paged_query* a, void* stream);
+
+/* The same result for a batch in which groups of sequences share a prefix,
+ * whose rows are read once a group instead of once a sequence.  Group i is
+ * sequences group_start[i] .. group_start[i+1] - 1 (device int32
+ * [n_groups + 1], non-decreasing, inside [0, n_seq]); their first
+ * prefix_len[i] rows are the same and are taken from the first member's table
+ * (the prefix may end inside a page).  Sequences outside the groups have no
+ * shared rows.  n_groups <= n_seq. */
+kvq_status kvq_paged_decode_shared(kvq_paged* cache, const kvq_paged_query* a, const int* group_start,
+                                   const int* prefix_len, int n_groups, void* stream);
+
+/* Key bounds.  For each page, KV head and 32-element block over the rows below
+ * the length: the smallest and largest dequantised key of each element, as
+ * codes floor(min / ds) and ceil(max / ds) within +-127 of ds = max|key| *
+ * (1/127) (f32 operations; zero codes when ds is 0).  Buffer: int8 [n_pages][Hkv][NB][2][32] (min,
+ * max), then f32 ds [n_pages][Hkv][NB].  Appends do this themselves; the call
+ * is for pages filled in another way: it renews those that hold the last T
+ * rows of each entry (or its rows by `starts`). */
+kvq_status kvq_paged_bounds(kvq_paged* cache, const int* tables, const int* lens, int n_seq, int T, const int* starts,
+                            int rows, void* stream);
+
+/* Choose pages by their bounds.  For each sequence, query row t and KV head:
+ * the query is coded per block (dq = amax * (1/127), c = rint(x * ((1/amax) *
+ * 127)), f32 operations), and a page scores max over the KV head's queries of sum over blocks, in order,
+ * of (dq ds) * sum_i (c_i > 0 ? c_i max_i : c_i min_i), in f32: an upper bound
+ * of the coded query's products with the page's keys, and the same on every
+ * run.  Pages: device int32 [n_seq][T][Hkv][keep] receives, ascending, the
+ * first n_first and last n_last pages of those with a visible row and then the
+ * best scored, ties to the lower index, -1 behind the last.  Uses q, dtype,
+ * n_seq, T, n_q_heads, tables and lens of `a`.  Needs n_first, n_last >= 0,
+ * n_first + n_last <= keep, n_seq * T <= 2048. */
+kvq_status kvq_paged_select(kvq_paged* cache, const kvq_paged_query* a, int* pages, int keep, int n_first, int n_last,
+                            void* stream);
+
+/* Decode attention over the listed pages only: entries are indexes into the
+ * sequence's table as kvq_paged_select gives them; negative ones are skipped,
+ * a repeated one counts as often as it stands there.  window must be 0;
+ * n_seq * T <= 2048. */
+kvq_status kvq_paged_decode_sparse(kvq_paged* cache, const kvq_paged_query* a, const int* pages, int keep,
+                                   void* stream);
+
+/* Synchronise `stream`, read the device error word into *err (0 = none, 1 = a
+ * page number or length out of range, 2 = a bounded wait ran out), clear it. */
+kvq_status kvq_paged_read_error(kvq_paged* cache, int* err, void* stream);
+
 /* Bytes per 32-element block of a format: 34 (q8_0), 24 (q5_1) or 32
  * (FP8 E4M3); -1 if unknown ("Module cache", fn kv_blk_bytes). */
 int kvq_block_bytes(kvq_fmt fmt);

@@ -28,6 +28,9 @@ EXPORTS = (
     "kvq_decode_noalloc", "kvq_truncate", "kvq_truncate_device", "kvq_sync_len", "kvq_get_len", "kvq_note_replayed", "kvq_ring_headroom",
     "kvq_physical_rows", "kvq_read_device_error", "kvq_set_split_rows", "kvq_set_row_slices", "kvq_set_decode_path",
     "kvq_set_softcap",
+    "kvq_paged_required_bytes", "kvq_paged_alloc", "kvq_paged_free", "kvq_paged_append", "kvq_paged_read",
+    "kvq_paged_bounds", "kvq_paged_decode", "kvq_paged_decode_shared", "kvq_paged_select", "kvq_paged_decode_sparse",
+    "kvq_paged_read_error",
     "kvq_block_bytes", "kvq_bytes_per_token", "kvq_last_error",
 )
 
@@ -53,6 +56,23 @@ class kvq_sizes(ctypes.Structure):
                 ("rows", ctypes.c_int), ("k_row_bytes", ctypes.c_int), ("v_row_bytes", ctypes.c_int)]
 
 
+class kvq_paged_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "n_pages", "page_rows", "n_kv_heads", "head_dim", "max_q_heads", "max_seqs", "max_pages", "max_t", "k_fmt",
+        "v_fmt", "bounds", "rope_dim", "rope_interleaved")] + [("rope_base", ctypes.c_double)]
+
+
+class kvq_paged_sizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("pool", "bounds", "workspace", "page_bytes", "cell_bytes")]
+
+
+class kvq_paged_query(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_seq", ctypes.c_int),
+                ("T", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("sinks", ctypes.c_void_p), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int)]
+
+
 _LIB = None
 
 
@@ -66,6 +86,8 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         IP = ctypes.POINTER(ctypes.c_int)
+        LL, DP = ctypes.c_longlong, ctypes.POINTER(ctypes.c_double)
+        QP = ctypes.POINTER(kvq_paged_query)
         sig = {
             "kvq_required_bytes": (I, [ctypes.POINTER(kvq_config), ctypes.POINTER(kvq_sizes)]),
             "kvq_alloc": (I, [ctypes.POINTER(kvq_config), P, P, P, P, P, ctypes.POINTER(P)]),
@@ -85,6 +107,17 @@ def lib():
             "kvq_set_row_slices": (I, [P, I]),
             "kvq_set_decode_path": (I, [P, I, I]),
             "kvq_set_softcap": (I, [P, ctypes.c_float]),
+            "kvq_paged_required_bytes": (I, [ctypes.POINTER(kvq_paged_config), ctypes.POINTER(kvq_paged_sizes)]),
+            "kvq_paged_alloc": (I, [ctypes.POINTER(kvq_paged_config), P, P, P, DP, P, ctypes.POINTER(P)]),
+            "kvq_paged_free": (None, [P]),
+            "kvq_paged_append": (I, [P, P, LL, P, LL, P, LL, P, I, I, P, P, I, I, P, I, P]),
+            "kvq_paged_read": (I, [P, P, P, I, P, P, I, I, P, I, P]),
+            "kvq_paged_bounds": (I, [P, P, P, I, I, P, I, P]),
+            "kvq_paged_decode": (I, [P, QP, P]),
+            "kvq_paged_decode_shared": (I, [P, QP, P, P, I, P]),
+            "kvq_paged_select": (I, [P, QP, P, I, I, I, P]),
+            "kvq_paged_decode_sparse": (I, [P, QP, P, I, P]),
+            "kvq_paged_read_error": (I, [P, IP, P]),
             "kvq_block_bytes": (I, [I]),
             "kvq_bytes_per_token": (S, [ctypes.POINTER(kvq_config)]),
             "kvq_last_error": (ctypes.c_char_p, []),
@@ -201,6 +234,69 @@ def kvq_set_decode_path(handle, path, query_bits=0):
 
 def kvq_set_softcap(handle, softcap):
     _check(lib().kvq_set_softcap(handle, float(softcap)))
+
+
+# -- paged cache: device addresses as integers, queries as a kvq_paged_query
+
+def make_paged_config(n_pages, page_rows, n_kv_heads, head_dim, max_q_heads, max_seqs, max_pages, max_t=1,
+                      k_fmt=KVQ_Q8_0, v_fmt=KVQ_Q5_1, bounds=0, rope_dim=0, rope_interleaved=0, rope_base=10000.0):
+    return kvq_paged_config(n_pages, page_rows, n_kv_heads, head_dim, max_q_heads, max_seqs, max_pages, max_t, k_fmt,
+                            v_fmt, int(bool(bounds)), rope_dim, int(bool(rope_interleaved)), float(rope_base))
+
+
+def kvq_paged_required_bytes(cfg):
+    out = kvq_paged_sizes()
+    _check(lib().kvq_paged_required_bytes(ctypes.byref(cfg), ctypes.byref(out)))
+    return out
+
+
+def kvq_paged_alloc(cfg, pool, bounds, workspace, rope_freq=None, stream=0):
+    h = ctypes.c_void_p()
+    freq = None
+    if rope_freq is not None:
+        freq = (ctypes.c_double * len(rope_freq))(*[float(x) for x in rope_freq])
+    _check(lib().kvq_paged_alloc(ctypes.byref(cfg), pool, bounds, workspace, freq, stream, ctypes.byref(h)))
+    return h
+
+
+def kvq_paged_free(handle):
+    lib().kvq_paged_free(handle)
+
+
+def kvq_paged_append(handle, k, k_stride, v, v_stride, q, q_stride, q_out, n_q_heads, dtype, tables, lens, n_seq, T,
+                     starts, rows, stream=0):
+    _check(lib().kvq_paged_append(handle, k, k_stride, v, v_stride, q, q_stride, q_out, n_q_heads, dtype, tables, lens,
+                                  n_seq, T, starts, rows, stream))
+
+
+def kvq_paged_read(handle, k_out, v_out, dtype, tables, lens, n_seq, T, starts, rows, stream=0):
+    _check(lib().kvq_paged_read(handle, k_out, v_out, dtype, tables, lens, n_seq, T, starts, rows, stream))
+
+
+def kvq_paged_bounds(handle, tables, lens, n_seq, T, starts, rows, stream=0):
+    _check(lib().kvq_paged_bounds(handle, tables, lens, n_seq, T, starts, rows, stream))
+
+
+def kvq_paged_decode(handle, query, stream=0):
+    _check(lib().kvq_paged_decode(handle, ctypes.byref(query), stream))
+
+
+def kvq_paged_decode_shared(handle, query, group_start, prefix_len, n_groups, stream=0):
+    _check(lib().kvq_paged_decode_shared(handle, ctypes.byref(query), group_start, prefix_len, n_groups, stream))
+
+
+def kvq_paged_select(handle, query, pages, keep, n_first, n_last, stream=0):
+    _check(lib().kvq_paged_select(handle, ctypes.byref(query), pages, keep, n_first, n_last, stream))
+
+
+def kvq_paged_decode_sparse(handle, query, pages, keep, stream=0):
+    _check(lib().kvq_paged_decode_sparse(handle, ctypes.byref(query), pages, keep, stream))
+
+
+def kvq_paged_read_error(handle, stream=0):
+    e = ctypes.c_int()
+    _check(lib().kvq_paged_read_error(handle, ctypes.byref(e), stream))
+    return e.value
 
 
 def kvq_block_bytes(fmt):

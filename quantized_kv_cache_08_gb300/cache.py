@@ -159,3 +159,233 @@ class KVCache:
         n = self.n_seq * self.rows * self.v_tok
         v = self.v_plane[:n].view(self.n_seq, self.rows, self.v_tok)
         return v[seq, phys_lo:phys_hi]
+
+
+def _token_rows(t, heads, dim, name):
+    """Address and row stride (in elements) of [..., heads, dim] rows that lie
+    evenly apart in memory (dense, or slices of a wider projection)."""
+    if t.shape[-2] != heads or t.shape[-1] != dim:
+        raise ValueError(f"{name} shape {tuple(t.shape)} does not match the cache")
+    st = t.stride()
+    if t.numel() and (st[-1] != 1 or (heads > 1 and st[-2] != dim)):
+        raise ValueError(f"{name} needs each row's heads side by side")
+    if t.dim() == 3:
+        stride = st[0] if t.shape[0] > 1 else heads * dim
+    else:
+        n, T = t.shape[0], t.shape[1]
+        stride = st[1] if T > 1 else st[0] if n > 1 else heads * dim
+        if n > 1 and T > 1 and st[0] != T * st[1]:
+            raise ValueError(f"{name} rows must lie evenly apart")
+    return t.data_ptr(), stride
+
+
+class PagedKVCache:
+    """One attention layer's cache in pages: a pool of `n_pages` pages of
+    `page_rows` rows, in the formats of KVCache.  The caller keeps, as int32
+    CUDA tensors, a table of page numbers per sequence ([n, max_pages]) and the
+    lengths ([n], counting the rows that a call appends or whose queries it
+    takes), and passes both to every call; all calls read them on the device.
+
+    rope_dim > 0: `append` rotates the first rope_dim elements of each head of
+    its keys (and queries) by their positions.  rope_freq gives rope_dim / 2
+    radians per position in place of rope_base^(-2i / rope_dim).  bounds: keep
+    key bounds per page, which `select` scores.  pool and bounds_buf take over
+    existing uint8 CUDA tensors of `sizes.pool` and `sizes.bounds` bytes."""
+
+    def __init__(self, n_pages, page_rows, n_kv_heads, head_dim, max_q_heads, max_seqs, max_pages, max_t=1,
+                 fmt="q8_0/q5_1", rope_dim=0, rope_base=10000.0, rope_interleaved=False, rope_freq=None, bounds=False,
+                 pool=None, bounds_buf=None, device=None, stream=None):
+        self.handle = None
+        if fmt not in KVCache.FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(KVCache.FORMATS)}")
+        k_fmt, v_fmt, _, _ = KVCache.FORMATS[fmt]
+        self.fmt = fmt
+        if rope_freq is not None and len(rope_freq) != rope_dim // 2:
+            raise ValueError("rope_freq needs rope_dim / 2 values")
+        self.cfg = B.make_paged_config(n_pages, page_rows, n_kv_heads, head_dim, max_q_heads, max_seqs, max_pages,
+                                       max_t, k_fmt, v_fmt, bounds, rope_dim, rope_interleaved, rope_base)
+        self.sizes = sz = B.kvq_paged_required_bytes(self.cfg)
+        if device is None:
+            device = pool.device if pool is not None else "cuda"
+        dev = torch.device(device)
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        self.n_kv_heads, self.head_dim, self.max_pages = n_kv_heads, head_dim, max_pages
+        self.pool = self._buffer(pool, sz.pool, "pool")
+        self.bounds = self._buffer(bounds_buf, sz.bounds, "bounds_buf") if bounds else None
+        self.workspace = torch.empty(sz.workspace, dtype=torch.uint8, device=dev)
+        with torch.cuda.device(dev):
+            self.handle = B.kvq_paged_alloc(self.cfg, self.pool.data_ptr(),
+                                            self.bounds.data_ptr() if bounds else None, self.workspace.data_ptr(),
+                                            rope_freq, _stream_handle(stream))
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None:
+            B.kvq_paged_free(h)
+            self.handle = None
+
+    def _buffer(self, t, size, name):
+        if t is None:
+            return torch.empty(size, dtype=torch.uint8, device=self.device)
+        if t.dtype != torch.uint8 or t.numel() != size or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous uint8 tensor of {size} bytes on {self.device}")
+        return t
+
+    def _dev(self, t, name):
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}")
+
+    def _ints(self, t, shape, name):
+        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on {self.device}")
+        return t.data_ptr()
+
+    def _batch(self, tables, lens):
+        n = lens.shape[0] if lens.dim() == 1 else -1
+        return n, self._ints(tables, (n, self.max_pages), "tables"), self._ints(lens, (n,), "lens")
+
+    def _rows(self, t, n, starts, name):
+        """T, address of starts, rows of a [n, T, H, D] or packed [rows, H, D] tensor."""
+        if starts is None:
+            if t.dim() != 4 or t.shape[0] != n:
+                raise ValueError(f"{name} must be [n, T, heads, dim] without starts")
+            return t.shape[1], None, n * t.shape[1]
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [rows, heads, dim] with starts")
+        return 0, self._ints(starts, (n + 1,), "starts"), t.shape[0]
+
+    def _call(self, fn, *args, stream):
+        if torch.cuda.current_device() == self.device.index:
+            fn(self.handle, *args, _stream_handle(stream))
+        else:
+            with torch.cuda.device(self.device):
+                fn(self.handle, *args, _stream_handle(stream))
+
+    def _new(self, shape, dtype, stream):
+        out = torch.empty(shape, dtype=dtype, device=self.device)
+        if stream is not None:
+            out.record_stream(stream)
+        return out
+
+    def append(self, k, v, tables, lens, starts=None, q=None, q_out=None, stream=None):
+        """k, v: float32/bfloat16 [n, T, Hkv, D], or packed [rows, Hkv, D] with
+        starts (int32 [n + 1]).  q (same form, any number of heads) is rotated
+        into q_out (made if None; q itself when dense), which is returned."""
+        n, tp, lp = self._batch(tables, lens)
+        if k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must have one shape and dtype")
+        self._dev(k, "k")
+        self._dev(v, "v")
+        T, sp, rows = self._rows(k, n, starts, "k")
+        kp, ks = _token_rows(k, self.n_kv_heads, self.head_dim, "k")
+        vp, vs = _token_rows(v, self.n_kv_heads, self.head_dim, "v")
+        qp, qs, op, hq = None, 0, None, 0
+        if q is not None:
+            hq = q.shape[-2]
+            if q.dtype != k.dtype or q.shape[:-2] != k.shape[:-2]:
+                raise ValueError("q must have k's rows and dtype")
+            self._dev(q, "q")
+            qp, qs = _token_rows(q, hq, self.head_dim, "q")
+            if q_out is None:
+                q_out = self._new(q.shape, q.dtype, stream)
+            if q_out.dtype != q.dtype or q_out.shape != q.shape or not q_out.is_contiguous():
+                raise ValueError("q_out must be contiguous with q's shape and dtype")
+            self._dev(q_out, "q_out")
+            op = q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        self._call(B.kvq_paged_append, kp, ks, vp, vs, qp, qs, op, hq, _dtype_code(k), tp, lp, n, T, sp, rows,
+                   stream=stream)
+        return q_out
+
+    def read(self, tables, lens, k_out, v_out, starts=None, stream=None):
+        """Each entry's last rows as values into k_out, v_out: float32/bfloat16
+        [n, T, Hkv, D], or packed [rows, Hkv, D] with starts."""
+        n, tp, lp = self._batch(tables, lens)
+        if k_out.shape != v_out.shape or k_out.dtype != v_out.dtype:
+            raise ValueError("k_out and v_out must have one shape and dtype")
+        if k_out.shape[-2:] != (self.n_kv_heads, self.head_dim):
+            raise ValueError(f"k_out shape {tuple(k_out.shape)} does not match the cache")
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            self._dev(t, name)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        T, sp, rows = self._rows(k_out, n, starts, "k_out")
+        self._call(B.kvq_paged_read, k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out), tp, lp, n, T, sp, rows,
+                   stream=stream)
+
+    def update_bounds(self, tables, lens, T, stream=None):
+        """Renew the key bounds of the pages that hold each sequence's last T
+        rows (appends do this; for pages filled in another way)."""
+        n, tp, lp = self._batch(tables, lens)
+        self._call(B.kvq_paged_bounds, tp, lp, n, T, None, n * T, stream=stream)
+
+    def _query(self, q, tables, lens, sinks, scale, window, softcap, out, stream):
+        n, tp, lp = self._batch(tables, lens)
+        _check_dev(q, "q")
+        self._dev(q, "q")
+        if q.dim() != 4 or q.shape[0] != n or q.shape[3] != self.head_dim:
+            raise ValueError(f"q shape {tuple(q.shape)} does not match the cache and lens")
+        if out is None:
+            out = self._new(q.shape, q.dtype, stream)
+        elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous with q's shape and dtype")
+        self._dev(out, "out")
+        sk = None
+        if sinks is not None:
+            _check_dev(sinks, "sinks")
+            self._dev(sinks, "sinks")
+            if sinks.dtype != torch.float32 or sinks.numel() != q.shape[2]:
+                raise ValueError("sinks must be float32 [Hq]")
+            sk = sinks.data_ptr()
+        return out, B.kvq_paged_query(q.data_ptr(), out.data_ptr(), _dtype_code(q), n, q.shape[1], q.shape[2], tp, lp,
+                                      sk, scale, softcap, window)
+
+    def decode(self, q, tables, lens, sinks=None, scale=0.0, window=0, softcap=0.0, out=None, stream=None):
+        """q: float32/bfloat16 [n, T, Hq, D], the last T rows of each sequence;
+        returns the attention outputs in q's shape and dtype."""
+        out, a = self._query(q, tables, lens, sinks, scale, window, softcap, out, stream)
+        self._call(B.kvq_paged_decode, a, stream=stream)
+        return out
+
+    def decode_shared(self, q, tables, lens, group_start, prefix_lens, sinks=None, scale=0.0, window=0, softcap=0.0,
+                      out=None, stream=None):
+        """decode for a batch whose sequences group_start[i] .. group_start[i+1]
+        share their first prefix_lens[i] rows, read once a group (int32 CUDA
+        tensors [groups + 1] and [groups])."""
+        out, a = self._query(q, tables, lens, sinks, scale, window, softcap, out, stream)
+        g = prefix_lens.numel()
+        self._call(B.kvq_paged_decode_shared, a, self._ints(group_start, (g + 1,), "group_start"),
+                   self._ints(prefix_lens, (g,), "prefix_lens"), g, stream=stream)
+        return out
+
+    def select(self, q, tables, lens, keep, n_first=1, n_last=1, pages=None, stream=None):
+        """Indexes into each table of the `keep` pages that each query row and
+        KV head reads: int32 [n, T, Hkv, keep], ascending, -1 behind the last."""
+        if pages is None:
+            pages = self._new((q.shape[0], q.shape[1], self.n_kv_heads, keep), torch.int32, stream)
+        out, a = self._query(q, tables, lens, None, 0.0, 0, 0.0, q, stream)
+        self._call(B.kvq_paged_select, a, self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"),
+                   keep, n_first, n_last, stream=stream)
+        return pages
+
+    def decode_sparse(self, q, tables, lens, pages, sinks=None, scale=0.0, softcap=0.0, out=None, stream=None):
+        """decode over the listed pages only (int32 [n, T, Hkv, keep])."""
+        out, a = self._query(q, tables, lens, sinks, scale, 0, softcap, out, stream)
+        keep = pages.shape[-1]
+        self._call(B.kvq_paged_decode_sparse, a,
+                   self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"), keep, stream=stream)
+        return out
+
+    def device_error(self, stream=None):
+        """0, or 1: a page number or length out of range, 2: a wait ran out (read and cleared)."""
+        e = None
+
+        def read(handle, s):
+            nonlocal e
+            e = B.kvq_paged_read_error(handle, s)
+
+        self._call(read, stream=stream)
+        return e

@@ -2,6 +2,7 @@
 // lengths, ring bookkeeping, workspace layout and kernel launches.  See
 // include/kvq.h for the contract of every entry point.
 #include "../../include/kvq.h"
+#include "kvq_error.h"
 #include "kvq_internal.cuh"
 
 #include <algorithm>
@@ -43,9 +44,9 @@ struct kvq_cache {
     std::vector<int> len_lo;
 };
 
-namespace {
+static thread_local std::string g_err;
 
-thread_local std::string g_err;
+namespace kvq {
 
 kvq_status fail(kvq_status st, const char* fmt, ...) {
     char buf[512];
@@ -60,6 +61,10 @@ kvq_status fail(kvq_status st, const char* fmt, ...) {
 kvq_status cuda_fail(cudaError_t e, const char* what) {
     return fail(KVQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+}  // namespace kvq
+
+namespace {
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

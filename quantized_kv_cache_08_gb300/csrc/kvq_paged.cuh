@@ -1,0 +1,182 @@
+// Declarations shared by the paged-cache translation units: geometry, the cell
+// layout (include/kvq.h), parameter blocks and launchers.
+#pragma once
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+namespace paged {
+
+constexpr int kCellRows = 16;
+constexpr int kMaxFreq = 128;          // rope_dim / 2 at most
+constexpr int kMaxSeqs = 1024;
+constexpr int kMaxEntries = 2048;      // work entries of one decode
+
+struct Geom {
+    uint8_t* pool;
+    int* err;
+    int n_pages, page_rows, page_shift, max_pages;
+    int Hkv, D, fp8;
+    int cell_bytes;
+    long long page_bytes;
+    __host__ __device__ int NB() const { return D / 32; }
+    __host__ __device__ int cells_per_page() const { return page_rows / kCellRows; }
+};
+
+// Rows of the batch entries: uniform (T each) or packed by starts
+struct Rows {
+    const int* tables;
+    const int* lens;
+    const int* starts;
+    int n_seq, T, rows;
+};
+
+// Where a packed row lies: the byte of its cell for KV head 0 (heads are
+// cells_per_page() cells apart) and its row in the cell; cell < 0: nowhere.
+struct Place {
+    long long cell;
+    int pos, t;
+    int first;             // position of the entry's first row of this call
+    int len;
+};
+
+#ifdef __CUDACC__
+// Byte of a page for a position of a sequence, or -1 with the error word set
+__device__ __forceinline__ long long page_at(const Geom& g, const int* table, int pos) {
+    const int pg = table[pos >> g.page_shift];
+    if (pg < 0 || pg >= g.n_pages) {
+        atomicExch(g.err, kErrCounter);
+        return -1;
+    }
+    return pg * g.page_bytes;
+}
+
+__device__ __forceinline__ Place place_row(const Geom& g, const Rows& r, int row, bool short_is_error) {
+    Place p{-1, -1, 0, 0, 0};
+    int i, n, at;
+    if (r.starts) {
+        if (row < r.starts[0] || row >= r.starts[r.n_seq]) return p;
+        int lo = 0, hi = r.n_seq;                  // the last entry that starts at or before the row
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (r.starts[mid] <= row) lo = mid;
+            else hi = mid;
+        }
+        i = lo;
+        at = row - r.starts[i];
+        n = r.starts[i + 1] - r.starts[i];
+    } else {
+        i = row / r.T;
+        at = row - i * r.T;
+        n = r.T;
+    }
+    p.len = r.lens[i];
+    if (p.len < 0 || p.len > (long long)g.max_pages << g.page_shift || (short_is_error && p.len < n)) {
+        atomicExch(g.err, kErrCounter);
+        p.pos = -2;
+        return p;
+    }
+    p.first = max(p.len - n, 0);
+    p.pos = p.len - n + at;
+    if (p.pos < 0) return p;
+    const long long pg = page_at(g, r.tables + (long long)i * g.max_pages, p.pos);
+    if (pg < 0) return p;
+    p.cell = pg + (long long)((p.pos & (g.page_rows - 1)) >> 4) * g.cell_bytes;
+    p.t = p.pos & 15;
+    return p;
+}
+#endif
+
+// Rotation frequencies in turns per position, as a sum of two floats
+struct Freqs {
+    float2 f[kMaxFreq];
+};
+
+struct AppendArgs {
+    Geom g;
+    Rows r;
+    const void* k;
+    const void* v;
+    const void* q;
+    void* q_out;
+    long long k_stride, v_stride, q_stride;
+    int Hq, bf16, rope_dim, interleaved;
+};
+cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cudaStream_t s);
+
+struct ReadArgs {
+    Geom g;
+    Rows r;
+    void* k_out;
+    void* v_out;
+    int bf16;
+};
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t s);
+
+struct BoundsArgs {
+    Geom g;
+    Rows r;
+    int8_t* codes;         // [n_pages][Hkv][NB][2][32]
+    float* scales;         // [n_pages][Hkv][NB]
+};
+cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t s);
+
+struct SelectArgs {
+    Geom g;
+    const int8_t* codes;
+    const float* scales;
+    const void* q;
+    int bf16, n_seq, T, Hq, hpk;
+    const int* tables;
+    const int* lens;
+    int* pages;            // [n_seq][T][Hkv][keep]
+    uint32_t* keys;        // [n_seq][T][Hkv][max_pages] scores as ordered integers
+    int keep, n_first, n_last;
+};
+cudaError_t launch_select(const SelectArgs& a, cudaStream_t s);
+
+struct PlanEntry;
+
+// Decode.  Work entries: sequences (dense), sequences then prefix groups
+// (shared), or (sequence, query row) pairs (sparse).  An entry has nc cells,
+// nq queries per KV head taken in slices of QPI, and its work is nc * slices *
+// Hkv cells; the CTAs cut the total into equal ranges.  The part of a CTA's
+// range inside one (entry, KV head, slice) key is a fragment and writes its
+// record to slot cta + key.
+struct SplitArgs {
+    Geom g;
+    const void* q;
+    void* out;
+    int bf16;
+    int n_seq, T, Hq, hpk;
+    const int* tables;
+    const int* lens;
+    const float* sinks;
+    float qscale;                  // scale * log2(e)
+    float softcap_a, softcap_b;    // log2 units: s -> b * tanh(a * s); b == 0: off
+    int window;
+    const int* group_start;        // shared: prefix groups
+    const int* prefix_len;
+    int n_groups;
+    const int* lists;              // sparse: [n_seq][T][Hkv][keep]
+    int keep;
+    int E;                         // work entries
+    int G;                         // CTAs of the split kernel
+    int rec_rows;                  // query rows of a record: min(QPI, most queries of a key)
+    long long max_keys;            // keys that the record area holds beside the CTAs' own
+    float* part_o;                 // [slot][rec_rows][D]
+    float* part_ml;                // [slot][rec_rows][2]  (max in log2 units, sum)
+    struct PlanEntry* plan;        // [E + 1], written by CTA 0 for the merge
+};
+// Work before an entry (cells x slices), keys before it (slices), its cells and
+// the first of them; entry E holds the totals.
+struct PlanEntry {
+    long long work;
+    int keys, nc, c0, pad;
+};
+int split_queries(const SplitArgs& a);                    // QPI of the kernel a call would use
+cudaError_t launch_split(const SplitArgs& a, cudaStream_t s);
+cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s);
+
+}  // namespace paged
+}  // namespace kvq

@@ -1,0 +1,418 @@
+// Paged cache: append with the position rotation applied on the way, rows read
+// back as values, and the key bounds of pages.
+//
+// Append.  A group of D / 8 lanes takes one head row of one token, 8 elements a
+// lane; four lanes hold a 32-element block.  Queries and keys are rotated in
+// registers (the partner half comes by shuffles, so queries may be rotated in
+// place), keys become q8_0 codes, values q5_1 codes, or both E4M3 bytes, and go
+// to their places in the page's cell.  The angles of a CTA's tokens are worked
+// out once into shared memory and serve all heads.
+//
+// Angles.  With f in turns per position held as f_hi + f_lo (48 bits), p f_hi
+// splits exactly into a rounded product and its error (fma), the whole turns
+// drop out exactly, and the rest is added: the angle is good to 2^-24 of a turn
+// at any position below 2^24, where p f in one fp32 product would be off by
+// p 2^-24 radians.
+#include "kvq_paged.cuh"
+#include "kvq_quant.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+namespace kvq {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+__device__ __forceinline__ void load8(const void* base, long long idx, int bf16, float (&x)[8]) {
+    if (bf16) {
+        const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + idx);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + idx);
+        const float4 a = p[0], b = p[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+}
+
+__device__ __forceinline__ void store8(void* base, long long idx, int bf16, const float (&x)[8]) {
+    if (bf16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + idx) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + idx);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// fp16 of the exact quotient num / den (num >= 0; den 127 or 31), to nearest
+// even in one rounding.  The fp32 quotient decides unless it lies within a few
+// of its own steps of a midpoint between two halves (low 13 bits near 0x1000),
+// or is so small that the half is subnormal; then fp64 does.  `lo` is what num
+// as a float leaves out.
+__device__ __forceinline__ unsigned short half_quotient(float num, double exact_num, float den) {
+    const float q = __fdiv_rn(num, den);
+    const unsigned low = __float_as_uint(q) & 0x1fffu;
+    if (q < 6.2e-5f || (low >= 0x0ff8u && low <= 0x1008u))
+        return __half_as_ushort(__double2half(exact_num / (double)den));
+    return __half_as_ushort(__float2half_rn(q));
+}
+
+// Rotate the 8 elements e0.. of a head row; cs: (cos, sin) of the token's pairs.
+// Every lane of the warp calls this (shuffles).
+__device__ __forceinline__ void rotate8(float (&x)[8], int e0, int rot, int interleaved, const float2* cs, int lane) {
+    if (rot == 0) return;
+    if (interleaved) {
+        if (e0 < rot) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = cs[e0 / 2 + i];
+                const float p = x[2 * i], q = x[2 * i + 1];
+                x[2 * i] = p * a.x - q * a.y;
+                x[2 * i + 1] = p * a.y + q * a.x;
+            }
+        }
+        return;
+    }
+    const int half = rot / 2;
+    const bool second = e0 >= half;
+    const int from = e0 < rot ? lane + (second ? -half / 8 : half / 8) : lane;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
+    if (e0 < rot) {
+        const float2* c = cs + (second ? e0 - half : e0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = second ? y[i] * c[i].y + x[i] * c[i].x : x[i] * c[i].x - y[i] * c[i].y;
+    }
+}
+
+// One append CTA: tokens [TT blockIdx.x, + TT), row units blockIdx.y, + gridDim.y..
+// A unit is 32 / LR heads of one kind (query, key, value) of one token.
+template <int LR>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
+    extern __shared__ float2 s_cs[];               // [TT][rope_dim / 2]
+    __shared__ Place s_place[16];
+    constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row0 = blockIdx.x * TT;
+    const int half = a.rope_dim / 2;
+    if (tid < TT) {
+        Place p{-1, -1, 0, 0, 0};
+        if (row0 + tid < a.r.rows) p = place_row(a.g, a.r, row0 + tid, true);
+        s_place[tid] = p;
+    }
+    __syncthreads();
+    for (int i = tid; i < TT * half; i += kThreads) {
+        const int tt = i / half, pr = i - tt * half;
+        const float p = (float)max(s_place[tt].pos, 0);
+        const float2 f = fq.f[pr];
+        const float t = p * f.x;
+        const float e = fmaf(p, f.x, -t);
+        const float turn = (t - rintf(t)) + fmaf(p, f.y, e);
+        float sn, cs;
+        sincospif(2.f * turn, &sn, &cs);
+        s_cs[i] = make_float2(cs, sn);
+    }
+    __syncthreads();
+    const int uq = a.q ? (a.Hq + JPW - 1) / JPW : 0, uk = (a.g.Hkv + JPW - 1) / JPW;
+    const int units = uq + 2 * uk;
+    const int li = lane % LR, e0 = 8 * li;
+    for (int w = blockIdx.y * kWarps + warp; w < units * TT; w += gridDim.y * kWarps) {
+        const int tt = w / units;
+        int u = w - tt * units;
+        const Place pl = s_place[tt];
+        if (pl.pos < 0) continue;                  // the same for the whole warp
+        const float2* cs = s_cs + tt * half;
+        const long long row = row0 + tt;
+        if (u < uq) {
+            const int h = u * JPW + lane / LR;
+            const bool on = h < a.Hq;
+            float x[8] = {};
+            if (on) load8(a.q, row * a.q_stride + h * D + e0, a.bf16, x);
+            rotate8(x, e0, a.rope_dim, a.interleaved, cs, lane);
+            if (on) store8(a.q_out, (row * a.Hq + h) * D + e0, a.bf16, x);
+            continue;
+        }
+        u -= uq;
+        const bool is_v = u >= uk;
+        const int h = (is_v ? u - uk : u) * JPW + lane / LR;
+        const bool on = h < a.g.Hkv && pl.cell >= 0;
+        float x[8] = {};
+        if (on) load8(is_v ? a.v : a.k, row * (is_v ? a.v_stride : a.k_stride) + h * D + e0, a.bf16, x);
+        uint8_t* cell = a.g.pool + pl.cell + (long long)h * a.g.cells_per_page() * a.g.cell_bytes;
+        const int t = pl.t, b = li >> 2, c = li & 3;
+        const int j = (t & 7) >> 1, s = t & 1, hh = t >> 3;
+        const int n = hh * NB + b, i4 = 2 * hh + s;
+        if (!is_v) {
+            rotate8(x, e0, a.rope_dim, a.interleaved, cs, lane);
+            uint32_t w2[2] = {0u, 0u};
+            if (a.g.fp8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w2[i >> 2] |= (uint32_t)__nv_cvt_float_to_fp8(x[i], __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
+            } else {
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const unsigned short db = half_quotient(m, (double)m, 127.f);
+                const float d = __half2float(__ushort_as_half(db));
+                const float inv = d > 0.f ? 1.0f / d : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int code = d > 0.f ? q8_code(x[i], d, inv) : 0;
+                    w2[i >> 2] |= (uint32_t)(code + 128) << (8 * (i & 3));
+                }
+                if (on && c == 0)
+                    *reinterpret_cast<unsigned short*>(cell + 512 * NB + (j * NB + b) * 8 + i4 * 2) = db;
+            }
+            if (on) *reinterpret_cast<uint2*>(cell + (b >> 1) * 1024 + t * 64 + c * 16 + (b & 1) * 8) = make_uint2(w2[0], w2[1]);
+            continue;
+        }
+        if (a.g.fp8) {
+            uint8_t* p = cell + 512 * NB + (n >> 1) * 512 + (n & 1) * 8 + s;
+            if (on) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    p[(4 * (2 * c + (i >> 2)) + j) * 16 + (i & 3) * 2] =
+                        __nv_cvt_float_to_fp8(x[i], __NV_SATFINITE, __NV_E4M3);
+            }
+            continue;
+        }
+        float mn = x[0], mx = x[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            mn = fminf(mn, x[i]);
+            mx = fmaxf(mx, x[i]);
+        }
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const unsigned short db = half_quotient(mx - mn, (double)mx - (double)mn, 31.f);
+        const unsigned short mb = __half_as_ushort(__float2half_rn(mn));
+        const float d = __half2float(__ushort_as_half(db)), m = __half2float(__ushort_as_half(mb));
+        const float inv = d > 0.f ? 1.0f / d : 0.f;
+        uint32_t unit[2], nib[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint32_t code[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) code[r] = d > 0.f ? (uint32_t)q5_code(x[4 * e + r], m, d, inv) : 0u;
+            unit[e] = code[0] | (code[1] << 5) | (code[2] << 10) | ((code[3] >> 4) << 15);
+            nib[e] = code[3] & 15u;
+        }
+        // nibbles of blocks b and b + 1 share a byte: the even block's lane
+        // writes the byte of g = 2c, the odd block's that of g = 2c + 1
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, (b & 1) ? nib[0] : nib[1], 4);
+        if (on) {
+            uint8_t* dm = cell + 864 * NB + (j * NB + b) * 16 + i4 * 2;
+            if (c == 0) *reinterpret_cast<unsigned short*>(dm) = db;
+            if (c == 1) *reinterpret_cast<unsigned short*>(dm + 8) = mb;
+            uint8_t* up = cell + 544 * NB + (n >> 2) * 512 + (n & 3) * 4 + s * 2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<unsigned short*>(up + (4 * (2 * c + e) + j) * 16) = (unsigned short)unit[e];
+            const int ne = n & ~1;                 // n is even where b is
+            const int g = 2 * c + (b & 1);
+            const uint32_t byte = (b & 1) ? (other | (nib[1] << 4)) : (nib[0] | (other << 4));
+            cell[800 * NB + (ne >> 2) * 128 + (4 * g + j) * 4 + s * 2 + ((ne & 3) >> 1)] = (uint8_t)byte;
+        }
+    }
+}
+
+// The 8 elements of lane li's K (or V) of row t of a cell, as f32
+template <int NB>
+__device__ __forceinline__ void read_k8(const uint8_t* cell, int fp8, int t, int b, int c, float (&x)[8]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(cell + (b >> 1) * 1024 + t * 64 + c * 16 + (b & 1) * 8);
+    const uint32_t w2[2] = {w.x, w.y};
+    if (fp8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw((w2[i >> 2] >> (8 * (i & 3))) & 255u, __NV_E4M3)));
+        return;
+    }
+    const int j = (t & 7) >> 1, i4 = 2 * (t >> 3) + (t & 1);
+    const float d = __half2float(*reinterpret_cast<const __half*>(cell + 512 * NB + (j * NB + b) * 8 + i4 * 2));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)((int)((w2[i >> 2] >> (8 * (i & 3))) & 255u) - 128) * d;
+}
+
+template <int NB>
+__device__ __forceinline__ void read_v8(const uint8_t* cell, int fp8, int t, int b, int c, float (&x)[8]) {
+    const int j = (t & 7) >> 1, s = t & 1, hh = t >> 3, n = hh * NB + b, i4 = 2 * hh + s;
+    if (fp8) {
+        const uint8_t* p = cell + 512 * NB + (n >> 1) * 512 + (n & 1) * 8 + s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(p[(4 * (2 * c + (i >> 2)) + j) * 16 + (i & 3) * 2], __NV_E4M3)));
+        return;
+    }
+    const uint8_t* dm = cell + 864 * NB + (j * NB + b) * 16 + i4 * 2;
+    const float d = __half2float(*reinterpret_cast<const __half*>(dm)), m = __half2float(*reinterpret_cast<const __half*>(dm + 8));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int ln = 4 * (2 * c + e) + j;
+        const uint32_t unit = *reinterpret_cast<const unsigned short*>(cell + 544 * NB + (n >> 2) * 512 + ln * 16 + (n & 3) * 4 + s * 2);
+        const uint32_t nb = (cell[800 * NB + (n >> 2) * 128 + ln * 4 + s * 2 + ((n & 3) >> 1)] >> (4 * (n & 1))) & 15u;
+        const uint32_t u[4] = {unit & 31u, (unit >> 5) & 31u, (unit >> 10) & 31u, ((unit >> 15) << 4) | nb};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * e + r] = fmaf((float)u[r], d, m);
+    }
+}
+
+// Rows back as values: LR lanes a (row, KV head), K and V both.
+template <int LR>
+__global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
+    constexpr int D = LR * 8, NB = D / 32;
+    const long long w = (long long)blockIdx.x * (kThreads / LR) + threadIdx.x / LR;
+    const int row = (int)(w / a.g.Hkv), h = (int)(w - (long long)row * a.g.Hkv);
+    if (row >= a.r.rows) return;
+    const Place p = place_row(a.g, a.r, row, false);
+    if (a.r.starts && (row < a.r.starts[0] || row >= a.r.starts[a.r.n_seq])) return;
+    const int li = threadIdx.x % LR, b = li >> 2, c = li & 3;
+    float k[8] = {}, v[8] = {};
+    if (p.cell >= 0) {
+        const uint8_t* cell = a.g.pool + p.cell + (long long)h * a.g.cells_per_page() * a.g.cell_bytes;
+        read_k8<NB>(cell, a.g.fp8, p.t, b, c, k);
+        read_v8<NB>(cell, a.g.fp8, p.t, b, c, v);
+    }
+    const long long at = ((long long)row * a.g.Hkv + h) * D + 8 * li;
+    store8(a.k_out, at, a.bf16, k);
+    store8(a.v_out, at, a.bf16, v);
+}
+
+// Key bounds: one warp per (row, KV head, pair of blocks) whose row is the
+// first of this call in its page; it goes over the page's rows below the length
+// 8 at a time (lane = row in the eight, 16 elements).
+template <int NB>
+__global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsArgs a) {
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int per = a.g.Hkv * (NB / 2);
+    const int row = (int)(w / per), rest = (int)(w - (long long)row * per);
+    const int h = rest / (NB / 2), bp = rest - h * (NB / 2);
+    if (row >= a.r.rows) return;
+    const Place p = place_row(a.g, a.r, row, false);
+    if (p.cell < 0) return;
+    const int in = p.pos & (a.g.page_rows - 1);
+    if (in != 0 && p.pos != p.first) return;
+    const int valid = min(a.g.page_rows, p.len - (p.pos - in));
+    const long long page = (p.cell - (long long)(in >> 4) * a.g.cell_bytes) / a.g.page_bytes;
+    const uint8_t* cell0 = a.g.pool + page * a.g.page_bytes + (long long)h * a.g.cells_per_page() * a.g.cell_bytes;
+    const int g8 = lane >> 2, c = lane & 3;
+    float mn[16], mx[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        mn[i] = __builtin_huge_valf();
+        mx[i] = -__builtin_huge_valf();
+    }
+    for (int r = g8; r < valid; r += 8) {
+        const uint8_t* cell = cell0 + (long long)(r >> 4) * a.g.cell_bytes;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x[8];
+            read_k8<NB>(cell, a.g.fp8, r & 15, 2 * bp + e, c, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                mn[8 * e + i] = fminf(mn[8 * e + i], x[i]);
+                mx[8 * e + i] = fmaxf(mx[8 * e + i], x[i]);
+            }
+        }
+    }
+    float am[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            mn[i] = fminf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], o));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+        }
+        am[i >> 3] = fmaxf(am[i >> 3], fmaxf(fabsf(mn[i]), fabsf(mx[i])));
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        am[e] = fmaxf(am[e], __shfl_xor_sync(0xffffffffu, am[e], 1));
+        am[e] = fmaxf(am[e], __shfl_xor_sync(0xffffffffu, am[e], 2));
+        const int b = 2 * bp + e;
+        const float ds = __fmul_rn(am[e], 1.0f / 127.0f);
+        const long long at = (page * a.g.Hkv + h) * NB + b;
+        if (g8 == 0) {
+            uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
+            if (ds > 0.f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float l = fminf(fmaxf(floorf(__fdiv_rn(mn[8 * e + i], ds)), -127.f), 127.f);
+                    const float u = fminf(fmaxf(ceilf(__fdiv_rn(mx[8 * e + i], ds)), -127.f), 127.f);
+                    lo[i >> 2] |= ((uint32_t)(int)l & 255u) << (8 * (i & 3));
+                    hi[i >> 2] |= ((uint32_t)(int)u & 255u) << (8 * (i & 3));
+                }
+            }
+            int8_t* dst = a.codes + at * 64 + 8 * c;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(dst + 32) = make_uint2(hi[0], hi[1]);
+            if (c == 0) a.scales[at] = ds;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cudaStream_t s) {
+    const int jpw = 256 / a.g.D;
+    const int units = (a.q ? (a.Hq + jpw - 1) / jpw : 0) + 2 * ((a.g.Hkv + jpw - 1) / jpw);
+    // tokens per CTA: the angles are shared by its heads; few rows spread over
+    // the SMs by heads instead
+    const int TT = a.r.rows >= 8 * num_sms ? 4 : 1;
+    const int gx = (a.r.rows + TT - 1) / TT;
+    const int most = (units * TT + kWarps - 1) / kWarps;
+    const int gy = std::max(1, std::min(most, (2 * num_sms + gx - 1) / gx));
+    const size_t smem = (size_t)TT * (a.rope_dim / 2) * sizeof(float2);
+    const dim3 grid((unsigned)gx, (unsigned)gy);
+    if (a.g.D == 64) append_kernel<8><<<grid, kThreads, smem, s>>>(a, f, TT);
+    else if (a.g.D == 128) append_kernel<16><<<grid, kThreads, smem, s>>>(a, f, TT);
+    else append_kernel<32><<<grid, kThreads, smem, s>>>(a, f, TT);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t s) {
+    const int lr = a.g.D / 8;
+    const long long groups = (long long)a.r.rows * a.g.Hkv;
+    const unsigned grid = (unsigned)((groups + kThreads / lr - 1) / (kThreads / lr));
+    if (lr == 8) read_kernel<8><<<grid, kThreads, 0, s>>>(a);
+    else if (lr == 16) read_kernel<16><<<grid, kThreads, 0, s>>>(a);
+    else read_kernel<32><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t s) {
+    const int nb = a.g.NB();
+    const long long warps = (long long)a.r.rows * a.g.Hkv * (nb / 2);
+    const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
+    if (nb == 2) bounds_kernel<2><<<grid, kThreads, 0, s>>>(a);
+    else if (nb == 4) bounds_kernel<4><<<grid, kThreads, 0, s>>>(a);
+    else bounds_kernel<8><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace kvq
