@@ -249,11 +249,11 @@ kvq_status kvq_paged_append(kvq_paged* c, const void* k, long long k_stride, con
                             const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,
                             void* stream) {
     if (!c) return fail(KVQ_EINVAL, "cache is NULL");
-    if (!k || !v) return fail(KVQ_EINVAL, "k or v is NULL");
     if (dtype != KVQ_F32 && dtype != KVQ_BF16) return fail(KVQ_EINVAL, "dtype must be f32 or bf16");
     AppendArgs a = {};
     kvq_status st = check_rows(c, tables, lens, n_seq, T, starts, rows, &a.r);
-    if (st != KVQ_OK) return st;
+    if (st != KVQ_OK || rows == 0) return st;
+    if (!k || !v) return fail(KVQ_EINVAL, "k or v is NULL");
     const long long kvd = (long long)c->cfg.n_kv_heads * c->cfg.head_dim;
     if ((st = check_stride("k", k, k_stride, kvd)) != KVQ_OK) return st;
     if ((st = check_stride("v", v, v_stride, kvd)) != KVQ_OK) return st;
@@ -264,7 +264,6 @@ kvq_status kvq_paged_append(kvq_paged* c, const void* k, long long k_stride, con
         if ((st = check_stride("q", q, q_stride, qd)) != KVQ_OK) return st;
         if (q_out == q && q_stride != qd) return fail(KVQ_EINVAL, "q is rotated in place only when it is dense");
     }
-    if (rows == 0) return KVQ_OK;
     a.g = c->g;
     a.k = k;
     a.v = v;
@@ -286,12 +285,12 @@ kvq_status kvq_paged_append(kvq_paged* c, const void* k, long long k_stride, con
 kvq_status kvq_paged_read(kvq_paged* c, void* k_out, void* v_out, kvq_dtype dtype, const int* tables, const int* lens,
                           int n_seq, int T, const int* starts, int rows, void* stream) {
     if (!c) return fail(KVQ_EINVAL, "cache is NULL");
-    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
-        return fail(KVQ_EINVAL, "k_out or v_out is NULL or not 16-byte aligned");
     if (dtype != KVQ_F32 && dtype != KVQ_BF16) return fail(KVQ_EINVAL, "dtype must be f32 or bf16");
     ReadArgs a = {};
     kvq_status st = check_rows(c, tables, lens, n_seq, T, starts, rows, &a.r);
     if (st != KVQ_OK || rows == 0) return st;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+        return fail(KVQ_EINVAL, "k_out or v_out is NULL or not 16-byte aligned");
     a.g = c->g;
     a.k_out = k_out;
     a.v_out = v_out;
