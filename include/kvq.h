@@ -373,7 +373,7 @@ typedef struct kvq_paged kvq_paged;
 kvq_status kvq_paged_required_bytes(const kvq_paged_config* cfg, kvq_paged_sizes* out);
 
 /* Build a paged cache over caller buffers and enqueue on `stream` the clearing
- * of the workspace's error word.  rope_freq: HOST array of rope_dim / 2
+ * of the workspace's error word and counters.  rope_freq: HOST array of rope_dim / 2
  * radians per position that replaces base^(-2i/rope_dim) (scaled or stretched
  * rotations), or NULL; copied.  bounds may be NULL without cfg.bounds. */
 kvq_status kvq_paged_alloc(const kvq_paged_config* cfg, void* pool, void* bounds, void* workspace,

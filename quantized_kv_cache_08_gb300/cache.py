@@ -257,11 +257,13 @@ class PagedKVCache:
         return 0, self._ints(starts, (n + 1,), "starts"), t.shape[0]
 
     def _call(self, fn, *args, stream):
-        if torch.cuda.current_device() == self.device.index:
-            fn(self.handle, *args, _stream_handle(stream))
+        index = self.device.index
+        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        if torch._C._cuda_getDevice() == index:
+            fn(self.handle, *args, s)
         else:
-            with torch.cuda.device(self.device):
-                fn(self.handle, *args, _stream_handle(stream))
+            with torch.cuda.device(index):
+                fn(self.handle, *args, s)
 
     def _new(self, shape, dtype, stream):
         out = torch.empty(shape, dtype=dtype, device=self.device)
@@ -329,10 +331,13 @@ class PagedKVCache:
         if q.dim() != 4 or q.shape[0] != n or q.shape[3] != self.head_dim:
             raise ValueError(f"q shape {tuple(q.shape)} does not match the cache and lens")
         if out is None:
-            out = self._new(q.shape, q.dtype, stream)
+            out = torch.empty_like(q)
+            if stream is not None:
+                out.record_stream(stream)
         elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous with q's shape and dtype")
-        self._dev(out, "out")
+        else:
+            self._dev(out, "out")
         sk = None
         if sinks is not None:
             _check_dev(sinks, "sinks")

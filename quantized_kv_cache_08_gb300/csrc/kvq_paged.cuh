@@ -163,6 +163,8 @@ struct SplitArgs {
     int E;                         // work entries
     int G;                         // CTAs of the split kernel
     int rec_rows;                  // query rows of a record: min(QPI, most queries of a key)
+    int fuse;                      // 1: the last CTA of a key joins its records (no merge kernel)
+    int* arrived;                  // [key] records written; 0 between calls
     long long max_keys;            // keys that the record area holds beside the CTAs' own
     float* part_o;                 // [slot][rec_rows][D]
     float* part_ml;                // [slot][rec_rows][2]  (max in log2 units, sum)

@@ -16,7 +16,7 @@ struct kvq_paged {
     Geom g;
     int num_sms;
     uint8_t* ws;
-    size_t off_plan, off_ml, off_o, off_keys, key_rows;
+    size_t off_plan, off_arrived, off_ml, off_o, off_keys, key_rows;
     int8_t* codes;
     float* scales;
     Freqs freqs;
@@ -31,7 +31,7 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned16(const void* p) { return ((size_t)p & 15) == 0; }
 
 struct Layout {
-    size_t cell, page, pool, bounds, plan, ml, o, keys, total, key_rows;
+    size_t cell, page, pool, bounds, plan, arrived, ml, o, keys, total, key_rows;
 };
 
 kvq_status layout(const kvq_paged_config* c, Layout* l) {
@@ -66,7 +66,8 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     l->key_rows = (size_t)c->n_kv_heads * c->max_seqs * (round_up(Qh, 16) + Qh + 16);
     const size_t recs = (size_t)kMaxGrid * 16 + l->key_rows;
     l->plan = 256;                                       // the error word comes first
-    l->ml = round_up(l->plan + (kMaxEntries + 1) * sizeof(PlanEntry), 256);
+    l->arrived = round_up(l->plan + (kMaxEntries + 1) * sizeof(PlanEntry), 256);
+    l->ml = round_up(l->arrived + l->key_rows * sizeof(int), 256);
     l->o = round_up(l->ml + recs * 8, 256);
     l->keys = round_up(l->o + recs * D * 4, 256);
     l->total = l->keys;
@@ -158,12 +159,14 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.rec_rows = std::min(qpi, most);
     a.max_keys = (long long)(c->key_rows / a.rec_rows);
     a.plan = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan);
+    a.arrived = reinterpret_cast<int*>(c->ws + c->off_arrived);
+    a.fuse = n_groups == 0;
     a.part_ml = reinterpret_cast<float*>(c->ws + c->off_ml);
     a.part_o = reinterpret_cast<float*>(c->ws + c->off_o);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_split(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode split kernel");
-    e = launch_merge(a, s);
+    if (!a.fuse) e = launch_merge(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode merge kernel");
     return KVQ_OK;
 }
@@ -210,8 +213,9 @@ kvq_status kvq_paged_alloc(const kvq_paged_config* cfg, void* pool, void* bounds
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-    e = cudaMemsetAsync(workspace, 0, 256, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(error word)");
+    // the error word, and the counters that every decode leaves at zero
+    e = cudaMemsetAsync(workspace, 0, l.ml, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace)");
     kvq_paged* c = new (std::nothrow) kvq_paged();
     if (!c) return fail(KVQ_ERANGE, "out of host memory");
     c->cfg = *cfg;
@@ -230,6 +234,7 @@ kvq_status kvq_paged_alloc(const kvq_paged_config* cfg, void* pool, void* bounds
     c->num_sms = sms;
     c->ws = static_cast<uint8_t*>(workspace);
     c->off_plan = l.plan;
+    c->off_arrived = l.arrived;
     c->off_ml = l.ml;
     c->off_o = l.o;
     c->off_keys = l.keys;

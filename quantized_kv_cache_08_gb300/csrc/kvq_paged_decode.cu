@@ -24,6 +24,7 @@
 // needs as many again for each 4 queries.
 //
 // Work is cut stream-K fashion: see kvq_paged.cuh.
+#include "kvq_device.cuh"
 #include "kvq_paged.cuh"
 
 #include <cuda_bf16.h>
@@ -37,11 +38,16 @@ namespace kvq {
 namespace paged {
 namespace {
 
-constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLazy = 8.0f;          // log2 units a score may pass the reference
+using dev::kLazy;
+using dev::kNegInf;
 constexpr float kShift = 6.0f;         // p is held as 2^6 p: fp16 keeps 2^-20 of the largest in full
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kMaxStages = 8;
+constexpr int kCombine = 4;            // warps' sums that the join holds at once
+
+// Warps of a CTA (one CTA an SM): as many as the accumulators leave registers
+// for; 12 of 168 registers at head_dim 128.
+template <int NB>
+constexpr int warps_of() { return NB == 2 ? 16 : NB == 4 ? 12 : 8; }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -437,20 +443,121 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, const uint8_t* __r
     }
 }
 
-// shared memory of the split kernel
+// Shared memory of the split kernel: query fragments, the join's sums, the
+// plan, then a ring of `stages` cells per warp.
 template <int NB, bool HL>
 struct Smem {
     static constexpr int D = NB * 32;
     static constexpr size_t qs = (size_t)(D / 16) * 512;
-    static constexpr size_t comb = (size_t)(kWarps / 2) * (HL ? 8 : 16) * D * 4;
-    static size_t total(int E) { return qs + comb + (size_t)(E + 1) * sizeof(PlanEntry); }
+    static constexpr size_t comb = (size_t)kCombine * (HL ? 8 : 16) * D * 4;
+    __host__ __device__ static size_t ring(int E) { return (qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
 };
 
-template <int NB, bool F8, bool HL>
-__global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
+// Bounded wait for a stage; false once any wait of the CTA has run out.
+__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    if (dev::mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (dev::mbar_try_sleep(bar, parity, 20000u)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > (1LL << 31)) {
+            atomicExch(err, kErrWait);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+// A part of a CTA's range: key kk (KV head kh, slice sl) of entry e, cells [ca, cb)
+struct Fragment {
+    int e, kk, kh, sl, nsl, nq, c0, ca, cb, keys;
+};
+__device__ __forceinline__ Fragment fragment_at(const PlanEntry* plan, const SplitArgs& a, int QPI, long long x, long long x1) {
+    Fragment f;
+    f.e = find_entry(plan, a.E, x / a.g.Hkv);
+    const PlanEntry pe = plan[f.e];
+    const long long rel = x - pe.work * a.g.Hkv;
+    f.kk = (int)(rel / pe.nc);
+    f.ca = (int)(rel - (long long)f.kk * pe.nc);
+    f.cb = (int)min((long long)pe.nc, f.ca + (x1 - x));
+    f.nq = pe.pad;
+    f.nsl = (pe.pad + QPI - 1) / QPI;
+    f.kh = f.kk / f.nsl;
+    f.sl = f.kk - f.kh * f.nsl;
+    f.c0 = pe.c0;
+    f.keys = pe.keys;
+    return f;
+}
+
+// CTAs whose ranges meet a key: [first, last]; G ranges of W in all
+__device__ __forceinline__ int cta_of(long long x, int G, long long W) { return (int)(((x + 1) * G - 1) / W); }
+
+// The sums of one output row over records first + key .. last + key
+template <int NB>
+struct RowSum {
+    float M, L, o[NB];
+};
+template <int NB>
+__device__ __forceinline__ void fold_records(const SplitArgs& a, long long slot0, int n_rec, int rr, int lane, RowSum<NB>& r) {
     constexpr int D = NB * 32;
+    for (int base = 0; base < n_rec; base += 32) {
+        const int n = min(32, n_rec - base);
+        float2 ml = make_float2(kNegInf, 0.f);
+        if (lane < n) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + ((slot0 + base + lane) * a.rec_rows + rr) * 2));
+        float m = ml.x;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+        m = fmaxf(m, r.M);
+        if (m == kNegInf) continue;
+        const float al = r.M == kNegInf ? 0.f : ex2(r.M - m);
+        r.M = m;
+        const float w = ml.x == kNegInf ? 0.f : ex2(ml.x - m);
+        float l = ml.y * w;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+        r.L = r.L * al + l;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) r.o[i] *= al;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float* src = a.part_o + ((slot0 + base + k) * a.rec_rows + rr) * D + lane;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) r.o[i] = fmaf(wk, __ldcg(src + 32 * i), r.o[i]);
+        }
+    }
+}
+
+// Weight of a row's sums in its output, the sink taken in: out = o * weight
+__device__ __forceinline__ float row_weight(const SplitArgs& a, int h, float M, float L) {
+    if (M == kNegInf) return 0.f;
+    if (a.sinks) {
+        const float s = a.sinks[h] * 1.4426950408889634f;
+        const float m = fmaxf(M, s);
+        const float al = ex2(M - m);
+        return al / (L * al + ex2(s - m));
+    }
+    return 1.0f / L;
+}
+
+template <int NB>
+__device__ __forceinline__ void store_row(const SplitArgs& a, long long row, int h, int lane, const RowSum<NB>& r) {
+    const float w = row_weight(a, h, r.M, r.L);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const long long at = row * (NB * 32) + 32 * i + lane;
+        if (a.bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16(r.o[i] * w);
+        else reinterpret_cast<float*>(a.out)[at] = r.o[i] * w;
+    }
+}
+
+template <int NB, bool F8, bool HL>
+__global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const SplitArgs a, const int stages) {
+    constexpr int D = NB * 32;
+    constexpr int kWarps = warps_of<NB>(), kThreads = kWarps * 32;
     constexpr int QPI = HL ? 8 : 16;
     constexpr int NR = HL ? 1 : 2;
+    constexpr int CELL = NB * (F8 ? 1024 : 928);
     using S = Smem<NB, HL>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint4* qs = reinterpret_cast<uint4*>(smem);
@@ -460,8 +567,14 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
     __shared__ float s_m[kWarps][16], s_l[kWarps][16];
     __shared__ long long s_wsum[kWarps];
     __shared__ int s_ksum[kWarps];
+    __shared__ int s_row0[kWarps][kMaxStages];        // first row of the cell in a stage, -1: none
+    __shared__ __align__(8) uint64_t s_bar[kWarps][kMaxStages];
+    __shared__ int s_abort, s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    if (lane < stages) dev::mbar_init(dev::smem_u32(&s_bar[warp][lane]), 1);
+    if (tid == 0) s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // ---- the plan: prefix sums of the entries' work
     {
@@ -520,38 +633,117 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
             plan[a.E].nc = plan[a.E].c0 = plan[a.E].pad = 0;
         }
         __syncthreads();
-        if (blockIdx.x == 0)
+        if (!a.fuse && blockIdx.x == 0)
             for (int e = tid; e <= a.E; e += kThreads) a.plan[e] = plan[e];
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long W = plan[a.E].work * a.g.Hkv;
     const int G = (int)min((long long)a.G, W);
+    if (a.fuse) {
+        // entries without rows have no key: their outputs are zeros
+        for (int e = blockIdx.x; e < a.E; e += gridDim.x) {
+            if (plan[e].nc != 0 && W != 0) continue;
+            const long long at = (long long)e * (a.lists ? 1 : a.T) * a.Hq * D, n = (long long)(a.lists ? 1 : a.T) * a.Hq * D;
+            for (long long i = tid; i < n; i += kThreads) {
+                if (a.bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at + i] = __float2bfloat16(0.f);
+                else reinterpret_cast<float*>(a.out)[at + i] = 0.f;
+            }
+        }
+    }
     if ((int)blockIdx.x >= G) return;
-    long long x = W * blockIdx.x / G;
-    const long long x1 = W * (blockIdx.x + 1) / G;
+    const long long x0 = W * blockIdx.x / G, x1 = W * (blockIdx.x + 1) / G;
     const int cpp = a.g.cells_per_page();
+    const uint32_t ring = dev::smem_u32(smem) + (uint32_t)S::ring(a.E) + (uint32_t)(warp * stages * CELL);
+    const uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
+    const uint32_t bar0 = dev::smem_u32(&s_bar[warp][0]);
 
+    // ---- the producer side of this warp's ring: its cells (every kWarps-th of
+    // each fragment) in order, `stages` ahead of their use.  Lanes look up the
+    // pages of 32 cells at once.
+    long long px = x0;                                  // first cell after the producer's fragment
+    int pc = 0, pcb = 0, pslot = -1, ppage = -1, pidx = 32;
+    const int* ptable = nullptr;
+    const int* plist = nullptr;
+    int pkh = 0, pc0 = 0, phi = 0;
+    auto produce = [&](int st) {
+        if (pc >= pcb) {
+            // the next fragment in which this warp has a cell
+            for (;;) {
+                if (px >= x1) return;
+                const Fragment f = fragment_at(plan, a, QPI, px, x1);
+                px += f.cb - f.ca;
+                pc = f.ca + warp;
+                if (pc >= f.cb) continue;
+                pcb = f.cb;
+                pc0 = f.c0;
+                pkh = f.kh;
+                int seq = f.e;
+                if (a.lists) seq = f.e / a.T;
+                else if (f.e >= a.n_seq) seq = a.group_start[f.e - a.n_seq];
+                ptable = a.tables + (long long)seq * a.g.max_pages;
+                plist = a.lists ? a.lists + ((long long)f.e * a.g.Hkv + f.kh) * a.keep : nullptr;
+                phi = a.lists ? a.lens[seq] - a.T + (f.e - seq * a.T) + 1 : 0x7fffffff;
+                pidx = 32;
+                break;
+            }
+        }
+        if (pidx == 32) {
+            pidx = 0;
+            const int c = pc + lane * kWarps;
+            pslot = ppage = -1;
+            if (c < pcb) {
+                if (plist) {
+                    pslot = plist[c / cpp];
+                    if (pslot >= a.g.max_pages) {
+                        atomicExch(a.g.err, kErrCounter);
+                        pslot = -1;
+                    }
+                    if (pslot >= 0 && pslot * a.g.page_rows + (c % cpp) * 16 >= phi) pslot = -1;
+                } else {
+                    pslot = (pc0 + c) / cpp;
+                }
+                if (pslot >= 0) ppage = ptable[pslot];
+                if (pslot >= 0 && (ppage < 0 || ppage >= a.g.n_pages)) {
+                    atomicExch(a.g.err, kErrCounter);
+                    ppage = -1;
+                }
+            }
+        }
+        const int page = __shfl_sync(0xffffffffu, ppage, pidx), slot = __shfl_sync(0xffffffffu, pslot, pidx);
+        if (lane == 0) {
+            const uint32_t bar = bar0 + 8u * st;
+            const int in = (plist ? pc : pc0 + pc) % cpp;
+            if (page >= 0) {
+                s_row0[warp][st] = slot * a.g.page_rows + in * 16;
+                dev::mbar_expect_tx(bar, CELL);
+                dev::bulk_g2s(ring + (uint32_t)(st * CELL), a.g.pool + page * a.g.page_bytes + (long long)(pkh * cpp + in) * CELL, CELL, bar);
+            } else {
+                s_row0[warp][st] = -1;
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+            }
+        }
+        ++pidx;
+        pc += kWarps;
+    };
+    for (int st = 0; st < stages; ++st) produce(st);
+
+    int st = 0;
+    uint32_t phase = 0;
+    long long x = x0;
     while (x < x1) {
-        // ---- the fragment: entry e, key kk of it (KV head kh, slice sl), cells [ca, cb)
-        const int e = find_entry(plan, a.E, x / a.g.Hkv);
-        const PlanEntry pe = plan[e];
-        const long long rel = x - pe.work * a.g.Hkv;
-        const int kk = (int)(rel / pe.nc), ca = (int)(rel - (long long)kk * pe.nc);
-        const int cb = (int)min((long long)pe.nc, ca + (x1 - x));
-        const int nsl = (pe.pad + QPI - 1) / QPI;
-        const int kh = kk / nsl, sl = kk - kh * nsl;
-        const long long slot = blockIdx.x + (long long)pe.keys * a.g.Hkv + kk;
-        x += cb - ca;
+        const Fragment f = fragment_at(plan, a, QPI, x, x1);
+        const long long xa = plan[f.e].work * a.g.Hkv + (long long)f.kk * plan[f.e].nc, xb = xa + plan[f.e].nc;
+        x += f.cb - f.ca;
 
         // ---- its queries, as A fragments in shared memory
         __syncthreads();
         for (int r = warp; r < QPI; r += kWarps) {
-            const int qi = sl * QPI + r;
+            const int qi = f.sl * QPI + r;
             Query q{0, 0, 0, 0, -1};
             float v[NB];
             float am = 0.f;
-            const bool valid = qi < pe.pad;
-            if (valid) q = query_of(a, e, kh, qi);
+            const bool valid = qi < f.nq;
+            if (valid) q = query_of(a, f.e, f.kh, qi);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 v[b] = valid ? load_q(a.q, (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + 32 * b + lane, a.bf16) : 0.f;
@@ -560,10 +752,10 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
             // scaled by a power of two to a largest element in [512, 1024)
-            int ex = 0;
-            if (am > 0.f) ex = ilogbf(am) - 9;
+            const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -117), 118) : 0;
+            const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
             if (lane == 0) {
-                ri.fac[r] = ldexpf(a.qscale, ex);
+                ri.fac[r] = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
                 ri.lo[r] = q.lo;
                 ri.hi[r] = q.hi;
             }
@@ -571,7 +763,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
             const int reg = ((wi & 3) >> 1) * 2, half = wi & 1;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const float y = ldexpf(v[b], -ex);
+                const float y = v[b] * up;
                 const __half hi = __float2half_rn(y);
                 __half* dst = reinterpret_cast<__half*>(qs + (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j);
                 if (HL) {
@@ -584,7 +776,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
         }
         __syncthreads();
         if (warp == 0) {
-            const bool v = lane < QPI && sl * QPI + lane < pe.pad;
+            const bool v = lane < QPI && f.sl * QPI + lane < f.nq;
             int lo_max = v ? ri.lo[lane] : 0, hi_min = v ? ri.hi[lane] : 0x7fffffff;
             int lo_min = v ? ri.lo[lane] : 0x7fffffff, hi_max = v ? ri.hi[lane] : 0;
             if (v && ri.hi[lane] <= ri.lo[lane]) lo_min = 0x7fffffff, hi_max = 0;
@@ -615,39 +807,20 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
         for (int b = 0; b < (HL && !F8 ? NB : 1); ++b) acc.mt[b] = 0.f;
 
         // ---- its cells, warp by warp
-        int seq = e;
-        if (a.lists) seq = e / a.T;
-        else if (e >= a.n_seq) seq = a.group_start[e - a.n_seq];
-        const int* table = a.tables + (long long)seq * a.g.max_pages;
-        const int* list = a.lists ? a.lists + ((long long)e * a.g.Hkv + kh) * a.keep : nullptr;
-        for (int c = ca + warp; c < cb; c += kWarps) {
-            int slot_in, in;
-            if (list) {
-                const int li = c / cpp;
-                in = c - li * cpp;
-                slot_in = list[li];
-                if (slot_in < 0) continue;
-                if (slot_in >= a.g.max_pages) {
-                    if (lane == 0) atomicExch(a.g.err, kErrCounter);
-                    continue;
-                }
-            } else {
-                const int C = pe.c0 + c;
-                slot_in = C / cpp;
-                in = C - slot_in * cpp;
+        for (int c = f.ca + warp; c < f.cb; c += kWarps) {
+            const bool there = wait_stage(bar0 + 8u * st, phase, &s_abort, a.g.err);
+            const int row0 = s_row0[warp][st];
+            if (there && row0 >= 0 && row0 < ri.hi_max)
+                take_cell<NB, F8, HL>(a, ring_p + st * CELL, row0, qs, ri, lane, acc);
+            __syncwarp();
+            if (there) produce(st);
+            if (++st == stages) {
+                st = 0;
+                phase ^= 1u;
             }
-            const int row0 = slot_in * a.g.page_rows + in * 16;
-            if (row0 >= ri.hi_max) continue;
-            const int pg = table[slot_in];
-            if (pg < 0 || pg >= a.g.n_pages) {
-                if (lane == 0) atomicExch(a.g.err, kErrCounter);
-                continue;
-            }
-            const uint8_t* cell = a.g.pool + pg * a.g.page_bytes + (long long)(kh * cpp + in) * a.g.cell_bytes;
-            take_cell<NB, F8, HL>(a, cell, row0, qs, ri, lane, acc);
         }
 
-        // ---- join the warps: common reference, then a tree over the warps
+        // ---- join the warps: common reference, then sums passed down four warps at a time
         const int g = lane >> 2, j = lane & 3;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -680,44 +853,75 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
         for (int r = 0; r < NR; ++r) {
             M[r] = kNegInf;
             L[r] = 0.f;
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) M[r] = fmaxf(M[r], s_m[w][g + 8 * r]);
+#pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 if (s_m[w][g + 8 * r] != kNegInf) L[r] += s_l[w][g + 8 * r] * ex2(s_m[w][g + 8 * r] - M[r]);
-            const float f = acc.m[r] == kNegInf ? 0.f : ex2(acc.m[r] - M[r]);
+            const float fa = acc.m[r] == kNegInf ? 0.f : ex2(acc.m[r] - M[r]);
 #pragma unroll
             for (int n = 0; n < 4 * NB; ++n) {
-                acc.o[n][2 * r] *= f;
-                acc.o[n][2 * r + 1] *= f;
+                acc.o[n][2 * r] *= fa;
+                acc.o[n][2 * r + 1] *= fa;
             }
         }
+        auto pass = [&](int lo, int n) {               // warps [lo + n, lo + 2n) add their sums to [lo, lo + n)
+            float2* buf = reinterpret_cast<float2*>(comb) + (size_t)(warp & (n - 1)) * (4 * NB * NR * 32);
+            if (warp >= lo + n && warp < lo + 2 * n) {
 #pragma unroll
-        for (int half = kWarps / 2; half >= 1; half >>= 1) {
-            float2* buf = reinterpret_cast<float2*>(comb) + (size_t)(warp & (half - 1)) * (4 * NB * NR * 32);
-            if (warp >= half && warp < 2 * half) {
-#pragma unroll
-                for (int n = 0; n < 4 * NB; ++n)
+                for (int i = 0; i < 4 * NB; ++i)
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
-                        buf[(n * NR + r) * 32 + lane] = make_float2(acc.o[n][2 * r], acc.o[n][2 * r + 1]);
+                        buf[(i * NR + r) * 32 + lane] = make_float2(acc.o[i][2 * r], acc.o[i][2 * r + 1]);
             }
             __syncthreads();
-            if (warp < half) {
+            if (warp >= lo && warp < lo + n) {
 #pragma unroll
-                for (int n = 0; n < 4 * NB; ++n)
+                for (int i = 0; i < 4 * NB; ++i)
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
-                        const float2 y = buf[(n * NR + r) * 32 + lane];
-                        acc.o[n][2 * r] += y.x;
-                        acc.o[n][2 * r + 1] += y.y;
+                        const float2 y = buf[(i * NR + r) * 32 + lane];
+                        acc.o[i][2 * r] += y.x;
+                        acc.o[i][2 * r + 1] += y.y;
                     }
             }
             __syncthreads();
-        }
+        };
+        for (int lo = kWarps - 2 * kCombine; lo >= 0; lo -= kCombine) pass(lo, kCombine);
+        for (int n = kCombine / 2; n >= 1; n >>= 1) pass(0, n);
+
+        const int cta0 = cta_of(xa, G, W), n_rec = cta_of(xb - 1, G, W) - cta0 + 1;
+        const long long key = (long long)f.keys * a.g.Hkv + f.kk;
+        const int rows = min(QPI, f.nq - f.sl * QPI);
         if (warp == 0) {
+            const bool whole = a.fuse && n_rec == 1;
+            const long long slot = blockIdx.x + key;
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 const int row = g + 8 * r;
-                if (sl * QPI + row >= pe.pad) continue;
+                if (row >= rows) continue;
+                if (whole) {
+                    const Query q = query_of(a, f.e, f.kh, f.sl * QPI + row);
+                    const float w = row_weight(a, q.h, M[r] == kNegInf ? kNegInf : M[r] - kShift, L[r]);
+                    const long long at = (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + 8 * j;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = acc.o[4 * b + (i & 3)][2 * r + (i >> 2)] * w;
+                        if (a.bf16) {
+                            uint32_t w4[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w4[i] = as_u32(__floats2bfloat162_rn(y[2 * i], y[2 * i + 1]));
+                            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at + 32 * b) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at + 32 * b);
+                            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                        }
+                    }
+                    continue;
+                }
                 float* dst = a.part_o + (slot * a.rec_rows + row) * D + 8 * j;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -728,17 +932,46 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
                     *reinterpret_cast<float2*>(a.part_ml + (slot * a.rec_rows + row) * 2) =
                         make_float2(M[r] == kNegInf ? kNegInf : M[r] - kShift, L[r]);
             }
+            if (a.fuse && n_rec > 1) {
+                // the CTA that completes a key's records joins them; the others go on
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) {
+                    const bool last = atomicAdd(a.arrived + key, 1) == n_rec - 1;
+                    if (last) a.arrived[key] = 0;
+                    s_last = last;
+                    __threadfence();
+                }
+            }
         }
+        if (a.fuse && n_rec > 1) {
+            __syncthreads();
+            if (s_last) {
+                for (int rr = warp; rr < rows; rr += kWarps) {
+                    RowSum<NB> r;
+                    r.M = kNegInf;
+                    r.L = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) r.o[i] = 0.f;
+                    fold_records<NB>(a, cta0 + key, n_rec, rr, lane, r);
+                    const Query q = query_of(a, f.e, f.kh, f.sl * QPI + rr);
+                    store_row<NB>(a, ((long long)q.seq * a.T + q.t) * a.Hq + q.h, q.h, lane, r);
+                }
+            }
+        }
+    }
+    if (s_abort) {                                     // a wait ran out: let copies in flight land before the CTA ends
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1LL << 30)) __nanosleep(1000);
     }
 }
 
 // ------------------------------------------------------------ merge kernel
 
-// One warp per output row (sequence, t, head): the records of its key (the
-// CTAs whose ranges meet it), those of its group's prefix, and the sink.
+// One warp per output row (sequence, t, head) of a shared decode: the records
+// of its own rows' key and of its group's prefix, and the sink.
 template <int NB>
 __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) {
-    constexpr int D = NB * 32;
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -748,90 +981,50 @@ __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) 
     const int kh = h / a.hpk, hr = h - kh * a.hpk;
     const long long W = a.plan[a.E].work * a.g.Hkv;
     const int G = (int)min((long long)a.G, W);
-    float M = kNegInf, L = 0.f, o[NB];
+    RowSum<NB> r;
+    r.M = kNegInf;
+    r.L = 0.f;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) o[i] = 0.f;
+    for (int i = 0; i < NB; ++i) r.o[i] = 0.f;
     auto fold = [&](int e, int qi) {
         const PlanEntry pe = a.plan[e];
         if (pe.nc == 0 || W == 0) return;
         const int nsl = (pe.pad + QPI - 1) / QPI;
-        const int kk = kh * nsl + qi / QPI, rr = qi % QPI;
-        const long long xa = pe.work * a.g.Hkv + (long long)kk * pe.nc, xb = xa + pe.nc;
-        const long long key = (long long)pe.keys * a.g.Hkv + kk;
-        const int c0 = (int)(((xa + 1) * G - 1) / W), c1 = (int)((xb * G - 1) / W);
-        for (int base = c0; base <= c1; base += 32) {
-            const int n = min(32, c1 - base + 1);
-            float2 ml = make_float2(kNegInf, 0.f);
-            if (lane < n) ml = *reinterpret_cast<const float2*>(a.part_ml + ((base + lane + key) * a.rec_rows + rr) * 2);
-            float m = ml.x;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-            m = fmaxf(m, M);
-            if (m == kNegInf) continue;
-            const float al = M == kNegInf ? 0.f : ex2(M - m);
-            M = m;
-            const float w = ml.x == kNegInf ? 0.f : ex2(ml.x - m);
-            float l = ml.y * w;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-            L = L * al + l;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) o[i] *= al;
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                const float* src = a.part_o + ((base + k + key) * a.rec_rows + rr) * D + lane;
-#pragma unroll
-                for (int i = 0; i < NB; ++i) o[i] = fmaf(wk, src[32 * i], o[i]);
-            }
-        }
+        const int kk = kh * nsl + qi / QPI;
+        const long long xa = pe.work * a.g.Hkv + (long long)kk * pe.nc;
+        const int c0 = cta_of(xa, G, W), c1 = cta_of(xa + pe.nc - 1, G, W);
+        fold_records<NB>(a, (long long)pe.keys * a.g.Hkv + kk + c0, c1 - c0 + 1, qi % QPI, lane, r);
     };
-    if (a.lists) {
-        fold(st, hr);
-    } else {
-        fold(seq, t * a.hpk + hr);
-        if (a.n_groups) {
-            const int grp = group_of(a, seq);
-            if (grp >= 0) {
-                int gs, ge;
-                members(a, grp, gs, ge);
-                if (seq >= gs && seq < ge) fold(a.n_seq + grp, ((seq - gs) * a.T + t) * a.hpk + hr);
-            }
-        }
+    fold(seq, t * a.hpk + hr);
+    const int grp = group_of(a, seq);
+    if (grp >= 0) {
+        int gs, ge;
+        members(a, grp, gs, ge);
+        if (seq >= gs && seq < ge) fold(a.n_seq + grp, ((seq - gs) * a.T + t) * a.hpk + hr);
     }
-    if (a.sinks && M != kNegInf) {
-        const float s = a.sinks[h] * 1.4426950408889634f;
-        const float m = fmaxf(M, s);
-        const float al = ex2(M - m);
-        L = L * al + ex2(s - m);
-#pragma unroll
-        for (int i = 0; i < NB; ++i) o[i] *= al;
-    }
-    const float inv = L > 0.f ? 1.0f / L : 0.f;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const long long at = row * D + 32 * i + lane;
-        if (a.bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16(o[i] * inv);
-        else reinterpret_cast<float*>(a.out)[at] = o[i] * inv;
-    }
+    store_row<NB>(a, row, h, lane, r);
 }
 
 template <int NB, bool F8, bool HL>
 cudaError_t launch_split_t(const SplitArgs& a, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = kernel_attrs_once(split_kernel<NB, F8, HL>, done, false);
+    cudaError_t e = kernel_attrs_once(split_kernel<NB, F8, HL>, done, true);
     if (e != cudaSuccess) return e;
+    using S = Smem<NB, HL>;
+    constexpr size_t cells = (size_t)warps_of<NB>() * NB * (F8 ? 1024 : 928);
+    // the ring takes what the plan leaves of 220 KB (2 to 8 stages)
+    const int stages = (int)std::min<size_t>(kMaxStages, (220 * 1024 - S::ring(a.E)) / cells);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.G);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Smem<NB, HL>::total(a.E);
+    cfg.blockDim = dim3(warps_of<NB>() * 32);
+    cfg.dynamicSmemBytes = S::ring(a.E) + stages * cells;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_kernel<NB, F8, HL>, a);
+    return cudaLaunchKernelEx(&cfg, split_kernel<NB, F8, HL>, a, stages);
 }
 
 template <int NB>
