@@ -162,7 +162,9 @@ struct SplitArgs {
     int keep;
     int E;                         // work entries
     int G;                         // CTAs of the split kernel
-    int rec_rows;                  // query rows of a record: min(QPI, most queries of a key)
+    int tile;                      // queries of a slice (QPI): 8, or 16 for more bf16 queries
+    int warps;                     // warps of the split kernel's CTAs
+    int rec_rows;                  // query rows of a record: min(tile, most queries of a key)
     int fuse;                      // 1: the last CTA of a key joins its records (no merge kernel)
     int* arrived;                  // [key] records written; 0 between calls
     long long max_keys;            // keys that the record area holds beside the CTAs' own
@@ -176,7 +178,8 @@ struct PlanEntry {
     long long work;
     int keys, nc, c0, pad;
 };
-int split_queries(const SplitArgs& a);                    // QPI of the kernel a call would use
+int split_tile(bool bf16, int most_queries);
+int split_warps(int NB, int tile);
 cudaError_t launch_split(const SplitArgs& a, cudaStream_t s);
 cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s);
 

@@ -154,9 +154,10 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.keep = keep;
     a.E = lists ? q->n_seq * q->T : q->n_seq + n_groups;
     a.G = std::min(c->num_sms, kMaxGrid);
-    const int qpi = split_queries(a);
     const int most = lists ? a.hpk : n_groups ? q->n_seq * a.hpk * q->T : a.hpk * q->T;
-    a.rec_rows = std::min(qpi, most);
+    a.tile = split_tile(a.bf16, most);
+    a.warps = split_warps(a.g.NB(), a.tile);
+    a.rec_rows = std::min(a.tile, most);
     a.max_keys = (long long)(c->key_rows / a.rec_rows);
     a.plan = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan);
     a.arrived = reinterpret_cast<int*>(c->ws + c->off_arrived);

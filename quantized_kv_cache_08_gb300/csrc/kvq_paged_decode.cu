@@ -5,23 +5,25 @@
 // p_t = 2^(s_t - m), s_t the scaled score in log2 units and m a reference that
 // only moves when a score passes it by 8 (one pass over the rows).  Rows come in
 // cells of 16 rows of one KV head; a warp takes a cell at a time and multiplies
-// 16 query rows with it on the tensor cores (mma.m16n8k16): S = Q K^T and
-// O += P V.  The cell layout is the operands' register layout, so a lane's
-// loads are its fragments: K and V bytes turn into fp16 pairs in registers,
-// two codes an instruction, and nothing passes through shared memory.
+// it on the tensor cores (mma.m16n8k16): S = Q K^T with query rows as M, then
+// O^T += V^T P^T with 16 elements as M and 8 queries as N.  The cell layout is
+// the operands' register layout, so a lane's loads are its fragments, K and V
+// codes turn into fp16 pairs in registers, and S's accumulators are P^T's B
+// fragments as they stand: nothing is transposed or passed through shared
+// memory on the way.
 //   K: codes are small integers, exact in fp16, so the products with the query
 //      run on codes and each 32-element block's sum is scaled by its d in f32.
 //   V: v = u d + m in one half2 fma a pair of rows (one rounding to fp16).
-// f32 queries (HL) keep f32 accuracy with 8 queries a tile: rows 0..7 of the A
-// operand carry the high part and rows 8..15 the low part of the same numbers.
-// For Q these are two fp16 (22 bits of a query scaled to its largest element);
-// for P d two bf16 (16 bits, any range) against the exact codes u - 16, with
+// Tiles of 8 or 16 queries of bf16 (the tile is taken by the most queries that
+// a key has); f32 queries keep f32 accuracy with tiles of 8: rows 0..7 of the S
+// tile carry the high part of the queries and rows 8..15 the low part, two fp16
+// numbers (22 bits of a query scaled to its largest element), and P d goes in as
+// two bf16 numbers (16 bits, any range) against the exact codes u - 16, with
 // sum p (m + 16 d) kept in f32 beside it.
 //
-// Why tensor cores for one token: a query-row tile costs the same for 1 or 16
-// queries, and the work that grows with the bytes is only the unpacking, about
-// 4.5 instructions a warp-element pair of K and V, where the multiply-add form
-// needs as many again for each 4 queries.
+// Why tensor cores for one token: the products cost the same for 1 or 8 queries,
+// so the work that grows with the bytes is the unpacking alone, where the
+// multiply-add form needs as many instructions again for each 4 queries.
 //
 // Work is cut stream-K fashion: see kvq_paged.cuh.
 #include "kvq_device.cuh"
@@ -44,10 +46,14 @@ constexpr float kShift = 6.0f;         // p is held as 2^6 p: fp16 keeps 2^-20 o
 constexpr int kMaxStages = 8;
 constexpr int kCombine = 4;            // warps' sums that the join holds at once
 
-// Warps of a CTA (one CTA an SM): as many as the accumulators leave registers
-// for; 12 of 168 registers at head_dim 128.
-template <int NB>
-constexpr int warps_of() { return NB == 2 ? 16 : NB == 4 ? 12 : 8; }
+// Query tiles: 8 or 16 bf16 queries, or 8 of f32 in two parts
+enum Tile { kT8 = 0, kT16 = 1, kF32 = 2 };
+
+// Warps of a CTA (one CTA an SM): as many as the accumulators leave registers for
+template <int NB, int TILE>
+constexpr int warps_of() { return NB == 8 ? 8 : NB == 4 && TILE == kT16 ? 12 : 16; }
+template <int TILE>
+constexpr int queries_of() { return TILE == kT16 ? 16 : 8; }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -55,6 +61,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// c = a b, without a sum to start from
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -225,11 +237,14 @@ __device__ __forceinline__ float load_q(const void* q, long long idx, int bf16) 
 
 // ------------------------------------------------------------ split kernel
 
-template <int NB, bool F8, bool HL>
+template <int NB, bool F8, int TILE>
 struct Acc {
-    float o[4 * NB][4];        // n-tile 4b + r: element 32b + 8j + r (cols 0) and + 4 (cols 1)
-    float m[2], l[2];          // rows g and g + 8 (HL: row g)
-    float mt[HL && !F8 ? NB : 1];
+    static constexpr int NQ = TILE == kT16 ? 2 : 1;       // groups of 8 queries
+    // O^T tile 2b + rp of a group: rows g / g + 8 are elements 32b + 4g + 2rp and
+    // + 1, columns 2j, 2j + 1 queries: [0] (el, 2j) [1] (el, 2j+1) [2] (el+1, 2j) ..
+    float o[NQ][2 * NB][4];
+    float m[NQ], l[NQ];                                   // query g (+ 8): reference, sum of p
+    float mt[TILE == kF32 && !F8 ? NB : 1];               // sum p (m + 16 d) of query g
 };
 
 struct RowInfo {
@@ -238,150 +253,204 @@ struct RowInfo {
     int lo_min, lo_max, hi_min, hi_max;
 };
 
-// One cell: 16 rows from logical row row0 on, into the warp's accumulators
-template <int NB, bool F8, bool HL>
-__device__ __forceinline__ void take_cell(const SplitArgs& a, const uint8_t* __restrict__ cell, int row0,
-                                          const uint4* __restrict__ qs, const RowInfo& ri, int lane,
-                                          Acc<NB, F8, HL>& acc) {
-    const int g = lane >> 2, j = lane & 3;
+// Per-lane facts of a fragment's queries g (+ 8)
+template <int NQ>
+struct LaneRows {
+    float fac[NQ];
+    int lo[NQ], hi[NQ];
+};
+
+constexpr float kNone = -1e30f;        // reference of a query that has seen no row: any score passes it
+
+// Values of rows that no query sees, in the staged cell: zeroed, for they may be any bytes
+template <int NB, bool F8>
+__device__ __forceinline__ void clear_rows(uint8_t* cell, int row0, const RowInfo& ri, int lane) {
+    if constexpr (F8) {
+        const int j = lane & 3;
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(cell + 512 * NB + c * 512 + lane * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int h = (2 * c + (i >> 1)) / NB;
+                const int at = row0 + 8 * h + 2 * j;
+                const uint32_t k = (at >= ri.lo_min && at < ri.hi_max ? 0x00ff00ffu : 0u) |
+                                   (at + 1 >= ri.lo_min && at + 1 < ri.hi_max ? 0xff00ff00u : 0u);
+                p[i] &= k;
+            }
+        }
+    } else {
+        for (int i = lane; i < 16 * NB; i += 32) {
+            const int t = i & 15, b = i >> 4;
+            if (row0 + t >= ri.lo_min && row0 + t < ri.hi_max) continue;
+            uint16_t* p = reinterpret_cast<uint16_t*>(cell + 864 * NB + (((t & 7) >> 1) * NB + b) * 16 + (2 * (t >> 3) + (t & 1)) * 2);
+            p[0] = 0;
+            p[4] = 0;
+        }
+    }
+    __syncwarp();
+}
+
+// One staged cell, 16 rows from logical row row0 on, into the warp's accumulators
+template <int NB, bool F8, int TILE>
+__device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int row0, const uint8_t* __restrict__ qs,
+                                          const RowInfo& ri, const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane,
+                                          Acc<NB, F8, TILE>& acc) {
+    constexpr bool HL = TILE == kF32;
+    constexpr int NQ = Acc<NB, F8, TILE>::NQ;
+    const int j = lane & 3;
+    const bool edge = row0 < ri.lo_max || row0 + 16 > ri.hi_min;
+    if (edge) clear_rows<NB, F8>(cell, row0, ri, lane);
     // ---- scores
     float sc[2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[t][i] = 0.f;
+    auto q_frag = [&](int step) {
+        if constexpr (TILE == kT8) {
+            const uint2 x = *reinterpret_cast<const uint2*>(qs + (step * 32 + lane) * 8);
+            return make_uint4(x.x, 0u, x.y, 0u);
+        } else {
+            return *reinterpret_cast<const uint4*>(qs + (step * 32 + lane) * 16);
+        }
+    };
 #pragma unroll
     for (int bp = 0; bp < NB / 2; ++bp) {
         uint4 kk[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) kk[t] = *reinterpret_cast<const uint4*>(cell + bp * 1024 + t * 512 + lane * 16);
+        uint4 ks;                                         // d of rows (2j, 2j+1), (2j+8, 2j+9), blocks 2bp and 2bp + 1
+        if constexpr (!F8) ks = *reinterpret_cast<const uint4*>(cell + 512 * NB + (j * NB + 2 * bp) * 8);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int b = 2 * bp + e;
-            const uint4 a0 = qs[(2 * b) * 32 + lane], a1 = qs[(2 * b + 1) * 32 + lane];
-            if constexpr (F8) {
+            const uint4 a0 = q_frag(2 * b), a1 = q_frag(2 * b + 1);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t w0 = e ? kk[t].z : kk[t].x, w1 = e ? kk[t].w : kk[t].y;
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t w0 = e ? kk[t].z : kk[t].x, w1 = e ? kk[t].w : kk[t].y;
+                if constexpr (F8) {
                     mma_f16(sc[t], a0, f8_pair(w0), f8_pair(w0 >> 16));
                     mma_f16(sc[t], a1, f8_pair(w1), f8_pair(w1 >> 16));
-                }
-            } else {
-                const uint2 ks = *reinterpret_cast<const uint2*>(cell + 512 * NB + (j * NB + b) * 8);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t w0 = e ? kk[t].z : kk[t].x, w1 = e ? kk[t].w : kk[t].y;
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(c, a0, k_pair(w0, 0x4140u), k_pair(w0, 0x4342u));
+                } else {
+                    float c[4];
+                    mma_f16_new(c, a0, k_pair(w0, 0x4140u), k_pair(w0, 0x4342u));
                     mma_f16(c, a1, k_pair(w1, 0x4140u), k_pair(w1, 0x4342u));
-                    const float2 d = __half22float2(as_h2(t ? ks.y : ks.x));
+                    const float2 d = __half22float2(as_h2(e ? (t ? ks.w : ks.z) : (t ? ks.y : ks.x)));
+                    if constexpr (HL) {
+                        c[0] += c[2];
+                        c[1] += c[3];
+                    }
                     sc[t][0] = fmaf(c[0], d.x, sc[t][0]);
                     sc[t][1] = fmaf(c[1], d.y, sc[t][1]);
-                    sc[t][2] = fmaf(c[2], d.x, sc[t][2]);
-                    sc[t][3] = fmaf(c[3], d.y, sc[t][3]);
+                    if constexpr (TILE == kT16) {
+                        sc[t][2] = fmaf(c[2], d.x, sc[t][2]);
+                        sc[t][3] = fmaf(c[3], d.y, sc[t][3]);
+                    }
                 }
             }
         }
     }
-    // ---- scale, cap, mask; the reference maximum
-    constexpr int NR = HL ? 1 : 2;
-    const bool edge = row0 < ri.lo_max || row0 + 16 > ri.hi_min;
-    bool move = false;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        const float f = ri.fac[g + 8 * r];
-        const int lo = ri.lo[g + 8 * r], hi = ri.hi[g + 8 * r];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float s = HL ? sc[t][i] + sc[t][2 + i] : sc[t][2 * r + i];
-                s *= f;
-                if (a.softcap_b > 0.f) s = a.softcap_b * tanhf(a.softcap_a * s);
-                const int at = row0 + 8 * t + 2 * j + i;
-                if (edge && (at < lo || at >= hi)) s = kNegInf;
-                sc[t][2 * r + i] = s;
-                move |= s > acc.m[r] + kLazy;
-            }
-    }
-    if (__any_sync(0xffffffffu, move)) {
-        float al[2] = {1.f, 1.f};
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            float v = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            if (v > acc.m[r] + kLazy) {
-                al[r] = acc.m[r] == kNegInf ? 0.f : ex2(acc.m[r] - v);
-                acc.m[r] = v;
-                acc.l[r] *= al[r];
-            }
-        }
-        if (HL) al[1] = al[0];
-#pragma unroll
-        for (int n = 0; n < 4 * NB; ++n) {
-            acc.o[n][0] *= al[0];
-            acc.o[n][1] *= al[0];
-            acc.o[n][2] *= al[1];
-            acc.o[n][3] *= al[1];
-        }
-        if constexpr (HL && !F8) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) acc.mt[b] *= al[0];
-        }
-    }
-    // ---- probabilities (a row without a reference yet has none but -inf scores)
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float s = sc[t][2 * r + i];
-                const float p = s == kNegInf ? 0.f : ex2(s - acc.m[r] + kShift);
-                acc.l[r] += p;
-                sc[t][2 * r + i] = p;
-            }
-    // rows that no query sees may hold any bytes: their values are taken as 0
-    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};           // half words of rows (2j, 2j+1), (2j+8, 2j+9)
-    if (edge) {
+    if constexpr (HL && F8) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int at = row0 + 8 * t + 2 * j;
-            const bool k0 = at >= ri.lo_min && at < ri.hi_max, k1 = at + 1 >= ri.lo_min && at + 1 < ri.hi_max;
-            keep[t] = (k0 ? 0x0000ffffu : 0u) | (k1 ? 0xffff0000u : 0u);
+            sc[t][0] += sc[t][2];
+            sc[t][1] += sc[t][3];
         }
     }
+    // ---- scale, cap, mask; the reference
+    float top[NQ];
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sc[t][2 * r + i] *= lr.fac[r];
+        if (a.softcap_b > 0.f) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) sc[t][2 * r + i] = a.softcap_b * tanhf(a.softcap_a * sc[t][2 * r + i]);
+        }
+        if (edge) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int at = row0 + 8 * t + 2 * j + i;
+                    if (at < lr.lo[r] || at >= lr.hi[r]) sc[t][2 * r + i] = kNegInf;
+                }
+        }
+        top[r] = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+    }
+    bool move = top[0] > acc.m[0] + kLazy;
+    if (NQ == 2) move |= top[NQ - 1] > acc.m[NQ - 1] + kLazy;
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int r = 0; r < NQ; ++r) {
+            float v = top[r];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+            float al = 1.f;
+            if (v > acc.m[r] + kLazy) {
+                al = ex2(acc.m[r] - v);
+                acc.m[r] = v;
+                acc.l[r] *= al;
+            }
+            if constexpr (HL && !F8) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) acc.mt[b] *= al;
+            }
+            const float al0 = __shfl_sync(0xffffffffu, al, 8 * j), al1 = __shfl_sync(0xffffffffu, al, 8 * j + 4);
+#pragma unroll
+            for (int n = 0; n < 2 * NB; ++n) {
+                acc.o[r][n][0] *= al0;
+                acc.o[r][n][1] *= al1;
+                acc.o[r][n][2] *= al0;
+                acc.o[r][n][3] *= al1;
+            }
+        }
+    }
+    // ---- probabilities
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+        const float c = kShift - acc.m[r];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sc[t][2 * r + i] = ex2(sc[t][2 * r + i] + c);
+        acc.l[r] += (sc[0][2 * r] + sc[0][2 * r + 1]) + (sc[1][2 * r] + sc[1][2 * r + 1]);
+    }
     // ---- values
-    uint4 pa;
-    if constexpr (!HL) {
-        pa.x = as_u32(__floats2half2_rn(sc[0][0], sc[0][1]));
-        pa.y = as_u32(__floats2half2_rn(sc[0][2], sc[0][3]));
-        pa.z = as_u32(__floats2half2_rn(sc[1][0], sc[1][1]));
-        pa.w = as_u32(__floats2half2_rn(sc[1][2], sc[1][3]));
-    } else if constexpr (F8) {
-        const __half2 h0 = __floats2half2_rn(sc[0][0], sc[0][1]), h1 = __floats2half2_rn(sc[1][0], sc[1][1]);
-        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-        pa.x = as_u32(h0);
-        pa.z = as_u32(h1);
-        pa.y = as_u32(__floats2half2_rn(sc[0][0] - f0.x, sc[0][1] - f0.y));
-        pa.w = as_u32(__floats2half2_rn(sc[1][0] - f1.x, sc[1][1] - f1.y));
+    uint32_t pb[NQ][2];                                   // B fragments: rows (2j, 2j+1), (2j+8, 2j+9) of query g (+ 8)
+    uint32_t pl[2];                                       // low parts (E4M3 rows, f32 queries)
+#pragma unroll
+    for (int r = 0; r < NQ; ++r)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) pb[r][t] = as_u32(__floats2half2_rn(sc[t][2 * r], sc[t][2 * r + 1]));
+    if constexpr (HL && F8) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float2 f = __half22float2(as_h2(pb[0][t]));
+            pl[t] = as_u32(__floats2half2_rn(sc[t][0] - f.x, sc[t][1] - f.y));
+        }
     }
     if constexpr (F8) {
-        const uint32_t k0 = __byte_perm(keep[0], 0, 0x2020), k1 = __byte_perm(keep[1], 0, 0x2020);
-        const uint32_t kb0 = k0, kb1 = k1;                   // bytes (row 2j, row 2j + 1) twice
         uint4 vv[NB];
 #pragma unroll
         for (int c = 0; c < NB; ++c) vv[c] = *reinterpret_cast<const uint4*>(cell + 512 * NB + c * 512 + lane * 16);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int n0 = b, n1 = NB + b;
-            const uint32_t x0 = (n0 & 1 ? vv[n0 / 2].z : vv[n0 / 2].x) & kb0, x1 = (n0 & 1 ? vv[n0 / 2].w : vv[n0 / 2].y) & kb0;
-            const uint32_t y0 = (n1 & 1 ? vv[n1 / 2].z : vv[n1 / 2].x) & kb1, y1 = (n1 & 1 ? vv[n1 / 2].w : vv[n1 / 2].y) & kb1;
-            mma_f16(acc.o[4 * b + 0], pa, f8_pair(x0), f8_pair(y0));
-            mma_f16(acc.o[4 * b + 1], pa, f8_pair(x0 >> 16), f8_pair(y0 >> 16));
-            mma_f16(acc.o[4 * b + 2], pa, f8_pair(x1), f8_pair(y1));
-            mma_f16(acc.o[4 * b + 3], pa, f8_pair(x1 >> 16), f8_pair(y1 >> 16));
+#pragma unroll
+            for (int rp = 0; rp < 2; ++rp) {
+                const uint32_t x = n0 & 1 ? (rp ? vv[n0 / 2].w : vv[n0 / 2].z) : (rp ? vv[n0 / 2].y : vv[n0 / 2].x);
+                const uint32_t y = n1 & 1 ? (rp ? vv[n1 / 2].w : vv[n1 / 2].z) : (rp ? vv[n1 / 2].y : vv[n1 / 2].x);
+                const uint4 va = make_uint4(f8_pair(x), f8_pair(x >> 16), f8_pair(y), f8_pair(y >> 16));
+#pragma unroll
+                for (int r = 0; r < NQ; ++r) mma_f16(acc.o[r][2 * b + rp], va, pb[r][0], pb[r][1]);
+                if constexpr (HL) mma_f16(acc.o[0][2 * b + rp], va, pl[0], pl[1]);
+            }
         }
     } else {
         uint32_t u[2 * NB], nb[NB / 2];
@@ -393,22 +462,24 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, const uint8_t* __r
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            uint4 dm = *reinterpret_cast<const uint4*>(cell + 864 * NB + (j * NB + b) * 16);
-            dm.x &= keep[0]; dm.z &= keep[0];
-            dm.y &= keep[1]; dm.w &= keep[1];
+            const uint4 dm = *reinterpret_cast<const uint4*>(cell + 864 * NB + (j * NB + b) * 16);
             const int n0 = b, n1 = NB + b;
             if constexpr (!HL) {
-                auto tile = [&](auto R) {
+                auto value = [&](auto R, int n, uint32_t d, uint32_t m) {
                     constexpr int r = decltype(R)::value;
-                    const __half2 c0 = __hsub2(as_h2(v_codes<r>(u[n0], nb[n0 / 4], n0 % 4, 0x64006400u)), as_h2(0x64006400u));
-                    const __half2 c1 = __hsub2(as_h2(v_codes<r>(u[n1], nb[n1 / 4], n1 % 4, 0x64006400u)), as_h2(0x64006400u));
-                    mma_f16(acc.o[4 * b + r], pa, as_u32(__hfma2(c0, as_h2(dm.x), as_h2(dm.z))),
-                            as_u32(__hfma2(c1, as_h2(dm.y), as_h2(dm.w))));
+                    const __half2 c = __hsub2(as_h2(v_codes<r>(u[n], nb[n / 4], n % 4, 0x64006400u)), as_h2(0x64006400u));
+                    return as_u32(__hfma2(c, as_h2(d), as_h2(m)));
                 };
-                tile(std::integral_constant<int, 0>{});
-                tile(std::integral_constant<int, 1>{});
-                tile(std::integral_constant<int, 2>{});
-                tile(std::integral_constant<int, 3>{});
+                const std::integral_constant<int, 0> r0{};
+                const std::integral_constant<int, 1> r1{};
+                const std::integral_constant<int, 2> r2{};
+                const std::integral_constant<int, 3> r3{};
+                const uint4 v0 = make_uint4(value(r0, n0, dm.x, dm.z), value(r1, n0, dm.x, dm.z), value(r0, n1, dm.y, dm.w), value(r1, n1, dm.y, dm.w));
+#pragma unroll
+                for (int r = 0; r < NQ; ++r) mma_f16(acc.o[r][2 * b], v0, pb[r][0], pb[r][1]);
+                const uint4 v1 = make_uint4(value(r2, n0, dm.x, dm.z), value(r3, n0, dm.x, dm.z), value(r2, n1, dm.y, dm.w), value(r3, n1, dm.y, dm.w));
+#pragma unroll
+                for (int r = 0; r < NQ; ++r) mma_f16(acc.o[r][2 * b + 1], v1, pb[r][0], pb[r][1]);
             } else {
                 const float2 d0 = __half22float2(as_h2(dm.x)), d1 = __half22float2(as_h2(dm.y));
                 const float2 m0 = __half22float2(as_h2(dm.z)), m1 = __half22float2(as_h2(dm.w));
@@ -420,36 +491,38 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, const uint8_t* __r
                 acc.mt[b] = fmaf(sc[1][1], fmaf(16.f, d1.y, m1.y), t);
                 const __nv_bfloat162 h0 = __floats2bfloat162_rn(x0, x1), h1 = __floats2bfloat162_rn(x2, x3);
                 const float2 f0 = __bfloat1622float2(h0), f1 = __bfloat1622float2(h1);
-                uint4 pd;
-                pd.x = as_u32(h0);
-                pd.z = as_u32(h1);
-                pd.y = as_u32(__floats2bfloat162_rn(x0 - f0.x, x1 - f0.y));
-                pd.w = as_u32(__floats2bfloat162_rn(x2 - f1.x, x3 - f1.y));
-                auto tile = [&](auto R) {
+                const uint32_t ph0 = as_u32(h0), ph1 = as_u32(h1);
+                const uint32_t pl0 = as_u32(__floats2bfloat162_rn(x0 - f0.x, x1 - f0.y));
+                const uint32_t pl1 = as_u32(__floats2bfloat162_rn(x2 - f1.x, x3 - f1.y));
+                auto code = [&](auto R, int n) {
                     constexpr int r = decltype(R)::value;
-                    const __nv_bfloat162 mid = __floats2bfloat162_rn(144.f, 144.f);
-                    uint32_t c0 = v_codes<r>(u[n0], nb[n0 / 4], n0 % 4, 0x43004300u);
-                    uint32_t c1 = v_codes<r>(u[n1], nb[n1 / 4], n1 % 4, 0x43004300u);
-                    c0 = as_u32(__hsub2(*reinterpret_cast<__nv_bfloat162*>(&c0), mid));
-                    c1 = as_u32(__hsub2(*reinterpret_cast<__nv_bfloat162*>(&c1), mid));
-                    mma_bf16(acc.o[4 * b + r], pd, c0, c1);
+                    uint32_t c = v_codes<r>(u[n], nb[n / 4], n % 4, 0x43004300u);
+                    return as_u32(__hsub2(*reinterpret_cast<__nv_bfloat162*>(&c), __floats2bfloat162_rn(144.f, 144.f)));
                 };
-                tile(std::integral_constant<int, 0>{});
-                tile(std::integral_constant<int, 1>{});
-                tile(std::integral_constant<int, 2>{});
-                tile(std::integral_constant<int, 3>{});
+                const std::integral_constant<int, 0> r0{};
+                const std::integral_constant<int, 1> r1{};
+                const std::integral_constant<int, 2> r2{};
+                const std::integral_constant<int, 3> r3{};
+                const uint4 v0 = make_uint4(code(r0, n0), code(r1, n0), code(r0, n1), code(r1, n1));
+                mma_bf16(acc.o[0][2 * b], v0, ph0, ph1);
+                mma_bf16(acc.o[0][2 * b], v0, pl0, pl1);
+                const uint4 v1 = make_uint4(code(r2, n0), code(r3, n0), code(r2, n1), code(r3, n1));
+                mma_bf16(acc.o[0][2 * b + 1], v1, ph0, ph1);
+                mma_bf16(acc.o[0][2 * b + 1], v1, pl0, pl1);
             }
         }
     }
+    // the stage's next copy comes by another proxy than clear_rows' writes
+    if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // Shared memory of the split kernel: query fragments, the join's sums, the
 // plan, then a ring of `stages` cells per warp.
-template <int NB, bool HL>
+template <int NB, int TILE>
 struct Smem {
     static constexpr int D = NB * 32;
-    static constexpr size_t qs = (size_t)(D / 16) * 512;
-    static constexpr size_t comb = (size_t)kCombine * (HL ? 8 : 16) * D * 4;
+    static constexpr size_t qs = (size_t)(D / 16) * (TILE == kT8 ? 256 : 512);
+    static constexpr size_t comb = (size_t)kCombine * queries_of<TILE>() * D * 4;
     __host__ __device__ static size_t ring(int E) { return (qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
 };
 
@@ -487,6 +560,12 @@ __device__ __forceinline__ Fragment fragment_at(const PlanEntry* plan, const Spl
     f.c0 = pe.c0;
     f.keys = pe.keys;
     return f;
+}
+
+// CTAs that share W cells: one each of its warps at least, so that a short
+// context is joined from few records
+__device__ __forceinline__ int ranges(const SplitArgs& a, long long W) {
+    return (int)min((long long)a.G, (W + a.warps - 1) / a.warps);
 }
 
 // CTAs whose ranges meet a key: [first, last]; G ranges of W in all
@@ -551,16 +630,16 @@ __device__ __forceinline__ void store_row(const SplitArgs& a, long long row, int
     }
 }
 
-template <int NB, bool F8, bool HL>
-__global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const SplitArgs a, const int stages) {
+template <int NB, bool F8, int TILE>
+__global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(const SplitArgs a, const int stages) {
     constexpr int D = NB * 32;
-    constexpr int kWarps = warps_of<NB>(), kThreads = kWarps * 32;
-    constexpr int QPI = HL ? 8 : 16;
-    constexpr int NR = HL ? 1 : 2;
+    constexpr int kWarps = warps_of<NB, TILE>(), kThreads = kWarps * 32;
+    constexpr bool HL = TILE == kF32;
+    constexpr int QPI = queries_of<TILE>(), NQ = QPI / 8;
     constexpr int CELL = NB * (F8 ? 1024 : 928);
-    using S = Smem<NB, HL>;
+    using S = Smem<NB, TILE>;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint4* qs = reinterpret_cast<uint4*>(smem);
+    uint8_t* qs = smem;
     float* comb = reinterpret_cast<float*>(smem + S::qs);
     PlanEntry* plan = reinterpret_cast<PlanEntry*>(smem + S::qs + S::comb);
     __shared__ RowInfo ri;
@@ -638,7 +717,7 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long W = plan[a.E].work * a.g.Hkv;
-    const int G = (int)min((long long)a.G, W);
+    const int G = ranges(a, W);
     if (a.fuse) {
         // entries without rows have no key: their outputs are zeros
         for (int e = blockIdx.x; e < a.E; e += gridDim.x) {
@@ -652,9 +731,9 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
     }
     if ((int)blockIdx.x >= G) return;
     const long long x0 = W * blockIdx.x / G, x1 = W * (blockIdx.x + 1) / G;
-    const int cpp = a.g.cells_per_page();
+    const int cpp = a.g.cells_per_page(), cps = a.g.page_shift - 4;       // cells a page, a power of two
     const uint32_t ring = dev::smem_u32(smem) + (uint32_t)S::ring(a.E) + (uint32_t)(warp * stages * CELL);
-    const uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
+    uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
     const uint32_t bar0 = dev::smem_u32(&s_bar[warp][0]);
 
     // ---- the producer side of this warp's ring: its cells (every kWarps-th of
@@ -693,14 +772,14 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
             pslot = ppage = -1;
             if (c < pcb) {
                 if (plist) {
-                    pslot = plist[c / cpp];
+                    pslot = plist[c >> cps];
                     if (pslot >= a.g.max_pages) {
                         atomicExch(a.g.err, kErrCounter);
                         pslot = -1;
                     }
-                    if (pslot >= 0 && pslot * a.g.page_rows + (c % cpp) * 16 >= phi) pslot = -1;
+                    if (pslot >= 0 && pslot * a.g.page_rows + (c & (cpp - 1)) * 16 >= phi) pslot = -1;
                 } else {
-                    pslot = (pc0 + c) / cpp;
+                    pslot = (pc0 + c) >> cps;
                 }
                 if (pslot >= 0) ppage = ptable[pslot];
                 if (pslot >= 0 && (ppage < 0 || ppage >= a.g.n_pages)) {
@@ -712,7 +791,7 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
         const int page = __shfl_sync(0xffffffffu, ppage, pidx), slot = __shfl_sync(0xffffffffu, pslot, pidx);
         if (lane == 0) {
             const uint32_t bar = bar0 + 8u * st;
-            const int in = (plist ? pc : pc0 + pc) % cpp;
+            const int in = (plist ? pc : pc0 + pc) & (cpp - 1);
             if (page >= 0) {
                 s_row0[warp][st] = slot * a.g.page_rows + in * 16;
                 dev::mbar_expect_tx(bar, CELL);
@@ -765,8 +844,11 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
             for (int b = 0; b < NB; ++b) {
                 const float y = v[b] * up;
                 const __half hi = __float2half_rn(y);
-                __half* dst = reinterpret_cast<__half*>(qs + (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j);
-                if (HL) {
+                const int at = (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
+                __half* dst = reinterpret_cast<__half*>(qs + at * (TILE == kT8 ? 8 : 16));
+                if (TILE == kT8) {
+                    dst[reg + half] = hi;
+                } else if (HL) {
                     dst[2 * reg + half] = hi;
                     dst[2 * (reg + 1) + half] = __float2half_rn(y - __half2float(hi));
                 } else {
@@ -796,13 +878,21 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
         }
         __syncthreads();
 
-        Acc<NB, F8, HL> acc;
+        const int g = lane >> 2, j = lane & 3;
+        Acc<NB, F8, TILE> acc;
+        LaneRows<NQ> lr;
 #pragma unroll
-        for (int n = 0; n < 4 * NB; ++n)
+        for (int r = 0; r < NQ; ++r) {
+            acc.m[r] = kNone;
+            acc.l[r] = 0.f;
+            lr.fac[r] = ri.fac[g + 8 * r];
+            lr.lo[r] = ri.lo[g + 8 * r];
+            lr.hi[r] = ri.hi[g + 8 * r];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc.o[n][i] = 0.f;
-        acc.m[0] = acc.m[1] = kNegInf;
-        acc.l[0] = acc.l[1] = 0.f;
+            for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc.o[r][n][i] = 0.f;
+        }
 #pragma unroll
         for (int b = 0; b < (HL && !F8 ? NB : 1); ++b) acc.mt[b] = 0.f;
 
@@ -811,7 +901,7 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
             const bool there = wait_stage(bar0 + 8u * st, phase, &s_abort, a.g.err);
             const int row0 = s_row0[warp][st];
             if (there && row0 >= 0 && row0 < ri.hi_max)
-                take_cell<NB, F8, HL>(a, ring_p + st * CELL, row0, qs, ri, lane, acc);
+                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, ri, lr, lane, acc);
             __syncwarp();
             if (there) produce(st);
             if (++st == stages) {
@@ -821,9 +911,8 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
         }
 
         // ---- join the warps: common reference, then sums passed down four warps at a time
-        const int g = lane >> 2, j = lane & 3;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < NQ; ++r) {
             acc.l[r] += __shfl_xor_sync(0xffffffffu, acc.l[r], 1);
             acc.l[r] += __shfl_xor_sync(0xffffffffu, acc.l[r], 2);
             if (j == 0) {
@@ -831,58 +920,63 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
                 s_l[warp][g + 8 * r] = acc.l[r];
             }
         }
-        if constexpr (HL) {
+        if constexpr (HL && !F8) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float t = 0.f;
-                if constexpr (!F8) {
-                    t = acc.mt[b];
-                    t += __shfl_xor_sync(0xffffffffu, t, 1);
-                    t += __shfl_xor_sync(0xffffffffu, t, 2);
-                }
+                float t = acc.mt[b];
+                t += __shfl_xor_sync(0xffffffffu, t, 1);
+                t += __shfl_xor_sync(0xffffffffu, t, 2);
+                const float t0 = __shfl_sync(0xffffffffu, t, 8 * j), t1 = __shfl_sync(0xffffffffu, t, 8 * j + 4);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    acc.o[4 * b + r][0] += acc.o[4 * b + r][2] + t;
-                    acc.o[4 * b + r][1] += acc.o[4 * b + r][3] + t;
+                for (int rp = 0; rp < 2; ++rp) {
+                    acc.o[0][2 * b + rp][0] += t0;
+                    acc.o[0][2 * b + rp][1] += t1;
+                    acc.o[0][2 * b + rp][2] += t0;
+                    acc.o[0][2 * b + rp][3] += t1;
                 }
             }
         }
         __syncthreads();
-        float M[2], L[2];
+        float M[NQ][2], L[NQ][2];                          // of queries 2j, 2j + 1 (+ 8)
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            M[r] = kNegInf;
-            L[r] = 0.f;
+        for (int r = 0; r < NQ; ++r)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M[r] = fmaxf(M[r], s_m[w][g + 8 * r]);
+            for (int i = 0; i < 2; ++i) {
+                const int row = 2 * j + i + 8 * r;
+                float m = kNone, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                if (s_m[w][g + 8 * r] != kNegInf) L[r] += s_l[w][g + 8 * r] * ex2(s_m[w][g + 8 * r] - M[r]);
-            const float fa = acc.m[r] == kNegInf ? 0.f : ex2(acc.m[r] - M[r]);
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][row]);
 #pragma unroll
-            for (int n = 0; n < 4 * NB; ++n) {
-                acc.o[n][2 * r] *= fa;
-                acc.o[n][2 * r + 1] *= fa;
+                for (int w = 0; w < kWarps; ++w) l = fmaf(s_l[w][row], ex2(s_m[w][row] - m), l);
+                const float fa = ex2(s_m[warp][row] - m);
+#pragma unroll
+                for (int n = 0; n < 2 * NB; ++n) {
+                    acc.o[r][n][i] *= fa;
+                    acc.o[r][n][2 + i] *= fa;
+                }
+                M[r][i] = l > 0.f ? m - kShift : kNegInf;
+                L[r][i] = l;
             }
-        }
         auto pass = [&](int lo, int n) {               // warps [lo + n, lo + 2n) add their sums to [lo, lo + n)
-            float2* buf = reinterpret_cast<float2*>(comb) + (size_t)(warp & (n - 1)) * (4 * NB * NR * 32);
+            float4* buf = reinterpret_cast<float4*>(comb) + (size_t)(warp & (n - 1)) * (2 * NB * NQ * 32);
             if (warp >= lo + n && warp < lo + 2 * n) {
 #pragma unroll
-                for (int i = 0; i < 4 * NB; ++i)
+                for (int r = 0; r < NQ; ++r)
 #pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        buf[(i * NR + r) * 32 + lane] = make_float2(acc.o[i][2 * r], acc.o[i][2 * r + 1]);
+                    for (int i = 0; i < 2 * NB; ++i)
+                        buf[(r * 2 * NB + i) * 32 + lane] = make_float4(acc.o[r][i][0], acc.o[r][i][1], acc.o[r][i][2], acc.o[r][i][3]);
             }
             __syncthreads();
             if (warp >= lo && warp < lo + n) {
 #pragma unroll
-                for (int i = 0; i < 4 * NB; ++i)
+                for (int r = 0; r < NQ; ++r)
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        const float2 y = buf[(i * NR + r) * 32 + lane];
-                        acc.o[i][2 * r] += y.x;
-                        acc.o[i][2 * r + 1] += y.y;
+                    for (int i = 0; i < 2 * NB; ++i) {
+                        const float4 y = buf[(r * 2 * NB + i) * 32 + lane];
+                        acc.o[r][i][0] += y.x;
+                        acc.o[r][i][1] += y.y;
+                        acc.o[r][i][2] += y.z;
+                        acc.o[r][i][3] += y.w;
                     }
             }
             __syncthreads();
@@ -897,41 +991,34 @@ __global__ void __launch_bounds__(warps_of<NB>() * 32, 1) split_kernel(const Spl
             const bool whole = a.fuse && n_rec == 1;
             const long long slot = blockIdx.x + key;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const int row = g + 8 * r;
-                if (row >= rows) continue;
-                if (whole) {
-                    const Query q = query_of(a, f.e, f.kh, f.sl * QPI + row);
-                    const float w = row_weight(a, q.h, M[r] == kNegInf ? kNegInf : M[r] - kShift, L[r]);
-                    const long long at = (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + 8 * j;
+            for (int r = 0; r < NQ; ++r)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        float y[8];
+                for (int i = 0; i < 2; ++i) {
+                    const int row = 2 * j + i + 8 * r;
+                    if (row >= rows) continue;
+                    if (whole) {
+                        const Query q = query_of(a, f.e, f.kh, f.sl * QPI + row);
+                        const float w = row_weight(a, q.h, M[r][i], L[r][i]);
+                        const long long at = (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + 4 * g;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = acc.o[4 * b + (i & 3)][2 * r + (i >> 2)] * w;
-                        if (a.bf16) {
-                            uint32_t w4[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) w4[i] = as_u32(__floats2bfloat162_rn(y[2 * i], y[2 * i + 1]));
-                            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at + 32 * b) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-                        } else {
-                            float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at + 32 * b);
-                            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                        for (int b = 0; b < NB; ++b) {
+                            const float y0 = acc.o[r][2 * b][i] * w, y1 = acc.o[r][2 * b][2 + i] * w;
+                            const float y2 = acc.o[r][2 * b + 1][i] * w, y3 = acc.o[r][2 * b + 1][2 + i] * w;
+                            if (a.bf16)
+                                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at + 32 * b) =
+                                    make_uint2(as_u32(__floats2bfloat162_rn(y0, y1)), as_u32(__floats2bfloat162_rn(y2, y3)));
+                            else
+                                *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at + 32 * b) = make_float4(y0, y1, y2, y3);
                         }
+                        continue;
                     }
-                    continue;
-                }
-                float* dst = a.part_o + (slot * a.rec_rows + row) * D + 8 * j;
+                    float* dst = a.part_o + (slot * a.rec_rows + row) * D + 4 * g;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    *reinterpret_cast<float4*>(dst + 32 * b) = make_float4(acc.o[4 * b][2 * r], acc.o[4 * b + 1][2 * r], acc.o[4 * b + 2][2 * r], acc.o[4 * b + 3][2 * r]);
-                    *reinterpret_cast<float4*>(dst + 32 * b + 4) = make_float4(acc.o[4 * b][2 * r + 1], acc.o[4 * b + 1][2 * r + 1], acc.o[4 * b + 2][2 * r + 1], acc.o[4 * b + 3][2 * r + 1]);
+                    for (int b = 0; b < NB; ++b)
+                        *reinterpret_cast<float4*>(dst + 32 * b) = make_float4(acc.o[r][2 * b][i], acc.o[r][2 * b][2 + i], acc.o[r][2 * b + 1][i], acc.o[r][2 * b + 1][2 + i]);
+                    if (g == 0)
+                        *reinterpret_cast<float2*>(a.part_ml + (slot * a.rec_rows + row) * 2) = make_float2(M[r][i], L[r][i]);
                 }
-                if (j == 0)
-                    *reinterpret_cast<float2*>(a.part_ml + (slot * a.rec_rows + row) * 2) =
-                        make_float2(M[r] == kNegInf ? kNegInf : M[r] - kShift, L[r]);
-            }
             if (a.fuse && n_rec > 1) {
                 // the CTA that completes a key's records joins them; the others go on
                 __threadfence();
@@ -980,7 +1067,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) 
     const int seq = st / a.T, t = st - seq * a.T;
     const int kh = h / a.hpk, hr = h - kh * a.hpk;
     const long long W = a.plan[a.E].work * a.g.Hkv;
-    const int G = (int)min((long long)a.G, W);
+    const int G = ranges(a, W);
     RowSum<NB> r;
     r.M = kNegInf;
     r.L = 0.f;
@@ -1005,18 +1092,18 @@ __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) 
     store_row<NB>(a, row, h, lane, r);
 }
 
-template <int NB, bool F8, bool HL>
+template <int NB, bool F8, int TILE>
 cudaError_t launch_split_t(const SplitArgs& a, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = kernel_attrs_once(split_kernel<NB, F8, HL>, done, true);
+    cudaError_t e = kernel_attrs_once(split_kernel<NB, F8, TILE>, done, true);
     if (e != cudaSuccess) return e;
-    using S = Smem<NB, HL>;
-    constexpr size_t cells = (size_t)warps_of<NB>() * NB * (F8 ? 1024 : 928);
-    // the ring takes what the plan leaves of 220 KB (2 to 8 stages)
+    using S = Smem<NB, TILE>;
+    constexpr size_t cells = (size_t)warps_of<NB, TILE>() * NB * (F8 ? 1024 : 928);
+    // the ring takes what the plan leaves of 220 KB
     const int stages = (int)std::min<size_t>(kMaxStages, (220 * 1024 - S::ring(a.E)) / cells);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.G);
-    cfg.blockDim = dim3(warps_of<NB>() * 32);
+    cfg.blockDim = dim3(warps_of<NB, TILE>() * 32);
     cfg.dynamicSmemBytes = S::ring(a.E) + stages * cells;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1024,18 +1111,30 @@ cudaError_t launch_split_t(const SplitArgs& a, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_kernel<NB, F8, HL>, a, stages);
+    return cudaLaunchKernelEx(&cfg, split_kernel<NB, F8, TILE>, a, stages);
+}
+
+template <int NB, bool F8>
+cudaError_t launch_split_f(const SplitArgs& a, cudaStream_t s) {
+    if (!a.bf16) return launch_split_t<NB, F8, kF32>(a, s);
+    return a.tile == 8 ? launch_split_t<NB, F8, kT8>(a, s) : launch_split_t<NB, F8, kT16>(a, s);
 }
 
 template <int NB>
 cudaError_t launch_split_nb(const SplitArgs& a, cudaStream_t s) {
-    if (a.g.fp8) return a.bf16 ? launch_split_t<NB, true, false>(a, s) : launch_split_t<NB, true, true>(a, s);
-    return a.bf16 ? launch_split_t<NB, false, false>(a, s) : launch_split_t<NB, false, true>(a, s);
+    return a.g.fp8 ? launch_split_f<NB, true>(a, s) : launch_split_f<NB, false>(a, s);
 }
 
 }  // namespace
 
-int split_queries(const SplitArgs& a) { return a.bf16 ? 16 : 8; }
+int split_tile(bool bf16, int most_queries) { return bf16 && most_queries > 8 ? 16 : 8; }
+
+int split_warps(int NB, int tile) {
+    if (tile == 16) return NB == 2 ? warps_of<2, kT16>() : NB == 4 ? warps_of<4, kT16>() : warps_of<8, kT16>();
+    return NB == 2 ? warps_of<2, kT8>() : NB == 4 ? warps_of<4, kT8>() : warps_of<8, kT8>();
+}
+static_assert(warps_of<2, kT8>() == warps_of<2, kF32>() && warps_of<4, kT8>() == warps_of<4, kF32>() &&
+              warps_of<8, kT8>() == warps_of<8, kF32>(), "tiles of 8 queries share a CTA size");
 
 cudaError_t launch_split(const SplitArgs& a, cudaStream_t s) {
     switch (a.g.NB()) {
@@ -1056,11 +1155,10 @@ cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const int qpi = split_queries(a);
     switch (a.g.NB()) {
-        case 2: return cudaLaunchKernelEx(&cfg, merge_kernel<2>, a, qpi);
-        case 4: return cudaLaunchKernelEx(&cfg, merge_kernel<4>, a, qpi);
-        default: return cudaLaunchKernelEx(&cfg, merge_kernel<8>, a, qpi);
+        case 2: return cudaLaunchKernelEx(&cfg, merge_kernel<2>, a, a.tile);
+        case 4: return cudaLaunchKernelEx(&cfg, merge_kernel<4>, a, a.tile);
+        default: return cudaLaunchKernelEx(&cfg, merge_kernel<8>, a, a.tile);
     }
 }
 
