@@ -139,10 +139,10 @@ struct PlanEntry;
 
 // Decode.  Work entries: sequences (dense), sequences then prefix groups
 // (shared), or (sequence, query row) pairs (sparse).  An entry has nc cells,
-// nq queries per KV head taken in slices of QPI, and its work is nc * slices *
-// Hkv cells; the CTAs cut the total into equal ranges.  The part of a CTA's
-// range inside one (entry, KV head, slice) key is a fragment and writes its
-// record to slot cta + key.
+// nq queries per KV head taken in slices of `tile`, and its work is nc * slices *
+// Hkv cells; the total is cut into equal ranges, one for each group of warps of
+// each CTA.  The part of a range inside one (entry, KV head, slice) key is a
+// fragment and writes its record to slot range + key.
 struct SplitArgs {
     Geom g;
     const void* q;
@@ -163,7 +163,7 @@ struct SplitArgs {
     int E;                         // work entries
     int G;                         // CTAs of the split kernel
     int tile;                      // queries of a slice (QPI): 8, or 16 for more bf16 queries
-    int warps;                     // warps of the split kernel's CTAs
+    int gw, groups;                // warps of a group, groups of a CTA of the split kernel
     int rec_rows;                  // query rows of a record: min(tile, most queries of a key)
     int fuse;                      // 1: the last CTA of a key joins its records (no merge kernel)
     int* arrived;                  // [key] records written; 0 between calls

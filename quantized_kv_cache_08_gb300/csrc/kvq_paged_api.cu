@@ -25,6 +25,8 @@ struct kvq_paged {
 namespace {
 
 constexpr int kMaxGrid = 256;          // most CTAs of a split kernel
+constexpr int kMaxRanges = 4 * kMaxGrid;
+constexpr int kManyKeys = 32;
 constexpr int kMaxT = 64;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -59,12 +61,12 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     l->page = l->cell * (R / kCellRows) * c->n_kv_heads;
     l->pool = l->page * c->n_pages;
     l->bounds = c->bounds ? round_up((size_t)c->n_pages * c->n_kv_heads * NB * 68, 16) : 0;
-    // record rows of a decode: 16 (8 for f32 queries) for each CTA, each key of
+    // record rows of a decode: 16 (8 for f32 queries) for each range, each key of
     // a sequence in whole slices, and the groups' queries, which are their
     // members', in whole slices too
     const size_t Qh = (size_t)(c->max_q_heads / c->n_kv_heads) * c->max_t;
     l->key_rows = (size_t)c->n_kv_heads * c->max_seqs * (round_up(Qh, 16) + Qh + 16);
-    const size_t recs = (size_t)kMaxGrid * 16 + l->key_rows;
+    const size_t recs = (size_t)kMaxRanges * 16 + l->key_rows;
     l->plan = 256;                                       // the error word comes first
     l->arrived = round_up(l->plan + (kMaxEntries + 1) * sizeof(PlanEntry), 256);
     l->ml = round_up(l->arrived + l->key_rows * sizeof(int), 256);
@@ -156,7 +158,13 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.G = std::min(c->num_sms, kMaxGrid);
     const int most = lists ? a.hpk : n_groups ? q->n_seq * a.hpk * q->T : a.hpk * q->T;
     a.tile = split_tile(a.bf16, most);
-    a.warps = split_warps(a.g.NB(), a.tile);
+    // many keys: four warps a group, for a fragment's end and start are hidden
+    // behind the other groups; few keys: the whole CTA, for a quarter of the
+    // records to join
+    const int warps = split_warps(a.g.NB(), a.tile);
+    const long long keys = (long long)a.E * c->cfg.n_kv_heads * ((most + a.tile - 1) / a.tile);
+    a.gw = keys >= kManyKeys ? 4 : warps;
+    a.groups = warps / a.gw;
     a.rec_rows = std::min(a.tile, most);
     a.max_keys = (long long)(c->key_rows / a.rec_rows);
     a.plan = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan);

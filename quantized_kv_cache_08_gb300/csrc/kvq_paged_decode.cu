@@ -44,7 +44,7 @@ using dev::kLazy;
 using dev::kNegInf;
 constexpr float kShift = 6.0f;         // p is held as 2^6 p: fp16 keeps 2^-20 of the largest in full
 constexpr int kMaxStages = 8;
-constexpr int kCombine = 4;            // warps' sums that the join holds at once
+constexpr int kMaxGroups = 4;          // groups of warps in a CTA
 
 // Query tiles: 8 or 16 bf16 queries, or 8 of f32 in two parts
 enum Tile { kT8 = 0, kT16 = 1, kF32 = 2 };
@@ -516,14 +516,14 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
     if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Shared memory of the split kernel: query fragments, the join's sums, the
-// plan, then a ring of `stages` cells per warp.
+// Shared memory of the split kernel: query fragments of each group, the joins'
+// sums, the plan, then a ring of `stages` cells per warp.
 template <int NB, int TILE>
 struct Smem {
     static constexpr int D = NB * 32;
     static constexpr size_t qs = (size_t)(D / 16) * (TILE == kT8 ? 256 : 512);
-    static constexpr size_t comb = (size_t)kCombine * queries_of<TILE>() * D * 4;
-    __host__ __device__ static size_t ring(int E) { return (qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
+    static constexpr size_t comb = (size_t)warps_of<NB, TILE>() / 2 * queries_of<TILE>() * D * 4;
+    __host__ __device__ static size_t ring(int E) { return (kMaxGroups * qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
 };
 
 // Bounded wait for a stage; false once any wait of the CTA has run out.
@@ -541,7 +541,7 @@ __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volati
     }
 }
 
-// A part of a CTA's range: key kk (KV head kh, slice sl) of entry e, cells [ca, cb)
+// A part of a range: key kk (KV head kh, slice sl) of entry e, cells [ca, cb)
 struct Fragment {
     int e, kk, kh, sl, nsl, nq, c0, ca, cb, keys;
 };
@@ -562,16 +562,18 @@ __device__ __forceinline__ Fragment fragment_at(const PlanEntry* plan, const Spl
     return f;
 }
 
-// CTAs that share W cells: one each of its warps at least, so that a short
-// context is joined from few records
+// Ranges that W cells are cut into: one for each group of warps, and a cell
+// for each of its warps at least, so that a short context is joined from few
+// records
 __device__ __forceinline__ int ranges(const SplitArgs& a, long long W) {
-    return (int)min((long long)a.G, (W + a.warps - 1) / a.warps);
+    return (int)min((long long)a.G * a.groups, (W + a.gw - 1) / a.gw);
 }
 
-// CTAs whose ranges meet a key: [first, last]; G ranges of W in all
-__device__ __forceinline__ int cta_of(long long x, int G, long long W) { return (int)(((x + 1) * G - 1) / W); }
+// The range that holds cell x; G ranges of W cells in all
+__device__ __forceinline__ int range_of(long long x, int G, long long W) { return (int)(((x + 1) * G - 1) / W); }
 
-// The sums of one output row over records first + key .. last + key
+// The sums of one output row over its key's records; a lane holds elements
+// 2 lane, + 1 (NB 2) or 4 lane .. + 3 of each 128
 template <int NB>
 struct RowSum {
     float M, L, o[NB];
@@ -597,12 +599,24 @@ __device__ __forceinline__ void fold_records(const SplitArgs& a, long long slot0
         r.L = r.L * al + l;
 #pragma unroll
         for (int i = 0; i < NB; ++i) r.o[i] *= al;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = 0; k < n; ++k) {
             const float wk = __shfl_sync(0xffffffffu, w, k);
-            const float* src = a.part_o + ((slot0 + base + k) * a.rec_rows + rr) * D + lane;
+            const float* src = a.part_o + ((slot0 + base + k) * a.rec_rows + rr) * D;
+            if constexpr (NB == 2) {
+                const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+                r.o[0] = fmaf(wk, y.x, r.o[0]);
+                r.o[1] = fmaf(wk, y.y, r.o[1]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) r.o[i] = fmaf(wk, __ldcg(src + 32 * i), r.o[i]);
+                for (int i = 0; i < NB; i += 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + 8 * i + lane);
+                    r.o[i] = fmaf(wk, y.x, r.o[i]);
+                    r.o[i + 1] = fmaf(wk, y.y, r.o[i + 1]);
+                    r.o[i + 2] = fmaf(wk, y.z, r.o[i + 2]);
+                    r.o[i + 3] = fmaf(wk, y.w, r.o[i + 3]);
+                }
+            }
         }
     }
 }
@@ -623,10 +637,11 @@ template <int NB>
 __device__ __forceinline__ void store_row(const SplitArgs& a, long long row, int h, int lane, const RowSum<NB>& r) {
     const float w = row_weight(a, h, r.M, r.L);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        const long long at = row * (NB * 32) + 32 * i + lane;
-        if (a.bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16(r.o[i] * w);
-        else reinterpret_cast<float*>(a.out)[at] = r.o[i] * w;
+    for (int i = 0; i < NB; i += 2) {
+        const long long at = row * (NB * 32) + (NB == 2 ? 2 * lane : 32 * (i & ~3) + 4 * lane + (i & 2));
+        const float x = r.o[i] * w, y = r.o[i + 1] * w;
+        if (a.bf16) *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + at) = as_u32(__floats2bfloat162_rn(x, y));
+        else *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at) = make_float2(x, y);
     }
 }
 
@@ -639,16 +654,14 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     constexpr int CELL = NB * (F8 ? 1024 : 928);
     using S = Smem<NB, TILE>;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* qs = smem;
-    float* comb = reinterpret_cast<float*>(smem + S::qs);
-    PlanEntry* plan = reinterpret_cast<PlanEntry*>(smem + S::qs + S::comb);
-    __shared__ RowInfo ri;
+    PlanEntry* plan = reinterpret_cast<PlanEntry*>(smem + kMaxGroups * S::qs + S::comb);
+    __shared__ RowInfo s_ri[kMaxGroups];
     __shared__ float s_m[kWarps][16], s_l[kWarps][16];
     __shared__ long long s_wsum[kWarps];
     __shared__ int s_ksum[kWarps];
     __shared__ int s_row0[kWarps][kMaxStages];        // first row of the cell in a stage, -1: none
     __shared__ __align__(8) uint64_t s_bar[kWarps][kMaxStages];
-    __shared__ int s_abort, s_last;
+    __shared__ int s_abort, s_last[kMaxGroups];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (lane < stages) dev::mbar_init(dev::smem_u32(&s_bar[warp][lane]), 1);
@@ -729,14 +742,22 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             }
         }
     }
-    if ((int)blockIdx.x >= G) return;
-    const long long x0 = W * blockIdx.x / G, x1 = W * (blockIdx.x + 1) / G;
+    // ---- the CTA's groups of gw warps work on ranges of their own: while one
+    // group joins and changes keys (some 5 us of latencies) the others compute
+    const int gw = a.gw, group = warp / gw, gwarp = warp - group * gw;
+    const int range = group * gridDim.x + blockIdx.x;
+    if (range >= G) return;
+    const long long x0 = W * range / G, x1 = W * (range + 1) / G;
+    uint8_t* qs = smem + group * S::qs;
+    float* comb = reinterpret_cast<float*>(smem + kMaxGroups * S::qs) + (size_t)group * (gw / 2) * QPI * D;
+    RowInfo& ri = s_ri[group];
+    auto sync_group = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gw * 32) : "memory"); };
     const int cpp = a.g.cells_per_page(), cps = a.g.page_shift - 4;       // cells a page, a power of two
     const uint32_t ring = dev::smem_u32(smem) + (uint32_t)S::ring(a.E) + (uint32_t)(warp * stages * CELL);
     uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
     const uint32_t bar0 = dev::smem_u32(&s_bar[warp][0]);
 
-    // ---- the producer side of this warp's ring: its cells (every kWarps-th of
+    // ---- the producer side of this warp's ring: its cells (every gw-th of
     // each fragment) in order, `stages` ahead of their use.  Lanes look up the
     // pages of 32 cells at once.
     long long px = x0;                                  // first cell after the producer's fragment
@@ -751,7 +772,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 if (px >= x1) return;
                 const Fragment f = fragment_at(plan, a, QPI, px, x1);
                 px += f.cb - f.ca;
-                pc = f.ca + warp;
+                pc = f.ca + gwarp;
                 if (pc >= f.cb) continue;
                 pcb = f.cb;
                 pc0 = f.c0;
@@ -768,7 +789,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         }
         if (pidx == 32) {
             pidx = 0;
-            const int c = pc + lane * kWarps;
+            const int c = pc + lane * gw;
             pslot = ppage = -1;
             if (c < pcb) {
                 if (plist) {
@@ -802,7 +823,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             }
         }
         ++pidx;
-        pc += kWarps;
+        pc += gw;
     };
     for (int st = 0; st < stages; ++st) produce(st);
 
@@ -815,8 +836,8 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         x += f.cb - f.ca;
 
         // ---- its queries, as A fragments in shared memory
-        __syncthreads();
-        for (int r = warp; r < QPI; r += kWarps) {
+        sync_group();
+        for (int r = gwarp; r < QPI; r += gw) {
             const int qi = f.sl * QPI + r;
             Query q{0, 0, 0, 0, -1};
             float v[NB];
@@ -856,8 +877,8 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 }
             }
         }
-        __syncthreads();
-        if (warp == 0) {
+        sync_group();
+        if (gwarp == 0) {
             const bool v = lane < QPI && f.sl * QPI + lane < f.nq;
             int lo_max = v ? ri.lo[lane] : 0, hi_min = v ? ri.hi[lane] : 0x7fffffff;
             int lo_min = v ? ri.lo[lane] : 0x7fffffff, hi_max = v ? ri.hi[lane] : 0;
@@ -876,7 +897,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 ri.hi_max = hi_max;
             }
         }
-        __syncthreads();
+        sync_group();
 
         const int g = lane >> 2, j = lane & 3;
         Acc<NB, F8, TILE> acc;
@@ -897,7 +918,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         for (int b = 0; b < (HL && !F8 ? NB : 1); ++b) acc.mt[b] = 0.f;
 
         // ---- its cells, warp by warp
-        for (int c = f.ca + warp; c < f.cb; c += kWarps) {
+        for (int c = f.ca + gwarp; c < f.cb; c += gw) {
             const bool there = wait_stage(bar0 + 8u * st, phase, &s_abort, a.g.err);
             const int row0 = s_row0[warp][st];
             if (there && row0 >= 0 && row0 < ri.hi_max)
@@ -910,7 +931,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             }
         }
 
-        // ---- join the warps: common reference, then sums passed down four warps at a time
+        // ---- join the group's warps: common reference, then sums passed down
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
             acc.l[r] += __shfl_xor_sync(0xffffffffu, acc.l[r], 1);
@@ -936,7 +957,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 }
             }
         }
-        __syncthreads();
+        sync_group();
         float M[NQ][2], L[NQ][2];                          // of queries 2j, 2j + 1 (+ 8)
 #pragma unroll
         for (int r = 0; r < NQ; ++r)
@@ -944,10 +965,11 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             for (int i = 0; i < 2; ++i) {
                 const int row = 2 * j + i + 8 * r;
                 float m = kNone, l = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][row]);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) l = fmaf(s_l[w][row], ex2(s_m[w][row] - m), l);
+                const int w0 = warp - gwarp;
+#pragma unroll 4
+                for (int w = w0; w < w0 + gw; ++w) m = fmaxf(m, s_m[w][row]);
+#pragma unroll 4
+                for (int w = w0; w < w0 + gw; ++w) l = fmaf(s_l[w][row], ex2(s_m[w][row] - m), l);
                 const float fa = ex2(s_m[warp][row] - m);
 #pragma unroll
                 for (int n = 0; n < 2 * NB; ++n) {
@@ -958,16 +980,16 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 L[r][i] = l;
             }
         auto pass = [&](int lo, int n) {               // warps [lo + n, lo + 2n) add their sums to [lo, lo + n)
-            float4* buf = reinterpret_cast<float4*>(comb) + (size_t)(warp & (n - 1)) * (2 * NB * NQ * 32);
-            if (warp >= lo + n && warp < lo + 2 * n) {
+            float4* buf = reinterpret_cast<float4*>(comb) + (size_t)(gwarp & (n - 1)) * (2 * NB * NQ * 32);
+            if (gwarp >= lo + n && gwarp < lo + 2 * n) {
 #pragma unroll
                 for (int r = 0; r < NQ; ++r)
 #pragma unroll
                     for (int i = 0; i < 2 * NB; ++i)
                         buf[(r * 2 * NB + i) * 32 + lane] = make_float4(acc.o[r][i][0], acc.o[r][i][1], acc.o[r][i][2], acc.o[r][i][3]);
             }
-            __syncthreads();
-            if (warp >= lo && warp < lo + n) {
+            sync_group();
+            if (gwarp >= lo && gwarp < lo + n) {
 #pragma unroll
                 for (int r = 0; r < NQ; ++r)
 #pragma unroll
@@ -979,17 +1001,18 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                         acc.o[r][i][3] += y.w;
                     }
             }
-            __syncthreads();
+            sync_group();
         };
-        for (int lo = kWarps - 2 * kCombine; lo >= 0; lo -= kCombine) pass(lo, kCombine);
-        for (int n = kCombine / 2; n >= 1; n >>= 1) pass(0, n);
+        const int n0 = gw & (gw - 1) ? 4 : gw / 2;         // 12 warps: 4 onto 4 onto 4
+        for (int lo = gw - 2 * n0; lo >= 0; lo -= n0) pass(lo, n0);
+        for (int n = n0 / 2; n >= 1; n >>= 1) pass(0, n);
 
-        const int cta0 = cta_of(xa, G, W), n_rec = cta_of(xb - 1, G, W) - cta0 + 1;
+        const int rec0 = range_of(xa, G, W), n_rec = range_of(xb - 1, G, W) - rec0 + 1;
         const long long key = (long long)f.keys * a.g.Hkv + f.kk;
         const int rows = min(QPI, f.nq - f.sl * QPI);
-        if (warp == 0) {
+        if (gwarp == 0) {
             const bool whole = a.fuse && n_rec == 1;
-            const long long slot = blockIdx.x + key;
+            const long long slot = range + key;
 #pragma unroll
             for (int r = 0; r < NQ; ++r)
 #pragma unroll
@@ -1020,27 +1043,27 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                         *reinterpret_cast<float2*>(a.part_ml + (slot * a.rec_rows + row) * 2) = make_float2(M[r][i], L[r][i]);
                 }
             if (a.fuse && n_rec > 1) {
-                // the CTA that completes a key's records joins them; the others go on
+                // the group that completes a key's records joins them; the others go on
                 __threadfence();
                 __syncwarp();
                 if (lane == 0) {
                     const bool last = atomicAdd(a.arrived + key, 1) == n_rec - 1;
                     if (last) a.arrived[key] = 0;
-                    s_last = last;
+                    s_last[group] = last;
                     __threadfence();
                 }
             }
         }
         if (a.fuse && n_rec > 1) {
-            __syncthreads();
-            if (s_last) {
-                for (int rr = warp; rr < rows; rr += kWarps) {
+            sync_group();
+            if (s_last[group]) {
+                for (int rr = gwarp; rr < rows; rr += gw) {
                     RowSum<NB> r;
                     r.M = kNegInf;
                     r.L = 0.f;
 #pragma unroll
                     for (int i = 0; i < NB; ++i) r.o[i] = 0.f;
-                    fold_records<NB>(a, cta0 + key, n_rec, rr, lane, r);
+                    fold_records<NB>(a, rec0 + key, n_rec, rr, lane, r);
                     const Query q = query_of(a, f.e, f.kh, f.sl * QPI + rr);
                     store_row<NB>(a, ((long long)q.seq * a.T + q.t) * a.Hq + q.h, q.h, lane, r);
                 }
@@ -1079,7 +1102,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) 
         const int nsl = (pe.pad + QPI - 1) / QPI;
         const int kk = kh * nsl + qi / QPI;
         const long long xa = pe.work * a.g.Hkv + (long long)kk * pe.nc;
-        const int c0 = cta_of(xa, G, W), c1 = cta_of(xa + pe.nc - 1, G, W);
+        const int c0 = range_of(xa, G, W), c1 = range_of(xa + pe.nc - 1, G, W);
         fold_records<NB>(a, (long long)pe.keys * a.g.Hkv + kk + c0, c1 - c0 + 1, qi % QPI, lane, r);
     };
     fold(seq, t * a.hpk + hr);
