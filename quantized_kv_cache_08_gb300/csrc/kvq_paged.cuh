@@ -139,8 +139,8 @@ struct PlanEntry;
 
 // Decode.  Work entries: sequences (dense), sequences then prefix groups
 // (shared), or (sequence, query row) pairs (sparse).  An entry has nc cells,
-// nq queries per KV head taken in slices of `tile`, and its work is nc * slices *
-// Hkv cells; the total is cut into equal ranges, one for each group of warps of
+// nq queries per KV head taken in slices of `tile`, and its work is (nc + setup) *
+// slices * Hkv; the total is cut into equal ranges, one for each group of warps of
 // each CTA.  The part of a range inside one (entry, KV head, slice) key is a
 // fragment and writes its record to slot range + key.
 struct SplitArgs {
@@ -163,6 +163,7 @@ struct SplitArgs {
     int E;                         // work entries
     int G;                         // CTAs of the split kernel
     int tile;                      // queries of a slice (QPI): 8, or 16 for more bf16 queries
+    int setup;                     // what starting a key costs, in cells
     int gw, groups;                // warps of a group, groups of a CTA of the split kernel
     int rec_rows;                  // query rows of a record: min(tile, most queries of a key)
     int fuse;                      // 1: the last CTA of a key joins its records (no merge kernel)

@@ -165,6 +165,7 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     const long long keys = (long long)a.E * c->cfg.n_kv_heads * ((most + a.tile - 1) / a.tile);
     a.gw = keys >= kManyKeys ? 4 : warps;
     a.groups = warps / a.gw;
+    a.setup = a.gw == 4 ? 8 : 32;
     a.rec_rows = std::min(a.tile, most);
     a.max_keys = (long long)(c->key_rows / a.rec_rows);
     a.plan = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan);

@@ -247,24 +247,25 @@ struct Acc {
     float mt[TILE == kF32 && !F8 ? NB : 1];               // sum p (m + 16 d) of query g
 };
 
+// The queries of a fragment: factor of a score, rows seen
 struct RowInfo {
     float fac[16];
     int lo[16], hi[16];
-    int lo_min, lo_max, hi_min, hi_max;
 };
 
-// Per-lane facts of a fragment's queries g (+ 8)
+// What a lane keeps of them: queries g (+ 8), and the extremes over all
 template <int NQ>
 struct LaneRows {
     float fac[NQ];
     int lo[NQ], hi[NQ];
+    int lo_min, lo_max, hi_min, hi_max;
 };
 
 constexpr float kNone = -1e30f;        // reference of a query that has seen no row: any score passes it
 
 // Values of rows that no query sees, in the staged cell: zeroed, for they may be any bytes
-template <int NB, bool F8>
-__device__ __forceinline__ void clear_rows(uint8_t* cell, int row0, const RowInfo& ri, int lane) {
+template <int NB, bool F8, typename Rows>
+__device__ __forceinline__ void clear_rows(uint8_t* cell, int row0, const Rows& ri, int lane) {
     if constexpr (F8) {
         const int j = lane & 3;
 #pragma unroll
@@ -294,13 +295,12 @@ __device__ __forceinline__ void clear_rows(uint8_t* cell, int row0, const RowInf
 // One staged cell, 16 rows from logical row row0 on, into the warp's accumulators
 template <int NB, bool F8, int TILE>
 __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int row0, const uint8_t* __restrict__ qs,
-                                          const RowInfo& ri, const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane,
-                                          Acc<NB, F8, TILE>& acc) {
+                                          const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane, Acc<NB, F8, TILE>& acc) {
     constexpr bool HL = TILE == kF32;
     constexpr int NQ = Acc<NB, F8, TILE>::NQ;
     const int j = lane & 3;
-    const bool edge = row0 < ri.lo_max || row0 + 16 > ri.hi_min;
-    if (edge) clear_rows<NB, F8>(cell, row0, ri, lane);
+    const bool edge = row0 < lr.lo_max || row0 + 16 > lr.hi_min;
+    if (edge) clear_rows<NB, F8>(cell, row0, lr, lane);
     // ---- scores
     float sc[2][4];
 #pragma unroll
@@ -522,7 +522,7 @@ template <int NB, int TILE>
 struct Smem {
     static constexpr int D = NB * 32;
     static constexpr size_t qs = (size_t)(D / 16) * (TILE == kT8 ? 256 : 512);
-    static constexpr size_t comb = (size_t)warps_of<NB, TILE>() / 2 * queries_of<TILE>() * D * 4;
+    static constexpr size_t comb = (size_t)warps_of<NB, TILE>() / 2 * queries_of<TILE>() * (D + 4) * 4;
     __host__ __device__ static size_t ring(int E) { return (kMaxGroups * qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
 };
 
@@ -541,117 +541,139 @@ __device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volati
     }
 }
 
+// x g / d and x / d for 0 <= x, in 32 bits where they fit
+__device__ __forceinline__ long long mul_div(long long x, int g, long long d) {
+    const unsigned long long n = (unsigned long long)x * (unsigned)g;
+    if (((n | (unsigned long long)d) >> 32) == 0) return (unsigned)n / (unsigned)d;
+    return (long long)(n / (unsigned long long)d);
+}
+
 // A part of a range: key kk (KV head kh, slice sl) of entry e, cells [ca, cb)
+// (none where the part lies in the key's setup), and the work of it.  base: the
+// key's first unit of work.
 struct Fragment {
-    int e, kk, kh, sl, nsl, nq, c0, ca, cb, keys;
+    int e, kk, kh, sl, nsl, nq, c0, nc, ca, cb, keys, work;
+    long long base;
 };
 __device__ __forceinline__ Fragment fragment_at(const PlanEntry* plan, const SplitArgs& a, int QPI, long long x, long long x1) {
     Fragment f;
-    f.e = find_entry(plan, a.E, x / a.g.Hkv);
+    f.e = find_entry(plan, a.E, mul_div(x, 1, a.g.Hkv));
     const PlanEntry pe = plan[f.e];
-    const long long rel = x - pe.work * a.g.Hkv;
-    f.kk = (int)(rel / pe.nc);
-    f.ca = (int)(rel - (long long)f.kk * pe.nc);
-    f.cb = (int)min((long long)pe.nc, f.ca + (x1 - x));
+    const long long first = pe.work * a.g.Hkv;
+    const int len = pe.nc + a.setup;
+    f.kk = (int)mul_div(x - first, 1, len);
+    f.base = first + (long long)f.kk * len;
+    const int va = (int)(x - f.base), vb = (int)min((long long)len, va + (x1 - x));
+    f.work = vb - va;
+    f.ca = max(0, va - a.setup);
+    f.cb = max(0, vb - a.setup);
     f.nq = pe.pad;
     f.nsl = (pe.pad + QPI - 1) / QPI;
     f.kh = f.kk / f.nsl;
     f.sl = f.kk - f.kh * f.nsl;
     f.c0 = pe.c0;
+    f.nc = pe.nc;
     f.keys = pe.keys;
     return f;
 }
 
-// Ranges that W cells are cut into: one for each group of warps, and a cell
-// for each of its warps at least, so that a short context is joined from few
-// records
+// Ranges that W units of work (cells, and `setup` for each key) are cut into:
+// one for each group of warps, and about a cell for each of its warps at least,
+// so that a short context is joined from few records
 __device__ __forceinline__ int ranges(const SplitArgs& a, long long W) {
-    return (int)min((long long)a.G * a.groups, (W + a.gw - 1) / a.gw);
+    const int least = a.gw + a.setup;
+    return (int)min((long long)a.G * a.groups, (W + least - 1) / least);
 }
 
-// The range that holds cell x; G ranges of W cells in all
-__device__ __forceinline__ int range_of(long long x, int G, long long W) { return (int)(((x + 1) * G - 1) / W); }
+// The range that holds unit x of W units of work in G ranges
+__device__ __forceinline__ int range_of(long long x, int G, long long W) {
+    const unsigned long long n = (unsigned long long)(x + 1) * (unsigned)G - 1;
+    if (((n | (unsigned long long)W) >> 32) == 0) return (int)((unsigned)n / (unsigned)W);
+    return (int)(n / (unsigned long long)W);
+}
 
-// The sums of one output row over its key's records; a lane holds elements
-// 2 lane, + 1 (NB 2) or 4 lane .. + 3 of each 128
-template <int NB>
-struct RowSum {
-    float M, L, o[NB];
+// Weight of a row's sums in its output, the sink (log2 units, -inf: none) taken in
+__device__ __forceinline__ float sink_weight(float sink, float M, float L) {
+    if (M == kNegInf) return 0.f;
+    if (sink == kNegInf) return 1.0f / L;
+    const float m = fmaxf(M, sink);
+    const float al = ex2(M - m);
+    return al / (L * al + ex2(sink - m));
+}
+__device__ __forceinline__ float sink_of(const SplitArgs& a, int h) {
+    return a.sinks ? a.sinks[h] * 1.4426950408889634f : kNegInf;
+}
+
+// Four consecutive elements of an output row
+__device__ __forceinline__ void store4(const SplitArgs& a, long long at, const float4& o, float w) {
+    if (a.bf16)
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+            make_uint2(as_u32(__floats2bfloat162_rn(o.x * w, o.y * w)), as_u32(__floats2bfloat162_rn(o.z * w, o.w * w)));
+    else
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
+}
+
+// Four elements of an output row summed over the records first, first + step ..
+// below last (slots of one key)
+struct Sum4 {
+    float M, L;
+    float4 o;
 };
-template <int NB>
-__device__ __forceinline__ void fold_records(const SplitArgs& a, long long slot0, int n_rec, int rr, int lane, RowSum<NB>& r) {
-    constexpr int D = NB * 32;
-    for (int base = 0; base < n_rec; base += 32) {
-        const int n = min(32, n_rec - base);
-        float2 ml = make_float2(kNegInf, 0.f);
-        if (lane < n) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + ((slot0 + base + lane) * a.rec_rows + rr) * 2));
-        float m = ml.x;
+__device__ __forceinline__ void add_sum(Sum4& s, float M, float L, const float4& o) {
+    const float m = fmaxf(s.M, M);
+    if (m == kNegInf) return;
+    const float x = s.M == kNegInf ? 0.f : ex2(s.M - m), y = M == kNegInf ? 0.f : ex2(M - m);
+    s.M = m;
+    s.L = s.L * x + L * y;
+    s.o.x = s.o.x * x + o.x * y;
+    s.o.y = s.o.y * x + o.y * y;
+    s.o.z = s.o.z * x + o.z * y;
+    s.o.w = s.o.w * x + o.w * y;
+}
+template <int D>
+__device__ __forceinline__ void add_records(const SplitArgs& a, Sum4& s, long long slot0, int first, int last, int step, int row, int col) {
+    constexpr int U = 8;                               // records in flight
+    for (int r0 = first; r0 < last; r0 += U * step) {
+        float2 ml[U];
+        float4 o[U];
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-        m = fmaxf(m, r.M);
-        if (m == kNegInf) continue;
-        const float al = r.M == kNegInf ? 0.f : ex2(r.M - m);
-        r.M = m;
-        const float w = ml.x == kNegInf ? 0.f : ex2(ml.x - m);
-        float l = ml.y * w;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-        r.L = r.L * al + l;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) r.o[i] *= al;
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            const float* src = a.part_o + ((slot0 + base + k) * a.rec_rows + rr) * D;
-            if constexpr (NB == 2) {
-                const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-                r.o[0] = fmaf(wk, y.x, r.o[0]);
-                r.o[1] = fmaf(wk, y.y, r.o[1]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < NB; i += 4) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + 8 * i + lane);
-                    r.o[i] = fmaf(wk, y.x, r.o[i]);
-                    r.o[i + 1] = fmaf(wk, y.y, r.o[i + 1]);
-                    r.o[i + 2] = fmaf(wk, y.z, r.o[i + 2]);
-                    r.o[i + 3] = fmaf(wk, y.w, r.o[i + 3]);
-                }
+        for (int i = 0; i < U; ++i) {
+            ml[i] = make_float2(kNegInf, 0.f);
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r0 + i * step < last) {
+                const long long at = (slot0 + r0 + i * step) * a.rec_rows + row;
+                ml[i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
+                o[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
             }
         }
-    }
-}
-
-// Weight of a row's sums in its output, the sink taken in: out = o * weight
-__device__ __forceinline__ float row_weight(const SplitArgs& a, int h, float M, float L) {
-    if (M == kNegInf) return 0.f;
-    if (a.sinks) {
-        const float s = a.sinks[h] * 1.4426950408889634f;
-        const float m = fmaxf(M, s);
-        const float al = ex2(M - m);
-        return al / (L * al + ex2(s - m));
-    }
-    return 1.0f / L;
-}
-
-template <int NB>
-__device__ __forceinline__ void store_row(const SplitArgs& a, long long row, int h, int lane, const RowSum<NB>& r) {
-    const float w = row_weight(a, h, r.M, r.L);
+        float m = s.M;
 #pragma unroll
-    for (int i = 0; i < NB; i += 2) {
-        const long long at = row * (NB * 32) + (NB == 2 ? 2 * lane : 32 * (i & ~3) + 4 * lane + (i & 2));
-        const float x = r.o[i] * w, y = r.o[i + 1] * w;
-        if (a.bf16) *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + at) = as_u32(__floats2bfloat162_rn(x, y));
-        else *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at) = make_float2(x, y);
+        for (int i = 0; i < U; ++i) m = fmaxf(m, ml[i].x);
+        if (m == kNegInf) continue;
+        const float al = s.M == kNegInf ? 0.f : ex2(s.M - m);
+        s.M = m;
+        s.L *= al;
+        s.o.x *= al; s.o.y *= al; s.o.z *= al; s.o.w *= al;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const float w = ml[i].x == kNegInf ? 0.f : ex2(ml[i].x - m);
+            s.L = fmaf(ml[i].y, w, s.L);
+            s.o.x = fmaf(o[i].x, w, s.o.x);
+            s.o.y = fmaf(o[i].y, w, s.o.y);
+            s.o.z = fmaf(o[i].z, w, s.o.z);
+            s.o.w = fmaf(o[i].w, w, s.o.w);
+        }
     }
 }
 
 template <int NB, bool F8, int TILE>
 __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(const SplitArgs a, const int stages) {
-    constexpr int D = NB * 32;
+    constexpr int D = NB * 32, D4 = D / 4;
     constexpr int kWarps = warps_of<NB, TILE>(), kThreads = kWarps * 32;
     constexpr bool HL = TILE == kF32;
     constexpr int QPI = queries_of<TILE>(), NQ = QPI / 8;
     constexpr int CELL = NB * (F8 ? 1024 : 928);
+    constexpr int PAD = D + 4;                        // row stride of the joins' sums: lanes of a store in different banks
     using S = Smem<NB, TILE>;
     extern __shared__ __align__(128) uint8_t smem[];
     PlanEntry* plan = reinterpret_cast<PlanEntry*>(smem + kMaxGroups * S::qs + S::comb);
@@ -668,61 +690,71 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     if (tid == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // ---- the plan: prefix sums of the entries' work
+    // ---- the plan: prefix sums of the entries' work (one warp's scan for up to
+    // 32 entries, else every thread's share and a scan over the CTA)
     {
         const int per = (a.E + kThreads - 1) / kThreads;
+        const bool one_warp = a.E <= 32;
         long long w = 0;
         int k = 0;
-        for (int i = 0; i < per; ++i) {
-            const int e = tid * per + i;
-            if (e < a.E) {
-                const EntryWork ew = entry_work(a, e, blockIdx.x == 0);
-                const int sl = (ew.nq + QPI - 1) / QPI;
-                plan[e].nc = ew.nc;
-                plan[e].c0 = ew.c0;
-                plan[e].pad = ew.nq;
-                plan[e].work = w;
-                plan[e].keys = k;
-                w += (long long)ew.nc * sl;
-                k += sl;
+        if (!one_warp || warp == 0) {
+            for (int i = 0; i < per; ++i) {
+                const int e = tid * per + i;
+                if (e < a.E) {
+                    const EntryWork ew = entry_work(a, e, blockIdx.x == 0);
+                    const int sl = (ew.nq + QPI - 1) / QPI;
+                    plan[e].nc = ew.nc;
+                    plan[e].c0 = ew.c0;
+                    plan[e].pad = ew.nq;
+                    plan[e].work = w;
+                    plan[e].keys = k;
+                    w += ew.nc ? (long long)(ew.nc + a.setup) * sl : 0;
+                    k += sl;
+                }
             }
         }
         long long wi = w;
         int ki = k;
+        if (!one_warp || warp == 0) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, wi, o);
-            const int z = __shfl_up_sync(0xffffffffu, ki, o);
-            if (lane >= o) {
-                wi += y;
-                ki += z;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, wi, o);
+                const int z = __shfl_up_sync(0xffffffffu, ki, o);
+                if (lane >= o) {
+                    wi += y;
+                    ki += z;
+                }
             }
         }
-        if (lane == 31) {
-            s_wsum[warp] = wi;
-            s_ksum[warp] = ki;
-        }
-        __syncthreads();
         long long wb = wi - w;
         int kb = ki - k;
-        for (int i = 0; i < warp; ++i) {
-            wb += s_wsum[i];
-            kb += s_ksum[i];
-        }
-        for (int i = 0; i < per; ++i) {
-            const int e = tid * per + i;
-            if (e < a.E) {
-                plan[e].work += wb;
-                plan[e].keys += kb;
+        if (!one_warp) {
+            if (lane == 31) {
+                s_wsum[warp] = wi;
+                s_ksum[warp] = ki;
+            }
+            __syncthreads();
+            for (int i = 0; i < warp; ++i) {
+                wb += s_wsum[i];
+                kb += s_ksum[i];
             }
         }
-        if (tid == kThreads - 1) {
-            // groups that overlap could ask for more records than there are
-            const bool fits = (long long)(kb + k) * a.g.Hkv <= a.max_keys;
-            if (!fits) atomicExch(a.g.err, kErrCounter);
-            plan[a.E].work = fits ? wb + w : 0;
-            plan[a.E].keys = kb + k;
-            plan[a.E].nc = plan[a.E].c0 = plan[a.E].pad = 0;
+        if (!one_warp || warp == 0) {
+            for (int i = 0; i < per; ++i) {
+                const int e = tid * per + i;
+                if (e < a.E) {
+                    plan[e].work += wb;
+                    plan[e].keys += kb;
+                }
+            }
+            if (tid == (one_warp ? 31 : kThreads - 1)) {
+                // groups that overlap could ask for more records than there are
+                const bool fits = (long long)(kb + k) * a.g.Hkv <= a.max_keys;
+                if (!fits) atomicExch(a.g.err, kErrCounter);
+                plan[a.E].work = fits ? wb + w : 0;
+                plan[a.E].keys = kb + k;
+                plan[a.E].nc = plan[a.E].c0 = plan[a.E].pad = 0;
+            }
         }
         __syncthreads();
         if (!a.fuse && blockIdx.x == 0)
@@ -735,21 +767,18 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         // entries without rows have no key: their outputs are zeros
         for (int e = blockIdx.x; e < a.E; e += gridDim.x) {
             if (plan[e].nc != 0 && W != 0) continue;
-            const long long at = (long long)e * (a.lists ? 1 : a.T) * a.Hq * D, n = (long long)(a.lists ? 1 : a.T) * a.Hq * D;
-            for (long long i = tid; i < n; i += kThreads) {
-                if (a.bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at + i] = __float2bfloat16(0.f);
-                else reinterpret_cast<float*>(a.out)[at + i] = 0.f;
-            }
+            const long long n = (long long)(a.lists ? 1 : a.T) * a.Hq * D, at = e * n;
+            for (long long i = 4 * tid; i < n; i += 4 * kThreads) store4(a, at + i, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
         }
     }
     // ---- the CTA's groups of gw warps work on ranges of their own: while one
     // group joins and changes keys (some 5 us of latencies) the others compute
-    const int gw = a.gw, group = warp / gw, gwarp = warp - group * gw;
+    const int gw = a.gw, group = warp / gw, gwarp = warp - group * gw, gtid = tid - group * gw * 32;
     const int range = group * gridDim.x + blockIdx.x;
     if (range >= G) return;
-    const long long x0 = W * range / G, x1 = W * (range + 1) / G;
+    const long long x0 = mul_div(W, range, G), x1 = mul_div(W, range + 1, G);
     uint8_t* qs = smem + group * S::qs;
-    float* comb = reinterpret_cast<float*>(smem + kMaxGroups * S::qs) + (size_t)group * (gw / 2) * QPI * D;
+    float* comb = reinterpret_cast<float*>(smem + kMaxGroups * S::qs) + (size_t)group * (gw / 2) * QPI * PAD;
     RowInfo& ri = s_ri[group];
     auto sync_group = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gw * 32) : "memory"); };
     const int cpp = a.g.cells_per_page(), cps = a.g.page_shift - 4;       // cells a page, a power of two
@@ -757,10 +786,79 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
     const uint32_t bar0 = dev::smem_u32(&s_bar[warp][0]);
 
+    // ---- queries: a warp takes every gw-th query row of the fragment, loads it
+    // into registers and later lays it out as A fragments in shared memory
+    constexpr int RPW = QPI / 4;                       // rows of a warp at most
+    float qv[RPW][NB];
+    Query qq[RPW];
+    auto load_queries = [&](const Fragment& f) {
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+            const int r = gwarp + i * gw, qi = f.sl * QPI + r;
+            qq[i] = Query{0, 0, 0, 0, -1};
+            const bool valid = r < QPI && qi < f.nq;
+            if (valid) qq[i] = query_of(a, f.e, f.kh, qi);
+            const long long at = (((long long)qq[i].seq * a.T + qq[i].t) * a.Hq + qq[i].h) * D + lane;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) qv[i][b] = valid ? load_q(a.q, at + 32 * b, a.bf16) : 0.f;
+        }
+    };
+    auto place_queries = [&]() {
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+            const int r = gwarp + i * gw;
+            if (r >= QPI) break;
+            float am = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) am = fmaxf(am, fabsf(qv[i][b]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            // scaled by a power of two to a largest element in [512, 1024)
+            const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -117), 118) : 0;
+            const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
+            if (lane == 0) {
+                ri.fac[r] = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
+                ri.lo[r] = qq[i].lo;
+                ri.hi[r] = qq[i].hi;
+            }
+            const int wi = lane & 7, j = lane >> 3;
+            const int reg = ((wi & 3) >> 1) * 2, half = wi & 1;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float y = qv[i][b] * up;
+                const __half hi = __float2half_rn(y);
+                const int at = (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
+                __half* dst = reinterpret_cast<__half*>(qs + at * (TILE == kT8 ? 8 : 16));
+                if (TILE == kT8) {
+                    dst[reg + half] = hi;
+                } else if (HL) {
+                    dst[2 * reg + half] = hi;
+                    dst[2 * (reg + 1) + half] = __float2half_rn(y - __half2float(hi));
+                } else {
+                    dst[2 * (reg + (r >> 3)) + half] = hi;
+                }
+            }
+        }
+    };
+    // the next fragment with cells from unit x on
+    auto next_fragment = [&](long long& x, Fragment& f) {
+        while (x < x1) {
+            f = fragment_at(plan, a, QPI, x, x1);
+            x += f.work;
+            if (f.ca < f.cb) return true;
+        }
+        return false;
+    };
+
+    long long x = x0;
+    Fragment f;
+    if (!next_fragment(x, f)) return;
+    load_queries(f);                                   // in flight while the first copies are issued
+
     // ---- the producer side of this warp's ring: its cells (every gw-th of
     // each fragment) in order, `stages` ahead of their use.  Lanes look up the
     // pages of 32 cells at once.
-    long long px = x0;                                  // first cell after the producer's fragment
+    long long px = x0;                                  // behind the producer's fragment
     int pc = 0, pcb = 0, pslot = -1, ppage = -1, pidx = 32;
     const int* ptable = nullptr;
     const int* plist = nullptr;
@@ -769,20 +867,19 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         if (pc >= pcb) {
             // the next fragment in which this warp has a cell
             for (;;) {
-                if (px >= x1) return;
-                const Fragment f = fragment_at(plan, a, QPI, px, x1);
-                px += f.cb - f.ca;
-                pc = f.ca + gwarp;
-                if (pc >= f.cb) continue;
-                pcb = f.cb;
-                pc0 = f.c0;
-                pkh = f.kh;
-                int seq = f.e;
-                if (a.lists) seq = f.e / a.T;
-                else if (f.e >= a.n_seq) seq = a.group_start[f.e - a.n_seq];
+                Fragment n;
+                if (!next_fragment(px, n)) return;
+                pc = n.ca + gwarp;
+                if (pc >= n.cb) continue;
+                pcb = n.cb;
+                pc0 = n.c0;
+                pkh = n.kh;
+                int seq = n.e;
+                if (a.lists) seq = n.e / a.T;
+                else if (n.e >= a.n_seq) seq = a.group_start[n.e - a.n_seq];
                 ptable = a.tables + (long long)seq * a.g.max_pages;
-                plist = a.lists ? a.lists + ((long long)f.e * a.g.Hkv + f.kh) * a.keep : nullptr;
-                phi = a.lists ? a.lens[seq] - a.T + (f.e - seq * a.T) + 1 : 0x7fffffff;
+                plist = a.lists ? a.lists + ((long long)n.e * a.g.Hkv + n.kh) * a.keep : nullptr;
+                phi = a.lists ? a.lens[seq] - a.T + (n.e - seq * a.T) + 1 : 0x7fffffff;
                 pidx = 32;
                 break;
             }
@@ -829,79 +926,21 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
 
     int st = 0;
     uint32_t phase = 0;
-    long long x = x0;
-    while (x < x1) {
-        const Fragment f = fragment_at(plan, a, QPI, x, x1);
-        const long long xa = plan[f.e].work * a.g.Hkv + (long long)f.kk * plan[f.e].nc, xb = xa + plan[f.e].nc;
-        x += f.cb - f.ca;
-
-        // ---- its queries, as A fragments in shared memory
+    for (bool more = true; more;) {
+        place_queries();
         sync_group();
-        for (int r = gwarp; r < QPI; r += gw) {
-            const int qi = f.sl * QPI + r;
-            Query q{0, 0, 0, 0, -1};
-            float v[NB];
-            float am = 0.f;
-            const bool valid = qi < f.nq;
-            if (valid) q = query_of(a, f.e, f.kh, qi);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                v[b] = valid ? load_q(a.q, (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + 32 * b + lane, a.bf16) : 0.f;
-                am = fmaxf(am, fabsf(v[b]));
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-            // scaled by a power of two to a largest element in [512, 1024)
-            const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -117), 118) : 0;
-            const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
-            if (lane == 0) {
-                ri.fac[r] = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
-                ri.lo[r] = q.lo;
-                ri.hi[r] = q.hi;
-            }
-            const int wi = lane & 7, j = lane >> 3;
-            const int reg = ((wi & 3) >> 1) * 2, half = wi & 1;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const float y = v[b] * up;
-                const __half hi = __float2half_rn(y);
-                const int at = (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
-                __half* dst = reinterpret_cast<__half*>(qs + at * (TILE == kT8 ? 8 : 16));
-                if (TILE == kT8) {
-                    dst[reg + half] = hi;
-                } else if (HL) {
-                    dst[2 * reg + half] = hi;
-                    dst[2 * (reg + 1) + half] = __float2half_rn(y - __half2float(hi));
-                } else {
-                    dst[2 * (reg + (r >> 3)) + half] = hi;
-                }
-            }
-        }
-        sync_group();
-        if (gwarp == 0) {
-            const bool v = lane < QPI && f.sl * QPI + lane < f.nq;
-            int lo_max = v ? ri.lo[lane] : 0, hi_min = v ? ri.hi[lane] : 0x7fffffff;
-            int lo_min = v ? ri.lo[lane] : 0x7fffffff, hi_max = v ? ri.hi[lane] : 0;
-            if (v && ri.hi[lane] <= ri.lo[lane]) lo_min = 0x7fffffff, hi_max = 0;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
-                hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, o));
-                lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
-                hi_max = max(hi_max, __shfl_xor_sync(0xffffffffu, hi_max, o));
-            }
-            if (lane == 0) {
-                ri.lo_max = lo_max;
-                ri.hi_min = hi_min;
-                ri.lo_min = lo_min;
-                ri.hi_max = hi_max;
-            }
-        }
-        sync_group();
-
         const int g = lane >> 2, j = lane & 3;
         Acc<NB, F8, TILE> acc;
         LaneRows<NQ> lr;
+        {
+            const bool v = lane < QPI && f.sl * QPI + lane < f.nq;
+            const int lo = v ? ri.lo[lane] : 0, hi = v ? ri.hi[lane] : 0;
+            const bool some = v && hi > lo;
+            lr.lo_max = __reduce_max_sync(0xffffffffu, v ? lo : 0);
+            lr.hi_min = __reduce_min_sync(0xffffffffu, v ? hi : 0x7fffffff);
+            lr.lo_min = __reduce_min_sync(0xffffffffu, some ? lo : 0x7fffffff);
+            lr.hi_max = __reduce_max_sync(0xffffffffu, some ? hi : 0);
+        }
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
             acc.m[r] = kNone;
@@ -921,8 +960,8 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         for (int c = f.ca + gwarp; c < f.cb; c += gw) {
             const bool there = wait_stage(bar0 + 8u * st, phase, &s_abort, a.g.err);
             const int row0 = s_row0[warp][st];
-            if (there && row0 >= 0 && row0 < ri.hi_max)
-                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, ri, lr, lane, acc);
+            if (there && row0 >= 0 && row0 < lr.hi_max)
+                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, acc);
             __syncwarp();
             if (there) produce(st);
             if (++st == stages) {
@@ -931,7 +970,9 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             }
         }
 
-        // ---- join the group's warps: common reference, then sums passed down
+        // ---- join the group's warps: a common reference, the upper warps' sums
+        // onto the lower half's (12 warps: 4 onto 4 first), then every thread
+        // adds up its elements over what is left
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
             acc.l[r] += __shfl_xor_sync(0xffffffffu, acc.l[r], 1);
@@ -958,119 +999,133 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             }
         }
         sync_group();
-        float M[NQ][2], L[NQ][2];                          // of queries 2j, 2j + 1 (+ 8)
+        const int w0 = warp - gwarp;
+        auto group_max = [&](int row) {
+            float m = kNone;
+#pragma unroll 4
+            for (int w = w0; w < w0 + gw; ++w) m = fmaxf(m, s_m[w][row]);
+            return m;
+        };
 #pragma unroll
         for (int r = 0; r < NQ; ++r)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 2 * j + i + 8 * r;
-                float m = kNone, l = 0.f;
-                const int w0 = warp - gwarp;
-#pragma unroll 4
-                for (int w = w0; w < w0 + gw; ++w) m = fmaxf(m, s_m[w][row]);
-#pragma unroll 4
-                for (int w = w0; w < w0 + gw; ++w) l = fmaf(s_l[w][row], ex2(s_m[w][row] - m), l);
-                const float fa = ex2(s_m[warp][row] - m);
+                const float fa = ex2(s_m[warp][row] - group_max(row));
 #pragma unroll
                 for (int n = 0; n < 2 * NB; ++n) {
                     acc.o[r][n][i] *= fa;
                     acc.o[r][n][2 + i] *= fa;
                 }
-                M[r][i] = l > 0.f ? m - kShift : kNegInf;
-                L[r][i] = l;
             }
-        auto pass = [&](int lo, int n) {               // warps [lo + n, lo + 2n) add their sums to [lo, lo + n)
-            float4* buf = reinterpret_cast<float4*>(comb) + (size_t)(gwarp & (n - 1)) * (2 * NB * NQ * 32);
-            if (gwarp >= lo + n && gwarp < lo + 2 * n) {
-#pragma unroll
-                for (int r = 0; r < NQ; ++r)
-#pragma unroll
-                    for (int i = 0; i < 2 * NB; ++i)
-                        buf[(r * 2 * NB + i) * 32 + lane] = make_float4(acc.o[r][i][0], acc.o[r][i][1], acc.o[r][i][2], acc.o[r][i][3]);
-            }
-            sync_group();
-            if (gwarp >= lo && gwarp < lo + n) {
-#pragma unroll
-                for (int r = 0; r < NQ; ++r)
-#pragma unroll
-                    for (int i = 0; i < 2 * NB; ++i) {
-                        const float4 y = buf[(r * 2 * NB + i) * 32 + lane];
-                        acc.o[r][i][0] += y.x;
-                        acc.o[r][i][1] += y.y;
-                        acc.o[r][i][2] += y.z;
-                        acc.o[r][i][3] += y.w;
-                    }
-            }
-            sync_group();
-        };
-        const int n0 = gw & (gw - 1) ? 4 : gw / 2;         // 12 warps: 4 onto 4 onto 4
-        for (int lo = gw - 2 * n0; lo >= 0; lo -= n0) pass(lo, n0);
-        for (int n = n0 / 2; n >= 1; n >>= 1) pass(0, n);
-
-        const int rec0 = range_of(xa, G, W), n_rec = range_of(xb - 1, G, W) - rec0 + 1;
-        const long long key = (long long)f.keys * a.g.Hkv + f.kk;
         const int rows = min(QPI, f.nq - f.sl * QPI);
-        if (gwarp == 0) {
-            const bool whole = a.fuse && n_rec == 1;
-            const long long slot = range + key;
+        auto region = [&](int w, auto&& body) {            // the lane's four-element pieces in region w
+            float* base = comb + (size_t)w * QPI * PAD + 4 * g;
 #pragma unroll
             for (int r = 0; r < NQ; ++r)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = 2 * j + i + 8 * r;
                     if (row >= rows) continue;
-                    if (whole) {
-                        const Query q = query_of(a, f.e, f.kh, f.sl * QPI + row);
-                        const float w = row_weight(a, q.h, M[r][i], L[r][i]);
-                        const long long at = (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + 4 * g;
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            const float y0 = acc.o[r][2 * b][i] * w, y1 = acc.o[r][2 * b][2 + i] * w;
-                            const float y2 = acc.o[r][2 * b + 1][i] * w, y3 = acc.o[r][2 * b + 1][2 + i] * w;
-                            if (a.bf16)
-                                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at + 32 * b) =
-                                    make_uint2(as_u32(__floats2bfloat162_rn(y0, y1)), as_u32(__floats2bfloat162_rn(y2, y3)));
-                            else
-                                *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at + 32 * b) = make_float4(y0, y1, y2, y3);
-                        }
-                        continue;
-                    }
-                    float* dst = a.part_o + (slot * a.rec_rows + row) * D + 4 * g;
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        *reinterpret_cast<float4*>(dst + 32 * b) = make_float4(acc.o[r][2 * b][i], acc.o[r][2 * b][2 + i], acc.o[r][2 * b + 1][i], acc.o[r][2 * b + 1][2 + i]);
-                    if (g == 0)
-                        *reinterpret_cast<float2*>(a.part_ml + (slot * a.rec_rows + row) * 2) = make_float2(M[r][i], L[r][i]);
+                        body(reinterpret_cast<float4*>(base + row * PAD + 32 * b), acc.o[r][2 * b][i], acc.o[r][2 * b][2 + i],
+                             acc.o[r][2 * b + 1][i], acc.o[r][2 * b + 1][2 + i]);
                 }
-            if (a.fuse && n_rec > 1) {
-                // the group that completes a key's records joins them; the others go on
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) {
-                    const bool last = atomicAdd(a.arrived + key, 1) == n_rec - 1;
-                    if (last) a.arrived[key] = 0;
-                    s_last[group] = last;
-                    __threadfence();
-                }
+        };
+        auto put = [](float4* p, float& x, float& y, float& z, float& w) { *p = make_float4(x, y, z, w); };
+        auto add = [](float4* p, float& x, float& y, float& z, float& w) {
+            const float4 v = *p;
+            x += v.x; y += v.y; z += v.z; w += v.w;
+        };
+        const int n0 = gw & (gw - 1) ? 4 : gw / 2;
+        for (int lo = gw - 2 * n0; lo >= 0; lo -= n0) {
+            if (gwarp >= lo + n0 && gwarp < lo + 2 * n0) region(gwarp & (n0 - 1), put);
+            sync_group();
+            if (gwarp >= lo && gwarp < lo + n0) region(gwarp & (n0 - 1), add);
+            if (lo > 0) sync_group();
+        }
+        if (gwarp < n0) region(gwarp, put);                // the region that only this warp read
+        sync_group();
+
+        const int rec0 = range_of(f.base + a.setup, G, W), n_rec = range_of(f.base + a.setup + f.nc - 1, G, W) - rec0 + 1;
+        const long long key = (long long)f.keys * a.g.Hkv + f.kk;
+        const bool whole = a.fuse && n_rec == 1;
+        for (int c = gtid; c < rows * D4; c += gw * 32) {
+            const int row = c / D4, col = 4 * (c % D4);
+            float4 o = *reinterpret_cast<const float4*>(comb + row * PAD + col);
+            for (int w = 1; w < n0; ++w) {
+                const float4 y = *reinterpret_cast<const float4*>(comb + (size_t)w * QPI * PAD + row * PAD + col);
+                o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
+            }
+            const float m = group_max(row);
+            float l = 0.f;
+#pragma unroll 4
+            for (int w = w0; w < w0 + gw; ++w) l = fmaf(s_l[w][row], ex2(s_m[w][row] - m), l);
+            const float M = l > 0.f ? m - kShift : kNegInf;
+            if (whole) {
+                const Query q = query_of(a, f.e, f.kh, f.sl * QPI + row);
+                store4(a, (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + col, o, sink_weight(sink_of(a, q.h), M, l));
+            } else {
+                const long long at = (range + key) * a.rec_rows + row;
+                *reinterpret_cast<float4*>(a.part_o + at * D + col) = o;
+                if (col == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(M, l);
             }
         }
-        if (a.fuse && n_rec > 1) {
+        if (a.fuse && !whole) {
+            // the group that completes a key's records joins them; the others go on
+            __threadfence();
+            sync_group();
+            if (gtid == 0) {
+                const bool last = atomicAdd(a.arrived + key, 1) == n_rec - 1;
+                if (last) a.arrived[key] = 0;
+                s_last[group] = last;
+                __threadfence();
+            }
             sync_group();
             if (s_last[group]) {
-                for (int rr = gwarp; rr < rows; rr += gw) {
-                    RowSum<NB> r;
-                    r.M = kNegInf;
-                    r.L = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) r.o[i] = 0.f;
-                    fold_records<NB>(a, rec0 + key, n_rec, rr, lane, r);
-                    const Query q = query_of(a, f.e, f.kh, f.sl * QPI + rr);
-                    store_row<NB>(a, ((long long)q.seq * a.T + q.t) * a.Hq + q.h, q.h, lane, r);
+                // threads in `sets` that share the records, then one of each adds them up
+                const int n = rows * D4;
+                int sets = 1;
+                while (2 * sets * n <= gw * 32 && 2 * sets <= n_rec && 2 * sets <= gw / 2) sets *= 2;
+                for (int c0 = 0; c0 < n; c0 += gw * 32) {
+                    const int set = sets > 1 ? gtid / n : 0, c = sets > 1 ? gtid - set * n : c0 + gtid;
+                    const int row = c / D4, col = 4 * (c % D4);
+                    const bool on = set < sets && c < n;
+                    Query q{0, 0, 0, 0, 0};
+                    float sink = kNegInf;
+                    Sum4 s{kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+                    if (on) {
+                        q = query_of(a, f.e, f.kh, f.sl * QPI + row);
+                        sink = sink_of(a, q.h);
+                        add_records<D>(a, s, rec0 + key, set, n_rec, sets, row, col);
+                    }
+                    if (sets > 1) {
+                        float* p = comb + (size_t)set * QPI * PAD;
+                        if (on && set > 0) {
+                            *reinterpret_cast<float4*>(p + row * PAD + col) = s.o;
+                            if (col == 0) {
+                                s_m[w0 + set][row] = s.M;
+                                s_l[w0 + set][row] = s.L;
+                            }
+                        }
+                        sync_group();
+                        if (on && set == 0)
+                            for (int w = 1; w < sets; ++w)
+                                add_sum(s, s_m[w0 + w][row], s_l[w0 + w][row], *reinterpret_cast<const float4*>(p + (size_t)w * QPI * PAD + row * PAD + col));
+                    }
+                    if (on && set == 0)
+                        store4(a, (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + col, s.o, sink_weight(sink, s.M, s.L));
                 }
             }
         }
+        more = next_fragment(x, f);
+        if (more) {
+            load_queries(f);
+            sync_group();                                  // the sums and queries are free again
+        }
     }
-    if (s_abort) {                                     // a wait ran out: let copies in flight land before the CTA ends
+    if (s_abort) {                                         // a wait ran out: let copies in flight land before the CTA ends
         const long long t0 = clock64();
         while (clock64() - t0 < (1LL << 30)) __nanosleep(1000);
     }
@@ -1078,32 +1133,31 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
 
 // ------------------------------------------------------------ merge kernel
 
-// One warp per output row (sequence, t, head) of a shared decode: the records
-// of its own rows' key and of its group's prefix, and the sink.
+// Outputs of a shared decode: D / 4 threads a row (sequence, t, head), over the
+// records of its own rows' key and of its group's prefix, and the sink.
 template <int NB>
 __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    constexpr int D = NB * 32, D4 = D / 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long row = i / D4;
+    const int col = 4 * (int)(i % D4);
     if (row >= (long long)a.n_seq * a.T * a.Hq) return;
     const int h = (int)(row % a.Hq), st = (int)(row / a.Hq);
     const int seq = st / a.T, t = st - seq * a.T;
     const int kh = h / a.hpk, hr = h - kh * a.hpk;
+    const float sink = sink_of(a, h);
     const long long W = a.plan[a.E].work * a.g.Hkv;
     const int G = ranges(a, W);
-    RowSum<NB> r;
-    r.M = kNegInf;
-    r.L = 0.f;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) r.o[i] = 0.f;
+    Sum4 s{kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     auto fold = [&](int e, int qi) {
         const PlanEntry pe = a.plan[e];
         if (pe.nc == 0 || W == 0) return;
         const int nsl = (pe.pad + QPI - 1) / QPI;
         const int kk = kh * nsl + qi / QPI;
-        const long long xa = pe.work * a.g.Hkv + (long long)kk * pe.nc;
+        const long long xa = pe.work * a.g.Hkv + (long long)kk * (pe.nc + a.setup) + a.setup;
         const int c0 = range_of(xa, G, W), c1 = range_of(xa + pe.nc - 1, G, W);
-        fold_records<NB>(a, (long long)pe.keys * a.g.Hkv + kk + c0, c1 - c0 + 1, qi % QPI, lane, r);
+        add_records<D>(a, s, (long long)pe.keys * a.g.Hkv + kk + c0, 0, c1 - c0 + 1, 1, qi % QPI, col);
     };
     fold(seq, t * a.hpk + hr);
     const int grp = group_of(a, seq);
@@ -1112,7 +1166,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) 
         members(a, grp, gs, ge);
         if (seq >= gs && seq < ge) fold(a.n_seq + grp, ((seq - gs) * a.T + t) * a.hpk + hr);
     }
-    store_row<NB>(a, row, h, lane, r);
+    store4(a, row * D + col, s.o, sink_weight(sink, s.M, s.L));
 }
 
 template <int NB, bool F8, int TILE>
@@ -1170,7 +1224,7 @@ cudaError_t launch_split(const SplitArgs& a, cudaStream_t s) {
 cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s) {
     const long long rows = (long long)a.n_seq * a.T * a.Hq;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+    cfg.gridDim = dim3((unsigned)((rows * (a.g.D / 4) + 255) / 256));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
