@@ -555,18 +555,18 @@ struct Fragment {
     int e, kk, kh, sl, nsl, nq, c0, nc, ca, cb, keys, work;
     long long base;
 };
-__device__ __forceinline__ Fragment fragment_at(const PlanEntry* plan, const SplitArgs& a, int QPI, long long x, long long x1) {
-    Fragment f;
-    f.e = find_entry(plan, a.E, mul_div(x, 1, a.g.Hkv));
+// (a call, not inlined: it is met three times a kernel and takes several divisions)
+__device__ __noinline__ void fragment_at(Fragment& f, const PlanEntry* plan, int E, int Hkv, int setup, int QPI, long long x, long long x1) {
+    f.e = find_entry(plan, E, mul_div(x, 1, Hkv));
     const PlanEntry pe = plan[f.e];
-    const long long first = pe.work * a.g.Hkv;
-    const int len = pe.nc + a.setup;
+    const long long first = pe.work * Hkv;
+    const int len = pe.nc + setup;
     f.kk = (int)mul_div(x - first, 1, len);
     f.base = first + (long long)f.kk * len;
     const int va = (int)(x - f.base), vb = (int)min((long long)len, va + (x1 - x));
     f.work = vb - va;
-    f.ca = max(0, va - a.setup);
-    f.cb = max(0, vb - a.setup);
+    f.ca = max(0, va - setup);
+    f.cb = max(0, vb - setup);
     f.nq = pe.pad;
     f.nsl = (pe.pad + QPI - 1) / QPI;
     f.kh = f.kk / f.nsl;
@@ -574,7 +574,6 @@ __device__ __forceinline__ Fragment fragment_at(const PlanEntry* plan, const Spl
     f.c0 = pe.c0;
     f.nc = pe.nc;
     f.keys = pe.keys;
-    return f;
 }
 
 // Ranges that W units of work (cells, and `setup` for each key) are cut into:
@@ -843,7 +842,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     // the next fragment with cells from unit x on
     auto next_fragment = [&](long long& x, Fragment& f) {
         while (x < x1) {
-            f = fragment_at(plan, a, QPI, x, x1);
+            fragment_at(f, plan, a.E, a.g.Hkv, a.setup, QPI, x, x1);
             x += f.work;
             if (f.ca < f.cb) return true;
         }
@@ -853,7 +852,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     long long x = x0;
     Fragment f;
     if (!next_fragment(x, f)) return;
-    load_queries(f);                                   // in flight while the first copies are issued
+    load_queries(f);
 
     // ---- the producer side of this warp's ring: its cells (every gw-th of
     // each fragment) in order, `stages` ahead of their use.  Lanes look up the
@@ -922,12 +921,15 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         ++pidx;
         pc += gw;
     };
-    for (int st = 0; st < stages; ++st) produce(st);
+    // one cell a warp, then the queries, then the other stages: query loads
+    // behind the whole first burst of copies would take 3 us
+    produce(0);
+    place_queries();
+    for (int st = 1; st < stages; ++st) produce(st);
 
     int st = 0;
     uint32_t phase = 0;
     for (bool more = true; more;) {
-        place_queries();
         sync_group();
         const int g = lane >> 2, j = lane & 3;
         Acc<NB, F8, TILE> acc;
@@ -1123,6 +1125,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         if (more) {
             load_queries(f);
             sync_group();                                  // the sums and queries are free again
+            place_queries();
         }
     }
     if (s_abort) {                                         // a wait ran out: let copies in flight land before the CTA ends
