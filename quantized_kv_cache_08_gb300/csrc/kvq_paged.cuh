@@ -172,17 +172,26 @@ struct SplitArgs {
     float* part_o;                 // [slot][rec_rows][D]
     float* part_ml;                // [slot][rec_rows][2]  (max in log2 units, sum)
     struct PlanEntry* plan;        // [E + 1], written by CTA 0 for the merge
+    int tiles;                     // 1: groups with many queries go to the tile kernel
+    int tile_rows;                 // queries of its blocks
+    long long max_keys2;           // its keys that the record area holds
+    float* part2_o;                // [CTA + key][tile_rows][D]
+    float* part2_ml;
+    struct PlanEntry* plan2;       // [n_groups + 1]
 };
 // Work before an entry (cells x slices), keys before it (slices), its cells and
 // the first of them; entry E holds the totals.
 struct PlanEntry {
     long long work;
-    int keys, nc, c0, pad;
+    int keys, nc, c0, pad, hi, pad2;     // pad: queries; hi: rows of a prefix
 };
 int split_tile(bool bf16, int most_queries);
 int split_warps(int NB, int tile);
 cudaError_t launch_split(const SplitArgs& a, cudaStream_t s);
 cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s);
+// prefixes of groups with many bf16 queries, 128-row tiles on tcgen05 (kvq_paged_prefix.cu)
+int prefix_rows_of(int NB);                               // tile_rows
+cudaError_t launch_prefix(const SplitArgs& a, cudaStream_t s);
 
 }  // namespace paged
 }  // namespace kvq

@@ -16,7 +16,7 @@ struct kvq_paged {
     Geom g;
     int num_sms;
     uint8_t* ws;
-    size_t off_plan, off_arrived, off_ml, off_o, off_keys, key_rows;
+    size_t off_plan, off_plan2, off_arrived, off_ml, off_o, off_ml2, off_o2, off_keys, key_rows, keys2;
     int8_t* codes;
     float* scales;
     Freqs freqs;
@@ -33,7 +33,7 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned16(const void* p) { return ((size_t)p & 15) == 0; }
 
 struct Layout {
-    size_t cell, page, pool, bounds, plan, arrived, ml, o, keys, total, key_rows;
+    size_t cell, page, pool, bounds, plan, plan2, arrived, ml, o, ml2, o2, keys, total, key_rows, keys2;
 };
 
 kvq_status layout(const kvq_paged_config* c, Layout* l) {
@@ -68,10 +68,19 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     l->key_rows = (size_t)c->n_kv_heads * c->max_seqs * (round_up(Qh, 16) + Qh + 16);
     const size_t recs = (size_t)kMaxRanges * 16 + l->key_rows;
     l->plan = 256;                                       // the error word comes first
-    l->arrived = round_up(l->plan + (kMaxEntries + 1) * sizeof(PlanEntry), 256);
+    l->plan2 = round_up(l->plan + (kMaxEntries + 1) * sizeof(PlanEntry), 256);
+    l->arrived = round_up(l->plan2 + (kMaxSeqs + 1) * sizeof(PlanEntry), 256);
     l->ml = round_up(l->arrived + l->key_rows * sizeof(int), 256);
     l->o = round_up(l->ml + recs * 8, 256);
-    l->keys = round_up(l->o + recs * D * 4, 256);
+    // records of the prefix tile kernel: tile_rows queries for each CTA and each
+    // key; groups that it takes have more than 16 queries each
+    const size_t tr = prefix_rows_of((int)NB);
+    const size_t total_q = (size_t)c->max_seqs * Qh;
+    l->keys2 = (size_t)c->n_kv_heads * (total_q / tr + std::min<size_t>(c->max_seqs, total_q / 17) + 1);
+    const size_t recs2 = total_q > 16 ? (kMaxGrid + l->keys2) * tr : 0;
+    l->ml2 = round_up(l->o + recs * D * 4, 256);
+    l->o2 = round_up(l->ml2 + recs2 * 8, 256);
+    l->keys = round_up(l->o2 + recs2 * D * 4, 256);
     l->total = l->keys;
     if (c->bounds)
         l->total += round_up((size_t)std::min(kMaxEntries, c->max_seqs * c->max_t) * c->n_kv_heads * c->max_pages * 4, 256);
@@ -165,7 +174,7 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     const long long keys = (long long)a.E * c->cfg.n_kv_heads * ((most + a.tile - 1) / a.tile);
     a.gw = keys >= kManyKeys ? 4 : warps;
     a.groups = warps / a.gw;
-    a.setup = a.gw == 4 ? 8 : 32;
+    a.setup = 8;
     a.rec_rows = std::min(a.tile, most);
     a.max_keys = (long long)(c->key_rows / a.rec_rows);
     a.plan = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan);
@@ -173,8 +182,19 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.fuse = n_groups == 0;
     a.part_ml = reinterpret_cast<float*>(c->ws + c->off_ml);
     a.part_o = reinterpret_cast<float*>(c->ws + c->off_o);
+    a.tile_rows = prefix_rows_of(a.g.NB());
+    a.tiles = n_groups > 0 && a.bf16 && most > 16;
+    a.max_keys2 = (long long)c->keys2;
+    a.plan2 = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan2);
+    a.part2_ml = reinterpret_cast<float*>(c->ws + c->off_ml2);
+    a.part2_o = reinterpret_cast<float*>(c->ws + c->off_o2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_split(a, s);
+    cudaError_t e = cudaSuccess;
+    if (a.tiles) {
+        e = launch_prefix(a, s);
+        if (e != cudaSuccess) return cuda_fail(e, "paged decode prefix kernel");
+    }
+    e = launch_split(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode split kernel");
     if (!a.fuse) e = launch_merge(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode merge kernel");
@@ -244,6 +264,10 @@ kvq_status kvq_paged_alloc(const kvq_paged_config* cfg, void* pool, void* bounds
     c->num_sms = sms;
     c->ws = static_cast<uint8_t*>(workspace);
     c->off_plan = l.plan;
+    c->off_plan2 = l.plan2;
+    c->off_ml2 = l.ml2;
+    c->off_o2 = l.o2;
+    c->keys2 = l.keys2;
     c->off_arrived = l.arrived;
     c->off_ml = l.ml;
     c->off_o = l.o;

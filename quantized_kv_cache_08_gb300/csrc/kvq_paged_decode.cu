@@ -28,6 +28,7 @@
 // Work is cut stream-K fashion: see kvq_paged.cuh.
 #include "kvq_device.cuh"
 #include "kvq_paged.cuh"
+#include "kvq_paged_work.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,10 +41,6 @@ namespace kvq {
 namespace paged {
 namespace {
 
-using dev::kLazy;
-using dev::kNegInf;
-constexpr float kShift = 6.0f;         // p is held as 2^6 p: fp16 keeps 2^-20 of the largest in full
-constexpr int kMaxStages = 8;
 constexpr int kMaxGroups = 4;          // groups of warps in a CTA
 
 // Query tiles: 8 or 16 bf16 queries, or 8 of f32 in two parts
@@ -54,12 +51,6 @@ template <int NB, int TILE>
 constexpr int warps_of() { return NB == 8 ? 8 : NB == 4 && TILE == kT16 ? 12 : 16; }
 template <int TILE>
 constexpr int queries_of() { return TILE == kT16 ? 16 : 8; }
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // c = a b, without a sum to start from
 __device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -78,158 +69,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint4& a, uint32_t
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
-__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
-__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
-
 // code bytes (biased by 128) sel of w under the exponent of 1024, minus 1152: exact
 __device__ __forceinline__ uint32_t k_pair(uint32_t w, uint32_t sel) {
     return as_u32(__hsub2(as_h2(__byte_perm(w, 0x64646464u, sel)), as_h2(0x64806480u)));
 }
-// two E4M3 bytes as a half pair, exact
-__device__ __forceinline__ uint32_t f8_pair(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// The 5-bit codes of element r of two rows, in the low bits of each half word
-template <int R>
-__device__ __forceinline__ uint32_t v_codes(uint32_t unit, uint32_t nib, int n4, uint32_t magic) {
-    if constexpr (R == 0) return (unit & 0x001f001fu) | magic;
-    else if constexpr (R == 1) return ((unit >> 5) & 0x001f001fu) | magic;
-    else if constexpr (R == 2) return ((unit >> 10) & 0x001f001fu) | magic;
-    else return (((unit >> 11) & 0x00100010u) | magic) | ((nib >> (4 * n4)) & 0x000f000fu);
-}
-
-// ------------------------------------------------------------ work entries
-
-__device__ __forceinline__ bool len_ok(const SplitArgs& a, int len) {
-    return len >= 0 && len <= (long long)a.g.max_pages << a.g.page_shift;
-}
-
-// group of a sequence (-1: none)
-__device__ __forceinline__ int group_of(const SplitArgs& a, int seq) {
-    if (a.n_groups == 0 || seq < a.group_start[0] || seq >= a.group_start[a.n_groups]) return -1;
-    int lo = 0, hi = a.n_groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.group_start[mid] <= seq) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-__device__ __forceinline__ int prefix_rows(const SplitArgs& a, int grp) {
-    const int p = a.prefix_len[grp];
-    return len_ok(a, p) ? p : 0;
-}
-
-// members of a group, [gs, ge); none if its bounds are out of order
-__device__ __forceinline__ void members(const SplitArgs& a, int grp, int& gs, int& ge) {
-    gs = a.group_start[grp];
-    ge = a.group_start[grp + 1];
-    if (gs < 0 || ge > a.n_seq || ge < gs) gs = ge = 0;
-}
-
-struct EntryWork {
-    int nc, c0, nq;
-};
-
-__device__ __forceinline__ EntryWork entry_work(const SplitArgs& a, int e, bool report) {
-    EntryWork w{0, 0, 0};
-    int lo = 0, hi = 0;
-    if (a.lists) {
-        const int seq = e / a.T, t = e - seq * a.T;
-        const int len = a.lens[seq];
-        if (!len_ok(a, len)) {
-            if (report) atomicExch(a.g.err, kErrCounter);
-            return w;
-        }
-        w.nq = a.hpk;
-        if (len - a.T + t >= 0) w.nc = a.keep * a.g.cells_per_page();
-        return w;
-    }
-    if (e < a.n_seq) {
-        const int len = a.lens[e];
-        if (!len_ok(a, len)) {
-            if (report) atomicExch(a.g.err, kErrCounter);
-            return w;
-        }
-        w.nq = a.hpk * a.T;
-        hi = len;
-        lo = a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;
-        const int grp = group_of(a, e);
-        if (grp >= 0) lo = max(lo, prefix_rows(a, grp));
-    } else {
-        const int grp = e - a.n_seq;
-        int gs, ge;
-        members(a, grp, gs, ge);
-        if (report && (a.group_start[grp + 1] < a.group_start[grp] || a.group_start[grp] < 0 ||
-                       a.group_start[grp + 1] > a.n_seq || !len_ok(a, a.prefix_len[grp])))
-            atomicExch(a.g.err, kErrCounter);
-        w.nq = (ge - gs) * a.hpk * a.T;
-        hi = prefix_rows(a, grp);
-        lo = 0;
-        if (a.window > 0) {                       // rows before every member's window are not read
-            lo = hi;
-            for (int m = gs; m < ge; ++m) lo = min(lo, max(0, a.lens[m] - a.T + 1 - a.window));
-        }
-        if (ge == gs) hi = lo;
-    }
-    if (hi > lo) {
-        w.c0 = lo >> 4;
-        w.nc = ((hi + 15) >> 4) - w.c0;
-    }
-    return w;
-}
-
-// Query row qi of an entry for KV head g: sequence, row t and head; and the
-// rows it sees, [lo, hi) (hi <= lo: none).
-struct Query {
-    int seq, t, h, lo, hi;
-};
-__device__ __forceinline__ Query query_of(const SplitArgs& a, int e, int g, int qi) {
-    Query q;
-    int within = qi;
-    const int Qh = a.hpk * a.T;
-    if (a.lists) {
-        q.seq = e / a.T;
-        q.t = e - q.seq * a.T;
-    } else {
-        q.seq = e;
-        if (e >= a.n_seq) {
-            const int m = qi / Qh;
-            q.seq = a.group_start[e - a.n_seq] + m;
-            within = qi - m * Qh;
-        }
-        q.t = within / a.hpk;
-        within -= q.t * a.hpk;
-    }
-    q.h = g * a.hpk + within;
-    const int len = a.lens[q.seq];
-    q.hi = len_ok(a, len) ? len - a.T + q.t + 1 : 0;
-    q.lo = a.window > 0 ? max(0, q.hi - a.window) : 0;
-    if (!a.lists) {
-        if (e >= a.n_seq) q.hi = min(q.hi, prefix_rows(a, e - a.n_seq));
-        else if (a.n_groups) {
-            const int grp = group_of(a, e);
-            if (grp >= 0) q.lo = max(q.lo, prefix_rows(a, grp));
-        }
-    }
-    return q;
-}
-
-// largest e with plan[e].work <= x (x below the total)
-__device__ __forceinline__ int find_entry(const PlanEntry* plan, int E, long long x) {
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (plan[mid].work <= x) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 __device__ __forceinline__ float load_q(const void* q, long long idx, int bf16) {
     if (bf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q)[idx]);
     return reinterpret_cast<const float*>(q)[idx];
@@ -260,8 +103,6 @@ struct LaneRows {
     int lo[NQ], hi[NQ];
     int lo_min, lo_max, hi_min, hi_max;
 };
-
-constexpr float kNone = -1e30f;        // reference of a query that has seen no row: any score passes it
 
 // Values of rows that no query sees, in the staged cell: zeroed, for they may be any bytes
 template <int NB, bool F8, typename Rows>
@@ -526,21 +367,6 @@ struct Smem {
     __host__ __device__ static size_t ring(int E) { return (kMaxGroups * qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
 };
 
-// Bounded wait for a stage; false once any wait of the CTA has run out.
-__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
-    if (dev::mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-        if (dev::mbar_try_sleep(bar, parity, 20000u)) return true;
-        if (*abort_flag) return false;
-        if (clock64() - t0 > (1LL << 31)) {
-            atomicExch(err, kErrWait);
-            *abort_flag = 1;
-            return false;
-        }
-    }
-}
-
 // x g / d and x / d for 0 <= x, in 32 bits where they fit
 __device__ __forceinline__ long long mul_div(long long x, int g, long long d) {
     const unsigned long long n = (unsigned long long)x * (unsigned)g;
@@ -580,8 +406,7 @@ __device__ __noinline__ void fragment_at(Fragment& f, const PlanEntry* plan, int
 // one for each group of warps, and about a cell for each of its warps at least,
 // so that a short context is joined from few records
 __device__ __forceinline__ int ranges(const SplitArgs& a, long long W) {
-    const int least = a.gw + a.setup;
-    return (int)min((long long)a.G * a.groups, (W + least - 1) / least);
+    return (int)min((long long)a.G * a.groups, (W + a.gw - 1) / a.gw);
 }
 
 // The range that holds unit x of W units of work in G ranges
@@ -960,7 +785,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
 
         // ---- its cells, warp by warp
         for (int c = f.ca + gwarp; c < f.cb; c += gw) {
-            const bool there = wait_stage(bar0 + 8u * st, phase, &s_abort, a.g.err);
+            const bool there = wait_bounded(bar0 + 8u * st, phase, &s_abort, a.g.err);
             const int row0 = s_row0[warp][st];
             if (there && row0 >= 0 && row0 < lr.hi_max)
                 take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, acc);
@@ -1167,7 +992,26 @@ __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) 
     if (grp >= 0) {
         int gs, ge;
         members(a, grp, gs, ge);
-        if (seq >= gs && seq < ge) fold(a.n_seq + grp, ((seq - gs) * a.T + t) * a.hpk + hr);
+        const int qi = ((seq - gs) * a.T + t) * a.hpk + hr;
+        if (seq >= gs && seq < ge) {
+            if (tile_group(a, (ge - gs) * a.hpk * a.T)) {
+                const long long W2 = a.plan2[a.n_groups].work * a.g.Hkv;
+                const PlanEntry pe = a.plan2[grp];
+                if (pe.nc != 0 && W2 != 0) {
+                    const int G2 = (int)min((long long)a.G, W2), nqb = (pe.pad + a.tile_rows - 1) / a.tile_rows;
+                    const int kk = kh * nqb + qi / a.tile_rows;
+                    const long long xa = pe.work * a.g.Hkv + (long long)kk * pe.nc;
+                    const int c0 = range_of(xa, G2, W2), c1 = range_of(xa + pe.nc - 1, G2, W2);
+                    SplitArgs b = a;
+                    b.part_o = a.part2_o;
+                    b.part_ml = a.part2_ml;
+                    b.rec_rows = a.tile_rows;
+                    add_records<D>(b, s, (long long)pe.keys * a.g.Hkv + kk + c0, 0, c1 - c0 + 1, 1, qi % a.tile_rows, col);
+                }
+            } else {
+                fold(a.n_seq + grp, qi);
+            }
+        }
     }
     store4(a, row * D + col, s.o, sink_weight(sink, s.M, s.L));
 }

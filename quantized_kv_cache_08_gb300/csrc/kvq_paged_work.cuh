@@ -1,0 +1,198 @@
+// Device helpers shared by the paged decode kernels: conversions of codes, work
+// entries, queries and the rows they see, bounded waits.
+#pragma once
+
+#include "kvq_device.cuh"
+#include "kvq_paged.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+namespace kvq {
+namespace paged {
+
+using dev::kLazy;
+using dev::kNegInf;
+constexpr float kShift = 6.0f;         // p is held as 2^6 p: fp16 keeps 2^-20 of the largest in full
+constexpr int kMaxStages = 8;
+constexpr float kNone = -1e30f;        // reference of a query that has seen no row: any score passes it
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
+// two E4M3 bytes as a half pair, exact
+__device__ __forceinline__ uint32_t f8_pair(uint32_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The 5-bit codes of element r of two rows, in the low bits of each half word
+template <int R>
+__device__ __forceinline__ uint32_t v_codes(uint32_t unit, uint32_t nib, int n4, uint32_t magic) {
+    if constexpr (R == 0) return (unit & 0x001f001fu) | magic;
+    else if constexpr (R == 1) return ((unit >> 5) & 0x001f001fu) | magic;
+    else if constexpr (R == 2) return ((unit >> 10) & 0x001f001fu) | magic;
+    else return (((unit >> 11) & 0x00100010u) | magic) | ((nib >> (4 * n4)) & 0x000f000fu);
+}
+
+// ------------------------------------------------------------ work entries
+
+__device__ __forceinline__ bool len_ok(const SplitArgs& a, int len) {
+    return len >= 0 && len <= (long long)a.g.max_pages << a.g.page_shift;
+}
+
+// group of a sequence (-1: none)
+__device__ __forceinline__ int group_of(const SplitArgs& a, int seq) {
+    if (a.n_groups == 0 || seq < a.group_start[0] || seq >= a.group_start[a.n_groups]) return -1;
+    int lo = 0, hi = a.n_groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.group_start[mid] <= seq) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int prefix_rows(const SplitArgs& a, int grp) {
+    const int p = a.prefix_len[grp];
+    return len_ok(a, p) ? p : 0;
+}
+
+// members of a group, [gs, ge); none if its bounds are out of order
+__device__ __forceinline__ void members(const SplitArgs& a, int grp, int& gs, int& ge) {
+    gs = a.group_start[grp];
+    ge = a.group_start[grp + 1];
+    if (gs < 0 || ge > a.n_seq || ge < gs) gs = ge = 0;
+}
+
+// A group's queries per KV head go to the tile kernel where they are more than a
+// 16-row tile holds (measured: up to 16 queries the split kernel reads the rows
+// at 0.7 of HBM speed; more cost it another pass over them for each 16)
+constexpr int kTileQueries = 16;
+__device__ __forceinline__ bool tile_group(const SplitArgs& a, int nq) { return a.tiles && nq > kTileQueries; }
+
+struct EntryWork {
+    int nc, c0, nq;
+};
+
+__device__ __forceinline__ EntryWork entry_work(const SplitArgs& a, int e, bool report) {
+    EntryWork w{0, 0, 0};
+    int lo = 0, hi = 0;
+    if (a.lists) {
+        const int seq = e / a.T, t = e - seq * a.T;
+        const int len = a.lens[seq];
+        if (!len_ok(a, len)) {
+            if (report) atomicExch(a.g.err, kErrCounter);
+            return w;
+        }
+        w.nq = a.hpk;
+        if (len - a.T + t >= 0) w.nc = a.keep * a.g.cells_per_page();
+        return w;
+    }
+    if (e < a.n_seq) {
+        const int len = a.lens[e];
+        if (!len_ok(a, len)) {
+            if (report) atomicExch(a.g.err, kErrCounter);
+            return w;
+        }
+        w.nq = a.hpk * a.T;
+        hi = len;
+        lo = a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;
+        const int grp = group_of(a, e);
+        if (grp >= 0) lo = max(lo, prefix_rows(a, grp));
+    } else {
+        const int grp = e - a.n_seq;
+        int gs, ge;
+        members(a, grp, gs, ge);
+        if (report && (a.group_start[grp + 1] < a.group_start[grp] || a.group_start[grp] < 0 ||
+                       a.group_start[grp + 1] > a.n_seq || !len_ok(a, a.prefix_len[grp])))
+            atomicExch(a.g.err, kErrCounter);
+        w.nq = (ge - gs) * a.hpk * a.T;
+        if (tile_group(a, w.nq)) return EntryWork{0, 0, 0};
+        hi = prefix_rows(a, grp);
+        lo = 0;
+        if (a.window > 0) {                       // rows before every member's window are not read
+            lo = hi;
+            for (int m = gs; m < ge; ++m) lo = min(lo, max(0, a.lens[m] - a.T + 1 - a.window));
+        }
+        if (ge == gs) hi = lo;
+    }
+    if (hi > lo) {
+        w.c0 = lo >> 4;
+        w.nc = ((hi + 15) >> 4) - w.c0;
+    }
+    return w;
+}
+
+// Query row qi of an entry for KV head g: sequence, row t and head; and the
+// rows it sees, [lo, hi) (hi <= lo: none).
+struct Query {
+    int seq, t, h, lo, hi;
+};
+__device__ __forceinline__ Query query_of(const SplitArgs& a, int e, int g, int qi) {
+    Query q;
+    int within = qi;
+    const int Qh = a.hpk * a.T;
+    if (a.lists) {
+        q.seq = e / a.T;
+        q.t = e - q.seq * a.T;
+    } else {
+        q.seq = e;
+        if (e >= a.n_seq) {
+            const int m = qi / Qh;
+            q.seq = a.group_start[e - a.n_seq] + m;
+            within = qi - m * Qh;
+        }
+        q.t = within / a.hpk;
+        within -= q.t * a.hpk;
+    }
+    q.h = g * a.hpk + within;
+    const int len = a.lens[q.seq];
+    q.hi = len_ok(a, len) ? len - a.T + q.t + 1 : 0;
+    q.lo = a.window > 0 ? max(0, q.hi - a.window) : 0;
+    if (!a.lists) {
+        if (e >= a.n_seq) q.hi = min(q.hi, prefix_rows(a, e - a.n_seq));
+        else if (a.n_groups) {
+            const int grp = group_of(a, e);
+            if (grp >= 0) q.lo = max(q.lo, prefix_rows(a, grp));
+        }
+    }
+    return q;
+}
+
+// largest e with plan[e].work <= x (x below the total)
+__device__ __forceinline__ int find_entry(const PlanEntry* plan, int E, long long x) {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (plan[mid].work <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Bounded wait; false once any wait of the CTA has run out.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    if (dev::mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (dev::mbar_try_sleep(bar, parity, 20000u)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > (1LL << 31)) {
+            atomicExch(err, kErrWait);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+}  // namespace paged
+}  // namespace kvq
