@@ -73,11 +73,11 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     l->ml = round_up(l->arrived + l->key_rows * sizeof(int), 256);
     l->o = round_up(l->ml + recs * 8, 256);
     // records of the prefix tile kernel: tile_rows queries for each CTA and each
-    // key; groups that it takes have more than 16 queries each
+    // key; groups that it takes have more than 8 queries each
     const size_t tr = prefix_rows_of((int)NB);
     const size_t total_q = (size_t)c->max_seqs * Qh;
-    l->keys2 = (size_t)c->n_kv_heads * (total_q / tr + std::min<size_t>(c->max_seqs, total_q / 17) + 1);
-    const size_t recs2 = total_q > 16 ? (kMaxGrid + l->keys2) * tr : 0;
+    l->keys2 = (size_t)c->n_kv_heads * (total_q / tr + std::min<size_t>(c->max_seqs, total_q / 9) + 1);
+    const size_t recs2 = total_q > 8 ? (kMaxGrid + l->keys2) * tr : 0;
     l->ml2 = round_up(l->o + recs * D * 4, 256);
     l->o2 = round_up(l->ml2 + recs2 * 8, 256);
     l->keys = round_up(l->o2 + recs2 * D * 4, 256);
@@ -165,8 +165,12 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.keep = keep;
     a.E = lists ? q->n_seq * q->T : q->n_seq + n_groups;
     a.G = std::min(c->num_sms, kMaxGrid);
-    const int most = lists ? a.hpk : n_groups ? q->n_seq * a.hpk * q->T : a.hpk * q->T;
-    a.tile = split_tile(a.bf16, most);
+    // queries of a key at most: the tile kernel takes the bf16 groups that have
+    // more than a slice
+    const int own = lists ? a.hpk : a.hpk * q->T;
+    a.tile = split_tile(a.bf16, own);
+    a.tiles = n_groups > 0 && a.bf16 && q->n_seq * own > a.tile;
+    const int most = n_groups > 0 ? (a.tiles ? a.tile : q->n_seq * own) : own;
     // many keys: four warps a group, for a fragment's end and start are hidden
     // behind the other groups; few keys: the whole CTA, for a quarter of the
     // records to join
@@ -183,7 +187,6 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.part_ml = reinterpret_cast<float*>(c->ws + c->off_ml);
     a.part_o = reinterpret_cast<float*>(c->ws + c->off_o);
     a.tile_rows = prefix_rows_of(a.g.NB());
-    a.tiles = n_groups > 0 && a.bf16 && most > 16;
     a.max_keys2 = (long long)c->keys2;
     a.plan2 = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan2);
     a.part2_ml = reinterpret_cast<float*>(c->ws + c->off_ml2);

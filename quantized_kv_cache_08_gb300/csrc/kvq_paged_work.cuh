@@ -73,11 +73,9 @@ __device__ __forceinline__ void members(const SplitArgs& a, int grp, int& gs, in
     if (gs < 0 || ge > a.n_seq || ge < gs) gs = ge = 0;
 }
 
-// A group's queries per KV head go to the tile kernel where they are more than a
-// 16-row tile holds (measured: up to 16 queries the split kernel reads the rows
-// at 0.7 of HBM speed; more cost it another pass over them for each 16)
-constexpr int kTileQueries = 16;
-__device__ __forceinline__ bool tile_group(const SplitArgs& a, int nq) { return a.tiles && nq > kTileQueries; }
+// A group whose queries per KV head are more than one slice of the split kernel
+// goes to the tile kernel: the split kernel reads the rows again for each slice
+__device__ __forceinline__ bool tile_group(const SplitArgs& a, int nq) { return a.tiles && nq > a.tile; }
 
 struct EntryWork {
     int nc, c0, nq;
