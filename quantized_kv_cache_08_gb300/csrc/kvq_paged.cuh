@@ -175,8 +175,8 @@ struct SplitArgs {
     int tiles;                     // 1: groups with many queries go to the tile kernel
     int tile_rows;                 // queries of its blocks
     long long max_keys2;           // its keys that the record area holds
-    float* part2_o;                // [CTA + key][tile_rows][D]
-    float* part2_ml;
+    uint16_t* part2_o;             // [CTA + key][tile_rows][D] fp16, divided by the sum
+    float* part2_ml;               // [CTA + key][tile_rows][2]
     struct PlanEntry* plan2;       // [n_groups + 1]
 };
 // Work before an entry (cells x slices), keys before it (slices), its cells and

@@ -80,7 +80,7 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     const size_t recs2 = total_q > 8 ? (kMaxGrid + l->keys2) * tr : 0;
     l->ml2 = round_up(l->o + recs * D * 4, 256);
     l->o2 = round_up(l->ml2 + recs2 * 8, 256);
-    l->keys = round_up(l->o2 + recs2 * D * 4, 256);
+    l->keys = round_up(l->o2 + recs2 * D * 2, 256);
     l->total = l->keys;
     if (c->bounds)
         l->total += round_up((size_t)std::min(kMaxEntries, c->max_seqs * c->max_t) * c->n_kv_heads * c->max_pages * 4, 256);
@@ -190,7 +190,7 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.max_keys2 = (long long)c->keys2;
     a.plan2 = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan2);
     a.part2_ml = reinterpret_cast<float*>(c->ws + c->off_ml2);
-    a.part2_o = reinterpret_cast<float*>(c->ws + c->off_o2);
+    a.part2_o = reinterpret_cast<uint16_t*>(c->ws + c->off_o2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (a.tiles) {

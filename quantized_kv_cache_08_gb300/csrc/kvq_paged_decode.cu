@@ -402,6 +402,62 @@ __device__ __noinline__ void fragment_at(Fragment& f, const PlanEntry* plan, int
     f.keys = pe.keys;
 }
 
+// The next fragment with cells from unit x on
+__device__ __forceinline__ bool next_fragment(Fragment& f, long long& x, long long x1, const SplitArgs& a, const PlanEntry* plan, int QPI) {
+    while (x < x1) {
+        fragment_at(f, plan, a.E, a.g.Hkv, a.setup, QPI, x, x1);
+        x += f.work;
+        if (f.ca < f.cb) return true;
+    }
+    return false;
+}
+
+// The producer side of a warp's ring: its cells (every gw-th of each fragment) in
+// order.  Lanes hold the pages of its next 32 cells of the fragment.
+struct Producer {
+    long long x;                   // behind the fragment
+    int c, cb;                     // next cell, and the fragment's end
+    int slot, page, i;             // the lane's looked-up cell (-1: none); next lane to use
+    int kh, c0, hi, listed;
+    const int* table;
+    const int* list;
+};
+__device__ __forceinline__ void refill(Producer& p, const SplitArgs& a, const PlanEntry* plan, int QPI, long long x1, int gwarp, int lane) {
+    while (p.c >= p.cb) {          // the next fragment in which this warp has a cell
+        Fragment n;
+        if (!next_fragment(n, p.x, x1, a, plan, QPI)) return;
+        p.c = n.ca + gwarp;
+        p.cb = n.cb;
+        p.c0 = n.c0;
+        p.kh = n.kh;
+        int seq = n.e;
+        if (a.lists) seq = n.e / a.T;
+        else if (n.e >= a.n_seq) seq = a.group_start[n.e - a.n_seq];
+        p.table = a.tables + (long long)seq * a.g.max_pages;
+        p.listed = a.lists != nullptr;
+        p.list = a.lists ? a.lists + ((long long)n.e * a.g.Hkv + n.kh) * a.keep : nullptr;
+        p.hi = a.lists ? a.lens[seq] - a.T + (n.e - seq * a.T) + 1 : 0x7fffffff;
+    }
+    p.i = 0;
+    const int cps = a.g.page_shift - 4, mask = (1 << cps) - 1;
+    const int c = p.c + lane * a.gw;
+    p.slot = p.page = -1;
+    if (c >= p.cb) return;
+    int slot = p.listed ? p.list[c >> cps] : (p.c0 + c) >> cps;
+    if (slot >= a.g.max_pages) {
+        atomicExch(a.g.err, kErrCounter);
+        slot = -1;
+    }
+    if (slot < 0 || slot * a.g.page_rows + (p.listed ? (c & mask) * 16 : 0) >= p.hi) return;
+    const int page = p.table[slot];
+    if (page < 0 || page >= a.g.n_pages) {
+        atomicExch(a.g.err, kErrCounter);
+        return;
+    }
+    p.slot = slot;
+    p.page = page;
+}
+
 // Ranges that W units of work (cells, and `setup` for each key) are cut into:
 // one for each group of warps, and about a cell for each of its warps at least,
 // so that a short context is joined from few records
@@ -454,7 +510,8 @@ __device__ __forceinline__ void add_sum(Sum4& s, float M, float L, const float4&
     s.o.z = s.o.z * x + o.z * y;
     s.o.w = s.o.w * x + o.w * y;
 }
-template <int D>
+// (kHalf: the prefix tiles' records, fp16 and divided by their sums)
+template <int D, bool kHalf = false>
 __device__ __forceinline__ void add_records(const SplitArgs& a, Sum4& s, long long slot0, int first, int last, int step, int row, int col) {
     constexpr int U = 8;                               // records in flight
     for (int r0 = first; r0 < last; r0 += U * step) {
@@ -465,9 +522,15 @@ __device__ __forceinline__ void add_records(const SplitArgs& a, Sum4& s, long lo
             ml[i] = make_float2(kNegInf, 0.f);
             o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r0 + i * step < last) {
-                const long long at = (slot0 + r0 + i * step) * a.rec_rows + row;
-                ml[i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
-                o[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
+                const long long at = (slot0 + r0 + i * step) * (kHalf ? a.tile_rows : a.rec_rows) + row;
+                ml[i] = __ldcg(reinterpret_cast<const float2*>(kHalf ? a.part2_ml : a.part_ml) + at);
+                if constexpr (kHalf) {
+                    const uint2 h = __ldcg(reinterpret_cast<const uint2*>(a.part2_o + at * D + col));
+                    const float2 x = __half22float2(as_h2(h.x)), y = __half22float2(as_h2(h.y));
+                    o[i] = make_float4(x.x, x.y, y.x, y.y);
+                } else {
+                    o[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
+                }
             }
         }
         float m = s.M;
@@ -482,16 +545,17 @@ __device__ __forceinline__ void add_records(const SplitArgs& a, Sum4& s, long lo
         for (int i = 0; i < U; ++i) {
             const float w = ml[i].x == kNegInf ? 0.f : ex2(ml[i].x - m);
             s.L = fmaf(ml[i].y, w, s.L);
-            s.o.x = fmaf(o[i].x, w, s.o.x);
-            s.o.y = fmaf(o[i].y, w, s.o.y);
-            s.o.z = fmaf(o[i].z, w, s.o.z);
-            s.o.w = fmaf(o[i].w, w, s.o.w);
+            const float v = kHalf ? ml[i].y * w : w;
+            s.o.x = fmaf(o[i].x, v, s.o.x);
+            s.o.y = fmaf(o[i].y, v, s.o.y);
+            s.o.z = fmaf(o[i].z, v, s.o.z);
+            s.o.w = fmaf(o[i].w, v, s.o.w);
         }
     }
 }
 
 template <int NB, bool F8, int TILE>
-__global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(const SplitArgs a, const int stages) {
+__global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(const __grid_constant__ SplitArgs a, const int stages) {
     constexpr int D = NB * 32, D4 = D / 4;
     constexpr int kWarps = warps_of<NB, TILE>(), kThreads = kWarps * 32;
     constexpr bool HL = TILE == kF32;
@@ -605,7 +669,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     float* comb = reinterpret_cast<float*>(smem + kMaxGroups * S::qs) + (size_t)group * (gw / 2) * QPI * PAD;
     RowInfo& ri = s_ri[group];
     auto sync_group = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gw * 32) : "memory"); };
-    const int cpp = a.g.cells_per_page(), cps = a.g.page_shift - 4;       // cells a page, a power of two
+    const int cpp = a.g.cells_per_page();                  // a power of two
     const uint32_t ring = dev::smem_u32(smem) + (uint32_t)S::ring(a.E) + (uint32_t)(warp * stages * CELL);
     uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
     const uint32_t bar0 = dev::smem_u32(&s_bar[warp][0]);
@@ -664,97 +728,48 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             }
         }
     };
-    // the next fragment with cells from unit x on
-    auto next_fragment = [&](long long& x, Fragment& f) {
-        while (x < x1) {
-            fragment_at(f, plan, a.E, a.g.Hkv, a.setup, QPI, x, x1);
-            x += f.work;
-            if (f.ca < f.cb) return true;
-        }
-        return false;
-    };
-
     long long x = x0;
     Fragment f;
-    if (!next_fragment(x, f)) return;
-    load_queries(f);
-
-    // ---- the producer side of this warp's ring: its cells (every gw-th of
-    // each fragment) in order, `stages` ahead of their use.  Lanes look up the
-    // pages of 32 cells at once.
-    long long px = x0;                                  // behind the producer's fragment
-    int pc = 0, pcb = 0, pslot = -1, ppage = -1, pidx = 32;
-    const int* ptable = nullptr;
-    const int* plist = nullptr;
-    int pkh = 0, pc0 = 0, phi = 0;
-    auto produce = [&](int st) {
-        if (pc >= pcb) {
-            // the next fragment in which this warp has a cell
-            for (;;) {
-                Fragment n;
-                if (!next_fragment(px, n)) return;
-                pc = n.ca + gwarp;
-                if (pc >= n.cb) continue;
-                pcb = n.cb;
-                pc0 = n.c0;
-                pkh = n.kh;
-                int seq = n.e;
-                if (a.lists) seq = n.e / a.T;
-                else if (n.e >= a.n_seq) seq = a.group_start[n.e - a.n_seq];
-                ptable = a.tables + (long long)seq * a.g.max_pages;
-                plist = a.lists ? a.lists + ((long long)n.e * a.g.Hkv + n.kh) * a.keep : nullptr;
-                phi = a.lists ? a.lens[seq] - a.T + (n.e - seq * a.T) + 1 : 0x7fffffff;
-                pidx = 32;
-                break;
-            }
+    if (!next_fragment(f, x, x1, a, plan, QPI)) return;
+    Producer pr;
+    pr.x = x0;
+    pr.c = pr.cb = 0;
+    pr.slot = pr.page = -1;
+    pr.i = 32;
+    auto produce = [&](int st) {                           // the next cell of the ring, into stage st
+        if (pr.c >= pr.cb || pr.i == 32) {
+            refill(pr, a, plan, QPI, x1, gwarp, lane);
+            if (pr.c >= pr.cb) return;
         }
-        if (pidx == 32) {
-            pidx = 0;
-            const int c = pc + lane * gw;
-            pslot = ppage = -1;
-            if (c < pcb) {
-                if (plist) {
-                    pslot = plist[c >> cps];
-                    if (pslot >= a.g.max_pages) {
-                        atomicExch(a.g.err, kErrCounter);
-                        pslot = -1;
-                    }
-                    if (pslot >= 0 && pslot * a.g.page_rows + (c & (cpp - 1)) * 16 >= phi) pslot = -1;
-                } else {
-                    pslot = (pc0 + c) >> cps;
-                }
-                if (pslot >= 0) ppage = ptable[pslot];
-                if (pslot >= 0 && (ppage < 0 || ppage >= a.g.n_pages)) {
-                    atomicExch(a.g.err, kErrCounter);
-                    ppage = -1;
-                }
-            }
-        }
-        const int page = __shfl_sync(0xffffffffu, ppage, pidx), slot = __shfl_sync(0xffffffffu, pslot, pidx);
+        const int page = __shfl_sync(0xffffffffu, pr.page, pr.i), slot = __shfl_sync(0xffffffffu, pr.slot, pr.i);
         if (lane == 0) {
             const uint32_t bar = bar0 + 8u * st;
-            const int in = (plist ? pc : pc0 + pc) & (cpp - 1);
+            const int in = (pr.listed ? pr.c : pr.c0 + pr.c) & (cpp - 1);
             if (page >= 0) {
                 s_row0[warp][st] = slot * a.g.page_rows + in * 16;
                 dev::mbar_expect_tx(bar, CELL);
-                dev::bulk_g2s(ring + (uint32_t)(st * CELL), a.g.pool + page * a.g.page_bytes + (long long)(pkh * cpp + in) * CELL, CELL, bar);
+                dev::bulk_g2s(ring + (uint32_t)(st * CELL), a.g.pool + page * a.g.page_bytes + (long long)(pr.kh * cpp + in) * CELL, CELL, bar);
             } else {
                 s_row0[warp][st] = -1;
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
             }
         }
-        ++pidx;
-        pc += gw;
+        ++pr.i;
+        pr.c += a.gw;
     };
-    // one cell a warp, then the queries, then the other stages: query loads
-    // behind the whole first burst of copies would take 3 us
-    produce(0);
-    place_queries();
-    for (int st = 1; st < stages; ++st) produce(st);
 
     int st = 0;
     uint32_t phase = 0;
-    for (bool more = true; more;) {
+    for (bool first = true;; first = false) {
+        // one cell a warp, then the queries, then the other stages: query loads
+        // behind the whole first burst of copies would take 3 us
+        load_queries(f);
+        if (!first) sync_group();                          // the last fragment's sums and queries are free
+#pragma unroll 1
+        for (int s = 0; s < (first ? stages : 1); ++s) {
+            if (first) produce(s);
+            if (s == 0) place_queries();
+        }
         sync_group();
         const int g = lane >> 2, j = lane & 3;
         Acc<NB, F8, TILE> acc;
@@ -946,12 +961,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 }
             }
         }
-        more = next_fragment(x, f);
-        if (more) {
-            load_queries(f);
-            sync_group();                                  // the sums and queries are free again
-            place_queries();
-        }
+        if (!next_fragment(f, x, x1, a, plan, QPI)) break;
     }
     if (s_abort) {                                         // a wait ran out: let copies in flight land before the CTA ends
         const long long t0 = clock64();
@@ -964,7 +974,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
 // Outputs of a shared decode: D / 4 threads a row (sequence, t, head), over the
 // records of its own rows' key and of its group's prefix, and the sink.
 template <int NB>
-__global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) {
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ SplitArgs a, int QPI) {
     constexpr int D = NB * 32, D4 = D / 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -1002,11 +1012,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a, int QPI) 
                     const int kk = kh * nqb + qi / a.tile_rows;
                     const long long xa = pe.work * a.g.Hkv + (long long)kk * pe.nc;
                     const int c0 = range_of(xa, G2, W2), c1 = range_of(xa + pe.nc - 1, G2, W2);
-                    SplitArgs b = a;
-                    b.part_o = a.part2_o;
-                    b.part_ml = a.part2_ml;
-                    b.rec_rows = a.tile_rows;
-                    add_records<D>(b, s, (long long)pe.keys * a.g.Hkv + kk + c0, 0, c1 - c0 + 1, 1, qi % a.tile_rows, col);
+                    add_records<D, true>(a, s, (long long)pe.keys * a.g.Hkv + kk + c0, 0, c1 - c0 + 1, 1, qi % a.tile_rows, col);
                 }
             } else {
                 fold(a.n_seq + grp, qi);

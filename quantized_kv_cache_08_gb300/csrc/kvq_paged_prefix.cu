@@ -117,9 +117,6 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Row of a 32-row group that place p of a tile holds
-__host__ __device__ constexpr int place_row32(int p) { return ((p >> 2) & 1) * 16 + ((p >> 1) & 1) * 8 + (p >> 3) * 2 + (p & 1); }
-
 // ------------------------------------------------------------ unpacking
 
 // One warp's raw bytes of a pair of cells: K or V, of up to four blocks
@@ -286,6 +283,19 @@ __device__ __forceinline__ void store_v(uint32_t tile, int pr, int b0, int lane,
     }
 }
 
+// Places of a 32-row group whose rows lie in [lo, hi) and whose cells (bits of
+// there) are present: the row mask with index bits 4 and 2, 3 and 1 exchanged
+__device__ __forceinline__ uint32_t seen_places(int lo, int hi, int there) {
+    lo = min(max(lo, 0), 32);
+    hi = min(max(hi, 0), 32);
+    uint32_t m = (hi >= 32 ? 0xffffffffu : (1u << hi) - 1u) & ~(lo >= 32 ? 0xffffffffu : (1u << lo) - 1u);
+    m &= ((there & 1) ? 0x0000ffffu : 0u) | ((there & 2) ? 0xffff0000u : 0u);
+    uint32_t t = ((m >> 12) ^ m) & 0x0000f0f0u;              // index bits 4 and 2
+    m ^= t ^ (t << 12);
+    t = ((m >> 6) ^ m) & 0x00cc00ccu;                        // index bits 3 and 1
+    return m ^ t ^ (t << 6);
+}
+
 // ------------------------------------------------------------ the kernel
 
 // A CTA's part of a key: group, KV head, query block qb, tiles [ta, tb)
@@ -294,7 +304,7 @@ struct Part {
 };
 
 template <int NB, bool F8>
-__global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const SplitArgs a) {
+__global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __grid_constant__ SplitArgs a) {
     using S = Shape<NB>;
     constexpr int D = S::D, QT = S::QT, ST = S::ST, QB = 128 * QT;
     constexpr int NBT = NB == 2 ? 2 : 4, NQ4 = NB / NBT;       // blocks of an unpacking task, tasks a pair of cells
@@ -441,32 +451,46 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const Sp
                 const Query q = valid ? query_of(a, a.n_seq + p.grp, p.kh, qi) : Query{0, 0, 0, 0, 0};
                 const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
                                                                   (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D);
+                constexpr int PER = 8;                         // 16-byte pieces in registers at once
+                uint4 v[PER];
+                auto load = [&](int i0) {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) v[i] = valid ? src[i0 + i] : make_uint4(0u, 0u, 0u, 0u);
+                };
                 float am = 0.f;
-                if (valid) {
-                    lo = q.lo;
-                    hi = q.hi;
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = src[i];
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+                for (int i0 = D / 8 - PER; i0 >= 0; i0 -= PER) {
+                    load(i0);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             am = fmaxf(am, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
                     }
+                }
+                if (valid) {
+                    lo = q.lo;
+                    hi = q.hi;
                 }
                 const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -109), 110) : 0;
                 const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
                 // (K tiles hold the keys times 2^-8)
                 fac = a.qscale * __uint_as_float((uint32_t)(127 + ex + (F8 ? 0 : 8)) << 23);
                 const uint32_t dst = q_tile + qt * S::tile + row * 128;
-                for (int i = 0; i < D / 8; ++i) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (valid) v = src[i];
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t o[4];
+#pragma unroll 1
+                for (int i0 = 0; i0 < D / 8; i0 += PER) {
+                    if (i0 > 0) load(i0);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up));
-                    sts16(dst + (i >> 3) * (kTileRows * 128) + (((i & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+                    for (int k = 0; k < PER; ++k) {
+                        const int i = i0 + k;
+                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up));
+                        sts16(dst + (i >> 3) * (kTileRows * 128) + (((i & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -485,71 +509,75 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const Sp
                 const int row0 = (p.t0 + t) * kTileRows;
                 const int* okc = s_ok[tile_no % ST];
                 const int all = okc[0] & okc[1] & okc[2] & okc[3];
-                const bool edge = row0 < lo || row0 + kTileRows > hi || all != 3;
-                const bool masked = __any_sync(0xffffffffu, edge) || a.softcap_b > 0.f;
-                // scores of 32 columns, in the order of their places
-                auto scores = [&](int c, float (&s)[32]) {
-                    uint32_t r[32];
-                    tmem_ld32(s_addr + 32 * c, r);
-                    tmem_wait_ld();
+                const bool masked = __any_sync(0xffffffffu, row0 < lo || row0 + kTileRows > hi || all != 3);
+                const bool capped = a.softcap_b > 0.f;
+                // Two passes over the scores in 32-column pieces: the largest, then
+                // the probabilities.  Capped or masked scores are worked out in
+                // both, in log2 units; plain ones enter as they are (the factor is
+                // positive) and meet it in the exponent's fma.
+                const float f0 = capped ? 1.f : fac;
+                float top = dev::kNegInf, add = 0.f, l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(s_addr + 32 * c, r);
+                        tmem_wait_ld();
+                        if (capped) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]) * fac;
-                    if (masked) {
-                        const int there = okc[c];
+                            for (int i = 0; i < 32; ++i)
+                                r[i] = __float_as_uint(a.softcap_b * tanhf(a.softcap_a * (__uint_as_float(r[i]) * fac)));
+                        }
+                        if (masked) {
+                            const uint32_t see = seen_places(lo - row0 - 32 * c, hi - row0 - 32 * c, okc[c]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (a.softcap_b > 0.f) s[i] = a.softcap_b * tanhf(a.softcap_a * s[i]);
-                            const int at = row0 + 32 * c + place_row32(i);
-                            if (at < lo || at >= hi || !((there >> ((i >> 2) & 1)) & 1)) s[i] = dev::kNegInf;
+                            for (int i = 0; i < 32; ++i)
+                                if (!((see >> i) & 1u)) r[i] = 0xff800000u;
+                        }
+                        if (pass == 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(r[i]));
+                        } else {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float p0 = ex2(fmaf(__uint_as_float(r[2 * i]), f0, add));
+                                const float p1 = ex2(fmaf(__uint_as_float(r[2 * i + 1]), f0, add));
+                                l0 += p0;
+                                l1 += p1;
+                                pk[i] = as_u32(__floats2half2_rn(p0, p1));
+                            }
+                            tmem_st16(s_addr + 16 * c, pk);    // over columns that have been read
                         }
                     }
-                };
-                float top = dev::kNegInf;
+                    if (pass == 1) break;
+                    top *= f0;
+                    const bool move = top > m + dev::kLazy;
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float al = move ? ex2(m - top) : 1.f;
+                        if (move) m = top;
+                        l *= al;
+                        if (t > p.ta) {                        // O holds the tiles before: scale it between its products
+                            ok = wait(bars.o_done[qt], (n_tile - 1) & 1u);
+                            if (!ok) break;
+                            fence_after();
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float s[32];
-                    scores(c, s);
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t r[32];
+                                tmem_ld32(o_addr + 32 * c, r);
+                                tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i]);
-                }
-                const bool move = top > m + dev::kLazy;
-                if (__any_sync(0xffffffffu, move)) {
-                    const float al = move ? ex2(m - top) : 1.f;
-                    if (move) m = top;
-                    l *= al;
-                    if (t > p.ta) {                            // O holds the tiles before: scale it between its products
-                        ok = wait(bars.o_done[qt], (n_tile - 1) & 1u);
-                        if (!ok) break;
-                        fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t r[32];
-                            tmem_ld32(o_addr + 32 * c, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * al);
-                            tmem_st32(o_addr + 32 * c, r);
-                            tmem_wait_st();
+                                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * al);
+                                tmem_st32(o_addr + 32 * c, r);
+                                tmem_wait_st();
+                            }
                         }
                     }
+                    add = kShift - m;
                 }
-                const float add = kShift - m;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float s[32];
-                    scores(c, s);
-                    uint32_t pk[16];
-                    float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float p0 = ex2(s[2 * i] + add), p1 = ex2(s[2 * i + 1] + add);
-                        l0 += p0;
-                        l1 += p1;
-                        pk[i] = as_u32(__floats2half2_rn(p0, p1));
-                    }
-                    l += l0 + l1;
-                    tmem_st16(s_addr + 16 * c, pk);            // over columns that have been read
-                }
+                if (!ok) break;
+                l += l0 + l1;
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
@@ -564,6 +592,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const Sp
                 fence_after();
                 const long long slot = blockIdx.x + (long long)p.keys * a.g.Hkv + p.kk;
                 const long long at = slot * QB + qt * 128 + row;
+                const float inv = l > 0.f ? 1.0f / l : 0.f;    // fp16 records hold O / l, no larger than the values
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t r[32];
@@ -571,8 +600,9 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const Sp
                     tmem_wait_ld();
                     if (valid) {
                         uint4* dst = reinterpret_cast<uint4*>(a.part2_o + at * D + 32 * c);
+                        auto two = [&](int i) { return as_u32(__floats2half2_rn(__uint_as_float(r[i]) * inv, __uint_as_float(r[i + 1]) * inv)); };
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
                     }
                 }
                 if (valid) *reinterpret_cast<float2*>(a.part2_ml + at * 2) = make_float2(l > 0.f ? m - kShift : dev::kNegInf, l);
