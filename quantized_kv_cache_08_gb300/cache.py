@@ -179,6 +179,12 @@ def _token_rows(t, heads, dim, name):
     return t.data_ptr(), stride
 
 
+_DTYPE = {torch.float32: B.KVQ_F32, torch.bfloat16: B.KVQ_BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 class PagedKVCache:
     """One attention layer's cache in pages: a pool of `n_pages` pages of
     `page_rows` rows, in the formats of KVCache.  The caller keeps, as int32
@@ -210,7 +216,7 @@ class PagedKVCache:
         dev = torch.device(device)
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.device = dev
+        self.device, self.index = dev, dev.index
         self.n_kv_heads, self.head_dim, self.max_pages = n_kv_heads, head_dim, max_pages
         self.pool = self._buffer(pool, sz.pool, "pool")
         self.bounds = self._buffer(bounds_buf, sz.bounds, "bounds_buf") if bounds else None
@@ -233,18 +239,24 @@ class PagedKVCache:
             raise ValueError(f"{name} must be a contiguous uint8 tensor of {size} bytes on {self.device}")
         return t
 
-    def _dev(self, t, name):
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}")
+    # The checks below run before every call of a decode step, so they ask each
+    # tensor for as little as they can.
+    def _bad_ints(self, t, shape, name):
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on {self.device}")
 
     def _ints(self, t, shape, name):
-        if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != self.device:
-            raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on {self.device}")
+        if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != self.index or not t.is_contiguous():
+            self._bad_ints(t, shape, name)
         return t.data_ptr()
 
     def _batch(self, tables, lens):
         n = lens.shape[0] if lens.dim() == 1 else -1
         return n, self._ints(tables, (n, self.max_pages), "tables"), self._ints(lens, (n,), "lens")
+
+    def _dense(self, t, name):
+        if t.get_device() != self.index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor on {self.device}")
+        return t.data_ptr()
 
     def _rows(self, t, n, starts, name):
         """T, address of starts, rows of a [n, T, H, D] or packed [rows, H, D] tensor."""
@@ -256,14 +268,24 @@ class PagedKVCache:
             raise ValueError(f"{name} must be [rows, heads, dim] with starts")
         return 0, self._ints(starts, (n + 1,), "starts"), t.shape[0]
 
-    def _call(self, fn, *args, stream):
-        index = self.device.index
-        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-        if torch._C._cuda_getDevice() == index:
-            fn(self.handle, *args, s)
+    def _strided(self, t, heads, name):
+        """Address and row stride (elements) of rows that lie evenly apart."""
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} must be on {self.device}")
+        if t.is_contiguous():
+            return t.data_ptr(), heads * self.head_dim
+        return _token_rows(t, heads, self.head_dim, name)
+
+    def _stream(self, stream):
+        return _raw_stream(self.index) if stream is None else stream.cuda_stream
+
+    def _call(self, fn, *args):
+        """A call of the binding with the cache's device current."""
+        if _current_device() == self.index:
+            fn(self.handle, *args)
         else:
-            with torch.cuda.device(index):
-                fn(self.handle, *args, s)
+            with torch.cuda.device(self.index):
+                fn(self.handle, *args)
 
     def _new(self, shape, dtype, stream):
         out = torch.empty(shape, dtype=dtype, device=self.device)
@@ -276,83 +298,77 @@ class PagedKVCache:
         starts (int32 [n + 1]).  q (same form, any number of heads) is rotated
         into q_out (made if None; q itself when dense), which is returned."""
         n, tp, lp = self._batch(tables, lens)
-        if k.shape != v.shape or k.dtype != v.dtype:
-            raise ValueError("k and v must have one shape and dtype")
-        self._dev(k, "k")
-        self._dev(v, "v")
+        shape, code = k.shape, _DTYPE.get(k.dtype)
+        if v.shape != shape or v.dtype is not k.dtype or code is None:
+            raise ValueError("k and v must have one shape and one dtype, float32 or bfloat16")
+        if shape[-2:] != (self.n_kv_heads, self.head_dim):
+            raise ValueError(f"k shape {tuple(shape)} does not match the cache")
         T, sp, rows = self._rows(k, n, starts, "k")
-        kp, ks = _token_rows(k, self.n_kv_heads, self.head_dim, "k")
-        vp, vs = _token_rows(v, self.n_kv_heads, self.head_dim, "v")
+        kp, ks = self._strided(k, self.n_kv_heads, "k")
+        vp, vs = self._strided(v, self.n_kv_heads, "v")
         qp, qs, op, hq = None, 0, None, 0
         if q is not None:
             hq = q.shape[-2]
-            if q.dtype != k.dtype or q.shape[:-2] != k.shape[:-2]:
-                raise ValueError("q must have k's rows and dtype")
-            self._dev(q, "q")
-            qp, qs = _token_rows(q, hq, self.head_dim, "q")
+            if q.dtype is not k.dtype or q.shape[:-2] != shape[:-2] or q.shape[-1] != self.head_dim:
+                raise ValueError("q must have k's rows, head_dim and dtype")
+            qp, qs = self._strided(q, hq, "q")
             if q_out is None:
                 q_out = self._new(q.shape, q.dtype, stream)
-            if q_out.dtype != q.dtype or q_out.shape != q.shape or not q_out.is_contiguous():
-                raise ValueError("q_out must be contiguous with q's shape and dtype")
-            self._dev(q_out, "q_out")
-            op = q_out.data_ptr()
+            elif q_out.dtype is not q.dtype or q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape and dtype")
+            op = self._dense(q_out, "q_out")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        self._call(B.kvq_paged_append, kp, ks, vp, vs, qp, qs, op, hq, _dtype_code(k), tp, lp, n, T, sp, rows,
-                   stream=stream)
+        self._call(B.kvq_paged_append, kp, ks, vp, vs, qp, qs, op, hq, code, tp, lp, n, T, sp, rows,
+                   self._stream(stream))
         return q_out
 
     def read(self, tables, lens, k_out, v_out, starts=None, stream=None):
         """Each entry's last rows as values into k_out, v_out: float32/bfloat16
         [n, T, Hkv, D], or packed [rows, Hkv, D] with starts."""
         n, tp, lp = self._batch(tables, lens)
-        if k_out.shape != v_out.shape or k_out.dtype != v_out.dtype:
-            raise ValueError("k_out and v_out must have one shape and dtype")
+        code = _DTYPE.get(k_out.dtype)
+        if v_out.shape != k_out.shape or v_out.dtype is not k_out.dtype or code is None:
+            raise ValueError("k_out and v_out must have one shape and one dtype, float32 or bfloat16")
         if k_out.shape[-2:] != (self.n_kv_heads, self.head_dim):
             raise ValueError(f"k_out shape {tuple(k_out.shape)} does not match the cache")
-        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            self._dev(t, name)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
         T, sp, rows = self._rows(k_out, n, starts, "k_out")
-        self._call(B.kvq_paged_read, k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out), tp, lp, n, T, sp, rows,
-                   stream=stream)
+        self._call(B.kvq_paged_read, self._dense(k_out, "k_out"), self._dense(v_out, "v_out"), code, tp, lp, n, T, sp,
+                   rows, self._stream(stream))
 
     def update_bounds(self, tables, lens, T, stream=None):
         """Renew the key bounds of the pages that hold each sequence's last T
         rows (appends do this; for pages filled in another way)."""
         n, tp, lp = self._batch(tables, lens)
-        self._call(B.kvq_paged_bounds, tp, lp, n, T, None, n * T, stream=stream)
+        self._call(B.kvq_paged_bounds, tp, lp, n, T, None, n * T, self._stream(stream))
 
     def _query(self, q, tables, lens, sinks, scale, window, softcap, out, stream):
         n, tp, lp = self._batch(tables, lens)
-        _check_dev(q, "q")
-        self._dev(q, "q")
-        if q.dim() != 4 or q.shape[0] != n or q.shape[3] != self.head_dim:
-            raise ValueError(f"q shape {tuple(q.shape)} does not match the cache and lens")
+        shape, code = q.shape, _DTYPE.get(q.dtype)
+        if code is None or len(shape) != 4 or shape[0] != n or shape[3] != self.head_dim:
+            raise ValueError(f"q {q.dtype} {tuple(shape)} does not match the cache and lens")
+        qp = self._dense(q, "q")
         if out is None:
             out = torch.empty_like(q)
             if stream is not None:
                 out.record_stream(stream)
-        elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
-            raise ValueError("out must be contiguous with q's shape and dtype")
+            op = out.data_ptr()
         else:
-            self._dev(out, "out")
+            if out.dtype is not q.dtype or out.shape != shape:
+                raise ValueError("out must have q's shape and dtype")
+            op = self._dense(out, "out")
         sk = None
         if sinks is not None:
-            _check_dev(sinks, "sinks")
-            self._dev(sinks, "sinks")
-            if sinks.dtype != torch.float32 or sinks.numel() != q.shape[2]:
+            if sinks.dtype is not torch.float32 or sinks.numel() != shape[2]:
                 raise ValueError("sinks must be float32 [Hq]")
-            sk = sinks.data_ptr()
-        return out, B.kvq_paged_query(q.data_ptr(), out.data_ptr(), _dtype_code(q), n, q.shape[1], q.shape[2], tp, lp,
-                                      sk, scale, softcap, window)
+            sk = self._dense(sinks, "sinks")
+        return out, B.kvq_paged_query(qp, op, code, n, shape[1], shape[2], tp, lp, sk, scale, softcap, window)
 
     def decode(self, q, tables, lens, sinks=None, scale=0.0, window=0, softcap=0.0, out=None, stream=None):
         """q: float32/bfloat16 [n, T, Hq, D], the last T rows of each sequence;
         returns the attention outputs in q's shape and dtype."""
         out, a = self._query(q, tables, lens, sinks, scale, window, softcap, out, stream)
-        self._call(B.kvq_paged_decode, a, stream=stream)
+        self._call(B.kvq_paged_decode, a, self._stream(stream))
         return out
 
     def decode_shared(self, q, tables, lens, group_start, prefix_lens, sinks=None, scale=0.0, window=0, softcap=0.0,
@@ -363,7 +379,7 @@ class PagedKVCache:
         out, a = self._query(q, tables, lens, sinks, scale, window, softcap, out, stream)
         g = prefix_lens.numel()
         self._call(B.kvq_paged_decode_shared, a, self._ints(group_start, (g + 1,), "group_start"),
-                   self._ints(prefix_lens, (g,), "prefix_lens"), g, stream=stream)
+                   self._ints(prefix_lens, (g,), "prefix_lens"), g, self._stream(stream))
         return out
 
     def select(self, q, tables, lens, keep, n_first=1, n_last=1, pages=None, stream=None):
@@ -373,7 +389,7 @@ class PagedKVCache:
             pages = self._new((q.shape[0], q.shape[1], self.n_kv_heads, keep), torch.int32, stream)
         out, a = self._query(q, tables, lens, None, 0.0, 0, 0.0, q, stream)
         self._call(B.kvq_paged_select, a, self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"),
-                   keep, n_first, n_last, stream=stream)
+                   keep, n_first, n_last, self._stream(stream))
         return pages
 
     def decode_sparse(self, q, tables, lens, pages, sinks=None, scale=0.0, softcap=0.0, out=None, stream=None):
@@ -381,16 +397,12 @@ class PagedKVCache:
         out, a = self._query(q, tables, lens, sinks, scale, 0, softcap, out, stream)
         keep = pages.shape[-1]
         self._call(B.kvq_paged_decode_sparse, a,
-                   self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"), keep, stream=stream)
+                   self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"), keep, self._stream(stream))
         return out
 
     def device_error(self, stream=None):
         """0, or 1: a page number or length out of range, 2: a wait ran out (read and cleared)."""
-        e = None
-
-        def read(handle, s):
-            nonlocal e
-            e = B.kvq_paged_read_error(handle, s)
-
-        self._call(read, stream=stream)
-        return e
+        if _current_device() == self.index:
+            return B.kvq_paged_read_error(self.handle, self._stream(stream))
+        with torch.cuda.device(self.index):
+            return B.kvq_paged_read_error(self.handle, self._stream(stream))

@@ -41,6 +41,25 @@ struct Place {
 };
 
 #ifdef __CUDACC__
+// Launch as a programmatic dependent: the kernel waits (griddepcontrol.wait)
+// before it reads anything, so its start overlaps the end of the one before
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Byte of a page for a position of a sequence, or -1 with the error word set
 __device__ __forceinline__ long long page_at(const Geom& g, const int* table, int pos) {
     const int pg = table[pos >> g.page_shift];
@@ -131,6 +150,7 @@ struct SelectArgs {
     const int* lens;
     int* pages;            // [n_seq][T][Hkv][keep]
     uint32_t* keys;        // [n_seq][T][Hkv][max_pages] scores as ordered integers
+    int* arrived;          // [n_seq * T * Hkv] CTAs done; 0 between calls
     int keep, n_first, n_last;
 };
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t s);

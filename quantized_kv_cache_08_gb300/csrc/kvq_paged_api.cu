@@ -387,11 +387,12 @@ kvq_status kvq_paged_select(kvq_paged* c, const kvq_paged_query* a, int* pages, 
     s.lens = a->lens;
     s.pages = pages;
     s.keys = reinterpret_cast<uint32_t*>(c->ws + c->off_keys);
+    s.arrived = reinterpret_cast<int*>(c->ws + c->off_arrived);
     s.keep = keep;
     s.n_first = n_first;
     s.n_last = n_last;
     cudaError_t e = launch_select(s, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "page selection kernels");
+    return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "page selection kernel");
 }
 
 kvq_status kvq_paged_decode_sparse(kvq_paged* c, const kvq_paged_query* a, const int* pages, int keep, void* stream) {

@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row0 = blockIdx.x * TT;
     const int half = a.rope_dim / 2;
+    wait_for_earlier();
+    let_next_start();
     if (tid < TT) {
         Place p{-1, -1, 0, 0, 0};
         if (row0 + tid < a.r.rows) p = place_row(a.g, a.r, row0 + tid, true);
@@ -284,6 +286,8 @@ __device__ __forceinline__ void read_v8(const uint8_t* cell, int fp8, int t, int
 template <int LR>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
     constexpr int D = LR * 8, NB = D / 32;
+    wait_for_earlier();
+    let_next_start();
     const long long w = (long long)blockIdx.x * (kThreads / LR) + threadIdx.x / LR;
     const int row = (int)(w / a.g.Hkv), h = (int)(w - (long long)row * a.g.Hkv);
     if (row >= a.r.rows) return;
@@ -306,6 +310,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs a) {
 // 8 at a time (lane = row in the eight, 16 elements).
 template <int NB>
 __global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsArgs a) {
+    wait_for_earlier();
+    let_next_start();
     const int lane = threadIdx.x & 31;
     const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int per = a.g.Hkv * (NB / 2);
@@ -388,30 +394,27 @@ cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cuda
     const int gy = std::max(1, std::min(most, (2 * num_sms + gx - 1) / gx));
     const size_t smem = (size_t)TT * (a.rope_dim / 2) * sizeof(float2);
     const dim3 grid((unsigned)gx, (unsigned)gy);
-    if (a.g.D == 64) append_kernel<8><<<grid, kThreads, smem, s>>>(a, f, TT);
-    else if (a.g.D == 128) append_kernel<16><<<grid, kThreads, smem, s>>>(a, f, TT);
-    else append_kernel<32><<<grid, kThreads, smem, s>>>(a, f, TT);
-    return cudaGetLastError();
+    if (a.g.D == 64) return launch_dependent(append_kernel<8>, grid, kThreads, smem, s, a, f, TT);
+    if (a.g.D == 128) return launch_dependent(append_kernel<16>, grid, kThreads, smem, s, a, f, TT);
+    return launch_dependent(append_kernel<32>, grid, kThreads, smem, s, a, f, TT);
 }
 
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t s) {
     const int lr = a.g.D / 8;
     const long long groups = (long long)a.r.rows * a.g.Hkv;
     const unsigned grid = (unsigned)((groups + kThreads / lr - 1) / (kThreads / lr));
-    if (lr == 8) read_kernel<8><<<grid, kThreads, 0, s>>>(a);
-    else if (lr == 16) read_kernel<16><<<grid, kThreads, 0, s>>>(a);
-    else read_kernel<32><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    if (lr == 8) return launch_dependent(read_kernel<8>, dim3(grid), kThreads, 0, s, a);
+    if (lr == 16) return launch_dependent(read_kernel<16>, dim3(grid), kThreads, 0, s, a);
+    return launch_dependent(read_kernel<32>, dim3(grid), kThreads, 0, s, a);
 }
 
 cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t s) {
     const int nb = a.g.NB();
     const long long warps = (long long)a.r.rows * a.g.Hkv * (nb / 2);
     const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
-    if (nb == 2) bounds_kernel<2><<<grid, kThreads, 0, s>>>(a);
-    else if (nb == 4) bounds_kernel<4><<<grid, kThreads, 0, s>>>(a);
-    else bounds_kernel<8><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    if (nb == 2) return launch_dependent(bounds_kernel<2>, dim3(grid), kThreads, 0, s, a);
+    if (nb == 4) return launch_dependent(bounds_kernel<4>, dim3(grid), kThreads, 0, s, a);
+    return launch_dependent(bounds_kernel<8>, dim3(grid), kThreads, 0, s, a);
 }
 
 }  // namespace paged

@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     if (lane < stages) dev::mbar_init(dev::smem_u32(&s_bar[warp][lane]), 1);
     if (tid == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_earlier();
     // ---- the plan: prefix sums of the entries' work (one warp's scan for up to
     // 32 entries, else every thread's share and a scan over the CTA)
     {
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         if (!a.fuse && blockIdx.x == 0)
             for (int e = tid; e <= a.E; e += kThreads) a.plan[e] = plan[e];
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
     const long long W = plan[a.E].work * a.g.Hkv;
     const int G = ranges(a, W);
     if (a.fuse) {
@@ -976,7 +976,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
 template <int NB>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ SplitArgs a, int QPI) {
     constexpr int D = NB * 32, D4 = D / 4;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_earlier();
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     const long long row = i / D4;
     const int col = 4 * (int)(i % D4);
@@ -1031,17 +1031,8 @@ cudaError_t launch_split_t(const SplitArgs& a, cudaStream_t s) {
     constexpr size_t cells = (size_t)warps_of<NB, TILE>() * NB * (F8 ? 1024 : 928);
     // the ring takes what the plan leaves of 220 KB
     const int stages = (int)std::min<size_t>(kMaxStages, (220 * 1024 - S::ring(a.E)) / cells);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.G);
-    cfg.blockDim = dim3(warps_of<NB, TILE>() * 32);
-    cfg.dynamicSmemBytes = S::ring(a.E) + stages * cells;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split_kernel<NB, F8, TILE>, a, stages);
+    return launch_dependent(split_kernel<NB, F8, TILE>, dim3((unsigned)a.G), warps_of<NB, TILE>() * 32,
+                            S::ring(a.E) + stages * cells, s, a, stages);
 }
 
 template <int NB, bool F8>
@@ -1076,19 +1067,11 @@ cudaError_t launch_split(const SplitArgs& a, cudaStream_t s) {
 
 cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s) {
     const long long rows = (long long)a.n_seq * a.T * a.Hq;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows * (a.g.D / 4) + 255) / 256));
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    const dim3 grid((unsigned)((rows * (a.g.D / 4) + 255) / 256));
     switch (a.g.NB()) {
-        case 2: return cudaLaunchKernelEx(&cfg, merge_kernel<2>, a, a.tile);
-        case 4: return cudaLaunchKernelEx(&cfg, merge_kernel<4>, a, a.tile);
-        default: return cudaLaunchKernelEx(&cfg, merge_kernel<8>, a, a.tile);
+        case 2: return launch_dependent(merge_kernel<2>, grid, 256, 0, s, a, a.tile);
+        case 4: return launch_dependent(merge_kernel<4>, grid, 256, 0, s, a, a.tile);
+        default: return launch_dependent(merge_kernel<8>, grid, 256, 0, s, a, a.tile);
     }
 }
 

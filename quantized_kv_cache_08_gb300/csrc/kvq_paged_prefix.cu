@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_earlier();
     // ---- the plan: a warp a group (the rows its members see of the prefix), then
     // a scan by one warp; CTA 0 keeps it for the merge
     PlanEntry* plan = reinterpret_cast<PlanEntry*>(smem_raw + (base - dev::smem_u32(smem_raw)) + (QT + 2 * ST) * S::tile);
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
     __syncthreads();
     if (blockIdx.x == 0)
         for (int e = tid; e <= a.n_groups; e += S::kThreads) a.plan2[e] = plan[e];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
     const long long W = plan[a.n_groups].work * a.g.Hkv;
     const int G = (int)min((long long)a.G, W);
     if ((int)blockIdx.x >= G) return;
@@ -763,17 +763,8 @@ cudaError_t launch_t(const SplitArgs& a, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = kernel_attrs_once(prefix_kernel<NB, F8>, done, true);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.G);
-    cfg.blockDim = dim3(Shape<NB>::kThreads);
-    cfg.dynamicSmemBytes = Shape<NB>::smem + (size_t)(a.n_groups + 1) * sizeof(PlanEntry);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_kernel<NB, F8>, a);
+    return launch_dependent(prefix_kernel<NB, F8>, dim3((unsigned)a.G), Shape<NB>::kThreads,
+                            Shape<NB>::smem + (size_t)(a.n_groups + 1) * sizeof(PlanEntry), s, a);
 }
 
 }  // namespace

@@ -6,8 +6,10 @@
 // positive and negative parts give it exactly; the two scales and the sum over
 // blocks are single f32 operations in a fixed order.  Scores are therefore the
 // same numbers on every run, and ties (common between codes) go to the lowest
-// index.  Two kernels: scores, then the largest `keep` by a radix search for
-// the threshold, eight bits a pass, and a compaction in index order.
+// index.  One kernel: a CTA scores 256 pages of a KV head (NB lanes a page, the
+// query codes of four queries in registers), and the last CTA of an (entry, KV
+// head) picks: a radix search for the threshold over the bits in which the scores
+// differ, eight a pass, then a compaction in index order.
 #include "kvq_paged.cuh"
 
 #include <cuda_bf16.h>
@@ -20,8 +22,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSelThreads = 512;
-constexpr uint32_t kForced = 0xffffffffu;
+constexpr int kPages = 256;            // pages of a CTA
+constexpr int kKeep = 8192;            // keys that the pick holds in shared memory
 
 // number of pages with a row that query row t sees, -1 for a bad length
 __device__ __forceinline__ int page_count(const SelectArgs& a, int seq, int t, bool report) {
@@ -34,118 +36,55 @@ __device__ __forceinline__ int page_count(const SelectArgs& a, int seq, int t, b
     return hi > 0 ? (hi + a.g.page_rows - 1) >> a.g.page_shift : 0;
 }
 
-// f32 -> an unsigned integer of the same order (-0 counts as 0), below kForced
+// f32 -> an unsigned integer of the same order (-0 counts as 0)
 __device__ __forceinline__ uint32_t ordered(float s) {
     const uint32_t u = __float_as_uint(s + 0.f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Scores of pages [PB blockIdx.x, + PB) for KV head blockIdx.y and entry
-// blockIdx.z: NB lanes a page, one 32-element block each.
-template <int NB>
-__global__ void __launch_bounds__(kThreads) score_kernel(const SelectArgs a, int PB) {
-    constexpr int D = NB * 32;
-    constexpr int PW = 32 / NB;                        // pages a warp takes at once
-    extern __shared__ __align__(16) uint32_t s_q[];    // [hpk][NB][8 words positive, 8 words negative], then dq [hpk][NB]
-    float* s_dq = reinterpret_cast<float*>(s_q + (size_t)a.hpk * NB * 16);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int e = blockIdx.z, kh = blockIdx.y;
-    const int seq = e / a.T, t = e - seq * a.T;
-    const int np = page_count(a, seq, t, blockIdx.x == 0 && kh == 0 && tid == 0);
-    const int p0 = blockIdx.x * PB;
-    if (p0 >= np) return;
-    // query codes: a warp takes a block at a time
-    for (int i = warp; i < a.hpk * NB; i += kWarps) {
-        const int h = kh * a.hpk + i / NB, b = i - (i / NB) * NB;
-        const long long at = ((long long)e * a.Hq + h) * D + 32 * b + lane;
-        const float x = a.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.q)[at])
-                               : reinterpret_cast<const float*>(a.q)[at];
-        float am = fabsf(x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-        const float inv = am > 0.f ? __fmul_rn(__frcp_rn(am), 127.f) : 0.f;
-        const int c = (int)rintf(__fmul_rn(x, inv));
-        int8_t* dst = reinterpret_cast<int8_t*>(s_q + (size_t)i * 16);
-        dst[lane] = (int8_t)max(min(c, 127), 0);
-        dst[32 + lane] = (int8_t)min(max(c, -127), 0);
-        if (lane == 0) s_dq[i] = __fmul_rn(am, 1.0f / 127.0f);
-    }
-    __syncthreads();
-    const int* table = a.tables + (long long)seq * a.g.max_pages;
-    uint32_t* keys = a.keys + ((long long)e * a.g.Hkv + kh) * a.g.max_pages;
-    const int b = lane % NB, pl = lane / NB;
-    const int pe = min(np, p0 + PB);
-    for (int pb = p0 + warp * PW; pb < pe; pb += kWarps * PW) {
-        const int p = pb + pl;
-        bool ok = p < pe;
-        int pg = ok ? table[p] : 0;
-        if (ok && (pg < 0 || pg >= a.g.n_pages)) {
-            atomicExch(a.g.err, kErrCounter);
-            ok = false;
-        }
-        uint32_t mn[8] = {}, mx[8] = {};
-        float ds = 0.f;
-        if (ok) {
-            const long long at = ((long long)pg * a.g.Hkv + kh) * NB + b;
-            const uint4* src = reinterpret_cast<const uint4*>(a.codes + at * 64);
-            const uint4 v0 = src[0], v1 = src[1], v2 = src[2], v3 = src[3];
-            mn[0] = v0.x; mn[1] = v0.y; mn[2] = v0.z; mn[3] = v0.w; mn[4] = v1.x; mn[5] = v1.y; mn[6] = v1.z; mn[7] = v1.w;
-            mx[0] = v2.x; mx[1] = v2.y; mx[2] = v2.z; mx[3] = v2.w; mx[4] = v3.x; mx[5] = v3.y; mx[6] = v3.z; mx[7] = v3.w;
-            ds = a.scales[at];
-        }
-        float best = -__builtin_huge_valf();
-        for (int q = 0; q < a.hpk; ++q) {
-            const uint4* w = reinterpret_cast<const uint4*>(s_q + ((size_t)q * NB + b) * 16);
-            const uint4 w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
-            const uint32_t qp[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            const uint32_t qn[8] = {w2.x, w2.y, w2.z, w2.w, w3.x, w3.y, w3.z, w3.w};
-            int dot = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dot = __dp4a((int)qp[i], (int)mx[i], dot);
-                dot = __dp4a((int)qn[i], (int)mn[i], dot);
-            }
-            const float part = __fmul_rn(__fmul_rn(s_dq[q * NB + b], ds), (float)dot);
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) s = __fadd_rn(s, __shfl_sync(0xffffffffu, part, pl * NB + i));
-            best = fmaxf(best, s);
-        }
-        if (p < pe && b == 0) {
-            uint32_t key = ok ? ordered(best) : 0u;
-            if (p < a.n_first || p >= np - a.n_last) key = kForced;
-            keys[p] = key;
-        }
-    }
-}
-
-// The `keep` largest keys of one (entry, KV head), ties to the lowest index.
-__global__ void __launch_bounds__(kSelThreads) pick_kernel(const SelectArgs a) {
+// The `keep` pages of one (entry, KV head) of np > keep: the first n_first, the
+// last n_last and the best keys of the others, ties to the lowest index.
+__device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, uint32_t* s_keys, int np, int* out) {
     __shared__ int s_hist[256];
-    __shared__ int s_wsum[kSelThreads / 32], s_weq[kSelThreads / 32];
-    __shared__ uint32_t s_prefix;
+    __shared__ int s_gt[kWarps], s_eq[kWarps];
+    __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
+    __shared__ uint32_t s_digit;
     __shared__ int s_need;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int e = blockIdx.y, kh = blockIdx.x;
-    const int seq = e / a.T, t = e - seq * a.T;
-    const int np = page_count(a, seq, t, false);
-    const uint32_t* keys = a.keys + ((long long)e * a.g.Hkv + kh) * a.g.max_pages;
-    int* out = a.pages + ((long long)e * a.g.Hkv + kh) * a.keep;
-    const int keep = min(a.keep, np);
-    for (int i = keep + tid; i < a.keep; i += kSelThreads) out[i] = -1;
-    if (keep == np) {
-        for (int i = tid; i < keep; i += kSelThreads) out[i] = i;
-        return;
+    const bool in_smem = np <= kKeep;
+    const int first = a.n_first, last = np - a.n_last;      // pages [first, last) compete
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    for (int i = tid; i < np; i += kThreads) {
+        const uint32_t k = __ldcg(g_keys + i);
+        if (in_smem) s_keys[i] = k;
+        if (i >= first && i < last) {
+            lo = min(lo, k);
+            hi = max(hi, k);
+        }
     }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        s_lo[warp] = lo;
+        s_hi[warp] = hi;
+    }
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+        lo = min(lo, s_lo[w]);
+        hi = max(hi, s_hi[w]);
+    }
+    auto key = [&](int i) { return (in_smem ? s_keys[i] : __ldcg(g_keys + i)) - lo; };
+    int need = a.keep - a.n_first - a.n_last;               // of the competing pages
     uint32_t prefix = 0;
-    int need = keep;                                    // keys still to find among those that share the prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) s_hist[tid] = 0;
+    int bits = hi > lo ? 32 - __clz(hi - lo) : 0;           // in which the keys differ
+    while (bits > 0 && need > 0) {
+        const int shift = max(0, bits - 8);
+        s_hist[tid] = 0;
         __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int i = tid; i < np; i += kSelThreads) {
-            const uint32_t k = keys[i];
-            if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255u], 1);
+        const uint32_t mask = bits >= 32 ? 0u : 0xffffffffu << bits;
+        for (int i = first + tid; i < last; i += kThreads) {
+            const uint32_t k = key(i);
+            if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << (bits - shift)) - 1u)], 1);
         }
         __syncthreads();
         if (warp == 0) {
@@ -165,68 +104,195 @@ __global__ void __launch_bounds__(kSelThreads) pick_kernel(const SelectArgs a) {
             int before = x - sum;
             if (before < need && x >= need) {
                 int i = 0;
-                while (before + c[i] < need) before += c[i++];
-                s_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
+#pragma unroll
+                for (int k = 0; k < 7; ++k)
+                    if (i == k && before + c[k] < need) {
+                        before += c[k];
+                        i = k + 1;
+                    }
+                s_digit = (uint32_t)(255 - 8 * lane - i);
                 s_need = need - before;
             }
         }
         __syncthreads();
-        prefix = s_prefix;
+        prefix |= s_digit << shift;
         need = s_need;
+        bits = shift;
     }
-    // keys above the threshold and the first `need` that equal it, in order
-    int done = 0, eq_done = 0;
-    for (int base = 0; base < np; base += kSelThreads) {
-        const int i = base + tid;
-        const uint32_t k = i < np ? keys[i] : 0u;
-        const bool gt = i < np && k > prefix, eq = i < np && k == prefix;
-        const unsigned me = __ballot_sync(0xffffffffu, eq), mg = __ballot_sync(0xffffffffu, gt);
-        const unsigned below = (1u << lane) - 1u;
-        if (lane == 0) {
-            s_weq[warp] = __popc(me);
-            s_wsum[warp] = __popc(mg);
+    // competing keys above the threshold and the first `need` that equal it, in
+    // index order: each warp counts its share of the pages, then writes it
+    const int per = ((np + kWarps - 1) / kWarps + 31) & ~31, b0 = warp * per, b1 = min(np, b0 + per);
+    const bool none = a.keep == a.n_first + a.n_last;
+    int gt = 0, eq = 0;
+    for (int base = b0; base < b1; base += 32) {
+        const int i = base + lane;
+        const bool in = i < b1, forced = in && (i < first || i >= last);
+        const uint32_t k = in ? key(i) : 0u;
+        gt += __popc(__ballot_sync(0xffffffffu, forced || (in && !none && k > prefix)));
+        eq += __popc(__ballot_sync(0xffffffffu, in && !forced && !none && k == prefix));
+    }
+    if (lane == 0) {
+        s_gt[warp] = gt;
+        s_eq[warp] = eq;
+    }
+    __syncthreads();
+    int at = 0, e0 = 0;
+    for (int w = 0; w < warp; ++w) {
+        at += s_gt[w];
+        e0 += s_eq[w];
+    }
+    const unsigned below = (1u << lane) - 1u;
+    for (int base = b0; base < b1; base += 32) {
+        const int i = base + lane;
+        const bool in = i < b1, forced = in && (i < first || i >= last);
+        const uint32_t k = in ? key(i) : 0u;
+        const bool up = forced || (in && !none && k > prefix), same = in && !forced && !none && k == prefix;
+        const unsigned mg = __ballot_sync(0xffffffffu, up), me = __ballot_sync(0xffffffffu, same);
+        const int rank = e0 + __popc(me & below);           // equal keys before this one
+        if (up || (same && rank < need)) out[at + __popc(mg & below) + min(rank, need)] = i;
+        at += __popc(mg);
+        e0 += __popc(me);
+    }
+}
+
+// Scores of pages [kPages blockIdx.x, + kPages) for KV head blockIdx.y and entry
+// blockIdx.z: NB lanes a page, one 32-element block each; then the pick.
+template <int NB>
+__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
+    constexpr int D = NB * 32;
+    constexpr int PW = 32 / NB;                        // pages a warp takes at once
+    constexpr int IT = kPages / (kWarps * PW);         // times it does
+    extern __shared__ __align__(16) uint32_t s_dyn[];  // query codes [hpk][NB][8 words positive, 8 negative], dq [hpk][NB]; then the pick's keys
+    __shared__ int s_last;
+    uint32_t* s_q = s_dyn;
+    float* s_dq = reinterpret_cast<float*>(s_q + (size_t)a.hpk * NB * 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int e = blockIdx.z, kh = blockIdx.y;
+    const int seq = e / a.T, t = e - seq * a.T;
+    wait_for_earlier();
+    let_next_start();
+    const int np = page_count(a, seq, t, blockIdx.x == 0 && kh == 0 && tid == 0);
+    const int p0 = blockIdx.x * kPages;
+    int* out = a.pages + ((long long)e * a.g.Hkv + kh) * a.keep;
+    if (blockIdx.x == 0)
+        for (int i = min(a.keep, np) + tid; i < a.keep; i += kThreads) out[i] = -1;
+    if (np <= a.keep) {                                // all pages: no scores
+        if (blockIdx.x == 0)
+            for (int i = tid; i < np; i += kThreads) out[i] = i;
+        return;
+    }
+    if (p0 >= np) return;
+    // page numbers and bounds of this lane's pages, on their way while the
+    // query is coded
+    const int* table = a.tables + (long long)seq * a.g.max_pages;
+    const int b = lane % NB, pl = lane / NB;
+    const int pe = min(np, p0 + kPages);
+    int pg[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int p = p0 + (i * kWarps + warp) * PW + pl;
+        pg[i] = p < pe ? table[p] : -2;
+    }
+    for (int i = warp; i < a.hpk * NB; i += kWarps) {  // a warp codes a block at a time
+        const int h = kh * a.hpk + i / NB, bb = i - (i / NB) * NB;
+        const long long at = ((long long)e * a.Hq + h) * D + 32 * bb + lane;
+        const float x = a.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.q)[at])
+                               : reinterpret_cast<const float*>(a.q)[at];
+        const float am = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(x))));
+        const float inv = am > 0.f ? __fmul_rn(__frcp_rn(am), 127.f) : 0.f;
+        const int c = (int)rintf(__fmul_rn(x, inv));
+        int8_t* dst = reinterpret_cast<int8_t*>(s_q + (size_t)i * 16);
+        dst[lane] = (int8_t)max(min(c, 127), 0);
+        dst[32 + lane] = (int8_t)min(max(c, -127), 0);
+        if (lane == 0) s_dq[i] = __fmul_rn(am, 1.0f / 127.0f);
+    }
+    __syncthreads();
+    uint32_t* keys = a.keys + ((long long)e * a.g.Hkv + kh) * a.g.max_pages;
+    float best[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) best[i] = -__builtin_huge_valf();
+    for (int q0 = 0; q0 < a.hpk; q0 += 4) {            // four queries' codes in registers
+        uint32_t qp[4][8], qn[4][8];
+        float dq[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int q = min(q0 + j, a.hpk - 1);      // (a repeated query changes no maximum)
+            const uint4* w = reinterpret_cast<const uint4*>(s_q + ((size_t)q * NB + b) * 16);
+            const uint4 w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
+            qp[j][0] = w0.x; qp[j][1] = w0.y; qp[j][2] = w0.z; qp[j][3] = w0.w;
+            qp[j][4] = w1.x; qp[j][5] = w1.y; qp[j][6] = w1.z; qp[j][7] = w1.w;
+            qn[j][0] = w2.x; qn[j][1] = w2.y; qn[j][2] = w2.z; qn[j][3] = w2.w;
+            qn[j][4] = w3.x; qn[j][5] = w3.y; qn[j][6] = w3.z; qn[j][7] = w3.w;
+            dq[j] = s_dq[q * NB + b];
         }
-        __syncthreads();
-        int eb = eq_done, gb = done, et = 0, gt_all = 0;
-        for (int w = 0; w < kSelThreads / 32; ++w) {
-            if (w < warp) {
-                eb += s_weq[w];
-                gb += s_wsum[w];
+#pragma unroll 2
+        for (int i = 0; i < IT; ++i) {
+            uint32_t mn[8] = {}, mx[8] = {};
+            float ds = 0.f;
+            if (pg[i] >= 0 && pg[i] < a.g.n_pages) {
+                const long long at = ((long long)pg[i] * a.g.Hkv + kh) * NB + b;
+                const uint4* src = reinterpret_cast<const uint4*>(a.codes + at * 64);
+                const uint4 v0 = src[0], v1 = src[1], v2 = src[2], v3 = src[3];
+                mn[0] = v0.x; mn[1] = v0.y; mn[2] = v0.z; mn[3] = v0.w; mn[4] = v1.x; mn[5] = v1.y; mn[6] = v1.z; mn[7] = v1.w;
+                mx[0] = v2.x; mx[1] = v2.y; mx[2] = v2.z; mx[3] = v2.w; mx[4] = v3.x; mx[5] = v3.y; mx[6] = v3.z; mx[7] = v3.w;
+                ds = a.scales[at];
             }
-            et += s_weq[w];
-            gt_all += s_wsum[w];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                int dot = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    dot = __dp4a((int)qp[j][k], (int)mx[k], dot);
+                    dot = __dp4a((int)qn[j][k], (int)mn[k], dot);
+                }
+                const float part = __fmul_rn(__fmul_rn(dq[j], ds), (float)dot);
+                float s = 0.f;
+#pragma unroll
+                for (int k = 0; k < NB; ++k) s = __fadd_rn(s, __shfl_sync(0xffffffffu, part, pl * NB + k));
+                best[i] = fmaxf(best[i], s);
+            }
         }
-        const int erank = eb + __popc(me & below);       // equal keys before this one
-        // taken before this one: greater keys, and equal ones up to `need`
-        const int at = gb + __popc(mg & below) + min(erank, need);
-        if (gt || (eq && erank < need)) out[at] = i;
-        done += gt_all;
-        eq_done += et;
-        __syncthreads();
     }
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int p = p0 + (i * kWarps + warp) * PW + pl;
+        if (p >= pe || b != 0) continue;
+        const bool ok = pg[i] >= 0 && pg[i] < a.g.n_pages;
+        if (!ok) atomicExch(a.g.err, kErrCounter);
+        keys[p] = ok ? ordered(best[i]) : 0u;
+    }
+    // the last CTA of the (entry, KV head) picks
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const int n = (np + kPages - 1) / kPages;
+        int* cnt = a.arrived + (long long)e * a.g.Hkv + kh;
+        s_last = n == 1 || atomicAdd(cnt, 1) == n - 1;
+        if (s_last && n > 1) *cnt = 0;
+        __threadfence();
+    }
+    __syncthreads();
+    if (s_last) pick(a, keys, s_dyn, np, out);
 }
 
 }  // namespace
 
-cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
-    const int E = a.n_seq * a.T, nb = a.g.NB();
-    const int PB = 64;
-    const dim3 grid((unsigned)((a.g.max_pages + PB - 1) / PB), (unsigned)a.g.Hkv, (unsigned)E);
-    const size_t smem = (size_t)a.hpk * nb * (16 * 4 + 4);
-    if (smem > 48 * 1024) {                              // 128 queries a KV head at head_dim 256: 68 KB
-        static std::atomic<unsigned long long> d2{0}, d4{0}, d8{0};
-        cudaError_t e = nb == 2 ? kernel_attrs_once(score_kernel<2>, d2, false)
-                      : nb == 4 ? kernel_attrs_once(score_kernel<4>, d4, false)
-                                : kernel_attrs_once(score_kernel<8>, d8, false);
-        if (e != cudaSuccess) return e;
-    }
-    if (nb == 2) score_kernel<2><<<grid, kThreads, smem, s>>>(a, PB);
-    else if (nb == 4) score_kernel<4><<<grid, kThreads, smem, s>>>(a, PB);
-    else score_kernel<8><<<grid, kThreads, smem, s>>>(a, PB);
-    cudaError_t e = cudaGetLastError();
+template <int NB>
+static cudaError_t launch_t(const SelectArgs& a, cudaStream_t s) {
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = kernel_attrs_once(select_kernel<NB>, done, false);
     if (e != cudaSuccess) return e;
-    pick_kernel<<<dim3((unsigned)a.g.Hkv, (unsigned)E), kSelThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const size_t codes = (size_t)a.hpk * NB * (16 * 4 + 4), keys = (size_t)std::min(a.g.max_pages, kKeep) * 4;
+    const dim3 grid((unsigned)((a.g.max_pages + kPages - 1) / kPages), (unsigned)a.g.Hkv, (unsigned)(a.n_seq * a.T));
+    return launch_dependent(select_kernel<NB>, grid, kThreads, std::max(codes, keys), s, a);
+}
+
+cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
+    switch (a.g.NB()) {
+        case 2: return launch_t<2>(a, s);
+        case 4: return launch_t<4>(a, s);
+        default: return launch_t<8>(a, s);
+    }
 }
 
 }  // namespace paged
