@@ -104,13 +104,49 @@ __device__ __forceinline__ void rotate8(float (&x)[8], int e0, int rot, int inte
     }
 }
 
+// Codes of 8 elements by q8_0's or q5_1's rule, round-half-away(t) for
+// t = x / d (or (x - m) / d) clamped to [lo, hi].  Adding 1.5 * 2^23 leaves the
+// nearest integer in the low bits of the sum; where t lies within 1e-3 of a
+// half, or the scale is a subnormal half (a quotient of low precision), the
+// format's own fp64 decision is taken instead.
+template <bool V>
+__device__ __forceinline__ void codes8(const float (&x)[8], float m, float d, int (&code)[8]) {
+    constexpr float kMagic = 12582912.f;
+    const float inv = d > 0.f ? 1.0f / d : 0.f;
+    bool near = d < 6.2e-5f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float t = (V ? x[i] - m : x[i]) * inv;
+        if (V) t = fminf(fmaxf(t, -0.25f), 31.25f);
+        const float y = t + kMagic;
+        near |= fabsf(t - (y - kMagic)) > 0.499f;
+        const int c = __float_as_int(y) - __float_as_int(kMagic);
+        code[i] = V ? min(max(c, 0), 31) : c;
+    }
+    if (near) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            float xi = x[0];
+#pragma unroll
+            for (int k = 1; k < 8; ++k)
+                if (k == i) xi = x[k];
+            const int c = d > 0.f ? (V ? q5_code(xi, m, d, inv) : q8_code(xi, d, inv)) : 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k == i) code[k] = c;
+        }
+    }
+}
+
 // One append CTA: tokens [TT blockIdx.x, + TT), row units blockIdx.y, + gridDim.y..
-// A unit is 32 / LR heads of one kind (query, key, value) of one token.
+// A unit is a warp's rows of one kind of one token: 64 / LR query heads (a lane
+// holds 8 elements and the 8 that they are rotated with), or 32 / LR key or
+// value heads (8 elements a lane, four lanes a block).
 template <int LR>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
     extern __shared__ float2 s_cs[];               // [TT][rope_dim / 2]
     __shared__ Place s_place[16];
-    constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR;
+    constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR, QPW = 64 / LR, QL = LR / 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row0 = blockIdx.x * TT;
     const int half = a.rope_dim / 2;
@@ -134,8 +170,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
         s_cs[i] = make_float2(cs, sn);
     }
     __syncthreads();
-    const int uq = a.q ? (a.Hq + JPW - 1) / JPW : 0, uk = (a.g.Hkv + JPW - 1) / JPW;
+    const int uq = a.q ? (a.Hq + QPW - 1) / QPW : 0, uk = (a.g.Hkv + JPW - 1) / JPW;
     const int units = uq + 2 * uk;
+    // a query lane's two pieces: partners of the half-split rotation, else side by side
+    const int ql = lane % QL, split = a.interleaved ? 0 : a.rope_dim / 16;
+    const int qa = 8 * (ql < split ? ql : split + 2 * (ql - split) + (a.interleaved ? 0 : split));
+    const int qb = ql < split ? qa + half : qa + 8;
     const int li = lane % LR, e0 = 8 * li;
     for (int w = blockIdx.y * kWarps + warp; w < units * TT; w += gridDim.y * kWarps) {
         const int tt = w / units;
@@ -145,12 +185,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
         const float2* cs = s_cs + tt * half;
         const long long row = row0 + tt;
         if (u < uq) {
-            const int h = u * JPW + lane / LR;
-            const bool on = h < a.Hq;
-            float x[8] = {};
-            if (on) load8(a.q, row * a.q_stride + h * D + e0, a.bf16, x);
-            rotate8(x, e0, a.rope_dim, a.interleaved, cs, lane);
-            if (on) store8(a.q_out, (row * a.Hq + h) * D + e0, a.bf16, x);
+            const int h = u * QPW + lane / QL;
+            if (h >= a.Hq) continue;               // (no shuffles on this path)
+            float x[8], y[8];
+            const long long src = row * a.q_stride + h * D, dst = (row * a.Hq + h) * D;
+            load8(a.q, src + qa, a.bf16, x);
+            load8(a.q, src + qb, a.bf16, y);
+            if (a.interleaved) {
+                rotate8(x, qa, a.rope_dim, 1, cs, lane);
+                rotate8(y, qb, a.rope_dim, 1, cs, lane);
+            } else if (ql < split) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 c = cs[qa + i];
+                    const float p = x[i], q = y[i];
+                    x[i] = p * c.x - q * c.y;
+                    y[i] = p * c.y + q * c.x;
+                }
+            }
+            store8(a.q_out, dst + qa, a.bf16, x);
+            store8(a.q_out, dst + qb, a.bf16, y);
             continue;
         }
         u -= uq;
@@ -168,8 +222,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
             uint32_t w2[2] = {0u, 0u};
             if (a.g.fp8) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w2[i >> 2] |= (uint32_t)__nv_cvt_float_to_fp8(x[i], __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
+                for (int i = 0; i < 8; i += 2)
+                    w2[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[i], x[i + 1]), __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
             } else {
                 float m = 0.f;
 #pragma unroll
@@ -177,13 +231,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 const unsigned short db = half_quotient(m, (double)m, 127.f);
-                const float d = __half2float(__ushort_as_half(db));
-                const float inv = d > 0.f ? 1.0f / d : 0.f;
+                int code[8];
+                codes8<false>(x, 0.f, __half2float(__ushort_as_half(db)), code);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int code = d > 0.f ? q8_code(x[i], d, inv) : 0;
-                    w2[i >> 2] |= (uint32_t)(code + 128) << (8 * (i & 3));
-                }
+                for (int i = 0; i < 8; i += 4)
+                    w2[i >> 2] = __byte_perm(__byte_perm(code[i], code[i + 1], 0x0040), __byte_perm(code[i + 2], code[i + 3], 0x0040), 0x5410) ^ 0x80808080u;
                 if (on && c == 0)
                     *reinterpret_cast<unsigned short*>(cell + 512 * NB + (j * NB + b) * 8 + i4 * 2) = db;
             }
@@ -212,24 +264,20 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, co
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const unsigned short db = half_quotient(mx - mn, (double)mx - (double)mn, 31.f);
         const unsigned short mb = __half_as_ushort(__float2half_rn(mn));
-        const float d = __half2float(__ushort_as_half(db)), m = __half2float(__ushort_as_half(mb));
-        const float inv = d > 0.f ? 1.0f / d : 0.f;
+        int code[8];
+        codes8<true>(x, __half2float(__ushort_as_half(mb)), __half2float(__ushort_as_half(db)), code);
         uint32_t unit[2], nib[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            uint32_t code[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) code[r] = d > 0.f ? (uint32_t)q5_code(x[4 * e + r], m, d, inv) : 0u;
-            unit[e] = code[0] | (code[1] << 5) | (code[2] << 10) | ((code[3] >> 4) << 15);
-            nib[e] = code[3] & 15u;
+            unit[e] = (uint32_t)(code[4 * e] | (code[4 * e + 1] << 5) | (code[4 * e + 2] << 10) | ((code[4 * e + 3] >> 4) << 15));
+            nib[e] = (uint32_t)code[4 * e + 3] & 15u;
         }
         // nibbles of blocks b and b + 1 share a byte: the even block's lane
         // writes the byte of g = 2c, the odd block's that of g = 2c + 1
         const uint32_t other = __shfl_xor_sync(0xffffffffu, (b & 1) ? nib[0] : nib[1], 4);
         if (on) {
             uint8_t* dm = cell + 864 * NB + (j * NB + b) * 16 + i4 * 2;
-            if (c == 0) *reinterpret_cast<unsigned short*>(dm) = db;
-            if (c == 1) *reinterpret_cast<unsigned short*>(dm + 8) = mb;
+            if (c < 2) *reinterpret_cast<unsigned short*>(dm + 8 * c) = c ? mb : db;
             uint8_t* up = cell + 544 * NB + (n >> 2) * 512 + (n & 3) * 4 + s * 2;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -384,11 +432,11 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsArgs a) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cudaStream_t s) {
-    const int jpw = 256 / a.g.D;
-    const int units = (a.q ? (a.Hq + jpw - 1) / jpw : 0) + 2 * ((a.g.Hkv + jpw - 1) / jpw);
+    const int jpw = 256 / a.g.D, qpw = 2 * jpw;
+    const int units = (a.q ? (a.Hq + qpw - 1) / qpw : 0) + 2 * ((a.g.Hkv + jpw - 1) / jpw);
     // tokens per CTA: the angles are shared by its heads; few rows spread over
     // the SMs by heads instead
-    const int TT = a.r.rows >= 8 * num_sms ? 4 : 1;
+    const int TT = a.r.rows >= 16 * num_sms ? 8 : a.r.rows >= 4 * num_sms ? 2 : 1;
     const int gx = (a.r.rows + TT - 1) / TT;
     const int most = (units * TT + kWarps - 1) / kWarps;
     const int gy = std::max(1, std::min(most, (2 * num_sms + gx - 1) / gx));
