@@ -62,16 +62,22 @@ __device__ __forceinline__ void store8(void* base, long long idx, int bf16, cons
     }
 }
 
-// fp16 of the exact quotient num / den (num >= 0; den 127 or 31), to nearest
-// even in one rounding.  The fp32 quotient decides unless it lies within a few
-// of its own steps of a midpoint between two halves (low 13 bits near 0x1000),
-// or is so small that the half is subnormal; then fp64 does.  `lo` is what num
-// as a float leaves out.
-__device__ __forceinline__ unsigned short half_quotient(float num, double exact_num, float den) {
+// fp16 of the exact quotient (num + err) / den, to nearest even in one rounding
+// (den 127 or 31; num >= 0, err what num as a float leaves out).  The fp32
+// quotient decides unless it lies within a few of its own steps of a midpoint
+// between two halves (low 13 bits near 0x1000): there num is compared with
+// midpoint x den, which is exact in fp32 (12 + 7 bits), as is the difference.
+// Subnormal halves are left to fp64.
+__device__ __forceinline__ unsigned short half_quotient(float num, float err, float den) {
     const float q = __fdiv_rn(num, den);
-    const unsigned low = __float_as_uint(q) & 0x1fffu;
-    if (q < 6.2e-5f || (low >= 0x0ff8u && low <= 0x1008u))
-        return __half_as_ushort(__double2half(exact_num / (double)den));
+    if (q < 6.2e-5f) return __half_as_ushort(__double2half(((double)num + (double)err) / (double)den));
+    const uint32_t bits = __float_as_uint(q), low = bits & 0x1fffu;
+    if (low >= 0x0ff8u && low <= 0x1008u) {
+        const uint32_t down = bits & ~0x1fffu;
+        const float r = (num - __uint_as_float(down | 0x1000u) * den) + err;
+        const bool up = r > 0.f || (r == 0.f && ((down >> 13) & 1u));
+        return __half_as_ushort(__float2half_rn(__uint_as_float(up ? down + 0x2000u : down)));
+    }
     return __half_as_ushort(__float2half_rn(q));
 }
 
@@ -104,26 +110,27 @@ __device__ __forceinline__ void rotate8(float (&x)[8], int e0, int rot, int inte
     }
 }
 
-// Codes of 8 elements by q8_0's or q5_1's rule, round-half-away(t) for
-// t = x / d (or (x - m) / d) clamped to [lo, hi].  Adding 1.5 * 2^23 leaves the
-// nearest integer in the low bits of the sum; where t lies within 1e-3 of a
-// half, or the scale is a subnormal half (a quotient of low precision), the
-// format's own fp64 decision is taken instead.
+// Codes of 8 elements by q8_0's or q5_1's rule: round-half-away(t) for t = x / d
+// or (x - m) / d, clamped.  Adding 1.5 * 2^23 leaves the nearest integer in the
+// low bits of the sum; t itself is off by less than 2e-5.  Where it lies within
+// 1e-4 of k + 1/2 the exact rule decides: 2 |x| >= (2k + 1) d, both sides exact
+// in fp32 (d has 11 bits, the odd number 8), or the same of x - m with the part
+// that its float leaves out.  Subnormal scales are left to the fp64 rule.
 template <bool V>
 __device__ __forceinline__ void codes8(const float (&x)[8], float m, float d, int (&code)[8]) {
     constexpr float kMagic = 12582912.f;
     const float inv = d > 0.f ? 1.0f / d : 0.f;
-    bool near = d < 6.2e-5f;
+    bool near = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float t = (V ? x[i] - m : x[i]) * inv;
         if (V) t = fminf(fmaxf(t, -0.25f), 31.25f);
         const float y = t + kMagic;
-        near |= fabsf(t - (y - kMagic)) > 0.499f;
+        near |= fabsf(t - (y - kMagic)) > 0.4999f;
         const int c = __float_as_int(y) - __float_as_int(kMagic);
         code[i] = V ? min(max(c, 0), 31) : c;
     }
-    if (near) {
+    if (d < 6.2e-5f) {
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
             float xi = x[0];
@@ -134,6 +141,20 @@ __device__ __forceinline__ void codes8(const float (&x)[8], float m, float d, in
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (k == i) code[k] = c;
+        }
+    } else if (near) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float s = V ? x[i] - m : x[i];
+            const float z = s - x[i];
+            const float e = V ? (x[i] - (s - z)) - (m + z) : 0.f;        // x - m = s + e
+            const float t = fabsf(s * inv);
+            const float k = floorf(t);
+            if (fabsf(t - k - 0.5f) < 1e-4f && !(V && (s < 0.f || k > 30.f))) {
+                const float r = (2.f * fabsf(s) - (2.f * k + 1.f) * d) + (s < 0.f ? -2.f : 2.f) * e;
+                const int n = (int)k + (r >= 0.f ? 1 : 0);
+                code[i] = s < 0.f ? -n : n;
+            }
         }
     }
 }
@@ -230,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                 for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const unsigned short db = half_quotient(m, (double)m, 127.f);
+                const unsigned short db = half_quotient(m, 0.f, 127.f);
                 int code[8];
                 codes8<false>(x, 0.f, __half2float(__ushort_as_half(db)), code);
 #pragma unroll
@@ -262,7 +283,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const unsigned short db = half_quotient(mx - mn, (double)mx - (double)mn, 31.f);
+        const float range = mx - mn, back = range - mx;
+        const unsigned short db = half_quotient(range, (mx - (range - back)) - (mn + back), 31.f);
         const unsigned short mb = __half_as_ushort(__float2half_rn(mn));
         int code[8];
         codes8<true>(x, __half2float(__ushort_as_half(mb)), __half2float(__ushort_as_half(db)), code);
