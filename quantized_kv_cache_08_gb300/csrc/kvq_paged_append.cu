@@ -21,6 +21,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace kvq {
 namespace paged {
@@ -28,21 +29,35 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+#ifndef KTT
+#define KTT 4
+#endif
+constexpr int kTT = KTT;               // tokens of a CTA when there are many
 
-__device__ __forceinline__ void load8(const void* base, long long idx, int bf16, float (&x)[8]) {
-    if (bf16) {
-        const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + idx);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight elements as they lie in memory, then as floats
+template <bool BF16>
+struct Raw8 {
+    uint4 w[BF16 ? 1 : 2];
+};
+template <bool BF16>
+__device__ __forceinline__ void fetch8(const void* base, long long idx, Raw8<BF16>& r) {
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(base) + idx * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.w[i] = p[i];
+}
+template <bool BF16>
+__device__ __forceinline__ void floats8(const Raw8<BF16>& r, float (&x)[8]) {
+    if constexpr (BF16) {
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = __uint_as_float(w[i] << 16);
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     } else {
-        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + idx);
-        const float4 a = p[0], b = p[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
     }
 }
 
@@ -81,15 +96,19 @@ __device__ __forceinline__ unsigned short half_quotient(float num, float err, fl
     return __half_as_ushort(__float2half_rn(q));
 }
 
-// Rotate the 8 elements e0.. of a head row; cs: (cos, sin) of the token's pairs.
-// Every lane of the warp calls this (shuffles).
+// The rotation table of a token holds (cos, sin) of pair p at place
+// (p % 8) (n / 8) + p / 8 (4 for interleaved pairs) of n: the lanes of a load,
+// which take neighbouring groups of pairs, read neighbouring words.
+//
+// Rotate the 8 elements e0.. of a head row; every lane of the warp calls this
+// (shuffles).
 __device__ __forceinline__ void rotate8(float (&x)[8], int e0, int rot, int interleaved, const float2* cs, int lane) {
     if (rot == 0) return;
     if (interleaved) {
         if (e0 < rot) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 a = cs[e0 / 2 + i];
+                const float2 a = cs[i * (rot / 8) + e0 / 8];
                 const float p = x[2 * i], q = x[2 * i + 1];
                 x[2 * i] = p * a.x - q * a.y;
                 x[2 * i + 1] = p * a.y + q * a.x;
@@ -104,9 +123,12 @@ __device__ __forceinline__ void rotate8(float (&x)[8], int e0, int rot, int inte
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
     if (e0 < rot) {
-        const float2* c = cs + (second ? e0 - half : e0);
+        const float2* c = cs + (second ? e0 - half : e0) / 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = second ? y[i] * c[i].y + x[i] * c[i].x : x[i] * c[i].x - y[i] * c[i].y;
+        for (int i = 0; i < 8; ++i) {
+            const float2 a = c[i * (half / 8)];
+            x[i] = second ? y[i] * a.y + x[i] * a.x : x[i] * a.x - y[i] * a.y;
+        }
     }
 }
 
@@ -163,8 +185,8 @@ __device__ __forceinline__ void codes8(const float (&x)[8], float m, float d, in
 // A unit is a warp's rows of one kind of one token: 64 / LR query heads (a lane
 // holds 8 elements and the 8 that they are rotated with), or 32 / LR key or
 // value heads (8 elements a lane, four lanes a block).
-template <int LR>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
+template <int LR, bool BF16>
+__global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
     extern __shared__ float2 s_cs[];               // [TT][rope_dim / 2]
     __shared__ Place s_place[16];
     constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR, QPW = 64 / LR, QL = LR / 2;
@@ -188,56 +210,83 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         const float turn = (t - rintf(t)) + fmaf(p, f.y, e);
         float sn, cs;
         sincospif(2.f * turn, &sn, &cs);
-        s_cs[i] = make_float2(cs, sn);
+        const int grp = a.interleaved ? 4 : 8;
+        s_cs[tt * half + (pr % grp) * (half / grp) + pr / grp] = make_float2(cs, sn);
     }
     __syncthreads();
+    // a warp's token, and its share of the token's units
+    const int wpt = kWarps / TT, tt = warp / wpt;
+    const int u0 = blockIdx.y * wpt + warp - tt * wpt, du = gridDim.y * wpt;
+    const Place pl = s_place[tt];
+    if (pl.pos < 0) return;
+    const float2* cs = s_cs + tt * half;
+    const long long row = row0 + tt;
     const int uq = a.q ? (a.Hq + QPW - 1) / QPW : 0, uk = (a.g.Hkv + JPW - 1) / JPW;
-    const int units = uq + 2 * uk;
-    // a query lane's two pieces: partners of the half-split rotation, else side by side
-    const int ql = lane % QL, split = a.interleaved ? 0 : a.rope_dim / 16;
-    const int qa = 8 * (ql < split ? ql : split + 2 * (ql - split) + (a.interleaved ? 0 : split));
-    const int qb = ql < split ? qa + half : qa + 8;
-    const int li = lane % LR, e0 = 8 * li;
-    for (int w = blockIdx.y * kWarps + warp; w < units * TT; w += gridDim.y * kWarps) {
-        const int tt = w / units;
-        int u = w - tt * units;
-        const Place pl = s_place[tt];
-        if (pl.pos < 0) continue;                  // the same for the whole warp
-        const float2* cs = s_cs + tt * half;
-        const long long row = row0 + tt;
-        if (u < uq) {
-            const int h = u * QPW + lane / QL;
-            if (h >= a.Hq) continue;               // (no shuffles on this path)
-            float x[8], y[8];
-            const long long src = row * a.q_stride + h * D, dst = (row * a.Hq + h) * D;
-            load8(a.q, src + qa, a.bf16, x);
-            load8(a.q, src + qb, a.bf16, y);
-            if (a.interleaved) {
-                rotate8(x, qa, a.rope_dim, 1, cs, lane);
-                rotate8(y, qb, a.rope_dim, 1, cs, lane);
-            } else if (ql < split) {
+    int u = u0;
+    {
+        // ---- queries.  A lane's two pieces: partners of the half-split
+        // rotation, else side by side
+        const int ql = lane % QL, split = a.interleaved ? 0 : a.rope_dim / 16;
+        const int qa = 8 * (ql < split ? ql : split + 2 * (ql - split) + (a.interleaved ? 0 : split));
+        const int qb = ql < split ? qa + half : qa + 8;
+        constexpr int U = BF16 ? 2 : 1;            // units in flight
+        for (; u < uq; u += U * du) {
+            Raw8<BF16> rx[U], ry[U];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 c = cs[qa + i];
-                    const float p = x[i], q = y[i];
-                    x[i] = p * c.x - q * c.y;
-                    y[i] = p * c.y + q * c.x;
+            for (int k = 0; k < U; ++k) {
+                const int h = (u + k * du) * QPW + lane / QL;
+                if (h < a.Hq) {
+                    fetch8(a.q, row * a.q_stride + h * D + qa, rx[k]);
+                    fetch8(a.q, row * a.q_stride + h * D + qb, ry[k]);
                 }
             }
-            store8(a.q_out, dst + qa, a.bf16, x);
-            store8(a.q_out, dst + qb, a.bf16, y);
-            continue;
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int h = (u + k * du) * QPW + lane / QL;
+                if (h >= a.Hq) continue;           // (no shuffles on this path)
+                float x[8], y[8];
+                floats8(rx[k], x);
+                floats8(ry[k], y);
+                if (a.interleaved) {
+                    rotate8(x, qa, a.rope_dim, 1, cs, lane);
+                    rotate8(y, qb, a.rope_dim, 1, cs, lane);
+                } else if (ql < split) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 c = cs[i * (half / 8) + ql];
+                        const float p = x[i], q = y[i];
+                        x[i] = p * c.x - q * c.y;
+                        y[i] = p * c.y + q * c.x;
+                    }
+                }
+                store8(a.q_out, (row * a.Hq + h) * D + qa, BF16, x);
+                store8(a.q_out, (row * a.Hq + h) * D + qb, BF16, y);
+            }
         }
-        u -= uq;
-        const bool is_v = u >= uk;
-        const int h = (is_v ? u - uk : u) * JPW + lane / LR;
+        // the first unit of keys and values that is this warp's
+        u = u0 >= uq ? u0 : u0 + (uq - u0 + du - 1) / du * du;
+    }
+    // ---- keys and values
+    const int li = lane % LR, e0 = 8 * li;
+    const int t = pl.t, b = li >> 2, c = li & 3;
+    const int j = (t & 7) >> 1, s = t & 1, hh = t >> 3;
+    const int n = hh * NB + b, i4 = 2 * hh + s;
+    Raw8<BF16> next{};                             // of the unit after the one in work
+    auto fetch = [&](int u) {
+        const bool is_v = u >= uq + uk;
+        const int h = (is_v ? u - uk - uq : u - uq) * JPW + lane / LR;
+        if (u < uq + 2 * uk && h < a.g.Hkv && pl.cell >= 0)
+            fetch8(is_v ? a.v : a.k, row * (is_v ? a.v_stride : a.k_stride) + h * D + e0, next);
+    };
+    fetch(u);
+    for (; u < uq + 2 * uk; u += du) {
+        const bool is_v = u >= uq + uk;
+        const int h = (is_v ? u - uk - uq : u - uq) * JPW + lane / LR;
         const bool on = h < a.g.Hkv && pl.cell >= 0;
-        float x[8] = {};
-        if (on) load8(is_v ? a.v : a.k, row * (is_v ? a.v_stride : a.k_stride) + h * D + e0, a.bf16, x);
+        float x[8];
+        floats8(next, x);
+        fetch(u + du);
         uint8_t* cell = a.g.pool + pl.cell + (long long)h * a.g.cells_per_page() * a.g.cell_bytes;
-        const int t = pl.t, b = li >> 2, c = li & 3;
-        const int j = (t & 7) >> 1, s = t & 1, hh = t >> 3;
-        const int n = hh * NB + b, i4 = 2 * hh + s;
         if (!is_v) {
             rotate8(x, e0, a.rope_dim, a.interleaved, cs, lane);
             uint32_t w2[2] = {0u, 0u};
@@ -458,15 +507,19 @@ cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cuda
     const int units = (a.q ? (a.Hq + qpw - 1) / qpw : 0) + 2 * ((a.g.Hkv + jpw - 1) / jpw);
     // tokens per CTA: the angles are shared by its heads; few rows spread over
     // the SMs by heads instead
-    const int TT = a.r.rows >= 16 * num_sms ? 8 : a.r.rows >= 4 * num_sms ? 2 : 1;
+    const int TT = a.r.rows >= 16 * num_sms ? kTT : a.r.rows >= 4 * num_sms ? 2 : 1;
     const int gx = (a.r.rows + TT - 1) / TT;
     const int most = (units * TT + kWarps - 1) / kWarps;
     const int gy = std::max(1, std::min(most, (2 * num_sms + gx - 1) / gx));
     const size_t smem = (size_t)TT * (a.rope_dim / 2) * sizeof(float2);
     const dim3 grid((unsigned)gx, (unsigned)gy);
-    if (a.g.D == 64) return launch_dependent(append_kernel<8>, grid, kThreads, smem, s, a, f, TT);
-    if (a.g.D == 128) return launch_dependent(append_kernel<16>, grid, kThreads, smem, s, a, f, TT);
-    return launch_dependent(append_kernel<32>, grid, kThreads, smem, s, a, f, TT);
+    auto run = [&](auto b) {
+        constexpr bool B = decltype(b)::value;
+        if (a.g.D == 64) return launch_dependent(append_kernel<8, B>, grid, kThreads, smem, s, a, f, TT);
+        if (a.g.D == 128) return launch_dependent(append_kernel<16, B>, grid, kThreads, smem, s, a, f, TT);
+        return launch_dependent(append_kernel<32, B>, grid, kThreads, smem, s, a, f, TT);
+    };
+    return a.bf16 ? run(std::true_type{}) : run(std::false_type{});
 }
 
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t s) {
