@@ -422,22 +422,23 @@ struct Producer {
     const int* table;
     const int* list;
 };
-__device__ __forceinline__ void refill(Producer& p, const SplitArgs& a, const PlanEntry* plan, int QPI, long long x1, int gwarp, int lane) {
-    while (p.c >= p.cb) {          // the next fragment in which this warp has a cell
-        Fragment n;
-        if (!next_fragment(n, p.x, x1, a, plan, QPI)) return;
-        p.c = n.ca + gwarp;
-        p.cb = n.cb;
-        p.c0 = n.c0;
-        p.kh = n.kh;
-        int seq = n.e;
-        if (a.lists) seq = n.e / a.T;
-        else if (n.e >= a.n_seq) seq = a.group_start[n.e - a.n_seq];
-        p.table = a.tables + (long long)seq * a.g.max_pages;
-        p.listed = a.lists != nullptr;
-        p.list = a.lists ? a.lists + ((long long)n.e * a.g.Hkv + n.kh) * a.keep : nullptr;
-        p.hi = a.lists ? a.lens[seq] - a.T + (n.e - seq * a.T) + 1 : 0x7fffffff;
-    }
+// The producer enters a fragment
+__device__ __forceinline__ void enter(Producer& p, const SplitArgs& a, const Fragment& n, int gwarp) {
+    p.c = n.ca + gwarp;
+    p.cb = n.cb;
+    p.c0 = n.c0;
+    p.kh = n.kh;
+    int seq = n.e;
+    if (a.lists) seq = n.e / a.T;
+    else if (n.e >= a.n_seq) seq = a.group_start[n.e - a.n_seq];
+    p.table = a.tables + (long long)seq * a.g.max_pages;
+    p.listed = a.lists != nullptr;
+    p.list = a.lists ? a.lists + ((long long)n.e * a.g.Hkv + n.kh) * a.keep : nullptr;
+    p.hi = a.lists ? a.lens[seq] - a.T + (n.e - seq * a.T) + 1 : 0x7fffffff;
+}
+// Look up this warp's next 32 cells of the fragment (page numbers are checked
+// where they are used, so that the load need not be waited for here)
+__device__ __forceinline__ void look_up(Producer& p, const SplitArgs& a, int lane) {
     p.i = 0;
     const int cps = a.g.page_shift - 4, mask = (1 << cps) - 1;
     const int c = p.c + lane * a.gw;
@@ -449,18 +450,23 @@ __device__ __forceinline__ void refill(Producer& p, const SplitArgs& a, const Pl
         slot = -1;
     }
     if (slot < 0 || slot * a.g.page_rows + (p.listed ? (c & mask) * 16 : 0) >= p.hi) return;
-    const int page = p.table[slot];
-    if (page < 0 || page >= a.g.n_pages) {
-        atomicExch(a.g.err, kErrCounter);
-        return;
-    }
     p.slot = slot;
-    p.page = page;
+    p.page = p.table[slot];
+}
+// On to the next fragment in which this warp has a cell; false: none
+__device__ __forceinline__ bool refill(Producer& p, const SplitArgs& a, const PlanEntry* plan, int QPI, long long x1, int gwarp) {
+    while (p.c >= p.cb) {
+        Fragment n;
+        if (!next_fragment(n, p.x, x1, a, plan, QPI)) return false;
+        enter(p, a, n, gwarp);
+    }
+    return true;
 }
 
 // Ranges that W units of work (cells, and `setup` for each key) are cut into:
-// one for each group of warps, and about a cell for each of its warps at least,
-// so that a short context is joined from few records
+// one for each group of warps, and about a cell for each of its warps at least
+// (of 1, 2, 4 and 6 cells a warp, 1 was best or near it at every size: longer
+// ranges save records but leave SMs idle)
 __device__ __forceinline__ int ranges(const SplitArgs& a, long long W) {
     return (int)min((long long)a.G * a.groups, (W + a.gw - 1) / a.gw);
 }
@@ -577,6 +583,107 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     if (lane < stages) dev::mbar_init(dev::smem_u32(&s_bar[warp][lane]), 1);
     if (tid == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // ---- the CTA's groups of gw warps work on ranges of their own: while one
+    // group joins and changes keys (some 5 us of latencies) the others compute
+    const int gw = a.gw, group = warp / gw, gwarp = warp - group * gw, gtid = tid - group * gw * 32;
+    const int range = group * gridDim.x + blockIdx.x;
+    uint8_t* qs = smem + group * S::qs;
+    float* comb = reinterpret_cast<float*>(smem + kMaxGroups * S::qs) + (size_t)group * (gw / 2) * QPI * PAD;
+    RowInfo& ri = s_ri[group];
+    auto sync_group = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gw * 32) : "memory"); };
+    const int cpp = a.g.cells_per_page();                  // a power of two
+    const uint32_t ring = dev::smem_u32(smem) + (uint32_t)S::ring(a.E) + (uint32_t)(warp * stages * CELL);
+    uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
+    const uint32_t bar0 = dev::smem_u32(&s_bar[warp][0]);
+
+    // ---- queries: a warp takes every gw-th query row of the fragment, loads it
+    // into registers and later lays it out as A fragments in shared memory
+    constexpr int RPW = QPI / 4;                       // rows of a warp at most
+    float qv[RPW][NB];
+    Query qq[RPW];
+    auto load_queries = [&](const Fragment& f) {
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+            const int r = gwarp + i * gw, qi = f.sl * QPI + r;
+            qq[i] = Query{0, 0, 0, 0, -1};
+            const bool valid = r < QPI && qi < f.nq;
+            if (valid) qq[i] = query_of(a, f.e, f.kh, qi);
+            const long long at = (((long long)qq[i].seq * a.T + qq[i].t) * a.Hq + qq[i].h) * D + lane;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) qv[i][b] = valid ? load_q(a.q, at + 32 * b, a.bf16) : 0.f;
+        }
+    };
+    auto place_queries = [&]() {
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+            const int r = gwarp + i * gw;
+            if (r >= QPI) break;
+            float am = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) am = fmaxf(am, fabsf(qv[i][b]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            // scaled by a power of two to a largest element in [512, 1024)
+            const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -117), 118) : 0;
+            const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
+            if (lane == 0) {
+                ri.fac[r] = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
+                ri.lo[r] = qq[i].lo;
+                ri.hi[r] = qq[i].hi;
+            }
+            const int wi = lane & 7, j = lane >> 3;
+            const int reg = ((wi & 3) >> 1) * 2, half = wi & 1;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float y = qv[i][b] * up;
+                const __half hi = __float2half_rn(y);
+                const int at = (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
+                __half* dst = reinterpret_cast<__half*>(qs + at * (TILE == kT8 ? 8 : 16));
+                if (TILE == kT8) {
+                    dst[reg + half] = hi;
+                } else if (HL) {
+                    dst[2 * reg + half] = hi;
+                    dst[2 * (reg + 1) + half] = __float2half_rn(y - __half2float(hi));
+                } else {
+                    dst[2 * (reg + (r >> 3)) + half] = hi;
+                }
+            }
+        }
+    };
+    long long W = 0, x = 0, x1 = 0;
+    int G = 1;
+    Fragment f{};
+    Producer pr;
+    pr.c = pr.cb = 0;
+    pr.slot = pr.page = -1;
+    pr.i = 32;
+    auto produce = [&](int st) {                           // the next cell of the ring, into stage st
+        if (pr.c >= pr.cb) {
+            if (!refill(pr, a, plan, QPI, x1, gwarp)) return;
+            pr.i = 32;
+        }
+        if (pr.i == 32) look_up(pr, a, lane);
+        const int page = __shfl_sync(0xffffffffu, pr.page, pr.i), slot = __shfl_sync(0xffffffffu, pr.slot, pr.i);
+        if (lane == 0) {
+            const uint32_t bar = bar0 + 8u * st;
+            const int in = (pr.listed ? pr.c : pr.c0 + pr.c) & (cpp - 1);
+            const bool there = page >= 0 && page < a.g.n_pages;
+            if (slot >= 0 && !there) atomicExch(a.g.err, kErrCounter);
+            if (there) {
+                s_row0[warp][st] = slot * a.g.page_rows + in * 16;
+                dev::mbar_expect_tx(bar, CELL);
+                dev::bulk_g2s(ring + (uint32_t)(st * CELL), a.g.pool + page * a.g.page_bytes + (long long)(pr.kh * cpp + in) * CELL, CELL, bar);
+            } else {
+                s_row0[warp][st] = -1;
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+            }
+        }
+        ++pr.i;
+        pr.c += a.gw;
+    };
+
+    int st = 0;
+    uint32_t phase = 0;
     wait_for_earlier();
     // ---- the plan: prefix sums of the entries' work (one warp's scan for up to
     // 32 entries, else every thread's share and a scan over the CTA)
@@ -649,8 +756,8 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             for (int e = tid; e <= a.E; e += kThreads) a.plan[e] = plan[e];
     }
     let_next_start();
-    const long long W = plan[a.E].work * a.g.Hkv;
-    const int G = ranges(a, W);
+    W = plan[a.E].work * a.g.Hkv;
+    G = ranges(a, W);
     if (a.fuse) {
         // entries without rows have no key: their outputs are zeros
         for (int e = blockIdx.x; e < a.E; e += gridDim.x) {
@@ -659,115 +766,21 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             for (long long i = 4 * tid; i < n; i += 4 * kThreads) store4(a, at + i, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
         }
     }
-    // ---- the CTA's groups of gw warps work on ranges of their own: while one
-    // group joins and changes keys (some 5 us of latencies) the others compute
-    const int gw = a.gw, group = warp / gw, gwarp = warp - group * gw, gtid = tid - group * gw * 32;
-    const int range = group * gridDim.x + blockIdx.x;
     if (range >= G) return;
-    const long long x0 = mul_div(W, range, G), x1 = mul_div(W, range + 1, G);
-    uint8_t* qs = smem + group * S::qs;
-    float* comb = reinterpret_cast<float*>(smem + kMaxGroups * S::qs) + (size_t)group * (gw / 2) * QPI * PAD;
-    RowInfo& ri = s_ri[group];
-    auto sync_group = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gw * 32) : "memory"); };
-    const int cpp = a.g.cells_per_page();                  // a power of two
-    const uint32_t ring = dev::smem_u32(smem) + (uint32_t)S::ring(a.E) + (uint32_t)(warp * stages * CELL);
-    uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
-    const uint32_t bar0 = dev::smem_u32(&s_bar[warp][0]);
-
-    // ---- queries: a warp takes every gw-th query row of the fragment, loads it
-    // into registers and later lays it out as A fragments in shared memory
-    constexpr int RPW = QPI / 4;                       // rows of a warp at most
-    float qv[RPW][NB];
-    Query qq[RPW];
-    auto load_queries = [&](const Fragment& f) {
-#pragma unroll
-        for (int i = 0; i < RPW; ++i) {
-            const int r = gwarp + i * gw, qi = f.sl * QPI + r;
-            qq[i] = Query{0, 0, 0, 0, -1};
-            const bool valid = r < QPI && qi < f.nq;
-            if (valid) qq[i] = query_of(a, f.e, f.kh, qi);
-            const long long at = (((long long)qq[i].seq * a.T + qq[i].t) * a.Hq + qq[i].h) * D + lane;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) qv[i][b] = valid ? load_q(a.q, at + 32 * b, a.bf16) : 0.f;
-        }
-    };
-    auto place_queries = [&]() {
-#pragma unroll
-        for (int i = 0; i < RPW; ++i) {
-            const int r = gwarp + i * gw;
-            if (r >= QPI) break;
-            float am = 0.f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) am = fmaxf(am, fabsf(qv[i][b]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-            // scaled by a power of two to a largest element in [512, 1024)
-            const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -117), 118) : 0;
-            const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
-            if (lane == 0) {
-                ri.fac[r] = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
-                ri.lo[r] = qq[i].lo;
-                ri.hi[r] = qq[i].hi;
-            }
-            const int wi = lane & 7, j = lane >> 3;
-            const int reg = ((wi & 3) >> 1) * 2, half = wi & 1;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const float y = qv[i][b] * up;
-                const __half hi = __float2half_rn(y);
-                const int at = (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
-                __half* dst = reinterpret_cast<__half*>(qs + at * (TILE == kT8 ? 8 : 16));
-                if (TILE == kT8) {
-                    dst[reg + half] = hi;
-                } else if (HL) {
-                    dst[2 * reg + half] = hi;
-                    dst[2 * (reg + 1) + half] = __float2half_rn(y - __half2float(hi));
-                } else {
-                    dst[2 * (reg + (r >> 3)) + half] = hi;
-                }
-            }
-        }
-    };
-    long long x = x0;
-    Fragment f;
+    x = mul_div(W, range, G);
+    x1 = mul_div(W, range + 1, G);
     if (!next_fragment(f, x, x1, a, plan, QPI)) return;
-    Producer pr;
-    pr.x = x0;
-    pr.c = pr.cb = 0;
-    pr.slot = pr.page = -1;
-    pr.i = 32;
-    auto produce = [&](int st) {                           // the next cell of the ring, into stage st
-        if (pr.c >= pr.cb || pr.i == 32) {
-            refill(pr, a, plan, QPI, x1, gwarp, lane);
-            if (pr.c >= pr.cb) return;
-        }
-        const int page = __shfl_sync(0xffffffffu, pr.page, pr.i), slot = __shfl_sync(0xffffffffu, pr.slot, pr.i);
-        if (lane == 0) {
-            const uint32_t bar = bar0 + 8u * st;
-            const int in = (pr.listed ? pr.c : pr.c0 + pr.c) & (cpp - 1);
-            if (page >= 0) {
-                s_row0[warp][st] = slot * a.g.page_rows + in * 16;
-                dev::mbar_expect_tx(bar, CELL);
-                dev::bulk_g2s(ring + (uint32_t)(st * CELL), a.g.pool + page * a.g.page_bytes + (long long)(pr.kh * cpp + in) * CELL, CELL, bar);
-            } else {
-                s_row0[warp][st] = -1;
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-            }
-        }
-        ++pr.i;
-        pr.c += a.gw;
-    };
-
-    int st = 0;
-    uint32_t phase = 0;
-    for (bool first = true;; first = false) {
+    pr.x = x;
+    enter(pr, a, f, gwarp);
+    look_up(pr, a, lane);
+    for (int pass = 0;; ++pass) {
         // one cell a warp, then the queries, then the other stages: query loads
         // behind the whole first burst of copies would take 3 us
         load_queries(f);
-        if (!first) sync_group();                          // the last fragment's sums and queries are free
+        if (pass > 0) sync_group();                        // the last fragment's sums and queries are free
 #pragma unroll 1
-        for (int s = 0; s < (first ? stages : 1); ++s) {
-            if (first) produce(s);
+        for (int s = 0; s < (pass == 0 ? stages : 1); ++s) {
+            if (pass == 0) produce(s);
             if (s == 0) place_queries();
         }
         sync_group();
