@@ -199,11 +199,13 @@ struct SplitArgs {
     float* part2_ml;               // [CTA + key][tile_rows][2]
     struct PlanEntry* plan2;       // [n_groups + 1]
 };
-// Work before an entry (cells x slices), keys before it (slices), its cells and
-// the first of them; entry E holds the totals.
+// Work before an entry ((cells + setup) x slices), keys before it (slices), its
+// cells, the first of them and its queries per KV head; entry E holds the totals.
+// Of a sequence (or one of its query rows): its length and the rows before `lo`
+// that are its group's.  Of a prefix group: its rows and first member.
 struct PlanEntry {
     long long work;
-    int keys, nc, c0, pad, hi, pad2;     // pad: queries; hi: rows of a prefix
+    int keys, nc, c0, nq, rows, lo;
 };
 int split_tile(bool bf16, int most_queries);
 int split_warps(int NB, int tile);

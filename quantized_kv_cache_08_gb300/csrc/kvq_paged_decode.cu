@@ -393,8 +393,8 @@ __device__ __noinline__ void fragment_at(Fragment& f, const PlanEntry* plan, int
     f.work = vb - va;
     f.ca = max(0, va - setup);
     f.cb = max(0, vb - setup);
-    f.nq = pe.pad;
-    f.nsl = (pe.pad + QPI - 1) / QPI;
+    f.nq = pe.nq;
+    f.nsl = (pe.nq + QPI - 1) / QPI;
     f.kh = f.kk / f.nsl;
     f.sl = f.kk - f.kh * f.nsl;
     f.c0 = pe.c0;
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             const int r = gwarp + i * gw, qi = f.sl * QPI + r;
             qq[i] = Query{0, 0, 0, 0, -1};
             const bool valid = r < QPI && qi < f.nq;
-            if (valid) qq[i] = query_of(a, f.e, f.kh, qi);
+            if (valid) qq[i] = query_of(a, plan[f.e], f.e, f.kh, qi);
             const long long at = (((long long)qq[i].seq * a.T + qq[i].t) * a.Hq + qq[i].h) * D + lane;
 #pragma unroll
             for (int b = 0; b < NB; ++b) qv[i][b] = valid ? load_q(a.q, at + 32 * b, a.bf16) : 0.f;
@@ -700,7 +700,9 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                     const int sl = (ew.nq + QPI - 1) / QPI;
                     plan[e].nc = ew.nc;
                     plan[e].c0 = ew.c0;
-                    plan[e].pad = ew.nq;
+                    plan[e].nq = ew.nq;
+                    plan[e].rows = ew.rows;
+                    plan[e].lo = ew.lo;
                     plan[e].work = w;
                     plan[e].keys = k;
                     w += ew.nc ? (long long)(ew.nc + a.setup) * sl : 0;
@@ -748,7 +750,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 if (!fits) atomicExch(a.g.err, kErrCounter);
                 plan[a.E].work = fits ? wb + w : 0;
                 plan[a.E].keys = kb + k;
-                plan[a.E].nc = plan[a.E].c0 = plan[a.E].pad = 0;
+                plan[a.E].nc = plan[a.E].c0 = plan[a.E].nq = plan[a.E].rows = plan[a.E].lo = 0;
             }
         }
         __syncthreads();
@@ -919,7 +921,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             for (int w = w0; w < w0 + gw; ++w) l = fmaf(s_l[w][row], ex2(s_m[w][row] - m), l);
             const float M = l > 0.f ? m - kShift : kNegInf;
             if (whole) {
-                const Query q = query_of(a, f.e, f.kh, f.sl * QPI + row);
+                const Query q = query_of(a, plan[f.e], f.e, f.kh, f.sl * QPI + row);
                 store4(a, (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + col, o, sink_weight(sink_of(a, q.h), M, l));
             } else {
                 const long long at = (range + key) * a.rec_rows + row;
@@ -951,7 +953,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                     float sink = kNegInf;
                     Sum4 s{kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
                     if (on) {
-                        q = query_of(a, f.e, f.kh, f.sl * QPI + row);
+                        q = query_of(a, plan[f.e], f.e, f.kh, f.sl * QPI + row);
                         sink = sink_of(a, q.h);
                         add_records<D>(a, s, rec0 + key, set, n_rec, sets, row, col);
                     }
@@ -1004,7 +1006,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Spli
     auto fold = [&](int e, int qi) {
         const PlanEntry pe = a.plan[e];
         if (pe.nc == 0 || W == 0) return;
-        const int nsl = (pe.pad + QPI - 1) / QPI;
+        const int nsl = (pe.nq + QPI - 1) / QPI;
         const int kk = kh * nsl + qi / QPI;
         const long long xa = pe.work * a.g.Hkv + (long long)kk * (pe.nc + a.setup) + a.setup;
         const int c0 = range_of(xa, G, W), c1 = range_of(xa + pe.nc - 1, G, W);
@@ -1021,7 +1023,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Spli
                 const long long W2 = a.plan2[a.n_groups].work * a.g.Hkv;
                 const PlanEntry pe = a.plan2[grp];
                 if (pe.nc != 0 && W2 != 0) {
-                    const int G2 = (int)min((long long)a.G, W2), nqb = (pe.pad + a.tile_rows - 1) / a.tile_rows;
+                    const int G2 = (int)min((long long)a.G, W2), nqb = (pe.nq + a.tile_rows - 1) / a.tile_rows;
                     const int kk = kh * nqb + qi / a.tile_rows;
                     const long long xa = pe.work * a.g.Hkv + (long long)kk * pe.nc;
                     const int c0 = range_of(xa, G2, W2), c1 = range_of(xa + pe.nc - 1, G2, W2);

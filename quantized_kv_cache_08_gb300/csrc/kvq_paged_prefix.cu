@@ -119,38 +119,48 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 
 // ------------------------------------------------------------ unpacking
 
-// One warp's raw bytes of a pair of cells: K or V, of up to four blocks
+// One warp's raw bytes of a pair of cells, K or V, of up to four blocks, in the
+// order in which they are used: the unpacking is a rolled loop that takes the
+// front words and shifts the rest down.  (Unrolled, the code of a tile is some
+// 20 KB, and fetching that for the first tile took 5 us.)
+//   K: for each block pair and cell, 8 words of codes (rows g, g + 8 of the cell)
+//      and 4 of scales;  V: for each block, 4 words of units (cell, half) and 8 of
+//      d, m, then 4 words of nibbles;  E4M3: 8 words of bytes each.
 template <int NBT, bool F8>
 struct Raw {
-    uint32_t w[F8 ? 8 * NBT : 13 * NBT];                      // the larger of K (8 words of codes, 4 of scales a block) and V (5, 8)
+    uint32_t w[F8 ? 8 * NBT : 12 * NBT], nib[4];
+    template <int N>
+    __device__ __forceinline__ void shift() {
+#pragma unroll
+        for (int i = 0; i + N < (F8 ? 8 * NBT : 12 * NBT); ++i) w[i] = w[i + N];
+    }
 };
 
 __device__ __forceinline__ uint4 ldg16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// bp0: first block pair of the task
+// b0: first block of the task
 template <int NB, int NBT, bool F8>
 __device__ __forceinline__ void load_k(const uint8_t* c0, const uint8_t* c1, int b0, int lane, Raw<NBT, F8>& r) {
+    constexpr int N = F8 ? 8 : 12;
     const int g = lane >> 2;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const uint8_t* cell = c ? c1 : c0;
+    for (int bp = 0; bp < NBT / 2; ++bp)
 #pragma unroll
-        for (int i = 0; i < NBT; ++i) {                       // i = 2 bp + t
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (cell) x = ldg16(cell + (b0 / 2 + (i >> 1)) * 1024 + (i & 1) * 512 + lane * 16);
-            uint32_t* w = r.w + (c * NBT + i) * 4;
-            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-        }
-        if constexpr (!F8) {
+        for (int c = 0; c < 2; ++c) {
+            const uint8_t* cell = c ? c1 : c0;
+            uint32_t* w = r.w + (2 * bp + c) * N;
 #pragma unroll
-            for (int b = 0; b < NBT; ++b) {
-                uint2 x = make_uint2(0u, 0u);
-                if (cell) x = *reinterpret_cast<const uint2*>(cell + 512 * NB + ((g >> 1) * NB + b0 + b) * 8);
-                r.w[8 * NBT + (c * NBT + b) * 2] = x.x;       // d of rows (g & ~1, + 1), then + 8
-                r.w[8 * NBT + (c * NBT + b) * 2 + 1] = x.y;
+            for (int t = 0; t < 2; ++t) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (cell) x = ldg16(cell + (b0 / 2 + bp) * 1024 + t * 512 + lane * 16);
+                w[4 * t] = x.x; w[4 * t + 1] = x.y; w[4 * t + 2] = x.z; w[4 * t + 3] = x.w;
+            }
+            if constexpr (!F8) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (cell) x = ldg16(cell + 512 * NB + ((g >> 1) * NB + b0 + 2 * bp) * 8);
+                w[8] = x.x; w[9] = x.y; w[10] = x.z; w[11] = x.w;   // d of rows (g & ~1, + 1), then + 8; two blocks
             }
         }
-    }
 }
 template <int NB, int NBT, bool F8>
 __device__ __forceinline__ void load_v(const uint8_t* c0, const uint8_t* c1, int b0, int lane, Raw<NBT, F8>& r) {
@@ -162,32 +172,38 @@ __device__ __forceinline__ void load_v(const uint8_t* c0, const uint8_t* c1, int
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < NBT / 2; ++i) {
+                for (int i = 0; i < NBT / 2; ++i) {           // blocks 2i, 2i + 1 of half h
                     uint4 x = make_uint4(0u, 0u, 0u, 0u);
                     if (cell) x = ldg16(cell + 512 * NB + ((h * NB + b0) / 2 + i) * 512 + lane * 16);
-                    uint32_t* w = r.w + ((c * 2 + h) * (NBT / 2) + i) * 4;   // blocks 2i, 2i + 1 of half h
-                    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                    uint32_t* w = r.w + 16 * i + 4 * c + 2 * h;
+                    w[0] = x.x; w[1] = x.y; w[8] = x.z; w[9] = x.w;
                 }
         } else {
-            // units (h NB + b): 4 a chunk.  NBT blocks of both halves: for NB 2 one
-            // chunk holds both, for NB >= 4 a chunk a half
+            // units (h NB + b), 4 a chunk: with two blocks one chunk holds both
+            // halves, else each half has its own
 #pragma unroll
-            for (int i = 0; i < NBT / 2; ++i) {
-                const int n = NB == 2 ? 0 : i * NB + b0;      // i is the half where NB >= 4
+            for (int h = 0; h < (NB == 2 ? 1 : 2); ++h) {
+                const int n = NB == 2 ? 0 : h * NB + b0;
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
                 uint32_t e = 0u;
                 if (cell) {
                     x = ldg16(cell + 544 * NB + (n / 4) * 512 + lane * 16);
                     e = *reinterpret_cast<const uint32_t*>(cell + 800 * NB + (n / 4) * 128 + lane * 4);
                 }
-                uint32_t* w = r.w + (c * (NBT / 2) + i) * 5;
-                w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w; w[4] = e;
+                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int b = NB == 2 ? (i & 1) : i, hh = NB == 2 ? (i >> 1) : h;
+                    r.w[12 * b + 2 * c + hh] = u[i];
+                }
+                r.nib[2 * c + h] = e;
+                if (NB == 2) r.nib[2 * c + 1] = e >> 8;
             }
 #pragma unroll
             for (int b = 0; b < NBT; ++b) {
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
                 if (cell) x = ldg16(cell + 864 * NB + (j * NB + b0 + b) * 16);
-                uint32_t* w = r.w + 5 * NBT + (c * NBT + b) * 4;
+                uint32_t* w = r.w + 12 * b + 4 + 4 * c;
                 w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
             }
         }
@@ -200,40 +216,40 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
 
 // K tile: rows of head_dim / 64 column blocks of 128 bytes; pr: the pair of cells
 template <int NB, int NBT, bool F8>
-__device__ __forceinline__ void store_k(uint32_t tile, int pr, int b0, int lane, const Raw<NBT, F8>& r) {
+__device__ __forceinline__ void store_k(uint32_t tile, int pr, int b0, int lane, Raw<NBT, F8>& r) {
     const int g = lane >> 2, j = lane & 3;
+    const uint32_t dsel = (g & 1) ? 0x3232u : 0x1010u;
+#pragma unroll 1
+    for (int it = 0; it < NBT; ++it) {                        // block pair it / 2, cell it % 2
+        const int row0 = 32 * pr + 8 * (g >> 1) + 4 * (it & 1) + (g & 1);
+        const uint32_t base = tile + (b0 / 2 + (it >> 1)) * (kTileRows * 128);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < NBT; ++i) {
-            const int bp = b0 / 2 + (i >> 1), t = i & 1;
-            const uint32_t* w = r.w + (c * NBT + i) * 4;
-            uint32_t o[8];
+        for (int t = 0; t < 2; ++t) {
+            const int row = row0 + 2 * t;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                const uint32_t x = r.w[4 * t + 2 * e], y = r.w[4 * t + 2 * e + 1];
+                uint32_t o[4];
                 if constexpr (F8) {
-                    o[4 * e] = f8_pair(w[2 * e]);
-                    o[4 * e + 1] = f8_pair(w[2 * e] >> 16);
-                    o[4 * e + 2] = f8_pair(w[2 * e + 1]);
-                    o[4 * e + 3] = f8_pair(w[2 * e + 1] >> 16);
+                    o[0] = f8_pair(x);
+                    o[1] = f8_pair(x >> 16);
+                    o[2] = f8_pair(y);
+                    o[3] = f8_pair(y >> 16);
                 } else {
-                    const uint32_t* ks = r.w + 8 * NBT + (c * NBT + (i >> 1) * 2 + e) * 2;
-                    const uint32_t dd = __byte_perm(ks[t], 0, (g & 1) ? 0x3232 : 0x1010);
-                    auto two = [&](uint32_t x, uint32_t sel) {
-                        const __half2 q = __hsub2(as_h2(__byte_perm(x, 0x44444444u, sel)), as_h2(0x44804480u));
-                        return as_u32(__hmul2(q, as_h2(dd)));
+                    const __half2 dd = as_h2(__byte_perm(r.w[8 + 2 * e + t], 0, dsel));
+                    auto two = [&](uint32_t v, uint32_t sel) {
+                        return as_u32(__hmul2(__hsub2(as_h2(__byte_perm(v, 0x44444444u, sel)), as_h2(0x44804480u)), dd));
                     };
-                    o[4 * e] = two(w[2 * e], 0x4140u);
-                    o[4 * e + 1] = two(w[2 * e], 0x4342u);
-                    o[4 * e + 2] = two(w[2 * e + 1], 0x4140u);
-                    o[4 * e + 3] = two(w[2 * e + 1], 0x4342u);
+                    o[0] = two(x, 0x4140u);
+                    o[1] = two(x, 0x4342u);
+                    o[2] = two(y, 0x4140u);
+                    o[3] = two(y, 0x4342u);
                 }
+                sts16(base + row * 128 + (((4 * e + j) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
             }
-            const int row = 32 * pr + 8 * (g >> 1) + 4 * c + 2 * t + (g & 1);
-            const uint32_t base = tile + bp * (kTileRows * 128) + row * 128;
-            sts16(base + ((j ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-            sts16(base + (((4 + j) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
         }
+        r.template shift<F8 ? 8 : 12>();
+    }
 }
 // V tile: rows are elements, columns the tile's rows, 64 a block of 128 bytes.
 // keep: half-word masks of the lane's rows (2j, 2j+1 | 2j+8, 2j+9) of both cells
@@ -243,43 +259,40 @@ __device__ __forceinline__ void store_v(uint32_t tile, int pr, int b0, int lane,
     const int g = lane >> 2, j = lane & 3;
     const uint32_t block = tile + (pr >> 1) * (D * 128);
     const int chunk = 4 * (pr & 1) + j;
-#pragma unroll
+#pragma unroll 1
     for (int b = 0; b < NBT; ++b) {
         uint32_t o[4][4];                                     // element r, (cell, half)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t k = keep[2 * c + h];
-                if constexpr (F8) {
-                    const uint32_t kb = __byte_perm(k, 0, 0x2020);
-                    const uint32_t* w = r.w + ((c * 2 + h) * (NBT / 2) + b / 2) * 4 + 2 * (b & 1);
-                    const uint32_t x = w[0] & kb, y = w[1] & kb;
-                    o[0][2 * c + h] = f8_pair(x);
-                    o[1][2 * c + h] = f8_pair(x >> 16);
-                    o[2][2 * c + h] = f8_pair(y);
-                    o[3][2 * c + h] = f8_pair(y >> 16);
-                } else {
-                    const uint32_t* q = NB == 2 ? r.w + c * (NBT / 2) * 5 : r.w + (c * (NBT / 2) + h) * 5;
-                    const int n4 = NB == 2 ? 2 * h + b : b;
-                    const uint32_t unit = q[n4], nib = q[4];
-                    const uint32_t* dm = r.w + 5 * NBT + (c * NBT + b) * 4;
-                    const __half2 d = as_h2(dm[h] & k), m = as_h2(dm[2 + h] & k);
-                    auto val = [&](auto R) {
-                        const __half2 u = __hsub2(as_h2(v_codes<decltype(R)::value>(unit, nib, n4, 0x64006400u)), as_h2(0x64006400u));
-                        return as_u32(__hfma2(u, d, m));
-                    };
-                    o[0][2 * c + h] = val(std::integral_constant<int, 0>{});
-                    o[1][2 * c + h] = val(std::integral_constant<int, 1>{});
-                    o[2][2 * c + h] = val(std::integral_constant<int, 2>{});
-                    o[3][2 * c + h] = val(std::integral_constant<int, 3>{});
-                }
+        for (int ch = 0; ch < 4; ++ch) {
+            const uint32_t k = keep[ch];
+            if constexpr (F8) {
+                const uint32_t kb = __byte_perm(k, 0, 0x2020);
+                const uint32_t x = r.w[2 * ch] & kb, y = r.w[2 * ch + 1] & kb;
+                o[0][ch] = f8_pair(x);
+                o[1][ch] = f8_pair(x >> 16);
+                o[2][ch] = f8_pair(y);
+                o[3][ch] = f8_pair(y >> 16);
+            } else {
+                const uint32_t unit = r.w[ch], nib = r.nib[ch];
+                const uint32_t* dm = r.w + 4 + 4 * (ch >> 1);
+                const __half2 d = as_h2(dm[ch & 1] & k), m = as_h2(dm[2 + (ch & 1)] & k);
+                auto val = [&](auto R) {
+                    const __half2 u = __hsub2(as_h2(v_codes<decltype(R)::value>(unit, nib, 0, 0x64006400u)), as_h2(0x64006400u));
+                    return as_u32(__hfma2(u, d, m));
+                };
+                o[0][ch] = val(std::integral_constant<int, 0>{});
+                o[1][ch] = val(std::integral_constant<int, 1>{});
+                o[2][ch] = val(std::integral_constant<int, 2>{});
+                o[3][ch] = val(std::integral_constant<int, 3>{});
+                r.nib[ch] = nib >> 4;
             }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 32 * (b0 + b) + 4 * g + i;
             sts16(block + row * 128 + ((chunk ^ (row & 7)) << 4), o[i][0], o[i][1], o[i][2], o[i][3]);
         }
+        r.template shift<F8 ? 8 : 12>();
     }
 }
 
@@ -300,7 +313,7 @@ __device__ __forceinline__ uint32_t seen_places(int lo, int hi, int there) {
 
 // A CTA's part of a key: group, KV head, query block qb, tiles [ta, tb)
 struct Part {
-    int grp, kh, qb, nqb, nq, gs, t0, ta, tb, kk, keys, hi;
+    int kh, qb, nqb, nq, gs, t0, ta, tb, kk, keys, hi;     // gs: first member; hi: rows of the prefix that are seen
 };
 
 template <int NB, bool F8>
@@ -352,8 +365,9 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
             if (tile_group(a, nq) && hi > lo) {
                 pe.c0 = lo / kTileRows;
                 pe.nc = (hi + kTileRows - 1) / kTileRows - pe.c0;
-                pe.pad = nq;
-                pe.hi = hi;
+                pe.nq = nq;
+                pe.rows = hi;
+                pe.lo = gs;
             }
             plan[grp] = pe;
         }
@@ -364,7 +378,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
         int k = 0;
         for (int g0 = 0; g0 < a.n_groups; g0 += 32) {
             const int grp = g0 + lane;
-            const int nqb = grp < a.n_groups ? (plan[grp].pad + QB - 1) / QB : 0;
+            const int nqb = grp < a.n_groups ? (plan[grp].nq + QB - 1) / QB : 0;
             const long long own = grp < a.n_groups ? (long long)plan[grp].nc * nqb : 0;
             long long wi = own;
             int ki = nqb;
@@ -413,20 +427,19 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
     auto wait = [&](uint64_t& bar, uint32_t parity) { return wait_bounded(dev::smem_u32(&bar), parity, abort_flag, a.g.err); };
     auto part_at = [&](long long x) {
         Part p;
-        p.grp = find_entry(plan, a.n_groups, x / a.g.Hkv);       // (entries without work are passed over: none starts behind x)
-        const PlanEntry pe = plan[p.grp];
+        const PlanEntry pe = plan[find_entry(plan, a.n_groups, x / a.g.Hkv)];
         const long long rel = x - pe.work * a.g.Hkv;
         p.kk = (int)(rel / pe.nc);
         p.ta = (int)(rel - (long long)p.kk * pe.nc);
         p.tb = (int)min((long long)pe.nc, p.ta + (x1 - x));
-        p.nq = pe.pad;
+        p.nq = pe.nq;
         p.nqb = (p.nq + QB - 1) / QB;
         p.kh = p.kk / p.nqb;
         p.qb = p.kk - p.kh * p.nqb;
         p.t0 = pe.c0;
         p.keys = pe.keys;
-        p.gs = a.group_start[p.grp];
-        p.hi = pe.hi;
+        p.gs = pe.lo;
+        p.hi = pe.rows;
         return p;
     };
     const long long xs = W * blockIdx.x / G;
@@ -448,9 +461,10 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
             int lo = 0, hi = 0x7fffffff;
             {
                 // the query, scaled by a power of two to a largest element in [512, 1024), as fp16
-                const Query q = valid ? query_of(a, a.n_seq + p.grp, p.kh, qi) : Query{0, 0, 0, 0, 0};
-                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
-                                                                  (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D);
+                const int Qh = a.hpk * a.T, seq = p.gs + (valid ? qi / Qh : 0), in = valid ? qi % Qh : 0, tq = in / a.hpk;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    reinterpret_cast<const uint16_t*>(a.q) + (((long long)seq * a.T + tq) * a.Hq + p.kh * a.hpk + in - tq * a.hpk) * D);
+                const int len = a.lens[seq];
                 constexpr int PER = 8;                         // 16-byte pieces in registers at once
                 uint4 v[PER];
                 auto load = [&](int i0) {
@@ -470,8 +484,9 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                     }
                 }
                 if (valid) {
-                    lo = q.lo;
-                    hi = q.hi;
+                    const int end = (len_ok(a, len) ? len : 0) - a.T + tq + 1;
+                    hi = min(end, p.hi);
+                    lo = a.window > 0 ? max(0, end - a.window) : 0;
                 }
                 const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -109), 110) : 0;
                 const float up = __uint_as_float((uint32_t)(127 - ex) << 23);

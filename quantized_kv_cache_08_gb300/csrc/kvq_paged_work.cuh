@@ -79,10 +79,11 @@ __device__ __forceinline__ bool tile_group(const SplitArgs& a, int nq) { return 
 
 struct EntryWork {
     int nc, c0, nq;
+    int rows, lo;                  // as in PlanEntry
 };
 
 __device__ __forceinline__ EntryWork entry_work(const SplitArgs& a, int e, bool report) {
-    EntryWork w{0, 0, 0};
+    EntryWork w{0, 0, 0, 0, 0};
     int lo = 0, hi = 0;
     if (a.lists) {
         const int seq = e / a.T, t = e - seq * a.T;
@@ -92,6 +93,7 @@ __device__ __forceinline__ EntryWork entry_work(const SplitArgs& a, int e, bool 
             return w;
         }
         w.nq = a.hpk;
+        w.rows = len;
         if (len - a.T + t >= 0) w.nc = a.keep * a.g.cells_per_page();
         return w;
     }
@@ -105,7 +107,9 @@ __device__ __forceinline__ EntryWork entry_work(const SplitArgs& a, int e, bool 
         hi = len;
         lo = a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;
         const int grp = group_of(a, e);
-        if (grp >= 0) lo = max(lo, prefix_rows(a, grp));
+        w.rows = len;
+        if (grp >= 0) w.lo = prefix_rows(a, grp);
+        lo = max(lo, w.lo);
     } else {
         const int grp = e - a.n_seq;
         int gs, ge;
@@ -114,9 +118,11 @@ __device__ __forceinline__ EntryWork entry_work(const SplitArgs& a, int e, bool 
                        a.group_start[grp + 1] > a.n_seq || !len_ok(a, a.prefix_len[grp])))
             atomicExch(a.g.err, kErrCounter);
         w.nq = (ge - gs) * a.hpk * a.T;
-        if (tile_group(a, w.nq)) return EntryWork{0, 0, 0};
+        if (tile_group(a, w.nq)) return EntryWork{0, 0, 0, 0, 0};
         hi = prefix_rows(a, grp);
         lo = 0;
+        w.rows = hi;
+        w.lo = gs;
         if (a.window > 0) {                       // rows before every member's window are not read
             lo = hi;
             for (int m = gs; m < ge; ++m) lo = min(lo, max(0, a.lens[m] - a.T + 1 - a.window));
@@ -135,34 +141,29 @@ __device__ __forceinline__ EntryWork entry_work(const SplitArgs& a, int e, bool 
 struct Query {
     int seq, t, h, lo, hi;
 };
-__device__ __forceinline__ Query query_of(const SplitArgs& a, int e, int g, int qi) {
+__device__ __forceinline__ Query query_of(const SplitArgs& a, const PlanEntry& pe, int e, int g, int qi) {
     Query q;
-    int within = qi;
-    const int Qh = a.hpk * a.T;
+    int within = qi, len = pe.rows;
     if (a.lists) {
         q.seq = e / a.T;
         q.t = e - q.seq * a.T;
     } else {
         q.seq = e;
         if (e >= a.n_seq) {
-            const int m = qi / Qh;
-            q.seq = a.group_start[e - a.n_seq] + m;
+            const int Qh = a.hpk * a.T, m = qi / Qh;
+            q.seq = pe.lo + m;
             within = qi - m * Qh;
+            len = a.lens[q.seq];
+            if (!len_ok(a, len)) len = 0;
         }
         q.t = within / a.hpk;
         within -= q.t * a.hpk;
     }
     q.h = g * a.hpk + within;
-    const int len = a.lens[q.seq];
-    q.hi = len_ok(a, len) ? len - a.T + q.t + 1 : 0;
+    q.hi = len - a.T + q.t + 1;
     q.lo = a.window > 0 ? max(0, q.hi - a.window) : 0;
-    if (!a.lists) {
-        if (e >= a.n_seq) q.hi = min(q.hi, prefix_rows(a, e - a.n_seq));
-        else if (a.n_groups) {
-            const int grp = group_of(a, e);
-            if (grp >= 0) q.lo = max(q.lo, prefix_rows(a, grp));
-        }
-    }
+    if (e >= a.n_seq && !a.lists) q.hi = min(q.hi, pe.rows);
+    else q.lo = max(q.lo, pe.lo);
     return q;
 }
 
