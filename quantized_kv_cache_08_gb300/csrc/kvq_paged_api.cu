@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kMaxGrid = 256;          // most CTAs of a split kernel
 constexpr int kMaxRanges = 4 * kMaxGrid;
-constexpr int kManyKeys = 32;
+constexpr int kManyKeys = 32;          // of 16, 32, 100 and 200, best or near it for each of the measured shapes
 constexpr int kMaxT = 64;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

@@ -6,10 +6,10 @@
 // positive and negative parts give it exactly; the two scales and the sum over
 // blocks are single f32 operations in a fixed order.  Scores are therefore the
 // same numbers on every run, and ties (common between codes) go to the lowest
-// index.  One kernel: a CTA scores 256 pages of a KV head (NB lanes a page, the
-// query codes of four queries in registers), and the last CTA of an (entry, KV
+// index.  One kernel: a CTA scores 256 pages of a KV head (NB lanes a page), and the last CTA of an (entry, KV
 // head) picks: a radix search for the threshold over the bits in which the scores
-// differ, eight a pass, then a compaction in index order.
+// differ, eight a pass, until the few that share its digits can be ranked one a
+// thread, then a compaction in index order.
 #include "kvq_paged.cuh"
 
 #include <cuda_bf16.h>
@@ -24,6 +24,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPages = 256;            // pages of a CTA
 constexpr int kKeep = 8192;            // keys that the pick holds in shared memory
+constexpr int kBlock = 20;             // words of a query block's codes and scale
 
 // number of pages with a row that query row t sees, -1 for a bad length
 __device__ __forceinline__ int page_count(const SelectArgs& a, int seq, int t, bool report) {
@@ -48,8 +49,8 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
     __shared__ int s_hist[256];
     __shared__ int s_gt[kWarps], s_eq[kWarps];
     __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
-    __shared__ uint32_t s_digit;
-    __shared__ int s_need;
+    __shared__ uint32_t s_digit, s_thr, s_key[kThreads];
+    __shared__ int s_need, s_in, s_count, s_cut, s_idx[kThreads];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool in_smem = np <= kKeep;
     const int first = a.n_first, last = np - a.n_last;      // pages [first, last) compete
@@ -77,6 +78,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
     int need = a.keep - a.n_first - a.n_last;               // of the competing pages
     uint32_t prefix = 0;
     int bits = hi > lo ? 32 - __clz(hi - lo) : 0;           // in which the keys differ
+    int cut = np;                                           // of the keys that equal the threshold, those below this index
     while (bits > 0 && need > 0) {
         const int shift = max(0, bits - 8);
         s_hist[tid] = 0;
@@ -112,12 +114,47 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
                     }
                 s_digit = (uint32_t)(255 - 8 * lane - i);
                 s_need = need - before;
+                s_in = c[0];
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    if (i == k) s_in = c[k];
             }
         }
         __syncthreads();
         prefix |= s_digit << shift;
         need = s_need;
         bits = shift;
+        if (s_in <= kThreads && bits > 0) {
+            // few keys share the digits: each thread ranks one of them
+            if (tid == 0) s_count = 0;
+            __syncthreads();
+            const uint32_t m = 0xffffffffu << bits;
+            for (int i = first + tid; i < last; i += kThreads) {
+                const uint32_t k = key(i);
+                if ((k & m) == prefix) {
+                    const int at = atomicAdd(&s_count, 1);
+                    s_key[at] = k;
+                    s_idx[at] = i;
+                }
+            }
+            __syncthreads();
+            const int n = s_count;
+            if (tid < n) {
+                const uint32_t k = s_key[tid];
+                const int i = s_idx[tid];
+                int rank = 0;
+                for (int o = 0; o < n; ++o) rank += s_key[o] > k || (s_key[o] == k && s_idx[o] < i);
+                if (rank == need - 1) {                     // the last that is taken
+                    s_thr = k;
+                    s_cut = i + 1;
+                }
+            }
+            __syncthreads();
+            prefix = s_thr;
+            cut = s_cut;
+            need = np;                                      // (the index decides among equals)
+            break;
+        }
     }
     // competing keys above the threshold and the first `need` that equal it, in
     // index order: each warp counts its share of the pages, then writes it
@@ -129,7 +166,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
         const bool in = i < b1, forced = in && (i < first || i >= last);
         const uint32_t k = in ? key(i) : 0u;
         gt += __popc(__ballot_sync(0xffffffffu, forced || (in && !none && k > prefix)));
-        eq += __popc(__ballot_sync(0xffffffffu, in && !forced && !none && k == prefix));
+        eq += __popc(__ballot_sync(0xffffffffu, in && !forced && !none && k == prefix && i < cut));
     }
     if (lane == 0) {
         s_gt[warp] = gt;
@@ -146,7 +183,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
         const int i = base + lane;
         const bool in = i < b1, forced = in && (i < first || i >= last);
         const uint32_t k = in ? key(i) : 0u;
-        const bool up = forced || (in && !none && k > prefix), same = in && !forced && !none && k == prefix;
+        const bool up = forced || (in && !none && k > prefix), same = in && !forced && !none && k == prefix && i < cut;
         const unsigned mg = __ballot_sync(0xffffffffu, up), me = __ballot_sync(0xffffffffu, same);
         const int rank = e0 + __popc(me & below);           // equal keys before this one
         if (up || (same && rank < need)) out[at + __popc(mg & below) + min(rank, need)] = i;
@@ -162,10 +199,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     constexpr int D = NB * 32;
     constexpr int PW = 32 / NB;                        // pages a warp takes at once
     constexpr int IT = kPages / (kWarps * PW);         // times it does
-    extern __shared__ __align__(16) uint32_t s_dyn[];  // query codes [hpk][NB][8 words positive, 8 negative], dq [hpk][NB]; then the pick's keys
+    // query codes [hpk][NB] of 8 words positive, 8 negative and dq; blocks kBlock
+    // words apart, so that lanes of different blocks read different banks; then the
+    // pick's keys
+    extern __shared__ __align__(16) uint32_t s_dyn[];
     __shared__ int s_last;
     uint32_t* s_q = s_dyn;
-    float* s_dq = reinterpret_cast<float*>(s_q + (size_t)a.hpk * NB * 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int e = blockIdx.z, kh = blockIdx.y;
     const int seq = e / a.T, t = e - seq * a.T;
@@ -201,65 +240,50 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
         const float am = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(x))));
         const float inv = am > 0.f ? __fmul_rn(__frcp_rn(am), 127.f) : 0.f;
         const int c = (int)rintf(__fmul_rn(x, inv));
-        int8_t* dst = reinterpret_cast<int8_t*>(s_q + (size_t)i * 16);
+        int8_t* dst = reinterpret_cast<int8_t*>(s_q + (size_t)i * kBlock);
         dst[lane] = (int8_t)max(min(c, 127), 0);
         dst[32 + lane] = (int8_t)min(max(c, -127), 0);
-        if (lane == 0) s_dq[i] = __fmul_rn(am, 1.0f / 127.0f);
+        if (lane == 0) s_q[(size_t)i * kBlock + 16] = __float_as_uint(__fmul_rn(am, 1.0f / 127.0f));
     }
     __syncthreads();
     uint32_t* keys = a.keys + ((long long)e * a.g.Hkv + kh) * a.g.max_pages;
-    float best[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) best[i] = -__builtin_huge_valf();
-    for (int q0 = 0; q0 < a.hpk; q0 += 4) {            // four queries' codes in registers
-        uint32_t qp[4][8], qn[4][8];
-        float dq[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int q = min(q0 + j, a.hpk - 1);      // (a repeated query changes no maximum)
-            const uint4* w = reinterpret_cast<const uint4*>(s_q + ((size_t)q * NB + b) * 16);
-            const uint4 w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3];
-            qp[j][0] = w0.x; qp[j][1] = w0.y; qp[j][2] = w0.z; qp[j][3] = w0.w;
-            qp[j][4] = w1.x; qp[j][5] = w1.y; qp[j][6] = w1.z; qp[j][7] = w1.w;
-            qn[j][0] = w2.x; qn[j][1] = w2.y; qn[j][2] = w2.z; qn[j][3] = w2.w;
-            qn[j][4] = w3.x; qn[j][5] = w3.y; qn[j][6] = w3.z; qn[j][7] = w3.w;
-            dq[j] = s_dq[q * NB + b];
-        }
 #pragma unroll 2
-        for (int i = 0; i < IT; ++i) {
-            uint32_t mn[8] = {}, mx[8] = {};
-            float ds = 0.f;
-            if (pg[i] >= 0 && pg[i] < a.g.n_pages) {
-                const long long at = ((long long)pg[i] * a.g.Hkv + kh) * NB + b;
-                const uint4* src = reinterpret_cast<const uint4*>(a.codes + at * 64);
-                const uint4 v0 = src[0], v1 = src[1], v2 = src[2], v3 = src[3];
-                mn[0] = v0.x; mn[1] = v0.y; mn[2] = v0.z; mn[3] = v0.w; mn[4] = v1.x; mn[5] = v1.y; mn[6] = v1.z; mn[7] = v1.w;
-                mx[0] = v2.x; mx[1] = v2.y; mx[2] = v2.z; mx[3] = v2.w; mx[4] = v3.x; mx[5] = v3.y; mx[6] = v3.z; mx[7] = v3.w;
-                ds = a.scales[at];
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                int dot = 0;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    dot = __dp4a((int)qp[j][k], (int)mx[k], dot);
-                    dot = __dp4a((int)qn[j][k], (int)mn[k], dot);
-                }
-                const float part = __fmul_rn(__fmul_rn(dq[j], ds), (float)dot);
-                float s = 0.f;
-#pragma unroll
-                for (int k = 0; k < NB; ++k) s = __fadd_rn(s, __shfl_sync(0xffffffffu, part, pl * NB + k));
-                best[i] = fmaxf(best[i], s);
-            }
-        }
-    }
-#pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int p = p0 + (i * kWarps + warp) * PW + pl;
-        if (p >= pe || b != 0) continue;
         const bool ok = pg[i] >= 0 && pg[i] < a.g.n_pages;
-        if (!ok) atomicExch(a.g.err, kErrCounter);
-        keys[p] = ok ? ordered(best[i]) : 0u;
+        uint32_t mn[8] = {}, mx[8] = {};
+        float ds = 0.f;
+        if (ok) {
+            const long long at = ((long long)pg[i] * a.g.Hkv + kh) * NB + b;
+            const uint4* src = reinterpret_cast<const uint4*>(a.codes + at * 64);
+            const uint4 v0 = src[0], v1 = src[1], v2 = src[2], v3 = src[3];
+            mn[0] = v0.x; mn[1] = v0.y; mn[2] = v0.z; mn[3] = v0.w; mn[4] = v1.x; mn[5] = v1.y; mn[6] = v1.z; mn[7] = v1.w;
+            mx[0] = v2.x; mx[1] = v2.y; mx[2] = v2.z; mx[3] = v2.w; mx[4] = v3.x; mx[5] = v3.y; mx[6] = v3.z; mx[7] = v3.w;
+            ds = a.scales[at];
+        }
+        float best = -__builtin_huge_valf();
+        for (int q = 0; q < a.hpk; ++q) {
+            const uint32_t* w = s_q + ((size_t)q * NB + b) * kBlock;
+            const uint4 w0 = *reinterpret_cast<const uint4*>(w), w1 = *reinterpret_cast<const uint4*>(w + 4);
+            const uint4 w2 = *reinterpret_cast<const uint4*>(w + 8), w3 = *reinterpret_cast<const uint4*>(w + 12);
+            const uint32_t qp[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            const uint32_t qn[8] = {w2.x, w2.y, w2.z, w2.w, w3.x, w3.y, w3.z, w3.w};
+            int d0 = 0, d1 = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                d0 = __dp4a((int)qp[k], (int)mx[k], d0);
+                d1 = __dp4a((int)qn[k], (int)mn[k], d1);
+            }
+            const float part = __fmul_rn(__fmul_rn(__uint_as_float(w[16]), ds), (float)(d0 + d1));
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) s = __fadd_rn(s, __shfl_sync(0xffffffffu, part, pl * NB + k));
+            best = fmaxf(best, s);
+        }
+        if (p < pe && b == 0) {
+            if (!ok) atomicExch(a.g.err, kErrCounter);
+            keys[p] = ok ? ordered(best) : 0u;
+        }
     }
     // the last CTA of the (entry, KV head) picks
     __threadfence();
@@ -282,7 +306,7 @@ static cudaError_t launch_t(const SelectArgs& a, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = kernel_attrs_once(select_kernel<NB>, done, false);
     if (e != cudaSuccess) return e;
-    const size_t codes = (size_t)a.hpk * NB * (16 * 4 + 4), keys = (size_t)std::min(a.g.max_pages, kKeep) * 4;
+    const size_t codes = (size_t)a.hpk * NB * kBlock * 4, keys = (size_t)std::min(a.g.max_pages, kKeep) * 4;
     const dim3 grid((unsigned)((a.g.max_pages + kPages - 1) / kPages), (unsigned)a.g.Hkv, (unsigned)(a.n_seq * a.T));
     return launch_dependent(select_kernel<NB>, grid, kThreads, std::max(codes, keys), s, a);
 }
