@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 
 // The `keep` pages of one (entry, KV head) of np > keep: the first n_first, the
 // last n_last and the best keys of the others, ties to the lowest index.
-__device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, uint32_t* s_keys, int np, int* out) {
+__device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* g_keys, uint32_t* s_keys, int np, int* out) {
     __shared__ int s_hist[256];
     __shared__ int s_gt[kWarps], s_eq[kWarps];
     __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
@@ -55,6 +55,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
     const bool in_smem = np <= kKeep;
     const int first = a.n_first, last = np - a.n_last;      // pages [first, last) compete
     uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll 4
     for (int i = tid; i < np; i += kThreads) {
         const uint32_t k = __ldcg(g_keys + i);
         if (in_smem) s_keys[i] = k;
@@ -74,7 +75,8 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
         lo = min(lo, s_lo[w]);
         hi = max(hi, s_hi[w]);
     }
-    auto key = [&](int i) { return (in_smem ? s_keys[i] : __ldcg(g_keys + i)) - lo; };
+    const uint32_t* keys = in_smem ? s_keys : g_keys;       // (written before the fence that the caller passed)
+    auto key = [&](int i) { return keys[i] - lo; };
     int need = a.keep - a.n_first - a.n_last;               // of the competing pages
     uint32_t prefix = 0;
     int bits = hi > lo ? 32 - __clz(hi - lo) : 0;           // in which the keys differ
@@ -84,6 +86,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
         s_hist[tid] = 0;
         __syncthreads();
         const uint32_t mask = bits >= 32 ? 0u : 0xffffffffu << bits;
+#pragma unroll 4
         for (int i = first + tid; i < last; i += kThreads) {
             const uint32_t k = key(i);
             if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << (bits - shift)) - 1u)], 1);
@@ -129,6 +132,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
             if (tid == 0) s_count = 0;
             __syncthreads();
             const uint32_t m = 0xffffffffu << bits;
+#pragma unroll 4
             for (int i = first + tid; i < last; i += kThreads) {
                 const uint32_t k = key(i);
                 if ((k & m) == prefix) {
@@ -143,6 +147,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
                 const uint32_t k = s_key[tid];
                 const int i = s_idx[tid];
                 int rank = 0;
+#pragma unroll 8
                 for (int o = 0; o < n; ++o) rank += s_key[o] > k || (s_key[o] == k && s_idx[o] < i);
                 if (rank == need - 1) {                     // the last that is taken
                     s_thr = k;
@@ -161,6 +166,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
     const int per = ((np + kWarps - 1) / kWarps + 31) & ~31, b0 = warp * per, b1 = min(np, b0 + per);
     const bool none = a.keep == a.n_first + a.n_last;
     int gt = 0, eq = 0;
+#pragma unroll 4
     for (int base = b0; base < b1; base += 32) {
         const int i = base + lane;
         const bool in = i < b1, forced = in && (i < first || i >= last);
@@ -179,6 +185,7 @@ __device__ void pick(const SelectArgs& a, const uint32_t* __restrict__ g_keys, u
         e0 += s_eq[w];
     }
     const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int base = b0; base < b1; base += 32) {
         const int i = base + lane;
         const bool in = i < b1, forced = in && (i < first || i >= last);
