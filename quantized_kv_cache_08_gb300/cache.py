@@ -6,6 +6,8 @@ stream; every operation is one call through the C ABI (see _binding).
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _binding as B
@@ -179,6 +181,7 @@ def _token_rows(t, heads, dim, name):
     return t.data_ptr(), stride
 
 
+_I32 = torch.int32
 _DTYPE = {torch.float32: B.KVQ_F32, torch.bfloat16: B.KVQ_BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     lambda index: torch.cuda.current_stream(index).cuda_stream
@@ -202,6 +205,7 @@ class PagedKVCache:
                  fmt="q8_0/q5_1", rope_dim=0, rope_base=10000.0, rope_interleaved=False, rope_freq=None, bounds=False,
                  pool=None, bounds_buf=None, device=None, stream=None):
         self.handle = None
+        self._lib = B.lib()
         if fmt not in KVCache.FORMATS:
             raise ValueError(f"fmt must be one of {sorted(KVCache.FORMATS)}")
         k_fmt, v_fmt, _, _ = KVCache.FORMATS[fmt]
@@ -251,7 +255,12 @@ class PagedKVCache:
 
     def _batch(self, tables, lens):
         n = lens.shape[0] if lens.dim() == 1 else -1
-        return n, self._ints(tables, (n, self.max_pages), "tables"), self._ints(lens, (n,), "lens")
+        if tables.dtype is not _I32 or lens.dtype is not _I32 or tables.shape != (n, self.max_pages) \
+                or tables.get_device() != self.index or lens.get_device() != self.index \
+                or not tables.is_contiguous() or not lens.is_contiguous():
+            self._ints(tables, (n, self.max_pages), "tables")
+            self._bad_ints(lens, (n,), "lens")
+        return n, tables.data_ptr(), lens.data_ptr()
 
     def _dense(self, t, name):
         if t.get_device() != self.index or not t.is_contiguous():
@@ -268,24 +277,18 @@ class PagedKVCache:
             raise ValueError(f"{name} must be [rows, heads, dim] with starts")
         return 0, self._ints(starts, (n + 1,), "starts"), t.shape[0]
 
-    def _strided(self, t, heads, name):
-        """Address and row stride (elements) of rows that lie evenly apart."""
-        if t.get_device() != self.index:
-            raise ValueError(f"{name} must be on {self.device}")
-        if t.is_contiguous():
-            return t.data_ptr(), heads * self.head_dim
-        return _token_rows(t, heads, self.head_dim, name)
-
     def _stream(self, stream):
         return _raw_stream(self.index) if stream is None else stream.cuda_stream
 
     def _call(self, fn, *args):
-        """A call of the binding with the cache's device current."""
+        """A call of the library with the cache's device current."""
         if _current_device() == self.index:
-            fn(self.handle, *args)
+            st = fn(self.handle, *args)
         else:
             with torch.cuda.device(self.index):
-                fn(self.handle, *args)
+                st = fn(self.handle, *args)
+        if st:
+            B._check(st)
 
     def _new(self, shape, dtype, stream):
         out = torch.empty(shape, dtype=dtype, device=self.device)
@@ -298,49 +301,54 @@ class PagedKVCache:
         starts (int32 [n + 1]).  q (same form, any number of heads) is rotated
         into q_out (made if None; q itself when dense), which is returned."""
         n, tp, lp = self._batch(tables, lens)
-        shape, code = k.shape, _DTYPE.get(k.dtype)
-        if v.shape != shape or v.dtype is not k.dtype or code is None:
-            raise ValueError("k and v must have one shape and one dtype, float32 or bfloat16")
-        if shape[-2:] != (self.n_kv_heads, self.head_dim):
-            raise ValueError(f"k shape {tuple(shape)} does not match the cache")
+        shape, dtype, hkv, dim, index = k.shape, k.dtype, self.n_kv_heads, self.head_dim, self.index
+        code = _DTYPE.get(dtype)
+        if code is None or v.dtype is not dtype or v.shape != shape or shape[-1] != dim or shape[-2] != hkv:
+            raise ValueError(f"k {dtype} {tuple(shape)} and v {v.dtype} {tuple(v.shape)} must be float32 or bfloat16 "
+                             "rows of the cache's heads, alike")
+        if k.get_device() != index or v.get_device() != index:
+            raise ValueError(f"k and v must be on {self.device}")
         T, sp, rows = self._rows(k, n, starts, "k")
-        kp, ks = self._strided(k, self.n_kv_heads, "k")
-        vp, vs = self._strided(v, self.n_kv_heads, "v")
+        kp, ks = (k.data_ptr(), hkv * dim) if k.is_contiguous() else _token_rows(k, hkv, dim, "k")
+        vp, vs = (v.data_ptr(), hkv * dim) if v.is_contiguous() else _token_rows(v, hkv, dim, "v")
         qp, qs, op, hq = None, 0, None, 0
         if q is not None:
-            hq = q.shape[-2]
-            if q.dtype is not k.dtype or q.shape[:-2] != shape[:-2] or q.shape[-1] != self.head_dim:
-                raise ValueError("q must have k's rows, head_dim and dtype")
-            qp, qs = self._strided(q, hq, "q")
+            qshape = q.shape
+            hq = qshape[-2]
+            if q.dtype is not dtype or qshape[-1] != dim or qshape[:-2] != shape[:-2] or q.get_device() != index:
+                raise ValueError("q must have k's rows, head_dim, dtype and device")
+            qp, qs = (q.data_ptr(), hq * dim) if q.is_contiguous() else _token_rows(q, hq, dim, "q")
             if q_out is None:
-                q_out = self._new(q.shape, q.dtype, stream)
-            elif q_out.dtype is not q.dtype or q_out.shape != q.shape:
+                q_out = self._new(qshape, dtype, stream)
+            elif q_out.dtype is not dtype or q_out.shape != qshape:
                 raise ValueError("q_out must have q's shape and dtype")
             op = self._dense(q_out, "q_out")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        self._call(B.kvq_paged_append, kp, ks, vp, vs, qp, qs, op, hq, code, tp, lp, n, T, sp, rows,
-                   self._stream(stream))
+        self._call(self._lib.kvq_paged_append, kp, ks, vp, vs, qp, qs, op, hq, code, tp, lp, n, T, sp, rows,
+                   _raw_stream(index) if stream is None else stream.cuda_stream)
         return q_out
 
     def read(self, tables, lens, k_out, v_out, starts=None, stream=None):
         """Each entry's last rows as values into k_out, v_out: float32/bfloat16
         [n, T, Hkv, D], or packed [rows, Hkv, D] with starts."""
         n, tp, lp = self._batch(tables, lens)
-        code = _DTYPE.get(k_out.dtype)
-        if v_out.shape != k_out.shape or v_out.dtype is not k_out.dtype or code is None:
-            raise ValueError("k_out and v_out must have one shape and one dtype, float32 or bfloat16")
-        if k_out.shape[-2:] != (self.n_kv_heads, self.head_dim):
-            raise ValueError(f"k_out shape {tuple(k_out.shape)} does not match the cache")
+        shape, code, index = k_out.shape, _DTYPE.get(k_out.dtype), self.index
+        if code is None or v_out.dtype is not k_out.dtype or v_out.shape != shape or shape[-1] != self.head_dim \
+                or shape[-2] != self.n_kv_heads:
+            raise ValueError("k_out and v_out must be float32 or bfloat16 rows of the cache's heads, alike")
+        if k_out.get_device() != index or v_out.get_device() != index or not k_out.is_contiguous() \
+                or not v_out.is_contiguous():
+            raise ValueError(f"k_out and v_out must be contiguous tensors on {self.device}")
         T, sp, rows = self._rows(k_out, n, starts, "k_out")
-        self._call(B.kvq_paged_read, self._dense(k_out, "k_out"), self._dense(v_out, "v_out"), code, tp, lp, n, T, sp,
-                   rows, self._stream(stream))
+        self._call(self._lib.kvq_paged_read, k_out.data_ptr(), v_out.data_ptr(), code, tp, lp, n, T, sp, rows,
+                   _raw_stream(index) if stream is None else stream.cuda_stream)
 
     def update_bounds(self, tables, lens, T, stream=None):
         """Renew the key bounds of the pages that hold each sequence's last T
         rows (appends do this; for pages filled in another way)."""
         n, tp, lp = self._batch(tables, lens)
-        self._call(B.kvq_paged_bounds, tp, lp, n, T, None, n * T, self._stream(stream))
+        self._call(self._lib.kvq_paged_bounds, tp, lp, n, T, None, n * T, self._stream(stream))
 
     def _query(self, q, tables, lens, sinks, scale, window, softcap, out, stream):
         n, tp, lp = self._batch(tables, lens)
@@ -362,13 +370,13 @@ class PagedKVCache:
             if sinks.dtype is not torch.float32 or sinks.numel() != shape[2]:
                 raise ValueError("sinks must be float32 [Hq]")
             sk = self._dense(sinks, "sinks")
-        return out, B.kvq_paged_query(qp, op, code, n, shape[1], shape[2], tp, lp, sk, scale, softcap, window)
+        return out, ctypes.byref(B.kvq_paged_query(qp, op, code, n, shape[1], shape[2], tp, lp, sk, scale, softcap, window))
 
     def decode(self, q, tables, lens, sinks=None, scale=0.0, window=0, softcap=0.0, out=None, stream=None):
         """q: float32/bfloat16 [n, T, Hq, D], the last T rows of each sequence;
         returns the attention outputs in q's shape and dtype."""
         out, a = self._query(q, tables, lens, sinks, scale, window, softcap, out, stream)
-        self._call(B.kvq_paged_decode, a, self._stream(stream))
+        self._call(self._lib.kvq_paged_decode, a, self._stream(stream))
         return out
 
     def decode_shared(self, q, tables, lens, group_start, prefix_lens, sinks=None, scale=0.0, window=0, softcap=0.0,
@@ -378,7 +386,7 @@ class PagedKVCache:
         tensors [groups + 1] and [groups])."""
         out, a = self._query(q, tables, lens, sinks, scale, window, softcap, out, stream)
         g = prefix_lens.numel()
-        self._call(B.kvq_paged_decode_shared, a, self._ints(group_start, (g + 1,), "group_start"),
+        self._call(self._lib.kvq_paged_decode_shared, a, self._ints(group_start, (g + 1,), "group_start"),
                    self._ints(prefix_lens, (g,), "prefix_lens"), g, self._stream(stream))
         return out
 
@@ -388,7 +396,7 @@ class PagedKVCache:
         if pages is None:
             pages = self._new((q.shape[0], q.shape[1], self.n_kv_heads, keep), torch.int32, stream)
         out, a = self._query(q, tables, lens, None, 0.0, 0, 0.0, q, stream)
-        self._call(B.kvq_paged_select, a, self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"),
+        self._call(self._lib.kvq_paged_select, a, self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"),
                    keep, n_first, n_last, self._stream(stream))
         return pages
 
@@ -396,7 +404,7 @@ class PagedKVCache:
         """decode over the listed pages only (int32 [n, T, Hkv, keep])."""
         out, a = self._query(q, tables, lens, sinks, scale, 0, softcap, out, stream)
         keep = pages.shape[-1]
-        self._call(B.kvq_paged_decode_sparse, a,
+        self._call(self._lib.kvq_paged_decode_sparse, a,
                    self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"), keep, self._stream(stream))
         return out
 
