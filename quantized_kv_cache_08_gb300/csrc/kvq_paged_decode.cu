@@ -52,11 +52,12 @@ constexpr int warps_of() { return NB == 8 ? 8 : NB == 4 && TILE == kT16 ? 12 : 1
 template <int TILE>
 constexpr int queries_of() { return TILE == kT16 ? 16 : 8; }
 
-// c = a b, without a sum to start from
-__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+// c = a b + z (z: four zeros that stay in registers, where a constant would be
+// written to four new ones for each product)
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1, const float (&z)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -136,7 +137,8 @@ __device__ __forceinline__ void clear_rows(uint8_t* cell, int row0, const Rows& 
 // One staged cell, 16 rows from logical row row0 on, into the warp's accumulators
 template <int NB, bool F8, int TILE>
 __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int row0, const uint8_t* __restrict__ qs,
-                                          const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane, Acc<NB, F8, TILE>& acc) {
+                                          const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane, const float (&zero)[4],
+                                          Acc<NB, F8, TILE>& acc) {
     constexpr bool HL = TILE == kF32;
     constexpr int NQ = Acc<NB, F8, TILE>::NQ;
     const int j = lane & 3;
@@ -149,12 +151,7 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[t][i] = 0.f;
     auto q_frag = [&](int step) {
-        if constexpr (TILE == kT8) {
-            const uint2 x = *reinterpret_cast<const uint2*>(qs + (step * 32 + lane) * 8);
-            return make_uint4(x.x, 0u, x.y, 0u);
-        } else {
-            return *reinterpret_cast<const uint4*>(qs + (step * 32 + lane) * 16);
-        }
+        return *reinterpret_cast<const uint4*>(qs + (step * 32 + lane) * 16);
     };
 #pragma unroll
     for (int bp = 0; bp < NB / 2; ++bp) {
@@ -175,7 +172,7 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
                     mma_f16(sc[t], a1, f8_pair(w1), f8_pair(w1 >> 16));
                 } else {
                     float c[4];
-                    mma_f16_new(c, a0, k_pair(w0, 0x4140u), k_pair(w0, 0x4342u));
+                    mma_f16_new(c, a0, k_pair(w0, 0x4140u), k_pair(w0, 0x4342u), zero);
                     mma_f16(c, a1, k_pair(w1, 0x4140u), k_pair(w1, 0x4342u));
                     const float2 d = __half22float2(as_h2(e ? (t ? ks.w : ks.z) : (t ? ks.y : ks.x)));
                     if constexpr (HL) {
@@ -362,7 +359,7 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
 template <int NB, int TILE>
 struct Smem {
     static constexpr int D = NB * 32;
-    static constexpr size_t qs = (size_t)(D / 16) * (TILE == kT8 ? 256 : 512);
+    static constexpr size_t qs = (size_t)(D / 16) * 512;
     static constexpr size_t comb = (size_t)warps_of<NB, TILE>() / 2 * queries_of<TILE>() * (D + 4) * 4;
     __host__ __device__ static size_t ring(int E) { return (kMaxGroups * qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
 };
@@ -417,7 +414,7 @@ __device__ __forceinline__ bool next_fragment(Fragment& f, long long& x, long lo
 struct Producer {
     long long x;                   // behind the fragment
     int c, cb;                     // next cell, and the fragment's end
-    int slot, page, i;             // the lane's looked-up cell (-1: none); next lane to use
+    int row0, page, off, i;        // the lane's looked-up cell (row0 -1: none) and its bytes in the page; next lane to use
     int kh, c0, hi, listed;
     const int* table;
     const int* list;
@@ -442,16 +439,18 @@ __device__ __forceinline__ void look_up(Producer& p, const SplitArgs& a, int lan
     p.i = 0;
     const int cps = a.g.page_shift - 4, mask = (1 << cps) - 1;
     const int c = p.c + lane * a.gw;
-    p.slot = p.page = -1;
+    p.row0 = -1;
     if (c >= p.cb) return;
-    int slot = p.listed ? p.list[c >> cps] : (p.c0 + c) >> cps;
-    if (slot >= a.g.max_pages) {
-        atomicExch(a.g.err, kErrCounter);
-        slot = -1;
+    const int at = p.listed ? c : p.c0 + c, in = at & mask;
+    int slot = at >> cps;
+    if (p.listed) {
+        slot = p.list[slot];
+        if (slot >= a.g.max_pages) atomicExch(a.g.err, kErrCounter);
+        if (slot < 0 || slot >= a.g.max_pages || slot * a.g.page_rows + in * 16 >= p.hi) return;
     }
-    if (slot < 0 || slot * a.g.page_rows + (p.listed ? (c & mask) * 16 : 0) >= p.hi) return;
-    p.slot = slot;
+    p.row0 = slot * a.g.page_rows + in * 16;
     p.page = p.table[slot];
+    p.off = (p.kh * (mask + 1) + in) * a.g.cell_bytes;
 }
 // On to the next fragment in which this warp has a cell; false: none
 __device__ __forceinline__ bool refill(Producer& p, const SplitArgs& a, const PlanEntry* plan, int QPI, long long x1, int gwarp) {
@@ -591,7 +590,6 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     float* comb = reinterpret_cast<float*>(smem + kMaxGroups * S::qs) + (size_t)group * (gw / 2) * QPI * PAD;
     RowInfo& ri = s_ri[group];
     auto sync_group = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gw * 32) : "memory"); };
-    const int cpp = a.g.cells_per_page();                  // a power of two
     const uint32_t ring = dev::smem_u32(smem) + (uint32_t)S::ring(a.E) + (uint32_t)(warp * stages * CELL);
     uint8_t* ring_p = smem + S::ring(a.E) + (size_t)warp * stages * CELL;
     const uint32_t bar0 = dev::smem_u32(&s_bar[warp][0]);
@@ -638,9 +636,10 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 const float y = qv[i][b] * up;
                 const __half hi = __float2half_rn(y);
                 const int at = (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
-                __half* dst = reinterpret_cast<__half*>(qs + at * (TILE == kT8 ? 8 : 16));
-                if (TILE == kT8) {
-                    dst[reg + half] = hi;
+                __half* dst = reinterpret_cast<__half*>(qs + at * 16);
+                if (TILE == kT8) {                         // (rows 8 .. 15 of the tile are zeros)
+                    dst[2 * reg + half] = hi;
+                    dst[2 * (reg + 1) + half] = __float2half_rn(0.f);
                 } else if (HL) {
                     dst[2 * reg + half] = hi;
                     dst[2 * (reg + 1) + half] = __float2half_rn(y - __half2float(hi));
@@ -655,26 +654,27 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     Fragment f{};
     Producer pr;
     pr.c = pr.cb = 0;
-    pr.slot = pr.page = -1;
+    pr.row0 = -1;
     pr.i = 32;
+    const uint64_t policy = dev::evict_first_policy();      // a decode reads each cell once, or nearly
     auto produce = [&](int st) {                           // the next cell of the ring, into stage st
         if (pr.c >= pr.cb) {
             if (!refill(pr, a, plan, QPI, x1, gwarp)) return;
             pr.i = 32;
         }
         if (pr.i == 32) look_up(pr, a, lane);
-        const int page = __shfl_sync(0xffffffffu, pr.page, pr.i), slot = __shfl_sync(0xffffffffu, pr.slot, pr.i);
-        if (lane == 0) {
+        if (lane == pr.i) {
             const uint32_t bar = bar0 + 8u * st;
-            const int in = (pr.listed ? pr.c : pr.c0 + pr.c) & (cpp - 1);
-            const bool there = page >= 0 && page < a.g.n_pages;
-            if (slot >= 0 && !there) atomicExch(a.g.err, kErrCounter);
+            const bool there = pr.row0 >= 0 && pr.page >= 0 && pr.page < a.g.n_pages;
+            if (pr.row0 >= 0 && !there) atomicExch(a.g.err, kErrCounter);
+            s_row0[warp][st] = there ? pr.row0 : -1;
             if (there) {
-                s_row0[warp][st] = slot * a.g.page_rows + in * 16;
                 dev::mbar_expect_tx(bar, CELL);
-                dev::bulk_g2s(ring + (uint32_t)(st * CELL), a.g.pool + page * a.g.page_bytes + (long long)(pr.kh * cpp + in) * CELL, CELL, bar);
+                asm volatile(
+                    "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                    ::"r"(ring + (uint32_t)(st * CELL)), "l"(a.g.pool + pr.page * a.g.page_bytes + pr.off), "r"(CELL), "r"(bar), "l"(policy)
+                    : "memory");
             } else {
-                s_row0[warp][st] = -1;
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
             }
         }
@@ -682,6 +682,9 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         pr.c += a.gw;
     };
 
+    float zero[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
     int st = 0;
     uint32_t phase = 0;
     wait_for_earlier();
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             const bool there = wait_bounded(bar0 + 8u * st, phase, &s_abort, a.g.err);
             const int row0 = s_row0[warp][st];
             if (there && row0 >= 0 && row0 < lr.hi_max)
-                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, acc);
+                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, zero, acc);
             __syncwarp();
             if (there) produce(st);
             if (++st == stages) {
