@@ -138,7 +138,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* cell, int row0, const Rows& 
 template <int NB, bool F8, int TILE>
 __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int row0, const uint8_t* __restrict__ qs,
                                           const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane, const float (&zero)[4],
-                                          Acc<NB, F8, TILE>& acc) {
+                                          uint32_t magic, Acc<NB, F8, TILE>& acc) {
     constexpr bool HL = TILE == kF32;
     constexpr int NQ = Acc<NB, F8, TILE>::NQ;
     const int j = lane & 3;
@@ -305,7 +305,7 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
             if constexpr (!HL) {
                 auto value = [&](auto R, int n, uint32_t d, uint32_t m) {
                     constexpr int r = decltype(R)::value;
-                    const __half2 c = __hsub2(as_h2(v_codes<r>(u[n], nb[n / 4], n % 4, 0x64006400u)), as_h2(0x64006400u));
+                    const __half2 c = __hsub2(as_h2(v_codes<r>(u[n], nb[n / 4], n % 4, magic)), as_h2(magic));
                     return as_u32(__hfma2(c, as_h2(d), as_h2(m)));
                 };
                 const std::integral_constant<int, 0> r0{};
@@ -334,7 +334,7 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
                 const uint32_t pl1 = as_u32(__floats2bfloat162_rn(x2 - f1.x, x3 - f1.y));
                 auto code = [&](auto R, int n) {
                     constexpr int r = decltype(R)::value;
-                    uint32_t c = v_codes<r>(u[n], nb[n / 4], n % 4, 0x43004300u);
+                    uint32_t c = v_codes<r>(u[n], nb[n / 4], n % 4, magic);
                     return as_u32(__hsub2(*reinterpret_cast<__nv_bfloat162*>(&c), __floats2bfloat162_rn(144.f, 144.f)));
                 };
                 const std::integral_constant<int, 0> r0{};
@@ -685,6 +685,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     float zero[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
+    const uint32_t magic = held(HL ? 0x43004300u : 0x64006400u);   // 128 in bf16, 1024 in fp16: codes in the low bits add to it
     int st = 0;
     uint32_t phase = 0;
     wait_for_earlier();
@@ -821,7 +822,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             const bool there = wait_bounded(bar0 + 8u * st, phase, &s_abort, a.g.err);
             const int row0 = s_row0[warp][st];
             if (there && row0 >= 0 && row0 < lr.hi_max)
-                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, zero, acc);
+                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, zero, magic, acc);
             __syncwarp();
             if (there) produce(st);
             if (++st == stages) {

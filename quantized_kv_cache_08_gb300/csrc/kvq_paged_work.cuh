@@ -34,13 +34,27 @@ __device__ __forceinline__ uint32_t f8_pair(uint32_t two) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The 5-bit codes of element r of two rows, in the low bits of each half word
+// (x & mask) | y in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t y) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(y));
+    return d;
+}
+// A constant that the compiler keeps in a register (an instruction takes one
+// immediate, so a mask and a magic number as constants would make two of one)
+__device__ __forceinline__ uint32_t held(uint32_t c) {
+    uint32_t r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(c));
+    return r;
+}
+// The 5-bit codes of element R of two rows, in the low bits of each half word, on
+// top of `magic`; the element 3 nibbles are at bit 4 n4 of nib's half words
 template <int R>
 __device__ __forceinline__ uint32_t v_codes(uint32_t unit, uint32_t nib, int n4, uint32_t magic) {
-    if constexpr (R == 0) return (unit & 0x001f001fu) | magic;
-    else if constexpr (R == 1) return ((unit >> 5) & 0x001f001fu) | magic;
-    else if constexpr (R == 2) return ((unit >> 10) & 0x001f001fu) | magic;
-    else return (((unit >> 11) & 0x00100010u) | magic) | ((nib >> (4 * n4)) & 0x000f000fu);
+    if constexpr (R == 0) return and_or(unit, 0x001f001fu, magic);
+    else if constexpr (R == 1) return and_or(unit >> 5, 0x001f001fu, magic);
+    else if constexpr (R == 2) return and_or(unit >> 10, 0x001f001fu, magic);
+    else return and_or(nib >> (4 * n4), 0x000f000fu, and_or(unit >> 11, 0x00100010u, magic));
 }
 
 // ------------------------------------------------------------ work entries
