@@ -408,8 +408,9 @@ kvq_status kvq_paged_read(kvq_paged* cache, void* k_out, void* v_out, kvq_dtype 
  * dtype; out the same shape and type (bf16 queries give bf16 outputs).  Row t
  * sees logical rows [max(0, p + 1 - window), p + 1), p = len - T + t (window
  * 0: all).  scale <= 0 selects 1/sqrt(D); softcap > 0 caps scaled scores to
- * softcap * tanh(s / softcap); sinks: device f32 [Hq] or NULL, logits that
- * join max and denominator without a value. */
+ * softcap * tanh(s / softcap) (either, where positive, within 1e-30 .. 1e30);
+ * sinks: device f32 [Hq] or NULL, logits that join max and denominator
+ * without a value (-inf: none).  out may be q. */
 typedef struct kvq_paged_query {
     const void* q;
     void* out;

@@ -139,7 +139,11 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     kvq_status st = check_query(c, q);
     if (st != KVQ_OK) return st;
     if (!q->out || !aligned16(q->out)) return fail(KVQ_EINVAL, "out is NULL or not 16-byte aligned");
-    if (!(q->softcap >= 0.f) || q->softcap > 3.0e38f) return fail(KVQ_EINVAL, "softcap must be finite and >= 0");
+    // (both go through products and quotients in f32)
+    if (!(q->softcap == 0.f || (q->softcap >= 1e-30f && q->softcap <= 1e30f)))
+        return fail(KVQ_EINVAL, "softcap must be 0 or within 1e-30 .. 1e30");
+    if (!(q->scale <= 0.f || (q->scale >= 1e-30f && q->scale <= 1e30f)))
+        return fail(KVQ_EINVAL, "scale must be <= 0 (1 / sqrt(head_dim)) or within 1e-30 .. 1e30");
     if (q->window < 0) return fail(KVQ_EINVAL, "window must be >= 0");
     SplitArgs a = {};
     a.g = c->g;

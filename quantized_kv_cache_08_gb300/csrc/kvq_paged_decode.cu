@@ -41,7 +41,6 @@ namespace kvq {
 namespace paged {
 namespace {
 
-constexpr int kMaxGroups = 4;          // groups of warps in a CTA
 
 // Query tiles: 8 or 16 bf16 queries, or 8 of f32 in two parts
 enum Tile { kT8 = 0, kT16 = 1, kF32 = 2 };
@@ -49,6 +48,9 @@ enum Tile { kT8 = 0, kT16 = 1, kF32 = 2 };
 // Warps of a CTA (one CTA an SM): as many as the accumulators leave registers for
 template <int NB, int TILE>
 constexpr int warps_of() { return NB == 8 ? 8 : NB == 4 && TILE == kT16 ? 12 : 16; }
+// Groups of four warps, which work on ranges of their own where there is enough work
+template <int NB, int TILE>
+constexpr int groups_of() { return warps_of<NB, TILE>() / 4; }
 template <int TILE>
 constexpr int queries_of() { return TILE == kT16 ? 16 : 8; }
 
@@ -71,8 +73,8 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint4& a, uint32_t
 }
 
 // code bytes (biased by 128) sel of w under the exponent of 1024, minus 1152: exact
-__device__ __forceinline__ uint32_t k_pair(uint32_t w, uint32_t sel) {
-    return as_u32(__hsub2(as_h2(__byte_perm(w, 0x64646464u, sel)), as_h2(0x64806480u)));
+__device__ __forceinline__ uint32_t k_pair(uint32_t w, uint32_t sel, uint32_t exps) {
+    return as_u32(__hsub2(as_h2(__byte_perm(w, exps, sel)), as_h2(0x64806480u)));
 }
 __device__ __forceinline__ float load_q(const void* q, long long idx, int bf16) {
     if (bf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q)[idx]);
@@ -138,7 +140,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* cell, int row0, const Rows& 
 template <int NB, bool F8, int TILE>
 __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int row0, const uint8_t* __restrict__ qs,
                                           const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane, const float (&zero)[4],
-                                          uint32_t magic, Acc<NB, F8, TILE>& acc) {
+                                          uint32_t magic, uint32_t exps, Acc<NB, F8, TILE>& acc) {
     constexpr bool HL = TILE == kF32;
     constexpr int NQ = Acc<NB, F8, TILE>::NQ;
     const int j = lane & 3;
@@ -172,8 +174,8 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
                     mma_f16(sc[t], a1, f8_pair(w1), f8_pair(w1 >> 16));
                 } else {
                     float c[4];
-                    mma_f16_new(c, a0, k_pair(w0, 0x4140u), k_pair(w0, 0x4342u), zero);
-                    mma_f16(c, a1, k_pair(w1, 0x4140u), k_pair(w1, 0x4342u));
+                    mma_f16_new(c, a0, k_pair(w0, 0x4140u, exps), k_pair(w0, 0x4342u, exps), zero);
+                    mma_f16(c, a1, k_pair(w1, 0x4140u, exps), k_pair(w1, 0x4342u, exps));
                     const float2 d = __half22float2(as_h2(e ? (t ? ks.w : ks.z) : (t ? ks.y : ks.x)));
                     if constexpr (HL) {
                         c[0] += c[2];
@@ -354,14 +356,17 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
     if (edge) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+constexpr size_t kRingEnd = 220 * 1024;
+
 // Shared memory of the split kernel: query fragments of each group, the joins'
 // sums, the plan, then a ring of `stages` cells per warp.
 template <int NB, int TILE>
 struct Smem {
     static constexpr int D = NB * 32;
     static constexpr size_t qs = (size_t)(D / 16) * 512;
+    static constexpr size_t all_qs = groups_of<NB, TILE>() * qs;
     static constexpr size_t comb = (size_t)warps_of<NB, TILE>() / 2 * queries_of<TILE>() * (D + 4) * 4;
-    __host__ __device__ static size_t ring(int E) { return (kMaxGroups * qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
+    __host__ __device__ static constexpr size_t ring(int E) { return (all_qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
 };
 
 // x g / d and x / d for 0 <= x, in 32 bits where they fit
@@ -569,14 +574,14 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     constexpr int PAD = D + 4;                        // row stride of the joins' sums: lanes of a store in different banks
     using S = Smem<NB, TILE>;
     extern __shared__ __align__(128) uint8_t smem[];
-    PlanEntry* plan = reinterpret_cast<PlanEntry*>(smem + kMaxGroups * S::qs + S::comb);
-    __shared__ RowInfo s_ri[kMaxGroups];
+    PlanEntry* plan = reinterpret_cast<PlanEntry*>(smem + S::all_qs + S::comb);
+    __shared__ RowInfo s_ri[groups_of<NB, TILE>()];
     __shared__ float s_m[kWarps][16], s_l[kWarps][16];
     __shared__ long long s_wsum[kWarps];
     __shared__ int s_ksum[kWarps];
     __shared__ int s_row0[kWarps][kMaxStages];        // first row of the cell in a stage, -1: none
     __shared__ __align__(8) uint64_t s_bar[kWarps][kMaxStages];
-    __shared__ int s_abort, s_last[kMaxGroups];
+    __shared__ int s_abort, s_last[groups_of<NB, TILE>()];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (lane < stages) dev::mbar_init(dev::smem_u32(&s_bar[warp][lane]), 1);
@@ -587,7 +592,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     const int gw = a.gw, group = warp / gw, gwarp = warp - group * gw, gtid = tid - group * gw * 32;
     const int range = group * gridDim.x + blockIdx.x;
     uint8_t* qs = smem + group * S::qs;
-    float* comb = reinterpret_cast<float*>(smem + kMaxGroups * S::qs) + (size_t)group * (gw / 2) * QPI * PAD;
+    float* comb = reinterpret_cast<float*>(smem + S::all_qs) + (size_t)group * (gw / 2) * QPI * PAD;
     RowInfo& ri = s_ri[group];
     auto sync_group = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gw * 32) : "memory"); };
     const uint32_t ring = dev::smem_u32(smem) + (uint32_t)S::ring(a.E) + (uint32_t)(warp * stages * CELL);
@@ -686,6 +691,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
     const uint32_t magic = held(HL ? 0x43004300u : 0x64006400u);   // 128 in bf16, 1024 in fp16: codes in the low bits add to it
+    const uint32_t exps = held(0x64646464u);
     int st = 0;
     uint32_t phase = 0;
     wait_for_earlier();
@@ -822,7 +828,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             const bool there = wait_bounded(bar0 + 8u * st, phase, &s_abort, a.g.err);
             const int row0 = s_row0[warp][st];
             if (there && row0 >= 0 && row0 < lr.hi_max)
-                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, zero, magic, acc);
+                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, zero, magic, exps, acc);
             __syncwarp();
             if (there) produce(st);
             if (++st == stages) {
@@ -1048,8 +1054,10 @@ cudaError_t launch_split_t(const SplitArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     using S = Smem<NB, TILE>;
     constexpr size_t cells = (size_t)warps_of<NB, TILE>() * NB * (F8 ? 1024 : 928);
-    // the ring takes what the plan leaves of 220 KB
-    const int stages = (int)std::min<size_t>(kMaxStages, (220 * 1024 - S::ring(a.E)) / cells);
+    // the ring takes what the plan leaves of 220 KB: a cell for each warp at least
+    static_assert(S::ring(kMaxEntries) + cells <= kRingEnd, "no room for the cells");
+    if (a.E > kMaxEntries) return cudaErrorInvalidValue;
+    const int stages = (int)std::min<size_t>(kMaxStages, (kRingEnd - S::ring(a.E)) / cells);
     return launch_dependent(split_kernel<NB, F8, TILE>, dim3((unsigned)a.G), warps_of<NB, TILE>() * 32,
                             S::ring(a.E) + stages * cells, s, a, stages);
 }

@@ -218,7 +218,7 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
 template <int NB, int NBT, bool F8>
 __device__ __forceinline__ void store_k(uint32_t tile, int pr, int b0, int lane, Raw<NBT, F8>& r) {
     const int g = lane >> 2, j = lane & 3;
-    const uint32_t dsel = (g & 1) ? 0x3232u : 0x1010u;
+    const uint32_t dsel = (g & 1) ? 0x3232u : 0x1010u, exps = held(0x44444444u);
 #pragma unroll 1
     for (int it = 0; it < NBT; ++it) {                        // block pair it / 2, cell it % 2
         const int row0 = 32 * pr + 8 * (g >> 1) + 4 * (it & 1) + (g & 1);
@@ -238,7 +238,7 @@ __device__ __forceinline__ void store_k(uint32_t tile, int pr, int b0, int lane,
                 } else {
                     const __half2 dd = as_h2(__byte_perm(r.w[8 + 2 * e + t], 0, dsel));
                     auto two = [&](uint32_t v, uint32_t sel) {
-                        return as_u32(__hmul2(__hsub2(as_h2(__byte_perm(v, 0x44444444u, sel)), as_h2(0x44804480u)), dd));
+                        return as_u32(__hmul2(__hsub2(as_h2(__byte_perm(v, exps, sel)), as_h2(0x44804480u)), dd));
                     };
                     o[0] = two(x, 0x4140u);
                     o[1] = two(x, 0x4342u);
@@ -259,6 +259,7 @@ __device__ __forceinline__ void store_v(uint32_t tile, int pr, int b0, int lane,
     const int g = lane >> 2, j = lane & 3;
     const uint32_t block = tile + (pr >> 1) * (D * 128);
     const int chunk = 4 * (pr & 1) + j;
+    const uint32_t magic = held(0x64006400u);
 #pragma unroll 1
     for (int b = 0; b < NBT; ++b) {
         uint32_t o[4][4];                                     // element r, (cell, half)
@@ -277,7 +278,7 @@ __device__ __forceinline__ void store_v(uint32_t tile, int pr, int b0, int lane,
                 const uint32_t* dm = r.w + 4 + 4 * (ch >> 1);
                 const __half2 d = as_h2(dm[ch & 1] & k), m = as_h2(dm[2 + (ch & 1)] & k);
                 auto val = [&](auto R) {
-                    const __half2 u = __hsub2(as_h2(v_codes<decltype(R)::value>(unit, nib, 0, 0x64006400u)), as_h2(0x64006400u));
+                    const __half2 u = __hsub2(as_h2(v_codes<decltype(R)::value>(unit, nib, 0, magic)), as_h2(magic));
                     return as_u32(__hfma2(u, d, m));
                 };
                 o[0][ch] = val(std::integral_constant<int, 0>{});

@@ -503,3 +503,231 @@ def test_a_serving_run(fmt):
                 lens[b] -= cut
                 p.k[b], p.v[b] = p.k[b][:lens[b]], p.v[b][:lens[b]]
     assert p.dev.device_error() == 0
+
+
+# ------------------------------------------------------------------ sizes and calls at the ends of the ranges
+
+@pytest.mark.parametrize("fmt,D,Hq,dtype", [(F8, 256, 16, BF), (F8, 256, 2, F32), (Q8, 128, 12, BF), (F8, 64, 3, BF)])
+def test_as_many_sequences_as_a_call_takes(fmt, D, Hq, dtype):
+    """1024 sequences, then 1024 groups of one over them, then 2048 listed rows."""
+    n = 1024
+    p = PagedPair(n, 1, D, Hq, page=16, max_pages=2, fmt=fmt, max_t=2, bounds=True, seed=D + Hq)
+    p.append([int(x) for x in p.rng.integers(0, 33, n)])
+    q = p.randn(n, 1, Hq, D).to(dtype)
+    want, mag = p.want(q)
+    got = p.dev.decode(q.cuda(), p.tables, p.lens())
+    assert p.dev.device_error() == 0
+    assert_attention(p, got, want, mag)
+    got = p.dev.decode_shared(q.cuda(), p.tables, p.lens(), i32(list(range(n + 1))), i32([16] * n))
+    assert p.dev.device_error() == 0
+    assert_attention(p, got, want, mag, "groups of one")
+    q = p.randn(n, 2, Hq, D).to(dtype)
+    pages = p.dev.select(q.cuda(), p.tables, p.lens(), 2)
+    want, mag = p.want(q)
+    got = p.dev.decode_sparse(q.cuda(), p.tables, p.lens(), pages)
+    assert p.dev.device_error() == 0
+    assert_attention(p, got, want, mag, "every page listed")
+
+
+@pytest.mark.parametrize("fmt", [Q8, F8])
+def test_a_pool_beyond_32_bits(fmt):
+    """The same rows in a small pool and at both ends of one of more than 2^32 bytes."""
+    torch.manual_seed(1)
+    cfg = dict(page_rows=256, n_kv_heads=8, head_dim=256, max_q_heads=16, max_seqs=2, max_pages=2, fmt=fmt, bounds=True,
+               rope_dim=64)
+    small, big = PagedKVCache(4, **cfg), PagedKVCache(5200, **cfg)
+    assert big.sizes.pool > 2 ** 32
+    k, v = (torch.randn(2, 500, 8, 256, device="cuda").to(BF) for _ in range(2))
+    q, lens = torch.randn(2, 1, 16, 256, device="cuda").to(BF), i32([500, 500])
+    outs = []
+    for c, tab in ((small, [[0, 1], [2, 3]]), (big, [[5199, 0], [2600, 5198]])):
+        tab = i32(tab)
+        c.append(k, v, tab, lens)
+        ko, vo = torch.empty(2, 3, 8, 256, device="cuda"), torch.empty(2, 3, 8, 256, device="cuda")
+        c.read(tab, lens, ko, vo)
+        pages = c.select(q, tab, lens, 1, n_first=0, n_last=0)
+        outs.append([c.decode(q, tab, lens), c.decode_sparse(q, tab, lens, pages), pages, ko, vo,
+                     c.decode_shared(q, tab[:1].expand(2, -1).contiguous(), lens, i32([0, 2]), i32([256]))])
+        assert c.device_error() == 0
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_one_row_through_long_ones():
+    """Every length around a cell, a page and the pages that one lookup takes."""
+    lens = [1, 15, 16, 17, 31, 32, 33, 127, 128, 129, 511, 512, 513, 527, 1023, 1025]
+    p = PagedPair(len(lens), 1, 64, 4, page=32, max_pages=33, seed=8)
+    p.append(lens)
+    for dtype in (BF, F32):
+        q = p.randn(p.n, 1, 4, 64).to(dtype)
+        want, mag = p.want(q)
+        assert_attention(p, p.dev.decode(q.cuda(), p.tables, p.lens()), want, mag)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sinks_of_no_weight_and_of_all(dtype):
+    """A sink of -inf is none, also where no row is visible; a huge one takes everything."""
+    p = PagedPair(3, 1, 64, 4, page=16, max_pages=4, max_t=2)
+    p.append([40, 0, 1])
+    q = p.randn(3, 2, 4, 64).to(dtype)
+    plain, mag = p.want(q)
+    sinks = torch.tensor([-float("inf"), 0.5, 1e4, -1e4])
+    got = p.dev.decode(q.cuda(), p.tables, p.lens(), sinks=sinks.cuda())
+    want, _ = p.want(q, sinks=torch.tensor([-1e9, 0.5, 1e4, -1e9]))
+    assert_attention(p, got, want, mag)
+    assert (got[1] == 0).all() and (got[:, :, 2] == 0).all()
+    shared = p.dev.decode_shared(q.cuda(), p.tables, p.lens(), i32([0, 1]), i32([32]), sinks=sinks.cuda())
+    assert_attention(p, shared, want, mag, "shared")
+
+
+def test_a_query_that_is_not_a_number_stays_alone():
+    """NaN and inf in one query head leave every other output as it was."""
+    p = PagedPair(2, 1, 128, 8, page=16, max_pages=8, max_t=2, bounds=True)
+    p.append([100, 128])
+    for dtype in (BF, F32):
+        q = p.randn(2, 2, 8, 128).to(dtype).cuda()
+        bad = q.clone()
+        bad[0, 1, 3, 5], bad[0, 1, 6, 0] = float("nan"), float("inf")
+        args = (p.tables, p.lens())
+        for call in (lambda x: p.dev.decode(x, *args),
+                     lambda x: p.dev.decode_shared(x, *args, i32([0, 2]), i32([0]))):
+            a, b = call(q), call(bad)
+            a[0, 1, 3], b[0, 1, 3], a[0, 1, 6], b[0, 1, 6] = 0, 0, 0, 0
+            assert torch.equal(a, b)
+        pages = p.dev.select(bad, *args, 3)
+        assert torch.equal(pages[1], p.dev.select(q, *args, 3)[1])
+        assert ((pages >= 0) & (pages < 8)).all()
+    assert p.dev.device_error() == 0
+
+
+def test_output_over_the_queries():
+    p = PagedPair(3, 2, 128, 8, page=16, max_pages=64, bounds=True, seed=4)
+    p.append([1000, 3, 700])
+    q = p.randn(3, 1, 8, 128).to(BF).cuda()
+    pages = p.dev.select(q, p.tables, p.lens(), 8)
+    args = (p.tables, p.lens())
+    for call, more in ((p.dev.decode, ()), (p.dev.decode_sparse, (pages,)),
+                       (p.dev.decode_shared, (i32([0, 1]), i32([512])))):
+        own = q.clone()
+        assert torch.equal(call(own, *args, *more, out=own), call(q, *args, *more))
+
+
+def test_two_graphs_share_one_cache():
+    """Graphs captured on the same workspace, replayed in turn, with eager calls between."""
+    p = PagedPair(2, 1, 128, 20, page=16, max_pages=32, bounds=True, seed=6)
+    p.append([400, 77])
+    lens, gs, pre = p.lens(), i32([0, 2]), i32([0])
+    q = [p.randn(2, 1, 20, 128).to(BF).cuda() for _ in range(2)]
+    want = [p.dev.decode(x, p.tables, lens) for x in q]
+    shared = [p.dev.decode_shared(x, p.tables, lens, gs, pre) for x in q]
+    graphs, outs = [], []
+    for x in q:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((p.dev.decode(x, p.tables, lens), p.dev.decode_shared(x, p.tables, lens, gs, pre)))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        for o in outs[i]:
+            o.zero_()
+        graphs[i].replay()
+        p.dev.decode(q[1 - i], p.tables, lens)
+        assert torch.equal(outs[i][0], want[i]) and torch.equal(outs[i][1], shared[i])
+
+
+def test_calls_of_another_stream_and_its_capture():
+    p = PagedPair(2, 1, 64, 4, page=16, max_pages=4, bounds=True, seed=9)
+    p.append([33, 50])
+    q, lens = p.randn(2, 1, 4, 64).to(BF).cuda(), p.lens()
+    want = p.dev.decode(q, p.tables, lens)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = p.dev.decode(q, p.tables, lens, stream=s)
+    pages = p.dev.select(q, p.tables, lens, 4, stream=s)
+    sparse = p.dev.decode_sparse(q, p.tables, lens, pages, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    assert_attention(p, sparse, *p.want(q.cpu()))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = p.dev.decode(q, p.tables, lens)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_refusals_of_the_calls():
+    p = PagedPair(2, 2, 64, 8, page=16, max_pages=4, max_t=2, bounds=True)
+    p.append([20, 40])
+    c, tab, lens = p.dev, p.tables, p.lens()
+    before = c.pool.clone()
+    q = torch.zeros(2, 1, 8, 64, device="cuda", dtype=BF)
+    kv = torch.zeros(2, 1, 2, 64, device="cuda", dtype=BF)
+    pages = torch.zeros(2, 1, 2, 3, device="cuda", dtype=torch.int32)
+
+    def refused(fn, *a, error=(ValueError, B.KvqError), **kw):
+        with pytest.raises(error):
+            fn(*a, **kw)
+
+    # queries
+    for bad in (q[:1], q[..., :32], q.half(), q[0], q.cpu(), q.transpose(1, 2), q[:, :, :3].contiguous(),
+                q[:, :, :, :].expand(2, 1, 8, 64)[:, :0], torch.zeros(2, 3, 8, 64, device="cuda", dtype=BF),
+                torch.zeros(2, 1, 16, 64, device="cuda", dtype=BF)):
+        refused(c.decode, bad, tab, lens)
+        refused(c.decode_shared, bad, tab, lens, i32([0, 2]), i32([16]))
+        refused(c.select, bad, tab, lens, 3)
+        refused(c.decode_sparse, bad, tab, lens, pages)
+    shifted = torch.zeros(2 * 8 * 64 + 1, device="cuda", dtype=BF)[1:].view(2, 1, 8, 64)
+    refused(c.decode, shifted, tab, lens)
+    refused(c.decode, q, tab, lens, out=shifted)
+    refused(c.decode, q, tab, lens, out=q.float())
+    # tables and lengths
+    for t, n in ((tab.long(), lens), (tab[:, :3], lens), (tab[:, :3].contiguous(), lens), (tab, lens.float()),
+                 (tab, lens[:1]), (tab.cpu(), lens), (tab, lens.cpu()), (tab[:1], lens)):
+        refused(c.decode, q, t, n)
+        refused(c.append, kv, kv, t, n)
+    many = torch.zeros(3, 4, dtype=torch.int32, device="cuda")
+    refused(c.decode, torch.zeros(3, 1, 8, 64, device="cuda", dtype=BF), many, i32([0, 0, 0]))
+    # numbers
+    for kw in (dict(window=-1), dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")),
+               dict(softcap=1e-35), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e-35),
+               dict(sinks=torch.zeros(7, device="cuda")), dict(sinks=torch.zeros(8)),
+               dict(sinks=torch.zeros(8, device="cuda", dtype=BF))):
+        refused(c.decode, q, tab, lens, **kw)
+    # groups
+    refused(c.decode_shared, q, tab, lens, i32([0]), i32([]))
+    refused(c.decode_shared, q, tab, lens, i32([0, 1, 2, 2]), i32([0, 0, 0]))
+    refused(c.decode_shared, q, tab, lens, i32([0, 2]).long(), i32([0]))
+    refused(c.decode_shared, q, tab, lens, i32([0, 1, 2]), i32([0]))
+    # selection and lists
+    for kw in (dict(keep=0), dict(keep=1), dict(keep=3, n_first=2, n_last=2), dict(keep=3, n_first=-1),
+               dict(keep=3, n_last=-1)):
+        refused(c.select, q, tab, lens, **kw, error=(ValueError, B.KvqError, RuntimeError))
+    refused(c.select, q, tab, lens, 3, pages=pages.long())
+    refused(c.select, q, tab, lens, 2, pages=pages)
+    refused(c.decode_sparse, q, tab, lens, pages.long())
+    refused(c.decode_sparse, q, tab, lens, pages[:, :, :1].contiguous())
+    plain = PagedKVCache(4, 16, 2, 64, 8, max_seqs=2, max_pages=4)
+    refused(plain.select, q, tab, lens, 3)
+    refused(plain.update_bounds, tab, lens, 1)
+    # rows
+    for k, v, kw in ((kv, kv.float(), {}), (kv.half(), kv.half(), {}), (kv[:, :, :1], kv[:, :, :1], {}),
+                     (kv[:1], kv[:1], {}), (kv[:, :0], kv[:, :0], {}), (kv[0], kv[0], {}), (kv, kv[:1], {}),
+                     (kv, kv, dict(starts=i32([0, 1, 2]))), (kv[:, 0], kv[:, 0], dict(starts=i32([0, 2]))),
+                     (kv[:, 0], kv[:, 0], dict(starts=i32([0, 1, 2]).long())), (kv.cpu(), kv.cpu(), {}),
+                     (kv, kv, dict(q=q.float())), (kv, kv, dict(q=q[:1])), (kv, kv, dict(q_out=q)),
+                     (kv, kv, dict(q=q, q_out=q.float())), (kv, kv, dict(q=torch.zeros(2, 1, 9, 64, device="cuda", dtype=BF))),
+                     (kv.transpose(2, 3), kv, {}), (kv.expand(2, 1, 2, 64)[..., ::2], kv[..., ::2], {})):
+        refused(c.append, k, v, tab, lens, **kw)
+    odd = torch.zeros(2, 1, 2 * 64 + 4, device="cuda", dtype=BF)[..., :128].unflatten(-1, (2, 64))
+    refused(c.append, odd, kv, tab, lens)
+    refused(c.read, tab, lens, kv, kv.float())
+    refused(c.read, tab, lens, kv.half(), kv.half())
+    refused(c.read, tab, lens, kv.transpose(2, 3), kv)
+    for bad in (torch.zeros(8, dtype=torch.uint8, device="cuda"), c.pool.view(torch.int8), c.pool.cpu()):
+        refused(PagedKVCache, p.n_pages, 16, 2, 64, 8, max_seqs=2, max_pages=4, pool=bad, device="cuda:0")
+    refused(PagedKVCache, 4, 16, 2, 64, 8, max_seqs=2, max_pages=4, fmt="q4")
+    refused(PagedKVCache, 4, 16, 2, 64, 8, max_seqs=2, max_pages=4, rope_dim=16, rope_freq=[1.0])
+    assert c.device_error() == 0 and torch.equal(c.pool, before)
