@@ -149,7 +149,8 @@ struct SelectArgs {
     const int* tables;
     const int* lens;
     int* pages;            // [n_seq][T][Hkv][keep]
-    uint32_t* keys;        // [n_seq][T][Hkv][max_pages] scores as ordered integers
+    uint32_t* keys;        // [n_seq][T][Hkv][key_stride] scores as ordered integers
+    int key_stride;        // max_pages in whole fours
     int* arrived;          // [n_seq * T * Hkv] CTAs done; 0 between calls
     int keep, n_first, n_last;
 };

@@ -87,7 +87,7 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     l->keys = round_up(l->o2 + recs2 * D * 2, 256);
     l->total = l->keys;
     if (c->bounds)
-        l->total += round_up((size_t)std::min(kMaxEntries, c->max_seqs * c->max_t) * c->n_kv_heads * c->max_pages * 4, 256);
+        l->total += round_up((size_t)std::min(kMaxEntries, c->max_seqs * c->max_t) * c->n_kv_heads * round_up(c->max_pages, 4) * 4, 256);
     return KVQ_OK;
 }
 
@@ -396,6 +396,7 @@ kvq_status kvq_paged_select(kvq_paged* c, const kvq_paged_query* a, int* pages, 
     s.pages = pages;
     s.keys = reinterpret_cast<uint32_t*>(c->ws + c->off_keys);
     s.arrived = reinterpret_cast<int*>(c->ws + c->off_arrived);
+    s.key_stride = (int)round_up(c->cfg.max_pages, 4);
     s.keep = keep;
     s.n_first = n_first;
     s.n_last = n_last;

@@ -20,10 +20,11 @@ namespace kvq {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPages = 256;            // pages of a CTA
 constexpr int kKeep = 8192;            // keys that the pick holds in shared memory
+constexpr int kRank = 256;             // keys that are ranked one a thread
 constexpr int kBlock = 20;             // words of a query block's codes and scale
 
 // number of pages with a row that query row t sees, -1 for a bad length
@@ -49,20 +50,23 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* g_keys
     __shared__ int s_hist[256];
     __shared__ int s_gt[kWarps], s_eq[kWarps];
     __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
-    __shared__ uint32_t s_digit, s_thr, s_key[kThreads];
-    __shared__ int s_need, s_in, s_count, s_cut, s_idx[kThreads];
+    __shared__ uint32_t s_digit, s_thr, s_key[kRank];
+    __shared__ int s_need, s_in, s_count, s_cut, s_idx[kRank];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool in_smem = np <= kKeep;
     const int first = a.n_first, last = np - a.n_last;      // pages [first, last) compete
     uint32_t lo = 0xffffffffu, hi = 0u;
 #pragma unroll 4
-    for (int i = tid; i < np; i += kThreads) {
-        const uint32_t k = __ldcg(g_keys + i);
-        if (in_smem) s_keys[i] = k;
-        if (i >= first && i < last) {
-            lo = min(lo, k);
-            hi = max(hi, k);
-        }
+    for (int i = 4 * tid; i < np; i += 4 * kThreads) {      // (rows of keys are padded to four)
+        const uint4 v = __ldcg(reinterpret_cast<const uint4*>(g_keys + i));
+        if (in_smem) *reinterpret_cast<uint4*>(s_keys + i) = v;
+        const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u >= first && i + u < last) {
+                lo = min(lo, k[u]);
+                hi = max(hi, k[u]);
+            }
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
@@ -77,20 +81,29 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* g_keys
     }
     const uint32_t* keys = in_smem ? s_keys : g_keys;       // (written before the fence that the caller passed)
     auto key = [&](int i) { return keys[i] - lo; };
+    // f(index, key) of the competing pages, four neighbours a thread
+    auto each = [&](auto f) {
+#pragma unroll 2
+        for (int i = 4 * tid; i < last; i += 4 * kThreads) {
+            const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+            const uint32_t k[4] = {v.x - lo, v.y - lo, v.z - lo, v.w - lo};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u >= first && i + u < last) f(i + u, k[u]);
+        }
+    };
     int need = a.keep - a.n_first - a.n_last;               // of the competing pages
     uint32_t prefix = 0;
     int bits = hi > lo ? 32 - __clz(hi - lo) : 0;           // in which the keys differ
     int cut = np;                                           // of the keys that equal the threshold, those below this index
     while (bits > 0 && need > 0) {
         const int shift = max(0, bits - 8);
-        s_hist[tid] = 0;
+        if (tid < 256) s_hist[tid] = 0;
         __syncthreads();
         const uint32_t mask = bits >= 32 ? 0u : 0xffffffffu << bits;
-#pragma unroll 4
-        for (int i = first + tid; i < last; i += kThreads) {
-            const uint32_t k = key(i);
+        each([&](int, uint32_t k) {
             if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << (bits - shift)) - 1u)], 1);
-        }
+        });
         __syncthreads();
         if (warp == 0) {
             // lane l sums bins 255 - 8 l .. 248 - 8 l; the bin in which the count reaches `need`
@@ -127,20 +140,18 @@ __device__ __forceinline__ void pick(const SelectArgs& a, const uint32_t* g_keys
         prefix |= s_digit << shift;
         need = s_need;
         bits = shift;
-        if (s_in <= kThreads && bits > 0) {
+        if (s_in <= kRank && bits > 0) {
             // few keys share the digits: each thread ranks one of them
             if (tid == 0) s_count = 0;
             __syncthreads();
             const uint32_t m = 0xffffffffu << bits;
-#pragma unroll 4
-            for (int i = first + tid; i < last; i += kThreads) {
-                const uint32_t k = key(i);
+            each([&](int i, uint32_t k) {
                 if ((k & m) == prefix) {
                     const int at = atomicAdd(&s_count, 1);
                     s_key[at] = k;
                     s_idx[at] = i;
                 }
-            }
+            });
             __syncthreads();
             const int n = s_count;
             if (tid < n) {
@@ -253,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
         if (lane == 0) s_q[(size_t)i * kBlock + 16] = __float_as_uint(__fmul_rn(am, 1.0f / 127.0f));
     }
     __syncthreads();
-    uint32_t* keys = a.keys + ((long long)e * a.g.Hkv + kh) * a.g.max_pages;
+    uint32_t* keys = a.keys + ((long long)e * a.g.Hkv + kh) * a.key_stride;
 #pragma unroll 2
     for (int i = 0; i < IT; ++i) {
         const int p = p0 + (i * kWarps + warp) * PW + pl;
@@ -313,7 +324,7 @@ static cudaError_t launch_t(const SelectArgs& a, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = kernel_attrs_once(select_kernel<NB>, done, false);
     if (e != cudaSuccess) return e;
-    const size_t codes = (size_t)a.hpk * NB * kBlock * 4, keys = (size_t)std::min(a.g.max_pages, kKeep) * 4;
+    const size_t codes = (size_t)a.hpk * NB * kBlock * 4, keys = (size_t)std::min(a.key_stride, kKeep) * 4;
     const dim3 grid((unsigned)((a.g.max_pages + kPages - 1) / kPages), (unsigned)a.g.Hkv, (unsigned)(a.n_seq * a.T));
     return launch_dependent(select_kernel<NB>, grid, kThreads, std::max(codes, keys), s, a);
 }
