@@ -120,6 +120,8 @@ struct AppendArgs {
     void* q_out;
     long long k_stride, v_stride, q_stride;
     int Hq, bf16, rope_dim, interleaved;
+    int8_t* codes;         // bounds of the pages that one row each goes to, or NULL
+    float* scales;
 };
 cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cudaStream_t s);
 

@@ -326,10 +326,16 @@ kvq_status kvq_paged_append(kvq_paged* c, const void* k, long long k_stride, con
     a.bf16 = dtype == KVQ_BF16;
     a.rope_dim = c->cfg.rope_dim;
     a.interleaved = c->cfg.rope_interleaved;
+    // one row a sequence: the warp that stores it renews its page's bounds
+    const bool one = !starts && T == 1;
+    if (c->cfg.bounds && one) {
+        a.codes = c->codes;
+        a.scales = c->scales;
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_append(a, c->freqs, c->num_sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged append kernel");
-    return c->cfg.bounds ? bounds_of(c, a.r, s) : KVQ_OK;
+    return c->cfg.bounds && !one ? bounds_of(c, a.r, s) : KVQ_OK;
 }
 
 kvq_status kvq_paged_read(kvq_paged* c, void* k_out, void* v_out, kvq_dtype dtype, const int* tables, const int* lens,

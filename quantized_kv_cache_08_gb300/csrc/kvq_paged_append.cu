@@ -178,12 +178,62 @@ __device__ __forceinline__ void codes8(const float (&x)[8], float m, float d, in
     }
 }
 
+// Bounds of the 8 elements of lane c of a block as codes: rounded outward in
+// steps of ds = max |k| / 127.
+__device__ __forceinline__ void store_bounds(int8_t* codes, float* scales, long long at, int c, float ds, const float* mn, const float* mx) {
+    uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
+    if (ds > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float l = fminf(fmaxf(floorf(__fdiv_rn(mn[i], ds)), -127.f), 127.f);
+            const float u = fminf(fmaxf(ceilf(__fdiv_rn(mx[i], ds)), -127.f), 127.f);
+            lo[i >> 2] |= ((uint32_t)(int)l & 255u) << (8 * (i & 3));
+            hi[i >> 2] |= ((uint32_t)(int)u & 255u) << (8 * (i & 3));
+        }
+    }
+    int8_t* dst = codes + at * 64 + 8 * c;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(lo[0], lo[1]);
+    *reinterpret_cast<uint2*>(dst + 32) = make_uint2(hi[0], hi[1]);
+    if (c == 0) scales[at] = ds;
+}
+
+// Least and greatest of the 8 elements that lane (b, c) holds, over the first
+// `rows` rows of a page's head: 16 rows' codes and scales in flight at a time.
+template <int NB>
+__device__ __forceinline__ void fold_rows(const uint8_t* cell, long long step, int fp8, int rows, int b, int c, float (&mn)[8], float (&mx)[8]) {
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 16, cell += step) {
+        uint2 w[16], d[4];
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+            if (r0 + t < rows) w[t] = *reinterpret_cast<const uint2*>(cell + (b >> 1) * 1024 + t * 64 + c * 16 + (b & 1) * 8);
+        if (!fp8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] = *reinterpret_cast<const uint2*>(cell + 512 * NB + (j * NB + b) * 8);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            if (r0 + t >= rows) continue;
+            const int j = (t & 7) >> 1;
+            const uint32_t dw = (t >> 3) ? d[j].y : d[j].x;
+            const float s = fp8 ? 1.f : __half2float(__ushort_as_half((unsigned short)(dw >> (16 * (t & 1)))));
+            const uint32_t w2[2] = {w[t].x, w[t].y};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u = (w2[i >> 2] >> (8 * (i & 3))) & 255u;
+                const float x = fp8 ? __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)u, __NV_E4M3))) : (float)((int)u - 128) * s;
+                mn[i] = fminf(mn[i], x);
+                mx[i] = fmaxf(mx[i], x);
+            }
+        }
+    }
+}
+
 // One append CTA: tokens [TT blockIdx.x, + TT), row units blockIdx.y, + gridDim.y..
 // A unit is a warp's rows of one kind of one token: 64 / LR query heads (a lane
 // holds 8 elements and the 8 that they are rotated with), or 32 / LR key or
 // value heads (8 elements a lane, four lanes a block).
-template <int LR, bool BF16>
-__global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
+template <int LR, bool BF16, bool BOUNDS>
+__global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
     extern __shared__ float2 s_cs[];               // [TT][rope_dim / 2]
     __shared__ Place s_place[16];
     constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR, QPW = 64 / LR, QL = LR / 2;
@@ -280,13 +330,25 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) append_kernel(const __
         const bool is_v = u >= uq + uk;
         const int h = (is_v ? u - uk - uq : u - uq) * JPW + lane / LR;
         const bool on = h < a.g.Hkv && pl.cell >= 0;
-        float x[8];
+        float x[8], mn[8], mx[8];
+        uint8_t* cell = a.g.pool + pl.cell + (long long)h * a.g.cells_per_page() * a.g.cell_bytes;
+        const int in = pl.pos & (a.g.page_rows - 1);       // row of the page
+        if constexpr (BOUNDS) {                            // the page's earlier rows, while this one's elements are on their way
+            if (!is_v) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    mn[i] = __builtin_huge_valf();
+                    mx[i] = -__builtin_huge_valf();
+                }
+                fold_rows<NB>(cell - (long long)(in >> 4) * a.g.cell_bytes, a.g.cell_bytes, a.g.fp8, on ? in : 0, b, c, mn, mx);
+            }
+        }
         floats8(next, x);
         fetch(u + du);
-        uint8_t* cell = a.g.pool + pl.cell + (long long)h * a.g.cells_per_page() * a.g.cell_bytes;
         if (!is_v) {
             rotate8(x, e0, a.rope_dim, a.interleaved, cs, lane);
             uint32_t w2[2] = {0u, 0u};
+            float kd = 0.f;
             if (a.g.fp8) {
 #pragma unroll
                 for (int i = 0; i < 8; i += 2)
@@ -299,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) append_kernel(const __
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 const unsigned short db = half_quotient(m, 0.f, 127.f);
                 int code[8];
-                codes8<false>(x, 0.f, __half2float(__ushort_as_half(db)), code);
+                kd = __half2float(__ushort_as_half(db));
+                codes8<false>(x, 0.f, kd, code);
 #pragma unroll
                 for (int i = 0; i < 8; i += 4)
                     w2[i >> 2] = __byte_perm(__byte_perm(code[i], code[i + 1], 0x0040), __byte_perm(code[i + 2], code[i + 3], 0x0040), 0x5410) ^ 0x80808080u;
@@ -307,6 +370,22 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) append_kernel(const __
                     *reinterpret_cast<unsigned short*>(cell + 512 * NB + (j * NB + b) * 8 + i4 * 2) = db;
             }
             if (on) *reinterpret_cast<uint2*>(cell + (b >> 1) * 1024 + t * 64 + c * 16 + (b & 1) * 8) = make_uint2(w2[0], w2[1]);
+            if constexpr (BOUNDS) {                // this row's values as stored, from registers
+                float am = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t u = (w2[i >> 2] >> (8 * (i & 3))) & 255u;
+                    const float y = a.g.fp8 ? __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)u, __NV_E4M3)))
+                                            : (float)((int)u - 128) * kd;
+                    mn[i] = fminf(mn[i], y);
+                    mx[i] = fmaxf(mx[i], y);
+                    am = fmaxf(am, fmaxf(fabsf(mn[i]), fabsf(mx[i])));
+                }
+                am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+                am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+                const long long page = (pl.cell - (long long)(in >> 4) * a.g.cell_bytes) / a.g.page_bytes;
+                if (on) store_bounds(a.codes, a.scales, (page * a.g.Hkv + h) * NB + b, c, __fmul_rn(am, 1.0f / 127.0f), mn, mx);
+            }
             continue;
         }
         if (a.g.fp8) {
@@ -319,19 +398,19 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) append_kernel(const __
             }
             continue;
         }
-        float mn = x[0], mx = x[0];
+        float least = x[0], most = x[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) {
-            mn = fminf(mn, x[i]);
-            mx = fmaxf(mx, x[i]);
+            least = fminf(least, x[i]);
+            most = fmaxf(most, x[i]);
         }
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float range = mx - mn, back = range - mx;
-        const unsigned short db = half_quotient(range, (mx - (range - back)) - (mn + back), 31.f);
-        const unsigned short mb = __half_as_ushort(__float2half_rn(mn));
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, 2));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        const float range = most - least, back = range - most;
+        const unsigned short db = half_quotient(range, (most - (range - back)) - (least + back), 31.f);
+        const unsigned short mb = __half_as_ushort(__float2half_rn(least));
         int code[8];
         codes8<true>(x, __half2float(__ushort_as_half(mb)), __half2float(__ushort_as_half(db)), code);
         uint32_t unit[2], nib[2];
@@ -478,22 +557,7 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsArgs a) {
         const int b = 2 * bp + e;
         const float ds = __fmul_rn(am[e], 1.0f / 127.0f);
         const long long at = (page * a.g.Hkv + h) * NB + b;
-        if (g8 == 0) {
-            uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
-            if (ds > 0.f) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float l = fminf(fmaxf(floorf(__fdiv_rn(mn[8 * e + i], ds)), -127.f), 127.f);
-                    const float u = fminf(fmaxf(ceilf(__fdiv_rn(mx[8 * e + i], ds)), -127.f), 127.f);
-                    lo[i >> 2] |= ((uint32_t)(int)l & 255u) << (8 * (i & 3));
-                    hi[i >> 2] |= ((uint32_t)(int)u & 255u) << (8 * (i & 3));
-                }
-            }
-            int8_t* dst = a.codes + at * 64 + 8 * c;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(lo[0], lo[1]);
-            *reinterpret_cast<uint2*>(dst + 32) = make_uint2(hi[0], hi[1]);
-            if (c == 0) a.scales[at] = ds;
-        }
+        if (g8 == 0) store_bounds(a.codes, a.scales, at, c, ds, &mn[8 * e], &mx[8 * e]);
     }
 }
 
@@ -510,13 +574,16 @@ cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cuda
     const int gy = std::max(1, std::min(most, (2 * num_sms + gx - 1) / gx));
     const size_t smem = (size_t)TT * (a.rope_dim / 2) * sizeof(float2);
     const dim3 grid((unsigned)gx, (unsigned)gy);
-    auto run = [&](auto b) {
-        constexpr bool B = decltype(b)::value;
-        if (a.g.D == 64) return launch_dependent(append_kernel<8, B>, grid, kThreads, smem, s, a, f, TT);
-        if (a.g.D == 128) return launch_dependent(append_kernel<16, B>, grid, kThreads, smem, s, a, f, TT);
-        return launch_dependent(append_kernel<32, B>, grid, kThreads, smem, s, a, f, TT);
+    auto run = [&](auto b, auto with_bounds) {
+        constexpr bool B = decltype(b)::value, W = decltype(with_bounds)::value;
+        if (a.g.D == 64) return launch_dependent(append_kernel<8, B, W>, grid, kThreads, smem, s, a, f, TT);
+        if (a.g.D == 128) return launch_dependent(append_kernel<16, B, W>, grid, kThreads, smem, s, a, f, TT);
+        return launch_dependent(append_kernel<32, B, W>, grid, kThreads, smem, s, a, f, TT);
     };
-    return a.bf16 ? run(std::true_type{}) : run(std::false_type{});
+    const std::true_type yes;
+    const std::false_type no;
+    if (a.codes) return a.bf16 ? run(yes, yes) : run(no, yes);
+    return a.bf16 ? run(yes, no) : run(no, no);
 }
 
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t s) {

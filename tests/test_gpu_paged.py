@@ -322,6 +322,28 @@ def test_bounds_and_selection_match_the_oracle(fmt, D, page):
     assert p.dev.device_error() == 0
 
 
+@pytest.mark.parametrize("fmt,D,Hkv,page,dtype", [(Q8, 64, 3, 16, BF), (Q8, 128, 2, 32, F32), (F8, 256, 1, 64, BF),
+                                                  (Q8, 256, 2, 16, F32), (F8, 64, 5, 32, F32)])
+def test_bounds_of_single_row_appends(fmt, D, Hkv, page, dtype):
+    """Steps of one row over a page's end leave what going over the pages again gives."""
+    p = PagedPair(4, Hkv, D, Hkv, page=page, max_pages=4, fmt=fmt, bounds=True, rope_dim=32, seed=D + page)
+    k, v = (p.randn(4, page, Hkv, D).to(dtype).cuda() for _ in range(2))
+    lens = np.array([page - 3, 5, 0, 2 * page - 1])
+    p.dev.append(k[:, :1].repeat(1, 2 * page, 1, 1), v[:, :1].repeat(1, 2 * page, 1, 1), p.tables, i32([2 * page] * 4))
+    for step in range(page):
+        lens += 1
+        kk = (k[:, step:step + 1] * (1 + step % 5)).contiguous()
+        p.dev.append(kk, v[:, step:step + 1].contiguous(), p.tables, i32(lens.tolist()))
+        got = p.dev.bounds.clone()
+        p.dev.update_bounds(p.tables, i32(lens.tolist()), 1)
+        assert torch.equal(got, p.dev.bounds), step
+    # a length of 0 and a bad page write nothing
+    p.dev.append(kk, v[:, :1].contiguous(), p.tables, i32([0] * 4))
+    assert p.dev.device_error() == 1
+    p.dev.append(kk, v[:, :1].contiguous(), torch.full_like(p.tables, -1), i32([1] * 4))
+    assert p.dev.device_error() == 1 and torch.equal(got, p.dev.bounds)
+
+
 def test_scores_bound_the_coded_products_and_ties_go_low():
     p = sparse_pair()
     codes, ds = host_bounds(p)
