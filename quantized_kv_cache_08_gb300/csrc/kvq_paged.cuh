@@ -210,7 +210,7 @@ struct PlanEntry {
     long long work;
     int keys, nc, c0, nq, rows, lo;
 };
-int split_tile(bool bf16, int most_queries);
+int split_tile(int NB, bool bf16, int most_queries);
 int split_warps(int NB, int tile);
 cudaError_t launch_split(const SplitArgs& a, cudaStream_t s);
 cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s);

@@ -176,7 +176,7 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     // queries of a key at most: the tile kernel takes the bf16 groups that have
     // more than a slice
     const int own = lists ? a.hpk : a.hpk * q->T;
-    a.tile = split_tile(a.bf16, own);
+    a.tile = split_tile(a.g.NB(), a.bf16, own);
     a.tiles = n_groups > 0 && a.bf16 && q->n_seq * own > a.tile;
     const int most = n_groups > 0 ? (a.tiles ? a.tile : q->n_seq * own) : own;
     // many keys: four warps a group, for a fragment's end and start are hidden

@@ -42,17 +42,19 @@ namespace paged {
 namespace {
 
 
-// Query tiles: 8 or 16 bf16 queries, or 8 of f32 in two parts
-enum Tile { kT8 = 0, kT16 = 1, kF32 = 2 };
+// Query tiles: 8 or 16 bf16 queries, or 8 or 16 of f32 in two parts
+enum Tile { kT8 = 0, kT16 = 1, kF32 = 2, kF32W = 3 };
+template <int TILE>
+constexpr bool two_parts() { return TILE == kF32 || TILE == kF32W; }
 
 // Warps of a CTA (one CTA an SM): as many as the accumulators leave registers for
 template <int NB, int TILE>
-constexpr int warps_of() { return NB == 8 ? 8 : NB == 4 && TILE == kT16 ? 12 : 16; }
+constexpr int warps_of() { return NB == 8 ? 8 : NB == 4 && (TILE == kT16 || TILE == kF32W) ? 12 : 16; }
 // Groups of four warps, which work on ranges of their own where there is enough work
 template <int NB, int TILE>
 constexpr int groups_of() { return warps_of<NB, TILE>() / 4; }
 template <int TILE>
-constexpr int queries_of() { return TILE == kT16 ? 16 : 8; }
+constexpr int queries_of() { return TILE == kT16 || TILE == kF32W ? 16 : 8; }
 
 // c = a b + z (z: four zeros that stay in registers, where a constant would be
 // written to four new ones for each product)
@@ -85,12 +87,12 @@ __device__ __forceinline__ float load_q(const void* q, long long idx, int bf16) 
 
 template <int NB, bool F8, int TILE>
 struct Acc {
-    static constexpr int NQ = TILE == kT16 ? 2 : 1;       // groups of 8 queries
+    static constexpr int NQ = queries_of<TILE>() / 8;     // groups of 8 queries
     // O^T tile 2b + rp of a group: rows g / g + 8 are elements 32b + 4g + 2rp and
     // + 1, columns 2j, 2j + 1 queries: [0] (el, 2j) [1] (el, 2j+1) [2] (el+1, 2j) ..
     float o[NQ][2 * NB][4];
     float m[NQ], l[NQ];                                   // query g (+ 8): reference, sum of p
-    float mt[TILE == kF32 && !F8 ? NB : 1];               // sum p (m + 16 d) of query g
+    float mt[NQ][two_parts<TILE>() && !F8 ? NB : 1];      // sum p (m + 16 d) of query g (+ 8)
 };
 
 // The queries of a fragment: factor of a score, rows seen
@@ -141,19 +143,28 @@ template <int NB, bool F8, int TILE>
 __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int row0, const uint8_t* __restrict__ qs,
                                           const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane, const float (&zero)[4],
                                           uint32_t magic, uint32_t exps, Acc<NB, F8, TILE>& acc) {
-    constexpr bool HL = TILE == kF32;
+    constexpr bool HL = two_parts<TILE>();
     constexpr int NQ = Acc<NB, F8, TILE>::NQ;
     const int j = lane & 3;
     const bool edge = row0 < lr.lo_max || row0 + 16 > lr.hi_min;
     if (edge) clear_rows<NB, F8>(cell, row0, lr, lane);
     // ---- scores
-    float sc[2][4];
+    float sc[2][2 * NQ];                                  // [rows 2j + 8t + i][2 r + i], query g + 8 r
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[t][i] = 0.f;
-    auto q_frag = [&](int step) {
-        return *reinterpret_cast<const uint4*>(qs + (step * 32 + lane) * 16);
+        for (int i = 0; i < 2 * NQ; ++i) sc[t][i] = 0.f;
+    // query fragments: 16 queries, or (two parts) 8 high parts over their 8 low ones
+    constexpr int QF = HL ? NQ : 1;
+    float raw[QF][2][4];                                  // E4M3: the products themselves
+#pragma unroll
+    for (int r = 0; r < QF; ++r)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[r][t][i] = 0.f;
+    auto q_frag = [&](int r, int step) {
+        return *reinterpret_cast<const uint4*>(qs + ((r * 2 * NB + step) * 32 + lane) * 16);
     };
 #pragma unroll
     for (int bp = 0; bp < NB / 2; ++bp) {
@@ -165,38 +176,51 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int b = 2 * bp + e;
-            const uint4 a0 = q_frag(2 * b), a1 = q_frag(2 * b + 1);
+            uint4 a0[QF], a1[QF];
+#pragma unroll
+            for (int r = 0; r < QF; ++r) {
+                a0[r] = q_frag(r, 2 * b);
+                a1[r] = q_frag(r, 2 * b + 1);
+            }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const uint32_t w0 = e ? kk[t].z : kk[t].x, w1 = e ? kk[t].w : kk[t].y;
                 if constexpr (F8) {
-                    mma_f16(sc[t], a0, f8_pair(w0), f8_pair(w0 >> 16));
-                    mma_f16(sc[t], a1, f8_pair(w1), f8_pair(w1 >> 16));
-                } else {
-                    float c[4];
-                    mma_f16_new(c, a0, k_pair(w0, 0x4140u, exps), k_pair(w0, 0x4342u, exps), zero);
-                    mma_f16(c, a1, k_pair(w1, 0x4140u, exps), k_pair(w1, 0x4342u, exps));
-                    const float2 d = __half22float2(as_h2(e ? (t ? ks.w : ks.z) : (t ? ks.y : ks.x)));
-                    if constexpr (HL) {
-                        c[0] += c[2];
-                        c[1] += c[3];
+                    const uint32_t k0 = f8_pair(w0), k1 = f8_pair(w0 >> 16), k2 = f8_pair(w1), k3 = f8_pair(w1 >> 16);
+#pragma unroll
+                    for (int r = 0; r < QF; ++r) {
+                        mma_f16(raw[r][t], a0[r], k0, k1);
+                        mma_f16(raw[r][t], a1[r], k2, k3);
                     }
-                    sc[t][0] = fmaf(c[0], d.x, sc[t][0]);
-                    sc[t][1] = fmaf(c[1], d.y, sc[t][1]);
-                    if constexpr (TILE == kT16) {
-                        sc[t][2] = fmaf(c[2], d.x, sc[t][2]);
-                        sc[t][3] = fmaf(c[3], d.y, sc[t][3]);
+                } else {
+                    const uint32_t k0 = k_pair(w0, 0x4140u, exps), k1 = k_pair(w0, 0x4342u, exps);
+                    const uint32_t k2 = k_pair(w1, 0x4140u, exps), k3 = k_pair(w1, 0x4342u, exps);
+                    const float2 d = __half22float2(as_h2(e ? (t ? ks.w : ks.z) : (t ? ks.y : ks.x)));
+#pragma unroll
+                    for (int r = 0; r < QF; ++r) {
+                        float c[4];
+                        mma_f16_new(c, a0[r], k0, k1, zero);
+                        mma_f16(c, a1[r], k2, k3);
+                        if constexpr (HL) {
+                            c[0] += c[2];
+                            c[1] += c[3];
+                        }
+                        sc[t][2 * r] = fmaf(c[0], d.x, sc[t][2 * r]);
+                        sc[t][2 * r + 1] = fmaf(c[1], d.y, sc[t][2 * r + 1]);
+                        if constexpr (TILE == kT16) {
+                            sc[t][2] = fmaf(c[2], d.x, sc[t][2]);
+                            sc[t][3] = fmaf(c[3], d.y, sc[t][3]);
+                        }
                     }
                 }
             }
         }
     }
-    if constexpr (HL && F8) {
+    if constexpr (F8) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            sc[t][0] += sc[t][2];
-            sc[t][1] += sc[t][3];
-        }
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 2 * NQ; ++i) sc[t][i] = HL ? raw[i / 2 % QF][t][i & 1] + raw[i / 2 % QF][t][2 + (i & 1)] : raw[0][t][i];
     }
     // ---- scale, cap, mask; the reference
     float top[NQ];
@@ -239,7 +263,7 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
             }
             if constexpr (HL && !F8) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b) acc.mt[b] *= al;
+                for (int b = 0; b < NB; ++b) acc.mt[r][b] *= al;
             }
             const float al0 = __shfl_sync(0xffffffffu, al, 8 * j), al1 = __shfl_sync(0xffffffffu, al, 8 * j + 4);
 #pragma unroll
@@ -263,17 +287,19 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
     }
     // ---- values
     uint32_t pb[NQ][2];                                   // B fragments: rows (2j, 2j+1), (2j+8, 2j+9) of query g (+ 8)
-    uint32_t pl[2];                                       // low parts (E4M3 rows, f32 queries)
+    uint32_t pl[NQ][2];                                   // low parts (E4M3 rows, f32 queries)
 #pragma unroll
     for (int r = 0; r < NQ; ++r)
 #pragma unroll
         for (int t = 0; t < 2; ++t) pb[r][t] = as_u32(__floats2half2_rn(sc[t][2 * r], sc[t][2 * r + 1]));
     if constexpr (HL && F8) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const float2 f = __half22float2(as_h2(pb[0][t]));
-            pl[t] = as_u32(__floats2half2_rn(sc[t][0] - f.x, sc[t][1] - f.y));
-        }
+        for (int r = 0; r < NQ; ++r)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float2 f = __half22float2(as_h2(pb[r][t]));
+                pl[r][t] = as_u32(__floats2half2_rn(sc[t][2 * r] - f.x, sc[t][2 * r + 1] - f.y));
+            }
     }
     if constexpr (F8) {
         uint4 vv[NB];
@@ -289,7 +315,9 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
                 const uint4 va = make_uint4(f8_pair(x), f8_pair(x >> 16), f8_pair(y), f8_pair(y >> 16));
 #pragma unroll
                 for (int r = 0; r < NQ; ++r) mma_f16(acc.o[r][2 * b + rp], va, pb[r][0], pb[r][1]);
-                if constexpr (HL) mma_f16(acc.o[0][2 * b + rp], va, pl[0], pl[1]);
+                if constexpr (HL)
+#pragma unroll
+                    for (int r = 0; r < NQ; ++r) mma_f16(acc.o[r][2 * b + rp], va, pl[r][0], pl[r][1]);
             }
         }
     } else {
@@ -323,17 +351,23 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
             } else {
                 const float2 d0 = __half22float2(as_h2(dm.x)), d1 = __half22float2(as_h2(dm.y));
                 const float2 m0 = __half22float2(as_h2(dm.z)), m1 = __half22float2(as_h2(dm.w));
-                const float x0 = sc[0][0] * d0.x, x1 = sc[0][1] * d0.y, x2 = sc[1][0] * d1.x, x3 = sc[1][1] * d1.y;
-                float t = acc.mt[b];
-                t = fmaf(sc[0][0], fmaf(16.f, d0.x, m0.x), t);
-                t = fmaf(sc[0][1], fmaf(16.f, d0.y, m0.y), t);
-                t = fmaf(sc[1][0], fmaf(16.f, d1.x, m1.x), t);
-                acc.mt[b] = fmaf(sc[1][1], fmaf(16.f, d1.y, m1.y), t);
-                const __nv_bfloat162 h0 = __floats2bfloat162_rn(x0, x1), h1 = __floats2bfloat162_rn(x2, x3);
-                const float2 f0 = __bfloat1622float2(h0), f1 = __bfloat1622float2(h1);
-                const uint32_t ph0 = as_u32(h0), ph1 = as_u32(h1);
-                const uint32_t pl0 = as_u32(__floats2bfloat162_rn(x0 - f0.x, x1 - f0.y));
-                const uint32_t pl1 = as_u32(__floats2bfloat162_rn(x2 - f1.x, x3 - f1.y));
+                uint32_t ph[NQ][2], pl[NQ][2];             // p d in two bf16 parts
+#pragma unroll
+                for (int r = 0; r < NQ; ++r) {
+                    const float p0 = sc[0][2 * r], p1 = sc[0][2 * r + 1], p2 = sc[1][2 * r], p3 = sc[1][2 * r + 1];
+                    const float x0 = p0 * d0.x, x1 = p1 * d0.y, x2 = p2 * d1.x, x3 = p3 * d1.y;
+                    float t = acc.mt[r][b];
+                    t = fmaf(p0, fmaf(16.f, d0.x, m0.x), t);
+                    t = fmaf(p1, fmaf(16.f, d0.y, m0.y), t);
+                    t = fmaf(p2, fmaf(16.f, d1.x, m1.x), t);
+                    acc.mt[r][b] = fmaf(p3, fmaf(16.f, d1.y, m1.y), t);
+                    const __nv_bfloat162 h0 = __floats2bfloat162_rn(x0, x1), h1 = __floats2bfloat162_rn(x2, x3);
+                    const float2 f0 = __bfloat1622float2(h0), f1 = __bfloat1622float2(h1);
+                    ph[r][0] = as_u32(h0);
+                    ph[r][1] = as_u32(h1);
+                    pl[r][0] = as_u32(__floats2bfloat162_rn(x0 - f0.x, x1 - f0.y));
+                    pl[r][1] = as_u32(__floats2bfloat162_rn(x2 - f1.x, x3 - f1.y));
+                }
                 auto code = [&](auto R, int n) {
                     constexpr int r = decltype(R)::value;
                     uint32_t c = v_codes<r>(u[n], nb[n / 4], n % 4, magic);
@@ -344,11 +378,17 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
                 const std::integral_constant<int, 2> r2{};
                 const std::integral_constant<int, 3> r3{};
                 const uint4 v0 = make_uint4(code(r0, n0), code(r1, n0), code(r0, n1), code(r1, n1));
-                mma_bf16(acc.o[0][2 * b], v0, ph0, ph1);
-                mma_bf16(acc.o[0][2 * b], v0, pl0, pl1);
+#pragma unroll
+                for (int r = 0; r < NQ; ++r) {
+                    mma_bf16(acc.o[r][2 * b], v0, ph[r][0], ph[r][1]);
+                    mma_bf16(acc.o[r][2 * b], v0, pl[r][0], pl[r][1]);
+                }
                 const uint4 v1 = make_uint4(code(r2, n0), code(r3, n0), code(r2, n1), code(r3, n1));
-                mma_bf16(acc.o[0][2 * b + 1], v1, ph0, ph1);
-                mma_bf16(acc.o[0][2 * b + 1], v1, pl0, pl1);
+#pragma unroll
+                for (int r = 0; r < NQ; ++r) {
+                    mma_bf16(acc.o[r][2 * b + 1], v1, ph[r][0], ph[r][1]);
+                    mma_bf16(acc.o[r][2 * b + 1], v1, pl[r][0], pl[r][1]);
+                }
             }
         }
     }
@@ -363,7 +403,7 @@ constexpr size_t kRingEnd = 220 * 1024;
 template <int NB, int TILE>
 struct Smem {
     static constexpr int D = NB * 32;
-    static constexpr size_t qs = (size_t)(D / 16) * 512;
+    static constexpr size_t qs = (size_t)(D / 16) * 512 * (TILE == kF32W ? 2 : 1);
     static constexpr size_t all_qs = groups_of<NB, TILE>() * qs;
     static constexpr size_t comb = (size_t)warps_of<NB, TILE>() / 2 * queries_of<TILE>() * (D + 4) * 4;
     __host__ __device__ static constexpr size_t ring(int E) { return (all_qs + comb + (size_t)(E + 1) * sizeof(PlanEntry) + 127) / 128 * 128; }
@@ -568,7 +608,7 @@ template <int NB, bool F8, int TILE>
 __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(const __grid_constant__ SplitArgs a, const int stages) {
     constexpr int D = NB * 32, D4 = D / 4;
     constexpr int kWarps = warps_of<NB, TILE>(), kThreads = kWarps * 32;
-    constexpr bool HL = TILE == kF32;
+    constexpr bool HL = two_parts<TILE>();
     constexpr int QPI = queries_of<TILE>(), NQ = QPI / 8;
     constexpr int CELL = NB * (F8 ? 1024 : 928);
     constexpr int PAD = D + 4;                        // row stride of the joins' sums: lanes of a store in different banks
@@ -640,7 +680,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             for (int b = 0; b < NB; ++b) {
                 const float y = qv[i][b] * up;
                 const __half hi = __float2half_rn(y);
-                const int at = (2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
+                const int at = ((HL ? (r >> 3) * 2 * NB : 0) + 2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
                 __half* dst = reinterpret_cast<__half*>(qs + at * 16);
                 if (TILE == kT8) {                         // (rows 8 .. 15 of the tile are zeros)
                     dst[2 * reg + half] = hi;
@@ -821,7 +861,9 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                 for (int i = 0; i < 4; ++i) acc.o[r][n][i] = 0.f;
         }
 #pragma unroll
-        for (int b = 0; b < (HL && !F8 ? NB : 1); ++b) acc.mt[b] = 0.f;
+        for (int r = 0; r < NQ; ++r)
+#pragma unroll
+            for (int b = 0; b < (HL && !F8 ? NB : 1); ++b) acc.mt[r][b] = 0.f;
 
         // ---- its cells, warp by warp
         for (int c = f.ca + gwarp; c < f.cb; c += gw) {
@@ -851,19 +893,21 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         }
         if constexpr (HL && !F8) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float t = acc.mt[b];
-                t += __shfl_xor_sync(0xffffffffu, t, 1);
-                t += __shfl_xor_sync(0xffffffffu, t, 2);
-                const float t0 = __shfl_sync(0xffffffffu, t, 8 * j), t1 = __shfl_sync(0xffffffffu, t, 8 * j + 4);
+            for (int r = 0; r < NQ; ++r)
 #pragma unroll
-                for (int rp = 0; rp < 2; ++rp) {
-                    acc.o[0][2 * b + rp][0] += t0;
-                    acc.o[0][2 * b + rp][1] += t1;
-                    acc.o[0][2 * b + rp][2] += t0;
-                    acc.o[0][2 * b + rp][3] += t1;
+                for (int b = 0; b < NB; ++b) {
+                    float t = acc.mt[r][b];
+                    t += __shfl_xor_sync(0xffffffffu, t, 1);
+                    t += __shfl_xor_sync(0xffffffffu, t, 2);
+                    const float t0 = __shfl_sync(0xffffffffu, t, 8 * j), t1 = __shfl_sync(0xffffffffu, t, 8 * j + 4);
+#pragma unroll
+                    for (int rp = 0; rp < 2; ++rp) {
+                        acc.o[r][2 * b + rp][0] += t0;
+                        acc.o[r][2 * b + rp][1] += t1;
+                        acc.o[r][2 * b + rp][2] += t0;
+                        acc.o[r][2 * b + rp][3] += t1;
+                    }
                 }
-            }
         }
         sync_group();
         const int w0 = warp - gwarp;
@@ -1064,6 +1108,8 @@ cudaError_t launch_split_t(const SplitArgs& a, cudaStream_t s) {
 
 template <int NB, bool F8>
 cudaError_t launch_split_f(const SplitArgs& a, cudaStream_t s) {
+    if constexpr (NB < 8)
+        if (!a.bf16 && a.tile == 16) return launch_split_t<NB, F8, kF32W>(a, s);
     if (!a.bf16) return launch_split_t<NB, F8, kF32>(a, s);
     return a.tile == 8 ? launch_split_t<NB, F8, kT8>(a, s) : launch_split_t<NB, F8, kT16>(a, s);
 }
@@ -1075,14 +1121,19 @@ cudaError_t launch_split_nb(const SplitArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int split_tile(bool bf16, int most_queries) { return bf16 && most_queries > 8 ? 16 : 8; }
+// f32 queries of head_dim 256 stay at 8: two parts of 16 leave few registers and
+// stages (16k rows, 4 KV heads of 8 x 4 queries: 43 us, 8: 38), where smaller heads
+// gain (8 sequences of 16k rows, 8 KV heads of 128, 16 queries: 102 us, 8: 119)
+int split_tile(int NB, bool bf16, int most_queries) { return most_queries > 8 && (bf16 || NB < 8) ? 16 : 8; }
 
 int split_warps(int NB, int tile) {
     if (tile == 16) return NB == 2 ? warps_of<2, kT16>() : NB == 4 ? warps_of<4, kT16>() : warps_of<8, kT16>();
     return NB == 2 ? warps_of<2, kT8>() : NB == 4 ? warps_of<4, kT8>() : warps_of<8, kT8>();
 }
 static_assert(warps_of<2, kT8>() == warps_of<2, kF32>() && warps_of<4, kT8>() == warps_of<4, kF32>() &&
-              warps_of<8, kT8>() == warps_of<8, kF32>(), "tiles of 8 queries share a CTA size");
+              warps_of<8, kT8>() == warps_of<8, kF32>() && warps_of<2, kT16>() == warps_of<2, kF32W>() &&
+              warps_of<4, kT16>() == warps_of<4, kF32W>(),
+              "tiles of as many queries share a CTA size");
 
 cudaError_t launch_split(const SplitArgs& a, cudaStream_t s) {
     switch (a.g.NB()) {
