@@ -134,6 +134,31 @@ def test_packed_rows_outside_the_starts_are_left_alone():
     assert p.dev.device_error() == 0
 
 
+@pytest.mark.parametrize("fmt", [Q8, F8])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("D,Hkv,page,rot,inter", [(64, 3, 16, 64, False), (128, 2, 32, 96, False), (256, 1, 64, 256, False),
+                                                  (64, 1, 128, 32, True), (128, 5, 16, 0, False), (256, 2, 32, 48, True)])
+@pytest.mark.parametrize("ctx,counts", [([3, 5, 0, 8, 16, 15], [37, 0, 1, 8, 64, 9]), ([0, 7, 1, 2, 30, 0, 3, 9], [70, 1, 1, 2, 0, 3, 1, 2]),
+                                        ([0], [16]), ([9, 24], [7, 40])])
+def test_many_rows_a_sequence_write_what_single_steps_write(fmt, dtype, D, Hkv, page, rot, inter, ctx, counts):
+    n, Hq = len(ctx), 3 * Hkv
+    kw = dict(page=page, max_pages=-(-96 // page), fmt=fmt, rope_dim=rot, rope_interleaved=inter)
+    a, b = (PagedPair(n, Hkv, D, Hq, seed=3, **kw) for _ in range(2))
+    front, rows = 2, sum(counts)
+    k, v, q = (a.randn(front + rows + 3, H, D).to(dtype).cuda() for H in (Hkv, Hkv, Hq))
+    starts = front + np.concatenate([[0], np.cumsum(counts)])
+    lens = np.array(ctx) + np.array(counts)
+    out = torch.full_like(q, 7.0)
+    a.dev.append(k, v, a.tables, i32(lens.tolist()), starts=i32(starts.tolist()), q=q, q_out=out)
+    want = torch.full_like(q, 7.0)
+    for i in range(n):
+        for r in range(counts[i]):
+            at = slice(int(starts[i]) + r, int(starts[i]) + r + 1)
+            want[at] = b.dev.append(k[at][None], v[at][None], b.tables[i:i + 1], i32([ctx[i] + r + 1]), q=q[at][None])[0]
+    assert torch.equal(a.dev.pool, b.dev.pool) and torch.equal(out, want)
+    assert a.dev.device_error() == 0 and b.dev.device_error() == 0
+
+
 # ------------------------------------------------------------------ decode
 
 LENS = [0, 1, 15, 16, 17, 40, 63]
