@@ -488,6 +488,48 @@ def test_graph_replays_follow_lengths_tables_and_inputs():
     assert p.dev.device_error() == 0
 
 
+def test_captured_steps_over_a_shared_prefix():
+    """Append, shared decode and dense decode in one graph, with more queries a group than a
+    slice holds: each replay sees its own step's rows and queries."""
+    p, starts, prefix = shared_case(sizes=[9, 7], prefix=[200, 64], suffix=[1, 9, 30], Hkv=2, Hq=8, D=64)
+    n, steps = p.n, 12
+    k, v = torch.zeros(n, 1, 2, 64, device="cuda", dtype=BF), torch.zeros(n, 1, 2, 64, device="cuda", dtype=BF)
+    q, lens = torch.zeros(n, 1, 8, 64, device="cuda", dtype=BF), p.lens()
+    data = [(p.randn(n, 1, 2, 64).to(BF).cuda(), p.randn(n, 1, 2, 64).to(BF).cuda(), p.randn(n, 1, 8, 64).to(BF).cuda())
+            for _ in range(steps)]
+    pool, first = p.dev.pool.clone(), lens.clone()
+
+    def step():
+        r = p.dev.append(k, v, p.tables, lens, q=q)
+        return p.dev.decode_shared(r, p.tables, lens, starts, prefix), p.dev.decode(r, p.tables, lens)
+
+    eager = []
+    for a, b, c in data:
+        k.copy_(a), v.copy_(b), q.copy_(c), lens.add_(1)
+        torch.cuda.synchronize()
+        eager.append([x.clone() for x in step()])
+        torch.cuda.synchronize()
+    # two steps a graph, so that kernels of one follow those of the other with nothing between
+    ins = [[torch.zeros_like(x) for x in (k, v, q)] + [torch.zeros_like(lens)] for _ in range(2)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = []
+        for a, b, c, m in ins:
+            r = p.dev.append(a, b, p.tables, m, q=c)
+            outs.append((p.dev.decode_shared(r, p.tables, m, starts, prefix), p.dev.decode(r, p.tables, m)))
+    p.dev.pool.copy_(pool)
+    for i in range(0, steps, 2):
+        for u in range(2):
+            for dst, src in zip(ins[u], (*data[i + u], first + (i + u + 1))):
+                dst.copy_(src)
+        g.replay()
+        for u in range(2):
+            assert torch.equal(outs[u][0], eager[i + u][0]) and torch.equal(outs[u][1], eager[i + u][1]), i + u
+    for got, want in zip(eager[-1], eager[-1][::-1]):
+        assert (got.float() - want.float()).abs().max() < 0.1
+    assert p.dev.device_error() == 0
+
+
 def test_two_caches_on_two_streams():
     a, b = PagedPair(2, 1, 64, 4, page=16, max_pages=4, seed=1), PagedPair(3, 2, 128, 4, page=32, max_pages=4, seed=2)
     for p in (a, b):
