@@ -225,6 +225,8 @@ class PagedKVCache:
         self.pool = self._buffer(pool, sz.pool, "pool")
         self.bounds = self._buffer(bounds_buf, sz.bounds, "bounds_buf") if bounds else None
         self.workspace = torch.empty(sz.workspace, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream(dev))   # the workspace's memory may still be in use there
         with torch.cuda.device(dev):
             self.handle = B.kvq_paged_alloc(self.cfg, self.pool.data_ptr(),
                                             self.bounds.data_ptr() if bounds else None, self.workspace.data_ptr(),
@@ -291,9 +293,12 @@ class PagedKVCache:
             B._check(st)
 
     def _new(self, shape, dtype, stream):
-        out = torch.empty(shape, dtype=dtype, device=self.device)
-        if stream is not None:
-            out.record_stream(stream)
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        # memory of the stream that writes it, kept for the one that asked for it
+        with torch.cuda.stream(stream):
+            out = torch.empty(shape, dtype=dtype, device=self.device)
+        out.record_stream(torch.cuda.current_stream(self.device))
         return out
 
     def append(self, k, v, tables, lens, starts=None, q=None, q_out=None, stream=None):
@@ -357,9 +362,7 @@ class PagedKVCache:
             raise ValueError(f"q {q.dtype} {tuple(shape)} does not match the cache and lens")
         qp = self._dense(q, "q")
         if out is None:
-            out = torch.empty_like(q)
-            if stream is not None:
-                out.record_stream(stream)
+            out = torch.empty_like(q) if stream is None else self._new(shape, q.dtype, stream)
             op = out.data_ptr()
         else:
             if out.dtype is not q.dtype or out.shape != shape:

@@ -15,10 +15,11 @@
 //      run on codes and each 32-element block's sum is scaled by its d in f32.
 //   V: v = u d + m in one half2 fma a pair of rows (one rounding to fp16).
 // Tiles of 8 or 16 queries of bf16 (the tile is taken by the most queries that
-// a key has); f32 queries keep f32 accuracy with tiles of 8: rows 0..7 of the S
-// tile carry the high part of the queries and rows 8..15 the low part, two fp16
+// a key has); f32 queries keep f32 accuracy: rows 0..7 of an S tile
+// carry the high part of the queries and rows 8..15 the low part, two fp16
 // numbers (22 bits of a query scaled to its largest element), and P d goes in as
-// two bf16 numbers (16 bits, any range) against the exact codes u - 16, with
+// three bf16 numbers (all its 24 bits; two left outputs off by up to 3e-6 of their
+// size where f32 arithmetic leaves 1e-6) against the exact codes u - 16, with
 // sum p (m + 16 d) kept in f32 beside it.
 //
 // Why tensor cores for one token: the products cost the same for 1 or 8 queries,
@@ -351,11 +352,11 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
             } else {
                 const float2 d0 = __half22float2(as_h2(dm.x)), d1 = __half22float2(as_h2(dm.y));
                 const float2 m0 = __half22float2(as_h2(dm.z)), m1 = __half22float2(as_h2(dm.w));
-                uint32_t ph[NQ][2], pl[NQ][2];             // p d in two bf16 parts
+                uint32_t px[3][NQ][2];                     // p d in three bf16 parts, largest first
 #pragma unroll
                 for (int r = 0; r < NQ; ++r) {
                     const float p0 = sc[0][2 * r], p1 = sc[0][2 * r + 1], p2 = sc[1][2 * r], p3 = sc[1][2 * r + 1];
-                    const float x0 = p0 * d0.x, x1 = p1 * d0.y, x2 = p2 * d1.x, x3 = p3 * d1.y;
+                    float x0 = p0 * d0.x, x1 = p1 * d0.y, x2 = p2 * d1.x, x3 = p3 * d1.y;
                     float t = acc.mt[r][b];
                     t = fmaf(p0, fmaf(16.f, d0.x, m0.x), t);
                     t = fmaf(p1, fmaf(16.f, d0.y, m0.y), t);
@@ -363,10 +364,22 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
                     acc.mt[r][b] = fmaf(p3, fmaf(16.f, d1.y, m1.y), t);
                     const __nv_bfloat162 h0 = __floats2bfloat162_rn(x0, x1), h1 = __floats2bfloat162_rn(x2, x3);
                     const float2 f0 = __bfloat1622float2(h0), f1 = __bfloat1622float2(h1);
-                    ph[r][0] = as_u32(h0);
-                    ph[r][1] = as_u32(h1);
-                    pl[r][0] = as_u32(__floats2bfloat162_rn(x0 - f0.x, x1 - f0.y));
-                    pl[r][1] = as_u32(__floats2bfloat162_rn(x2 - f1.x, x3 - f1.y));
+                    px[0][r][0] = as_u32(h0);
+                    px[0][r][1] = as_u32(h1);
+                    x0 -= f0.x;
+                    x1 -= f0.y;
+                    x2 -= f1.x;
+                    x3 -= f1.y;
+                    // 16 bits are left: 8 in the upper half, then 8 behind it
+                    const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1), u2 = __float_as_uint(x2), u3 = __float_as_uint(x3);
+                    px[1][r][0] = __byte_perm(u0, u1, 0x7632);
+                    px[1][r][1] = __byte_perm(u2, u3, 0x7632);
+                    x0 -= __uint_as_float(u0 & 0xffff0000u);
+                    x1 -= __uint_as_float(u1 & 0xffff0000u);
+                    x2 -= __uint_as_float(u2 & 0xffff0000u);
+                    x3 -= __uint_as_float(u3 & 0xffff0000u);
+                    px[2][r][0] = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+                    px[2][r][1] = __byte_perm(__float_as_uint(x2), __float_as_uint(x3), 0x7632);
                 }
                 auto code = [&](auto R, int n) {
                     constexpr int r = decltype(R)::value;
@@ -379,16 +392,14 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
                 const std::integral_constant<int, 3> r3{};
                 const uint4 v0 = make_uint4(code(r0, n0), code(r1, n0), code(r0, n1), code(r1, n1));
 #pragma unroll
-                for (int r = 0; r < NQ; ++r) {
-                    mma_bf16(acc.o[r][2 * b], v0, ph[r][0], ph[r][1]);
-                    mma_bf16(acc.o[r][2 * b], v0, pl[r][0], pl[r][1]);
-                }
+                for (int r = 0; r < NQ; ++r)
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) mma_bf16(acc.o[r][2 * b], v0, px[i][r][0], px[i][r][1]);
                 const uint4 v1 = make_uint4(code(r2, n0), code(r3, n0), code(r2, n1), code(r3, n1));
 #pragma unroll
-                for (int r = 0; r < NQ; ++r) {
-                    mma_bf16(acc.o[r][2 * b + 1], v1, ph[r][0], ph[r][1]);
-                    mma_bf16(acc.o[r][2 * b + 1], v1, pl[r][0], pl[r][1]);
-                }
+                for (int r = 0; r < NQ; ++r)
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) mma_bf16(acc.o[r][2 * b + 1], v1, px[i][r][0], px[i][r][1]);
             }
         }
     }
@@ -1131,8 +1142,9 @@ cudaError_t launch_split_nb(const SplitArgs& a, cudaStream_t s) {
 }  // namespace
 
 // f32 queries of head_dim 256 stay at 8: two parts of 16 leave few registers and
-// stages (16k rows, 4 KV heads of 8 x 4 queries: 43 us, 8: 38), where smaller heads
-// gain (8 sequences of 16k rows, 8 KV heads of 128, 16 queries: 102 us, 8: 119)
+// stages (16k rows, 4 KV heads of 8 x 4 queries, P d in two parts: 43 us, 8: 38),
+// where smaller heads gain (8 sequences of 16k rows, 8 KV heads of 128, 16 queries:
+// 102 us, 8: 119)
 int split_tile(int NB, bool bf16, int most_queries) { return most_queries > 8 && (bf16 || NB < 8) ? 16 : 8; }
 
 int split_warps(int NB, int tile) {

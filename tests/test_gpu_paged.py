@@ -1,6 +1,9 @@
 """Paged cache on the GPU against the fp64 oracle: bytes of the append, the
 rotation, decode, shared prefixes, key bounds, selection, listed pages."""
 
+import re
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -743,6 +746,47 @@ def test_calls_of_another_stream_and_its_capture():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fmt,dtype,D,Hkv,Hq,T,n", [(Q8, BF, 64, 1, 16, 64, 1), (F8, F32, 128, 1, 8, 33, 2), (Q8, F32, 64, 2, 32, 17, 1),
+                                                    (Q8, BF, 64, 128, 128, 1, 2), (F8, BF, 64, 1, 128, 1, 2)])
+def test_many_query_rows_and_many_heads(fmt, dtype, D, Hkv, Hq, T, n):
+    p = PagedPair(n, Hkv, D, Hq, page=32, max_pages=4, max_t=64, fmt=fmt, seed=T)
+    p.append([90, 41][:n])
+    q = p.randn(n, T, Hq, D).to(dtype)
+    want, mag = p.want(q)
+    assert_attention(p, p.dev.decode(q.cuda(), p.tables, p.lens()), want, mag)
+    shared = p.dev.decode_shared(q.cuda(), p.tables, p.lens(), i32([0, 1]), i32([32]))
+    assert_attention(p, shared, want, mag, "shared")
+    assert p.dev.device_error() == 0
+
+
+def test_table_entries_behind_a_length_are_not_read():
+    """Unused entries may hold anything."""
+    p, starts, prefix = shared_case(sizes=[9], prefix=[40], suffix=[3, 30], Hkv=1, Hq=4)
+    b = PagedKVCache(p.n_pages, 16, 1, 64, 4, max_seqs=9, max_pages=p.max_pages, max_t=1, bounds=True, pool=p.dev.pool)
+    lens = p.lens()
+    tab = p.tables.clone()
+    for i, x in enumerate(lens.tolist()):
+        tab[i, -(-x // 16):] = (-1, 1 << 30)[i % 2]
+    b.update_bounds(tab, lens, max(lens.tolist()))
+    q = p.randn(9, 1, 4, 64).to(BF).cuda()
+    pages = b.select(q, tab, lens, 2)
+    b.decode_sparse(q, tab, lens, pages)
+    want, mag = p.want(q.cpu())
+    assert_attention(p, b.decode(q, tab, lens), want, mag)
+    assert_attention(p, b.decode_shared(q, tab, lens, starts, prefix), want, mag, "shared")
+    assert b.device_error() == 0
+
+
+def test_the_documented_example():
+    need_gpu()
+    text = (Path(__file__).resolve().parents[1] / "README.md").read_text()
+    code = next(x for x in re.findall(r"```python\n(.*?)```", text, re.S) if "PagedKVCache(" in x)
+    names = {"torch": torch}
+    exec(code, names)
+    assert names["out"].shape == (2, 1, 32, 128) and torch.isfinite(names["out"]).all()
+    assert names["c"].device_error() == 0
 
 
 # ------------------------------------------------------------------ refusals
