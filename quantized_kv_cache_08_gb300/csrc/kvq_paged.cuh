@@ -70,25 +70,12 @@ __device__ __forceinline__ long long page_at(const Geom& g, const int* table, in
     return pg * g.page_bytes;
 }
 
-__device__ __forceinline__ Place place_row(const Geom& g, const Rows& r, int row, bool short_is_error) {
+// Place of a row of entry i (i < 0: the row is none's)
+__device__ __forceinline__ Place place_in(const Geom& g, const Rows& r, int row, int i, bool short_is_error) {
     Place p{-1, -1, 0, 0, 0};
-    int i, n, at;
-    if (r.starts) {
-        if (row < r.starts[0] || row >= r.starts[r.n_seq]) return p;
-        int lo = 0, hi = r.n_seq;                  // the last entry that starts at or before the row
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (r.starts[mid] <= row) lo = mid;
-            else hi = mid;
-        }
-        i = lo;
-        at = row - r.starts[i];
-        n = r.starts[i + 1] - r.starts[i];
-    } else {
-        i = row / r.T;
-        at = row - i * r.T;
-        n = r.T;
-    }
+    if (i < 0) return p;
+    const int from = r.starts ? r.starts[i] : i * r.T, at = row - from;
+    const int n = r.starts ? r.starts[i + 1] - from : r.T;
     p.len = r.lens[i];
     if (p.len < 0 || p.len > (long long)g.max_pages << g.page_shift || (short_is_error && p.len < n)) {
         atomicExch(g.err, kErrCounter);
@@ -103,6 +90,43 @@ __device__ __forceinline__ Place place_row(const Geom& g, const Rows& r, int row
     p.cell = pg + (long long)((p.pos & (g.page_rows - 1)) >> 4) * g.cell_bytes;
     p.t = p.pos & 15;
     return p;
+}
+
+// Entry of a row: the last that starts at or before it, -1 outside them
+__device__ __forceinline__ int entry_of_row(const Rows& r, int row) {
+    if (!r.starts) return row / r.T;
+    if (row < r.starts[0] || row >= r.starts[r.n_seq]) return -1;
+    int lo = 0, hi = r.n_seq;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (r.starts[mid] <= row) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// The same for rows row0 + lane, lane < W, by a warp: 32 starts a step, where the
+// search of one row is a chain of loads
+template <int W>
+__device__ __forceinline__ int entry_of_rows(const Rows& r, int row0, int lane) {
+    const int row = row0 + lane;
+    if (!r.starts) return row / r.T;
+    int i = -1;
+    for (int c = 0; c < r.n_seq; c += 32) {
+        const int st = c + lane < r.n_seq ? r.starts[c + lane] : 0x7fffffff;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int k = __popc(__ballot_sync(0xffffffffu, st <= row0 + w));
+            if (lane == w) i += k;
+        }
+    }
+    // (behind the last start, or starts in no order)
+    if (i >= 0 && (r.starts[i] > row || r.starts[i + 1] <= row)) i = entry_of_row(r, row);
+    return i;
+}
+
+__device__ __forceinline__ Place place_row(const Geom& g, const Rows& r, int row, bool short_is_error) {
+    return place_in(g, r, row, entry_of_row(r, row), short_is_error);
 }
 #endif
 

@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCellThreads = 128, kCellWarps = kCellThreads / 32;
 constexpr int kTT = 4;                 // tokens of a CTA when there are many (2: 64 us, 8: 57 us where 4 takes 56)
 
 // Eight elements as they lie in memory, then as floats
@@ -96,37 +97,53 @@ __device__ __forceinline__ unsigned short half_quotient(float num, float err, fl
 // The rotation table of a token holds (cos, sin) of pair p at place
 // (p % 8) (n / 8) + p / 8 (4 for interleaved pairs) of n: the lanes of a load,
 // which take neighbouring groups of pairs, read neighbouring words.
-//
-// Rotate the 8 elements e0.. of a head row; every lane of the warp calls this
-// (shuffles).
-__device__ __forceinline__ void rotate8(float (&x)[8], int e0, int rot, int interleaved, const float2* cs, int lane) {
-    if (rot == 0) return;
+// (cos, sin) of pair pr at position pos into a token's table of `half` pairs
+__device__ __forceinline__ void put_angle(float2* cs_of, float2 f, int pos, int pr, int half, int interleaved) {
+    const float p = (float)max(pos, 0);
+    const float t = p * f.x;
+    const float e = fmaf(p, f.x, -t);
+    const float turn = (t - rintf(t)) + fmaf(p, f.y, e);
+    float sn, cs;
+    sincospif(2.f * turn, &sn, &cs);
+    const int grp = interleaved ? 4 : 8;
+    cs_of[(pr % grp) * (half / grp) + pr / grp] = make_float2(cs, sn);
+}
+
+// Rotate elements e0 .. e0 + 7 (x) below rot of a head row; y: those that the half-split rotation pairs them with
+__device__ __forceinline__ void turn8(float (&x)[8], const float (&y)[8], int e0, int rot, int interleaved, const float2* cs) {
     if (interleaved) {
-        if (e0 < rot) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 a = cs[i * (rot / 8) + e0 / 8];
-                const float p = x[2 * i], q = x[2 * i + 1];
-                x[2 * i] = p * a.x - q * a.y;
-                x[2 * i + 1] = p * a.y + q * a.x;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = cs[i * (rot / 8) + e0 / 8];
+            const float p = x[2 * i], q = x[2 * i + 1];
+            x[2 * i] = p * a.x - q * a.y;
+            x[2 * i + 1] = p * a.y + q * a.x;
         }
         return;
     }
     const int half = rot / 2;
     const bool second = e0 >= half;
-    const int from = e0 < rot ? lane + (second ? -half / 8 : half / 8) : lane;
+    const float2* c = cs + (second ? e0 - half : e0) / 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 a = c[i * (half / 8)];
+        x[i] = second ? y[i] * a.y + x[i] * a.x : x[i] * a.x - y[i] * a.y;
+    }
+}
+
+// Rotate the 8 elements e0.. of a head row; every lane of the warp calls this
+// (shuffles).
+__device__ __forceinline__ void rotate8(float (&x)[8], int e0, int rot, int interleaved, const float2* cs, int lane) {
+    if (rot == 0) return;
+    if (interleaved) {
+        if (e0 < rot) turn8(x, x, e0, rot, 1, cs);
+        return;
+    }
+    const int half = rot / 2, from = e0 < rot ? lane + (e0 >= half ? -half / 8 : half / 8) : lane;
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
-    if (e0 < rot) {
-        const float2* c = cs + (second ? e0 - half : e0) / 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 a = c[i * (half / 8)];
-            x[i] = second ? y[i] * a.y + x[i] * a.x : x[i] * a.x - y[i] * a.y;
-        }
-    }
+    if (e0 < rot) turn8(x, y, e0, rot, 0, cs);
 }
 
 // Codes of 8 elements by q8_0's or q5_1's rule: round-half-away(t) for t = x / d
@@ -228,6 +245,52 @@ __device__ __forceinline__ void fold_rows(const uint8_t* cell, long long step, i
     }
 }
 
+// Query units u0, u0 + du .. of a token (64 / LR heads each) rotated into q_out by
+// one warp.  A lane's two pieces: partners of the half-split rotation, else side
+// by side.
+template <int LR, bool BF16>
+__device__ __forceinline__ void rotate_queries(const AppendArgs& a, long long row, const float2* cs, int u0, int du, int lane) {
+    constexpr int D = LR * 8, QPW = 64 / LR, QL = LR / 2;
+    const int half = a.rope_dim / 2, uq = a.q ? (a.Hq + QPW - 1) / QPW : 0;
+    const int ql = lane % QL, split = a.interleaved ? 0 : a.rope_dim / 16;
+    const int qa = 8 * (ql < split ? ql : split + 2 * (ql - split) + (a.interleaved ? 0 : split));
+    const int qb = ql < split ? qa + half : qa + 8;
+    constexpr int U = BF16 ? 2 : 1;                // units in flight
+    for (int u = u0; u < uq; u += U * du) {
+        Raw8<BF16> rx[U], ry[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int h = (u + k * du) * QPW + lane / QL;
+            if (h < a.Hq) {
+                fetch8(a.q, row * a.q_stride + h * D + qa, rx[k]);
+                fetch8(a.q, row * a.q_stride + h * D + qb, ry[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int h = (u + k * du) * QPW + lane / QL;
+            if (h >= a.Hq) continue;           // (no shuffles on this path)
+            float x[8], y[8];
+            floats8(rx[k], x);
+            floats8(ry[k], y);
+            if (a.interleaved) {
+                rotate8(x, qa, a.rope_dim, 1, cs, lane);
+                rotate8(y, qb, a.rope_dim, 1, cs, lane);
+            } else if (ql < split) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 c = cs[i * (half / 8) + ql];
+                    const float p = x[i], q = y[i];
+                    x[i] = p * c.x - q * c.y;
+                    y[i] = p * c.y + q * c.x;
+                }
+            }
+            store8(a.q_out, (row * a.Hq + h) * D + qa, BF16, x);
+            store8(a.q_out, (row * a.Hq + h) * D + qb, BF16, y);
+        }
+    }
+}
+
 // One append CTA: tokens [TT blockIdx.x, + TT), row units blockIdx.y, + gridDim.y..
 // A unit is a warp's rows of one kind of one token: 64 / LR query heads (a lane
 // holds 8 elements and the 8 that they are rotated with), or 32 / LR key or
@@ -235,30 +298,24 @@ __device__ __forceinline__ void fold_rows(const uint8_t* cell, long long step, i
 template <int LR, bool BF16, bool BOUNDS>
 __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
     extern __shared__ float2 s_cs[];               // [TT][rope_dim / 2]
-    __shared__ Place s_place[16];
-    constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR, QPW = 64 / LR, QL = LR / 2;
+    __shared__ Place s_place[kTT];
+    constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR, QPW = 64 / LR;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row0 = blockIdx.x * TT;
     const int half = a.rope_dim / 2;
     wait_for_earlier();
     let_next_start();
-    if (tid < TT) {
+    if (warp == 0) {
+        const int row = row0 + lane, i = entry_of_rows<kTT>(a.r, row0, lane);
         Place p{-1, -1, 0, 0, 0};
-        if (row0 + tid < a.r.rows) p = place_row(a.g, a.r, row0 + tid, true);
-        s_place[tid] = p;
+        if (lane < TT && row < a.r.rows) p = place_in(a.g, a.r, row, i, true);
+        if (lane < TT) s_place[lane] = p;
     }
     __syncthreads();
-    for (int i = tid; i < TT * half; i += kThreads) {
-        const int tt = i / half, pr = i - tt * half;
-        const float p = (float)max(s_place[tt].pos, 0);
-        const float2 f = fq.f[pr];
-        const float t = p * f.x;
-        const float e = fmaf(p, f.x, -t);
-        const float turn = (t - rintf(t)) + fmaf(p, f.y, e);
-        float sn, cs;
-        sincospif(2.f * turn, &sn, &cs);
-        const int grp = a.interleaved ? 4 : 8;
-        s_cs[tt * half + (pr % grp) * (half / grp) + pr / grp] = make_float2(cs, sn);
+    // (an indexed read of the frequencies takes a step for each lane: one a thread)
+    for (int pr = tid % (kThreads / TT); pr < half; pr += kThreads / TT) {
+        const int tt = tid / (kThreads / TT);
+        put_angle(s_cs + tt * half, fq.f[pr], s_place[tt].pos, pr, half, a.interleaved);
     }
     __syncthreads();
     // a warp's token, and its share of the token's units
@@ -269,50 +326,9 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
     const float2* cs = s_cs + tt * half;
     const long long row = row0 + tt;
     const int uq = a.q ? (a.Hq + QPW - 1) / QPW : 0, uk = (a.g.Hkv + JPW - 1) / JPW;
-    int u = u0;
-    {
-        // ---- queries.  A lane's two pieces: partners of the half-split
-        // rotation, else side by side
-        const int ql = lane % QL, split = a.interleaved ? 0 : a.rope_dim / 16;
-        const int qa = 8 * (ql < split ? ql : split + 2 * (ql - split) + (a.interleaved ? 0 : split));
-        const int qb = ql < split ? qa + half : qa + 8;
-        constexpr int U = BF16 ? 2 : 1;            // units in flight
-        for (; u < uq; u += U * du) {
-            Raw8<BF16> rx[U], ry[U];
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int h = (u + k * du) * QPW + lane / QL;
-                if (h < a.Hq) {
-                    fetch8(a.q, row * a.q_stride + h * D + qa, rx[k]);
-                    fetch8(a.q, row * a.q_stride + h * D + qb, ry[k]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int h = (u + k * du) * QPW + lane / QL;
-                if (h >= a.Hq) continue;           // (no shuffles on this path)
-                float x[8], y[8];
-                floats8(rx[k], x);
-                floats8(ry[k], y);
-                if (a.interleaved) {
-                    rotate8(x, qa, a.rope_dim, 1, cs, lane);
-                    rotate8(y, qb, a.rope_dim, 1, cs, lane);
-                } else if (ql < split) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 c = cs[i * (half / 8) + ql];
-                        const float p = x[i], q = y[i];
-                        x[i] = p * c.x - q * c.y;
-                        y[i] = p * c.y + q * c.x;
-                    }
-                }
-                store8(a.q_out, (row * a.Hq + h) * D + qa, BF16, x);
-                store8(a.q_out, (row * a.Hq + h) * D + qb, BF16, y);
-            }
-        }
-        // the first unit of keys and values that is this warp's
-        u = u0 >= uq ? u0 : u0 + (uq - u0 + du - 1) / du * du;
-    }
+    rotate_queries<LR, BF16>(a, row, cs, u0, du, lane);
+    // the first unit of keys and values that is this warp's
+    int u = u0 >= uq ? u0 : u0 + (uq - u0 + du - 1) / du * du;
     // ---- keys and values
     const int li = lane % LR, e0 = 8 * li;
     const int t = pl.t, b = li >> 2, c = li & 3;
@@ -433,6 +449,148 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
             const int g = 2 * c + (b & 1);
             const uint32_t byte = (b & 1) ? (other | (nib[1] << 4)) : (nib[0] | (other << 4));
             cell[800 * NB + (ne >> 2) * 128 + (4 * g + j) * 4 + s * 2 + ((ne & 3) >> 1)] = (uint8_t)byte;
+        }
+    }
+}
+
+// E4M3 rows, many a sequence: pieces of RT rows of one entry that lie at
+// RT-aligned positions (RT 8, at head_dim 64 16), so that what a piece holds of V
+// in a cell is whole 512-byte stretches.  A CTA takes the pieces whose first row of
+// this call is one of its RT rows: at most RT, nearly always one.  A warp's task is
+// a piece of one KV head, up to four blocks of K or of V, a lane a block of one
+// row; values go through shared memory into 16-byte stores, where append_kernel
+// stores them byte by byte.  6 x 1379 rows, 32 query and 8 KV heads of 128: 42 us,
+// append_kernel 67 (its q8_0 / q5_1 rows: 48; by pieces they took 56: the exact rounding of
+// a whole block a lane is much code).
+template <int NB, bool BF16>
+__global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq) {
+    constexpr int D = NB * 32, LR = D / 8, BL = NB < 4 ? NB : 4, RT = 32 / BL, W = 2 * RT;
+    extern __shared__ float2 s_cs[];                 // [W][rope_dim / 2]
+    __shared__ Place s_place[W];
+    __shared__ int s_from[W];                        // the piece of a row: index of its first row, -1 none of this CTA's
+    __shared__ __align__(16) uint8_t s_stage[kCellWarps][1024];
+    constexpr int kSlots = 32;                       // threads that take different pairs
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // every other CTA rotates queries, which HBM bounds, beside those that work codes out
+    const bool queries = a.q && (blockIdx.x & 1);
+    const int row0 = (a.q ? blockIdx.x >> 1 : blockIdx.x) * RT, half = a.rope_dim / 2;
+    wait_for_earlier();
+    let_next_start();
+    if (warp == 0) {
+        const int row = row0 + lane, i = entry_of_rows<W>(a.r, row0, lane);
+        if (lane < W) {
+            Place p{-1, -1, 0, 0, 0};
+            if (row < a.r.rows) p = place_in(a.g, a.r, row, i, true);
+            const int from = p.pos < 0 ? -1 : queries ? lane : lane - min(p.pos & (RT - 1), p.pos - p.first);
+            s_place[lane] = p;
+            s_from[lane] = from < RT ? from : -1;    // (below 0: the CTA before has it)
+        }
+    }
+    __syncthreads();
+    // a pair a thread (an indexed read of the frequencies takes a step for each lane), every token
+    const int stride_cs = half + 1;                  // rows of the tables start in different banks
+    for (int pr = tid % kSlots; pr < half; pr += kSlots) {
+        const float2 f = fq.f[pr];
+        for (int tt = tid / kSlots; tt < W; tt += kCellThreads / kSlots)
+            if (s_from[tt] >= 0) put_angle(s_cs + tt * stride_cs, f, s_place[tt].pos, pr, half, a.interleaved);
+    }
+    const int per = a.g.Hkv * (NB / BL);             // tasks of a piece and kind
+    const int li = lane / BL, bl = lane % BL;        // row of the piece, block of the four
+    if (queries) {
+        __syncthreads();
+        for (int i = warp; i < RT; i += kCellWarps)      // a row a warp
+            if (s_from[i] >= 0) rotate_queries<LR, BF16>(a, row0 + i, s_cs + i * stride_cs, 0, 1, lane);
+        return;
+    }
+    // values first, for they need no angles
+#pragma unroll 1
+    for (int kind = 1; kind >= 0; --kind) {
+        if (kind == 0) __syncthreads();              // the angles are there
+#pragma unroll 1
+        for (int s = 0; s < RT; ++s) {
+            if (s_from[s] != s) continue;
+            // the piece's rows: aligned row li is row s + li - skew of the window
+            const Place pf = s_place[s];
+            const int skew = pf.pos & (RT - 1), wi = s + li - skew;
+            if (pf.cell < 0) continue;
+            const bool on = wi >= s && wi < W && s_from[wi] == s;
+            const bool full = __all_sync(0xffffffffu, on);
+            const int t = (pf.pos - skew + li) & 15, j = (t & 7) >> 1, sb = t & 1, hh = t >> 3;
+            const long long row = row0 + wi;
+            const float2* cs = s_cs + (on ? wi : s) * stride_cs;
+            const void* src = kind ? a.v : a.k;
+            const long long stride = kind ? a.v_stride : a.k_stride;
+#pragma unroll 1
+            for (int task = warp; task < per; task += kCellWarps) {
+                const int h = task / (NB / BL), b = (task - h * (NB / BL)) * BL + bl, n = hh * NB + b, e0 = 32 * b;
+                uint8_t* cell = a.g.pool + pf.cell + (long long)h * a.g.cells_per_page() * a.g.cell_bytes;
+                const long long at = row * stride + h * D;
+                float x[32];
+                {
+                    Raw8<BF16> raw[4] = {};
+                    if (on)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) fetch8(src, at + e0 + 8 * k, raw[k]);
+                    Raw8<BF16> other[4] = {};        // what the half-split rotation pairs them with
+                    if (on && !kind && !a.interleaved)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int e = e0 + 8 * k;
+                            if (e < a.rope_dim) fetch8(src, at + (e < half ? e + half : e - half), other[k]);
+                        }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int e = e0 + 8 * k;
+                        float v[8], y[8];
+                        floats8(raw[k], v);
+                        if (!kind && e < a.rope_dim) {
+                            floats8(other[k], y);
+                            turn8(v, y, e, a.rope_dim, a.interleaved, cs);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[8 * k + i] = v[i];
+                    }
+                }
+                uint32_t w[8];                       // elements 4 g ..
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                    w[g] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[4 * g], x[4 * g + 1]), __NV_SATFINITE, __NV_E4M3) |
+                           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[4 * g + 2], x[4 * g + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
+                if (kind == 0) {
+                    // the lanes of blocks b and b + 1 swap halves: 16 bytes hold both blocks' eight of a chunk
+                    const bool odd = b & 1;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t g0 = odd ? w[2 * k] : w[4 + 2 * k], g1 = odd ? w[2 * k + 1] : w[5 + 2 * k];
+                        const uint32_t m0 = odd ? w[4 + 2 * k] : w[2 * k], m1 = odd ? w[5 + 2 * k] : w[2 * k + 1];
+                        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, g0, 1), r1 = __shfl_xor_sync(0xffffffffu, g1, 1);
+                        const uint4 v = odd ? make_uint4(r0, r1, m0, m1) : make_uint4(m0, m1, r0, r1);
+                        if (on) *reinterpret_cast<uint4*>(cell + (b >> 1) * 1024 + t * 64 + ((odd ? 2 : 0) + k) * 16) = v;
+                    }
+                    continue;
+                }
+                if (full) {
+                    // rows t and t + 1 alternate byte by byte: their lanes swap halves
+                    uint8_t* st = s_stage[warp] + (NB == 2 ? hh : (b >> 1) & 1) * 512 + j * 16 + (n & 1) * 8;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t r = __shfl_xor_sync(0xffffffffu, sb ? w[k] : w[4 + k], BL), m = sb ? w[4 + k] : w[k];
+                        const uint32_t even = sb ? r : m, od = sb ? m : r;
+                        *reinterpret_cast<uint2*>(st + (k + 4 * sb) * 64) = make_uint2(__byte_perm(even, od, 0x5140), __byte_perm(even, od, 0x7362));
+                    }
+                    __syncwarp();
+                    // regions n >> 1: of NB 2 the cell's two, else this half's pair of pairs
+                    uint8_t* dst = cell + 512 * NB + (NB == 2 ? 0 : (hh * NB + b - bl) / 2 * 512);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4*>(dst + 512 * k + lane * 16) = *reinterpret_cast<const uint4*>(s_stage[warp] + 512 * k + lane * 16);
+                    __syncwarp();
+                } else if (on) {
+                    uint8_t* p = cell + 512 * NB + (n >> 1) * 512 + (n & 1) * 8 + sb;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) p[(4 * (i >> 2) + j) * 16 + (i & 3) * 2] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+                }
+            }
         }
     }
 }
@@ -564,6 +722,19 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsArgs a) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cudaStream_t s) {
+    // pieces of cells where a sequence brings 8 rows or more on average
+    if (a.g.fp8 && a.r.rows / 8 >= a.r.n_seq) {
+        const int rt = a.g.D == 64 ? 16 : 8;
+        const dim3 grid((unsigned)((a.r.rows + rt - 1) / rt * (a.q ? 2 : 1)));
+        const size_t smem = (size_t)2 * rt * (a.rope_dim / 2 + 1) * sizeof(float2);
+        auto run = [&](auto b) {
+            constexpr bool B = decltype(b)::value;
+            if (a.g.D == 64) return launch_dependent(append_cells_kernel<2, B>, grid, kCellThreads, smem, s, a, f);
+            if (a.g.D == 128) return launch_dependent(append_cells_kernel<4, B>, grid, kCellThreads, smem, s, a, f);
+            return launch_dependent(append_cells_kernel<8, B>, grid, kCellThreads, smem, s, a, f);
+        };
+        return a.bf16 ? run(std::true_type{}) : run(std::false_type{});
+    }
     const int jpw = 256 / a.g.D, qpw = 2 * jpw;
     const int units = (a.q ? (a.Hq + qpw - 1) / qpw : 0) + 2 * ((a.g.Hkv + jpw - 1) / jpw);
     // tokens per CTA: the angles are shared by its heads; few rows spread over
