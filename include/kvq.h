@@ -391,7 +391,7 @@ void kvq_paged_free(kvq_paged* cache);
  * quantised.  q (or NULL): device [rows][Hq][D] of dtype, q_stride apart,
  * rotated likewise into q_out, dense [rows][Hq][D]; q_out may be q when q is
  * dense.  With cfg.bounds the bounds of the pages that got rows are renewed
- * from all rows below the length. */
+ * from all rows below the length.  A page that gets rows belongs to one entry. */
 kvq_status kvq_paged_append(kvq_paged* cache, const void* k, long long k_stride, const void* v, long long v_stride,
                             const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,
                             const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,
@@ -423,9 +423,9 @@ typedef struct kvq_paged_query {
     int window;
 } kvq_paged_query;
 
-/* Decode attention over the pages.  f32 queries keep f32 accuracy (products
- * split in two parts); bf16 queries round probabilities and values to fp16
- * inside, sums are f32 throughout. */
+/* Decode attention over the pages.  f32 queries keep f32 accuracy (factors
+ * split in two or three parts); bf16 queries round probabilities and values
+ * (and the keys of a shared prefix) to fp16 inside, sums are f32 throughout. */
 kvq_status kvq_paged_decode(kvq_paged* cache, const kvq_paged_query* a, void* stream);
 
 /* The same result for a batch in which groups of sequences share a prefix,
@@ -441,8 +441,8 @@ kvq_status kvq_paged_decode_shared(kvq_paged* cache, const kvq_paged_query* a, c
 /* Key bounds.  For each page, KV head and 32-element block over the rows below
  * the length: the smallest and largest dequantised key of each element, as
  * codes floor(min / ds) and ceil(max / ds) within +-127 of ds = max|key| *
- * (1/127) (f32 operations; zero codes when ds is 0).  Buffer: int8 [n_pages][Hkv][NB][2][32] (min,
- * max), then f32 ds [n_pages][Hkv][NB].  Appends do this themselves; the call
+ * (1/127) (f32 operations; zero codes when ds is 0).  Buffer: int8
+ * [n_pages][Hkv][NB][2][32] (min, max), then f32 ds [n_pages][Hkv][NB].  Appends do this themselves; the call
  * is for pages filled in another way: it renews those that hold the last T
  * rows of each entry (or its rows by `starts`). */
 kvq_status kvq_paged_bounds(kvq_paged* cache, const int* tables, const int* lens, int n_seq, int T, const int* starts,
@@ -450,8 +450,8 @@ kvq_status kvq_paged_bounds(kvq_paged* cache, const int* tables, const int* lens
 
 /* Choose pages by their bounds.  For each sequence, query row t and KV head:
  * the query is coded per block (dq = amax * (1/127), c = rint(x * ((1/amax) *
- * 127)), f32 operations), and a page scores max over the KV head's queries of sum over blocks, in order,
- * of (dq ds) * sum_i (c_i > 0 ? c_i max_i : c_i min_i), in f32: an upper bound
+ * 127)), f32 operations), and a page scores max over the KV head's queries of
+ * sum over blocks, in order, of (dq ds) * sum_i (c_i > 0 ? c_i max_i : c_i min_i), in f32: an upper bound
  * of the coded query's products with the page's keys, and the same on every
  * run.  Pages: device int32 [n_seq][T][Hkv][keep] receives, ascending, the
  * first n_first and last n_last pages of those with a visible row and then the
