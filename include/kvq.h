@@ -391,7 +391,10 @@ void kvq_paged_free(kvq_paged* cache);
  * quantised.  q (or NULL): device [rows][Hq][D] of dtype, q_stride apart,
  * rotated likewise into q_out, dense [rows][Hq][D]; q_out may be q when q is
  * dense.  With cfg.bounds the bounds of the pages that got rows are renewed
- * from all rows below the length.  A page that gets rows belongs to one entry. */
+ * from all rows below the length.  A page that gets rows belongs to one entry.
+ * Stored values are finite: a q5_1 block's ends stay within +-65280, a NaN is
+ * stored as its block's least value (a block of NaN as zeros), in E4M3 as zero.  Keys that are not finite make the scores of the queries that see them
+ * NaN, and no others. */
 kvq_status kvq_paged_append(kvq_paged* cache, const void* k, long long k_stride, const void* v, long long v_stride,
                             const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,
                             const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,

@@ -94,6 +94,19 @@ __device__ __forceinline__ unsigned short half_quotient(float num, float err, fl
     return __half_as_ushort(__float2half_rn(q));
 }
 
+// Stored values are finite whatever comes in: a row that one query does not see
+// meets it with weight 0 in the same matrix product as the queries that see it,
+// and 0 x inf would reach its output.  A q5_1 block's ends stay within +-65280, so
+// that 31 d + m with d rounded up (by 2^-12, here up to 64 in all) stays below
+// fp16's 65504; an infinite element takes the code at that end, a NaN the lowest, a
+// block of NaN is zeros.  An E4M3 NaN is zero.
+__device__ __forceinline__ void bound_block(float& least, float& most) {
+    if (!(least <= most)) least = most = 0.f;
+    least = fminf(fmaxf(least, -65280.f), 65280.f);
+    most = fminf(fmaxf(most, -65280.f), 65280.f);
+}
+__device__ __forceinline__ float number(float x) { return x == x ? x : 0.f; }
+
 // The rotation table of a token holds (cos, sin) of pair p at place
 // (p % 8) (n / 8) + p / 8 (4 for interleaved pairs) of n: the lanes of a load,
 // which take neighbouring groups of pairs, read neighbouring words.
@@ -410,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     p[(4 * (2 * c + (i >> 2)) + j) * 16 + (i & 3) * 2] =
-                        __nv_cvt_float_to_fp8(x[i], __NV_SATFINITE, __NV_E4M3);
+                        __nv_cvt_float_to_fp8(number(x[i]), __NV_SATFINITE, __NV_E4M3);
             }
             continue;
         }
@@ -424,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         least = fminf(least, __shfl_xor_sync(0xffffffffu, least, 2));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        bound_block(least, most);
         const float range = most - least, back = range - most;
         const unsigned short db = half_quotient(range, (most - (range - back)) - (least + back), 31.f);
         const unsigned short mb = __half_as_ushort(__float2half_rn(least));
@@ -551,6 +565,9 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
                         for (int i = 0; i < 8; ++i) x[8 * k + i] = v[i];
                     }
                 }
+                if (kind)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = number(x[i]);
                 uint32_t w[8];                       // elements 4 g ..
 #pragma unroll
                 for (int g = 0; g < 8; ++g)

@@ -692,6 +692,46 @@ def test_a_query_that_is_not_a_number_stays_alone():
     assert p.dev.device_error() == 0
 
 
+@pytest.mark.parametrize("fmt", [Q8, F8])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 1e30])
+def test_rows_that_are_not_finite_stay_with_the_queries_that_see_them(fmt, dtype, bad):
+    """Draft rows and rows before a window: queries that do not see them give the same bits."""
+    Hkv, Hq, D, T = 1, 4, 64, 4
+    p = PagedPair(5, Hkv, D, Hq, page=16, max_pages=6, fmt=fmt, max_t=24, seed=13)
+    lens = i32([40, 17, 80, 33, 64])
+    rows = 20
+    k, v = p.randn(5, rows, Hkv, D).to(dtype).cuda(), p.randn(5, rows, Hkv, D).to(dtype).cuda()
+    fill_k, fill_v = p.randn(5, 96, Hkv, D).cuda(), p.randn(5, 96, Hkv, D).cuda()
+    q = p.randn(5, T, Hq, D).to(dtype).cuda()
+    outs = []
+    for x in (0.5, bad):
+        for b, L in enumerate(lens.tolist()):
+            p.dev.append(fill_k[b:b + 1, :L].contiguous(), fill_v[b:b + 1, :L].contiguous(), p.tables[b:b + 1], i32([L]))
+        kk, vv = k[:, -4:].clone(), v[:, -4:].clone()
+        kk[:, -1], vv[:, -1] = x, x                  # the newest row: only the last query row sees it
+        vv[:, -2, :, 5] = x                          # one value of the row before
+        p.dev.append(kk.contiguous(), vv.contiguous(), p.tables, lens)
+        outs.append([p.dev.decode(q, p.tables, lens), p.dev.decode(q, p.tables, lens, window=9),
+                     p.dev.decode_shared(q, p.tables, lens, i32([0, 5]), i32([16]))])
+    for a, b in zip(*outs):
+        assert torch.equal(a[:, :2], b[:, :2])
+        assert torch.isfinite(b[:, :3]).all()
+    # a prefix whose row 8 is seen by some members only (window 8, lengths 9 .. 24)
+    lens = i32([16, 24, 17, 20, 16])
+    tab = p.tables.clone()
+    tab[:, 0] = tab[0, 0]
+    outs = []
+    for x in (0.5, bad):
+        kk, vv = fill_k[:1, :16].to(dtype), fill_v[:1, :16].to(dtype)
+        kk[:, 8], vv[:, 8] = x, x
+        p.dev.append(kk.contiguous(), vv.contiguous(), tab[:1], i32([16]))
+        outs.append(p.dev.decode_shared(q, tab, lens, i32([0, 5]), i32([16]), window=8))
+    see = torch.tensor([[0 <= p_ - 8 < 8 for p_ in range(L - T, L)] for L in lens.tolist()], device="cuda")
+    assert see.any() and not see.all()
+    assert torch.equal(outs[0][~see], outs[1][~see])
+
+
 def test_output_over_the_queries():
     p = PagedPair(3, 2, 128, 8, page=16, max_pages=64, bounds=True, seed=4)
     p.append([1000, 3, 700])
