@@ -393,8 +393,9 @@ void kvq_paged_free(kvq_paged* cache);
  * dense.  With cfg.bounds the bounds of the pages that got rows are renewed
  * from all rows below the length.  A page that gets rows belongs to one entry.
  * Stored values are finite: a q5_1 block's ends stay within +-65280, a NaN is
- * stored as its block's least value (a block of NaN as zeros), in E4M3 as zero.  Keys that are not finite make the scores of the queries that see them
- * NaN, and no others. */
+ * stored as its block's least value (a block of NaN as zeros), in E4M3 as zero.
+ * Keys that are not finite make the scores of the queries that see them NaN,
+ * and no others. */
 kvq_status kvq_paged_append(kvq_paged* cache, const void* k, long long k_stride, const void* v, long long v_stride,
                             const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,
                             const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,

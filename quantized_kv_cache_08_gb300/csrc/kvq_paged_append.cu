@@ -6,7 +6,9 @@
 // registers (the partner half comes by shuffles, so queries may be rotated in
 // place), keys become q8_0 codes, values q5_1 codes, or both E4M3 bytes, and go
 // to their places in the page's cell.  The angles of a CTA's tokens are worked
-// out once into shared memory and serve all heads.
+// out once into shared memory and serve all heads.  8k rows of 32 query and 8 KV
+// heads of 128: 56 us where the bytes take 29, bound by instructions (the exact
+// rounding of every code); 64 rows 4 us.
 //
 // Angles.  With f in turns per position held as f_hi + f_lo (48 bits), p f_hi
 // splits exactly into a rounded product and its error (fma), the whole turns

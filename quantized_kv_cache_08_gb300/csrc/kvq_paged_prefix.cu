@@ -21,9 +21,9 @@
 // exponentials of the other are worked out.
 //
 // Bound: per 128 rows x 128 queries 8.4 MFLOP (head_dim 128) take about 1250
-// clocks on the tensor cores, the exponentials and the unpacking some 500 issue
-// slots each; reading the rows at HBM speed takes 1260 clocks, so up to 128
-// queries a KV head cost what the bytes cost.
+// queries a KV head cost what the bytes cost.  Measured: 8192 rows for 64
+// sequences of 4 queries a KV head, 8 KV heads of 128: 21 us for 3.4 tiles an SM,
+// half of it before the first products and after the last.
 #include "kvq_device.cuh"
 #include "kvq_paged.cuh"
 #include "kvq_paged_work.cuh"

