@@ -26,7 +26,12 @@ namespace {
 
 constexpr int kMaxGrid = 256;          // most CTAs of a split kernel
 constexpr int kMaxRanges = 4 * kMaxGrid;
-constexpr int kManyKeys = 32;          // of 16, 32, 100 and 200, best or near it for each of the measured shapes
+// Keys from which groups of four warps work on ranges of their own.  16: 47 us for
+// 32 f32 queries over 16k rows of 4 KV heads of 256 (16 keys), 32 and 64: 40; a
+// window over 7 sequences of 8 KV heads of 64 (56 keys) 17 us, at 64: 22.  At head_dim
+// 256 a CTA has two groups only, which hide less of each other: 4 sequences of 32768
+// rows there (32 keys) 127 us, at 64: 118.
+constexpr int many_keys(int NB) { return NB == 8 ? 64 : 32; }
 // what a change of key costs a group of warps, in cells.  8: 196 us for a batch
 // of 64 (1024 to 16k rows, 8 KV heads of 128), 24: 189, 48: 193; a window of 4096
 // rows over 7 sequences 21.3, 17.2, 17.8
@@ -184,7 +189,7 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     // records to join
     const int warps = split_warps(a.g.NB(), a.tile);
     const long long keys = (long long)a.E * c->cfg.n_kv_heads * ((most + a.tile - 1) / a.tile);
-    a.gw = keys >= kManyKeys ? 4 : warps;
+    a.gw = keys >= many_keys(a.g.NB()) ? 4 : warps;
     a.groups = warps / a.gw;
     a.setup = kSetup;
     a.rec_rows = std::min(a.tile, most);

@@ -553,6 +553,31 @@ def test_two_caches_on_two_streams():
             assert_attention(p, o, want, mag)
 
 
+def test_shared_decodes_on_two_streams():
+    """Both kernels of a shared decode of two caches at once, with appends between."""
+    cases = [shared_case(sizes=[12], prefix=[300], suffix=[1, 40], Hkv=2, Hq=8, D=64, seed=1),
+             shared_case(sizes=[5, 9], prefix=[130, 64], suffix=[9, 2], Hkv=1, Hq=4, D=128, fmt=F8, seed=2)]
+    q = [p.randn(p.n, 1, p.Hq, p.D).to(BF).cuda() for p, _, _ in cases]
+    lens = [p.lens() for p, _, _ in cases]
+    again = [[torch.zeros(p.n, 1, p.Hkv, p.D, device="cuda") for _ in range(2)] for p, _, _ in cases]
+    for (p, _, _), n, (k, v) in zip(cases, lens, again):
+        p.dev.read(p.tables, n, k, v)                # the last rows, to be written over themselves
+    want = [p.dev.decode_shared(x, p.tables, n, st, pre) for (p, st, pre), x, n in zip(cases, q, lens)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(30):
+        for i, (p, st, pre) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                if i == 1:                           # E4M3 rows give their bytes back
+                    p.dev.append(*again[i], p.tables, lens[i])
+                outs[i].append(p.dev.decode_shared(q[i], p.tables, lens[i], st, pre))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+        assert cases[i][0].dev.device_error() == 0
+
+
 @pytest.mark.parametrize("fmt", [Q8, F8])
 def test_a_serving_run(fmt):
     """A shared prompt, its sequences' own prompts, decode steps with rotation, a rollback, sparse and shared decodes."""
