@@ -70,7 +70,7 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     l->page = l->cell * (R / kCellRows) * c->n_kv_heads;
     l->pool = l->page * c->n_pages;
     l->bounds = c->bounds ? round_up((size_t)c->n_pages * c->n_kv_heads * NB * 68, 16) : 0;
-    // record rows of a decode: 16 (8 for f32 queries) for each range, each key of
+    // record rows of a decode: 16 (or 8) for each range, each key of
     // a sequence in whole slices, and the groups' queries, which are their
     // members', in whole slices too
     const size_t Qh = (size_t)(c->max_q_heads / c->n_kv_heads) * c->max_t;
