@@ -429,7 +429,9 @@ typedef struct kvq_paged_query {
 
 /* Decode attention over the pages.  f32 queries keep f32 accuracy (factors
  * split in two or three parts); bf16 queries round probabilities and values
- * (and the keys of a shared prefix) to fp16 inside, sums are f32 throughout. */
+ * to fp16 inside, and so the keys of a shared prefix, scaled by a power of two
+ * for each 32 rows (a key below 2^-28 of the largest of them keeps fewer than
+ * fp16's 11 bits); sums are f32 throughout. */
 kvq_status kvq_paged_decode(kvq_paged* cache, const kvq_paged_query* a, void* stream);
 
 /* The same result for a batch in which groups of sequences share a prefix,

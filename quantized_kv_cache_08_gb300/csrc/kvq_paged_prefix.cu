@@ -8,8 +8,11 @@
 //   P = 2^(s - m), fp16, written over S;
 //   O += P V    (A operand P from tensor memory), f32 in tensor memory.
 // K and V are turned from codes into fp16 tiles in shared memory once for all
-// queries: K as d c 2^-8 (c 2^-8 exact, one rounding; the 2^8 joins the score's
-// factor, so no key that q8_0 can hold overflows), V as u d + m (one rounding).
+// queries: K as (d 2^s) (c 2^-8), both factors exact and one rounding, with s of
+// each 32 rows such that their largest d 2^s lies in [2^15, 2^16): no key overflows,
+// and one of 2^-28 of the largest still has its 11 bits (a fixed power would leave
+// keys around 1e-4 four of them); 2^(8 - s) joins the score's factor.  V as u d + m
+// (one rounding).
 // Both tiles are K-major in the 128-byte swizzle; the rows of a tile are taken in
 // the order in which a lane of the unpacking warps holds them (of 32 rows, place
 // p is row 16 (p/4 % 2) + 8 (p/2 % 2) + 2 (p/8) + p % 2), which makes each lane's
@@ -214,11 +217,48 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// K tile: rows of head_dim / 64 column blocks of 128 bytes; pr: the pair of cells
+// The scales d of a pair of cells, words of two rows: index w of a cell's 8 NB words
+// is rows 8 (w % 2) + 2 (w / (2 NB)) and + 1 of block w / 2 % NB.
+template <int NB>
+struct Scales {
+    static constexpr int N = NB == 8 ? 2 : 1;                 // words of a lane (NB 2: half of the lanes)
+    uint32_t w[2][N];
+    __device__ __forceinline__ void load(const uint8_t* c0, const uint8_t* c1, int lane) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint8_t* cell = c ? c1 : c0;
+                const int at = lane + 32 * i;
+                w[c][i] = 0u;
+                if (cell && at < 8 * NB) w[c][i] = *reinterpret_cast<const uint32_t*>(cell + 512 * NB + 4 * at);
+            }
+    }
+    // s by the largest finite d of the pair's first `rows` rows (those behind may be any bytes)
+    __device__ __forceinline__ int shift(int rows, int lane) const {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = lane + 32 * i, r = 16 * c + 8 * (at & 1) + 2 * (at / (2 * NB));
+                const uint32_t a = w[c][i] & 0x7fffu, b = (w[c][i] >> 16) & 0x7fffu;
+                if (r < rows && a < 0x7c00u) top = max(top, a);
+                if (r + 1 < rows && b < 0x7c00u) top = max(top, b);
+            }
+        return 30 - (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
+    }
+};
+// 2^e as a half pair, 0 <= e <= 15
+__device__ __forceinline__ __half2 pow2_pair(int e) { return as_h2((uint32_t)(15 + e) * 0x04000400u); }
+
+// K tile: rows of head_dim / 64 column blocks of 128 bytes; pr: the pair of cells,
+// shift: their s, 0 .. 30
 template <int NB, int NBT, bool F8>
-__device__ __forceinline__ void store_k(uint32_t tile, int pr, int b0, int lane, Raw<NBT, F8>& r) {
+__device__ __forceinline__ void store_k(uint32_t tile, int pr, int b0, int lane, int shift, Raw<NBT, F8>& r) {
     const int g = lane >> 2, j = lane & 3;
     const uint32_t dsel = (g & 1) ? 0x3232u : 0x1010u, exps = held(0x44444444u);
+    const __half2 up0 = pow2_pair(min(shift, 15)), up1 = pow2_pair(max(shift - 15, 0));
 #pragma unroll 1
     for (int it = 0; it < NBT; ++it) {                        // block pair it / 2, cell it % 2
         const int row0 = 32 * pr + 8 * (g >> 1) + 4 * (it & 1) + (g & 1);
@@ -236,7 +276,7 @@ __device__ __forceinline__ void store_k(uint32_t tile, int pr, int b0, int lane,
                     o[2] = f8_pair(y);
                     o[3] = f8_pair(y >> 16);
                 } else {
-                    const __half2 dd = as_h2(__byte_perm(r.w[8 + 2 * e + t], 0, dsel));
+                    const __half2 dd = __hmul2(__hmul2(as_h2(__byte_perm(r.w[8 + 2 * e + t], 0, dsel)), up0), up1);
                     auto two = [&](uint32_t v, uint32_t sel) {
                         return as_u32(__hmul2(__hsub2(as_h2(__byte_perm(v, exps, sel)), as_h2(0x44804480u)), dd));
                     };
@@ -327,7 +367,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
     __shared__ Barriers bars;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    __shared__ int s_ok[2][4];                                 // cells of a stage that were there, two bits a pair
+    __shared__ int s_ok[2][4];                                 // of each pair of a stage: cells that were there (two bits), s << 2
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (dev::smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t q_tile = base, kv_tile = base + QT * S::tile;
@@ -491,8 +531,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                 }
                 const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -109), 110) : 0;
                 const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
-                // (K tiles hold the keys times 2^-8)
-                fac = a.qscale * __uint_as_float((uint32_t)(127 + ex + (F8 ? 0 : 8)) << 23);
+                fac = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
                 const uint32_t dst = q_tile + qt * S::tile + row * 128;
 #pragma unroll 1
                 for (int i0 = 0; i0 < D / 8; i0 += PER) {
@@ -524,14 +563,14 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                 fence_after();
                 const int row0 = (p.t0 + t) * kTileRows;
                 const int* okc = s_ok[tile_no % ST];
-                const int all = okc[0] & okc[1] & okc[2] & okc[3];
+                const int all = okc[0] & okc[1] & okc[2] & okc[3] & 3;
                 const bool masked = __any_sync(0xffffffffu, row0 < lo || row0 + kTileRows > hi || all != 3);
                 const bool capped = a.softcap_b > 0.f;
                 // Two passes over the scores in 32-column pieces: the largest, then
                 // the probabilities.  Capped or masked scores are worked out in
                 // both, in log2 units; plain ones enter as they are (the factor is
-                // positive) and meet it in the exponent's fma.
-                const float f0 = capped ? 1.f : fac;
+                // positive) and meet it in the exponent's fma.  A piece is a pair of
+                // cells, with its own power of two in the factor.
                 float top = dev::kNegInf, add = 0.f, l0 = 0.f, l1 = 0.f;
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
@@ -540,10 +579,12 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         uint32_t r[32];
                         tmem_ld32(s_addr + 32 * c, r);
                         tmem_wait_ld();
+                        const float fc = F8 ? fac : fac * __uint_as_float((uint32_t)(127 + 8 - (okc[c] >> 2)) << 23);
+                        const float f0 = capped ? 1.f : fc;
                         if (capped) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                r[i] = __float_as_uint(a.softcap_b * tanhf(a.softcap_a * (__uint_as_float(r[i]) * fac)));
+                                r[i] = __float_as_uint(a.softcap_b * tanhf(a.softcap_a * (__uint_as_float(r[i]) * fc)));
                         }
                         if (masked) {
                             const uint32_t see = seen_places(lo - row0 - 32 * c, hi - row0 - 32 * c, okc[c]);
@@ -552,8 +593,10 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                                 if (!((see >> i) & 1u)) r[i] = 0xff800000u;
                         }
                         if (pass == 0) {
+                            float most = dev::kNegInf;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(r[i]));
+                            for (int i = 0; i < 32; ++i) most = fmaxf(most, __uint_as_float(r[i]));
+                            top = fmaxf(top, most * f0);
                         } else {
                             uint32_t pk[16];
 #pragma unroll
@@ -568,7 +611,6 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         }
                     }
                     if (pass == 1) break;
-                    top *= f0;
                     const bool move = top > m + dev::kLazy;
                     if (__any_sync(0xffffffffu, move)) {
                         const float al = move ? ex2(m - top) : 1.f;
@@ -633,6 +675,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
         int tile_no = 0;
         bool ok = true;
         Raw<NBT, F8> raw;
+        Scales<NB> scales;
         const uint8_t *c0 = nullptr, *c1 = nullptr;
         int pages[2];                                          // of the tile after next, on their way
         // page numbers of pair pr of tile t of a part; -2: beyond its rows
@@ -664,6 +707,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
         auto fetch = [&](int part) {
             if (is_v) load_v<NB, NBT, F8>(c0, c1, part * NBT, lane, raw);
             else load_k<NB, NBT, F8>(c0, c1, part * NBT, lane, raw);
+            if (!F8 && !is_v && part == 0) scales.load(c0, c1, lane);
         };
         for (long long x = xs; x < x1 && ok;) {
             const Part p = part_at(x);
@@ -688,12 +732,16 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         keep[i] = (r < rows ? 0x0000ffffu : 0u) | (r + 1 < rows ? 0xffff0000u : 0u);
                     }
                 }
-                if (!is_v && lane == 0) s_ok[st][pr] = (c0 || rows <= 0 ? 1 : 0) | (c1 || rows <= 16 ? 2 : 0);
+                int shift = 0;
+                if (!is_v) {
+                    if (!F8) shift = scales.shift(rows, lane);
+                    if (lane == 0) s_ok[st][pr] = (c0 || rows <= 0 ? 1 : 0) | (c1 || rows <= 16 ? 2 : 0) | shift << 2;
+                }
 #pragma unroll 1
                 for (int part = 0; part < NQ4; ++part) {
                     if (part > 0) fetch(part);
                     if (is_v) store_v<NB, NBT, F8>(tile, pr, part * NBT, lane, keep, raw);
-                    else store_k<NB, NBT, F8>(tile, pr, part * NBT, lane, raw);
+                    else store_k<NB, NBT, F8>(tile, pr, part * NBT, lane, shift, raw);
                 }
                 if (t + 1 < p.tb) {
                     find(p, t + 1);

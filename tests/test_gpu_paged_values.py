@@ -1,0 +1,93 @@
+"""Paged cache on the GPU: values at the ends of their ranges (keys and values
+far from 1, numbers that are not finite, extreme scales and windows), against
+the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kvq_paged_oracle as P
+from tests.paged_testutil import PagedPair
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+Q8, F8 = "q8_0/q5_1", "e4m3"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def prefix_pair(n, rows, suffix, D=128, Hkv=1, Hq=4, page=16, ks=1.0, vs=1.0, fmt=Q8, seed=0, **kw):
+    """n sequences whose first `rows` rows (whole pages) are the same pages."""
+    p = PagedPair(n, Hkv, D, Hq, page=page, max_pages=-(-(rows + suffix) // page), fmt=fmt, seed=seed, **kw)
+    assert rows % page == 0
+    p.tab[1:, :rows // page] = p.tab[0, :rows // page]
+    p.tables = torch.from_numpy(p.tab).cuda()
+    k, v = p.randn(rows, Hkv, D) * ks, p.randn(rows, Hkv, D) * vs
+    for b in range(n):
+        p.note(b, k.numpy(), v.numpy())
+    p.dev.append(k[None].cuda(), v[None].cuda(), p.tables[:1], i32([rows]))
+    k, v = p.randn(n, suffix, Hkv, D) * ks, p.randn(n, suffix, Hkv, D) * vs
+    for b in range(n):
+        p.note(b, k[b].numpy(), v[b].numpy())
+    p.dev.append(k.cuda(), v.cuda(), p.tables, p.lens())
+    return p
+
+
+def assert_bf16(p, q, got, want, mag, scale):
+    """The output's rounding (2^-8), fp16 roundings of p and v (2^-11 each of p |v|) with as much again for
+    sums and records, and keys as fp16: each off by 2^-11 of itself at most, a score so by d = 2^-11 of
+    sum |q k| scale, and an output by at most 2 d sum p |v|."""
+    qf, hpk = q.double().numpy(), p.Hq // p.Hkv
+    a = np.zeros(want.shape[:3] + (1,))
+    for b in range(p.n):
+        for h in range(p.Hq):
+            a[b, :, h, 0] = (np.abs(qf[b, :, h]) @ np.abs(p.k[b][:, h // hpk]).T).max(-1)
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -9 + 2.0 ** -10 * a * scale) * mag + 1e-30
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), f"worst ratio {np.nanmax(err / tol):.2f}"
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 8), (128, 4), (256, 4)])
+@pytest.mark.parametrize("ks", [1e4, 30.0, 1.0, 1e-2, 1e-4, 1e-5, 1e-6])
+def test_shared_prefix_of_keys_far_from_one(D, Hq, ks):
+    """Keys of any size that the format holds, scores of the same size all the same."""
+    p = prefix_pair(10, 160, 3, D=D, Hq=Hq, ks=ks, seed=D)
+    q = p.randn(10, 1, Hq, D).to(BF)
+    scale = 1.5 / (ks * D ** 0.5)
+    want, mag = p.want(q, scale=scale)
+    args = (q.cuda(), p.tables, p.lens())
+    assert_bf16(p, q, p.dev.decode(*args, scale=scale), want, mag, scale)
+    assert_bf16(p, q, p.dev.decode_shared(*args, i32([0, 10]), i32([160]), scale=scale), want, mag, scale)
+
+
+def test_shared_prefix_of_keys_unlike_each_other():
+    """Rows 32 and more apart, and blocks of a row, from 1e-5 to 1e3 in one prefix."""
+    D, rows = 128, 256
+    p = prefix_pair(10, rows, 3, D=D, seed=5)
+    size = 10.0 ** torch.linspace(-5, 3, 8)
+    k = p.randn(rows, 1, D) * size.repeat_interleave(32)[:, None, None]
+    k[:, :, :32] *= 1e-3                                 # (one block of each row)
+    v = p.randn(rows, 1, D)
+    kb, vb = P.blocks(k.numpy(), Q8, "k"), P.blocks(v.numpy(), Q8, "v")
+    for b in range(p.n):
+        p.k[b][:rows], p.v[b][:rows] = P.values(kb, Q8, "k"), P.values(vb, Q8, "v")
+    p.dev.append(k[None].cuda(), v[None].cuda(), p.tables[:1], i32([rows]))
+    q = p.randn(10, 1, 4, D).to(BF)
+    args = (p.tables, p.lens(), i32([0, 10]), i32([rows]))
+    for only in range(8):
+        # the other rows are not seen: a window over one stretch of 32, by sequences that end there
+        lens = i32([32 * only + 32] * 10)
+        scale = 1.5 / (float(size[only]) * D ** 0.5)
+        want, mag = np.zeros((10, 1, 4, D)), np.zeros((10, 1, 4, D))
+        at = slice(32 * only, 32 * only + 32)
+        a = 0.0
+        for b in range(10):
+            for h in range(4):
+                x = q[b, 0, h].double().numpy()
+                want[b, 0, h], mag[b, 0, h] = P.attend(x, p.k[b][at, 0], p.v[b][at, 0], np.ones(32, np.int64), scale)
+                a = max(a, float((np.abs(x) @ np.abs(p.k[b][at, 0]).T).max()) * scale)
+        got = p.dev.decode_shared(q.cuda(), p.tables, lens, *args[2:], scale=scale, window=32)
+        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -9 + 2.0 ** -10 * a) * mag
+        assert (np.abs(got.double().cpu().numpy() - want) <= tol).all(), only
