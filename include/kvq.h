@@ -431,7 +431,8 @@ typedef struct kvq_paged_query {
  * split in two or three parts); bf16 queries round probabilities and values
  * to fp16 inside, and so the keys of a shared prefix, scaled by a power of two
  * for each 32 rows (a key below 2^-28 of the largest of them keeps fewer than
- * fp16's 11 bits); sums are f32 throughout. */
+ * fp16's 11 bits); a shared prefix's partial outputs are kept as fp16 scaled by
+ * a power of two for each query; sums are f32 throughout. */
 kvq_status kvq_paged_decode(kvq_paged* cache, const kvq_paged_query* a, void* stream);
 
 /* The same result for a batch in which groups of sequences share a prefix,

@@ -222,8 +222,8 @@ struct SplitArgs {
     int tiles;                     // 1: groups with many queries go to the tile kernel
     int tile_rows;                 // queries of its blocks
     long long max_keys2;           // its keys that the record area holds
-    uint16_t* part2_o;             // [CTA + key][tile_rows][D] fp16, divided by the sum
-    float* part2_ml;               // [CTA + key][tile_rows][2]
+    uint16_t* part2_o;             // [CTA + key][tile_rows][D] fp16, times a power of two for each row
+    float* part2_ml;               // [CTA + key][tile_rows][4]  (max, sum, what takes the power out again, -)
     struct PlanEntry* plan2;       // [n_groups + 1]
 };
 // Work before an entry ((cells + setup) x slices), keys before it (slices), its

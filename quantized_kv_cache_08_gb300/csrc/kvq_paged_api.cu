@@ -88,7 +88,7 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     l->keys2 = (size_t)c->n_kv_heads * (total_q / tr + std::min<size_t>(c->max_seqs, total_q / 9) + 1);
     const size_t recs2 = total_q > 8 ? (kMaxGrid + l->keys2) * tr : 0;
     l->ml2 = round_up(l->o + recs * D * 4, 256);
-    l->o2 = round_up(l->ml2 + recs2 * 8, 256);
+    l->o2 = round_up(l->ml2 + recs2 * 16, 256);
     l->keys = round_up(l->o2 + recs2 * D * 2, 256);
     l->total = l->keys;
     if (c->bounds)

@@ -577,25 +577,30 @@ __device__ __forceinline__ void add_sum(Sum4& s, float M, float L, const float4&
     s.o.z = s.o.z * x + o.z * y;
     s.o.w = s.o.w * x + o.w * y;
 }
-// (kHalf: the prefix tiles' records, fp16 and divided by their sums)
+// (kHalf: the prefix tiles' records, fp16 times a power of two)
 template <int D, bool kHalf = false>
 __device__ __forceinline__ void add_records(const SplitArgs& a, Sum4& s, long long slot0, int first, int last, int step, int row, int col) {
     constexpr int U = 8;                               // records in flight
     for (int r0 = first; r0 < last; r0 += U * step) {
         float2 ml[U];
+        float back[U];
         float4 o[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             ml[i] = make_float2(kNegInf, 0.f);
+            back[i] = 1.f;
             o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r0 + i * step < last) {
                 const long long at = (slot0 + r0 + i * step) * (kHalf ? a.tile_rows : a.rec_rows) + row;
-                ml[i] = __ldcg(reinterpret_cast<const float2*>(kHalf ? a.part2_ml : a.part_ml) + at);
                 if constexpr (kHalf) {
+                    const float4 x4 = __ldcg(reinterpret_cast<const float4*>(a.part2_ml) + at);
+                    ml[i] = make_float2(x4.x, x4.y);
+                    back[i] = x4.z;
                     const uint2 h = __ldcg(reinterpret_cast<const uint2*>(a.part2_o + at * D + col));
                     const float2 x = __half22float2(as_h2(h.x)), y = __half22float2(as_h2(h.y));
                     o[i] = make_float4(x.x, x.y, y.x, y.y);
                 } else {
+                    ml[i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
                     o[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
                 }
             }
@@ -612,7 +617,7 @@ __device__ __forceinline__ void add_records(const SplitArgs& a, Sum4& s, long lo
         for (int i = 0; i < U; ++i) {
             const float w = ml[i].x == kNegInf ? 0.f : ex2(ml[i].x - m);
             s.L = fmaf(ml[i].y, w, s.L);
-            const float v = kHalf ? ml[i].y * w : w;
+            const float v = kHalf ? back[i] * w : w;
             s.o.x = fmaf(o[i].x, v, s.o.x);
             s.o.y = fmaf(o[i].y, v, s.o.y);
             s.o.z = fmaf(o[i].z, v, s.o.z);

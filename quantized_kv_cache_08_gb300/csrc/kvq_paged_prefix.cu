@@ -650,7 +650,20 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                 fence_after();
                 const long long slot = blockIdx.x + (long long)p.keys * a.g.Hkv + p.kk;
                 const long long at = slot * QB + qt * 128 + row;
-                const float inv = l > 0.f ? 1.0f / l : 0.f;    // fp16 records hold O / l, no larger than the values
+                // fp16 records hold O times the power of two that brings its largest
+                // element into [2^14, 2^15): eleven bits for each that is not below 2^-28
+                // of it, where O / l would leave values around 1e-5 few
+                float most = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(o_addr + 32 * c, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) most = fmaxf(most, fabsf(__uint_as_float(r[i])));
+                }
+                const uint32_t ue = min(268u - (__float_as_uint(most) >> 23), 253u);
+                const float inv = __uint_as_float(ue << 23), back = __uint_as_float((254u - ue) << 23);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t r[32];
@@ -663,7 +676,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         for (int i = 0; i < 4; ++i) dst[i] = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
                     }
                 }
-                if (valid) *reinterpret_cast<float2*>(a.part2_ml + at * 2) = make_float2(l > 0.f ? m - kShift : dev::kNegInf, l);
+                if (valid) *reinterpret_cast<float4*>(a.part2_ml + at * 4) = make_float4(l > 0.f ? m - kShift : dev::kNegInf, l, back, 0.f);
                 fence_before();
             }
         }

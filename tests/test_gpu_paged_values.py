@@ -91,3 +91,15 @@ def test_shared_prefix_of_keys_unlike_each_other():
         got = p.dev.decode_shared(q.cuda(), p.tables, lens, *args[2:], scale=scale, window=32)
         tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -9 + 2.0 ** -10 * a) * mag
         assert (np.abs(got.double().cpu().numpy() - want) <= tol).all(), only
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 8), (128, 4), (256, 4)])
+@pytest.mark.parametrize("vs", [1e4, 1.0, 1e-4, 1e-5, 1e-6])
+def test_shared_prefix_of_values_far_from_one(D, Hq, vs):
+    """A query of zeros takes the mean of the values: no key's rounding is in it."""
+    p = prefix_pair(10, 160, 3, D=D, Hq=Hq, vs=vs, seed=D)
+    q = torch.zeros(10, 1, Hq, D, dtype=BF)
+    want, mag = p.want(q)
+    args = (q.cuda(), p.tables, p.lens())
+    assert_bf16(p, q, p.dev.decode(*args), want, mag, 1.0)
+    assert_bf16(p, q, p.dev.decode_shared(*args, i32([0, 10]), i32([160])), want, mag, 1.0)
