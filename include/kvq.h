@@ -392,10 +392,10 @@ void kvq_paged_free(kvq_paged* cache);
  * rotated likewise into q_out, dense [rows][Hq][D]; q_out may be q when q is
  * dense.  With cfg.bounds the bounds of the pages that got rows are renewed
  * from all rows below the length.  A page that gets rows belongs to one entry.
- * Stored values are finite: a q5_1 block's ends stay within +-65280, a NaN is
- * stored as its block's least value (a block of NaN as zeros), in E4M3 as zero.
- * Keys that are not finite make the scores of the queries that see them NaN,
- * and no others. */
+ * Stored rows are finite: a q8_0 key stays within +-8319008 (127 x 65504), a
+ * q5_1 block's ends within +-65280, E4M3 within +-448, what lies beyond (an
+ * infinity too) is stored as that end.  A NaN is stored as zero, in q5_1 as its
+ * block's least value (a block of NaN as zeros). */
 kvq_status kvq_paged_append(kvq_paged* cache, const void* k, long long k_stride, const void* v, long long v_stride,
                             const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,
                             const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,

@@ -96,9 +96,11 @@ __device__ __forceinline__ unsigned short half_quotient(float num, float err, fl
     return __half_as_ushort(__float2half_rn(q));
 }
 
-// Stored values are finite whatever comes in: a row that one query does not see
+// Stored rows are finite whatever comes in: a row that one query does not see
 // meets it with weight 0 in the same matrix product as the queries that see it,
-// and 0 x inf would reach its output.  A q5_1 block's ends stay within +-65280, so
+// and 0 x inf would reach its output; and a key's scores are numbers for every
+// query.  A q8_0 element stays within +-kKeyEnd, the largest that a scale of fp16
+// holds, a NaN is zero.  A q5_1 block's ends stay within +-65280, so
 // that 31 d + m with d rounded up (by 2^-12, here up to 64 in all) stays below
 // fp16's 65504; an infinite element takes the code at that end, a NaN the lowest, a
 // block of NaN is zeros.  An E4M3 NaN is zero.
@@ -108,6 +110,7 @@ __device__ __forceinline__ void bound_block(float& least, float& most) {
     most = fminf(fmaxf(most, -65280.f), 65280.f);
 }
 __device__ __forceinline__ float number(float x) { return x == x ? x : 0.f; }
+constexpr float kKeyEnd = 65504.f * 127.f;
 
 // The rotation table of a token holds (cos, sin) of pair p at place
 // (p % 8) (n / 8) + p / 8 (4 for interleaved pairs) of n: the lanes of a load,
@@ -383,13 +386,23 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
             if (a.g.fp8) {
 #pragma unroll
                 for (int i = 0; i < 8; i += 2)
-                    w2[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[i], x[i + 1]), __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
+                    w2[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(number(x[i]), number(x[i + 1])), __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
             } else {
-                float m = 0.f;
+                // the largest |element|, by its bits: NaN lies above infinity
+                auto largest = [&]() {
+                    uint32_t m = 0u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    return __uint_as_float(m);
+                };
+                float m = largest();
+                if (__any_sync(0xffffffffu, !(m <= kKeyEnd))) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(number(x[i]), -kKeyEnd), kKeyEnd);
+                    m = largest();
+                }
                 const unsigned short db = half_quotient(m, 0.f, 127.f);
                 int code[8];
                 kd = __half2float(__ushort_as_half(db));
@@ -567,9 +580,8 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
                         for (int i = 0; i < 8; ++i) x[8 * k + i] = v[i];
                     }
                 }
-                if (kind)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = number(x[i]);
+                for (int i = 0; i < 32; ++i) x[i] = number(x[i]);
                 uint32_t w[8];                       // elements 4 g ..
 #pragma unroll
                 for (int g = 0; g < 8; ++g)

@@ -12,6 +12,7 @@ from tests.paged_testutil import PagedPair
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 Q8, F8 = "q8_0/q5_1", "e4m3"
+NAN, INF = float("nan"), float("inf")
 
 
 def i32(x):
@@ -103,3 +104,34 @@ def test_shared_prefix_of_values_far_from_one(D, Hq, vs):
     args = (q.cuda(), p.tables, p.lens())
     assert_bf16(p, q, p.dev.decode(*args), want, mag, 1.0)
     assert_bf16(p, q, p.dev.decode_shared(*args, i32([0, 10]), i32([160])), want, mag, 1.0)
+
+
+# ------------------------------------------------------------------ numbers that are not finite
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fmt", [Q8, F8])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF, 1e30, -1e7])
+@pytest.mark.parametrize("many", [1, 9])
+def test_keys_that_are_not_finite_are_stored_as_the_header_says(dtype, fmt, bad, many):
+    """One element, a block, a row; few rows and many: what is read back is finite, NaN as zero and the rest at the
+    format's end, and the rows that see them attend to that."""
+    D, n, page = 64, 3, 16
+    p = PagedPair(n, 1, D, 4, page=page, max_pages=3, fmt=fmt, bounds=True, seed=many)
+    k, v = p.randn(n, many, 1, D).to(dtype), p.randn(n, many, 1, D).to(dtype)
+    for b, cut in enumerate((slice(37, 38), slice(32, 64), slice(0, 64))):
+        k[b, -1, :, cut] = bad
+    end = 448.0 if fmt == F8 else 65504.0 * 127
+    clean = torch.nan_to_num(k.float(), nan=0.0, posinf=end, neginf=-end).clamp(-end, end)
+    for b in range(n):
+        p.note(b, clean[b].numpy(), v[b].float().numpy())
+    p.dev.append(k.cuda(), v.cuda(), p.tables, p.lens())
+    assert np.array_equal(p.dev.pool.cpu().numpy(), p.expected_pool())
+    bounds = p.dev.bounds.clone()
+    p.dev.update_bounds(p.tables, p.lens(), many)
+    assert torch.equal(p.dev.bounds, bounds)
+    q = (p.randn(n, 1, 4, D) * 1e-3).to(dtype)
+    want, mag = p.want(q, scale=1e-4)
+    for o in (p.dev.decode(q.cuda(), p.tables, p.lens(), scale=1e-4),
+              p.dev.decode_shared(q.cuda(), p.tables, p.lens(), i32([0, 1, 2, 3]), i32([0, 0, 0]), scale=1e-4)):
+        assert_bf16(p, q, o, want, mag, 1e-4)
+    assert p.dev.device_error() == 0
