@@ -339,7 +339,8 @@ kvq_status kvq_set_split_rows(kvq_cache* cache, int rows);
  * page_rows sets the device error word to 1: appends skip the row, decodes
  * take a bad page's rows as masked and a bad sequence as empty.  A query row
  * that sees no row (a sequence of length 0, a position below 0) gives zeros,
- * with or without a sink.  Calls on one cache share its workspace: order them
+ * with or without a sink; one that is not finite, or whose score of a row
+ * overflows f32, gives NaN where it sees a row, and leaves all others as they are.  Calls on one cache share its workspace: order them
  * on one stream (captured graphs that share a cache included). */
 typedef struct kvq_paged_config {
     int n_pages;         /* pages in the pool                                     */

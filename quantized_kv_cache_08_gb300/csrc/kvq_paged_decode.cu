@@ -106,6 +106,7 @@ struct Acc {
 struct RowInfo {
     float fac[16];
     int lo[16], hi[16];
+    int bad[16];                                          // not finite
 };
 
 // What a lane keeps of them: queries g (+ 8), and the extremes over all
@@ -683,24 +684,25 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         for (int i = 0; i < RPW; ++i) {
             const int r = gwarp + i * gw;
             if (r >= QPI) break;
-            float am = 0.f;
+            uint32_t am = 0u;                              // bits of the largest |element|: NaN above infinity
 #pragma unroll
-            for (int b = 0; b < NB; ++b) am = fmaxf(am, fabsf(qv[i][b]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            for (int b = 0; b < NB; ++b) am = max(am, __float_as_uint(qv[i][b]) & 0x7fffffffu);
+            am = __reduce_max_sync(0xffffffffu, am);
+            const bool bad = am >= kInfBits;
             // scaled by a power of two to a largest element in [512, 1024)
-            const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -117), 118) : 0;
+            const int ex = am > 0u && !bad ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
             const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
             if (lane == 0) {
                 ri.fac[r] = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
                 ri.lo[r] = qq[i].lo;
                 ri.hi[r] = qq[i].hi;
+                ri.bad[r] = bad;
             }
             const int wi = lane & 7, j = lane >> 3;
             const int reg = ((wi & 3) >> 1) * 2, half = wi & 1;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const float y = qv[i][b] * up;
+                const float y = bad ? 0.f : qv[i][b] * up;
                 const __half hi = __float2half_rn(y);
                 const int at = ((HL ? (r >> 3) * 2 * NB : 0) + 2 * b + (wi >> 2)) * 32 + 4 * (r & 7) + j;
                 __half* dst = reinterpret_cast<__half*>(qs + at * 16);
@@ -1003,7 +1005,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             float l = 0.f;
 #pragma unroll 4
             for (int w = w0; w < w0 + gw; ++w) l = fmaf(s_l[w][row], ex2(s_m[w][row] - m), l);
-            const float M = l > 0.f ? m - kShift : kNegInf;
+            const float M = settle(l, m, ri.bad[row]) ? m - kShift : kNegInf;
             if (whole) {
                 const Query q = query_of(a, plan[f.e], f.e, f.kh, f.sl * QPI + row);
                 store4(a, (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + col, o, sink_weight(sink_of(a, q.h), M, l));

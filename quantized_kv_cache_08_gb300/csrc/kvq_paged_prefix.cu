@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
             const int qi = p.qb * QB + qt * 128 + row;
             const bool valid = qi < p.nq, tile_on = p.qb * QB + qt * 128 < p.nq;
             float fac = 1.f;
+            bool bad = false;
             int lo = 0, hi = 0x7fffffff;
             {
                 // the query, scaled by a power of two to a largest element in [512, 1024), as fp16
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
 #pragma unroll
                     for (int i = 0; i < PER; ++i) v[i] = valid ? src[i0 + i] : make_uint4(0u, 0u, 0u, 0u);
                 };
-                float am = 0.f;
+                uint32_t am = 0u;                              // bits of the largest |element|: NaN above infinity
 #pragma unroll 1
                 for (int i0 = D / 8 - PER; i0 >= 0; i0 -= PER) {
                     load(i0);
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                            am = max(am, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
                     }
                 }
                 if (valid) {
@@ -529,7 +530,8 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                     hi = min(end, p.hi);
                     lo = a.window > 0 ? max(0, end - a.window) : 0;
                 }
-                const int ex = am > 0.f ? min(max((int)(__float_as_uint(am) >> 23) - 127 - 9, -109), 110) : 0;
+                bad = am >= kInfBits;
+                const int ex = am > 0u && !bad ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
                 const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
                 fac = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
                 const uint32_t dst = q_tile + qt * S::tile + row * 128;
@@ -539,7 +541,8 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
 #pragma unroll
                     for (int k = 0; k < PER; ++k) {
                         const int i = i0 + k;
-                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        const uint32_t keep = bad ? 0u : 0xffffffffu;
+                        const uint32_t w[4] = {v[k].x & keep, v[k].y & keep, v[k].z & keep, v[k].w & keep};
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -676,7 +679,8 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         for (int i = 0; i < 4; ++i) dst[i] = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
                     }
                 }
-                if (valid) *reinterpret_cast<float4*>(a.part2_ml + at * 4) = make_float4(l > 0.f ? m - kShift : dev::kNegInf, l, back, 0.f);
+                const bool seen = settle(l, m, bad);
+                if (valid) *reinterpret_cast<float4*>(a.part2_ml + at * 4) = make_float4(seen ? m - kShift : dev::kNegInf, l, back, 0.f);
                 fence_before();
             }
         }

@@ -17,6 +17,18 @@ using dev::kNegInf;
 constexpr float kShift = 6.0f;         // p is held as 2^6 p: fp16 keeps 2^-20 of the largest in full
 constexpr int kMaxStages = 8;
 constexpr float kNone = -1e30f;        // reference of a query that has seen no row: any score passes it
+constexpr float kInf = __builtin_huge_valf();
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Sum of a fragment's weights as its record has it, and whether the query saw a row.
+// A query that is not finite goes through the products as zeros (`bad`) and a score
+// that overflows leaves the reference at infinity: both make the sum NaN, which every
+// join keeps, so that the output is NaN however the work was cut.
+__device__ __forceinline__ bool settle(float& l, float m, bool bad) {
+    const bool seen = l > 0.f || m == kInf;
+    if (seen && (bad || m == kInf)) l = __uint_as_float(0x7fffffffu);
+    return seen;
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -110,6 +110,62 @@ def test_shared_prefix_of_values_far_from_one(D, Hq, vs):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("fmt", [Q8, F8])
+@pytest.mark.parametrize("rows", [16, 1600])
+def test_a_query_of_nan_gives_nan_however_the_work_is_cut(dtype, fmt, rows):
+    """One range a key, many ranges, listed pages, a shared prefix: NaN for that head, numbers for the others."""
+    p = prefix_pair(3, rows, 5, D=64, Hkv=1, Hq=12, fmt=fmt, bounds=True, seed=rows)
+    q = p.randn(3, 1, 12, 64).to(dtype).cuda()
+    q[1, 0, 7, 3] = NAN
+    lens = p.lens()
+    pages = i32(np.tile(np.arange(p.max_pages), (3, 1, 1, 1)).tolist())
+    outs = [p.dev.decode(q, p.tables, lens), p.dev.decode_sparse(q, p.tables, lens, pages),
+            p.dev.decode(q, p.tables, lens, sinks=torch.zeros(12, device="cuda")),
+            p.dev.decode_shared(q, p.tables, lens, i32([0, 3]), i32([rows])),
+            p.dev.decode_shared(q, p.tables, lens, i32([0, 3]), i32([rows]), softcap=5.0)]
+    for i, o in enumerate(outs):
+        assert torch.isnan(o[1, 0, 7]).all(), i
+        o[1, 0, 7] = 0
+        assert torch.isfinite(o).all(), i
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fmt", [Q8, F8])
+@pytest.mark.parametrize("rows", [16, 1600])
+def test_a_score_that_overflows_gives_nan_however_the_work_is_cut(dtype, fmt, rows):
+    """The largest queries over keys of one sign: in the prefix alone, among a sequence's own rows alone."""
+    for where in ("prefix", "own"):
+        p = PagedPair(2, 1, 64, 12, page=16, max_pages=rows // 16 + 1, fmt=fmt, bounds=True, seed=rows)
+        p.tab[1:, :rows // 16] = p.tab[0, :rows // 16]
+        p.tables = torch.from_numpy(p.tab).cuda()
+        k, v = p.randn(2, rows + 5, 1, 64), p.randn(2, rows + 5, 1, 64)
+        k[1], v[1, :rows] = k[0], v[0, :rows]
+        k[:, slice(3, 4) if where == "prefix" else slice(rows + 2, rows + 3)] = 400.0
+        k[:, rows + 3] = 0.0
+        p.dev.append(k.cuda(), v.cuda(), p.tables, i32([rows + 5] * 2))
+        q = p.randn(2, 1, 12, 64)
+        q[1, 0, 7] = 3e38
+        q, lens = q.to(dtype).cuda(), i32([rows + 5] * 2)
+        pages = i32(np.tile(np.arange(p.max_pages), (2, 1, 1, 1)).tolist())
+        for i, o in enumerate((p.dev.decode(q, p.tables, lens), p.dev.decode_sparse(q, p.tables, lens, pages),
+                               p.dev.decode_shared(q, p.tables, lens, i32([0, 2]), i32([rows])))):
+            assert torch.isnan(o[1, 0, 7]).all(), (where, i)
+            o[1, 0, 7] = 0
+            assert torch.isfinite(o).all(), (where, i)
+
+
+def test_a_query_that_is_not_finite_and_sees_no_row_gives_zeros():
+    p = prefix_pair(3, 16, 2, D=64, Hq=12, max_t=4)
+    q = p.randn(3, 4, 12, 64)
+    q[0, 0], q[0, 3] = NAN, INF
+    for dtype in (BF, F32):
+        x, lens = q.to(dtype).cuda(), i32([2, 18, 18])
+        for o in (p.dev.decode(x, p.tables, lens), p.dev.decode_shared(x, p.tables, lens, i32([0, 3]), i32([16]))):
+            assert (o[0, :2] == 0).all() and torch.isfinite(o[0, 2]).all() and torch.isnan(o[0, 3]).all()
+            assert torch.isfinite(o[1:]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fmt", [Q8, F8])
 @pytest.mark.parametrize("bad", [NAN, INF, -INF, 1e30, -1e7])
 @pytest.mark.parametrize("many", [1, 9])
 def test_keys_that_are_not_finite_are_stored_as_the_header_says(dtype, fmt, bad, many):
