@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             const int ex = am > 0u && !bad ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
             const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
             if (lane == 0) {
-                ri.fac[r] = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
+                ri.fac[r] = factor(a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23));
                 ri.lo[r] = qq[i].lo;
                 ri.hi[r] = qq[i].hi;
                 ri.bad[r] = bad;

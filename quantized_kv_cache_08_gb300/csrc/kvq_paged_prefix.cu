@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
             x += p.tb - p.ta;
             const int qi = p.qb * QB + qt * 128 + row;
             const bool valid = qi < p.nq, tile_on = p.qb * QB + qt * 128 < p.nq;
-            float fac = 1.f;
+            int ex = 0;                                        // the query times 2^-ex is in the tile
             bool bad = false;
             int lo = 0, hi = 0x7fffffff;
             {
@@ -531,9 +531,8 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                     lo = a.window > 0 ? max(0, end - a.window) : 0;
                 }
                 bad = am >= kInfBits;
-                const int ex = am > 0u && !bad ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
+                ex = am > 0u && !bad ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
                 const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
-                fac = a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23);
                 const uint32_t dst = q_tile + qt * S::tile + row * 128;
 #pragma unroll 1
                 for (int i0 = 0; i0 < D / 8; i0 += PER) {
@@ -582,7 +581,8 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         uint32_t r[32];
                         tmem_ld32(s_addr + 32 * c, r);
                         tmem_wait_ld();
-                        const float fc = F8 ? fac : fac * __uint_as_float((uint32_t)(127 + 8 - (okc[c] >> 2)) << 23);
+                        const int e2 = max(F8 ? ex : ex + 8 - (okc[c] >> 2), -126);
+                        const float fc = factor(a.qscale * __uint_as_float((uint32_t)(127 + e2) << 23));
                         const float f0 = capped ? 1.f : fc;
                         if (capped) {
 #pragma unroll

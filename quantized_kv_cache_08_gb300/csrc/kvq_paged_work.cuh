@@ -20,6 +20,11 @@ constexpr float kNone = -1e30f;        // reference of a query that has seen no 
 constexpr float kInf = __builtin_huge_valf();
 constexpr uint32_t kInfBits = 0x7f800000u;
 
+// A score's factor inside f32's normal numbers: 0 x -inf (a masked row) and 0 x inf
+// (a key of zeros) would be NaN.  Scores that the bounds move are far below any
+// rounding, or beyond f32 unless they are 0.
+__device__ __forceinline__ float factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 3.402823466e38f); }
+
 // Sum of a fragment's weights as its record has it, and whether the query saw a row.
 // A query that is not finite goes through the products as zeros (`bad`) and a score
 // that overflows leaves the reference at infinity: both make the sum NaN, which every

@@ -191,3 +191,26 @@ def test_keys_that_are_not_finite_are_stored_as_the_header_says(dtype, fmt, bad,
               p.dev.decode_shared(q.cuda(), p.tables, p.lens(), i32([0, 1, 2, 3]), i32([0, 0, 0]), scale=1e-4)):
         assert_bf16(p, q, o, want, mag, 1e-4)
     assert p.dev.device_error() == 0
+
+
+# ------------------------------------------------------------------ ends of the arguments' ranges
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("att", [{}, dict(softcap=2.0)])
+def test_scales_and_queries_at_the_ends_of_their_ranges(dtype, att):
+    """Scores that vanish, masked rows among them, are zeros: the mean of the visible values.  So are scores of
+    zero keys under the largest factors."""
+    p = prefix_pair(10, 144, 3, D=128, Hq=4)
+    q = p.randn(10, 1, 4, 128)
+    args = (p.tables, p.lens(), i32([0, 10]), i32([144]))
+    want, mag = p.want(torch.zeros_like(q))
+    calls = [(1e-30, (q * 1e-15).to(dtype)), (1e-30, (q * 1e-30).to(dtype)), (1e-30, torch.zeros_like(q).to(dtype))]
+    z = prefix_pair(10, 144, 3, D=128, Hq=4, ks=0.0)
+    for scale, x in calls:
+        for got in (p.dev.decode(x.cuda(), *args[:2], scale=scale, **att), p.dev.decode_shared(x.cuda(), *args, scale=scale, **att)):
+            assert_bf16(p, torch.zeros_like(q), got, want, mag, 1.0)
+    want, mag = z.want(torch.zeros_like(q))
+    x = (q * 1e36).clamp(-3e38, 3e38).to(dtype)
+    for got in (z.dev.decode(x.cuda(), z.tables, z.lens(), scale=1e30, **att),
+                z.dev.decode_shared(x.cuda(), z.tables, z.lens(), *args[2:], scale=1e30, **att)):
+        assert_bf16(z, torch.zeros_like(q), got, want, mag, 1.0)
