@@ -572,8 +572,11 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                 // the probabilities.  Capped or masked scores are worked out in
                 // both, in log2 units; plain ones enter as they are (the factor is
                 // positive) and meet it in the exponent's fma.  A piece is a pair of
-                // cells, with its own power of two in the factor.
+                // cells, with its own power of two in the factor.  Where the reference
+                // is so large that its last bits show in the fma's exact product (2^-24
+                // of it; from 2^27 on p would overflow), plain scores are rounded first.
                 float top = dev::kNegInf, add = 0.f, l0 = 0.f, l1 = 0.f;
+                bool large = false;
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -583,11 +586,14 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         tmem_wait_ld();
                         const int e2 = max(F8 ? ex : ex + 8 - (okc[c] >> 2), -126);
                         const float fc = factor(a.qscale * __uint_as_float((uint32_t)(127 + e2) << 23));
-                        const float f0 = capped ? 1.f : fc;
+                        const float f0 = capped || large ? 1.f : fc;
                         if (capped) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 r[i] = __float_as_uint(a.softcap_b * tanhf(a.softcap_a * (__uint_as_float(r[i]) * fc)));
+                        } else if (large) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fc);
                         }
                         if (masked) {
                             const uint32_t see = seen_places(lo - row0 - 32 * c, hi - row0 - 32 * c, okc[c]);
@@ -636,6 +642,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) prefix_kernel(const __
                         }
                     }
                     add = kShift - m;
+                    large = __any_sync(0xffffffffu, fabsf(m) > 1048576.f && m != kNone);
                 }
                 if (!ok) break;
                 l += l0 + l1;

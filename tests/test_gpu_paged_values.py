@@ -214,3 +214,29 @@ def test_scales_and_queries_at_the_ends_of_their_ranges(dtype, att):
     for got in (z.dev.decode(x.cuda(), z.tables, z.lens(), scale=1e30, **att),
                 z.dev.decode_shared(x.cuda(), z.tables, z.lens(), *args[2:], scale=1e30, **att)):
         assert_bf16(z, torch.zeros_like(q), got, want, mag, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,ks,qs,scale", [(128, 1e4, 1e4, 0.0), (64, 3e3, 1e6, 1.0), (256, 1e6, 1e25, 1.0), (128, 1e-6, 1e38, 4096.0)])
+def test_scores_far_apart_leave_the_largest_alone(D, ks, qs, scale, dtype):
+    """Scores of 1e8 to 1e37: the row of the largest takes all, where the next one is further from it than the
+    keys' roundings to fp16 can be (2^-11 of sum |q k| each)."""
+    p = prefix_pair(10, 144, 3, D=D, Hq=4, ks=ks, seed=D)
+    q = (p.randn(10, 1, 4, D) * qs).clamp(-3e38, 3e38).to(dtype)
+    more = (i32([0, 10]), i32([144]))
+    outs = (p.dev.decode(q.cuda(), p.tables, p.lens(), scale=scale),
+            p.dev.decode_shared(q.cuda(), p.tables, p.lens(), *more, scale=scale))
+    n = 0
+    for b in range(10):
+        for h in range(4):
+            x = q[b, 0, h].double().numpy()
+            s = p.k[b][:, 0] @ x
+            top, next_ = np.sort(s)[-1], np.sort(s)[-2]
+            if top - next_ < 2.0 ** -10 * (np.abs(p.k[b][:, 0]) @ np.abs(x)).max():
+                continue
+            n += 1
+            want = p.v[b][int(s.argmax()), 0]
+            for i, o in enumerate(outs):
+                assert (np.abs(o[b, 0, h].double().cpu().numpy() - want) <=
+                        2.0 ** -7 * np.abs(want) + 2.0 ** -18 * p.spread()).all(), (i, b, h)
+    assert n >= 10                                       # (19 of 40 at the least: it depends on the inputs alone)
