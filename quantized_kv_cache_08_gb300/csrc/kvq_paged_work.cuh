@@ -16,7 +16,7 @@ using dev::kLazy;
 using dev::kNegInf;
 constexpr float kShift = 6.0f;         // p is held as 2^6 p: fp16 keeps 2^-20 of the largest in full
 constexpr int kMaxStages = 8;
-constexpr float kNone = -1e30f;        // reference of a query that has seen no row: any score passes it
+constexpr float kNone = -3.402823466e38f;   // reference of a query that has seen no row: no score lies below it
 constexpr float kInf = __builtin_huge_valf();
 constexpr uint32_t kInfBits = 0x7f800000u;
 

@@ -240,3 +240,26 @@ def test_scores_far_apart_leave_the_largest_alone(D, ks, qs, scale, dtype):
                 assert (np.abs(o[b, 0, h].double().cpu().numpy() - want) <=
                         2.0 ** -7 * np.abs(want) + 2.0 ** -18 * p.spread()).all(), (i, b, h)
     assert n >= 10                                       # (19 of 40 at the least: it depends on the inputs alone)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scores_below_any_reference_still_count(dtype):
+    """Rows whose scores are all far below -1e30: the largest takes all."""
+    p = prefix_pair(10, 48, 1, D=64, Hq=4, seed=7)
+    q = p.randn(10, 1, 4, 64).abs().to(dtype)
+    for b in range(10):
+        p.k[b] = np.zeros_like(p.k[b])
+    k = -torch.arange(1, 50, dtype=torch.float32)[:, None, None].expand(49, 1, 64) * 64
+    v = p.randn(49, 1, 64)
+    for b in range(10):
+        p.v[b] = P.values(P.blocks(v.numpy(), Q8, "v"), Q8, "v")
+        p.dev.append(k[None].contiguous().cuda(), v[None].cuda(), p.tables[b:b + 1], i32([49]))
+    want = np.stack([np.repeat(p.v[b][None, 0], 4, 1) for b in range(10)])[:, None].reshape(10, 1, 4, 64)   # row 0 has the largest score
+    args = (q.cuda(), p.tables, p.lens())
+    # (capped at 1e30, all scores are the same)
+    mean = np.stack([np.repeat(p.v[b][None].mean(1)[None], 4, 2) for b in range(10)]).reshape(want.shape)
+    for att, w in (({}, want), (dict(softcap=1e30), mean)):
+        for got in (p.dev.decode(*args, scale=1e30, **att), p.dev.decode_shared(*args, i32([0, 10]), i32([48]), scale=1e30, **att)):
+            # the output's rounding, and fp16 roundings of p and v: 2^-9 of the largest value
+            tol = 2.0 ** -8 * np.abs(w) + 2.0 ** -9 * np.abs(p.v[0]).max()
+            assert (np.abs(got.double().cpu().numpy() - w) <= tol).all(), att
