@@ -758,12 +758,9 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     const uint32_t exps = held(0x64646464u);
     int st = 0;
     uint32_t phase = 0;
-    // After the tile kernel: nothing here reads what that writes, and it lets this
-    // kernel start only behind its own wait for what came before, so this one runs
-    // in the SMs that it leaves and waits for it last, for the sake of whatever
-    // waits for this one (64 sequences over 8192 shared rows: 61 us, waiting first 64)
-    if (a.tiles) __threadfence();
-    else wait_for_earlier();
+    // (After the tile kernel too: that waited for what came before, but only a grid's
+    // own wait makes earlier grids' writes visible to it.)
+    wait_for_earlier();
     // ---- the plan: prefix sums of the entries' work (one warp's scan for up to
     // 32 entries, else every thread's share and a scan over the CTA)
     {
@@ -847,13 +844,10 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             for (long long i = 4 * tid; i < n; i += 4 * kThreads) store4(a, at + i, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
         }
     }
-    auto done = [&]() {
-        if (a.tiles) wait_for_earlier();
-    };
-    if (range >= G) return done();
+    if (range >= G) return;
     x = mul_div(W, range, G);
     x1 = mul_div(W, range + 1, G);
-    if (!next_fragment(f, x, x1, a, plan, QPI)) return done();
+    if (!next_fragment(f, x, x1, a, plan, QPI)) return;
     pr.x = x;
     enter(pr, a, f, gwarp);
     look_up(pr, a, lane);
@@ -1068,7 +1062,6 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
         const long long t0 = clock64();
         while (clock64() - t0 < (1LL << 30)) __nanosleep(1000);
     }
-    done();
 }
 
 // ------------------------------------------------------------ merge kernel
