@@ -360,6 +360,8 @@ class PagedKVCache:
         shape, code = q.shape, _DTYPE.get(q.dtype)
         if code is None or len(shape) != 4 or shape[0] != n or shape[3] != self.head_dim:
             raise ValueError(f"q {q.dtype} {tuple(shape)} does not match the cache and lens")
+        if not 0 <= window < 1 << 31:
+            raise ValueError("window must be >= 0 and fit an int32")
         qp = self._dense(q, "q")
         if out is None:
             out = torch.empty_like(q) if stream is None else self._new(shape, q.dtype, stream)

@@ -37,6 +37,7 @@ constexpr int many_keys(int NB) { return NB == 8 ? 64 : 32; }
 // rows over 7 sequences 21.3, 17.2, 17.8
 constexpr int kSetup = 24;
 constexpr int kMaxT = 64;
+constexpr int kMaxRows = 1 << 24;      // rows of a sequence at most
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned16(const void* p) { return ((size_t)p & 15) == 0; }
@@ -60,7 +61,7 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     if (c->max_q_heads < c->n_kv_heads || c->max_q_heads % c->n_kv_heads || c->max_q_heads / c->n_kv_heads > 128)
         return fail(KVQ_EINVAL, "max_q_heads must be a multiple of n_kv_heads, at most 128 times it");
     if (c->max_seqs < 1 || c->max_seqs > kMaxSeqs) return fail(KVQ_EINVAL, "max_seqs must be in [1, %d]", kMaxSeqs);
-    if (c->max_pages < 1 || (long long)c->max_pages * R > (1LL << 24))
+    if (c->max_pages < 1 || (long long)c->max_pages * R > kMaxRows)
         return fail(KVQ_EINVAL, "max_pages must be >= 1 and max_pages * page_rows at most 2^24");
     if (c->max_t < 1 || c->max_t > kMaxT) return fail(KVQ_EINVAL, "max_t must be in [1, %d]", kMaxT);
     if (c->rope_dim < 0 || c->rope_dim > c->head_dim || c->rope_dim % 16)
@@ -170,7 +171,8 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.qscale = (q->scale > 0.f ? q->scale : 1.0f / sqrtf((float)c->cfg.head_dim)) * log2e;
     a.softcap_a = q->softcap > 0.f ? 1.0f / (q->softcap * log2e) : 0.f;
     a.softcap_b = q->softcap > 0.f ? q->softcap * log2e : 0.f;
-    a.window = q->window;
+    // (a window of the longest sequence is none; positions less a larger one could pass 32 bits)
+    a.window = std::min(q->window, kMaxRows);
     a.group_start = group_start;
     a.prefix_len = prefix_len;
     a.n_groups = n_groups;

@@ -263,3 +263,19 @@ def test_scores_below_any_reference_still_count(dtype):
             # the output's rounding, and fp16 roundings of p and v: 2^-9 of the largest value
             tol = 2.0 ** -8 * np.abs(w) + 2.0 ** -9 * np.abs(p.v[0]).max()
             assert (np.abs(got.double().cpu().numpy() - w) <= tol).all(), att
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_windows_of_any_size(dtype):
+    """A window beyond every length is none, for sequences shorter than the rows of queries too."""
+    p = prefix_pair(10, 32, 7, D=64, Hq=4, max_t=8)
+    lens = i32([1, 2, 5, 8, 33, 39, 39, 39, 39, 3])
+    q = p.randn(10, 8, 4, 64).to(dtype).cuda()
+    more = (i32([0, 10]), i32([32]))
+    dense, shared = p.dev.decode(q, p.tables, lens), p.dev.decode_shared(q, p.tables, lens, *more)
+    for w in (39, 1 << 24, (1 << 24) + 1, 2 ** 31 - 1):
+        assert torch.equal(p.dev.decode(q, p.tables, lens, window=w), dense), w
+        assert torch.equal(p.dev.decode_shared(q, p.tables, lens, *more, window=w), shared), w
+    for w in (2 ** 31, 2 ** 32 + 5, -1, -2 ** 32 + 5):
+        with pytest.raises(Exception):
+            p.dev.decode(q, p.tables, lens, window=w)
