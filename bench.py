@@ -86,11 +86,13 @@ def measured_peak():
 
 
 def kernel_source_hash():
-    """Hash of the CUDA sources with comments removed and whitespace collapsed,
-    so that recorded counters stay valid across comment-only edits and no
-    longer."""
+    """Hash of the flat cache's CUDA sources (the paged cache's translation units
+    are not launched here) with comments removed and whitespace collapsed, so
+    that recorded counters stay valid across comment-only edits and no longer."""
     h = hashlib.sha256()
     for f in sorted(os.listdir(os.path.join(ROOT, "quantized_kv_cache_08_gb300", "csrc"))):
+        if f.startswith("kvq_paged"):
+            continue
         with open(os.path.join(ROOT, "quantized_kv_cache_08_gb300", "csrc", f)) as fh:
             src = fh.read()
         src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
