@@ -430,12 +430,16 @@ kvq_status kvq_paged_decode_sparse(kvq_paged* c, const kvq_paged_query* a, const
 kvq_status kvq_paged_read_error(kvq_paged* c, int* err, void* stream) {
     if (!c || !err) return fail(KVQ_EINVAL, "NULL argument");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-    e = cudaMemcpy(err, c->g.err, sizeof(int), cudaMemcpyDeviceToHost);
+    // in the stream's own order: on another stream the clearing could fall behind the
+    // next call's report
+    int word = 0;
+    cudaError_t e = cudaMemcpyAsync(&word, c->g.err, sizeof(int), cudaMemcpyDeviceToHost, s);
     if (e != cudaSuccess) return cuda_fail(e, "read error word");
-    e = cudaMemset(c->g.err, 0, sizeof(int));
+    e = cudaMemsetAsync(c->g.err, 0, sizeof(int), s);
     if (e != cudaSuccess) return cuda_fail(e, "clear error word");
+    e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
+    *err = word;
     return KVQ_OK;
 }
 

@@ -279,3 +279,17 @@ def test_windows_of_any_size(dtype):
     for w in (2 ** 31, 2 ** 32 + 5, -1, -2 ** 32 + 5):
         with pytest.raises(Exception):
             p.dev.decode(q, p.tables, lens, window=w)
+
+
+def test_errors_of_calls_behind_a_read_error_are_kept():
+    """On a stream that does not wait for the default one: each bad call is reported, none is cleared away."""
+    p = PagedPair(1, 1, 64, 2, page=16, max_pages=2)
+    p.append([20])
+    q = p.randn(1, 1, 2, 64).to(BF).cuda()
+    bad, s = torch.full_like(p.tables, -1), torch.cuda.Stream()
+    lens = p.lens()
+    torch.cuda.synchronize()
+    for _ in range(300):
+        p.dev.decode(q, bad, lens, stream=s)
+        assert p.dev.device_error(stream=s) == 1
+    assert p.dev.device_error(stream=s) == 0
