@@ -253,8 +253,11 @@ kvq_status kvq_paged_alloc(const kvq_paged_config* cfg, void* pool, void* bounds
     for (int i = 0; i < cfg->rope_dim / 2; ++i) {
         const double w = rope_freq ? rope_freq[i] : std::pow(cfg->rope_base, -2.0 * i / cfg->rope_dim);
         if (!(std::fabs(w) <= 64.0)) return fail(KVQ_EINVAL, "rope frequency %d is not within 64 radians a position", i);
-        f.f[i].x = (float)(w / turn);
-        f.f[i].y = (float)(w / turn - (double)f.f[i].x);
+        // whole turns a position are none: what is left is half a turn at most, of which
+        // the two floats keep 2^-50 and the kernel's sums 2^-24 at any position
+        const double turns = w / turn - std::nearbyint(w / turn);
+        f.f[i].x = (float)turns;
+        f.f[i].y = (float)(turns - (double)f.f[i].x);
     }
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -7,6 +7,8 @@ import pytest
 import torch
 
 from oracle import kvq_paged_oracle as P
+from quantized_kv_cache_08_gb300.cache import PagedKVCache
+from tests.kvq_testutil import need_gpu
 from tests.paged_testutil import PagedPair
 
 pytestmark = pytest.mark.gpu
@@ -293,3 +295,19 @@ def test_errors_of_calls_behind_a_read_error_are_kept():
         p.dev.decode(q, bad, lens, stream=s)
         assert p.dev.device_error(stream=s) == 1
     assert p.dev.device_error(stream=s) == 0
+
+
+def test_rotation_by_more_than_half_a_turn_a_position():
+    """Frequencies up to the 64 radians that a call takes, at the farthest positions."""
+    need_gpu()
+    D, page, far = 64, 256, 1 << 24
+    freq = [64.0, -63.7, 50.3, 33.3, 20.123, 12.9, 6.5, 6.2, 4.0, 3.2] + [1.0, 0.3, -0.2, 0.1, 0.01, 0.001]
+    c = PagedKVCache(2, page, 1, D, 2, max_seqs=1, max_pages=1 << 16, rope_dim=32, rope_freq=freq)
+    tab = torch.zeros(1, 1 << 16, dtype=torch.int32, device="cuda")
+    k = torch.randn(1, 64, 1, D, generator=torch.Generator().manual_seed(1))
+    for end in (far, far - 1234567, 1 << 20):
+        q = c.append(k.cuda(), k.cuda(), tab, i32([end]), q=k.cuda())
+        want = P.rotate(k.double().numpy().reshape(64, 1, D), end - 64 + np.arange(64), 32, freq=freq)
+        # 2^-24 of a turn are 2^-21.3 radians; twice that for the fp64 product of position and frequency and f32 arithmetic
+        assert np.abs(q.cpu().double().numpy().reshape(64, 1, D) - want).max() <= 2.0 ** -20 * 4
+    assert c.device_error() == 0
