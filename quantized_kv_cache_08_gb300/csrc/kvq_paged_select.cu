@@ -29,7 +29,7 @@ constexpr int kKeep = 8192;            // keys that the pick holds in shared mem
 constexpr int kRank = 256;             // keys that are ranked one a thread
 constexpr int kBlock = 20;             // words of a query block's codes and scale
 
-// number of pages with a row that query row t sees, -1 for a bad length
+// number of pages with a row that query row t sees, 0 for a bad length
 __device__ __forceinline__ int page_count(const SelectArgs& a, int seq, int t, bool report) {
     const int len = a.lens[seq];
     if (len < 0 || len > (long long)a.g.max_pages << a.g.page_shift) {

@@ -311,3 +311,72 @@ def test_rotation_by_more_than_half_a_turn_a_position():
         # 2^-24 of a turn are 2^-21.3 radians; twice that for the fp64 product of position and frequency and f32 arithmetic
         assert np.abs(q.cpu().double().numpy().reshape(64, 1, D) - want).max() <= 2.0 ** -20 * 4
     assert c.device_error() == 0
+
+
+# ------------------------------------------------------------------ accuracy of f32 queries
+
+@pytest.mark.parametrize("D,Hq", [(64, 4), (64, 16), (128, 8), (128, 16), (256, 4), (256, 16)])
+def test_f32_outputs_keep_all_24_bits_of_p_d(D, Hq):
+    """Scores without a rounding of their own: each key has one element that is not zero, 127 d of a d with few
+    bits, and each query one power of two, so that a score is off by its factors' roundings alone.  Row 0 has
+    the largest score and values of zero, row 1 values d (u - 16).  p_1 is then off by its exponent's roundings,
+    at most 2^-22 for each of factor, product and sum (the sum is below 8), ln 2 of that, and 2^-22 of ex2: less
+    than 2^-20 together; as much again covers the sum of weights, its reciprocal, the final product and the
+    three parts of p d (2^-24).  Two rounded parts of 8 bits would leave up to 2^-18: the case tells them apart."""
+    n = 64
+    p = PagedPair(n, 1, D, Hq, page=16, max_pages=1, seed=D + Hq)
+    rng = np.random.default_rng(D)
+    k, v = np.zeros((n, 2, 1, D), np.float32), np.zeros((n, 2, 1, D), np.float32)
+    k[:, 0, 0, 0] = 127 * 2.0 ** -10
+    d = rng.integers(1024, 2047, n) * 2.0 ** -17                   # eleven bits
+    k[:, 1, 0, 0] = -127 * rng.integers(1024, 2047, n) * 2.0 ** -17
+    u = rng.integers(0, 32, (n, D))
+    u[:, 0::32], u[:, 1::32] = 0, 31
+    v[:, 1, 0] = (u - 16) * d[:, None]
+    for b in range(n):
+        p.note(b, k[b], v[b])
+        assert np.array_equal(p.k[b], k[b]) and np.array_equal(p.v[b], v[b])
+    p.dev.append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), p.tables, p.lens())
+    q = torch.zeros(n, 1, Hq, D)
+    q[..., 0] = 2.0 ** torch.randint(0, 3, (n, 1, Hq), generator=torch.Generator().manual_seed(1)).float()
+    scale = 0.11
+    want, mag = p.want(q, scale=scale)
+    got = p.dev.decode(q.cuda(), p.tables, p.lens(), scale=scale).double().cpu().numpy()
+    assert (np.abs(got - want) <= 2.0 ** -19 * np.abs(want)).all(), (np.abs(got - want)[want != 0] / np.abs(want)[want != 0]).max()
+    # what two parts would have given, on the host
+    s = q[:, 0, :, 0].double().numpy() * (k[:, 1, 0, 0].astype(np.float64) - float(k[0, 0, 0, 0]))[:, None] * scale
+    x = np.float32(64 * np.exp(s) * d[:, None])
+    bf = lambda y: torch.from_numpy(y).bfloat16().float().numpy()
+    rest = x - bf(x)
+    assert (np.abs(rest - bf(rest)) / x).max() > 1.5 * 2.0 ** -19
+
+
+# ------------------------------------------------------------------ selection over more pages than the pick holds
+
+@pytest.mark.parametrize("np_", [8191, 8192, 8193, 20001])
+def test_selection_around_and_beyond_8192_pages(np_):
+    """Two KV heads whose rows of scores share cache lines, scores with many ties."""
+    need_gpu()
+    D, page, Hkv, Hq, NB = 64, 16, 2, 6, 2
+    g = np.random.default_rng(np_)
+    n_pages, width = 20011, 20001
+    c = PagedKVCache(n_pages, page, Hkv, D, Hq, max_seqs=2, max_pages=width, max_t=2, bounds=True)
+    lo, hi = g.integers(-3, 1, (n_pages, Hkv, NB, 32)), g.integers(0, 4, (n_pages, Hkv, NB, 32))
+    codes = np.stack([lo, hi], 3).astype(np.int8)
+    ds = g.choice([0.5, 1.0], (n_pages, Hkv, NB)).astype(np.float32)
+    raw = np.concatenate([codes.reshape(-1).view(np.uint8), ds.reshape(-1).view(np.uint8)])
+    c.bounds[:raw.size].copy_(torch.from_numpy(raw))
+    tab = np.stack([g.permutation(n_pages)[:width] for _ in range(2)]).astype(np.int32)
+    q = torch.from_numpy(g.choice([-1.0, 0.0, 0.0, 1.0], (2, 2, Hq, D)).astype(np.float32))
+    lens = np.array([np_ * page - 3, width * page])
+    for keep in (1, 64, 300, 5000):
+        got = c.select(q.cuda(), torch.from_numpy(tab).cuda(), i32(lens.tolist()), keep, n_first=min(1, keep), n_last=0).cpu().numpy()
+        for b in range(2):
+            for t in range(2):
+                m = -(-(int(lens[b]) - 2 + t + 1) // page)
+                for h in range(Hkv):
+                    sc = P.scores(q[b, t, 3 * h:3 * h + 3].numpy(), codes[tab[b, :m], h], ds[tab[b, :m], h])
+                    # (ties to the lower index, as the oracle's select, which is slow at this size)
+                    order = [0] + [int(i) + 1 for i in np.argsort(-sc[1:], kind="stable")]
+                    assert got[b, t, h].tolist() == sorted(order[:keep]), (keep, b, t, h)
+    assert c.device_error() == 0
