@@ -335,13 +335,17 @@ kvq_status kvq_set_split_rows(kvq_cache* cache, int rows);
  *   E4M3 V      512 NB + (n/2)*512 + lane*16 + (n%2)*8 + r*2 + s
  * A cell is 928 NB bytes (58 per 32 elements, as in the flat cache) or 1024 NB.
  *
- * Errors.  A page number outside the pool or a length above max_pages *
- * page_rows sets the device error word to 1: appends skip the row, decodes
- * take a bad page's rows as masked and a bad sequence as empty.  A query row
+ * Errors.  A page number outside the pool, a length below 0 or above max_pages *
+ * page_rows, or one below the rows that an append brings (an entry that only
+ * pads a batch is given none, by `starts`) sets the device error word to 1:
+ * appends skip the row, decodes take a bad page's rows as masked and a bad
+ * sequence as empty.  Rows that a length counts and no append wrote may be any
+ * bytes: outputs of the queries that see them are undefined.  A query row
  * that sees no row (a sequence of length 0, a position below 0) gives zeros,
  * with or without a sink; one that is not finite, or whose score of a row
  * overflows f32, gives NaN where it sees a row, and leaves all others as they are.  Calls on one cache share its workspace: order them
- * on one stream (captured graphs that share a cache included). */
+ * on one stream (captured graphs that share a cache included).  A workspace
+ * belongs to one cache: its counters are zero between that cache's calls. */
 typedef struct kvq_paged_config {
     int n_pages;         /* pages in the pool                                     */
     int page_rows;       /* rows per page: 16, 32, 64, 128 or 256                 */
@@ -414,8 +418,8 @@ kvq_status kvq_paged_read(kvq_paged* cache, void* k_out, void* v_out, kvq_dtype 
  * sees logical rows [max(0, p + 1 - window), p + 1), p = len - T + t (window
  * 0: all).  scale <= 0 selects 1/sqrt(D); softcap > 0 caps scaled scores to
  * softcap * tanh(s / softcap) (either, where positive, within 1e-30 .. 1e30);
- * sinks: device f32 [Hq] or NULL, logits that join max and denominator
- * without a value (-inf: none).  out may be q. */
+ * sinks: device f32 [Hq] or NULL, logits (finite, or -inf: none) that join max
+ * and denominator without a value.  out may be q. */
 typedef struct kvq_paged_query {
     const void* q;
     void* out;

@@ -303,7 +303,7 @@ class PagedKVCache:
 
     def append(self, k, v, tables, lens, starts=None, q=None, q_out=None, stream=None):
         """k, v: float32/bfloat16 [n, T, Hkv, D], or packed [rows, Hkv, D] with
-        starts (int32 [n + 1]).  q (same form, any number of heads) is rotated
+        starts (int32 [n + 1]).  q (same form, up to max_q_heads heads) is rotated
         into q_out (made if None; q itself when dense), which is returned."""
         n, tp, lp = self._batch(tables, lens)
         shape, dtype, hkv, dim, index = k.shape, k.dtype, self.n_kv_heads, self.head_dim, self.index

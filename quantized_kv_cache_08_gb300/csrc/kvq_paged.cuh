@@ -209,7 +209,7 @@ struct SplitArgs {
     int keep;
     int E;                         // work entries
     int G;                         // CTAs of the split kernel
-    int tile;                      // queries of a slice (QPI): 8, or 16 for more bf16 queries
+    int tile;                      // queries of a slice (QPI): 8, or 16 where a key has more (split_tile)
     int setup;                     // what starting a key costs, in cells
     int gw, groups;                // warps of a group, groups of a CTA of the split kernel
     int rec_rows;                  // query rows of a record: min(tile, most queries of a key)

@@ -30,7 +30,7 @@
 //
 // Measured (q8_0 / q5_1, bf16, 32 query and 8 KV heads of 128): 64 sequences of 1024
 // to 16384 rows 191 us, 0.80 of the copy rate, bound by some 520 instructions a
-// cell; one of 32768 rows 22 us and one of 512 (8 query and 2 KV heads) 11 us, of
+// cell; one of 32768 rows 23 us and one of 512 (8 query and 2 KV heads) 12 us, of
 // which 11 are the start and the end: plan, first lookups and copies, joins,
 // records, and fetching code that runs once.
 #include "kvq_device.cuh"

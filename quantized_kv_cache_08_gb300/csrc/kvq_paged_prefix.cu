@@ -23,10 +23,12 @@
 // the products.  With two query tiles the products of one run while the
 // exponentials of the other are worked out.
 //
-// Bound: per 128 rows x 128 queries 8.4 MFLOP (head_dim 128) take about 1250
-// queries a KV head cost what the bytes cost.  Measured: 8192 rows for 64
-// sequences of 4 queries a KV head, 8 KV heads of 128: 21 us for 3.4 tiles an SM,
-// half of it before the first products and after the last.
+// Bound: a row of head_dim 128 costs 232 bytes of HBM a KV head and 512 flops a
+// query, so at the measured rates (6.8 TB/s, 1.9 PFLOP/s) the products cost what the
+// bytes cost from about 130 queries a KV head on.  Measured: 8192 rows for 64
+// sequences of 4 queries a KV head, 8 KV heads of 128: 27 us for 3.4 tiles an SM
+// (the products 4.4 us at cuBLAS's rate), tensor cores 13 % busy: half is before the
+// first products and after the last, and a tile's products wait for its softmax.
 #include "kvq_device.cuh"
 #include "kvq_paged.cuh"
 #include "kvq_paged_work.cuh"

@@ -105,7 +105,16 @@ __device__ __forceinline__ void members(const SplitArgs& a, int grp, int& gs, in
 }
 
 // A group whose queries per KV head are more than one slice of the split kernel
-// goes to the tile kernel: the split kernel reads the rows again for each slice
+// goes to the tile kernel: the split kernel reads the rows again for each slice.
+// Whole calls with the groups in either, 8 KV heads of 128, 16 rows of each
+// sequence's own (tile / split / a dense decode, us):
+//   queries   2048 rows         8192 rows
+//        9    40 / 27 / 23      54 / 34 / 40
+//       64    43 / 30 / 28      56 / 43 / 59
+//      128    44 / 38 / 41      56 / 59 / 101
+//      256    48 / 49 / 63      63 / 91 / 186
+// The tile kernel pays from about 128 queries over 8192 rows on; in smaller groups
+// its start and end, some 25 us, are more than the reading that it saves.
 __device__ __forceinline__ bool tile_group(const SplitArgs& a, int nq) { return a.tiles && nq > a.tile; }
 
 struct EntryWork {
