@@ -342,8 +342,9 @@ kvq_status kvq_set_split_rows(kvq_cache* cache, int rows);
  * sequence as empty.  Rows that a length counts and no append wrote may be any
  * bytes: outputs of the queries that see them are undefined.  A query row
  * that sees no row (a sequence of length 0, a position below 0) gives zeros,
- * with or without a sink; one that is not finite, or whose score of a row
- * overflows f32, gives NaN where it sees a row, and leaves all others as they are.  Calls on one cache share its workspace: order them
+ * with or without a sink; one that is not finite, or whose score of a row is
+ * above f32's range, gives NaN where it sees a row, and leaves all others as they
+ * are (a score below f32's range is one of no weight).  Calls on one cache share its workspace: order them
  * on one stream (captured graphs that share a cache included).  A workspace
  * belongs to one cache: its counters are zero between that cache's calls. */
 typedef struct kvq_paged_config {
