@@ -340,7 +340,8 @@ kvq_status kvq_set_split_rows(kvq_cache* cache, int rows);
  * pads a batch is given none, by `starts`) sets the device error word to 1:
  * appends skip the row, decodes take a bad page's rows as masked and a bad
  * sequence as empty.  Rows that a length counts and no append wrote may be any
- * bytes: outputs of the queries that see them are undefined.  A query row
+ * bytes: outputs of the queries that see them are undefined, unless they were
+ * filled in another way with finite scales and values.  A query row
  * that sees no row (a sequence of length 0, a position below 0) gives zeros,
  * with or without a sink; one that is not finite, or whose score of a row is
  * above f32's range, gives NaN where it sees a row, and leaves all others as they
