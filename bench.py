@@ -86,12 +86,12 @@ def measured_peak():
 
 
 def kernel_source_hash():
-    """Hash of the flat cache's CUDA sources (the paged cache's translation units
-    are not launched here) with comments removed and whitespace collapsed, so
+    """Hash of the flat cache's CUDA sources (the paged cache's and the draft
+    verification's translation units are not launched here) with comments removed and whitespace collapsed, so
     that recorded counters stay valid across comment-only edits and no longer."""
     h = hashlib.sha256()
     for f in sorted(os.listdir(os.path.join(ROOT, "quantized_kv_cache_08_gb300", "csrc"))):
-        if f.startswith("kvq_paged"):
+        if f.startswith(("kvq_paged", "kvq_verify", "kvq_cluster")):
             continue
         with open(os.path.join(ROOT, "quantized_kv_cache_08_gb300", "csrc", f)) as fh:
             src = fh.read()

@@ -235,6 +235,50 @@ kvq_status kvq_truncate(kvq_cache* cache, const int* new_len, void* stream);
  * any other call on the cache (kvq_note_replayed cannot know the counts). */
 kvq_status kvq_truncate_device(kvq_cache* cache, const int* accept_d, int T, void* stream);
 
+/* Verification of drafted tokens: the accepted counts that
+ * kvq_truncate_device takes, and each sequence's next token, from the
+ * probabilities of a T-row step (the last token, then up to T - 1 drafts) and
+ * random numbers of the caller's.  No passage: the pages take accepted counts
+ * as given ("Struct Cache", fn rollback, item C.1).
+ *
+ * target: device [n_seq][T][vocab] of dtype (f32 or bf16): row t is the
+ * target's distribution behind row t of the step.  draft: device
+ * [n_seq][T - 1][vocab] of the same type: row t is what tokens[t] was drawn
+ * from; NULL: the drafts were not drawn (each has probability 1).  Sequences
+ * and rows lie target_seq / target_row (draft_seq / draft_row) elements apart,
+ * any number >= 0, a row's elements side by side.  tokens: device int32
+ * [n_seq][T - 1]; one outside [0, vocab) is no draft: the sequence's drafts end
+ * there (its step may hold fewer than T - 1).  uniform: device f32 [n_seq][T] in [0, 1).
+ * A probability that is not above 0 (NaN too) counts as 0, one above 1 as 1.
+ *
+ * Draft t stands while uniform[t] * q_t(tokens[t]) < p_t(tokens[t]) (the exact
+ * products) and all before it stand.  With a the number that do:
+ *   accept[b] = a + 1: the rows of the step that stay;
+ *   next[b]: drawn from row a of target.  Weights are max(P_i - Q_i, 0) where
+ *     draft a fell (P_i itself where those are all 0), else P_i, with P, Q the
+ *     probabilities in whole units of 2^-52, rounded down.  The token is the
+ *     first whose running sum passes floor(S * floor(uniform[T-1] * 2^31) /
+ *     2^31), S the weights' sum: whole numbers throughout, the same token on
+ *     every run.  -1 where all weights are 0.  (A row's probabilities sum to
+ *     less than 4096, or the token is any, or -1.)
+ *   lens[b] -= T - accept[b], where lens (device int32 [n_seq], or NULL) counts
+ *     the step's rows, as a paged cache's lengths do.
+ * One kernel; nothing is read of a row that is not needed.  T in [1, 512] (T =
+ * 1: a draw from row 0), vocab up to 2^24, n_seq up to 65536. */
+typedef struct kvq_verify_args {
+    const void* target;
+    const void* draft;
+    const int* tokens;
+    const float* uniform;
+    kvq_dtype dtype;
+    int n_seq, T, vocab;
+    long long target_seq, target_row, draft_seq, draft_row;
+    int* accept;          /* device int32 [n_seq]                            */
+    int* next;            /* device int32 [n_seq]                            */
+    int* lens;            /* device int32 [n_seq], read and written, or NULL */
+} kvq_verify_args;
+kvq_status kvq_verify(const kvq_verify_args* a, void* stream);
+
 /* Synchronise `stream` and read the device lengths into the host mirror,
  * making it exact (after kvq_truncate_device).  KVQ_ERANGE if a device length
  * lies outside its sequence's resident rows (the mirror is then unchanged). */
@@ -408,6 +452,24 @@ kvq_status kvq_paged_append(kvq_paged* cache, const void* k, long long k_stride,
                             const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,
                             void* stream);
 
+/* The append with each row's position given instead of its index in the
+ * sequence: after an eviction (kvq_paged_compact) a row's index is no longer
+ * its position, and rows of pictures and video have a position on each of
+ * several axes (time, height, width).  positions: device int32 [rows][n_axes],
+ * each in [0, 2^24); pair i of a head turns by positions[row][axis of pair i]
+ * times its frequency.  A row with a position outside sets the error word and
+ * is skipped, its query too.  Rows are placed, and everything else is done, as by
+ * kvq_paged_append.  Needs rope_dim > 0. */
+kvq_status kvq_paged_append_at(kvq_paged* cache, const void* k, long long k_stride, const void* v, long long v_stride,
+                               const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,
+                               const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,
+                               const int* positions, void* stream);
+
+/* The axis of each rotated pair for later kvq_paged_append_at calls: a HOST
+ * array of rope_dim / 2 numbers in [0, n_axes), copied; n_axes in [1, 4].  A
+ * cache starts with one axis.  Enqueues nothing. */
+kvq_status kvq_paged_set_axes(kvq_paged* cache, const int* axis, int n_axes);
+
 /* Rows back as values: entry i's last T rows (or its rows by `starts`, as in
  * the append) into k_out, v_out, dense [rows][Hkv][D] of dtype, rounded once.
  * A row below 0 or in a bad page gives zeros (the latter sets the error
@@ -481,6 +543,53 @@ kvq_status kvq_paged_select(kvq_paged* cache, const kvq_paged_query* a, int* pag
  * n_seq * T <= 2048. */
 kvq_status kvq_paged_decode_sparse(kvq_paged* cache, const kvq_paged_query* a, const int* pages, int keep,
                                    void* stream);
+
+/* Row scores: an f32 for each row and KV head of the pool, device
+ * [n_pages][Hkv][page_rows], 16-byte aligned, kept until the cache is freed or
+ * another buffer (or NULL: none) takes its place.  With a buffer set, appends
+ * set the scores of the rows they write to 0, kvq_paged_decode_scored adds
+ * attention weights and kvq_paged_compact moves scores with their rows.  The
+ * contents are the caller's to read or write.  Enqueues nothing. */
+kvq_status kvq_paged_set_scores(kvq_paged* cache, float* scores);
+
+/* kvq_paged_decode, and the weights that its queries gave to each row added to
+ * the row scores: for every row r below a sequence's length and every KV head,
+ *   score = decay * score + sum over the T query rows and the head's queries of
+ *           exp(s_r) / (sum over the rows seen of exp(s) + exp(sink)),
+ * s the scaled (and capped) score, 0 for rows that a query does not see.
+ * decay in [0, 1]; 0 does not read the old scores.  A query that is not finite
+ * (its output is NaN) adds nothing.  Sums are f32 in a fixed order: two runs
+ * give the same bits.  The pages of one call's sequences are their own: a page
+ * in two tables of the call is written by both.  Rows of bad pages are left
+ * out.  out must not be q.  Needs a buffer (kvq_paged_set_scores). */
+kvq_status kvq_paged_decode_scored(kvq_paged* cache, const kvq_paged_query* a, float decay, void* stream);
+
+/* Choose the rows that stay.  rows: device int32 [n_seq][Hkv][keep] receives for
+ * each sequence and KV head, ascending, the first n_first and last n_last rows
+ * below the length and the best scored of the others, ties to the lower index
+ * (a NaN score is the lowest); all rows where the length is at most keep; -1
+ * behind the last.  Each KV head chooses for itself.  Needs n_first, n_last >= 0 and n_first + n_last
+ * <= keep, keep in [1, 2^24], and a score buffer.  A bad length or page sets the
+ * error word: no rows of that sequence, a score below all others for rows of that page. */
+kvq_status kvq_paged_select_rows(kvq_paged* cache, const int* tables, const int* lens, int n_seq, int keep,
+                                 int n_first, int n_last, int* rows, void* stream);
+
+/* Move the listed rows together: entry i of rows[b][h] (int32 [n_seq][Hkv][keep]
+ * as kvq_paged_select_rows gives them: the first min(lens[b], keep) entries are
+ * rows of the sequence, strictly ascending) becomes row i of KV head h, bit for
+ * bit, with its score where a buffer is set; with cfg.bounds the pages' key
+ * bounds are renewed.  lens_out[b] = min(lens[b], keep) (lens_out may be lens).
+ * The keys stay turned by the positions they were appended with: append the
+ * next rows with kvq_paged_append_at.
+ *   tables_out NULL: in place, into the sequence's own pages; what lies behind
+ *     the new length is then free.  A page belongs to one sequence.
+ *   tables_out (device int32 [n_seq][max_pages]): into other pages (of a sequence that
+ *     shares its first pages with others, say), none of which is in `tables`.
+ * Of a sequence in error (a bad length, an entry out of range or order, a bad
+ * page) the rows concerned are not moved and the error word is set; the others
+ * are. */
+kvq_status kvq_paged_compact(kvq_paged* cache, const int* tables, const int* lens, int n_seq, const int* rows,
+                             int keep, const int* tables_out, int* lens_out, void* stream);
 
 /* Synchronise `stream`, read the device error word into *err (0 = none, 1 = a
  * page number or length out of range, 2 = a bounded wait ran out), clear it. */

@@ -9,14 +9,16 @@ import numpy as np
 from oracle import kvq_oracle as O
 
 
-def rotate(x, pos, rope_dim, interleaved=False, base=10000.0, freq=None):
-    """x float64 [rows, H, D] turned by pos [rows]: pair i by pos * freq[i]."""
+def rotate(x, pos, rope_dim, interleaved=False, base=10000.0, freq=None, axes=None):
+    """x float64 [rows, H, D] turned by pos [rows]: pair i by pos * freq[i]; with
+    axes (of each pair) by pos[:, axes[i]] * freq[i], pos [rows, n]."""
     x = np.array(x, dtype=np.float64)
     if rope_dim == 0:
         return x
     half = rope_dim // 2
     f = np.asarray(freq, np.float64) if freq is not None else float(base) ** (-2.0 * np.arange(half) / rope_dim)
-    a = np.asarray(pos, np.float64)[:, None] * f
+    pos = np.asarray(pos, np.float64)
+    a = (pos[:, None] if axes is None else pos[:, list(axes)]) * f
     w = (np.cos(a) + 1j * np.sin(a))[:, None, :]
     one, two = (slice(0, rope_dim, 2), slice(1, rope_dim, 2)) if interleaved else (slice(0, half), slice(half, rope_dim))
     z = (x[..., one] + 1j * x[..., two]) * w
@@ -134,3 +136,51 @@ def select(score, keep, n_first, n_last):
     rest = sorted((p for p in range(P) if p not in set(forced)), key=lambda p: (-score[p], p))
     order = forced + rest
     return sorted(order[:keep])
+
+
+def weights(q, k, see, scale=None, softcap=0.0, sink=None):
+    """The softmax weights of one query over rows k [L, D]: 0 where see [L] is not."""
+    D = q.shape[0]
+    scale = 1.0 / np.sqrt(D) if not scale or scale <= 0 else scale
+    w = np.zeros(len(k))
+    idx = np.flatnonzero(see)
+    if len(idx) == 0:
+        return w
+    s = k[idx] @ q * scale
+    if softcap > 0:
+        s = softcap * np.tanh(s / softcap)
+    m = s.max() if sink is None else max(s.max(), sink)
+    p = np.exp(s - m)
+    w[idx] = p / (p.sum() + (0.0 if sink is None else np.exp(sink - m)))
+    return w
+
+
+def verify(target, draft, tokens, uniform):
+    """One sequence: target [T, V], draft [T - 1, V] or None, tokens [T - 1],
+    uniform [T] (float64 arrays of the inputs' values).  Returns (accept, next)."""
+    T, V = target.shape
+    clean = lambda x: np.minimum(np.where(x > 0, x, 0.0), 1.0)
+    units = lambda x: [int(v) for v in np.floor(np.ldexp(clean(x), 52))]
+    a, held = 0, False
+    while a < T - 1 and 0 <= tokens[a] < V:
+        held = True
+        qd = 1.0 if draft is None else draft[a, tokens[a]]
+        if not uniform[a] * qd < target[a, tokens[a]]:
+            break
+        a, held = a + 1, False
+    w = p = units(target[a])
+    if held:
+        q = units(draft[a]) if draft is not None else [1 << 52 if i == tokens[a] else 0 for i in range(V)]
+        w = [max(x - y, 0) for x, y in zip(p, q)]
+        if sum(w) == 0:
+            w = p
+    S = sum(w)
+    if S == 0:
+        return a + 1, -1
+    u = uniform[T - 1]
+    x = (S * int(min(max(u, 0.0) * 2.0 ** 31, 2.0 ** 31 - 128))) >> 31 if u == u else 0
+    run = 0
+    for i, v in enumerate(w):
+        run += v
+        if run > x:
+            return a + 1, i

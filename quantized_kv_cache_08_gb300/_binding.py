@@ -30,7 +30,8 @@ EXPORTS = (
     "kvq_set_softcap",
     "kvq_paged_required_bytes", "kvq_paged_alloc", "kvq_paged_free", "kvq_paged_append", "kvq_paged_read",
     "kvq_paged_bounds", "kvq_paged_decode", "kvq_paged_decode_shared", "kvq_paged_select", "kvq_paged_decode_sparse",
-    "kvq_paged_read_error",
+    "kvq_paged_read_error", "kvq_paged_append_at", "kvq_paged_set_axes", "kvq_paged_set_scores", "kvq_paged_decode_scored",
+    "kvq_paged_select_rows", "kvq_paged_compact", "kvq_verify",
     "kvq_block_bytes", "kvq_bytes_per_token", "kvq_last_error",
 )
 
@@ -71,6 +72,14 @@ class kvq_paged_query(ctypes.Structure):
                 ("T", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p),
                 ("sinks", ctypes.c_void_p), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
                 ("window", ctypes.c_int)]
+
+
+class kvq_verify_args(ctypes.Structure):
+    _fields_ = [("target", ctypes.c_void_p), ("draft", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("uniform", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_seq", ctypes.c_int), ("T", ctypes.c_int),
+                ("vocab", ctypes.c_int), ("target_seq", ctypes.c_longlong), ("target_row", ctypes.c_longlong),
+                ("draft_seq", ctypes.c_longlong), ("draft_row", ctypes.c_longlong), ("accept", ctypes.c_void_p),
+                ("next", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -118,6 +127,13 @@ def lib():
             "kvq_paged_select": (I, [P, QP, P, I, I, I, P]),
             "kvq_paged_decode_sparse": (I, [P, QP, P, I, P]),
             "kvq_paged_read_error": (I, [P, IP, P]),
+            "kvq_paged_append_at": (I, [P, P, LL, P, LL, P, LL, P, I, I, P, P, I, I, P, I, P, P]),
+            "kvq_paged_set_axes": (I, [P, IP, I]),
+            "kvq_paged_set_scores": (I, [P, P]),
+            "kvq_paged_decode_scored": (I, [P, QP, ctypes.c_float, P]),
+            "kvq_paged_select_rows": (I, [P, P, P, I, I, I, I, P, P]),
+            "kvq_paged_compact": (I, [P, P, P, I, P, I, P, P, P]),
+            "kvq_verify": (I, [ctypes.POINTER(kvq_verify_args), P]),
             "kvq_block_bytes": (I, [I]),
             "kvq_bytes_per_token": (S, [ctypes.POINTER(kvq_config)]),
             "kvq_last_error": (ctypes.c_char_p, []),
@@ -291,6 +307,36 @@ def kvq_paged_select(handle, query, pages, keep, n_first, n_last, stream=0):
 
 def kvq_paged_decode_sparse(handle, query, pages, keep, stream=0):
     _check(lib().kvq_paged_decode_sparse(handle, ctypes.byref(query), pages, keep, stream))
+
+
+def kvq_paged_append_at(handle, k, k_stride, v, v_stride, q, q_stride, q_out, n_q_heads, dtype, tables, lens, n_seq, T,
+                        starts, rows, positions, stream=0):
+    _check(lib().kvq_paged_append_at(handle, k, k_stride, v, v_stride, q, q_stride, q_out, n_q_heads, dtype, tables, lens,
+                                     n_seq, T, starts, rows, positions, stream))
+
+
+def kvq_paged_set_axes(handle, axis, n_axes):
+    _check(lib().kvq_paged_set_axes(handle, None if axis is None else _ints(axis), n_axes))
+
+
+def kvq_paged_set_scores(handle, scores):
+    _check(lib().kvq_paged_set_scores(handle, scores))
+
+
+def kvq_paged_decode_scored(handle, query, decay, stream=0):
+    _check(lib().kvq_paged_decode_scored(handle, ctypes.byref(query), float(decay), stream))
+
+
+def kvq_paged_select_rows(handle, tables, lens, n_seq, keep, n_first, n_last, rows, stream=0):
+    _check(lib().kvq_paged_select_rows(handle, tables, lens, n_seq, keep, n_first, n_last, rows, stream))
+
+
+def kvq_paged_compact(handle, tables, lens, n_seq, rows, keep, tables_out, lens_out, stream=0):
+    _check(lib().kvq_paged_compact(handle, tables, lens, n_seq, rows, keep, tables_out, lens_out, stream))
+
+
+def kvq_verify(args, stream=0):
+    _check(lib().kvq_verify(ctypes.byref(args), stream))
 
 
 def kvq_paged_read_error(handle, stream=0):

@@ -199,11 +199,17 @@ class PagedKVCache:
     its keys (and queries) by their positions.  rope_freq gives rope_dim / 2
     radians per position in place of rope_base^(-2i / rope_dim).  bounds: keep
     key bounds per page, which `select` scores.  pool and bounds_buf take over
-    existing uint8 CUDA tensors of `sizes.pool` and `sizes.bounds` bytes."""
+    existing uint8 CUDA tensors of `sizes.pool` and `sizes.bounds` bytes.
+
+    rope_axes: the axis of each of the rope_dim / 2 rotated pairs, for appends
+    whose rows are given positions on several axes.  scores: keep an attention score per row and KV head in
+    `scores` (float32 [n_pages, Hkv, page_rows], zeros at first; scores_buf takes over an existing
+    tensor), which `decode_scored` adds to, `select_rows` goes by and `compact`
+    moves; appended rows start at 0."""
 
     def __init__(self, n_pages, page_rows, n_kv_heads, head_dim, max_q_heads, max_seqs, max_pages, max_t=1,
                  fmt="q8_0/q5_1", rope_dim=0, rope_base=10000.0, rope_interleaved=False, rope_freq=None, bounds=False,
-                 pool=None, bounds_buf=None, device=None, stream=None):
+                 pool=None, bounds_buf=None, device=None, stream=None, rope_axes=None, scores=False, scores_buf=None):
         self.handle = None
         self._lib = B.lib()
         if fmt not in KVCache.FORMATS:
@@ -212,6 +218,8 @@ class PagedKVCache:
         self.fmt = fmt
         if rope_freq is not None and len(rope_freq) != rope_dim // 2:
             raise ValueError("rope_freq needs rope_dim / 2 values")
+        if rope_axes is not None and len(rope_axes) != rope_dim // 2:
+            raise ValueError("rope_axes needs rope_dim / 2 values")
         self.cfg = B.make_paged_config(n_pages, page_rows, n_kv_heads, head_dim, max_q_heads, max_seqs, max_pages,
                                        max_t, k_fmt, v_fmt, bounds, rope_dim, rope_interleaved, rope_base)
         self.sizes = sz = B.kvq_paged_required_bytes(self.cfg)
@@ -224,6 +232,15 @@ class PagedKVCache:
         self.n_kv_heads, self.head_dim, self.max_pages = n_kv_heads, head_dim, max_pages
         self.pool = self._buffer(pool, sz.pool, "pool")
         self.bounds = self._buffer(bounds_buf, sz.bounds, "bounds_buf") if bounds else None
+        self.n_axes, self.scores = 1, None
+        if scores or scores_buf is not None:
+            shape = (n_pages, n_kv_heads, page_rows)
+            if scores_buf is None:
+                scores_buf = torch.zeros(shape, dtype=torch.float32, device=dev)
+            if scores_buf.dtype != torch.float32 or tuple(scores_buf.shape) != shape or scores_buf.device != dev \
+                    or not scores_buf.is_contiguous():
+                raise ValueError(f"scores_buf must be a contiguous float32 {list(shape)} tensor on {dev}")
+            self.scores = scores_buf
         self.workspace = torch.empty(sz.workspace, dtype=torch.uint8, device=dev)
         if stream is not None:
             stream.wait_stream(torch.cuda.current_stream(dev))   # the workspace's memory may still be in use there
@@ -231,6 +248,11 @@ class PagedKVCache:
             self.handle = B.kvq_paged_alloc(self.cfg, self.pool.data_ptr(),
                                             self.bounds.data_ptr() if bounds else None, self.workspace.data_ptr(),
                                             rope_freq, _stream_handle(stream))
+        if rope_axes is not None:
+            self.n_axes = max(rope_axes, default=0) + 1
+            B.kvq_paged_set_axes(self.handle, rope_axes, self.n_axes)
+        if self.scores is not None:
+            B.kvq_paged_set_scores(self.handle, self.scores.data_ptr())
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -301,10 +323,12 @@ class PagedKVCache:
         out.record_stream(torch.cuda.current_stream(self.device))
         return out
 
-    def append(self, k, v, tables, lens, starts=None, q=None, q_out=None, stream=None):
+    def append(self, k, v, tables, lens, starts=None, q=None, q_out=None, stream=None, positions=None):
         """k, v: float32/bfloat16 [n, T, Hkv, D], or packed [rows, Hkv, D] with
         starts (int32 [n + 1]).  q (same form, up to max_q_heads heads) is rotated
-        into q_out (made if None; q itself when dense), which is returned."""
+        into q_out (made if None; q itself when dense), which is returned.
+        positions (int32, k's rows, [n, T, axes] or [rows, axes]; with one axis
+        the last dimension may be left out) take the place of each row's index."""
         n, tp, lp = self._batch(tables, lens)
         shape, dtype, hkv, dim, index = k.shape, k.dtype, self.n_kv_heads, self.head_dim, self.index
         code = _DTYPE.get(dtype)
@@ -330,8 +354,15 @@ class PagedKVCache:
             op = self._dense(q_out, "q_out")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        self._call(self._lib.kvq_paged_append, kp, ks, vp, vs, qp, qs, op, hq, code, tp, lp, n, T, sp, rows,
-                   _raw_stream(index) if stream is None else stream.cuda_stream)
+        raw = _raw_stream(index) if stream is None else stream.cuda_stream
+        if positions is None:
+            self._call(self._lib.kvq_paged_append, kp, ks, vp, vs, qp, qs, op, hq, code, tp, lp, n, T, sp, rows, raw)
+            return q_out
+        want = (*shape[:-2], self.n_axes)
+        if self.n_axes == 1 and positions.shape == shape[:-2]:
+            want = shape[:-2]
+        self._call(self._lib.kvq_paged_append_at, kp, ks, vp, vs, qp, qs, op, hq, code, tp, lp, n, T, sp, rows,
+                   self._ints(positions, want, "positions"), raw)
         return q_out
 
     def read(self, tables, lens, k_out, v_out, starts=None, stream=None):
@@ -413,9 +444,92 @@ class PagedKVCache:
                    self._ints(pages, (q.shape[0], q.shape[1], self.n_kv_heads, keep), "pages"), keep, self._stream(stream))
         return out
 
+    def decode_scored(self, q, tables, lens, decay=1.0, sinks=None, scale=0.0, window=0, softcap=0.0, out=None,
+                      stream=None):
+        """decode, with the weights of each row added to its score: decay * score
+        + the sum over the T query rows and the queries of the KV head."""
+        if not 0.0 <= decay <= 1.0:
+            raise ValueError("decay must be in [0, 1]")
+        out, a = self._query(q, tables, lens, sinks, scale, window, softcap, out, stream)
+        self._call(self._lib.kvq_paged_decode_scored, a, decay, self._stream(stream))
+        return out
+
+    def select_rows(self, tables, lens, keep, n_first=0, n_last=0, rows=None, stream=None):
+        """The rows that stay of each sequence and KV head: int32 [n, Hkv, keep],
+        the first n_first, the last n_last and the best scored of the others,
+        ascending, -1 behind the last."""
+        n, tp, lp = self._batch(tables, lens)
+        if rows is None:
+            rows = self._new((n, self.n_kv_heads, keep), torch.int32, stream)
+        self._call(self._lib.kvq_paged_select_rows, tp, lp, n, keep, n_first, n_last,
+                   self._ints(rows, (n, self.n_kv_heads, keep), "rows"), self._stream(stream))
+        return rows
+
+    def compact(self, tables, lens, rows, lens_out=None, tables_out=None, stream=None):
+        """Move the listed rows (int32 [n, Hkv, keep], ascending) to the front of
+        their sequence's pages, or into those of tables_out; returns the new
+        lengths (lens_out, made if None; may be lens)."""
+        n, tp, lp = self._batch(tables, lens)
+        keep = rows.shape[-1]
+        if lens_out is None:
+            lens_out = self._new((n,), torch.int32, stream)
+        to = None if tables_out is None else self._ints(tables_out, (n, self.max_pages), "tables_out")
+        self._call(self._lib.kvq_paged_compact, tp, lp, n, self._ints(rows, (n, self.n_kv_heads, keep), "rows"), keep, to,
+                   self._ints(lens_out, (n,), "lens_out"), self._stream(stream))
+        return lens_out
+
     def device_error(self, stream=None):
         """0, or 1: a page number or length out of range, 2: a wait ran out (read and cleared)."""
         if _current_device() == self.index:
             return B.kvq_paged_read_error(self.handle, self._stream(stream))
         with torch.cuda.device(self.index):
             return B.kvq_paged_read_error(self.handle, self._stream(stream))
+
+
+def verify(target, draft, tokens, uniform, lens=None, accept=None, next_tokens=None, stream=None):
+    """Which drafted tokens stand, and each sequence's next token.
+
+    target: float32/bfloat16 [n, T, V] probabilities behind each row of a T-row
+    step; draft: [n, T - 1, V] that tokens (int32 [n, T - 1]; outside [0, V): no
+    draft) were drawn from, or None (looked up: probability 1); uniform: float32
+    [n, T] in [0, 1).  Rows may lie apart (strides), elements side by side.
+    Returns (accept, next_tokens), int32 [n] each, made if None: accept counts the rows of the step
+    that stay, as KVCache.truncate_device takes them; lens (int32 [n], the
+    lengths of a paged cache) is lowered by the others."""
+    code = _DTYPE.get(target.dtype)
+    if code is None or target.dim() != 3 or not target.is_cuda:
+        raise ValueError("target must be a float32 or bfloat16 [n, T, V] CUDA tensor")
+    n, T, V = target.shape
+    dev, index = target.device, target.get_device()
+
+    def rows(t, shape, name):
+        if t.dtype is not target.dtype or t.shape != shape or t.get_device() != index or (t.numel() and V > 1 and t.stride(2) != 1):
+            raise ValueError(f"{name} must be {target.dtype} {list(shape)} on {dev}, a row's elements side by side")
+        return t.data_ptr(), t.stride(0), t.stride(1)
+
+    def flat(t, shape, dtype, name):
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {dev}")
+        return t.data_ptr()
+
+    tp, ts, tr = rows(target, (n, T, V), "target")
+    dp, ds, dr = (None, 0, 0) if draft is None else rows(draft, (n, T - 1, V), "draft")
+    kp = flat(tokens, (n, T - 1), _I32, "tokens")
+    up = flat(uniform, (n, T), torch.float32, "uniform")
+
+    def make():
+        if stream is None:
+            return torch.empty(n, dtype=_I32, device=dev)
+        with torch.cuda.stream(stream):
+            t = torch.empty(n, dtype=_I32, device=dev)
+        t.record_stream(torch.cuda.current_stream(dev))
+        return t
+
+    accept = make() if accept is None else accept
+    next_tokens = make() if next_tokens is None else next_tokens
+    a = B.kvq_verify_args(tp, dp, kp, up, code, n, T, V, ts, tr, ds, dr, flat(accept, (n,), _I32, "accept"),
+                          flat(next_tokens, (n,), _I32, "next_tokens"),
+                          None if lens is None else flat(lens, (n,), _I32, "lens"))
+    with torch.cuda.device(index):
+        B.kvq_verify(a, _raw_stream(index) if stream is None else stream.cuda_stream)
+    return accept, next_tokens

@@ -11,6 +11,8 @@ constexpr int kCellRows = 16;
 constexpr int kMaxFreq = 128;          // rope_dim / 2 at most
 constexpr int kMaxSeqs = 1024;
 constexpr int kMaxEntries = 2048;      // work entries of one decode
+constexpr int kMaxAxes = 4;            // of given positions
+constexpr int kMaxPosition = 1 << 24;  // given positions lie below (exact in f32)
 
 struct Geom {
     uint8_t* pool;
@@ -130,9 +132,11 @@ __device__ __forceinline__ Place place_row(const Geom& g, const Rows& r, int row
 }
 #endif
 
-// Rotation frequencies in turns per position, as a sum of two floats
+// Rotation frequencies in turns per position, as a sum of two floats, and which
+// of a row's given positions they turn by
 struct Freqs {
     float2 f[kMaxFreq];
+    uint8_t axis[kMaxFreq];
 };
 
 struct AppendArgs {
@@ -146,6 +150,9 @@ struct AppendArgs {
     int Hq, bf16, rope_dim, interleaved;
     int8_t* codes;         // bounds of the pages that one row each goes to, or NULL
     float* scales;
+    const int* positions;  // [rows][n_axes], or NULL: a row's index in its sequence
+    int n_axes;
+    float* row_scores;     // set to 0 for the rows written, or NULL
 };
 cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cudaStream_t s);
 
@@ -215,6 +222,7 @@ struct SplitArgs {
     int rec_rows;                  // query rows of a record: min(tile, most queries of a key)
     int fuse;                      // 1: the last CTA of a key joins its records (no merge kernel)
     int* arrived;                  // [key] records written; 0 between calls
+    float2* stats;                 // [n_seq][T][Hq] reference (log2 units) and weight of 2^(s - reference), or NULL
     long long max_keys;            // keys that the record area holds beside the CTAs' own
     float* part_o;                 // [slot][rec_rows][D]
     float* part_ml;                // [slot][rec_rows][2]  (max in log2 units, sum)
@@ -238,6 +246,49 @@ int split_tile(int NB, bool bf16, int most_queries);
 int split_warps(int NB, int tile);
 cudaError_t launch_split(const SplitArgs& a, cudaStream_t s);
 cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s);
+// The weights of a decode's queries onto the row scores (kvq_paged_scored.cu)
+struct ScoredArgs {
+    Geom g;
+    const void* q;
+    int bf16, n_seq, T, Hq, hpk;
+    const int* tables;
+    const int* lens;
+    float qscale, softcap_a, softcap_b;    // as in SplitArgs
+    int window;
+    float decay;
+    const float2* stats;           // as in SplitArgs
+    float* scores;                 // [n_pages][Hkv][page_rows]
+    int slices;                    // query tiles in shared memory at a time
+    int sms;
+};
+cudaError_t launch_scored(const ScoredArgs& a, cudaStream_t s);
+
+// Eviction (kvq_paged_evict.cu)
+struct RowsArgs {
+    Geom g;
+    const int* tables;
+    const int* lens;
+    const float* scores;           // [n_pages][Hkv][page_rows]
+    int* rows;                     // [n_seq][Hkv][keep]
+    int n_seq, keep, n_first, n_last;
+    int cap;                       // keys that a block holds in shared memory
+};
+cudaError_t launch_select_rows(RowsArgs a, int num_sms, cudaStream_t s);
+struct CompactArgs {
+    Geom g;
+    const int* tables;
+    const int* tables_out;         // tables itself: in place
+    const int* lens;
+    int* lens_out;
+    const int* rows;
+    float* scores;                 // or NULL
+    int* arrived;                  // [n_seq] blocks done; 0 between calls
+    int n_seq, keep, in_place;
+    int most;                      // rows that a sequence keeps at most
+    int blocks;                    // of a (sequence, KV head)
+};
+cudaError_t launch_compact(CompactArgs a, int num_sms, cudaStream_t s);
+
 // prefixes of groups with many bf16 queries, 128-row tiles on tcgen05 (kvq_paged_prefix.cu)
 int prefix_rows_of(int NB);                               // tile_rows
 cudaError_t launch_prefix(const SplitArgs& a, cudaStream_t s);

@@ -16,9 +16,11 @@ struct kvq_paged {
     Geom g;
     int num_sms;
     uint8_t* ws;
-    size_t off_plan, off_plan2, off_arrived, off_ml, off_o, off_ml2, off_o2, off_keys, key_rows, keys2;
+    size_t off_plan, off_plan2, off_arrived, off_ml, off_o, off_ml2, off_o2, off_stats, off_keys, key_rows, keys2;
     int8_t* codes;
     float* scales;
+    float* row_scores;
+    int n_axes;
     Freqs freqs;
 };
 
@@ -43,7 +45,7 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned16(const void* p) { return ((size_t)p & 15) == 0; }
 
 struct Layout {
-    size_t cell, page, pool, bounds, plan, plan2, arrived, ml, o, ml2, o2, keys, total, key_rows, keys2;
+    size_t cell, page, pool, bounds, plan, plan2, arrived, ml, o, ml2, o2, stats, keys, total, key_rows, keys2;
 };
 
 kvq_status layout(const kvq_paged_config* c, Layout* l) {
@@ -90,7 +92,8 @@ kvq_status layout(const kvq_paged_config* c, Layout* l) {
     const size_t recs2 = total_q > 8 ? (kMaxGrid + l->keys2) * tr : 0;
     l->ml2 = round_up(l->o + recs * D * 4, 256);
     l->o2 = round_up(l->ml2 + recs2 * 16, 256);
-    l->keys = round_up(l->o2 + recs2 * D * 2, 256);
+    l->stats = round_up(l->o2 + recs2 * D * 2, 256);     // of each query, for the row scores
+    l->keys = round_up(l->stats + (size_t)c->max_seqs * c->max_t * c->max_q_heads * sizeof(float2), 256);
     l->total = l->keys;
     if (c->bounds)
         l->total += round_up((size_t)std::min(kMaxEntries, c->max_seqs * c->max_t) * c->n_kv_heads * round_up(c->max_pages, 4) * 4, 256);
@@ -144,8 +147,28 @@ kvq_status check_query(const kvq_paged* c, const kvq_paged_query* a) {
     return KVQ_OK;
 }
 
+// What the scores of a call's queries go through
+SplitArgs factors(const kvq_paged* c, const kvq_paged_query* q) {
+    SplitArgs a = {};
+    const float log2e = 1.4426950408889634f;
+    a.qscale = (q->scale > 0.f ? q->scale : 1.0f / sqrtf((float)c->cfg.head_dim)) * log2e;
+    a.softcap_a = q->softcap > 0.f ? 1.0f / (q->softcap * log2e) : 0.f;
+    a.softcap_b = q->softcap > 0.f ? q->softcap * log2e : 0.f;
+    // (a window of the longest sequence is none; positions less a larger one could pass 32 bits)
+    a.window = std::min(q->window, kMaxRows);
+    return a;
+}
+
+kvq_status check_evict(const kvq_paged* c, const int* tables, const int* lens, int n_seq, const int* rows, int keep) {
+    if (!c) return fail(KVQ_EINVAL, "cache is NULL");
+    if (!tables || !lens || !rows) return fail(KVQ_EINVAL, "tables, lens or rows is NULL");
+    if (n_seq < 1 || n_seq > c->cfg.max_seqs) return fail(KVQ_EINVAL, "n_seq=%d outside [1, max_seqs=%d]", n_seq, c->cfg.max_seqs);
+    if (keep < 1 || keep > kMaxRows) return fail(KVQ_EINVAL, "keep=%d outside [1, 2^24]", keep);
+    return KVQ_OK;
+}
+
 kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start, const int* prefix_len, int n_groups,
-                  const int* lists, int keep, void* stream) {
+                  const int* lists, int keep, float2* stats, void* stream) {
     kvq_status st = check_query(c, q);
     if (st != KVQ_OK) return st;
     if (!q->out || !aligned16(q->out)) return fail(KVQ_EINVAL, "out is NULL or not 16-byte aligned");
@@ -155,7 +178,7 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     if (!(q->scale <= 0.f || (q->scale >= 1e-30f && q->scale <= 1e30f)))
         return fail(KVQ_EINVAL, "scale must be <= 0 (1 / sqrt(head_dim)) or within 1e-30 .. 1e30");
     if (q->window < 0) return fail(KVQ_EINVAL, "window must be >= 0");
-    SplitArgs a = {};
+    SplitArgs a = factors(c, q);
     a.g = c->g;
     a.q = q->q;
     a.out = q->out;
@@ -167,12 +190,6 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.tables = q->tables;
     a.lens = q->lens;
     a.sinks = q->sinks;
-    const float log2e = 1.4426950408889634f;
-    a.qscale = (q->scale > 0.f ? q->scale : 1.0f / sqrtf((float)c->cfg.head_dim)) * log2e;
-    a.softcap_a = q->softcap > 0.f ? 1.0f / (q->softcap * log2e) : 0.f;
-    a.softcap_b = q->softcap > 0.f ? q->softcap * log2e : 0.f;
-    // (a window of the longest sequence is none; positions less a larger one could pass 32 bits)
-    a.window = std::min(q->window, kMaxRows);
     a.group_start = group_start;
     a.prefix_len = prefix_len;
     a.n_groups = n_groups;
@@ -199,6 +216,7 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.plan = reinterpret_cast<PlanEntry*>(c->ws + c->off_plan);
     a.arrived = reinterpret_cast<int*>(c->ws + c->off_arrived);
     a.fuse = n_groups == 0;
+    a.stats = stats;
     a.part_ml = reinterpret_cast<float*>(c->ws + c->off_ml);
     a.part_o = reinterpret_cast<float*>(c->ws + c->off_o);
     a.tile_rows = prefix_rows_of(a.g.NB());
@@ -217,6 +235,52 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     if (!a.fuse) e = launch_merge(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode merge kernel");
     return KVQ_OK;
+}
+
+kvq_status append(kvq_paged* c, const void* k, long long k_stride, const void* v, long long v_stride,
+                  const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype, const int* tables,
+                  const int* lens, int n_seq, int T, const int* starts, int rows, const int* positions, void* stream) {
+    if (!c) return fail(KVQ_EINVAL, "cache is NULL");
+    if (dtype != KVQ_F32 && dtype != KVQ_BF16) return fail(KVQ_EINVAL, "dtype must be f32 or bf16");
+    AppendArgs a = {};
+    kvq_status st = check_rows(c, tables, lens, n_seq, T, starts, rows, &a.r);
+    if (st != KVQ_OK || rows == 0) return st;
+    if (!k || !v) return fail(KVQ_EINVAL, "k or v is NULL");
+    const long long kvd = (long long)c->cfg.n_kv_heads * c->cfg.head_dim;
+    if ((st = check_stride("k", k, k_stride, kvd)) != KVQ_OK) return st;
+    if ((st = check_stride("v", v, v_stride, kvd)) != KVQ_OK) return st;
+    if (q) {
+        if (!q_out || !aligned16(q_out)) return fail(KVQ_EINVAL, "q_out is NULL or not 16-byte aligned");
+        if (n_q_heads < 1 || n_q_heads > c->cfg.max_q_heads) return fail(KVQ_EINVAL, "n_q_heads outside [1, max_q_heads]");
+        const long long qd = (long long)n_q_heads * c->cfg.head_dim;
+        if ((st = check_stride("q", q, q_stride, qd)) != KVQ_OK) return st;
+        if (q_out == q && q_stride != qd) return fail(KVQ_EINVAL, "q is rotated in place only when it is dense");
+    }
+    a.g = c->g;
+    a.k = k;
+    a.v = v;
+    a.q = q;
+    a.q_out = q_out;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_stride = q_stride;
+    a.Hq = n_q_heads;
+    a.bf16 = dtype == KVQ_BF16;
+    a.rope_dim = c->cfg.rope_dim;
+    a.interleaved = c->cfg.rope_interleaved;
+    // one row a sequence: the warp that stores it renews its page's bounds
+    const bool one = !starts && T == 1;
+    a.positions = positions;
+    a.n_axes = c->n_axes;
+    a.row_scores = c->row_scores;
+    if (c->cfg.bounds && one) {
+        a.codes = c->codes;
+        a.scales = c->scales;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_append(a, c->freqs, c->num_sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "paged append kernel");
+    return c->cfg.bounds && !one ? bounds_of(c, a.r, s) : KVQ_OK;
 }
 
 }  // namespace
@@ -292,12 +356,15 @@ kvq_status kvq_paged_alloc(const kvq_paged_config* cfg, void* pool, void* bounds
     c->off_arrived = l.arrived;
     c->off_ml = l.ml;
     c->off_o = l.o;
+    c->off_stats = l.stats;
     c->off_keys = l.keys;
     c->key_rows = l.key_rows;
     c->codes = static_cast<int8_t*>(bounds);
     const size_t nb = (size_t)cfg->n_pages * cfg->n_kv_heads * (cfg->head_dim / 32);
     c->scales = bounds ? reinterpret_cast<float*>(static_cast<uint8_t*>(bounds) + nb * 64) : nullptr;
     c->freqs = f;
+    c->n_axes = 1;
+    c->row_scores = nullptr;
     *out = c;
     return KVQ_OK;
 }
@@ -308,44 +375,30 @@ kvq_status kvq_paged_append(kvq_paged* c, const void* k, long long k_stride, con
                             const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,
                             const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,
                             void* stream) {
+    return append(c, k, k_stride, v, v_stride, q, q_stride, q_out, n_q_heads, dtype, tables, lens, n_seq, T, starts, rows,
+                  nullptr, stream);
+}
+
+kvq_status kvq_paged_append_at(kvq_paged* c, const void* k, long long k_stride, const void* v, long long v_stride,
+                               const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,
+                               const int* tables, const int* lens, int n_seq, int T, const int* starts, int rows,
+                               const int* positions, void* stream) {
     if (!c) return fail(KVQ_EINVAL, "cache is NULL");
-    if (dtype != KVQ_F32 && dtype != KVQ_BF16) return fail(KVQ_EINVAL, "dtype must be f32 or bf16");
-    AppendArgs a = {};
-    kvq_status st = check_rows(c, tables, lens, n_seq, T, starts, rows, &a.r);
-    if (st != KVQ_OK || rows == 0) return st;
-    if (!k || !v) return fail(KVQ_EINVAL, "k or v is NULL");
-    const long long kvd = (long long)c->cfg.n_kv_heads * c->cfg.head_dim;
-    if ((st = check_stride("k", k, k_stride, kvd)) != KVQ_OK) return st;
-    if ((st = check_stride("v", v, v_stride, kvd)) != KVQ_OK) return st;
-    if (q) {
-        if (!q_out || !aligned16(q_out)) return fail(KVQ_EINVAL, "q_out is NULL or not 16-byte aligned");
-        if (n_q_heads < 1 || n_q_heads > c->cfg.max_q_heads) return fail(KVQ_EINVAL, "n_q_heads outside [1, max_q_heads]");
-        const long long qd = (long long)n_q_heads * c->cfg.head_dim;
-        if ((st = check_stride("q", q, q_stride, qd)) != KVQ_OK) return st;
-        if (q_out == q && q_stride != qd) return fail(KVQ_EINVAL, "q is rotated in place only when it is dense");
-    }
-    a.g = c->g;
-    a.k = k;
-    a.v = v;
-    a.q = q;
-    a.q_out = q_out;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.q_stride = q_stride;
-    a.Hq = n_q_heads;
-    a.bf16 = dtype == KVQ_BF16;
-    a.rope_dim = c->cfg.rope_dim;
-    a.interleaved = c->cfg.rope_interleaved;
-    // one row a sequence: the warp that stores it renews its page's bounds
-    const bool one = !starts && T == 1;
-    if (c->cfg.bounds && one) {
-        a.codes = c->codes;
-        a.scales = c->scales;
-    }
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_append(a, c->freqs, c->num_sms, s);
-    if (e != cudaSuccess) return cuda_fail(e, "paged append kernel");
-    return c->cfg.bounds && !one ? bounds_of(c, a.r, s) : KVQ_OK;
+    if (!c->cfg.rope_dim) return fail(KVQ_EINVAL, "the cache rotates nothing (config.rope_dim): positions have no use");
+    if (!positions && rows != 0) return fail(KVQ_EINVAL, "positions is NULL");
+    return append(c, k, k_stride, v, v_stride, q, q_stride, q_out, n_q_heads, dtype, tables, lens, n_seq, T, starts, rows,
+                  positions, stream);
+}
+
+kvq_status kvq_paged_set_axes(kvq_paged* c, const int* axis, int n_axes) {
+    if (!c) return fail(KVQ_EINVAL, "cache is NULL");
+    if (!c->cfg.rope_dim) return fail(KVQ_EINVAL, "the cache rotates nothing (config.rope_dim)");
+    if (!axis || n_axes < 1 || n_axes > kMaxAxes) return fail(KVQ_EINVAL, "axis is NULL or n_axes outside [1, %d]", kMaxAxes);
+    for (int i = 0; i < c->cfg.rope_dim / 2; ++i)
+        if (axis[i] < 0 || axis[i] >= n_axes) return fail(KVQ_EINVAL, "axis %d of pair %d outside [0, n_axes)", axis[i], i);
+    for (int i = 0; i < c->cfg.rope_dim / 2; ++i) c->freqs.axis[i] = (uint8_t)axis[i];
+    c->n_axes = n_axes;
+    return KVQ_OK;
 }
 
 kvq_status kvq_paged_read(kvq_paged* c, void* k_out, void* v_out, kvq_dtype dtype, const int* tables, const int* lens,
@@ -376,7 +429,7 @@ kvq_status kvq_paged_bounds(kvq_paged* c, const int* tables, const int* lens, in
 }
 
 kvq_status kvq_paged_decode(kvq_paged* c, const kvq_paged_query* a, void* stream) {
-    return decode(c, a, nullptr, nullptr, 0, nullptr, 0, stream);
+    return decode(c, a, nullptr, nullptr, 0, nullptr, 0, nullptr, stream);
 }
 
 kvq_status kvq_paged_decode_shared(kvq_paged* c, const kvq_paged_query* a, const int* group_start,
@@ -385,7 +438,7 @@ kvq_status kvq_paged_decode_shared(kvq_paged* c, const kvq_paged_query* a, const
     if (st != KVQ_OK) return st;
     if (!group_start || !prefix_len) return fail(KVQ_EINVAL, "group_start or prefix_len is NULL");
     if (n_groups < 1 || n_groups > a->n_seq) return fail(KVQ_EINVAL, "n_groups must be in [1, n_seq]");
-    return decode(c, a, group_start, prefix_len, n_groups, nullptr, 0, stream);
+    return decode(c, a, group_start, prefix_len, n_groups, nullptr, 0, nullptr, stream);
 }
 
 kvq_status kvq_paged_select(kvq_paged* c, const kvq_paged_query* a, int* pages, int keep, int n_first, int n_last,
@@ -427,7 +480,100 @@ kvq_status kvq_paged_decode_sparse(kvq_paged* c, const kvq_paged_query* a, const
     if ((long long)keep * c->cfg.page_rows > (1LL << 24)) return fail(KVQ_EINVAL, "keep * page_rows above 2^24");
     if (a->window != 0) return fail(KVQ_EINVAL, "listed pages take no window");
     if (a->n_seq * a->T > kMaxEntries) return fail(KVQ_ERANGE, "n_seq * T above %d", kMaxEntries);
-    return decode(c, a, nullptr, nullptr, 0, pages, keep, stream);
+    return decode(c, a, nullptr, nullptr, 0, pages, keep, nullptr, stream);
+}
+
+kvq_status kvq_paged_set_scores(kvq_paged* c, float* scores) {
+    if (!c) return fail(KVQ_EINVAL, "cache is NULL");
+    if (!aligned16(scores)) return fail(KVQ_EINVAL, "scores must be 16-byte aligned");
+    c->row_scores = scores;
+    return KVQ_OK;
+}
+
+kvq_status kvq_paged_decode_scored(kvq_paged* c, const kvq_paged_query* q, float decay, void* stream) {
+    kvq_status st = check_query(c, q);
+    if (st != KVQ_OK) return st;
+    if (!c->row_scores) return fail(KVQ_EINVAL, "the cache keeps no row scores (kvq_paged_set_scores)");
+    if (!(decay >= 0.f && decay <= 1.f)) return fail(KVQ_EINVAL, "decay must be in [0, 1]");
+    // (out may be q: the weights are worked out from the queries afterwards)
+    if (q->out == q->q) return fail(KVQ_EINVAL, "out must not be q");
+    ScoredArgs a = {};
+    a.stats = reinterpret_cast<float2*>(c->ws + c->off_stats);
+    st = decode(c, q, nullptr, nullptr, 0, nullptr, 0, const_cast<float2*>(a.stats), stream);
+    if (st != KVQ_OK) return st;
+    a.g = c->g;
+    a.q = q->q;
+    a.bf16 = q->dtype == KVQ_BF16;
+    a.n_seq = q->n_seq;
+    a.T = q->T;
+    a.Hq = q->n_q_heads;
+    a.hpk = q->n_q_heads / c->cfg.n_kv_heads;
+    a.tables = q->tables;
+    a.lens = q->lens;
+    const SplitArgs f = factors(c, q);
+    a.qscale = f.qscale;
+    a.softcap_a = f.softcap_a;
+    a.softcap_b = f.softcap_b;
+    a.window = f.window;
+    a.decay = decay;
+    a.scores = c->row_scores;
+    a.sms = c->num_sms;
+    cudaError_t e = launch_scored(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "row score kernel");
+}
+
+kvq_status kvq_paged_select_rows(kvq_paged* c, const int* tables, const int* lens, int n_seq, int keep, int n_first,
+                                 int n_last, int* rows, void* stream) {
+    kvq_status st = check_evict(c, tables, lens, n_seq, rows, keep);
+    if (st != KVQ_OK) return st;
+    if (!c->row_scores) return fail(KVQ_EINVAL, "the cache keeps no row scores (kvq_paged_set_scores)");
+    if (n_first < 0 || n_last < 0 || n_first > keep || n_last > keep - n_first)
+        return fail(KVQ_EINVAL, "keep must hold n_first + n_last rows");
+    RowsArgs a = {};
+    a.g = c->g;
+    a.tables = tables;
+    a.lens = lens;
+    a.scores = c->row_scores;
+    a.rows = rows;
+    a.n_seq = n_seq;
+    a.keep = keep;
+    a.n_first = n_first;
+    a.n_last = n_last;
+    cudaError_t e = launch_select_rows(a, c->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "row selection kernel");
+}
+
+kvq_status kvq_paged_compact(kvq_paged* c, const int* tables, const int* lens, int n_seq, const int* rows, int keep,
+                             const int* tables_out, int* lens_out, void* stream) {
+    kvq_status st = check_evict(c, tables, lens, n_seq, rows, keep);
+    if (st != KVQ_OK) return st;
+    if (!lens_out) return fail(KVQ_EINVAL, "lens_out is NULL");
+    if (tables_out == tables) return fail(KVQ_EINVAL, "tables_out must be NULL (in place) or hold other pages than tables");
+    // (a sequence holds no more)
+    const int most = std::min(keep, c->cfg.max_pages * c->cfg.page_rows);
+    if (c->cfg.bounds && (long long)n_seq * most * c->cfg.n_kv_heads > (1LL << 31))
+        return fail(KVQ_ERANGE, "n_seq * keep too large for one call");
+    if ((long long)n_seq * c->cfg.n_kv_heads * (most / 128 + 1) > 0x7fffffffLL)     // (a block for 128 rows at least)
+        return fail(KVQ_ERANGE, "n_seq * keep too large for one call");
+    CompactArgs a = {};
+    a.g = c->g;
+    a.tables = tables;
+    a.tables_out = tables_out ? tables_out : tables;
+    a.lens = lens;
+    a.lens_out = lens_out;
+    a.rows = rows;
+    a.scores = c->row_scores;
+    a.arrived = reinterpret_cast<int*>(c->ws + c->off_arrived);
+    a.n_seq = n_seq;
+    a.keep = keep;
+    a.most = most;
+    a.in_place = !tables_out;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_compact(a, c->num_sms, s);
+    if (e != cudaSuccess) return cuda_fail(e, "row compaction kernel");
+    if (!c->cfg.bounds) return KVQ_OK;
+    const Rows r{a.tables_out, lens_out, nullptr, n_seq, most, n_seq * most};
+    return bounds_of(c, r, s);
 }
 
 kvq_status kvq_paged_read_error(kvq_paged* c, int* err, void* stream) {

@@ -15,7 +15,8 @@
 // splits exactly into a rounded product and its error (fma), the whole turns
 // drop out exactly, and the rest is added: the angle is good to 2^-24 of a turn
 // at any position below 2^24, where p f in one fp32 product would be off by
-// p 2^-24 radians.
+// p 2^-24 radians.  Positions are a row's index in its sequence, or given for each
+// row on up to four axes, of which each pair of elements has one.
 #include "kvq_paged.cuh"
 #include "kvq_quant.cuh"
 
@@ -126,6 +127,27 @@ __device__ __forceinline__ void put_angle(float2* cs_of, float2 f, int pos, int 
     sincospif(2.f * turn, &sn, &cs);
     const int grp = interleaved ? 4 : 8;
     cs_of[(pr % grp) * (half / grp) + pr / grp] = make_float2(cs, sn);
+}
+
+// A row's given positions, all -1 (and the error word set) where one is out of range
+__device__ __forceinline__ void given_positions(const AppendArgs& a, int row, int (&at)[kMaxAxes]) {
+    bool ok = true;
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; ++x) {
+        at[x] = x < a.n_axes ? a.positions[(long long)row * a.n_axes + x] : 0;
+        ok = ok && at[x] >= 0 && at[x] < kMaxPosition;
+    }
+    if (ok) return;
+    atomicExch(a.g.err, kErrCounter);
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; ++x) at[x] = -1;
+}
+
+// The row scores of a row just placed start at 0: KV heads h, h + step ..
+__device__ __forceinline__ void clear_scores(const AppendArgs& a, const Place& p, int h, int step) {
+    const int in = p.pos & (a.g.page_rows - 1);
+    const long long page = (p.cell - (long long)(in >> 4) * a.g.cell_bytes) / a.g.page_bytes;
+    for (; h < a.g.Hkv; h += step) a.row_scores[(page * a.g.Hkv + h) * a.g.page_rows + in] = 0.f;
 }
 
 // Rotate elements e0 .. e0 + 7 (x) below rot of a head row; y: those that the half-split rotation pairs them with
@@ -318,6 +340,7 @@ template <int LR, bool BF16, bool BOUNDS>
 __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
     extern __shared__ float2 s_cs[];               // [TT][rope_dim / 2]
     __shared__ Place s_place[kTT];
+    __shared__ int s_at[kTT][kMaxAxes];            // given positions
     constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR, QPW = 64 / LR;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row0 = blockIdx.x * TT;
@@ -328,13 +351,20 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
         const int row = row0 + lane, i = entry_of_rows<kTT>(a.r, row0, lane);
         Place p{-1, -1, 0, 0, 0};
         if (lane < TT && row < a.r.rows) p = place_in(a.g, a.r, row, i, true);
+        if (a.positions && p.pos >= 0) {
+            int at[kMaxAxes];
+            given_positions(a, row, at);
+            if (at[0] < 0) p = Place{-1, -2, 0, 0, 0};
+#pragma unroll
+            for (int x = 0; x < kMaxAxes; ++x) s_at[lane][x] = at[x];
+        }
         if (lane < TT) s_place[lane] = p;
     }
     __syncthreads();
     // (an indexed read of the frequencies takes a step for each lane: one a thread)
     for (int pr = tid % (kThreads / TT); pr < half; pr += kThreads / TT) {
         const int tt = tid / (kThreads / TT);
-        put_angle(s_cs + tt * half, fq.f[pr], s_place[tt].pos, pr, half, a.interleaved);
+        put_angle(s_cs + tt * half, fq.f[pr], a.positions && s_place[tt].pos >= 0 ? s_at[tt][fq.axis[pr]] : s_place[tt].pos, pr, half, a.interleaved);
     }
     __syncthreads();
     // a warp's token, and its share of the token's units
@@ -342,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
     const int u0 = blockIdx.y * wpt + warp - tt * wpt, du = gridDim.y * wpt;
     const Place pl = s_place[tt];
     if (pl.pos < 0) return;
+    if (a.row_scores && blockIdx.y == 0 && pl.cell >= 0) clear_scores(a, pl, (warp - tt * wpt) * 32 + lane, wpt * 32);
     const float2* cs = s_cs + tt * half;
     const long long row = row0 + tt;
     const int uq = a.q ? (a.Hq + QPW - 1) / QPW : 0, uk = (a.g.Hkv + JPW - 1) / JPW;
@@ -497,6 +528,7 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
     constexpr int D = NB * 32, LR = D / 8, BL = NB < 4 ? NB : 4, RT = 32 / BL, W = 2 * RT;
     extern __shared__ float2 s_cs[];                 // [W][rope_dim / 2]
     __shared__ Place s_place[W];
+    __shared__ int s_at[W][kMaxAxes];                // given positions; -1: the row is skipped
     __shared__ int s_from[W];                        // the piece of a row: index of its first row, -1 none of this CTA's
     __shared__ __align__(16) uint8_t s_stage[kCellWarps][1024];
     constexpr int kSlots = 32;                       // threads that take different pairs
@@ -514,24 +546,36 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
             const int from = p.pos < 0 ? -1 : queries ? lane : lane - min(p.pos & (RT - 1), p.pos - p.first);
             s_place[lane] = p;
             s_from[lane] = from < RT ? from : -1;    // (below 0: the CTA before has it)
+            if (a.positions && from >= 0 && from < RT) {
+                int at[kMaxAxes];
+                given_positions(a, row, at);
+#pragma unroll
+                for (int x = 0; x < kMaxAxes; ++x) s_at[lane][x] = at[x];
+            }
         }
     }
     __syncthreads();
+    const auto skipped = [&](int i) { return a.positions && s_at[i][0] < 0; };   // (of rows that are this CTA's)
     // a pair a thread (an indexed read of the frequencies takes a step for each lane), every token
     const int stride_cs = half + 1;                  // rows of the tables start in different banks
     for (int pr = tid % kSlots; pr < half; pr += kSlots) {
         const float2 f = fq.f[pr];
+        const int axis = a.positions ? fq.axis[pr] : 0;
         for (int tt = tid / kSlots; tt < W; tt += kCellThreads / kSlots)
-            if (s_from[tt] >= 0) put_angle(s_cs + tt * stride_cs, f, s_place[tt].pos, pr, half, a.interleaved);
+            if (s_from[tt] >= 0)
+                put_angle(s_cs + tt * stride_cs, f, a.positions ? s_at[tt][axis] : s_place[tt].pos, pr, half, a.interleaved);
     }
     const int per = a.g.Hkv * (NB / BL);             // tasks of a piece and kind
     const int li = lane / BL, bl = lane % BL;        // row of the piece, block of the four
     if (queries) {
         __syncthreads();
         for (int i = warp; i < RT; i += kCellWarps)      // a row a warp
-            if (s_from[i] >= 0) rotate_queries<LR, BF16>(a, row0 + i, s_cs + i * stride_cs, 0, 1, lane);
+            if (s_from[i] >= 0 && !skipped(i)) rotate_queries<LR, BF16>(a, row0 + i, s_cs + i * stride_cs, 0, 1, lane);
         return;
     }
+    if (a.row_scores)
+        for (int i = warp; i < W; i += kCellWarps)
+            if (s_from[i] >= 0 && s_place[i].cell >= 0 && !skipped(i)) clear_scores(a, s_place[i], lane, 32);
     // values first, for they need no angles
 #pragma unroll 1
     for (int kind = 1; kind >= 0; --kind) {
@@ -543,7 +587,7 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
             const Place pf = s_place[s];
             const int skew = pf.pos & (RT - 1), wi = s + li - skew;
             if (pf.cell < 0) continue;
-            const bool on = wi >= s && wi < W && s_from[wi] == s;
+            const bool on = wi >= s && wi < W && s_from[wi] == s && !skipped(wi);
             const bool full = __all_sync(0xffffffffu, on);
             const int t = (pf.pos - skew + li) & 15, j = (t & 7) >> 1, sb = t & 1, hh = t >> 3;
             const long long row = row0 + wi;

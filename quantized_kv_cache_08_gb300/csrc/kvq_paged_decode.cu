@@ -63,31 +63,10 @@ constexpr int groups_of() { return warps_of<NB, TILE>() / 4; }
 template <int TILE>
 constexpr int queries_of() { return TILE == kT16 || TILE == kF32W ? 16 : 8; }
 
-// c = a b + z (z: four zeros that stay in registers, where a constant would be
-// written to four new ones for each product)
-__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1, const float (&z)[4]) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
-}
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
-// code bytes (biased by 128) sel of w under the exponent of 1024, minus 1152: exact
-__device__ __forceinline__ uint32_t k_pair(uint32_t w, uint32_t sel, uint32_t exps) {
-    return as_u32(__hsub2(as_h2(__byte_perm(w, exps, sel)), as_h2(0x64806480u)));
-}
-__device__ __forceinline__ float load_q(const void* q, long long idx, int bf16) {
-    if (bf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q)[idx]);
-    return reinterpret_cast<const float*>(q)[idx];
 }
 
 // ------------------------------------------------------------ split kernel
@@ -1002,7 +981,10 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             const float M = settle(l, m, ri.bad[row]) ? m - kShift : kNegInf;
             if (whole) {
                 const Query q = query_of(a, plan[f.e], f.e, f.kh, f.sl * QPI + row);
-                store4(a, (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + col, o, sink_weight(sink_of(a, q.h), M, l));
+                const long long orow = ((long long)q.seq * a.T + q.t) * a.Hq + q.h;
+                const float w = sink_weight(sink_of(a, q.h), M, l);
+                store4(a, orow * D + col, o, w);
+                if (a.stats && col == 0) a.stats[orow] = make_float2(M, w);
             } else {
                 const long long at = (range + key) * a.rec_rows + row;
                 *reinterpret_cast<float4*>(a.part_o + at * D + col) = o;
@@ -1051,8 +1033,12 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
                             for (int w = 1; w < sets; ++w)
                                 add_sum(s, s_m[w0 + w][row], s_l[w0 + w][row], *reinterpret_cast<const float4*>(p + (size_t)w * QPI * PAD + row * PAD + col));
                     }
-                    if (on && set == 0)
-                        store4(a, (((long long)q.seq * a.T + q.t) * a.Hq + q.h) * D + col, s.o, sink_weight(sink, s.M, s.L));
+                    if (on && set == 0) {
+                        const long long orow = ((long long)q.seq * a.T + q.t) * a.Hq + q.h;
+                        const float w = sink_weight(sink, s.M, s.L);
+                        store4(a, orow * D + col, s.o, w);
+                        if (a.stats && col == 0) a.stats[orow] = make_float2(s.M, w);
+                    }
                 }
             }
         }

@@ -74,6 +74,28 @@ __device__ __forceinline__ uint32_t v_codes(uint32_t unit, uint32_t nib, int n4,
     else return and_or(nib >> (4 * n4), 0x000f000fu, and_or(unit >> 11, 0x00100010u, magic));
 }
 
+// c = a b + z (z: four zeros that stay in registers, where a constant would be
+// written to four new ones for each product)
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1, const float (&z)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// code bytes (biased by 128) sel of w under the exponent of 1024, minus 1152: exact
+__device__ __forceinline__ uint32_t k_pair(uint32_t w, uint32_t sel, uint32_t exps) {
+    return as_u32(__hsub2(as_h2(__byte_perm(w, exps, sel)), as_h2(0x64806480u)));
+}
+__device__ __forceinline__ float load_q(const void* q, long long idx, int bf16) {
+    if (bf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q)[idx]);
+    return reinterpret_cast<const float*>(q)[idx];
+}
+
 // ------------------------------------------------------------ work entries
 
 __device__ __forceinline__ bool len_ok(const SplitArgs& a, int len) {

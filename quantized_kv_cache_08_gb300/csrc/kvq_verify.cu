@@ -1,0 +1,282 @@
+// Verification of drafted tokens (include/kvq.h, kvq_verify).
+//
+// Mathematics.  Draft d_t of a sequence stands while u_t q_t(d_t) < p_t(d_t); the
+// products of two f32 numbers are exact in f64, so the test is one of real
+// numbers.  At row a, the first whose draft falls or is none, the next token is
+// drawn from weights w_i = max(P_i - Q_i, 0) (P_i where no draft stood), P and Q
+// the probabilities in whole units of 2^-52: with S their sum it is the first i
+// whose running sum passes floor(S u).  Sums of whole numbers do not depend on
+// their order, so the row may be cut anywhere and the token stays the same, run
+// by run and cut by cut; f32 sums over a row of 2^17 are off by more than its
+// smaller probabilities.
+//
+// A cluster of blocks shares a row: each sums its part (every warp a stretch of
+// it), the blocks tell each other their sums, and the one in whose part the
+// running sum passes goes down into it, a warp's stretch cut over all warps at a
+// time, until a stretch is 32 elements.  One row of p and q is read of T; the
+// parts read again come from L2.
+#include "../../include/kvq.h"
+#include "kvq_cluster.cuh"
+#include "kvq_error.h"
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace kvq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+using u64 = unsigned long long;
+
+struct Args {
+    const void* target;
+    const void* draft;
+    const int* tokens;
+    const float* uniform;
+    long long target_seq, target_row, draft_seq, draft_row;
+    int T, vocab;
+    int* accept;
+    int* next;
+    int* lens;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float element(const void* row, long long i) {
+    if constexpr (BF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
+    else return reinterpret_cast<const float*>(row)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ const void* row_at(const void* base, long long i) {
+    return reinterpret_cast<const uint8_t*>(base) + i * (BF16 ? 2 : 4);
+}
+
+// a probability in units of 2^-52, rounded down: 0 where it is not above 0 (NaN too), 1 where it is above 1
+__device__ __forceinline__ u64 units(float x) {
+    x = x > 0.f ? fminf(x, 1.f) : 0.f;
+    const uint32_t b = __float_as_uint(x);
+    const int e = (int)(b >> 23) - 98;                   // x = m 2^(e - 52); (subnormals end as 0)
+    const uint32_t m = ((b & 0x7fffffu) | 0x800000u) >> min(max(-e, 0), 31);
+    return (u64)m * (1u << max(e, 0));
+}
+
+struct Sum {
+    u64 w, p;
+};
+
+// What an element weighs.  tok: of a lone draft, which weighs nothing (-1: none)
+template <bool Q>
+__device__ __forceinline__ void add(Sum& s, float p, float q, bool out) {
+    const u64 P = units(p);
+    s.p += P;
+    if constexpr (Q) {
+        const u64 R = units(q);
+        s.w += P > R ? P - R : 0ull;
+    } else {
+        s.w += out ? 0ull : P;
+    }
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The sums over [lo, hi) by one warp, every lane's share.  lo and hi are
+// multiples of 8 (or the row's end); vec: both rows start on 16 bytes
+template <bool BF16, bool Q>
+__device__ __forceinline__ Sum sum_range(const void* p, const void* q, int lo, int hi, int tok, bool vec, int lane) {
+    constexpr int V = BF16 ? 8 : 4, U = 4;               // elements of a load, loads in flight
+    Sum s{0, 0};
+    int i = lo;
+    if (vec) {
+        for (; i + U * V * 32 <= hi; i += U * V * 32) {
+            uint4 a[U], b[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const long long at = i + (k * 32 + lane) * V;
+                a[k] = __ldg(reinterpret_cast<const uint4*>(row_at<BF16>(p, at)));
+                if constexpr (Q) b[k] = __ldg(reinterpret_cast<const uint4*>(row_at<BF16>(q, at)));
+                else b[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int at = i + (k * 32 + lane) * V;
+                const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, y[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    if constexpr (BF16) {
+                        add<Q>(s, __uint_as_float(x[w] << 16), __uint_as_float(y[w] << 16), at + 2 * w == tok);
+                        add<Q>(s, __uint_as_float(x[w] & 0xffff0000u), __uint_as_float(y[w] & 0xffff0000u), at + 2 * w + 1 == tok);
+                    } else {
+                        add<Q>(s, __uint_as_float(x[w]), __uint_as_float(y[w]), at + w == tok);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll 8
+    for (int at = i + lane; at < hi; at += 32) add<Q>(s, element<BF16>(p, at), Q ? element<BF16>(q, at) : 0.f, at == tok);
+    return s;
+}
+
+// Sequence blockIdx.x / C by a cluster of C blocks
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ Args a) {
+    __shared__ int s_row, s_held, s_tok;
+    __shared__ u64 s_w[kWarps], s_p[kWarps];
+    __shared__ u64 s_all[cluster::kMaxCluster][2];       // the blocks' sums, written by themselves
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int C = cluster::size(), rank = cluster::rank();
+    const long long b = blockIdx.x / C;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // ---- the first draft that does not stand
+    if (warp == 0) {
+        int row = a.T - 1, tok = -1;
+        for (int t0 = 0; t0 < a.T - 1; t0 += 32) {
+            const int t = t0 + lane;
+            int d = -1;
+            bool ok = false;
+            if (t < a.T - 1) {
+                d = a.tokens[b * (a.T - 1) + t];
+                if (d >= 0 && d < a.vocab) {
+                    const float p = element<BF16>(a.target, b * a.target_seq + t * a.target_row + d);
+                    const float q = a.draft ? element<BF16>(a.draft, b * a.draft_seq + t * a.draft_row + d) : 1.f;
+                    ok = (double)a.uniform[b * a.T + t] * (double)q < (double)p;
+                } else {
+                    d = -1;
+                }
+            }
+            const unsigned no = __ballot_sync(0xffffffffu, t < a.T - 1 && !ok);
+            if (no) {
+                const int l = __ffs(no) - 1;
+                row = t0 + l;
+                tok = __shfl_sync(0xffffffffu, d, l);
+                break;
+            }
+        }
+        if (lane == 0) {
+            s_row = row;
+            s_held = tok >= 0;                           // a draft stood here: its share is taken off
+            s_tok = tok;
+            if (rank == 0) {
+                a.accept[b] = row + 1;
+                a.next[b] = -1;                          // (the block that finds the token writes it behind the cluster's barrier)
+                if (a.lens) a.lens[b] -= a.T - 1 - row;
+            }
+        }
+    }
+    __syncthreads();
+    const int row = s_row;
+    const bool with_q = s_held && a.draft;
+    const int tok = s_held && !a.draft ? s_tok : -1;
+    const void* p = row_at<BF16>(a.target, b * a.target_seq + row * a.target_row);
+    const void* q = with_q ? row_at<BF16>(a.draft, b * a.draft_seq + row * a.draft_row) : p;
+    const bool vec = (((uintptr_t)p | (uintptr_t)q) & 15) == 0;
+    // ---- sums of this block's part
+    auto part = [](int n, int parts) { return ((n + parts - 1) / parts + 31) & ~31; };
+    int lo = min(a.vocab, rank * part(a.vocab, C)), hi = min(a.vocab, lo + part(a.vocab, C));
+    int per = part(hi - lo, kWarps);
+    auto sums = [&](int from, int to) {
+        const int x = min(to, from + warp * per), y = min(to, x + per);
+        Sum s = with_q ? sum_range<BF16, true>(p, q, x, y, -1, vec, lane) : sum_range<BF16, false>(p, q, x, y, tok, vec, lane);
+        s.w = warp_sum(s.w);
+        s.p = warp_sum(s.p);
+        if (lane == 0) {
+            s_w[warp] = s.w;
+            s_p[warp] = s.p;
+        }
+        __syncthreads();
+    };
+    sums(lo, hi);
+    if (tid < 2 * C) {
+        u64 t = 0;
+        const u64* from = tid & 1 ? s_p : s_w;
+        for (int w = 0; w < kWarps; ++w) t += from[w];
+        cluster::store(cluster::map(&s_all[rank][tid & 1], tid >> 1), t);
+    }
+    cluster::sync();
+    u64 before[2] = {0, 0}, all[2] = {0, 0};
+    for (int r = 0; r < C; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (r < rank) before[k] += s_all[r][k];
+            all[k] += s_all[r][k];
+        }
+    const bool by_p = all[0] == 0;                       // nothing is left of p over q: p itself
+    const u64 S = all[by_p], first = before[by_p], mine = s_all[rank][by_p];
+    if (S == 0) return;
+    const float u = a.uniform[b * a.T + a.T - 1];
+    const uint32_t U = u > 0.f ? (uint32_t)fminf(u * 2147483648.f, 2147483520.f) : 0u;   // (the f32 below 2^31)
+    u64 x = __umul64hi(S, (u64)U << 33);                 // floor(S U 2^-31)
+    if (x < first || x - first >= mine) return;
+    x -= first;
+    // ---- down into the stretch where the running sum passes x
+    for (;;) {
+        const u64* s = by_p ? s_p : s_w;
+        int w = 0;
+        while (w < kWarps - 1 && x >= s[w]) x -= s[w++];
+        lo = min(hi, lo + w * per);
+        hi = min(hi, lo + per);
+        __syncthreads();                                 // (before the sums are written again)
+        if (hi - lo <= 32) break;
+        per = part(hi - lo, kWarps);
+        sums(lo, hi);
+    }
+    if (warp == 0) {
+        const int i = lo + lane;
+        u64 v = 0;
+        if (i < hi) {
+            Sum s{0, 0};
+            const float pi = element<BF16>(p, i);
+            if (with_q) add<true>(s, pi, element<BF16>(q, i), false);
+            else add<false>(s, pi, 0.f, i == tok);
+            v = by_p ? s.p : s.w;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, i < hi && v > x);
+        if (lane == 0 && over) a.next[b] = lo + __ffs(over) - 1;
+    }
+}
+
+}  // namespace
+
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" kvq_status kvq_verify(const kvq_verify_args* v, void* stream) {
+    if (!v) return fail(KVQ_EINVAL, "args is NULL");
+    if (v->dtype != KVQ_F32 && v->dtype != KVQ_BF16) return fail(KVQ_EINVAL, "dtype must be f32 or bf16");
+    if (v->n_seq < 1 || v->n_seq > 65536) return fail(KVQ_EINVAL, "n_seq=%d outside [1, 65536]", v->n_seq);
+    if (v->T < 1 || v->T > 512) return fail(KVQ_EINVAL, "T=%d outside [1, 512]", v->T);
+    if (v->vocab < 1 || v->vocab > (1 << 24)) return fail(KVQ_EINVAL, "vocab=%d outside [1, 2^24]", v->vocab);
+    if (!v->target || !v->uniform || !v->accept || !v->next) return fail(KVQ_EINVAL, "target, uniform, accept or next is NULL");
+    if (v->T > 1 && !v->tokens) return fail(KVQ_EINVAL, "tokens is NULL");
+    const size_t size = v->dtype == KVQ_BF16 ? 2 : 4;
+    if ((size_t)v->target % size || (size_t)v->draft % size || ((size_t)v->tokens | (size_t)v->uniform | (size_t)v->accept | (size_t)v->next | (size_t)v->lens) % 4)
+        return fail(KVQ_EINVAL, "a pointer is not aligned to its elements");
+    if (v->target_seq < 0 || v->target_row < 0 || v->draft_seq < 0 || v->draft_row < 0)
+        return fail(KVQ_EINVAL, "strides must be >= 0");
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+    Args a{v->target, v->draft, v->tokens, v->uniform, v->target_seq, v->target_row, v->draft_seq, v->draft_row,
+           v->T, v->vocab, v->accept, v->next, v->lens};
+    // blocks of a row: more while SMs are idle and a part keeps some 2000 elements
+    int C = 1;
+    while (C < cluster::kMaxCluster && (long long)v->n_seq * C < 4LL * sms && v->vocab > 2048 * C) C *= 2;
+    const dim3 grid((unsigned)(v->n_seq * C));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    e = v->dtype == KVQ_BF16 ? cluster::launch(verify_kernel<true>, grid, C, kThreads, 0, s, a)
+                             : cluster::launch(verify_kernel<false>, grid, C, kThreads, 0, s, a);
+    return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "verify kernel");
+}
