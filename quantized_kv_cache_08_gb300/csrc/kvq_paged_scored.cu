@@ -9,12 +9,14 @@
 // scores s are computed as the decode computes them, on the same instructions, so
 // that numerators and denominators agree.
 //
-// A cell's keys lie in the order of the products' operand registers, so a warp
-// loads them from global memory straight into its fragments, the next cell's while
-// it multiplies this one's: no shared memory, no barriers and no copies to wait for, and as
-// many small blocks an SM as registers allow.  Blocks take equal ranges of the
-// cells of all (sequence, KV head) pairs.  Queries stay in shared memory in tiles
-// (16 of bf16, 8 of f32 in two fp16 parts), and what does not fit is another pass over
+// A cell's keys lie in the order of the products' operand registers.  The rows
+// are M here (16 of them, both halves of a cell in one product) and 8 queries N, the
+// other way round than in the decode, for nothing follows that wants the weights
+// in another order: half as many products, and a lane's sums are of two rows only.
+// Each warp keeps its own ring of bulk copies of keys.  Blocks are small, several an SM, and
+// take equal ranges of the cells of all (sequence, KV head) pairs: while one
+// changes its queries the others multiply.  Queries stay in shared memory in tiles of 8
+// (f32 ones as two fp16 parts), and what does not fit is another pass over
 // the range's keys, which then come from L2.  A row's score is one lane's alone and its
 // gains are added in the tiles' order: the same bits on every run.
 #include "kvq_paged.cuh"
@@ -29,37 +31,46 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 8;               // queries
 template <int NB>
-constexpr int blocks_of() { return NB == 2 ? 5 : NB == 4 ? 4 : 2; }
+constexpr int blocks_of() { return NB == 8 ? 4 : 5; }
+template <int NB>
+constexpr int stages_of() { return NB == 8 ? 2 : 4; }
+template <int NB, bool F8>
+constexpr int key_bytes() { return NB * (F8 ? 512 : 544); }
+template <int NB, bool F32Q>
+constexpr int tile_bytes() { return NB * 512 * (F32Q ? 2 : 1); }
 
 struct Row {
-    float fac, m, w;
-    int lo, hi;
+    float fac, m, w;                   // a weight is w 2^(fac x product - m)
+    int lo, hi, pad[3];
 };
 
-// What a warp holds of a cell's keys
-template <int NB, bool F8>
-struct Keys {
-    uint4 k[NB / 2][2];
-    uint4 d[F8 ? 1 : NB / 2];
-    float old;                     // this lane's row's score
-    long long at;                  // where the cell's scores lie, -1: no cell
-    int row0;
-    bool seen;                     // by a query: the keys are loaded
-};
+// Shared memory: query tiles, their rows, the plan, then each warp's ring
+template <int NB, bool F8, bool F32Q>
+__host__ __device__ constexpr size_t ring_at(int slices, int n_seq) {
+    return ((size_t)slices * (tile_bytes<NB, F32Q>() + kTile * sizeof(Row)) + (size_t)(n_seq + 1) * 8 + 127) / 128 * 128;
+}
 
 template <int NB, bool F8, bool F32Q>
 __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const __grid_constant__ ScoredArgs a) {
-    constexpr int D = NB * 32, QPI = F32Q ? 8 : 16, NQ = QPI / 8;
+    constexpr int D = NB * 32, STAGES = stages_of<NB>(), KEYS = key_bytes<NB, F8>(), TILE = tile_bytes<NB, F32Q>();
     constexpr int CELL = NB * (F8 ? 1024 : 928);
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_wsum[kWarps];
-    __shared__ int s_ext[4];
+    __shared__ int s_ext[4], s_abort;
+    __shared__ int s_page[kWarps][STAGES];         // of the cell in a stage, -1: none
+    __shared__ __align__(8) uint64_t s_bar[kWarps][STAGES];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
-    const int QB = a.slices * QPI;
+    const int QB = a.slices * kTile;
     uint8_t* qs = smem;
-    Row* rows = reinterpret_cast<Row*>(smem + (size_t)a.slices * NB * 1024);
-    long long* plan = reinterpret_cast<long long*>(smem + (size_t)a.slices * NB * 1024 + (((size_t)QB * sizeof(Row) + 15) & ~(size_t)15));
+    Row* rows = reinterpret_cast<Row*>(smem + (size_t)a.slices * TILE);
+    long long* plan = reinterpret_cast<long long*>(rows + QB);
+    uint8_t* ring = smem + ring_at<NB, F8, F32Q>(a.slices, a.n_seq) + (size_t)warp * STAGES * KEYS;
+    const uint32_t ring_u = dev::smem_u32(ring), bar0 = dev::smem_u32(&s_bar[warp][0]);
+    if (lane < STAGES) dev::mbar_init(bar0 + 8u * lane, 1);
+    if (tid == 0) s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     wait_for_earlier();
     let_next_start();
     // ---- cells of each sequence: all below its length (with nothing to fade, those that a query sees)
@@ -103,8 +114,11 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
     float zero[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
-    const uint32_t exps = held(0x64646464u);
+    const uint32_t exps = held(0x64646464u), pick = g & 1 ? 0x7632u : 0x5410u;
     const int cps = a.g.page_shift - 4, mask = (1 << cps) - 1;
+    const int my = g + 8 * (j & 1);                        // the row of a cell whose score is this lane's (j < 2)
+    int st = 0;
+    uint32_t phase = 0;
     while (x < x1) {
         // ---- fragment: cells [ca, cb) of KV head kh of sequence e
         int e = 0;
@@ -116,33 +130,62 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
                 else hi = mid;
             }
         }
-        const long long nc = plan[e + 1] - plan[e], in_e = x - plan[e] * a.g.Hkv;
-        const int kh = (int)(in_e / nc);
-        const int ca = (int)(in_e - kh * nc), cb = (int)min(nc, ca + (x1 - x));
+        const long long in_e = x - plan[e] * a.g.Hkv;
+        const int nc = (int)(plan[e + 1] - plan[e]);
+        const int kh = in_e < (1LL << 31) ? (int)((unsigned)in_e / (unsigned)nc) : (int)(in_e / nc);
+        const int ca = (int)(in_e - (long long)kh * nc), cb = (int)min((long long)nc, ca + (x1 - x));
         x += cb - ca;
         const int len = a.lens[e], c0 = first_cell(len), nq = a.hpk * a.T;
+        const int lo_row = first_row(len);                 // rows before it no query sees
         const int* table = a.tables + (long long)e * a.g.max_pages;
         for (int q0 = 0; q0 < nq; q0 += QB) {
-            const int n = min(QB, nq - q0), ns = (n + QPI - 1) / QPI;
-            // ---- queries [q0, q0 + n) into tiles, as the decode lays them out; one that
-            // adds nothing is zeros with weight 0
+            const int n = min(QB, nq - q0), ns = (n + kTile - 1) / kTile;
+            const float decay = q0 == 0 ? a.decay : 1.f;
+            // ---- the producer side: the warp's cells in order, a lane holding one of the next 32 pages
+            int pages = 0, from = 32, pc = ca + warp, ps = st;
+            auto produce = [&]() {
+                if (pc >= cb) return;
+                if (from == 32) {
+                    from = 0;
+                    const int c = pc + lane * kWarps;
+                    pages = c < cb ? table[(c0 + c) >> cps] : 0;
+                }
+                if (lane == from) {
+                    const int at = c0 + pc, in = at & mask;
+                    const bool there = pages >= 0 && pages < a.g.n_pages;              // (reported by the decode)
+                    const uint32_t bar = bar0 + 8u * ps;
+                    s_page[warp][ps] = there ? pages : -1;
+                    if (there && at * 16 + 16 > lo_row) {
+                        dev::mbar_expect_tx(bar, KEYS);
+                        dev::bulk_g2s(ring_u + (uint32_t)(ps * KEYS), a.g.pool + (long long)pages * a.g.page_bytes + (long long)(kh * (mask + 1) + in) * CELL, KEYS, bar);
+                    } else {
+                        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+                    }
+                }
+                ++from;
+                pc += kWarps;
+                if (++ps == STAGES) ps = 0;
+            };
+#pragma unroll 1
+            for (int i = 0; i < STAGES; ++i) produce();
+            // ---- queries [q0, q0 + n) into tiles; one that adds nothing is zeros with weight 0
             __syncthreads();
             if (tid < 4) s_ext[tid] = tid == 0 || tid == 3 ? 0 : 0x7fffffff;      // lo_max, hi_min, lo_min, hi_max
             __syncthreads();
-            for (int r = warp; r < ns * QPI; r += kWarps) {
+            for (int r = warp; r < ns * kTile; r += kWarps) {
                 float v[NB];
-                float2 st = make_float2(0.f, 0.f);
+                float2 stat = make_float2(0.f, 0.f);
                 int lo = 0, hi = 0;
                 if (r < n) {
                     const int t = (q0 + r) / a.hpk, h = kh * a.hpk + (q0 + r) - t * a.hpk;
                     const long long at = ((long long)e * a.T + t) * a.Hq + h;
                     hi = len - a.T + t + 1;
                     lo = a.window > 0 ? max(0, hi - a.window) : 0;
-                    if (hi > lo) st = a.stats[at];
+                    if (hi > lo) stat = a.stats[at];
 #pragma unroll
                     for (int b = 0; b < NB; ++b) v[b] = load_q(a.q, at * D + 32 * b + lane, a.bf16);
                 }
-                const bool on = hi > lo && st.y > 0.f && st.x > kNegInf && st.x < kInf;
+                const bool on = hi > lo && stat.y > 0.f && stat.x > kNegInf && stat.x < kInf;
                 uint32_t am = 0u;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -153,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
                 const int ex = am > 0u ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
                 const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
                 if (lane == 0) {
-                    rows[r] = Row{factor(a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23)), on ? st.x : 0.f, on ? st.y : 0.f, on ? lo : 0, on ? hi : 0};
+                    rows[r] = Row{factor(a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23)), on ? stat.x : 0.f, on ? stat.y : 0.f, on ? lo : 0, on ? hi : 0, {}};
                     if (on) {
                         atomicMax(&s_ext[0], lo);
                         atomicMin(&s_ext[1], hi);
@@ -162,159 +205,136 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
                     }
                 }
                 const int wi = lane & 7, jj = lane >> 3;
-                const int reg = ((wi & 3) >> 1) * 2, half = wi & 1, rr = r % QPI;
-                uint8_t* tile = qs + (size_t)(r / QPI) * NB * 1024;
+                uint8_t* tile = qs + (size_t)(r / kTile) * TILE + (4 * (r % kTile) + jj) * 8 + ((wi & 3) >> 1) * 4 + (wi & 1) * 2;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const float y = v[b] * up;
                     const __half top = __float2half_rn(y);
-                    const int at = (2 * b + (wi >> 2)) * 32 + 4 * (rr & 7) + jj;
-                    __half* dst = reinterpret_cast<__half*>(tile + at * 16);
-                    if (F32Q) {
-                        dst[2 * reg + half] = top;
-                        dst[2 * (reg + 1) + half] = __float2half_rn(y - __half2float(top));
-                    } else {
-                        dst[2 * (reg + (rr >> 3)) + half] = top;
-                    }
+                    __half* dst = reinterpret_cast<__half*>(tile + (2 * b + (wi >> 2)) * 256);
+                    *dst = top;
+                    if constexpr (F32Q) dst[NB * 256] = __float2half_rn(y - __half2float(top));      // the low parts lie behind
                 }
             }
             __syncthreads();
             const int lo_max = s_ext[0], hi_min = s_ext[1], lo_min = s_ext[2], hi_max = s_ext[3];
-            const float decay = q0 == 0 ? a.decay : 1.f;
-            // ---- its cells, warp by warp; lane (g, j) keeps row 8 (g / 4) + 2 j + g / 2 % 2 of their scores (g even)
-            const int my = 8 * (g >> 2) + 2 * j + ((g >> 1) & 1);
-            int pages = 0, from = 32;                              // of the warp's next 32 cells, a lane each
-            auto fetch = [&](int c, Keys<NB, F8>& y) {
-                y.at = -1;
-                if (c >= cb) return;
-                if (from == 32) {
-                    from = 0;
-                    const int cc = c + lane * kWarps;
-                    pages = cc < cb ? table[(c0 + cc) >> cps] : 0;
+            // ---- its cells, warp by warp; the next one's score is on its way
+            auto score_of = [&](int page, int c) { return ((long long)page * a.g.Hkv + kh) * a.g.page_rows + ((c0 + c) & mask) * 16 + my; };
+            auto old_of = [&](int stage, int c) {
+                float v = 0.f;
+                if (c < cb && j < 2 && decay > 0.f) {
+                    const int page = s_page[warp][stage];
+                    if (page >= 0) v = a.scores[score_of(page, c)];
                 }
-                const int pg = __shfl_sync(0xffffffffu, pages, from++);
-                if (pg < 0 || pg >= a.g.n_pages) return;           // (reported by the decode)
-                const int in = (c0 + c) & mask;
-                y.row0 = (c0 + c) * 16;
-                y.at = ((long long)pg * a.g.Hkv + kh) * a.g.page_rows + in * 16;
-                y.seen = y.row0 < hi_max && y.row0 + 16 > lo_min;
-                y.old = 0.f;
-                if (!(g & 1) && decay > 0.f) y.old = a.scores[y.at + my];
-                if (!y.seen) return;
-                const uint8_t* cell = a.g.pool + (long long)pg * a.g.page_bytes + (long long)(kh * (mask + 1) + in) * CELL;
-#pragma unroll
-                for (int bp = 0; bp < NB / 2; ++bp) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) y.k[bp][t] = __ldg(reinterpret_cast<const uint4*>(cell + bp * 1024 + t * 512 + lane * 16));
-                    if constexpr (!F8) y.d[bp] = __ldg(reinterpret_cast<const uint4*>(cell + 512 * NB + (j * NB + 2 * bp) * 8));
-                }
+                return v;
             };
-            auto take = [&](const Keys<NB, F8>& y) {
-                if (y.at < 0) return;
-                float gain[2][2] = {{0.f, 0.f}, {0.f, 0.f}};       // rows 2 j + i + 8 t, this lane's queries
-                if (y.seen) {
-                    const bool edge = y.row0 < lo_max || y.row0 + 16 > hi_min;
+            __syncwarp();
+            float old = old_of(st, ca + warp);
+            for (int c = ca + warp; c < cb; c += kWarps) {
+                const bool there = wait_bounded(bar0 + 8u * st, phase, &s_abort, a.g.err);
+                const int row0 = (c0 + c) * 16, page = s_page[warp][st];
+                const float next = old_of(st + 1 == STAGES ? 0 : st + 1, c + kWarps);
+                float gain[2] = {0.f, 0.f};                        // rows g and g + 8, this lane's queries
+                if (there && page >= 0 && row0 < hi_max && row0 + 16 > lo_min) {
+                    const uint8_t* cell = ring + st * KEYS;
+                    const bool edge = row0 < lo_max || row0 + 16 > hi_min;
 #pragma unroll 1
                     for (int s = 0; s < ns; ++s) {
-                        const uint8_t* tile = qs + (size_t)s * NB * 1024;
-                        float sc[2][2 * NQ], raw[2][4];
+                        const uint8_t* tile = qs + (size_t)s * TILE + lane * 8;
+                        float sc[4] = {0.f, 0.f, 0.f, 0.f};        // (g, 2 j), (g, 2 j + 1), (g + 8, 2 j), (g + 8, 2 j + 1)
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
+                        for (int bp = 0; bp < NB / 2; ++bp) {
+                            const uint4 k0 = *reinterpret_cast<const uint4*>(cell + bp * 1024 + lane * 16);
+                            const uint4 k1 = *reinterpret_cast<const uint4*>(cell + bp * 1024 + 512 + lane * 16);
+                            uint4 ks;                              // d of rows 2 (g / 2) + s and + 8, blocks 2 bp and 2 bp + 1
+                            if constexpr (!F8) ks = *reinterpret_cast<const uint4*>(cell + 512 * NB + ((g >> 1) * NB + 2 * bp) * 8);
 #pragma unroll
-                            for (int i = 0; i < 2 * NQ; ++i) sc[t][i] = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) raw[t][i] = 0.f;
-                        }
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            const int bp = b / 2, ee = b % 2;
-                            const uint4 a0 = *reinterpret_cast<const uint4*>(tile + (2 * b * 32 + lane) * 16);
-                            const uint4 a1 = *reinterpret_cast<const uint4*>(tile + ((2 * b + 1) * 32 + lane) * 16);
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                const uint32_t w0 = ee ? y.k[bp][t].z : y.k[bp][t].x, w1 = ee ? y.k[bp][t].w : y.k[bp][t].y;
+                            for (int ee = 0; ee < 2; ++ee) {
+                                const int b = 2 * bp + ee;
+                                const uint32_t x0 = ee ? k0.z : k0.x, y0 = ee ? k0.w : k0.y, x1_ = ee ? k1.z : k1.x, y1 = ee ? k1.w : k1.y;
+                                uint4 p, q;
                                 if constexpr (F8) {
-                                    mma_f16(raw[t], a0, f8_pair(w0), f8_pair(w0 >> 16));
-                                    mma_f16(raw[t], a1, f8_pair(w1), f8_pair(w1 >> 16));
+                                    p = make_uint4(f8_pair(x0), f8_pair(x1_), f8_pair(x0 >> 16), f8_pair(x1_ >> 16));
+                                    q = make_uint4(f8_pair(y0), f8_pair(y1), f8_pair(y0 >> 16), f8_pair(y1 >> 16));
                                 } else {
-                                    const float2 d = __half22float2(as_h2(ee ? (t ? y.d[bp].w : y.d[bp].z) : (t ? y.d[bp].y : y.d[bp].x)));
-                                    float c[4];
-                                    mma_f16_new(c, a0, k_pair(w0, 0x4140u, exps), k_pair(w0, 0x4342u, exps), zero);
-                                    mma_f16(c, a1, k_pair(w1, 0x4140u, exps), k_pair(w1, 0x4342u, exps));
+                                    p = make_uint4(k_pair(x0, 0x4140u, exps), k_pair(x1_, 0x4140u, exps), k_pair(x0, 0x4342u, exps), k_pair(x1_, 0x4342u, exps));
+                                    q = make_uint4(k_pair(y0, 0x4140u, exps), k_pair(y1, 0x4140u, exps), k_pair(y0, 0x4342u, exps), k_pair(y1, 0x4342u, exps));
+                                }
+                                const uint2 b0 = *reinterpret_cast<const uint2*>(tile + 2 * b * 256), b1 = *reinterpret_cast<const uint2*>(tile + (2 * b + 1) * 256);
+                                if constexpr (F8) {
+                                    mma_f16(sc, p, b0.x, b0.y);
+                                    mma_f16(sc, q, b1.x, b1.y);
                                     if constexpr (F32Q) {
-                                        c[0] += c[2];
-                                        c[1] += c[3];
+                                        const uint2 l0 = *reinterpret_cast<const uint2*>(tile + NB * 512 + 2 * b * 256), l1 = *reinterpret_cast<const uint2*>(tile + NB * 512 + (2 * b + 1) * 256);
+                                        mma_f16(sc, p, l0.x, l0.y);
+                                        mma_f16(sc, q, l1.x, l1.y);
                                     }
-                                    sc[t][0] = fmaf(c[0], d.x, sc[t][0]);
-                                    sc[t][1] = fmaf(c[1], d.y, sc[t][1]);
-                                    if constexpr (!F32Q) {
-                                        sc[t][2] = fmaf(c[2], d.x, sc[t][2]);
-                                        sc[t][3] = fmaf(c[3], d.y, sc[t][3]);
+                                } else {
+                                    float acc[4];
+                                    mma_f16_new(acc, p, b0.x, b0.y, zero);
+                                    mma_f16(acc, q, b1.x, b1.y);
+                                    if constexpr (F32Q) {
+                                        const uint2 l0 = *reinterpret_cast<const uint2*>(tile + NB * 512 + 2 * b * 256), l1 = *reinterpret_cast<const uint2*>(tile + NB * 512 + (2 * b + 1) * 256);
+                                        mma_f16(acc, p, l0.x, l0.y);
+                                        mma_f16(acc, q, l1.x, l1.y);
                                     }
+                                    const float2 d = __half22float2(as_h2(__byte_perm(ee ? ks.z : ks.x, ee ? ks.w : ks.y, pick)));
+                                    sc[0] = fmaf(acc[0], d.x, sc[0]);
+                                    sc[1] = fmaf(acc[1], d.x, sc[1]);
+                                    sc[2] = fmaf(acc[2], d.y, sc[2]);
+                                    sc[3] = fmaf(acc[3], d.y, sc[3]);
                                 }
                             }
                         }
-                        if constexpr (F8) {
+                        const Row* w = rows + s * kTile + 2 * j;
 #pragma unroll
-                            for (int t = 0; t < 2; ++t)
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 f = *reinterpret_cast<const float4*>(w + i);      // fac, m, w, lo
+                            float v[2] = {sc[i] * f.x, sc[2 + i] * f.x};
+                            if (a.softcap_b > 0.f)
 #pragma unroll
-                                for (int i = 0; i < 2 * NQ; ++i) sc[t][i] = F32Q ? raw[t][i] + raw[t][2 + i] : raw[t][i];
-                        }
+                                for (int r = 0; r < 2; ++r) v[r] = a.softcap_b * tanhf(a.softcap_a * v[r]);
 #pragma unroll
-                        for (int r = 0; r < NQ; ++r) {
-                            const Row w = rows[s * QPI + g + 8 * r];
-#pragma unroll
-                            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    float v = sc[t][2 * r + i] * w.fac;
-                                    if (a.softcap_b > 0.f) v = a.softcap_b * tanhf(a.softcap_a * v);
-                                    float p = ex2(v - w.m) * w.w;
-                                    const int at = y.row0 + 8 * t + 2 * j + i;
-                                    if (edge && (at < w.lo || at >= w.hi)) p = 0.f;
-                                    gain[t][i] += p;
+                            for (int r = 0; r < 2; ++r) {
+                                float p = ex2(v[r] - f.y) * f.z;
+                                if (edge) {
+                                    const int at = row0 + g + 8 * r;
+                                    if (at < w[i].lo || at >= w[i].hi) p = 0.f;
                                 }
+                                gain[r] += p;
+                            }
                         }
                     }
                 }
-                // ---- over the queries (g): each step halves the rows that a lane keeps
-                float v0 = g & 4 ? gain[1][0] : gain[0][0], v1 = g & 4 ? gain[1][1] : gain[0][1];
-                v0 += __shfl_xor_sync(0xffffffffu, g & 4 ? gain[0][0] : gain[1][0], 16);
-                v1 += __shfl_xor_sync(0xffffffffu, g & 4 ? gain[0][1] : gain[1][1], 16);
-                float v = g & 2 ? v1 : v0;
-                v += __shfl_xor_sync(0xffffffffu, g & 2 ? v0 : v1, 8);
-                v += __shfl_xor_sync(0xffffffffu, v, 4);
-                if (!(g & 1) && y.row0 + my < len) a.scores[y.at + my] = decay > 0.f ? fmaf(decay, y.old, v) : v;
-            };
-            if constexpr (NB == 8) {                               // (two cells' keys are more registers than there are)
-                Keys<NB, F8> y;
-                for (int c = ca + warp; c < cb; c += kWarps) {
-                    fetch(c, y);
-                    take(y);
-                }
-            } else {
-                Keys<NB, F8> y, z;
-                fetch(ca + warp, y);
-                for (int c = ca + warp; c < cb; c += 2 * kWarps) {
-                    fetch(c + kWarps, z);
-                    take(y);
-                    fetch(c + 2 * kWarps, y);
-                    take(z);
+                // ---- over the queries (j): the first step leaves each lane one of its two rows
+                float v = j & 1 ? gain[1] : gain[0];
+                v += __shfl_xor_sync(0xffffffffu, j & 1 ? gain[0] : gain[1], 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                if (j < 2 && page >= 0 && row0 + my < len && there) a.scores[score_of(page, c)] = decay > 0.f ? fmaf(decay, old, v) : v;
+                old = next;
+                __syncwarp();                                      // (the stage is read)
+                if (there) produce();
+                __syncwarp();
+                if (++st == STAGES) {
+                    st = 0;
+                    phase ^= 1u;
                 }
             }
         }
+    }
+    if (s_abort) {                                         // a wait ran out: let copies in flight land before the block ends
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1LL << 30)) __nanosleep(1000);
     }
 }
 
 template <int NB, bool F8, bool F32Q>
 cudaError_t launch_t(ScoredArgs a, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = kernel_attrs_once(scored_kernel<NB, F8, F32Q>, done, false);
+    cudaError_t e = kernel_attrs_once(scored_kernel<NB, F8, F32Q>, done, true);
     if (e != cudaSuccess) return e;
-    constexpr int QPI = F32Q ? 8 : 16;
-    // tiles: all queries of a KV head, or what 32 KB hold
-    a.slices = std::min((a.hpk * a.T + QPI - 1) / QPI, 32 / NB);
-    const size_t smem = (size_t)a.slices * NB * 1024 + (((size_t)a.slices * QPI * sizeof(Row) + 15) & ~(size_t)15) + (size_t)(a.n_seq + 1) * 8;
+    // tiles: all queries of a KV head, or what 16 KB hold
+    a.slices = std::min((a.hpk * a.T + kTile - 1) / kTile, 16 * 1024 / tile_bytes<NB, F32Q>());
+    const size_t smem = ring_at<NB, F8, F32Q>(a.slices, a.n_seq) + (size_t)kWarps * stages_of<NB>() * key_bytes<NB, F8>();
     return launch_dependent(scored_kernel<NB, F8, F32Q>, dim3((unsigned)(a.sms * blocks_of<NB>())), kThreads, smem, s, a);
 }
 
