@@ -34,6 +34,7 @@ namespace {
 constexpr int kPick = 512;             // threads of a block
 constexpr int kPickWarps = kPick / 32;
 constexpr int kBits = 11, kBins = 1 << kBits;
+constexpr uint32_t kForced = 0xffffffffu;      // key of a row that stays whatever its score (above infinity's)
 
 // a score as an unsigned integer of the same order; a NaN is the lowest, -0 is 0
 __device__ __forceinline__ uint32_t ordered(float s) {
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
     const int per = (((len + C - 1) / C) + 15) & ~15;
     const int s0 = min(len, rank * per), s1 = min(len, s0 + per), m = s1 - s0;
     const int* table = a.tables + (long long)seq * a.g.max_pages;
-    auto competes = [&](int r) { return r >= first && r < last; };
+    const int f0 = min(max(first - s0, 0), m), f1 = min(max(last - s0, f0), m);   // of this part: [f0, f1)
     auto place = [&](int r) -> const float* {                      // of row r's score
         const int pg = table[r >> a.g.page_shift];
         if (pg < 0 || pg >= a.g.n_pages) {
@@ -81,20 +82,30 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
     // ---- keys (four rows a load: they start at a multiple of 16)
     uint32_t lo = 0xffffffffu, hi = 0u;
     const int held = min(m, a.cap);
-#pragma unroll 4
-    for (int i = 4 * tid; i < m; i += 4 * kPick) {
-        const float* p = place(s0 + i);
+    auto four_of = [&](int i, const float* p, uint32_t (&k)[4]) {  // keys of rows s0 + i .. + 3 from their scores at p
         const float4 v = p ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
-        uint32_t k[4] = {ordered(v.x), ordered(v.y), ordered(v.z), ordered(v.w)};
+        k[0] = ordered(v.x); k[1] = ordered(v.y); k[2] = ordered(v.z); k[3] = ordered(v.w);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (!p) k[u] = 0u;
-            if (i + u < m && competes(s0 + i + u)) {
-                lo = min(lo, k[u]);
-                hi = max(hi, k[u]);
-            }
+        for (int u = 0; u < 4; ++u) k[u] = i + u >= f0 && i + u < f1 ? (p ? k[u] : 0u) : kForced;
+    };
+    for (int i0 = 4 * tid; i0 < m; i0 += 16 * kPick) {
+        const float* p[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) p[x] = i0 + 4 * x * kPick < m ? place(s0 + i0 + 4 * x * kPick) : nullptr;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int i = i0 + 4 * x * kPick;
+            if (i >= m) break;
+            uint32_t k[4];
+            four_of(i, p[x], k);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (k[u] != kForced) {
+                    lo = min(lo, k[u]);
+                    hi = max(hi, k[u]);
+                }
+            if (i < held) *reinterpret_cast<uint4*>(s_keys + i) = make_uint4(k[0], k[1], k[2], k[3]);   // (cap is a multiple of 4)
         }
-        if (i < held) *reinterpret_cast<uint4*>(s_keys + i) = make_uint4(k[0], k[1], k[2], k[3]);   // (cap is a multiple of 4)
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
@@ -130,9 +141,10 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
         reinterpret_cast<uint4*>(hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
         const uint32_t mask = bits >= 32 ? 0u : 0xffffffffu << bits, digit = (1u << (bits - shift)) - 1u;
-        for (int i = tid; i < m; i += kPick) {
+#pragma unroll 4
+        for (int i = f0 + tid; i < f1; i += kPick) {
             const uint32_t k = key_of(i) - lo;
-            if (competes(s0 + i) && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
         }
         cluster::sync();
         // thread t sums bins kBins - 4 t - 1 .. - 4 of all blocks; where the count from the top reaches `need`
@@ -169,24 +181,37 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
         need = s_need;
         bits = shift;
     }
-    const uint32_t thr = lo + prefix;
+    const uint32_t thr = any ? lo + prefix : kForced - 1u;         // (no score's key)
     // ---- rows above the threshold, and the first `need` at it, in index order: a
-    // stretch of the part for each warp
-    const int stretch = ((m + kPickWarps - 1) / kPickWarps + 31) & ~31, b0 = min(m, warp * stretch), b1 = min(m, b0 + stretch);
-    auto look = [&](int i, bool& up, bool& same) {
-        const bool in = i < b1, free = in && competes(s0 + i);
-        const uint32_t k = free && any ? key_of(i) : 0u;
-        up = in && (!free || (any && k > thr));
-        same = free && any && k == thr;
+    // stretch of the part for each warp, four neighbours a lane, the counts of 128 in the halves of a word
+    const int stretch = ((m + kPickWarps - 1) / kPickWarps + 127) & ~127, b0 = min(m, warp * stretch), b1 = min(m, b0 + stretch);
+    auto look = [&](int i, uint32_t& up, uint32_t& same) {         // masks of rows i .. i + 3
+        up = same = 0u;
+        if (i >= b1) return;
+        uint32_t k[4];
+        if (i < held) {
+            const uint4 v = *reinterpret_cast<const uint4*>(s_keys + i);
+            k[0] = v.x; k[1] = v.y; k[2] = v.z; k[3] = v.w;
+        } else {
+            four_of(i, place(s0 + i), k);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool in = i + u < b1;
+            up |= in && k[u] > thr ? 1u << u : 0u;
+            same |= in && k[u] == thr ? 1u << u : 0u;
+        }
     };
     uint32_t above = 0, at = 0;
-#pragma unroll 4
-    for (int i = b0; i < b1; i += 32) {
-        bool up, same;
-        look(i + lane, up, same);
-        above += __popc(__ballot_sync(0xffffffffu, up));
-        at += __popc(__ballot_sync(0xffffffffu, same));
+#pragma unroll 2
+    for (int i = b0 + 4 * lane; i < b1; i += 128) {
+        uint32_t up, same;
+        look(i, up, same);
+        above += __popc(up);
+        at += __popc(same);
     }
+    above = __reduce_add_sync(0xffffffffu, above);
+    at = __reduce_add_sync(0xffffffffu, at);
     if (lane == 0) {
         s_lo[warp] = above;
         s_hi[warp] = at;
@@ -207,16 +232,28 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
         pos += s_lo[w];
         eq += s_hi[w];
     }
-    const unsigned below = (1u << lane) - 1u;
-#pragma unroll 4
-    for (int i = b0; i < b1; i += 32) {
-        bool up, same;
-        look(i + lane, up, same);
-        const unsigned mu = __ballot_sync(0xffffffffu, up), ms = __ballot_sync(0xffffffffu, same);
-        const uint32_t e = eq + __popc(ms & below);                // rows at the threshold before this one
-        if (up || (same && e < need)) out[pos + __popc(mu & below) + min(e, need)] = s0 + i + lane;
-        pos += __popc(mu);
-        eq += __popc(ms);
+    for (int i0 = b0; i0 < b1; i0 += 128) {
+        uint32_t up, same;
+        look(i0 + 4 * lane, up, same);
+        const uint32_t mine = __popc(up) | __popc(same) << 16;
+        uint32_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, sum, 31), before = sum - mine;
+        uint32_t to = pos + (before & 0xffffu), e = eq + (before >> 16);      // rows above, and at it, before this lane's
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (up >> u & 1u) out[to++ + min(e, need)] = s0 + i0 + 4 * lane + u;
+            if (same >> u & 1u) {
+                if (e < need) out[to + e] = s0 + i0 + 4 * lane + u;
+                ++e;
+            }
+        }
+        pos += all & 0xffffu;
+        eq += all >> 16;
     }
 }
 
