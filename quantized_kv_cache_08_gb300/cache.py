@@ -496,40 +496,59 @@ def verify(target, draft, tokens, uniform, lens=None, accept=None, next_tokens=N
     Returns (accept, next_tokens), int32 [n] each, made if None: accept counts the rows of the step
     that stay, as KVCache.truncate_device takes them; lens (int32 [n], the
     lengths of a paged cache) is lowered by the others."""
-    code = _DTYPE.get(target.dtype)
+    dtype = target.dtype
+    code = _DTYPE.get(dtype)
     if code is None or target.dim() != 3 or not target.is_cuda:
         raise ValueError("target must be a float32 or bfloat16 [n, T, V] CUDA tensor")
     n, T, V = target.shape
-    dev, index = target.device, target.get_device()
+    index = target.get_device()
+    ts, tr, te = target.stride()
+    dp, ds, dr = None, 0, 0
+    if draft is not None:
+        if draft.dtype is not dtype or draft.shape != (n, T - 1, V) or draft.get_device() != index:
+            raise ValueError(f"draft must be {dtype} {[n, T - 1, V]} on target's device")
+        ds, dr, de = draft.stride()
+        if de != 1 and V > 1 and T > 1:
+            raise ValueError("draft needs each row's elements side by side")
+        dp = draft.data_ptr()
+    if te != 1 and V > 1:
+        raise ValueError("target needs each row's elements side by side")
+    if tokens.dtype is not _I32 or tokens.shape != (n, T - 1) or tokens.get_device() != index or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous int32 {[n, T - 1]} tensor on target's device")
+    if uniform.dtype is not torch.float32 or uniform.shape != (n, T) or uniform.get_device() != index \
+            or not uniform.is_contiguous():
+        raise ValueError(f"uniform must be a contiguous float32 {[n, T]} tensor on target's device")
 
-    def rows(t, shape, name):
-        if t.dtype is not target.dtype or t.shape != shape or t.get_device() != index or (t.numel() and V > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name} must be {target.dtype} {list(shape)} on {dev}, a row's elements side by side")
-        return t.data_ptr(), t.stride(0), t.stride(1)
-
-    def flat(t, shape, dtype, name):
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {dev}")
+    def counts(t, name):
+        if t.dtype is not _I32 or t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 {[n]} tensor on target's device")
         return t.data_ptr()
-
-    tp, ts, tr = rows(target, (n, T, V), "target")
-    dp, ds, dr = (None, 0, 0) if draft is None else rows(draft, (n, T - 1, V), "draft")
-    kp = flat(tokens, (n, T - 1), _I32, "tokens")
-    up = flat(uniform, (n, T), torch.float32, "uniform")
 
     def make():
         if stream is None:
-            return torch.empty(n, dtype=_I32, device=dev)
+            return torch.empty(n, dtype=_I32, device=target.device)
         with torch.cuda.stream(stream):
-            t = torch.empty(n, dtype=_I32, device=dev)
-        t.record_stream(torch.cuda.current_stream(dev))
+            t = torch.empty(n, dtype=_I32, device=target.device)
+        t.record_stream(torch.cuda.current_stream(target.device))
         return t
 
-    accept = make() if accept is None else accept
-    next_tokens = make() if next_tokens is None else next_tokens
-    a = B.kvq_verify_args(tp, dp, kp, up, code, n, T, V, ts, tr, ds, dr, flat(accept, (n,), _I32, "accept"),
-                          flat(next_tokens, (n,), _I32, "next_tokens"),
-                          None if lens is None else flat(lens, (n,), _I32, "lens"))
-    with torch.cuda.device(index):
-        B.kvq_verify(a, _raw_stream(index) if stream is None else stream.cuda_stream)
+    ap = counts(accept, "accept") if accept is not None else None
+    np_ = counts(next_tokens, "next_tokens") if next_tokens is not None else None
+    lp = counts(lens, "lens") if lens is not None else None
+    if accept is None:
+        accept = make()
+        ap = accept.data_ptr()
+    if next_tokens is None:
+        next_tokens = make()
+        np_ = next_tokens.data_ptr()
+    a = ctypes.byref(B.kvq_verify_args(target.data_ptr(), dp, tokens.data_ptr(), uniform.data_ptr(), code, n, T, V, ts, tr, ds,
+                                       dr, ap, np_, lp))
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
+        st = B.lib().kvq_verify(a, raw)
+    else:
+        with torch.cuda.device(index):
+            st = B.lib().kvq_verify(a, raw)
+    if st:
+        B._check(st)
     return accept, next_tokens

@@ -21,7 +21,9 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 namespace kvq {
 namespace {
@@ -54,27 +56,21 @@ __device__ __forceinline__ const void* row_at(const void* base, long long i) {
 
 // a probability in units of 2^-52, rounded down: 0 where it is not above 0 (NaN too), 1 where it is above 1
 __device__ __forceinline__ u64 units(float x) {
-    x = x > 0.f ? fminf(x, 1.f) : 0.f;
+    x = fminf(fmaxf(x, 0.f), 1.f);                       // (of a NaN and a number the number)
     const uint32_t b = __float_as_uint(x);
     const int e = (int)(b >> 23) - 98;                   // x = m 2^(e - 52); (subnormals end as 0)
     const uint32_t m = ((b & 0x7fffffu) | 0x800000u) >> min(max(-e, 0), 31);
     return (u64)m * (1u << max(e, 0));
 }
 
-struct Sum {
-    u64 w, p;
-};
-
-// What an element weighs.  tok: of a lone draft, which weighs nothing (-1: none)
+// What an element weighs: by p less q, or by p alone.  out: a lone draft's element, which weighs nothing
 template <bool Q>
-__device__ __forceinline__ void add(Sum& s, float p, float q, bool out) {
-    const u64 P = units(p);
-    s.p += P;
+__device__ __forceinline__ u64 weight(float p, float q, bool out) {
     if constexpr (Q) {
-        const u64 R = units(q);
-        s.w += P > R ? P - R : 0ull;
+        const long long w = (long long)(units(p) - units(q));
+        return (u64)(w & ~(w >> 63));
     } else {
-        s.w += out ? 0ull : P;
+        return out ? 0ull : units(p);
     }
 }
 
@@ -84,41 +80,56 @@ __device__ __forceinline__ u64 warp_sum(u64 x) {
     return x;
 }
 
-// The sums over [lo, hi) by one warp, every lane's share.  lo and hi are
-// multiples of 8 (or the row's end); vec: both rows start on 16 bytes
+// The weights of [lo, hi) by one warp, a lane's share.  lo and hi are multiples of
+// 32 (or the row's end); vec: both rows start on 16 bytes
 template <bool BF16, bool Q>
-__device__ __forceinline__ Sum sum_range(const void* p, const void* q, int lo, int hi, int tok, bool vec, int lane) {
-    constexpr int V = BF16 ? 8 : 4, U = 4;               // elements of a load, loads in flight
-    Sum s{0, 0};
+__device__ __forceinline__ u64 sum_range(const void* p, const void* q, int lo, int hi, int tok, bool vec, int lane) {
+    constexpr int V = BF16 ? 8 : 4, U = Q ? 4 : 8;       // elements of a load, loads of a row in flight
+    u64 s = 0;
     int i = lo;
-    if (vec) {
-        for (; i + U * V * 32 <= hi; i += U * V * 32) {
-            uint4 a[U], b[U];
+    auto step = [&](auto u) {
+        constexpr int N = decltype(u)::value;
+        uint4 a[N], b[N];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const long long at = i + (k * 32 + lane) * V;
-                a[k] = __ldg(reinterpret_cast<const uint4*>(row_at<BF16>(p, at)));
-                if constexpr (Q) b[k] = __ldg(reinterpret_cast<const uint4*>(row_at<BF16>(q, at)));
-                else b[k] = make_uint4(0u, 0u, 0u, 0u);
-            }
+        for (int k = 0; k < N; ++k) {
+            const long long at = i + (k * 32 + lane) * V;
+            a[k] = __ldg(reinterpret_cast<const uint4*>(row_at<BF16>(p, at)));
+            if constexpr (Q) b[k] = __ldg(reinterpret_cast<const uint4*>(row_at<BF16>(q, at)));
+            else b[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int at = i + (k * 32 + lane) * V;
-                const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, y[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+        for (int k = 0; k < N; ++k) {
+            const int at = i + (k * 32 + lane) * V;
+            const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, y[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    if constexpr (BF16) {
-                        add<Q>(s, __uint_as_float(x[w] << 16), __uint_as_float(y[w] << 16), at + 2 * w == tok);
-                        add<Q>(s, __uint_as_float(x[w] & 0xffff0000u), __uint_as_float(y[w] & 0xffff0000u), at + 2 * w + 1 == tok);
-                    } else {
-                        add<Q>(s, __uint_as_float(x[w]), __uint_as_float(y[w]), at + w == tok);
-                    }
+            for (int w = 0; w < 4; ++w) {
+                if constexpr (BF16) {
+                    s += weight<Q>(__uint_as_float(x[w] << 16), __uint_as_float(y[w] << 16), at + 2 * w == tok);
+                    s += weight<Q>(__uint_as_float(x[w] & 0xffff0000u), __uint_as_float(y[w] & 0xffff0000u), at + 2 * w + 1 == tok);
+                } else {
+                    s += weight<Q>(__uint_as_float(x[w]), __uint_as_float(y[w]), at + w == tok);
                 }
             }
         }
+        i += N * V * 32;
+    };
+    if (vec) {
+        while (i + U * V * 32 <= hi) step(std::integral_constant<int, U>{});
+        while (i + V * 32 <= hi) step(std::integral_constant<int, 1>{});
     }
-#pragma unroll 8
-    for (int at = i + lane; at < hi; at += 32) add<Q>(s, element<BF16>(p, at), Q ? element<BF16>(q, at) : 0.f, at == tok);
+    // element by element: rows that start anywhere, and what is left of a row
+    constexpr int W = 8;
+    for (; i < hi; i += W * 32) {
+        float x[W], y[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const int at = i + k * 32 + lane;
+            x[k] = at < hi ? element<BF16>(p, at) : 0.f;
+            y[k] = Q && at < hi ? element<BF16>(q, at) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < W; ++k) s += weight<Q>(x[k], y[k], i + k * 32 + lane == tok);
+    }
     return s;
 }
 
@@ -126,8 +137,8 @@ __device__ __forceinline__ Sum sum_range(const void* p, const void* q, int lo, i
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ Args a) {
     __shared__ int s_row, s_held, s_tok;
-    __shared__ u64 s_w[kWarps], s_p[kWarps];
-    __shared__ u64 s_all[cluster::kMaxCluster][2];       // the blocks' sums, written by themselves
+    __shared__ u64 s_sum[kWarps];
+    __shared__ u64 s_all[2][cluster::kMaxCluster];       // the blocks' sums, written by themselves
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = cluster::size(), rank = cluster::rank();
     const long long b = blockIdx.x / C;
@@ -171,43 +182,39 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     }
     __syncthreads();
     const int row = s_row;
-    const bool with_q = s_held && a.draft;
-    const int tok = s_held && !a.draft ? s_tok : -1;
+    bool with_q = s_held && a.draft;
+    int tok = s_held && !a.draft ? s_tok : -1;
     const void* p = row_at<BF16>(a.target, b * a.target_seq + row * a.target_row);
     const void* q = with_q ? row_at<BF16>(a.draft, b * a.draft_seq + row * a.draft_row) : p;
     const bool vec = (((uintptr_t)p | (uintptr_t)q) & 15) == 0;
-    // ---- sums of this block's part
+    // ---- sums of this block's part; where nothing is left of p over q, of p itself
     auto part = [](int n, int parts) { return ((n + parts - 1) / parts + 31) & ~31; };
     int lo = min(a.vocab, rank * part(a.vocab, C)), hi = min(a.vocab, lo + part(a.vocab, C));
     int per = part(hi - lo, kWarps);
     auto sums = [&](int from, int to) {
         const int x = min(to, from + warp * per), y = min(to, x + per);
-        Sum s = with_q ? sum_range<BF16, true>(p, q, x, y, -1, vec, lane) : sum_range<BF16, false>(p, q, x, y, tok, vec, lane);
-        s.w = warp_sum(s.w);
-        s.p = warp_sum(s.p);
-        if (lane == 0) {
-            s_w[warp] = s.w;
-            s_p[warp] = s.p;
-        }
+        const u64 s = warp_sum(with_q ? sum_range<BF16, true>(p, q, x, y, -1, vec, lane) : sum_range<BF16, false>(p, q, x, y, tok, vec, lane));
+        if (lane == 0) s_sum[warp] = s;
         __syncthreads();
     };
-    sums(lo, hi);
-    if (tid < 2 * C) {
-        u64 t = 0;
-        const u64* from = tid & 1 ? s_p : s_w;
-        for (int w = 0; w < kWarps; ++w) t += from[w];
-        cluster::store(cluster::map(&s_all[rank][tid & 1], tid >> 1), t);
-    }
-    cluster::sync();
-    u64 before[2] = {0, 0}, all[2] = {0, 0};
-    for (int r = 0; r < C; ++r)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (r < rank) before[k] += s_all[r][k];
-            all[k] += s_all[r][k];
+    u64 S = 0, first = 0, mine = 0;
+    for (int mode = 0; mode < 2; ++mode) {
+        sums(lo, hi);
+        if (tid < C) {
+            u64 t = 0;
+            for (int w = 0; w < kWarps; ++w) t += s_sum[w];
+            cluster::store(cluster::map(&s_all[mode][rank], tid), t);
         }
-    const bool by_p = all[0] == 0;                       // nothing is left of p over q: p itself
-    const u64 S = all[by_p], first = before[by_p], mine = s_all[rank][by_p];
+        cluster::sync();
+        for (int r = 0; r < C; ++r) {
+            if (r == rank) first = S;
+            S += s_all[mode][r];
+        }
+        mine = s_all[mode][rank];
+        if (S != 0) break;                               // (the same in all blocks of the cluster)
+        with_q = false;
+        tok = -1;
+    }
     if (S == 0) return;
     const float u = a.uniform[b * a.T + a.T - 1];
     const uint32_t U = u > 0.f ? (uint32_t)fminf(u * 2147483648.f, 2147483520.f) : 0u;   // (the f32 below 2^31)
@@ -216,9 +223,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     x -= first;
     // ---- down into the stretch where the running sum passes x
     for (;;) {
-        const u64* s = by_p ? s_p : s_w;
         int w = 0;
-        while (w < kWarps - 1 && x >= s[w]) x -= s[w++];
+        while (w < kWarps - 1 && x >= s_sum[w]) x -= s_sum[w++];
         lo = min(hi, lo + w * per);
         hi = min(hi, lo + per);
         __syncthreads();                                 // (before the sums are written again)
@@ -229,13 +235,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     if (warp == 0) {
         const int i = lo + lane;
         u64 v = 0;
-        if (i < hi) {
-            Sum s{0, 0};
-            const float pi = element<BF16>(p, i);
-            if (with_q) add<true>(s, pi, element<BF16>(q, i), false);
-            else add<false>(s, pi, 0.f, i == tok);
-            v = by_p ? s.p : s.w;
-        }
+        if (i < hi) v = with_q ? weight<true>(element<BF16>(p, i), element<BF16>(q, i), false) : weight<false>(element<BF16>(p, i), 0.f, i == tok);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const u64 y = __shfl_up_sync(0xffffffffu, v, o);
@@ -265,10 +265,16 @@ extern "C" kvq_status kvq_verify(const kvq_verify_args* v, void* stream) {
         return fail(KVQ_EINVAL, "a pointer is not aligned to its elements");
     if (v->target_seq < 0 || v->target_row < 0 || v->draft_seq < 0 || v->draft_row < 0)
         return fail(KVQ_EINVAL, "strides must be >= 0");
-    int dev = 0, sms = 0;
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    static std::atomic<int> known[64];                   // SMs of each device, asked for once
+    int sms = known[dev & 63].load(std::memory_order_relaxed);
+    if (sms == 0) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+        known[dev & 63].store(sms, std::memory_order_relaxed);
+    }
     Args a{v->target, v->draft, v->tokens, v->uniform, v->target_seq, v->target_row, v->draft_seq, v->draft_row,
            v->T, v->vocab, v->accept, v->next, v->lens};
     // blocks of a row: more while SMs are idle and a part keeps some 2000 elements
