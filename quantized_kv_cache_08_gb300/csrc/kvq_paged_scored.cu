@@ -13,7 +13,8 @@
 // are M here (16 of them, both halves of a cell in one product) and 8 queries N, the
 // other way round than in the decode, for nothing follows that wants the weights
 // in another order: half as many products, and a lane's sums are of two rows only.
-// Each warp keeps its own ring of bulk copies of keys.  Blocks are small, several an SM, and
+// Each warp keeps its own ring of bulk copies of keys, two cells a stage, which share
+// the queries' fragments and what goes round a stage.  Blocks are small, several an SM, and
 // take equal ranges of the cells of all (sequence, KV head) pairs: while one
 // changes its queries the others multiply.  Queries stay in shared memory in tiles of 8
 // (f32 ones as two fp16 parts), and what does not fit is another pass over
@@ -32,10 +33,11 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 8;               // queries
+constexpr int kPair = 2;               // cells of a stage
 template <int NB>
 constexpr int blocks_of() { return NB == 8 ? 4 : 5; }
 template <int NB>
-constexpr int stages_of() { return NB == 8 ? 2 : 4; }
+constexpr int stages_of() { return 2; }
 template <int NB, bool F8>
 constexpr int key_bytes() { return NB * (F8 ? 512 : 544); }
 template <int NB, bool F32Q>
@@ -59,16 +61,16 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_wsum[kWarps];
     __shared__ int s_ext[4], s_abort;
-    __shared__ int s_page[kWarps][STAGES];         // of the cell in a stage, -1: none
+    __shared__ long long s_at[kWarps][STAGES][kPair];      // where the scores of a stage's cells lie, -1: no cell
     __shared__ __align__(8) uint64_t s_bar[kWarps][STAGES];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int QB = a.slices * kTile;
     uint8_t* qs = smem;
     Row* rows = reinterpret_cast<Row*>(smem + (size_t)a.slices * TILE);
     long long* plan = reinterpret_cast<long long*>(rows + QB);
-    uint8_t* ring = smem + ring_at<NB, F8, F32Q>(a.slices, a.n_seq) + (size_t)warp * STAGES * KEYS;
+    uint8_t* ring = smem + ring_at<NB, F8, F32Q>(a.slices, a.n_seq) + (size_t)warp * STAGES * kPair * KEYS;
     const uint32_t ring_u = dev::smem_u32(ring), bar0 = dev::smem_u32(&s_bar[warp][0]);
-    if (lane < STAGES) dev::mbar_init(bar0 + 8u * lane, 1);
+    if (lane < STAGES) dev::mbar_init(bar0 + 8u * lane, kPair);
     if (tid == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     wait_for_earlier();
@@ -106,8 +108,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
         if (tid == kThreads - 1) plan[a.n_seq] = base + w;
         __syncthreads();
     }
-    // ---- this block's range: a cell for each of its warps at least
-    const long long U = plan[a.n_seq] * a.g.Hkv, G = min((long long)gridDim.x, (U + kWarps - 1) / kWarps);
+    // ---- this block's range: a stage for each of its warps at least
+    const long long U = plan[a.n_seq] * a.g.Hkv, G = min((long long)gridDim.x, (U + kPair * kWarps - 1) / (kPair * kWarps));
     if (blockIdx.x >= G) return;
     long long x = U * blockIdx.x / G;
     const long long x1 = U * (blockIdx.x + 1) / G;
@@ -116,7 +118,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
     for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
     const uint32_t exps = held(0x64646464u), pick = g & 1 ? 0x7632u : 0x5410u;
     const int cps = a.g.page_shift - 4, mask = (1 << cps) - 1;
-    const int my = g + 8 * (j & 1);                        // the row of a cell whose score is this lane's (j < 2)
+    const int my = g + 8 * (j & 1);                        // the row of cell j / 2 of a stage whose score is this lane's
+    const uint64_t policy = dev::evict_first_policy();
     int st = 0;
     uint32_t phase = 0;
     while (x < x1) {
@@ -141,29 +144,40 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
         for (int q0 = 0; q0 < nq; q0 += QB) {
             const int n = min(QB, nq - q0), ns = (n + kTile - 1) / kTile;
             const float decay = q0 == 0 ? a.decay : 1.f;
-            // ---- the producer side: the warp's cells in order, a lane holding one of the next 32 pages
-            int pages = 0, from = 32, pc = ca + warp, ps = st;
+            // ---- the producer side: the warp's cells in order, a lane holding one of the next 32
+            int from = 32, pc = ca + kPair * warp, ps = st;
+            long long at = -1;                                     // of the lane's cell: its scores, and its keys (NULL: not read)
+            const uint8_t* keys = nullptr;
             auto produce = [&]() {
                 if (pc >= cb) return;
                 if (from == 32) {
                     from = 0;
-                    const int c = pc + lane * kWarps;
-                    pages = c < cb ? table[(c0 + c) >> cps] : 0;
+                    const int c = pc + (lane & 1) + (lane >> 1) * (kPair * kWarps);
+                    at = -1;
+                    keys = nullptr;
+                    if (c < cb) {
+                        const int cell = c0 + c, in = cell & mask, page = table[cell >> cps];
+                        if (page >= 0 && page < a.g.n_pages) {     // (reported by the decode)
+                            at = ((long long)page * a.g.Hkv + kh) * a.g.page_rows + in * 16;
+                            if (cell * 16 + 16 > lo_row) keys = a.g.pool + (long long)page * a.g.page_bytes + (long long)(kh * (mask + 1) + in) * CELL;
+                        }
+                    }
                 }
-                if (lane == from) {
-                    const int at = c0 + pc, in = at & mask;
-                    const bool there = pages >= 0 && pages < a.g.n_pages;              // (reported by the decode)
+                if ((unsigned)(lane - from) < kPair) {
                     const uint32_t bar = bar0 + 8u * ps;
-                    s_page[warp][ps] = there ? pages : -1;
-                    if (there && at * 16 + 16 > lo_row) {
+                    s_at[warp][ps][lane - from] = at;
+                    if (keys) {
                         dev::mbar_expect_tx(bar, KEYS);
-                        dev::bulk_g2s(ring_u + (uint32_t)(ps * KEYS), a.g.pool + (long long)pages * a.g.page_bytes + (long long)(kh * (mask + 1) + in) * CELL, KEYS, bar);
+                        asm volatile(
+                            "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                            ::"r"(ring_u + (uint32_t)((ps * kPair + lane - from) * KEYS)), "l"(keys), "r"(KEYS), "r"(bar), "l"(policy)
+                            : "memory");
                     } else {
                         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
                     }
                 }
-                ++from;
-                pc += kWarps;
+                from += kPair;
+                pc += kPair * kWarps;
                 if (++ps == STAGES) ps = 0;
             };
 #pragma unroll 1
@@ -217,71 +231,78 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
             }
             __syncthreads();
             const int lo_max = s_ext[0], hi_min = s_ext[1], lo_min = s_ext[2], hi_max = s_ext[3];
-            // ---- its cells, warp by warp; the next one's score is on its way
-            auto score_of = [&](int page, int c) { return ((long long)page * a.g.Hkv + kh) * a.g.page_rows + ((c0 + c) & mask) * 16 + my; };
+            // ---- its cells, warp by warp; the next stage's scores are on their way
             auto old_of = [&](int stage, int c) {
                 float v = 0.f;
-                if (c < cb && j < 2 && decay > 0.f) {
-                    const int page = s_page[warp][stage];
-                    if (page >= 0) v = a.scores[score_of(page, c)];
+                if (c < cb && decay > 0.f) {
+                    const long long to = s_at[warp][stage][j >> 1];
+                    if (to >= 0) v = a.scores[to + my];
                 }
                 return v;
             };
             __syncwarp();
-            float old = old_of(st, ca + warp);
-            for (int c = ca + warp; c < cb; c += kWarps) {
+            float old = old_of(st, ca + kPair * warp);
+            for (int c = ca + kPair * warp; c < cb; c += kPair * kWarps) {
                 const bool there = wait_bounded(bar0 + 8u * st, phase, &s_abort, a.g.err);
-                const int row0 = (c0 + c) * 16, page = s_page[warp][st];
-                const float next = old_of(st + 1 == STAGES ? 0 : st + 1, c + kWarps);
-                float gain[2] = {0.f, 0.f};                        // rows g and g + 8, this lane's queries
-                if (there && page >= 0 && row0 < hi_max && row0 + 16 > lo_min) {
-                    const uint8_t* cell = ring + st * KEYS;
-                    const bool edge = row0 < lo_max || row0 + 16 > hi_min;
+                const int row0 = (c0 + c) * 16;
+                const long long to = s_at[warp][st][j >> 1];
+                const float next = old_of(st + 1 == STAGES ? 0 : st + 1, c + kPair * kWarps);
+                float gain[kPair][2] = {{0.f, 0.f}, {0.f, 0.f}};   // rows g and g + 8 of the cells, this lane's queries
+                if (there && row0 < hi_max && row0 + 16 * kPair > lo_min) {
+                    // (what the ring holds of a cell that was not read reaches no other's sums: its
+                    // rows are masked, or their scores not stored)
+                    const uint8_t* cell = ring + st * kPair * KEYS;
+                    const bool edge = row0 < lo_max || row0 + 16 * kPair > hi_min;
 #pragma unroll 1
                     for (int s = 0; s < ns; ++s) {
                         const uint8_t* tile = qs + (size_t)s * TILE + lane * 8;
-                        float sc[4] = {0.f, 0.f, 0.f, 0.f};        // (g, 2 j), (g, 2 j + 1), (g + 8, 2 j), (g + 8, 2 j + 1)
-#pragma unroll
+                        float sc[kPair][4] = {};                   // (g, 2 j), (g, 2 j + 1), (g + 8, 2 j), (g + 8, 2 j + 1)
+#pragma unroll 1                                           // (unrolled, its loads take more registers than there are)
                         for (int bp = 0; bp < NB / 2; ++bp) {
-                            const uint4 k0 = *reinterpret_cast<const uint4*>(cell + bp * 1024 + lane * 16);
-                            const uint4 k1 = *reinterpret_cast<const uint4*>(cell + bp * 1024 + 512 + lane * 16);
-                            uint4 ks;                              // d of rows 2 (g / 2) + s and + 8, blocks 2 bp and 2 bp + 1
-                            if constexpr (!F8) ks = *reinterpret_cast<const uint4*>(cell + 512 * NB + ((g >> 1) * NB + 2 * bp) * 8);
+                            uint4 k0[kPair], k1[kPair], ks[kPair]; // ks: d of rows 2 (g / 2) + s and + 8, blocks 2 bp and 2 bp + 1
+#pragma unroll
+                            for (int x = 0; x < kPair; ++x) {
+                                k0[x] = *reinterpret_cast<const uint4*>(cell + x * KEYS + bp * 1024 + lane * 16);
+                                k1[x] = *reinterpret_cast<const uint4*>(cell + x * KEYS + bp * 1024 + 512 + lane * 16);
+                                if constexpr (!F8) ks[x] = *reinterpret_cast<const uint4*>(cell + x * KEYS + 512 * NB + ((g >> 1) * NB + 2 * bp) * 8);
+                            }
 #pragma unroll
                             for (int ee = 0; ee < 2; ++ee) {
                                 const int b = 2 * bp + ee;
-                                const uint32_t x0 = ee ? k0.z : k0.x, y0 = ee ? k0.w : k0.y, x1_ = ee ? k1.z : k1.x, y1 = ee ? k1.w : k1.y;
-                                uint4 p, q;
-                                if constexpr (F8) {
-                                    p = make_uint4(f8_pair(x0), f8_pair(x1_), f8_pair(x0 >> 16), f8_pair(x1_ >> 16));
-                                    q = make_uint4(f8_pair(y0), f8_pair(y1), f8_pair(y0 >> 16), f8_pair(y1 >> 16));
-                                } else {
-                                    p = make_uint4(k_pair(x0, 0x4140u, exps), k_pair(x1_, 0x4140u, exps), k_pair(x0, 0x4342u, exps), k_pair(x1_, 0x4342u, exps));
-                                    q = make_uint4(k_pair(y0, 0x4140u, exps), k_pair(y1, 0x4140u, exps), k_pair(y0, 0x4342u, exps), k_pair(y1, 0x4342u, exps));
-                                }
                                 const uint2 b0 = *reinterpret_cast<const uint2*>(tile + 2 * b * 256), b1 = *reinterpret_cast<const uint2*>(tile + (2 * b + 1) * 256);
-                                if constexpr (F8) {
-                                    mma_f16(sc, p, b0.x, b0.y);
-                                    mma_f16(sc, q, b1.x, b1.y);
-                                    if constexpr (F32Q) {
-                                        const uint2 l0 = *reinterpret_cast<const uint2*>(tile + NB * 512 + 2 * b * 256), l1 = *reinterpret_cast<const uint2*>(tile + NB * 512 + (2 * b + 1) * 256);
-                                        mma_f16(sc, p, l0.x, l0.y);
-                                        mma_f16(sc, q, l1.x, l1.y);
+                                uint2 l0 = b0, l1 = b1;
+                                if constexpr (F32Q) {
+                                    l0 = *reinterpret_cast<const uint2*>(tile + NB * 512 + 2 * b * 256);
+                                    l1 = *reinterpret_cast<const uint2*>(tile + NB * 512 + (2 * b + 1) * 256);
+                                }
+#pragma unroll
+                                for (int x = 0; x < kPair; ++x) {
+                                    const uint32_t v0 = ee ? k0[x].z : k0[x].x, w0 = ee ? k0[x].w : k0[x].y, v1 = ee ? k1[x].z : k1[x].x, w1 = ee ? k1[x].w : k1[x].y;
+                                    if constexpr (F8) {
+                                        const uint4 p = make_uint4(f8_pair(v0), f8_pair(v1), f8_pair(v0 >> 16), f8_pair(v1 >> 16));
+                                        const uint4 q = make_uint4(f8_pair(w0), f8_pair(w1), f8_pair(w0 >> 16), f8_pair(w1 >> 16));
+                                        mma_f16(sc[x], p, b0.x, b0.y);
+                                        mma_f16(sc[x], q, b1.x, b1.y);
+                                        if constexpr (F32Q) {
+                                            mma_f16(sc[x], p, l0.x, l0.y);
+                                            mma_f16(sc[x], q, l1.x, l1.y);
+                                        }
+                                    } else {
+                                        const uint4 p = make_uint4(k_pair(v0, 0x4140u, exps), k_pair(v1, 0x4140u, exps), k_pair(v0, 0x4342u, exps), k_pair(v1, 0x4342u, exps));
+                                        const uint4 q = make_uint4(k_pair(w0, 0x4140u, exps), k_pair(w1, 0x4140u, exps), k_pair(w0, 0x4342u, exps), k_pair(w1, 0x4342u, exps));
+                                        float acc[4];
+                                        mma_f16_new(acc, p, b0.x, b0.y, zero);
+                                        mma_f16(acc, q, b1.x, b1.y);
+                                        if constexpr (F32Q) {
+                                            mma_f16(acc, p, l0.x, l0.y);
+                                            mma_f16(acc, q, l1.x, l1.y);
+                                        }
+                                        const float2 d = __half22float2(as_h2(__byte_perm(ee ? ks[x].z : ks[x].x, ee ? ks[x].w : ks[x].y, pick)));
+                                        sc[x][0] = fmaf(acc[0], d.x, sc[x][0]);
+                                        sc[x][1] = fmaf(acc[1], d.x, sc[x][1]);
+                                        sc[x][2] = fmaf(acc[2], d.y, sc[x][2]);
+                                        sc[x][3] = fmaf(acc[3], d.y, sc[x][3]);
                                     }
-                                } else {
-                                    float acc[4];
-                                    mma_f16_new(acc, p, b0.x, b0.y, zero);
-                                    mma_f16(acc, q, b1.x, b1.y);
-                                    if constexpr (F32Q) {
-                                        const uint2 l0 = *reinterpret_cast<const uint2*>(tile + NB * 512 + 2 * b * 256), l1 = *reinterpret_cast<const uint2*>(tile + NB * 512 + (2 * b + 1) * 256);
-                                        mma_f16(acc, p, l0.x, l0.y);
-                                        mma_f16(acc, q, l1.x, l1.y);
-                                    }
-                                    const float2 d = __half22float2(as_h2(__byte_perm(ee ? ks.z : ks.x, ee ? ks.w : ks.y, pick)));
-                                    sc[0] = fmaf(acc[0], d.x, sc[0]);
-                                    sc[1] = fmaf(acc[1], d.x, sc[1]);
-                                    sc[2] = fmaf(acc[2], d.y, sc[2]);
-                                    sc[3] = fmaf(acc[3], d.y, sc[3]);
                                 }
                             }
                         }
@@ -289,27 +310,30 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float4 f = *reinterpret_cast<const float4*>(w + i);      // fac, m, w, lo
-                            float v[2] = {sc[i] * f.x, sc[2 + i] * f.x};
-                            if (a.softcap_b > 0.f)
 #pragma unroll
-                                for (int r = 0; r < 2; ++r) v[r] = a.softcap_b * tanhf(a.softcap_a * v[r]);
+                            for (int x = 0; x < kPair; ++x)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                float p = ex2(v[r] - f.y) * f.z;
-                                if (edge) {
-                                    const int at = row0 + g + 8 * r;
-                                    if (at < w[i].lo || at >= w[i].hi) p = 0.f;
+                                for (int r = 0; r < 2; ++r) {
+                                    float v = sc[x][2 * r + i] * f.x;
+                                    if (a.softcap_b > 0.f) v = a.softcap_b * tanhf(a.softcap_a * v);
+                                    float p = ex2(v - f.y) * f.z;
+                                    if (edge) {
+                                        const int at_row = row0 + 16 * x + g + 8 * r;
+                                        if (at_row < w[i].lo || at_row >= w[i].hi) p = 0.f;
+                                    }
+                                    gain[x][r] += p;
                                 }
-                                gain[r] += p;
-                            }
                         }
                     }
                 }
-                // ---- over the queries (j): the first step leaves each lane one of its two rows
-                float v = j & 1 ? gain[1] : gain[0];
-                v += __shfl_xor_sync(0xffffffffu, j & 1 ? gain[0] : gain[1], 1);
-                v += __shfl_xor_sync(0xffffffffu, v, 2);
-                if (j < 2 && page >= 0 && row0 + my < len && there) a.scores[score_of(page, c)] = decay > 0.f ? fmaf(decay, old, v) : v;
+                // ---- over the queries (j): the first step leaves each lane one of the cells, the second one of its two rows
+                const bool up = j & 2, odd = j & 1;
+                float v0 = up ? gain[1][0] : gain[0][0], v1 = up ? gain[1][1] : gain[0][1];
+                v0 += __shfl_xor_sync(0xffffffffu, up ? gain[0][0] : gain[1][0], 2);
+                v1 += __shfl_xor_sync(0xffffffffu, up ? gain[0][1] : gain[1][1], 2);
+                float v = odd ? v1 : v0;
+                v += __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                if (to >= 0 && row0 + 16 * (j >> 1) + my < len && there) a.scores[to + my] = decay > 0.f ? fmaf(decay, old, v) : v;
                 old = next;
                 __syncwarp();                                      // (the stage is read)
                 if (there) produce();
@@ -334,7 +358,7 @@ cudaError_t launch_t(ScoredArgs a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // tiles: all queries of a KV head, or what 16 KB hold
     a.slices = std::min((a.hpk * a.T + kTile - 1) / kTile, 16 * 1024 / tile_bytes<NB, F32Q>());
-    const size_t smem = ring_at<NB, F8, F32Q>(a.slices, a.n_seq) + (size_t)kWarps * stages_of<NB>() * key_bytes<NB, F8>();
+    const size_t smem = ring_at<NB, F8, F32Q>(a.slices, a.n_seq) + (size_t)kWarps * stages_of<NB>() * kPair * key_bytes<NB, F8>();
     return launch_dependent(scored_kernel<NB, F8, F32Q>, dim3((unsigned)(a.sms * blocks_of<NB>())), kThreads, smem, s, a);
 }
 
