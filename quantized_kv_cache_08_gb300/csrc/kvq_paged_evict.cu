@@ -148,10 +148,15 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
         }
         cluster::sync();
         // thread t sums bins kBins - 4 t - 1 .. - 4 of all blocks; where the count from the top reaches `need`
-        uint4 c = make_uint4(0u, 0u, 0u, 0u);
-        for (int r = 0; r < C; ++r) {
-            const uint4 v = cluster::load4(cluster::map(&hist[kBins - 4 * tid - 4], r));
-            c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+        uint4 all[cluster::kMaxCluster], c = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int r = 0; r < cluster::kMaxCluster; ++r) {           // (all on their way at once)
+            all[r] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < C) all[r] = cluster::load4(cluster::map(&hist[kBins - 4 * tid - 4], r));
+        }
+#pragma unroll
+        for (int r = 0; r < cluster::kMaxCluster; ++r) {
+            c.x += all[r].x; c.y += all[r].y; c.z += all[r].z; c.w += all[r].w;
         }
         const uint32_t sum = c.x + c.y + c.z + c.w;
         uint32_t x = sum;
@@ -380,9 +385,8 @@ struct Piece {
     }
 };
 
-// (sequence, KV head) blockIdx.x / a.blocks; cell window w of it is blocks x warps
-// cells.  In place the blocks are a cluster and take window after window; into other
-// pages there is one window.
+// (sequence, KV head) blockIdx.x / a.blocks, whose blocks take window after window of
+// blocks x warps cells; in place they are a cluster.
 template <int NB, bool F8>
 __global__ void __launch_bounds__(kMove) compact_kernel(const __grid_constant__ CompactArgs a) {
     constexpr int CELL = NB * (F8 ? 1024 : 928);
@@ -400,45 +404,59 @@ __global__ void __launch_bounds__(kMove) compact_kernel(const __grid_constant__ 
     const int* from = a.tables + (long long)seq * a.g.max_pages;
     const int* to = a.tables_out + (long long)seq * a.g.max_pages;
     const int cps = a.g.page_shift - 4, mask = (1 << cps) - 1;
-    // (page, row in it) of row r in table t; -1 and the error word set if the page is none
-    auto page_of = [&](const int* t, int r) {
-        const int pg = t[r >> a.g.page_shift];
-        if (pg >= 0 && pg < a.g.n_pages) return pg;
+    auto good = [&](int page) {
+        if (page >= 0 && page < a.g.n_pages) return true;
         atomicExch(a.g.err, kErrCounter);
-        return -1;
+        return false;
     };
-    for (int c0 = part * kMoveWarps; c0 - part * kMoveWarps < cells; c0 += a.blocks * kMoveWarps) {
-        const int c = c0 + warp;
+    // What a cell's turn needs is asked for ahead: two turns the list's entries (lane l
+    // entry l - 1 of the cell's, lane 0 the one before them), one turn the pages
+    const int step = a.blocks * kMoveWarps, first = part * kMoveWarps;
+    auto entry = [&](int c) {
+        const int i = 16 * c + lane - 1;
+        return c < cells && lane <= 16 && i >= 0 && i < n ? list[i] : -1;
+    };
+    struct Pages {
+        int r, prev, src, dst;                                     // of lane < 16: its row, the one before it in the list, pages
+    };
+    auto pages_of = [&](int c, int e) {
+        Pages p{-1, e, -1, -1};
+        p.r = __shfl_down_sync(0xffffffffu, e, 1);
+        if (c < cells) {
+            p.dst = to[(16 * c) >> a.g.page_shift];
+            if (lane < 16 && p.r >= 0 && p.r < len) p.src = from[p.r >> a.g.page_shift];
+        }
+        return p;
+    };
+    int c = first + warp;
+    Pages now = pages_of(c, entry(c));
+    int ahead = entry(c + step);
+    for (int c0 = first; c0 - first < cells; c0 += step, c += step) {
+        const Pages next = pages_of(c + step, ahead);
+        ahead = entry(c + 2 * step);
         uint8_t* dst = nullptr;
-        long long row_at = 0, score_at = 0;                        // lane t < 16: byte of its row's cell; its score
+        long long row_at = 0, score_from = 0, score_to = 0;        // lane t < 16: byte of its row's cell; scores
         int t = lane & 15;
         bool moved = false;
         Piece<NB, F8> p;
-        if (c < cells) {
-            const int pg = page_of(to, 16 * c);
-            if (pg >= 0) {
-                const long long cell = (long long)pg * a.g.page_bytes + (long long)(h * (mask + 1) + (c & mask)) * CELL;
-                const long long sc = ((long long)pg * a.g.Hkv + h) * a.g.page_rows + (c & mask) * 16 + (lane & 15);
-                row_at = cell;                                     // (a row that is not moved stays as it is)
-                score_at = sc;
-                const int i = 16 * c + lane;
-                if (lane < 16 && i < n) {
-                    const int r = list[i], prev = i > 0 ? list[i - 1] : -1;
-                    if (r >= i && r > prev && r < len) {
-                        const int sp = page_of(from, r);
-                        if (sp >= 0 && !(a.in_place && r == i)) {
-                            const int in = (r >> 4) & mask;
-                            row_at = (long long)sp * a.g.page_bytes + (long long)(h * (mask + 1) + in) * CELL;
-                            score_at = ((long long)sp * a.g.Hkv + h) * a.g.page_rows + (r & (a.g.page_rows - 1));
-                            t = r & 15;
-                            moved = true;
-                        }
-                    } else {
-                        atomicExch(a.g.err, kErrCounter);
+        if (c < cells && good(now.dst)) {
+            const long long cell = (long long)now.dst * a.g.page_bytes + (long long)(h * (mask + 1) + (c & mask)) * CELL;
+            score_to = ((long long)now.dst * a.g.Hkv + h) * a.g.page_rows + (c & mask) * 16 + (lane & 15);
+            row_at = cell;                                         // (a row that is not moved stays as it is)
+            const int i = 16 * c + lane;
+            if (lane < 16 && i < n) {
+                if (now.r >= i && now.r > now.prev && now.r < len) {
+                    if (good(now.src) && !(a.in_place && now.r == i)) {
+                        row_at = (long long)now.src * a.g.page_bytes + (long long)(h * (mask + 1) + ((now.r >> 4) & mask)) * CELL;
+                        score_from = ((long long)now.src * a.g.Hkv + h) * a.g.page_rows + (now.r & (a.g.page_rows - 1));
+                        t = now.r & 15;
+                        moved = true;
                     }
+                } else {
+                    atomicExch(a.g.err, kErrCounter);
                 }
-                if (__any_sync(0xffffffffu, moved)) dst = a.g.pool + cell;
             }
+            if (__any_sync(0xffffffffu, moved)) dst = a.g.pool + cell;
         }
         float score = 0.f;
         if (dst) {
@@ -451,16 +469,14 @@ __global__ void __launch_bounds__(kMove) compact_kernel(const __grid_constant__ 
                 rt[i] = __shfl_sync(0xffffffffu, t, at);
             }
             p.load(cell, rt, g, j);
-            if (a.scores && moved) score = a.scores[score_at];
+            if (a.scores && moved) score = a.scores[score_from];
         }
         if (a.in_place) cluster::sync();                           // all of this window is read
         if (dst) {
             p.store(dst, g, j);
-            if (a.scores && moved) {
-                const int pg = to[(16 * c) >> a.g.page_shift];
-                a.scores[((long long)pg * a.g.Hkv + h) * a.g.page_rows + (c & mask) * 16 + lane] = score;
-            }
+            if (a.scores && moved) a.scores[score_to] = score;
         }
+        now = next;
     }
     if (tid == 0 && a.lens_out) {
         // the sequence's last block sets the length, when all have read it
@@ -502,7 +518,9 @@ cudaError_t launch_compact(CompactArgs a, int num_sms, cudaStream_t s) {
         while (C < cluster::kMaxCluster && C < windows && (long long)a.n_seq * a.g.Hkv * C < 2LL * num_sms) C *= 2;
         a.blocks = C;
     } else {
-        a.blocks = windows;
+        // two rounds of what the SMs hold: a block's start is a chain of four loads, of which a
+        // warp's later cells wait for the last only
+        a.blocks = (int)std::min<long long>(windows, std::max<long long>(1, 6LL * num_sms / ((long long)a.n_seq * a.g.Hkv)));
     }
     switch (a.g.NB()) {
         case 2: return launch_compact_nb<2>(a, C, s);

@@ -34,8 +34,10 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 8;               // queries
 constexpr int kPair = 2;               // cells of a stage
-template <int NB>
-constexpr int blocks_of() { return NB == 8 ? 4 : 5; }
+constexpr int kFade = 32;              // cells without a query that cost about as much as one with them
+// Blocks an SM, as registers allow: many queries take two tiles of them at a time
+template <int NB, bool MANY>
+constexpr int blocks_of() { return NB == 8 ? (MANY ? 3 : 4) : MANY ? 4 : 5; }
 template <int NB>
 constexpr int stages_of() { return 2; }
 template <int NB, bool F8>
@@ -54,8 +56,8 @@ __host__ __device__ constexpr size_t ring_at(int slices, int n_seq) {
     return ((size_t)slices * (tile_bytes<NB, F32Q>() + kTile * sizeof(Row)) + (size_t)(n_seq + 1) * 8 + 127) / 128 * 128;
 }
 
-template <int NB, bool F8, bool F32Q>
-__global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const __grid_constant__ ScoredArgs a) {
+template <int NB, bool F8, bool F32Q, bool MANY>
+__global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel(const __grid_constant__ ScoredArgs a) {
     constexpr int D = NB * 32, STAGES = stages_of<NB>(), KEYS = key_bytes<NB, F8>(), TILE = tile_bytes<NB, F32Q>();
     constexpr int CELL = NB * (F8 ? 1024 : 928);
     extern __shared__ __align__(128) uint8_t smem[];
@@ -75,13 +77,14 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     wait_for_earlier();
     let_next_start();
-    // ---- cells of each sequence: all below its length (with nothing to fade, those that a query sees)
+    // ---- work of each sequence: the cells that a query sees, and before them (where
+    // scores fade) those that none does, kFade a unit
     auto first_row = [&](int len) { return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0; };
-    auto first_cell = [&](int len) { return a.decay == 1.f ? first_row(len) >> 4 : 0; };
-    auto cells = [&](int e) {
+    auto fading = [&](int len) { return a.decay == 1.f ? 0 : ((first_row(len) >> 4) + kFade - 1) / kFade; };
+    auto units = [&](int e) {
         const int len = a.lens[e];
         if (len <= 0 || len > (long long)a.g.max_pages << a.g.page_shift) return 0;      // (reported by the decode)
-        return ((len + 15) >> 4) - first_cell(len);
+        return ((len + 15) >> 4) - (first_row(len) >> 4) + fading(len);
     };
     {
         const int per = (a.n_seq + kThreads - 1) / kThreads;
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
             const int e = tid * per + i;
             if (e < a.n_seq) {
                 plan[e] = w;
-                w += cells(e);
+                w += units(e);
             }
         }
         long long wi = w;
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
     int st = 0;
     uint32_t phase = 0;
     while (x < x1) {
-        // ---- fragment: cells [ca, cb) of KV head kh of sequence e
+        // ---- fragment: units [ua, ub) of KV head kh of sequence e, cells [ca, cb) and those that only fade
         int e = 0;
         {
             int hi = a.n_seq;
@@ -136,17 +139,31 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
         const long long in_e = x - plan[e] * a.g.Hkv;
         const int nc = (int)(plan[e + 1] - plan[e]);
         const int kh = in_e < (1LL << 31) ? (int)((unsigned)in_e / (unsigned)nc) : (int)(in_e / nc);
-        const int ca = (int)(in_e - (long long)kh * nc), cb = (int)min((long long)nc, ca + (x1 - x));
-        x += cb - ca;
-        const int len = a.lens[e], c0 = first_cell(len), nq = a.hpk * a.T;
+        const int ua = (int)(in_e - (long long)kh * nc), ub = (int)min((long long)nc, ua + (x1 - x));
+        x += ub - ua;
+        const int len = a.lens[e], nq = a.hpk * a.T;
         const int lo_row = first_row(len);                 // rows before it no query sees
+        const int unseen = lo_row >> 4, nf = fading(len);
+        const int ca = unseen + max(0, ua - nf), cb = unseen + max(0, ub - nf);
         const int* table = a.tables + (long long)e * a.g.max_pages;
-        for (int q0 = 0; q0 < nq; q0 += QB) {
+        // (four rows a thread)
+        for (int r = min(unseen, ua * kFade) * 16 + 4 * tid, end = min(unseen, min(ub, nf) * kFade) * 16; r < end; r += 4 * kThreads) {
+            const int page = table[r >> a.g.page_shift];
+            if (page < 0 || page >= a.g.n_pages) continue;
+            float4* p = reinterpret_cast<float4*>(a.scores + ((long long)page * a.g.Hkv + kh) * a.g.page_rows + (r & (a.g.page_rows - 1)));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.decay > 0.f) {
+                v = *p;
+                v = make_float4(a.decay * v.x, a.decay * v.y, a.decay * v.z, a.decay * v.w);
+            }
+            *p = v;
+        }
+        for (int q0 = 0; q0 < nq && ca < cb; q0 += QB) {
             const int n = min(QB, nq - q0), ns = (n + kTile - 1) / kTile;
             const float decay = q0 == 0 ? a.decay : 1.f;
             // ---- the producer side: the warp's cells in order, a lane holding one of the next 32
             int from = 32, pc = ca + kPair * warp, ps = st;
-            long long at = -1;                                     // of the lane's cell: its scores, and its keys (NULL: not read)
+            long long at = -1;                                     // of the lane's cell: its scores, and its keys (NULL: no cell)
             const uint8_t* keys = nullptr;
             auto produce = [&]() {
                 if (pc >= cb) return;
@@ -156,10 +173,10 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
                     at = -1;
                     keys = nullptr;
                     if (c < cb) {
-                        const int cell = c0 + c, in = cell & mask, page = table[cell >> cps];
+                        const int in = c & mask, page = table[c >> cps];
                         if (page >= 0 && page < a.g.n_pages) {     // (reported by the decode)
                             at = ((long long)page * a.g.Hkv + kh) * a.g.page_rows + in * 16;
-                            if (cell * 16 + 16 > lo_row) keys = a.g.pool + (long long)page * a.g.page_bytes + (long long)(kh * (mask + 1) + in) * CELL;
+                            keys = a.g.pool + (long long)page * a.g.page_bytes + (long long)(kh * (mask + 1) + in) * CELL;
                         }
                     }
                 }
@@ -244,22 +261,22 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
             float old = old_of(st, ca + kPair * warp);
             for (int c = ca + kPair * warp; c < cb; c += kPair * kWarps) {
                 const bool there = wait_bounded(bar0 + 8u * st, phase, &s_abort, a.g.err);
-                const int row0 = (c0 + c) * 16;
+                const int row0 = c * 16;
                 const long long to = s_at[warp][st][j >> 1];
                 const float next = old_of(st + 1 == STAGES ? 0 : st + 1, c + kPair * kWarps);
                 float gain[kPair][2] = {{0.f, 0.f}, {0.f, 0.f}};   // rows g and g + 8 of the cells, this lane's queries
                 if (there && row0 < hi_max && row0 + 16 * kPair > lo_min) {
-                    // (what the ring holds of a cell that was not read reaches no other's sums: its
-                    // rows are masked, or their scores not stored)
+                    // (what the ring holds in the place of a cell that is none reaches no other's sums, and is not stored)
                     const uint8_t* cell = ring + st * kPair * KEYS;
                     const bool edge = row0 < lo_max || row0 + 16 * kPair > hi_min;
-#pragma unroll 1
-                    for (int s = 0; s < ns; ++s) {
+                    // products of TB tiles of queries with the stage's cells, and their weights
+                    auto tiles = [&](auto tb, int s) {
+                        constexpr int TB = decltype(tb)::value;
                         const uint8_t* tile = qs + (size_t)s * TILE + lane * 8;
-                        float sc[kPair][4] = {};                   // (g, 2 j), (g, 2 j + 1), (g + 8, 2 j), (g + 8, 2 j + 1)
+                        float sc[TB][kPair][4] = {};               // (g, 2 j), (g, 2 j + 1), (g + 8, 2 j), (g + 8, 2 j + 1)
 #pragma unroll 1                                           // (unrolled, its loads take more registers than there are)
                         for (int bp = 0; bp < NB / 2; ++bp) {
-                            uint4 k0[kPair], k1[kPair], ks[kPair]; // ks: d of rows 2 (g / 2) + s and + 8, blocks 2 bp and 2 bp + 1
+                            [[maybe_unused]] uint4 k0[kPair], k1[kPair], ks[kPair];      // ks: d of rows 2 (g / 2) + s and + 8, blocks 2 bp and 2 bp + 1
 #pragma unroll
                             for (int x = 0; x < kPair; ++x) {
                                 k0[x] = *reinterpret_cast<const uint4*>(cell + x * KEYS + bp * 1024 + lane * 16);
@@ -269,61 +286,80 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
 #pragma unroll
                             for (int ee = 0; ee < 2; ++ee) {
                                 const int b = 2 * bp + ee;
-                                const uint2 b0 = *reinterpret_cast<const uint2*>(tile + 2 * b * 256), b1 = *reinterpret_cast<const uint2*>(tile + (2 * b + 1) * 256);
-                                uint2 l0 = b0, l1 = b1;
-                                if constexpr (F32Q) {
-                                    l0 = *reinterpret_cast<const uint2*>(tile + NB * 512 + 2 * b * 256);
-                                    l1 = *reinterpret_cast<const uint2*>(tile + NB * 512 + (2 * b + 1) * 256);
+                                [[maybe_unused]] uint2 b0[TB], b1[TB], l0[TB], l1[TB];
+#pragma unroll
+                                for (int u = 0; u < TB; ++u) {
+                                    const uint8_t* f = tile + u * TILE + 2 * b * 256;
+                                    b0[u] = *reinterpret_cast<const uint2*>(f);
+                                    b1[u] = *reinterpret_cast<const uint2*>(f + 256);
+                                    if constexpr (F32Q) {
+                                        l0[u] = *reinterpret_cast<const uint2*>(f + NB * 512);
+                                        l1[u] = *reinterpret_cast<const uint2*>(f + NB * 512 + 256);
+                                    }
                                 }
 #pragma unroll
                                 for (int x = 0; x < kPair; ++x) {
                                     const uint32_t v0 = ee ? k0[x].z : k0[x].x, w0 = ee ? k0[x].w : k0[x].y, v1 = ee ? k1[x].z : k1[x].x, w1 = ee ? k1[x].w : k1[x].y;
+                                    uint4 p, q;
+                                    [[maybe_unused]] float2 d;
                                     if constexpr (F8) {
-                                        const uint4 p = make_uint4(f8_pair(v0), f8_pair(v1), f8_pair(v0 >> 16), f8_pair(v1 >> 16));
-                                        const uint4 q = make_uint4(f8_pair(w0), f8_pair(w1), f8_pair(w0 >> 16), f8_pair(w1 >> 16));
-                                        mma_f16(sc[x], p, b0.x, b0.y);
-                                        mma_f16(sc[x], q, b1.x, b1.y);
-                                        if constexpr (F32Q) {
-                                            mma_f16(sc[x], p, l0.x, l0.y);
-                                            mma_f16(sc[x], q, l1.x, l1.y);
-                                        }
+                                        p = make_uint4(f8_pair(v0), f8_pair(v1), f8_pair(v0 >> 16), f8_pair(v1 >> 16));
+                                        q = make_uint4(f8_pair(w0), f8_pair(w1), f8_pair(w0 >> 16), f8_pair(w1 >> 16));
                                     } else {
-                                        const uint4 p = make_uint4(k_pair(v0, 0x4140u, exps), k_pair(v1, 0x4140u, exps), k_pair(v0, 0x4342u, exps), k_pair(v1, 0x4342u, exps));
-                                        const uint4 q = make_uint4(k_pair(w0, 0x4140u, exps), k_pair(w1, 0x4140u, exps), k_pair(w0, 0x4342u, exps), k_pair(w1, 0x4342u, exps));
+                                        p = make_uint4(k_pair(v0, 0x4140u, exps), k_pair(v1, 0x4140u, exps), k_pair(v0, 0x4342u, exps), k_pair(v1, 0x4342u, exps));
+                                        q = make_uint4(k_pair(w0, 0x4140u, exps), k_pair(w1, 0x4140u, exps), k_pair(w0, 0x4342u, exps), k_pair(w1, 0x4342u, exps));
+                                        d = __half22float2(as_h2(__byte_perm(ee ? ks[x].z : ks[x].x, ee ? ks[x].w : ks[x].y, pick)));
+                                    }
+#pragma unroll
+                                    for (int u = 0; u < TB; ++u) {
                                         float acc[4];
-                                        mma_f16_new(acc, p, b0.x, b0.y, zero);
-                                        mma_f16(acc, q, b1.x, b1.y);
+                                        float (&to)[4] = F8 ? sc[u][x] : acc;
+                                        if constexpr (F8) mma_f16(to, p, b0[u].x, b0[u].y);
+                                        else mma_f16_new(to, p, b0[u].x, b0[u].y, zero);
+                                        mma_f16(to, q, b1[u].x, b1[u].y);
                                         if constexpr (F32Q) {
-                                            mma_f16(acc, p, l0.x, l0.y);
-                                            mma_f16(acc, q, l1.x, l1.y);
+                                            mma_f16(to, p, l0[u].x, l0[u].y);
+                                            mma_f16(to, q, l1[u].x, l1[u].y);
                                         }
-                                        const float2 d = __half22float2(as_h2(__byte_perm(ee ? ks[x].z : ks[x].x, ee ? ks[x].w : ks[x].y, pick)));
-                                        sc[x][0] = fmaf(acc[0], d.x, sc[x][0]);
-                                        sc[x][1] = fmaf(acc[1], d.x, sc[x][1]);
-                                        sc[x][2] = fmaf(acc[2], d.y, sc[x][2]);
-                                        sc[x][3] = fmaf(acc[3], d.y, sc[x][3]);
+                                        if constexpr (!F8) {
+                                            sc[u][x][0] = fmaf(acc[0], d.x, sc[u][x][0]);
+                                            sc[u][x][1] = fmaf(acc[1], d.x, sc[u][x][1]);
+                                            sc[u][x][2] = fmaf(acc[2], d.y, sc[u][x][2]);
+                                            sc[u][x][3] = fmaf(acc[3], d.y, sc[u][x][3]);
+                                        }
                                     }
                                 }
                             }
                         }
-                        const Row* w = rows + s * kTile + 2 * j;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float4 f = *reinterpret_cast<const float4*>(w + i);      // fac, m, w, lo
+                        for (int u = 0; u < TB; ++u) {
+                            const Row* w = rows + (s + u) * kTile + 2 * j;
 #pragma unroll
-                            for (int x = 0; x < kPair; ++x)
+                            for (int i = 0; i < 2; ++i) {
+                                const float4 f = *reinterpret_cast<const float4*>(w + i);      // fac, m, w, lo
 #pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    float v = sc[x][2 * r + i] * f.x;
-                                    if (a.softcap_b > 0.f) v = a.softcap_b * tanhf(a.softcap_a * v);
-                                    float p = ex2(v - f.y) * f.z;
-                                    if (edge) {
-                                        const int at_row = row0 + 16 * x + g + 8 * r;
-                                        if (at_row < w[i].lo || at_row >= w[i].hi) p = 0.f;
+                                for (int x = 0; x < kPair; ++x)
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) {
+                                        float v = sc[u][x][2 * r + i] * f.x;
+                                        if (a.softcap_b > 0.f) v = a.softcap_b * tanhf(a.softcap_a * v);
+                                        float p = ex2(v - f.y) * f.z;
+                                        if (edge) {
+                                            const int at_row = row0 + 16 * x + g + 8 * r;
+                                            if (at_row < w[i].lo || at_row >= w[i].hi) p = 0.f;
+                                        }
+                                        gain[x][r] += p;
                                     }
-                                    gain[x][r] += p;
-                                }
+                            }
                         }
+                    };
+                    if constexpr (MANY) {
+                        int s = 0;
+#pragma unroll 1
+                        for (; s + 1 < ns; s += 2) tiles(std::integral_constant<int, 2>{}, s);
+                        if (s < ns) tiles(std::integral_constant<int, 1>{}, s);
+                    } else {
+                        tiles(std::integral_constant<int, 1>{}, 0);
                     }
                 }
                 // ---- over the queries (j): the first step leaves each lane one of the cells, the second one of its two rows
@@ -351,15 +387,20 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB>()) scored_kernel(const
     }
 }
 
+template <int NB, bool F8, bool F32Q, bool MANY>
+cudaError_t launch_many(const ScoredArgs& a, cudaStream_t s) {
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = kernel_attrs_once(scored_kernel<NB, F8, F32Q, MANY>, done, true);
+    if (e != cudaSuccess) return e;
+    const size_t smem = ring_at<NB, F8, F32Q>(a.slices, a.n_seq) + (size_t)kWarps * stages_of<NB>() * kPair * key_bytes<NB, F8>();
+    return launch_dependent(scored_kernel<NB, F8, F32Q, MANY>, dim3((unsigned)(a.sms * blocks_of<NB, MANY>())), kThreads, smem, s, a);
+}
+
 template <int NB, bool F8, bool F32Q>
 cudaError_t launch_t(ScoredArgs a, cudaStream_t s) {
-    static std::atomic<unsigned long long> done{0};
-    cudaError_t e = kernel_attrs_once(scored_kernel<NB, F8, F32Q>, done, true);
-    if (e != cudaSuccess) return e;
     // tiles: all queries of a KV head, or what 16 KB hold
     a.slices = std::min((a.hpk * a.T + kTile - 1) / kTile, 16 * 1024 / tile_bytes<NB, F32Q>());
-    const size_t smem = ring_at<NB, F8, F32Q>(a.slices, a.n_seq) + (size_t)kWarps * stages_of<NB>() * kPair * key_bytes<NB, F8>();
-    return launch_dependent(scored_kernel<NB, F8, F32Q>, dim3((unsigned)(a.sms * blocks_of<NB>())), kThreads, smem, s, a);
+    return a.slices > 1 ? launch_many<NB, F8, F32Q, true>(a, s) : launch_many<NB, F8, F32Q, false>(a, s);
 }
 
 template <int NB>

@@ -12,9 +12,9 @@
 //
 // A cluster of blocks shares a row: each sums its part (every warp a stretch of
 // it), the blocks tell each other their sums, and the one in whose part the
-// running sum passes goes down into it, a warp's stretch cut over all warps at a
-// time, until a stretch is 32 elements.  One row of p and q is read of T; the
-// parts read again come from L2.
+// running sum passes goes down into it: a warp's stretch is cut over all warps until
+// 2048 elements are left, eight a thread at most, whose running sums end it.  One row
+// of p and q is read of T; the parts read again come from L2.
 #include "../../include/kvq.h"
 #include "kvq_cluster.cuh"
 #include "kvq_error.h"
@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kEach = 8;               // elements of a thread in the last step
 using u64 = unsigned long long;
 
 struct Args {
@@ -228,22 +229,37 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         lo = min(hi, lo + w * per);
         hi = min(hi, lo + per);
         __syncthreads();                                 // (before the sums are written again)
-        if (hi - lo <= 32) break;
+        if (hi - lo <= kEach * kThreads) break;
         per = part(hi - lo, kWarps);
         sums(lo, hi);
     }
-    if (warp == 0) {
-        const int i = lo + lane;
-        u64 v = 0;
-        if (i < hi) v = with_q ? weight<true>(element<BF16>(p, i), element<BF16>(q, i), false) : weight<false>(element<BF16>(p, i), 0.f, i == tok);
+    const int each = (hi - lo + kThreads - 1) / kThreads, i0 = lo + tid * each;
+    u64 v[kEach], sum = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 y = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += y;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, i < hi && v > x);
-        if (lane == 0 && over) a.next[b] = lo + __ffs(over) - 1;
+    for (int k = 0; k < kEach; ++k) {
+        const int i = i0 + k;
+        v[k] = 0;
+        if (k < each && i < hi) v[k] = with_q ? weight<true>(element<BF16>(p, i), element<BF16>(q, i), false) : weight<false>(element<BF16>(p, i), 0.f, i == tok);
+        sum += v[k];
     }
+    u64 run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+    }
+    if (lane == 31) s_sum[warp] = run;
+    __syncthreads();
+    u64 at = run - sum;                                  // before this thread's elements
+    for (int w = 0; w < warp; ++w) at += s_sum[w];
+    if (x < at || x - at >= sum) return;                 // (one thread goes on)
+    int found = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        at += v[k];
+        found += at <= x;
+    }
+    a.next[b] = min(i0 + found, a.vocab - 1);
 }
 
 }  // namespace
