@@ -31,8 +31,6 @@ namespace {
 
 // ------------------------------------------------------------ choosing
 
-constexpr int kPick = 512;             // threads of a block
-constexpr int kPickWarps = kPick / 32;
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr uint32_t kForced = 0xffffffffu;      // key of a row that stays whatever its score (above infinity's)
 
@@ -44,13 +42,15 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 }
 
 // (sequence, KV head) blockIdx.x / C, rows [s0, s1) of it
+template <int kPick>
 __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constant__ RowsArgs a) {
+    constexpr int kPickWarps = kPick / 32, BPT = kBins / kPick;    // bins of a thread
     extern __shared__ __align__(16) uint32_t s_keys[];
     __shared__ __align__(16) uint32_t s_hist[2][kBins];
     __shared__ uint32_t s_range[cluster::kMaxCluster][2];          // of each block's keys, as it says itself
     __shared__ uint32_t s_taken[cluster::kMaxCluster][2];          // its rows above the threshold, and at it
-    __shared__ uint32_t s_lo[kPickWarps], s_hi[kPickWarps], s_sum[kPickWarps];
-    __shared__ uint32_t s_digit, s_need;
+    __shared__ uint32_t s_lo[kPickWarps], s_hi[kPickWarps];
+    __shared__ uint32_t s_digit, s_need, s_whole;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = cluster::size(), rank = cluster::rank();
     const int key = blockIdx.x / C, seq = key / a.g.Hkv, h = key - seq * a.g.Hkv;
@@ -71,8 +71,7 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
     const int s0 = min(len, rank * per), s1 = min(len, s0 + per), m = s1 - s0;
     const int* table = a.tables + (long long)seq * a.g.max_pages;
     const int f0 = min(max(first - s0, 0), m), f1 = min(max(last - s0, f0), m);   // of this part: [f0, f1)
-    auto place = [&](int r) -> const float* {                      // of row r's score
-        const int pg = table[r >> a.g.page_shift];
+    auto place = [&](int r, int pg) -> const float* {              // of row r's score, in page pg
         if (pg < 0 || pg >= a.g.n_pages) {
             atomicExch(a.g.err, kErrCounter);
             return nullptr;
@@ -82,22 +81,38 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
     // ---- keys (four rows a load: they start at a multiple of 16)
     uint32_t lo = 0xffffffffu, hi = 0u;
     const int held = min(m, a.cap);
-    auto four_of = [&](int i, const float* p, uint32_t (&k)[4]) {  // keys of rows s0 + i .. + 3 from their scores at p
-        const float4 v = p ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool all_held = held == m;
+    auto keys_of = [&](int i, const float* p, float4 v, uint32_t (&k)[4]) {      // of rows s0 + i .. + 3 from their scores v at p
         k[0] = ordered(v.x); k[1] = ordered(v.y); k[2] = ordered(v.z); k[3] = ordered(v.w);
 #pragma unroll
         for (int u = 0; u < 4; ++u) k[u] = i + u >= f0 && i + u < f1 ? (p ? k[u] : 0u) : kForced;
     };
-    for (int i0 = 4 * tid; i0 < m; i0 += 16 * kPick) {
-        const float* p[4];
+    constexpr int W = 4;                                           // loads in flight, and the next ones' pages
+    int pg[W];
+    auto pages = [&](int i0) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) p[x] = i0 + 4 * x * kPick < m ? place(s0 + i0 + 4 * x * kPick) : nullptr;
+        for (int x = 0; x < W; ++x) {
+            const int i = i0 + 4 * x * kPick;
+            pg[x] = i < m ? table[(s0 + i) >> a.g.page_shift] : 0;
+        }
+    };
+    pages(4 * tid);
+    for (int i0 = 4 * tid; i0 < m; i0 += 4 * W * kPick) {
+        const float* p[W];
+        float4 v[W];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < W; ++x) {
+            const int i = i0 + 4 * x * kPick;
+            p[x] = i < m ? place(s0 + i, pg[x]) : nullptr;
+            v[x] = p[x] ? *reinterpret_cast<const float4*>(p[x]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        pages(i0 + 4 * W * kPick);
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
             const int i = i0 + 4 * x * kPick;
             if (i >= m) break;
             uint32_t k[4];
-            four_of(i, p[x], k);
+            keys_of(i, p[x], v[x], k);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 if (k[u] != kForced) {
@@ -114,10 +129,11 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
         s_hi[warp] = hi;
     }
     __syncthreads();
-    if (tid < 2 * C) {
-        uint32_t v = tid & 1 ? s_hi[0] : s_lo[0];
-        for (int w = 1; w < kPickWarps; ++w) v = tid & 1 ? max(v, s_hi[w]) : min(v, s_lo[w]);
-        cluster::store(cluster::map(&s_range[rank][tid & 1], tid >> 1), v);
+    if (warp < 2) {
+        uint32_t v = warp ? 0u : 0xffffffffu;
+        if (lane < kPickWarps) v = warp ? s_hi[lane] : s_lo[lane];
+        v = warp ? __reduce_max_sync(0xffffffffu, v) : __reduce_min_sync(0xffffffffu, v);
+        if (lane < C) cluster::store(cluster::map(&s_range[rank][warp], lane), v);
     }
     cluster::sync();
     lo = s_range[0][0];
@@ -126,139 +142,188 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
         lo = min(lo, s_range[r][0]);
         hi = max(hi, s_range[r][1]);
     }
-    auto key_of = [&](int i) -> uint32_t {                         // of row s0 + i
-        if (i < held) return s_keys[i];
-        const float* p = place(s0 + i);
-        return p ? ordered(*p) : 0u;
+    // keys of rows s0 + i .. + 3, i a multiple of 4 below m (kForced behind the part, too, where they are read again)
+    auto four = [&](int i, uint32_t (&k)[4]) {
+        if (all_held || i < held) {
+            const uint4 v = *reinterpret_cast<const uint4*>(s_keys + i);
+            k[0] = v.x; k[1] = v.y; k[2] = v.z; k[3] = v.w;
+        } else {
+            const float* p = place(s0 + i, table[(s0 + i) >> a.g.page_shift]);
+            keys_of(i, p, p ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f), k);
+        }
     };
-    // ---- the threshold: digit by digit from the top
+    // ---- the threshold: digit by digit from the top, until all keys that share the digits are wanted
     uint32_t need = (uint32_t)(a.keep - a.n_first - a.n_last), prefix = 0;
     const bool any = need > 0;
+    bool whole = false;
     int bits = hi > lo ? 32 - __clz(hi - lo) : 0;
-    for (int pass = 0; any && bits > 0; ++pass) {
+    for (int pass = 0; any && bits > 0 && !whole; ++pass) {
         const int shift = max(0, bits - kBits);
         uint32_t* hist = s_hist[pass & 1];
-        reinterpret_cast<uint4*>(hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) hist[i * kPick + tid] = 0u;
         __syncthreads();
         const uint32_t mask = bits >= 32 ? 0u : 0xffffffffu << bits, digit = (1u << (bits - shift)) - 1u;
-#pragma unroll 4
-        for (int i = f0 + tid; i < f1; i += kPick) {
-            const uint32_t k = key_of(i) - lo;
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+#pragma unroll 2
+        for (int i = 4 * tid; i < m; i += 4 * kPick) {
+            uint32_t k[4];
+            four(i, k);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (k[u] != kForced && ((k[u] - lo) & mask) == prefix) atomicAdd(&hist[((k[u] - lo) >> shift) & digit], 1u);
         }
         cluster::sync();
-        // thread t sums bins kBins - 4 t - 1 .. - 4 of all blocks; where the count from the top reaches `need`
-        uint4 all[cluster::kMaxCluster], c = make_uint4(0u, 0u, 0u, 0u);
+        // thread t sums its bins, kBins - BPT t - 1 downwards, of all blocks; where the count from the top reaches `need`
+        uint32_t c[BPT];
+        {
+            uint4 v4[cluster::kMaxCluster];
+            uint2 v2[cluster::kMaxCluster];
 #pragma unroll
-        for (int r = 0; r < cluster::kMaxCluster; ++r) {           // (all on their way at once)
-            all[r] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < C) all[r] = cluster::load4(cluster::map(&hist[kBins - 4 * tid - 4], r));
-        }
+            for (int r = 0; r < cluster::kMaxCluster; ++r) {       // (all on their way at once)
+                v4[r] = make_uint4(0u, 0u, 0u, 0u);
+                v2[r] = make_uint2(0u, 0u);
+                if (r < C) {
+                    const uint32_t at = cluster::map(&hist[kBins - BPT * tid - BPT], r);
+                    if constexpr (BPT == 4) v4[r] = cluster::load4(at);
+                    else v2[r] = cluster::load2(at);
+                }
+            }
 #pragma unroll
-        for (int r = 0; r < cluster::kMaxCluster; ++r) {
-            c.x += all[r].x; c.y += all[r].y; c.z += all[r].z; c.w += all[r].w;
+            for (int i = 0; i < BPT; ++i) c[i] = 0u;
+#pragma unroll
+            for (int r = 0; r < cluster::kMaxCluster; ++r) {
+                if constexpr (BPT == 4) {
+                    c[0] += v4[r].w; c[1] += v4[r].z; c[2] += v4[r].y; c[BPT - 1] += v4[r].x;
+                } else {
+                    c[0] += v2[r].y; c[1] += v2[r].x;
+                }
+            }
         }
-        const uint32_t sum = c.x + c.y + c.z + c.w;
+        uint32_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < BPT; ++i) sum += c[i];
         uint32_t x = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) s_sum[warp] = x;
+        if (lane == 31) s_lo[warp] = x;
         __syncthreads();
-        uint32_t before = x - sum;
-        for (int w = 0; w < warp; ++w) before += s_sum[w];
+        const uint32_t w = lane < warp ? s_lo[lane] : 0u;          // (at most 32 warps)
+        uint32_t before = x - sum + __reduce_add_sync(0xffffffffu, w);
         if (before < need && before + sum >= need) {
-            const uint32_t n[4] = {c.w, c.z, c.y, c.x};
             int i = 0;
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-                if (i == k && before + n[k] < need) {
-                    before += n[k];
+            for (int k = 0; k < BPT - 1; ++k)
+                if (i == k && before + c[k] < need) {
+                    before += c[k];
                     i = k + 1;
                 }
-            s_digit = (uint32_t)(kBins - 4 * tid - 1 - i);
+            uint32_t in = c[0];
+#pragma unroll
+            for (int k = 1; k < BPT; ++k)
+                if (i == k) in = c[k];
+            s_digit = (uint32_t)(kBins - BPT * tid - 1 - i);
             s_need = need - before;
+            s_whole = in == need - before;
         }
         __syncthreads();
         prefix |= s_digit << shift;
         need = s_need;
+        whole = s_whole;
         bits = shift;
     }
-    const uint32_t thr = any ? lo + prefix : kForced - 1u;         // (no score's key)
-    // ---- rows above the threshold, and the first `need` at it, in index order: a
-    // stretch of the part for each warp, four neighbours a lane, the counts of 128 in the halves of a word
-    const int stretch = ((m + kPickWarps - 1) / kPickWarps + 127) & ~127, b0 = min(m, warp * stretch), b1 = min(m, b0 + stretch);
-    auto look = [&](int i, uint32_t& up, uint32_t& same) {         // masks of rows i .. i + 3
+    // ---- keys from `from` on are taken, and of those at `at_key` the first `need`, in
+    // index order (forced ones have the highest key): a stretch of the part for each
+    // warp, 32 rows a step, whose masks lane `step` keeps
+    const uint32_t at_key = lo + prefix, from = !any ? kForced : whole ? at_key : at_key + 1u;
+    const bool ties = any && !whole;
+    constexpr int kGroup = 32 * 32;
+    const int stretch = ((m + kPickWarps - 1) / kPickWarps + 31) & ~31;
+    const int b0 = min(m, warp * stretch), b1 = min(m, b0 + stretch);
+    auto masks = [&](int base, uint32_t& up, uint32_t& same) {     // of rows base + 32 lane .. + 31
         up = same = 0u;
-        if (i >= b1) return;
-        uint32_t k[4];
-        if (i < held) {
-            const uint4 v = *reinterpret_cast<const uint4*>(s_keys + i);
-            k[0] = v.x; k[1] = v.y; k[2] = v.z; k[3] = v.w;
-        } else {
-            four_of(i, place(s0 + i), k);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const bool in = i + u < b1;
-            up |= in && k[u] > thr ? 1u << u : 0u;
-            same |= in && k[u] == thr ? 1u << u : 0u;
-        }
-    };
-    uint32_t above = 0, at = 0;
-#pragma unroll 2
-    for (int i = b0 + 4 * lane; i < b1; i += 128) {
-        uint32_t up, same;
-        look(i, up, same);
-        above += __popc(up);
-        at += __popc(same);
-    }
-    above = __reduce_add_sync(0xffffffffu, above);
-    at = __reduce_add_sync(0xffffffffu, at);
-    if (lane == 0) {
-        s_lo[warp] = above;
-        s_hi[warp] = at;
-    }
-    __syncthreads();
-    if (tid < 2 * C) {
-        uint32_t v = 0;
-        for (int w = 0; w < kPickWarps; ++w) v += tid & 1 ? s_hi[w] : s_lo[w];
-        cluster::store(cluster::map(&s_taken[rank][tid & 1], tid >> 1), v);
-    }
-    cluster::sync();                                               // (the last: no block touches another's memory behind it)
-    uint32_t pos = 0, eq = 0;
-    for (int r = 0; r < rank; ++r) {
-        pos += s_taken[r][0];
-        eq += s_taken[r][1];
-    }
-    for (int w = 0; w < warp; ++w) {
-        pos += s_lo[w];
-        eq += s_hi[w];
-    }
-    for (int i0 = b0; i0 < b1; i0 += 128) {
-        uint32_t up, same;
-        look(i0 + 4 * lane, up, same);
-        const uint32_t mine = __popc(up) | __popc(same) << 16;
-        uint32_t sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
-        }
-        const uint32_t all = __shfl_sync(0xffffffffu, sum, 31), before = sum - mine;
-        uint32_t to = pos + (before & 0xffffu), e = eq + (before >> 16);      // rows above, and at it, before this lane's
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (up >> u & 1u) out[to++ + min(e, need)] = s0 + i0 + 4 * lane + u;
-            if (same >> u & 1u) {
-                if (e < need) out[to + e] = s0 + i0 + 4 * lane + u;
-                ++e;
+#pragma unroll 8
+        for (int st = 0; st < 32; ++st) {
+            const int i = base + 32 * st + lane;
+            if (base + 32 * st >= b1) break;
+            uint32_t k = 0u;
+            bool in = i < b1;
+            if (in) {
+                if (all_held || i < held) {
+                    k = s_keys[i];
+                } else {
+                    const float* p = place(s0 + i, table[(s0 + i) >> a.g.page_shift]);
+                    k = i >= f0 && i < f1 ? (p ? ordered(*p) : 0u) : kForced;
+                }
+            }
+            const uint32_t u = __ballot_sync(0xffffffffu, in && k >= from);
+            if (lane == st) up = u;
+            if (ties) {
+                const uint32_t e = __ballot_sync(0xffffffffu, in && k == at_key);
+                if (lane == st) same = e;
             }
         }
-        pos += all & 0xffffu;
-        eq += all >> 16;
+    };
+    uint32_t up0 = 0, same0 = 0, above = 0, equal = 0;             // (of the first group, kept for the writing)
+    for (int base = b0; base < b1; base += kGroup) {
+        uint32_t up, same;
+        masks(base, up, same);
+        if (base == b0) {
+            up0 = up;
+            same0 = same;
+        }
+        above += __popc(up);
+        equal += __popc(same);
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    __syncthreads();                                               // (s_lo may still be read)
+    if (lane == 0) {
+        s_lo[warp] = above;
+        s_hi[warp] = equal;
+    }
+    __syncthreads();
+    if (warp < 2) {
+        const uint32_t v = __reduce_add_sync(0xffffffffu, lane < kPickWarps ? (warp ? s_hi[lane] : s_lo[lane]) : 0u);
+        if (lane < C) cluster::store(cluster::map(&s_taken[rank][warp], lane), v);
+    }
+    cluster::sync();                                               // (the last: no block touches another's memory behind it)
+    uint32_t pos = __reduce_add_sync(0xffffffffu, (lane < rank ? s_taken[lane][0] : 0u) + (lane < warp ? s_lo[lane] : 0u));
+    uint32_t eq = __reduce_add_sync(0xffffffffu, (lane < rank ? s_taken[lane][1] : 0u) + (lane < warp ? s_hi[lane] : 0u));
+    const uint32_t below = (1u << lane) - 1u;
+    for (int base = b0; base < b1; base += kGroup) {
+        uint32_t up = up0, same = same0;
+        if (base != b0) masks(base, up, same);
+        // rows above, and at it, before this lane's 32
+        uint32_t pu = __popc(up), pe = __popc(same);
+        const uint32_t mu = pu, me = pe;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, pu, o), z = __shfl_up_sync(0xffffffffu, pe, o);
+            if (lane >= o) {
+                pu += y;
+                pe += z;
+            }
+        }
+        const uint32_t all_u = __shfl_sync(0xffffffffu, pu, 31), all_e = __shfl_sync(0xffffffffu, pe, 31);
+        pu += pos - mu;
+        pe += eq - me;
+#pragma unroll 8
+        for (int st = 0; st < 32; ++st) {
+            if (base + 32 * st >= b1) break;
+            const uint32_t u = __shfl_sync(0xffffffffu, up, st), at_u = __shfl_sync(0xffffffffu, pu, st);
+            uint32_t at_e = 0, e = 0;
+            if (ties) {
+                e = __shfl_sync(0xffffffffu, same, st);
+                at_e = __shfl_sync(0xffffffffu, pe, st) + __popc(e & below);
+            }
+            const bool taken = u >> lane & 1u, tied = (e >> lane & 1u) && at_e < need;
+            if (taken || tied) out[at_u + __popc(u & below) + min(at_e, need)] = s0 + base + 32 * st + lane;
+        }
+        pos += all_u;
+        eq += all_e;
     }
 }
 
@@ -491,17 +556,24 @@ __global__ void __launch_bounds__(kMove) compact_kernel(const __grid_constant__ 
 
 }  // namespace
 
-cudaError_t launch_select_rows(RowsArgs a, int num_sms, cudaStream_t s) {
+template <int kPick>
+static cudaError_t launch_select_t(const RowsArgs& a, unsigned grid, int C, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = kernel_attrs_once(select_rows_kernel, done, false);
+    cudaError_t e = kernel_attrs_once(select_rows_kernel<kPick>, done, false);
     if (e != cudaSuccess) return e;
+    return cluster::launch(select_rows_kernel<kPick>, dim3(grid), C, kPick, (size_t)a.cap * 4, s, a);
+}
+
+cudaError_t launch_select_rows(RowsArgs a, int num_sms, cudaStream_t s) {
     const long long keys = (long long)a.n_seq * a.g.Hkv, rows = (long long)a.g.max_pages << a.g.page_shift;
     // blocks of a (sequence, KV head): more while SMs are idle and a part keeps 2048 rows
     int C = 1;
     while (C < cluster::kMaxCluster && keys * C * 2 <= 2LL * num_sms && rows > 2048LL * C) C *= 2;
     const long long part = (rows / C + 31) / 16 * 16;
     a.cap = (int)std::min<long long>(part, 40 * 1024);             // 160 KB; rows behind that are read again in each pass
-    return cluster::launch(select_rows_kernel, dim3((unsigned)(keys * C)), C, kPick, (size_t)a.cap * 4, s, a);
+    // large blocks where each has an SM for itself
+    return keys * C <= num_sms && part > 2048 ? launch_select_t<1024>(a, (unsigned)(keys * C), C, s)
+                                              : launch_select_t<512>(a, (unsigned)(keys * C), C, s);
 }
 
 template <int NB>
