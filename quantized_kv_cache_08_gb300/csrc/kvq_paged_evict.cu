@@ -45,6 +45,7 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 template <int kPick>
 __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constant__ RowsArgs a) {
     constexpr int kPickWarps = kPick / 32, BPT = kBins / kPick;    // bins of a thread
+    static_assert(BPT == 2 || BPT == 4, "a thread reads its bins in one load");
     extern __shared__ __align__(16) uint32_t s_keys[];
     __shared__ __align__(16) uint32_t s_hist[2][kBins];
     __shared__ uint32_t s_range[cluster::kMaxCluster][2];          // of each block's keys, as it says itself
@@ -329,8 +330,11 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
 
 // ------------------------------------------------------------ moving
 
-constexpr int kMove = 256;             // threads of a block
-constexpr int kMoveWarps = kMove / 32;
+// Threads of a block.  In place a window is what a cluster's warps hold, and each
+// waits for its slowest load and a barrier: large ones where a cluster has SMs to
+// itself (131072 rows of 8 heads to 16384: 39 us, large 29; 32 sequences of up to
+// 16384 to 2000: 79 and 89).
+constexpr int kMove = 256, kMoveLarge = 512;
 
 template <typename T>
 __device__ __forceinline__ T get(const uint8_t* p) { return *reinterpret_cast<const T*>(p); }
@@ -452,9 +456,9 @@ struct Piece {
 
 // (sequence, KV head) blockIdx.x / a.blocks, whose blocks take window after window of
 // blocks x warps cells; in place they are a cluster.
-template <int NB, bool F8>
-__global__ void __launch_bounds__(kMove) compact_kernel(const __grid_constant__ CompactArgs a) {
-    constexpr int CELL = NB * (F8 ? 1024 : 928);
+template <int NB, bool F8, bool IN_PLACE, int THREADS>
+__global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant__ CompactArgs a) {
+    constexpr int CELL = NB * (F8 ? 1024 : 928), kMoveWarps = THREADS / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
     const int key = blockIdx.x / a.blocks, part = blockIdx.x - key * a.blocks;
     const int seq = key / a.g.Hkv, h = key - seq * a.g.Hkv;
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(kMove) compact_kernel(const __grid_constant__ 
             const int i = 16 * c + lane;
             if (lane < 16 && i < n) {
                 if (now.r >= i && now.r > now.prev && now.r < len) {
-                    if (good(now.src) && !(a.in_place && now.r == i)) {
+                    if (good(now.src) && !(IN_PLACE && now.r == i)) {
                         row_at = (long long)now.src * a.g.page_bytes + (long long)(h * (mask + 1) + ((now.r >> 4) & mask)) * CELL;
                         score_from = ((long long)now.src * a.g.Hkv + h) * a.g.page_rows + (now.r & (a.g.page_rows - 1));
                         t = now.r & 15;
@@ -536,7 +540,7 @@ __global__ void __launch_bounds__(kMove) compact_kernel(const __grid_constant__ 
             p.load(cell, rt, g, j);
             if (a.scores && moved) score = a.scores[score_from];
         }
-        if (a.in_place) cluster::sync();                           // all of this window is read
+        if constexpr (IN_PLACE) cluster::sync();                           // all of this window is read
         if (dst) {
             p.store(dst, g, j);
             if (a.scores && moved) a.scores[score_to] = score;
@@ -576,28 +580,33 @@ cudaError_t launch_select_rows(RowsArgs a, int num_sms, cudaStream_t s) {
                                               : launch_select_t<512>(a, (unsigned)(keys * C), C, s);
 }
 
-template <int NB>
-static cudaError_t launch_compact_nb(const CompactArgs& a, int C, cudaStream_t s) {
+template <int NB, bool F8>
+static cudaError_t launch_compact_t(const CompactArgs& a, int C, bool large, cudaStream_t s) {
     const dim3 grid((unsigned)((long long)a.n_seq * a.g.Hkv * a.blocks));
-    return a.g.fp8 ? cluster::launch(compact_kernel<NB, true>, grid, C, kMove, 0, s, a)
-                   : cluster::launch(compact_kernel<NB, false>, grid, C, kMove, 0, s, a);
+    if (!a.in_place) return cluster::launch(compact_kernel<NB, F8, false, kMove>, grid, C, kMove, 0, s, a);
+    return large ? cluster::launch(compact_kernel<NB, F8, true, kMoveLarge>, grid, C, kMoveLarge, 0, s, a)
+                 : cluster::launch(compact_kernel<NB, F8, true, kMove>, grid, C, kMove, 0, s, a);
 }
 
 cudaError_t launch_compact(CompactArgs a, int num_sms, cudaStream_t s) {
-    const int windows = ((a.most + 15) / 16 + kMoveWarps - 1) / kMoveWarps;      // blocks that take a cell a warp each
+    const long long keys = (long long)a.n_seq * a.g.Hkv;
+    const int cells = (a.most + 15) / 16;
     int C = 1;
+    bool large = false;
     if (a.in_place) {
-        while (C < cluster::kMaxCluster && C < windows && (long long)a.n_seq * a.g.Hkv * C < 2LL * num_sms) C *= 2;
+        while (C < cluster::kMaxCluster && C * (kMove / 32) < cells && keys * C < 2LL * num_sms) C *= 2;
+        large = keys * C <= num_sms;
         a.blocks = C;
     } else {
         // two rounds of what the SMs hold: a block's start is a chain of four loads, of which a
         // warp's later cells wait for the last only
-        a.blocks = (int)std::min<long long>(windows, std::max<long long>(1, 6LL * num_sms / ((long long)a.n_seq * a.g.Hkv)));
+        const int windows = (cells + kMove / 32 - 1) / (kMove / 32);
+        a.blocks = (int)std::min<long long>(windows, std::max<long long>(1, 6LL * num_sms / keys));
     }
     switch (a.g.NB()) {
-        case 2: return launch_compact_nb<2>(a, C, s);
-        case 4: return launch_compact_nb<4>(a, C, s);
-        default: return launch_compact_nb<8>(a, C, s);
+        case 2: return a.g.fp8 ? launch_compact_t<2, true>(a, C, large, s) : launch_compact_t<2, false>(a, C, large, s);
+        case 4: return a.g.fp8 ? launch_compact_t<4, true>(a, C, large, s) : launch_compact_t<4, false>(a, C, large, s);
+        default: return a.g.fp8 ? launch_compact_t<8, true>(a, C, large, s) : launch_compact_t<8, false>(a, C, large, s);
     }
 }
 
