@@ -55,14 +55,55 @@ __device__ __forceinline__ const void* row_at(const void* base, long long i) {
     return reinterpret_cast<const uint8_t*>(base) + i * (BF16 ? 2 : 4);
 }
 
-// a probability in units of 2^-52, rounded down: 0 where it is not above 0 (NaN too), 1 where it is above 1
-__device__ __forceinline__ u64 units(float x) {
-    x = fminf(fmaxf(x, 0.f), 1.f);                       // (of a NaN and a number the number)
-    const uint32_t b = __float_as_uint(x);
-    const int e = (int)(b >> 23) - 98;                   // x = m 2^(e - 52); (subnormals end as 0)
-    const uint32_t m = ((b & 0x7fffffu) | 0x800000u) >> min(max(-e, 0), 31);
-    return (u64)m * (1u << max(e, 0));
+// A probability in units of 2^-52, rounded down (0 where it is not above 0, NaN too, 1
+// where it is above 1), as 22 + 15 + 15 bits in the low bits of three floats above
+// 2^23: x 2^22 + 2^23 rounded down leaves the first, what that leaves out is exact,
+// and so on.  That is eight operations of the multiply-add pipe a number, where shifts
+// and masks by the exponent take ten of the integer pipe at half its rate; and sums of
+// the floats' bits are sums of the parts, for the offsets of a p and a q cancel.
+struct Parts {
+    uint32_t h, m, l;
+};
+constexpr uint32_t kBase = 0x4b000000u;                  // of 2^23
+__device__ __forceinline__ float clean(float x) {        // in [0, 1], of a NaN 0
+    asm("add.sat.f32 %0, %1, 0f00000000;" : "=f"(x) : "f"(x));
+    return x;
 }
+__device__ __forceinline__ Parts parts(float x) {        // (clean)
+    const float base = 8388608.f;
+    const float h = __fmaf_rz(x, 4194304.f, base);
+    x = __fmaf_rn(x, 4194304.f, base - h);
+    const float m = __fmaf_rz(x, 32768.f, base);
+    x = __fmaf_rn(x, 32768.f, base - m);
+    return {__float_as_uint(h), __float_as_uint(m), __float_as_uint(__fmaf_rz(x, 32768.f, base))};
+}
+__device__ __forceinline__ u64 units(float x) {
+    const Parts p = parts(clean(x));
+    return ((u64)(p.h - kBase) << 30) + ((p.m - kBase) << 15) + (p.l - kBase);
+}
+
+// Sums of up to 256 weights in three parts
+struct Sum3 {
+    uint32_t h = 0, m = 0, l = 0;
+    // p less q, where that is above 0 (p > q: then P >= Q)
+    __device__ __forceinline__ void add(float p, float q) {
+        p = clean(p);
+        q = clean(q);
+        const Parts x = parts(p), y = parts(q);
+        if (p > q) {
+            h += x.h - y.h;
+            m += x.m - y.m;
+            l += x.l - y.l;
+        }
+    }
+    __device__ __forceinline__ void add(float p) {
+        const Parts x = parts(clean(p));
+        h += x.h - kBase;
+        m += x.m - kBase;
+        l += x.l - kBase;
+    }
+    __device__ __forceinline__ u64 all() const { return ((u64)h << 30) + (u64)((long long)(int)m << 15) + (u64)(long long)(int)l; }
+};
 
 // What an element weighs: by p less q, or by p alone.  out: a lone draft's element, which weighs nothing
 template <bool Q>
@@ -90,28 +131,38 @@ __device__ __forceinline__ u64 sum_range(const void* p, const void* q, int lo, i
     int i = lo;
     auto step = [&](auto u) {
         constexpr int N = decltype(u)::value;
-        uint4 a[N], b[N];
+        uint4 a[N];
+        [[maybe_unused]] uint4 b[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const long long at = i + (k * 32 + lane) * V;
             a[k] = __ldg(reinterpret_cast<const uint4*>(row_at<BF16>(p, at)));
             if constexpr (Q) b[k] = __ldg(reinterpret_cast<const uint4*>(row_at<BF16>(q, at)));
-            else b[k] = make_uint4(0u, 0u, 0u, 0u);
         }
+        Sum3 t;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const int at = i + (k * 32 + lane) * V;
-            const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, y[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+            const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+            [[maybe_unused]] uint32_t y[4] = {};
+            if constexpr (Q) y[0] = b[k].x, y[1] = b[k].y, y[2] = b[k].z, y[3] = b[k].w;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 if constexpr (BF16) {
-                    s += weight<Q>(__uint_as_float(x[w] << 16), __uint_as_float(y[w] << 16), at + 2 * w == tok);
-                    s += weight<Q>(__uint_as_float(x[w] & 0xffff0000u), __uint_as_float(y[w] & 0xffff0000u), at + 2 * w + 1 == tok);
+                    const float p0 = __uint_as_float(x[w] << 16), p1 = __uint_as_float(x[w] & 0xffff0000u);
+                    if constexpr (Q) {
+                        t.add(p0, __uint_as_float(y[w] << 16));
+                        t.add(p1, __uint_as_float(y[w] & 0xffff0000u));
+                    } else {
+                        t.add(p0);
+                        t.add(p1);
+                    }
                 } else {
-                    s += weight<Q>(__uint_as_float(x[w]), __uint_as_float(y[w]), at + w == tok);
+                    if constexpr (Q) t.add(__uint_as_float(x[w]), __uint_as_float(y[w]));
+                    else t.add(__uint_as_float(x[w]));
                 }
             }
         }
+        s += t.all();
         i += N * V * 32;
     };
     if (vec) {
@@ -128,9 +179,16 @@ __device__ __forceinline__ u64 sum_range(const void* p, const void* q, int lo, i
             x[k] = at < hi ? element<BF16>(p, at) : 0.f;
             y[k] = Q && at < hi ? element<BF16>(q, at) : 0.f;
         }
+        Sum3 t;
 #pragma unroll
-        for (int k = 0; k < W; ++k) s += weight<Q>(x[k], y[k], i + k * 32 + lane == tok);
+        for (int k = 0; k < W; ++k) {
+            if constexpr (Q) t.add(x[k], y[k]);
+            else t.add(x[k]);
+        }
+        s += t.all();
     }
+    // (a sum of whole numbers: what a lone draft's element brought is taken off again)
+    if (!Q && lane == 0 && tok >= lo && tok < hi) s -= units(element<BF16>(p, tok));
     return s;
 }
 
