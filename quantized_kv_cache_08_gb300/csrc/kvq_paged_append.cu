@@ -336,11 +336,13 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a, long long ro
 // A unit is a warp's rows of one kind of one token: 64 / LR query heads (a lane
 // holds 8 elements and the 8 that they are rotated with), or 32 / LR key or
 // value heads (8 elements a lane, four lanes a block).
-template <int LR, bool BF16, bool BOUNDS>
+// MORE: positions are given, or scores kept (apart, for the branches alone cost an
+// append of 8k rows 1 us and a step 0.2).
+template <int LR, bool BF16, bool BOUNDS, bool MORE>
 __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq, int TT) {
     extern __shared__ float2 s_cs[];               // [TT][rope_dim / 2]
     __shared__ Place s_place[kTT];
-    __shared__ int s_at[kTT][kMaxAxes];            // given positions
+    __shared__ int s_at[MORE ? kTT : 1][kMaxAxes]; // given positions
     constexpr int D = LR * 8, NB = D / 32, JPW = 32 / LR, QPW = 64 / LR;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row0 = blockIdx.x * TT;
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
         const int row = row0 + lane, i = entry_of_rows<kTT>(a.r, row0, lane);
         Place p{-1, -1, 0, 0, 0};
         if (lane < TT && row < a.r.rows) p = place_in(a.g, a.r, row, i, true);
-        if (a.positions && p.pos >= 0) {
+        if (MORE && a.positions && p.pos >= 0) {
             int at[kMaxAxes];
             given_positions(a, row, at);
             if (at[0] < 0) p = Place{-1, -2, 0, 0, 0};
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
     // (an indexed read of the frequencies takes a step for each lane: one a thread)
     for (int pr = tid % (kThreads / TT); pr < half; pr += kThreads / TT) {
         const int tt = tid / (kThreads / TT);
-        put_angle(s_cs + tt * half, fq.f[pr], a.positions && s_place[tt].pos >= 0 ? s_at[tt][fq.axis[pr]] : s_place[tt].pos, pr, half, a.interleaved);
+        put_angle(s_cs + tt * half, fq.f[pr], MORE && a.positions && s_place[tt].pos >= 0 ? s_at[tt][fq.axis[pr]] : s_place[tt].pos, pr, half, a.interleaved);
     }
     __syncthreads();
     // a warp's token, and its share of the token's units
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
     const int u0 = blockIdx.y * wpt + warp - tt * wpt, du = gridDim.y * wpt;
     const Place pl = s_place[tt];
     if (pl.pos < 0) return;
-    if (a.row_scores && blockIdx.y == 0 && pl.cell >= 0) clear_scores(a, pl, (warp - tt * wpt) * 32 + lane, wpt * 32);
+    if (MORE && a.row_scores && blockIdx.y == 0 && pl.cell >= 0) clear_scores(a, pl, (warp - tt * wpt) * 32 + lane, wpt * 32);
     const float2* cs = s_cs + tt * half;
     const long long row = row0 + tt;
     const int uq = a.q ? (a.Hq + QPW - 1) / QPW : 0, uk = (a.g.Hkv + JPW - 1) / JPW;
@@ -523,12 +525,12 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
 // stores them byte by byte.  6 x 1379 rows, 32 query and 8 KV heads of 128: 42 us,
 // append_kernel 67 (its q8_0 / q5_1 rows: 48; by pieces they took 56: the exact rounding of
 // a whole block a lane is much code).
-template <int NB, bool BF16>
+template <int NB, bool BF16, bool MORE>
 __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ Freqs fq) {
     constexpr int D = NB * 32, LR = D / 8, BL = NB < 4 ? NB : 4, RT = 32 / BL, W = 2 * RT;
     extern __shared__ float2 s_cs[];                 // [W][rope_dim / 2]
     __shared__ Place s_place[W];
-    __shared__ int s_at[W][kMaxAxes];                // given positions; -1: the row is skipped
+    __shared__ int s_at[MORE ? W : 1][kMaxAxes];     // given positions; -1: the row is skipped
     __shared__ int s_from[W];                        // the piece of a row: index of its first row, -1 none of this CTA's
     __shared__ __align__(16) uint8_t s_stage[kCellWarps][1024];
     constexpr int kSlots = 32;                       // threads that take different pairs
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
             const int from = p.pos < 0 ? -1 : queries ? lane : lane - min(p.pos & (RT - 1), p.pos - p.first);
             s_place[lane] = p;
             s_from[lane] = from < RT ? from : -1;    // (below 0: the CTA before has it)
-            if (a.positions && from >= 0 && from < RT) {
+            if (MORE && a.positions && from >= 0 && from < RT) {
                 int at[kMaxAxes];
                 given_positions(a, row, at);
 #pragma unroll
@@ -555,15 +557,15 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
         }
     }
     __syncthreads();
-    const auto skipped = [&](int i) { return a.positions && s_at[i][0] < 0; };   // (of rows that are this CTA's)
+    const auto skipped = [&](int i) { return MORE && a.positions && s_at[i][0] < 0; };   // (of rows that are this CTA's)
     // a pair a thread (an indexed read of the frequencies takes a step for each lane), every token
     const int stride_cs = half + 1;                  // rows of the tables start in different banks
     for (int pr = tid % kSlots; pr < half; pr += kSlots) {
         const float2 f = fq.f[pr];
-        const int axis = a.positions ? fq.axis[pr] : 0;
+        const int axis = MORE && a.positions ? fq.axis[pr] : 0;
         for (int tt = tid / kSlots; tt < W; tt += kCellThreads / kSlots)
             if (s_from[tt] >= 0)
-                put_angle(s_cs + tt * stride_cs, f, a.positions ? s_at[tt][axis] : s_place[tt].pos, pr, half, a.interleaved);
+                put_angle(s_cs + tt * stride_cs, f, MORE && a.positions ? s_at[tt][axis] : s_place[tt].pos, pr, half, a.interleaved);
     }
     const int per = a.g.Hkv * (NB / BL);             // tasks of a piece and kind
     const int li = lane / BL, bl = lane % BL;        // row of the piece, block of the four
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
             if (s_from[i] >= 0 && !skipped(i)) rotate_queries<LR, BF16>(a, row0 + i, s_cs + i * stride_cs, 0, 1, lane);
         return;
     }
-    if (a.row_scores)
+    if (MORE && a.row_scores)
         for (int i = warp; i < W; i += kCellWarps)
             if (s_from[i] >= 0 && s_place[i].cell >= 0 && !skipped(i)) clear_scores(a, s_place[i], lane, 32);
     // values first, for they need no angles
@@ -799,18 +801,22 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsArgs a) {
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cudaStream_t s) {
+    const std::true_type yes;
+    const std::false_type no;
+    const bool more = a.positions || a.row_scores;
     // pieces of cells where a sequence brings 8 rows or more on average
     if (a.g.fp8 && a.r.rows / 8 >= a.r.n_seq) {
         const int rt = a.g.D == 64 ? 16 : 8;
         const dim3 grid((unsigned)((a.r.rows + rt - 1) / rt * (a.q ? 2 : 1)));
         const size_t smem = (size_t)2 * rt * (a.rope_dim / 2 + 1) * sizeof(float2);
-        auto run = [&](auto b) {
-            constexpr bool B = decltype(b)::value;
-            if (a.g.D == 64) return launch_dependent(append_cells_kernel<2, B>, grid, kCellThreads, smem, s, a, f);
-            if (a.g.D == 128) return launch_dependent(append_cells_kernel<4, B>, grid, kCellThreads, smem, s, a, f);
-            return launch_dependent(append_cells_kernel<8, B>, grid, kCellThreads, smem, s, a, f);
+        auto run = [&](auto b, auto with_more) {
+            constexpr bool B = decltype(b)::value, M = decltype(with_more)::value;
+            if (a.g.D == 64) return launch_dependent(append_cells_kernel<2, B, M>, grid, kCellThreads, smem, s, a, f);
+            if (a.g.D == 128) return launch_dependent(append_cells_kernel<4, B, M>, grid, kCellThreads, smem, s, a, f);
+            return launch_dependent(append_cells_kernel<8, B, M>, grid, kCellThreads, smem, s, a, f);
         };
-        return a.bf16 ? run(std::true_type{}) : run(std::false_type{});
+        if (more) return a.bf16 ? run(yes, yes) : run(no, yes);
+        return a.bf16 ? run(yes, no) : run(no, no);
     }
     const int jpw = 256 / a.g.D, qpw = 2 * jpw;
     const int units = (a.q ? (a.Hq + qpw - 1) / qpw : 0) + 2 * ((a.g.Hkv + jpw - 1) / jpw);
@@ -822,16 +828,18 @@ cudaError_t launch_append(const AppendArgs& a, const Freqs& f, int num_sms, cuda
     const int gy = std::max(1, std::min(most, (2 * num_sms + gx - 1) / gx));
     const size_t smem = (size_t)TT * (a.rope_dim / 2) * sizeof(float2);
     const dim3 grid((unsigned)gx, (unsigned)gy);
-    auto run = [&](auto b, auto with_bounds) {
-        constexpr bool B = decltype(b)::value, W = decltype(with_bounds)::value;
-        if (a.g.D == 64) return launch_dependent(append_kernel<8, B, W>, grid, kThreads, smem, s, a, f, TT);
-        if (a.g.D == 128) return launch_dependent(append_kernel<16, B, W>, grid, kThreads, smem, s, a, f, TT);
-        return launch_dependent(append_kernel<32, B, W>, grid, kThreads, smem, s, a, f, TT);
+    auto run = [&](auto b, auto with_bounds, auto with_more) {
+        constexpr bool B = decltype(b)::value, W = decltype(with_bounds)::value, M = decltype(with_more)::value;
+        if (a.g.D == 64) return launch_dependent(append_kernel<8, B, W, M>, grid, kThreads, smem, s, a, f, TT);
+        if (a.g.D == 128) return launch_dependent(append_kernel<16, B, W, M>, grid, kThreads, smem, s, a, f, TT);
+        return launch_dependent(append_kernel<32, B, W, M>, grid, kThreads, smem, s, a, f, TT);
     };
-    const std::true_type yes;
-    const std::false_type no;
-    if (a.codes) return a.bf16 ? run(yes, yes) : run(no, yes);
-    return a.bf16 ? run(yes, no) : run(no, no);
+    if (more) {
+        if (a.codes) return a.bf16 ? run(yes, yes, yes) : run(no, yes, yes);
+        return a.bf16 ? run(yes, no, yes) : run(no, no, yes);
+    }
+    if (a.codes) return a.bf16 ? run(yes, yes, no) : run(no, yes, no);
+    return a.bf16 ? run(yes, no, no) : run(no, no, no);
 }
 
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t s) {
