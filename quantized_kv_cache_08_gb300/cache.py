@@ -526,9 +526,9 @@ def verify(target, draft, tokens, uniform, lens=None, accept=None, next_tokens=N
 
     def make():
         if stream is None:
-            return torch.empty(n, dtype=_I32, device=target.device)
+            return tokens.new_empty(n)
         with torch.cuda.stream(stream):
-            t = torch.empty(n, dtype=_I32, device=target.device)
+            t = tokens.new_empty(n)
         t.record_stream(torch.cuda.current_stream(target.device))
         return t
 

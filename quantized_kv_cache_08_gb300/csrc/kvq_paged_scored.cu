@@ -46,7 +46,7 @@ template <int NB, bool F32Q>
 constexpr int tile_bytes() { return NB * 512 * (F32Q ? 2 : 1); }
 
 struct Row {
-    float fac, m, w;                   // a weight is w 2^(fac x product - m)
+    float fac, m, w;                   // a weight is w 2^(fac x product + m)
     int lo, hi, pad[3];
 };
 
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                 const int ex = am > 0u ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
                 const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
                 if (lane == 0) {
-                    rows[r] = Row{factor(a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23)), on ? stat.x : 0.f, on ? stat.y : 0.f, on ? lo : 0, on ? hi : 0, {}};
+                    rows[r] = Row{factor(a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23)), on ? -stat.x : 0.f, on ? stat.y : 0.f, on ? lo : 0, on ? hi : 0, {}};
                     if (on) {
                         atomicMax(&s_ext[0], lo);
                         atomicMin(&s_ext[1], hi);
@@ -341,14 +341,14 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                                 for (int x = 0; x < kPair; ++x)
 #pragma unroll
                                     for (int r = 0; r < 2; ++r) {
-                                        float v = sc[u][x][2 * r + i] * f.x;
-                                        if (a.softcap_b > 0.f) v = a.softcap_b * tanhf(a.softcap_a * v);
-                                        float p = ex2(v - f.y) * f.z;
+                                        float v = fmaf(sc[u][x][2 * r + i], f.x, f.y);
+                                        if (a.softcap_b > 0.f) v = fmaf(a.softcap_b, tanhf(a.softcap_a * (sc[u][x][2 * r + i] * f.x)), f.y);
+                                        float p = ex2(v);
                                         if (edge) {
                                             const int at_row = row0 + 16 * x + g + 8 * r;
                                             if (at_row < w[i].lo || at_row >= w[i].hi) p = 0.f;
                                         }
-                                        gain[x][r] += p;
+                                        gain[x][r] = fmaf(p, f.z, gain[x][r]);
                                     }
                             }
                         }
