@@ -203,47 +203,62 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
             __syncthreads();
             if (tid < 4) s_ext[tid] = tid == 0 || tid == 3 ? 0 : 0x7fffffff;      // lo_max, hi_min, lo_min, hi_max
             __syncthreads();
-            for (int r = warp; r < ns * kTile; r += kWarps) {
-                float v[NB];
-                float2 stat = make_float2(0.f, 0.f);
-                int lo = 0, hi = 0;
-                if (r < n) {
-                    const int t = (q0 + r) / a.hpk, h = kh * a.hpk + (q0 + r) - t * a.hpk;
-                    const long long at = ((long long)e * a.T + t) * a.Hq + h;
-                    hi = len - a.T + t + 1;
-                    lo = a.window > 0 ? max(0, hi - a.window) : 0;
-                    if (hi > lo) stat = a.stats[at];
+            // (a warp's next queries are all on their way before it lays the first out)
+            constexpr int QA = MANY && NB < 8 ? 4 : 2;
+            for (int r0 = warp; r0 < ns * kTile; r0 += QA * kWarps) {
+                float v[QA][NB];
+                float2 stat[QA];
+                int lo[QA], hi[QA];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) v[b] = load_q(a.q, at * D + 32 * b + lane, a.bf16);
-                }
-                const bool on = hi > lo && stat.y > 0.f && stat.x > kNegInf && stat.x < kInf;
-                uint32_t am = 0u;
+                for (int i = 0; i < QA; ++i) {
+                    const int r = r0 + i * kWarps;
+                    stat[i] = make_float2(0.f, 0.f);
+                    lo[i] = hi[i] = 0;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if (!on) v[b] = 0.f;
-                    am = max(am, __float_as_uint(v[b]) & 0x7fffffffu);
-                }
-                am = __reduce_max_sync(0xffffffffu, am);
-                const int ex = am > 0u ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
-                const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
-                if (lane == 0) {
-                    rows[r] = Row{factor(a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23)), on ? -stat.x : 0.f, on ? stat.y : 0.f, on ? lo : 0, on ? hi : 0, {}};
-                    if (on) {
-                        atomicMax(&s_ext[0], lo);
-                        atomicMin(&s_ext[1], hi);
-                        atomicMin(&s_ext[2], lo);
-                        atomicMax(&s_ext[3], hi);
+                    for (int b = 0; b < NB; ++b) v[i][b] = 0.f;
+                    if (r < n) {
+                        const int t = (q0 + r) / a.hpk, h = kh * a.hpk + (q0 + r) - t * a.hpk;
+                        const long long at = ((long long)e * a.T + t) * a.Hq + h;
+                        hi[i] = len - a.T + t + 1;
+                        lo[i] = a.window > 0 ? max(0, hi[i] - a.window) : 0;
+                        if (hi[i] > lo[i]) stat[i] = a.stats[at];
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) v[i][b] = load_q(a.q, at * D + 32 * b + lane, a.bf16);
                     }
                 }
-                const int wi = lane & 7, jj = lane >> 3;
-                uint8_t* tile = qs + (size_t)(r / kTile) * TILE + (4 * (r % kTile) + jj) * 8 + ((wi & 3) >> 1) * 4 + (wi & 1) * 2;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const float y = v[b] * up;
-                    const __half top = __float2half_rn(y);
-                    __half* dst = reinterpret_cast<__half*>(tile + (2 * b + (wi >> 2)) * 256);
-                    *dst = top;
-                    if constexpr (F32Q) dst[NB * 256] = __float2half_rn(y - __half2float(top));      // the low parts lie behind
+                for (int i = 0; i < QA; ++i) {
+                    const int r = r0 + i * kWarps;
+                    if (r >= ns * kTile) break;
+                    const bool on = hi[i] > lo[i] && stat[i].y > 0.f && stat[i].x > kNegInf && stat[i].x < kInf;
+                    uint32_t am = 0u;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        if (!on) v[i][b] = 0.f;
+                        am = max(am, __float_as_uint(v[i][b]) & 0x7fffffffu);
+                    }
+                    am = __reduce_max_sync(0xffffffffu, am);
+                    const int ex = am > 0u ? min(max((int)(am >> 23) - 127 - 9, -117), 118) : 0;
+                    const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
+                    if (lane == 0) {
+                        rows[r] = Row{factor(a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23)), on ? -stat[i].x : 0.f, on ? stat[i].y : 0.f, on ? lo[i] : 0, on ? hi[i] : 0, {}};
+                        if (on) {
+                            atomicMax(&s_ext[0], lo[i]);
+                            atomicMin(&s_ext[1], hi[i]);
+                            atomicMin(&s_ext[2], lo[i]);
+                            atomicMax(&s_ext[3], hi[i]);
+                        }
+                    }
+                    const int wi = lane & 7, jj = lane >> 3;
+                    uint8_t* tile = qs + (size_t)(r / kTile) * TILE + (4 * (r % kTile) + jj) * 8 + ((wi & 3) >> 1) * 4 + (wi & 1) * 2;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const float y = v[i][b] * up;
+                        const __half top = __float2half_rn(y);
+                        __half* dst = reinterpret_cast<__half*>(tile + (2 * b + (wi >> 2)) * 256);
+                        *dst = top;
+                        if constexpr (F32Q) dst[NB * 256] = __float2half_rn(y - __half2float(top));      // the low parts lie behind
+                    }
                 }
             }
             __syncthreads();
