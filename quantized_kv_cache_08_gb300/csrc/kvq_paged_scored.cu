@@ -35,6 +35,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 8;               // queries
 constexpr int kPair = 2;               // cells of a stage
 constexpr int kFade = 32;              // cells without a query that cost about as much as one with them
+// (what a change of key costs a block, in cells: kSetup)
 // Blocks an SM, as registers allow: many queries take two tiles of them at a time
 template <int NB, bool MANY>
 constexpr int blocks_of() { return NB == 8 ? (MANY ? 3 : 4) : MANY ? 4 : 5; }
@@ -59,10 +60,10 @@ __host__ __device__ constexpr size_t ring_at(int slices, int n_seq) {
 template <int NB, bool F8, bool F32Q, bool MANY>
 __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel(const __grid_constant__ ScoredArgs a) {
     constexpr int D = NB * 32, STAGES = stages_of<NB>(), KEYS = key_bytes<NB, F8>(), TILE = tile_bytes<NB, F32Q>();
-    constexpr int CELL = NB * (F8 ? 1024 : 928);
+    constexpr int CELL = NB * (F8 ? 1024 : 928), kSetup = MANY ? 16 : 8;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_wsum[kWarps];
-    __shared__ int s_ext[4], s_abort;
+    __shared__ int s_ext[kWarps][4], s_abort;
     __shared__ long long s_at[kWarps][STAGES][kPair];      // where the scores of a stage's cells lie, -1: no cell
     __shared__ __align__(8) uint64_t s_bar[kWarps][STAGES];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, j = lane & 3;
@@ -77,14 +78,14 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     wait_for_earlier();
     let_next_start();
-    // ---- work of each sequence: the cells that a query sees, and before them (where
-    // scores fade) those that none does, kFade a unit
+    // ---- work of each sequence and KV head: its setup, the cells that a query sees, and
+    // before them (where scores fade) those that none does, kFade a unit
     auto first_row = [&](int len) { return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0; };
     auto fading = [&](int len) { return a.decay == 1.f ? 0 : ((first_row(len) >> 4) + kFade - 1) / kFade; };
     auto units = [&](int e) {
         const int len = a.lens[e];
         if (len <= 0 || len > (long long)a.g.max_pages << a.g.page_shift) return 0;      // (reported by the decode)
-        return ((len + 15) >> 4) - (first_row(len) >> 4) + fading(len);
+        return kSetup + ((len + 15) >> 4) - (first_row(len) >> 4) + fading(len);
     };
     {
         const int per = (a.n_seq + kThreads - 1) / kThreads;
@@ -144,10 +145,11 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
         const int len = a.lens[e], nq = a.hpk * a.T;
         const int lo_row = first_row(len);                 // rows before it no query sees
         const int unseen = lo_row >> 4, nf = fading(len);
-        const int ca = unseen + max(0, ua - nf), cb = unseen + max(0, ub - nf);
+        const int fa = max(0, ua - kSetup), fb = max(0, ub - kSetup);      // (a key's first units stand for its setup)
+        const int ca = unseen + max(0, fa - nf), cb = unseen + max(0, fb - nf);
         const int* table = a.tables + (long long)e * a.g.max_pages;
         // (four rows a thread)
-        for (int r = min(unseen, ua * kFade) * 16 + 4 * tid, end = min(unseen, min(ub, nf) * kFade) * 16; r < end; r += 4 * kThreads) {
+        for (int r = min(unseen, fa * kFade) * 16 + 4 * tid, end = min(unseen, min(fb, nf) * kFade) * 16; r < end; r += 4 * kThreads) {
             const int page = table[r >> a.g.page_shift];
             if (page < 0 || page >= a.g.n_pages) continue;
             float4* p = reinterpret_cast<float4*>(a.scores + ((long long)page * a.g.Hkv + kh) * a.g.page_rows + (r & (a.g.page_rows - 1)));
@@ -201,10 +203,9 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
             for (int i = 0; i < STAGES; ++i) produce();
             // ---- queries [q0, q0 + n) into tiles; one that adds nothing is zeros with weight 0
             __syncthreads();
-            if (tid < 4) s_ext[tid] = tid == 0 || tid == 3 ? 0 : 0x7fffffff;      // lo_max, hi_min, lo_min, hi_max
-            __syncthreads();
             // (a warp's next queries are all on their way before it lays the first out)
             constexpr int QA = MANY && NB < 8 ? 4 : 2;
+            int ext[4] = {0, 0x7fffffff, 0x7fffffff, 0};           // lo_max, hi_min, lo_min, hi_max
             for (int r0 = warp; r0 < ns * kTile; r0 += QA * kWarps) {
                 float v[QA][NB];
                 float2 stat[QA];
@@ -242,12 +243,12 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                     const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
                     if (lane == 0) {
                         rows[r] = Row{factor(a.qscale * __uint_as_float((uint32_t)(127 + ex) << 23)), on ? -stat[i].x : 0.f, on ? stat[i].y : 0.f, on ? lo[i] : 0, on ? hi[i] : 0, {}};
-                        if (on) {
-                            atomicMax(&s_ext[0], lo[i]);
-                            atomicMin(&s_ext[1], hi[i]);
-                            atomicMin(&s_ext[2], lo[i]);
-                            atomicMax(&s_ext[3], hi[i]);
-                        }
+                    }
+                    if (on) {
+                        ext[0] = max(ext[0], lo[i]);
+                        ext[1] = min(ext[1], hi[i]);
+                        ext[2] = min(ext[2], lo[i]);
+                        ext[3] = max(ext[3], hi[i]);
                     }
                     const int wi = lane & 7, jj = lane >> 3;
                     uint8_t* tile = qs + (size_t)(r / kTile) * TILE + (4 * (r % kTile) + jj) * 8 + ((wi & 3) >> 1) * 4 + (wi & 1) * 2;
@@ -261,8 +262,16 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                     }
                 }
             }
+            if (lane < 4) s_ext[warp][lane] = lane == 0 ? ext[0] : lane == 1 ? ext[1] : lane == 2 ? ext[2] : ext[3];
             __syncthreads();
-            const int lo_max = s_ext[0], hi_min = s_ext[1], lo_min = s_ext[2], hi_max = s_ext[3];
+            int lo_max = 0, hi_min = 0x7fffffff, lo_min = 0x7fffffff, hi_max = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                lo_max = max(lo_max, s_ext[w][0]);
+                hi_min = min(hi_min, s_ext[w][1]);
+                lo_min = min(lo_min, s_ext[w][2]);
+                hi_max = max(hi_max, s_ext[w][3]);
+            }
             // ---- its cells, warp by warp; the next stage's scores are on their way
             auto old_of = [&](int stage, int c) {
                 float v = 0.f;
