@@ -129,14 +129,16 @@ __device__ __forceinline__ void put_angle(float2* cs_of, float2 f, int pos, int 
     cs_of[(pr % grp) * (half / grp) + pr / grp] = make_float2(cs, sn);
 }
 
-// A row's given positions, all -1 (and the error word set) where one is out of range
-__device__ __forceinline__ void given_positions(const AppendArgs& a, int row, int (&at)[kMaxAxes]) {
+// A row's given positions (asked for before its place is known: the two chains of loads overlap)
+__device__ __forceinline__ void load_positions(const AppendArgs& a, int row, int (&at)[kMaxAxes]) {
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; ++x) at[x] = x < a.n_axes ? a.positions[(long long)row * a.n_axes + x] : 0;
+}
+// All -1, and the error word set, where one is out of range
+__device__ __forceinline__ void check_positions(const AppendArgs& a, int (&at)[kMaxAxes]) {
     bool ok = true;
 #pragma unroll
-    for (int x = 0; x < kMaxAxes; ++x) {
-        at[x] = x < a.n_axes ? a.positions[(long long)row * a.n_axes + x] : 0;
-        ok = ok && at[x] >= 0 && at[x] < kMaxPosition;
-    }
+    for (int x = 0; x < kMaxAxes; ++x) ok = ok && at[x] >= 0 && at[x] < kMaxPosition;
     if (ok) return;
     atomicExch(a.g.err, kErrCounter);
 #pragma unroll
@@ -350,12 +352,14 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
     wait_for_earlier();
     let_next_start();
     if (warp == 0) {
-        const int row = row0 + lane, i = entry_of_rows<kTT>(a.r, row0, lane);
+        const int row = row0 + lane;
+        [[maybe_unused]] int at[kMaxAxes] = {};
+        if (MORE && a.positions && lane < TT && row < a.r.rows) load_positions(a, row, at);
+        const int i = entry_of_rows<kTT>(a.r, row0, lane);
         Place p{-1, -1, 0, 0, 0};
         if (lane < TT && row < a.r.rows) p = place_in(a.g, a.r, row, i, true);
         if (MORE && a.positions && p.pos >= 0) {
-            int at[kMaxAxes];
-            given_positions(a, row, at);
+            check_positions(a, at);
             if (at[0] < 0) p = Place{-1, -2, 0, 0, 0};
 #pragma unroll
             for (int x = 0; x < kMaxAxes; ++x) s_at[lane][x] = at[x];
@@ -541,7 +545,10 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
     wait_for_earlier();
     let_next_start();
     if (warp == 0) {
-        const int row = row0 + lane, i = entry_of_rows<W>(a.r, row0, lane);
+        const int row = row0 + lane;
+        [[maybe_unused]] int at[kMaxAxes] = {};
+        if (MORE && a.positions && lane < W && row < a.r.rows) load_positions(a, row, at);
+        const int i = entry_of_rows<W>(a.r, row0, lane);
         if (lane < W) {
             Place p{-1, -1, 0, 0, 0};
             if (row < a.r.rows) p = place_in(a.g, a.r, row, i, true);
@@ -549,8 +556,7 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
             s_place[lane] = p;
             s_from[lane] = from < RT ? from : -1;    // (below 0: the CTA before has it)
             if (MORE && a.positions && from >= 0 && from < RT) {
-                int at[kMaxAxes];
-                given_positions(a, row, at);
+                check_positions(a, at);
 #pragma unroll
                 for (int x = 0; x < kMaxAxes; ++x) s_at[lane][x] = at[x];
             }
