@@ -561,7 +561,7 @@ kvq_status kvq_paged_set_scores(kvq_paged* cache, float* scores);
  * (its output is NaN) adds nothing.  Sums are f32 in a fixed order: two runs
  * give the same bits.  The pages of one call's sequences are their own: a page
  * in two tables of the call is written by both.  Rows of bad pages are left
- * out.  out must not be q.  Needs a buffer (kvq_paged_set_scores). */
+ * out.  out must not overlap q.  Needs a buffer (kvq_paged_set_scores). */
 kvq_status kvq_paged_decode_scored(kvq_paged* cache, const kvq_paged_query* a, float decay, void* stream);
 
 /* Choose the rows that stay.  rows: device int32 [n_seq][Hkv][keep] receives for

@@ -43,6 +43,7 @@ constexpr int kMaxRows = 1 << 24;      // rows of a sequence at most
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned16(const void* p) { return ((size_t)p & 15) == 0; }
+bool aligned4(const void* p) { return ((size_t)p & 3) == 0; }
 
 struct Layout {
     size_t cell, page, pool, bounds, plan, plan2, arrived, ml, o, ml2, o2, stats, keys, total, key_rows, keys2;
@@ -162,6 +163,7 @@ SplitArgs factors(const kvq_paged* c, const kvq_paged_query* q) {
 kvq_status check_evict(const kvq_paged* c, const int* tables, const int* lens, int n_seq, const int* rows, int keep) {
     if (!c) return fail(KVQ_EINVAL, "cache is NULL");
     if (!tables || !lens || !rows) return fail(KVQ_EINVAL, "tables, lens or rows is NULL");
+    if (!aligned4(tables) || !aligned4(lens) || !aligned4(rows)) return fail(KVQ_EINVAL, "tables, lens or rows is not aligned to its elements");
     if (n_seq < 1 || n_seq > c->cfg.max_seqs) return fail(KVQ_EINVAL, "n_seq=%d outside [1, max_seqs=%d]", n_seq, c->cfg.max_seqs);
     if (keep < 1 || keep > kMaxRows) return fail(KVQ_EINVAL, "keep=%d outside [1, 2^24]", keep);
     return KVQ_OK;
@@ -385,7 +387,7 @@ kvq_status kvq_paged_append_at(kvq_paged* c, const void* k, long long k_stride, 
                                const int* positions, void* stream) {
     if (!c) return fail(KVQ_EINVAL, "cache is NULL");
     if (!c->cfg.rope_dim) return fail(KVQ_EINVAL, "the cache rotates nothing (config.rope_dim): positions have no use");
-    if (!positions && rows != 0) return fail(KVQ_EINVAL, "positions is NULL");
+    if ((!positions && rows != 0) || !aligned4(positions)) return fail(KVQ_EINVAL, "positions is NULL or not aligned to its elements");
     return append(c, k, k_stride, v, v_stride, q, q_stride, q_out, n_q_heads, dtype, tables, lens, n_seq, T, starts, rows,
                   positions, stream);
 }
@@ -495,8 +497,10 @@ kvq_status kvq_paged_decode_scored(kvq_paged* c, const kvq_paged_query* q, float
     if (st != KVQ_OK) return st;
     if (!c->row_scores) return fail(KVQ_EINVAL, "the cache keeps no row scores (kvq_paged_set_scores)");
     if (!(decay >= 0.f && decay <= 1.f)) return fail(KVQ_EINVAL, "decay must be in [0, 1]");
-    // (out may be q: the weights are worked out from the queries afterwards)
-    if (q->out == q->q) return fail(KVQ_EINVAL, "out must not be q");
+    // (the weights are worked out from the queries when the outputs are written)
+    const size_t bytes = (size_t)q->n_seq * q->T * q->n_q_heads * c->cfg.head_dim * (q->dtype == KVQ_BF16 ? 2 : 4);
+    if (q->out && (size_t)q->out < (size_t)q->q + bytes && (size_t)q->q < (size_t)q->out + bytes)
+        return fail(KVQ_EINVAL, "out must not overlap q");
     ScoredArgs a = {};
     a.stats = reinterpret_cast<float2*>(c->ws + c->off_stats);
     st = decode(c, q, nullptr, nullptr, 0, nullptr, 0, const_cast<float2*>(a.stats), stream);
@@ -548,12 +552,11 @@ kvq_status kvq_paged_compact(kvq_paged* c, const int* tables, const int* lens, i
     kvq_status st = check_evict(c, tables, lens, n_seq, rows, keep);
     if (st != KVQ_OK) return st;
     if (!lens_out) return fail(KVQ_EINVAL, "lens_out is NULL");
+    if (!aligned4(lens_out) || !aligned4(tables_out)) return fail(KVQ_EINVAL, "lens_out or tables_out is not aligned to its elements");
     if (tables_out == tables) return fail(KVQ_EINVAL, "tables_out must be NULL (in place) or hold other pages than tables");
     // (a sequence holds no more)
     const int most = std::min(keep, c->cfg.max_pages * c->cfg.page_rows);
     if (c->cfg.bounds && (long long)n_seq * most * c->cfg.n_kv_heads > (1LL << 31))
-        return fail(KVQ_ERANGE, "n_seq * keep too large for one call");
-    if ((long long)n_seq * c->cfg.n_kv_heads * (most / 128 + 1) > 0x7fffffffLL)     // (a block for 128 rows at least)
         return fail(KVQ_ERANGE, "n_seq * keep too large for one call");
     CompactArgs a = {};
     a.g = c->g;

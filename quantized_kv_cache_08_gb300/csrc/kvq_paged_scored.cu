@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                         constexpr int TB = decltype(tb)::value;
                         const uint8_t* tile = qs + (size_t)s * TILE + lane * 8;
                         float sc[TB][kPair][4] = {};               // (g, 2 j), (g, 2 j + 1), (g + 8, 2 j), (g + 8, 2 j + 1)
+                        [[maybe_unused]] float lows[F8 && F32Q ? TB : 1][kPair][4] = {};
 #pragma unroll 1                                           // (unrolled, its loads take more registers than there are)
                         for (int bp = 0; bp < NB / 2; ++bp) {
                             [[maybe_unused]] uint4 k0[kPair], k1[kPair], ks[kPair];      // ks: d of rows 2 (g / 2) + s and + 8, blocks 2 bp and 2 bp + 1
@@ -336,14 +337,25 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                                     }
 #pragma unroll
                                     for (int u = 0; u < TB; ++u) {
-                                        float acc[4];
-                                        float (&to)[4] = F8 ? sc[u][x] : acc;
-                                        if constexpr (F8) mma_f16(to, p, b0[u].x, b0[u].y);
-                                        else mma_f16_new(to, p, b0[u].x, b0[u].y, zero);
-                                        mma_f16(to, q, b1[u].x, b1[u].y);
-                                        if constexpr (F32Q) {
-                                            mma_f16(to, p, l0[u].x, l0[u].y);
-                                            mma_f16(to, q, l1[u].x, l1[u].y);
+                                        // (the low parts' sums apart until the end, as the decode has them: the same numbers)
+                                        [[maybe_unused]] float acc[4];
+                                        if constexpr (F8) {
+                                            mma_f16(sc[u][x], p, b0[u].x, b0[u].y);
+                                            mma_f16(sc[u][x], q, b1[u].x, b1[u].y);
+                                            if constexpr (F32Q) {
+                                                mma_f16(lows[u][x], p, l0[u].x, l0[u].y);
+                                                mma_f16(lows[u][x], q, l1[u].x, l1[u].y);
+                                            }
+                                        } else {
+                                            mma_f16_new(acc, p, b0[u].x, b0[u].y, zero);
+                                            mma_f16(acc, q, b1[u].x, b1[u].y);
+                                            if constexpr (F32Q) {
+                                                float low[4];
+                                                mma_f16_new(low, p, l0[u].x, l0[u].y, zero);
+                                                mma_f16(low, q, l1[u].x, l1[u].y);
+#pragma unroll
+                                                for (int i = 0; i < 4; ++i) acc[i] += low[i];
+                                            }
                                         }
                                         if constexpr (!F8) {
                                             sc[u][x][0] = fmaf(acc[0], d.x, sc[u][x][0]);
@@ -355,6 +367,14 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                                 }
                             }
                         }
+                        if constexpr (F8 && F32Q) {
+#pragma unroll
+                            for (int u = 0; u < TB; ++u)
+#pragma unroll
+                                for (int x = 0; x < kPair; ++x)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) sc[u][x][i] += lows[u][x][i];
+                        }
 #pragma unroll
                         for (int u = 0; u < TB; ++u) {
                             const Row* w = rows + (s + u) * kTile + 2 * j;
@@ -365,9 +385,11 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                                 for (int x = 0; x < kPair; ++x)
 #pragma unroll
                                     for (int r = 0; r < 2; ++r) {
-                                        float v = fmaf(sc[u][x][2 * r + i], f.x, f.y);
-                                        if (a.softcap_b > 0.f) v = fmaf(a.softcap_b, tanhf(a.softcap_a * (sc[u][x][2 * r + i] * f.x)), f.y);
-                                        float p = ex2(v);
+                                        // (rounded before the reference is taken off, as in the decode: at scores of
+                                        // thousands one rounding less would be another number than its sums hold)
+                                        float v = __fmul_rn(sc[u][x][2 * r + i], f.x);
+                                        if (a.softcap_b > 0.f) v = __fmul_rn(a.softcap_b, tanhf(a.softcap_a * v));
+                                        float p = ex2(__fadd_rn(v, f.y));
                                         if (edge) {
                                             const int at_row = row0 + 16 * x + g + 8 * r;
                                             if (at_row < w[i].lo || at_row >= w[i].hi) p = 0.f;

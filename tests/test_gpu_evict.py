@@ -122,25 +122,42 @@ def test_weights_add_up_and_repeat():
     assert ((c.scores - 2 * got[0]).abs() <= 2.0 ** -23 * c.scores).all()
 
 
-def test_appended_rows_start_at_zero():
-    for fmt in (Q8, F8):
-        for counts in ([1, 1, 1], [40, 0, 23]):
-            p = PagedPair(3, 2, 128, 4, page=16, max_pages=4, fmt=fmt, scores=True)
-            p.append([5, 7, 0])
-            p.dev.scores.fill_(3.0)
-            old = [len(x) for x in p.k]
-            if counts[0] == 1:
-                k = p.randn(3, 1, 2, 128)
-                for b in range(3):
-                    p.note(b, k[b].numpy(), k[b].numpy())
-                p.dev.append(k.cuda(), k.cuda(), p.tables, p.lens())
-            else:
-                p.append(counts)
-            want = torch.full(p.dev.scores.shape, 3.0)
-            for b in range(3):
-                for r in range(old[b], len(p.k[b])):
-                    want[p.tab[b, r // 16], :, r % 16] = 0.0
-            assert torch.equal(p.dev.scores.cpu(), want)
+@pytest.mark.parametrize("bounds", [False, True])
+@pytest.mark.parametrize("fmt", [Q8, F8])
+@pytest.mark.parametrize("counts", [[1, 1, 1], [40, 0, 23]])
+def test_appended_rows_start_at_zero(fmt, counts, bounds):
+    p = PagedPair(3, 2, 128, 4, page=16, max_pages=4, fmt=fmt, scores=True, bounds=bounds)
+    p.append([5, 7, 0])
+    p.dev.scores.fill_(3.0)
+    old = [len(x) for x in p.k]
+    if counts[0] == 1:                                  # a row each, without starts
+        k = p.randn(3, 1, 2, 128)
+        for b in range(3):
+            p.note(b, k[b].numpy(), k[b].numpy())
+        p.dev.append(k.cuda(), k.cuda(), p.tables, p.lens())
+    else:
+        p.append(counts)
+    want = torch.full(p.dev.scores.shape, 3.0)
+    for b in range(3):
+        for r in range(old[b], len(p.k[b])):
+            want[p.tab[b, r // 16], :, r % 16] = 0.0
+    assert torch.equal(p.dev.scores.cpu(), want)
+    assert np.array_equal(p.dev.pool.cpu().numpy(), p.expected_pool())
+
+
+@pytest.mark.parametrize("fmt", [Q8, F8])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("scale", [1e2, 1e4, 1e6, 1e12])
+def test_weights_of_large_scores_add_up(fmt, dtype, scale):
+    """Scores of thousands and more: their steps in f32 are no small change of a weight any more, but weights are
+    worked out from the same numbers as the softmax's sum, so that they add up to 1 a query: 2^-21 for the sum of 300 f32
+    numbers either way, as much again for the product."""
+    p = PagedPair(2, 2, 128, 8, page=16, max_pages=20, fmt=fmt, scores=True)
+    p.append([300, 33])
+    out = p.dev.decode_scored(p.randn(2, 1, 8, 128, dtype=dtype).cuda(), p.tables, p.lens(), scale=scale)
+    assert torch.isfinite(out).all()
+    for b in range(2):
+        assert np.abs(scores_of(p, b).astype(np.float64).sum(0) - 4).max() <= 4 * 2.0 ** -19
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
@@ -541,6 +558,10 @@ def test_refusals():
     buf = torch.zeros(p.n_pages, 2, 16, device="cuda")
     with pytest.raises(B.KvqError):
         B.kvq_paged_set_scores(p.dev.handle, buf.data_ptr() + 4)
+    for off in ((2, 0, 0, 0, 0), (0, 1, 0, 0, 0), (0, 0, 2, 0, 0), (0, 0, 0, 3, 0), (0, 0, 0, 0, 2)):      # not on their elements
+        at = [x.data_ptr() + o for x, o in zip((p.tables, lens, rows, p.tables.clone(), lens.clone()), off)]
+        with pytest.raises(B.KvqError):
+            B.kvq_paged_compact(p.dev.handle, at[0], at[1], 2, at[2], 2, at[3], at[4])
     B.kvq_paged_set_scores(p.dev.handle, buf.data_ptr())
     for bad in (dict(decay=-0.1), dict(decay=1.5), dict(decay=float("nan")), dict(out=q), dict(softcap=-1.0), dict(window=-1)):
         with pytest.raises((ValueError, B.KvqError)):

@@ -152,6 +152,9 @@ def test_refusals():
     with pytest.raises(B.KvqError):
         B.kvq_paged_append_at(c.handle, k.data_ptr(), 64, k.data_ptr(), 64, None, 0, None, 0, 0, tab.data_ptr(), lens.data_ptr(), 1, 2,
                               None, 2, None)
+    with pytest.raises(B.KvqError):                                            # not on its elements
+        B.kvq_paged_append_at(c.handle, k.data_ptr(), 64, k.data_ptr(), 64, None, 0, None, 0, 0, tab.data_ptr(), lens.data_ptr(), 1, 2,
+                              None, 2, tab.data_ptr() + 2)
     for axis, n in (([0] * 16, 0), ([0] * 16, 5), (None, 1), ([2] * 16, 2)):
         with pytest.raises(B.KvqError):
             B.kvq_paged_set_axes(c.handle, axis, n)
