@@ -525,8 +525,6 @@ def verify(target, draft, tokens, uniform, lens=None, accept=None, next_tokens=N
         return t.data_ptr()
 
     def make():
-        if stream is None:
-            return tokens.new_empty(n)
         with torch.cuda.stream(stream):
             t = tokens.new_empty(n)
         t.record_stream(torch.cuda.current_stream(target.device))
@@ -536,10 +534,10 @@ def verify(target, draft, tokens, uniform, lens=None, accept=None, next_tokens=N
     np_ = counts(next_tokens, "next_tokens") if next_tokens is not None else None
     lp = counts(lens, "lens") if lens is not None else None
     if accept is None:
-        accept = make()
+        accept = tokens.new_empty(n) if stream is None else make()
         ap = accept.data_ptr()
     if next_tokens is None:
-        next_tokens = make()
+        next_tokens = tokens.new_empty(n) if stream is None else make()
         np_ = next_tokens.data_ptr()
     a = ctypes.byref(B.kvq_verify_args(target.data_ptr(), dp, tokens.data_ptr(), uniform.data_ptr(), code, n, T, V, ts, tr, ds,
                                        dr, ap, np_, lp))
