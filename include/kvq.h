@@ -458,7 +458,9 @@ kvq_status kvq_paged_append(kvq_paged* cache, const void* k, long long k_stride,
  * several axes (time, height, width).  positions: device int32 [rows][n_axes],
  * each in [0, 2^24); pair i of a head turns by positions[row][axis of pair i]
  * times its frequency.  A row with a position outside sets the error word and
- * is skipped, its query too.  Rows are placed, and everything else is done, as by
+ * is skipped, its query too.  Angles are worked out to nearly the last bits of
+ * f32 at any position (kvq_paged_append's to 2^-24 of a turn: the two may differ
+ * in a code here and there).  Rows are placed, and everything else is done, as by
  * kvq_paged_append.  Needs rope_dim > 0. */
 kvq_status kvq_paged_append_at(kvq_paged* cache, const void* k, long long k_stride, const void* v, long long v_stride,
                                const void* q, long long q_stride, void* q_out, int n_q_heads, kvq_dtype dtype,

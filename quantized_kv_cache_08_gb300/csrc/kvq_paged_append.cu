@@ -16,7 +16,8 @@
 // drop out exactly, and the rest is added: the angle is good to 2^-24 of a turn
 // at any position below 2^24, where p f in one fp32 product would be off by
 // p 2^-24 radians.  Positions are a row's index in its sequence, or given for each
-// row on up to four axes, of which each pair of elements has one.
+// row on up to four axes, of which each pair of elements has one; those angles are worked out
+// further (put_angle_at; 8k rows 54.9 us in all, by index 50.7).
 #include "kvq_paged.cuh"
 #include "kvq_quant.cuh"
 
@@ -150,6 +151,54 @@ __device__ __forceinline__ void clear_scores(const AppendArgs& a, const Place& p
     const int in = p.pos & (a.g.page_rows - 1);
     const long long page = (p.cell - (long long)(in >> 4) * a.g.cell_bytes) / a.g.page_bytes;
     for (; h < a.g.Hkv; h += step) a.row_scores[(page * a.g.Hkv + h) * a.g.page_rows + in] = 0.f;
+}
+
+// The same for a given position, to nearly the last bit of f32: E4M3 codes lie so far
+// apart that whatever an angle is off moves some of them over a border.  The rounding
+// errors of products and sums are carried along, so that the turn is off by no more
+// than its frequency leaves out; from the nearest quarter the angle z = zh + zl is
+// within pi / 4, where in
+//   sin z = zh + (zl + zh^3 S(zh^2)), cos z = 1 - zh^2 / 2 + (zh^4 C(zh^2) - zh zl)
+// (S and C by their Taylor series) the terms in brackets are small: 0.6 of a last bit.
+// Some 50 operations a pair.
+__device__ __forceinline__ void put_angle_at(float2* cs_of, float2 f, int pos, int pr, int half, int interleaved) {
+    const float p = (float)max(pos, 0);
+    const float t = __fmul_rn(p, f.x), e = __fmaf_rn(p, f.x, -t);               // p f.x = t + e
+    const float m = __fmul_rn(p, f.y), ml = __fmaf_rn(p, f.y, -m);              // p f.y = m + ml
+    float s = __fadd_rn(e, m), b = __fadd_rn(s, -e);
+    const float sl = __fadd_rn(__fadd_rn(e, -__fadd_rn(s, -b)), __fadd_rn(m, -b));      // e + m = s + sl
+    s = __fadd_rn(s, -rintf(s));
+    const float a = __fadd_rn(t, -rintf(t));
+    float h = __fadd_rn(a, s);
+    b = __fadd_rn(h, -a);
+    const float hl = __fadd_rn(__fadd_rn(a, -__fadd_rn(h, -b)), __fadd_rn(s, -b));      // a + s = h + hl
+    const float lo = __fadd_rn(hl, __fadd_rn(sl, ml));
+    const float q = rintf(4.f * h);                                             // quarters
+    const int k = (int)q;
+    h = __fmaf_rn(q, -0.25f, h);                                                // (exact)
+    const float two_pi = 6.28318548f, rest = -1.74845553e-7f;                   // 2 pi as a sum of two floats
+    const float zh = __fmul_rn(h, two_pi);
+    const float zl = __fadd_rn(__fmaf_rn(h, two_pi, -zh), __fmaf_rn(h, rest, __fmul_rn(lo, two_pi)));
+    const float z2 = __fmul_rn(zh, zh);
+    float S = -2.50521084e-8f;                                                  // -1 / 11!, 1 / 9! ..
+    S = __fmaf_rn(S, z2, 2.75573192e-6f);
+    S = __fmaf_rn(S, z2, -1.98412698e-4f);
+    S = __fmaf_rn(S, z2, 8.33333333e-3f);
+    S = __fmaf_rn(S, z2, -1.66666667e-1f);
+    const float sn = __fadd_rn(zh, __fmaf_rn(__fmul_rn(z2, zh), S, zl));
+    float C = 2.08767570e-9f;                                                   // 1 / 12!, -1 / 10! ..
+    C = __fmaf_rn(C, z2, -2.75573192e-7f);
+    C = __fmaf_rn(C, z2, 2.48015873e-5f);
+    C = __fmaf_rn(C, z2, -1.38888889e-3f);
+    C = __fmaf_rn(C, z2, 4.16666667e-2f);
+    const float hz = __fmul_rn(0.5f, z2), w = __fadd_rn(1.f, -hz);
+    const float left = __fadd_rn(__fadd_rn(__fadd_rn(1.f, -w), -hz), __fmul_rn(-0.5f, __fmaf_rn(zh, zh, -z2)));      // what w leaves of 1 - zh^2 / 2
+    const float cs = __fadd_rn(w, __fadd_rn(left, __fmaf_rn(__fmul_rn(z2, z2), C, -__fmul_rn(zh, zl))));
+    float c = k & 1 ? sn : cs, n = k & 1 ? cs : sn;
+    if ((k + 1) & 2) c = -c;
+    if (k & 2) n = -n;
+    const int grp = interleaved ? 4 : 8;
+    cs_of[(pr % grp) * (half / grp) + pr / grp] = make_float2(c, n);
 }
 
 // Rotate elements e0 .. e0 + 7 (x) below rot of a head row; y: those that the half-split rotation pairs them with
@@ -370,7 +419,11 @@ __global__ void __launch_bounds__(kThreads, BOUNDS ? 2 : BF16 ? 4 : 3) append_ke
     // (an indexed read of the frequencies takes a step for each lane: one a thread)
     for (int pr = tid % (kThreads / TT); pr < half; pr += kThreads / TT) {
         const int tt = tid / (kThreads / TT);
-        put_angle(s_cs + tt * half, fq.f[pr], MORE && a.positions && s_place[tt].pos >= 0 ? s_at[tt][fq.axis[pr]] : s_place[tt].pos, pr, half, a.interleaved);
+        if (MORE && a.positions) {
+            if (s_place[tt].pos >= 0) put_angle_at(s_cs + tt * half, fq.f[pr], s_at[tt][fq.axis[pr]], pr, half, a.interleaved);
+        } else {
+            put_angle(s_cs + tt * half, fq.f[pr], s_place[tt].pos, pr, half, a.interleaved);
+        }
     }
     __syncthreads();
     // a warp's token, and its share of the token's units
@@ -570,8 +623,10 @@ __global__ void __launch_bounds__(kCellThreads, BF16 ? 5 : 4) append_cells_kerne
         const float2 f = fq.f[pr];
         const int axis = MORE && a.positions ? fq.axis[pr] : 0;
         for (int tt = tid / kSlots; tt < W; tt += kCellThreads / kSlots)
-            if (s_from[tt] >= 0)
-                put_angle(s_cs + tt * stride_cs, f, MORE && a.positions ? s_at[tt][axis] : s_place[tt].pos, pr, half, a.interleaved);
+            if (s_from[tt] >= 0) {
+                if (MORE && a.positions) put_angle_at(s_cs + tt * stride_cs, f, s_at[tt][axis], pr, half, a.interleaved);
+                else put_angle(s_cs + tt * stride_cs, f, s_place[tt].pos, pr, half, a.interleaved);
+            }
     }
     const int per = a.g.Hkv * (NB / BL);             // tasks of a piece and kind
     const int li = lane / BL, bl = lane % BL;        // row of the piece, block of the four

@@ -20,6 +20,12 @@
 // In place a cluster takes one (sequence, KV head), a window of cells at a time:
 // rows only move to lower places, so what a later window reads lies behind what
 // this one writes, and the only wait is between a window's loads and its stores.
+//
+// Measured.  Choosing: 131072 rows of 8 KV heads 20 us (4 MB: some 2 us each for the
+// load, a digit's counts and their exchange, twice, the masks and the writing), 4608 rows
+// 8, 32 sequences of up to 16384 22.  Moving: those 32 to 2000 rows each 70 us, for 291 MB
+// of sectors read (a row in five stays, in sectors that it shares with others) and 115
+// written, 0.88 of the copy rate; 131072 rows of E4M3 heads of 64 to 16384 18.7, in place 29; 4608 to 4096 4.8 and 9.
 #include "kvq_cluster.cuh"
 #include "kvq_paged.cuh"
 

@@ -20,6 +20,13 @@
 // (f32 ones as two fp16 parts), and what does not fit is another pass over
 // the range's keys, which then come from L2.  A row's score is one lane's alone and its
 // gains are added in the tiles' order: the same bits on every run.
+//
+// Measured: 64 sequences of 1024 to 16384 rows, 32 query and 8 KV heads of 128, 108 us
+// (keys and scores take 102 at the copy rate) behind the decode's 190; one of 512 rows
+// 5; the last 8 rows of 4 sequences in a window of 16384, f32, E4M3, 64 query and 8 KV heads
+// of 64: 39, bound by the products of 64 queries in two parts (a tile of 8 at a time: 62).
+// Keys loaded straight into registers, a cell ahead, took 304 for the first: what
+// was loaded ahead spilled, and a spill waits for its load.
 #include "kvq_paged.cuh"
 #include "kvq_paged_work.cuh"
 

@@ -15,6 +15,12 @@
 // running sum passes goes down into it: a warp's stretch is cut over all warps until
 // 2048 elements are left, eight a thread at most, whose running sums end it.  One row
 // of p and q is read of T; the parts read again come from L2.
+//
+// Measured: 64 sequences of 8 rows of 131072 tokens, f32, 17 us where the 67 MB take
+// 10: 2.7 us until the row is known (two dependent loads), 8 of reading, then the
+// slowest block of each cluster, its barrier and the last step, 1 each.  One
+// sequence of 32000 tokens 5 us.  With sums by the exponent's shifts the integer pipe was the bound (21 us); loads
+// of the next turn ahead of the sums cost registers and so blocks an SM (26 us).
 #include "../../include/kvq.h"
 #include "kvq_cluster.cuh"
 #include "kvq_error.h"

@@ -1,6 +1,9 @@
 """Row scores, the rows that stay and their move, on the GPU against the oracle:
 weights within what the decode's arithmetic leaves, choices and bytes exactly."""
 
+import re
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -518,6 +521,61 @@ def test_captured_steps_follow_the_lengths():
     (a, pa, sa), (b, pb, sb) = got
     assert [x[0] for x in a] == [x[0] for x in b] and all(torch.equal(x[1], y[1]) for x, y in zip(a, b))
     assert torch.equal(pa, pb) and torch.equal(sa, sb) and a[-1][0][0] == keep
+
+
+def test_the_documented_round():
+    need_gpu()
+    text = (Path(__file__).resolve().parents[1] / "README.md").read_text()
+    code = next(x for x in re.findall(r"```python\n(.*?)```", text, re.S) if "decode_scored" in x)
+    names = {"torch": torch}
+    exec(code, names)
+    assert names["out"].shape == (2, 4, 32, 128) and torch.isfinite(names["out"]).all()
+    assert names["lens"].tolist() == [512, 512] and names["c"].device_error() == 0
+    assert all(1 <= x <= 4 for x in names["accept"].tolist()) and all(0 <= x < 1000 for x in names["token"].tolist())
+
+
+def test_two_caches_on_two_streams():
+    """Whole steps of two caches at once on streams of their own give what they give one after the other."""
+    need_gpu()
+    n, Hkv, D, page, mp, keep = 4, 2, 64, 16, 32, 200
+
+    def make(seed):
+        g = torch.Generator().manual_seed(seed)
+        c = PagedKVCache(n * mp, page, Hkv, D, 8, max_seqs=n, max_pages=mp, rope_dim=D, scores=True)
+        c.pool.zero_()
+        tab = torch.randperm(n * mp, generator=g).view(n, mp).int().cuda()
+        k, q = torch.randn(n, 400, Hkv, D, generator=g).cuda(), torch.randn(n, 1, 8, D, generator=g).cuda()
+        p = torch.softmax(torch.randn(n, 3, 5000, generator=g), -1).cuda()
+        tok = torch.randint(0, 5000, (n, 2), generator=g).int().cuda()
+        return c, tab, k, q, p, tok, torch.rand(n, 3, generator=g).cuda(), torch.arange(400).int().cuda().expand(n, 400).contiguous()
+
+    def step(s, stream):
+        c, tab, k, q, p, tok, u, at = s
+        lens = i32([400] * n)
+        stream.wait_stream(torch.cuda.current_stream())
+        c.append(k, k, tab, lens, positions=at, stream=stream)
+        for _ in range(8):
+            out = c.decode_scored(q, tab, lens, stream=stream)
+            verify(p, p[:, :2], tok, u, stream=stream)
+        rows = c.select_rows(tab, lens, keep, n_first=2, n_last=20, stream=stream)
+        new = c.compact(tab, lens, rows, stream=stream)
+        a, t = verify(p, p[:, :2], tok, u, lens=new, stream=stream)
+        return out, rows, new, a, t, lens
+
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    ref = []
+    for seed in (1, 2):
+        s = make(seed)
+        r = step(s, one)
+        torch.cuda.synchronize()
+        ref.append([x.clone() for x in r] + [s[0].pool.clone(), s[0].scores.clone()])
+    both = [make(1), make(2)]
+    torch.cuda.synchronize()
+    got = [step(both[0], one), step(both[1], two)]
+    torch.cuda.synchronize()
+    for s, r, w in zip(both, got, ref):
+        for x, y in zip(list(r) + [s[0].pool, s[0].scores], w):
+            assert torch.equal(x, y)
 
 
 def test_on_another_stream():
