@@ -566,6 +566,14 @@ kvq_status kvq_paged_set_scores(kvq_paged* cache, float* scores);
  * out.  out must not overlap q.  Needs a buffer (kvq_paged_set_scores). */
 kvq_status kvq_paged_decode_scored(kvq_paged* cache, const kvq_paged_query* a, float decay, void* stream);
 
+/* Room for a scored decode's scores: device f32 [n_pages][Hkv][page_rows][queries],
+ * 16-byte aligned, queries in [1, 8], kept until another (or NULL: none) takes its
+ * place.  With it, calls of at most `queries` queries a KV head (n_q_heads / Hkv * T)
+ * whose scores are fewer bytes than the keys keep them in the first pass, where
+ * the second pass else works them out again from the keys: the same scores, at
+ * half the extra time.  Its contents are the library's.  Enqueues nothing. */
+kvq_status kvq_paged_set_score_scratch(kvq_paged* cache, float* scratch, int queries);
+
 /* Choose the rows that stay.  rows: device int32 [n_seq][Hkv][keep] receives for
  * each sequence and KV head, ascending, the first n_first and last n_last rows
  * below the length and the best scored of the others, ties to the lower index

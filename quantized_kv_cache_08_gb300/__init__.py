@@ -21,7 +21,7 @@ from ._binding import (  # noqa: F401
     kvq_note_replayed, kvq_paged_alloc, kvq_paged_append, kvq_paged_append_at, kvq_paged_bounds, kvq_paged_compact,
     kvq_paged_decode, kvq_paged_decode_scored, kvq_paged_decode_shared, kvq_paged_decode_sparse, kvq_paged_free,
     kvq_paged_query, kvq_paged_read, kvq_paged_read_error, kvq_paged_required_bytes, kvq_paged_select,
-    kvq_paged_select_rows, kvq_paged_set_axes, kvq_paged_set_scores, kvq_physical_rows, kvq_read_device_error,
+    kvq_paged_select_rows, kvq_paged_set_axes, kvq_paged_set_score_scratch, kvq_paged_set_scores, kvq_physical_rows, kvq_read_device_error,
     kvq_required_bytes,
     kvq_ring_headroom, kvq_set_decode_path, kvq_set_softcap, kvq_set_split_rows, kvq_sync_len, kvq_truncate,
     kvq_truncate_device, kvq_verify, kvq_verify_args, lib,

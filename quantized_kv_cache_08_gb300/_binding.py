@@ -30,7 +30,8 @@ EXPORTS = (
     "kvq_set_softcap",
     "kvq_paged_required_bytes", "kvq_paged_alloc", "kvq_paged_free", "kvq_paged_append", "kvq_paged_read",
     "kvq_paged_bounds", "kvq_paged_decode", "kvq_paged_decode_shared", "kvq_paged_select", "kvq_paged_decode_sparse",
-    "kvq_paged_read_error", "kvq_paged_append_at", "kvq_paged_set_axes", "kvq_paged_set_scores", "kvq_paged_decode_scored",
+    "kvq_paged_read_error", "kvq_paged_append_at", "kvq_paged_set_axes", "kvq_paged_set_scores", "kvq_paged_set_score_scratch",
+    "kvq_paged_decode_scored",
     "kvq_paged_select_rows", "kvq_paged_compact", "kvq_verify",
     "kvq_block_bytes", "kvq_bytes_per_token", "kvq_last_error",
 )
@@ -130,6 +131,7 @@ def lib():
             "kvq_paged_append_at": (I, [P, P, LL, P, LL, P, LL, P, I, I, P, P, I, I, P, I, P, P]),
             "kvq_paged_set_axes": (I, [P, IP, I]),
             "kvq_paged_set_scores": (I, [P, P]),
+            "kvq_paged_set_score_scratch": (I, [P, P, I]),
             "kvq_paged_decode_scored": (I, [P, QP, ctypes.c_float, P]),
             "kvq_paged_select_rows": (I, [P, P, P, I, I, I, I, P, P]),
             "kvq_paged_compact": (I, [P, P, P, I, P, I, P, P, P]),
@@ -321,6 +323,10 @@ def kvq_paged_set_axes(handle, axis, n_axes):
 
 def kvq_paged_set_scores(handle, scores):
     _check(lib().kvq_paged_set_scores(handle, scores))
+
+
+def kvq_paged_set_score_scratch(handle, scratch, queries):
+    _check(lib().kvq_paged_set_score_scratch(handle, scratch, queries))
 
 
 def kvq_paged_decode_scored(handle, query, decay, stream=0):

@@ -21,7 +21,7 @@ BUILD = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_decode.cu", "kvq_decode_stream.cu", "kvq_decode_stream_f8.cu",
            "kvq_paged_api.cu", "kvq_paged_append.cu", "kvq_paged_decode.cu", "kvq_paged_prefix.cu", "kvq_paged_select.cu",
-           "kvq_paged_scored.cu", "kvq_paged_evict.cu", "kvq_verify.cu"]
+           "kvq_paged_decode_kept.cu", "kvq_paged_scored.cu", "kvq_paged_evict.cu", "kvq_verify.cu"]
 
 
 def _nvcc() -> str:

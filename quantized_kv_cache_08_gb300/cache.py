@@ -205,11 +205,13 @@ class PagedKVCache:
     whose rows are given positions on several axes.  scores: keep an attention score per row and KV head in
     `scores` (float32 [n_pages, Hkv, page_rows], zeros at first; scores_buf takes over an existing
     tensor), which `decode_scored` adds to, `select_rows` goes by and `compact`
-    moves; appended rows start at 0."""
+    moves; appended rows start at 0.  score_scratch: room beside it for the scores of up to 8 queries a KV head
+    (as many as max_q_heads and max_t allow, 4 bytes a row and query), which spares decode_scored a second pass over the keys."""
 
     def __init__(self, n_pages, page_rows, n_kv_heads, head_dim, max_q_heads, max_seqs, max_pages, max_t=1,
                  fmt="q8_0/q5_1", rope_dim=0, rope_base=10000.0, rope_interleaved=False, rope_freq=None, bounds=False,
-                 pool=None, bounds_buf=None, device=None, stream=None, rope_axes=None, scores=False, scores_buf=None):
+                 pool=None, bounds_buf=None, device=None, stream=None, rope_axes=None, scores=False, scores_buf=None,
+                 score_scratch=True):
         self.handle = None
         self._lib = B.lib()
         if fmt not in KVCache.FORMATS:
@@ -232,7 +234,7 @@ class PagedKVCache:
         self.n_kv_heads, self.head_dim, self.max_pages = n_kv_heads, head_dim, max_pages
         self.pool = self._buffer(pool, sz.pool, "pool")
         self.bounds = self._buffer(bounds_buf, sz.bounds, "bounds_buf") if bounds else None
-        self.n_axes, self.scores = 1, None
+        self.n_axes, self.scores, self.scratch = 1, None, None
         if scores or scores_buf is not None:
             shape = (n_pages, n_kv_heads, page_rows)
             if scores_buf is None:
@@ -241,6 +243,9 @@ class PagedKVCache:
                     or not scores_buf.is_contiguous():
                 raise ValueError(f"scores_buf must be a contiguous float32 {list(shape)} tensor on {dev}")
             self.scores = scores_buf
+            queries = max_q_heads // n_kv_heads * max_t
+            if score_scratch and queries <= 8:
+                self.scratch = torch.empty(n_pages * n_kv_heads * page_rows * queries, dtype=torch.float32, device=dev)
         self.workspace = torch.empty(sz.workspace, dtype=torch.uint8, device=dev)
         if stream is not None:
             stream.wait_stream(torch.cuda.current_stream(dev))   # the workspace's memory may still be in use there
@@ -253,6 +258,8 @@ class PagedKVCache:
             B.kvq_paged_set_axes(self.handle, rope_axes, self.n_axes)
         if self.scores is not None:
             B.kvq_paged_set_scores(self.handle, self.scores.data_ptr())
+            if self.scratch is not None:
+                B.kvq_paged_set_score_scratch(self.handle, self.scratch.data_ptr(), queries)
 
     def __del__(self):
         h = getattr(self, "handle", None)

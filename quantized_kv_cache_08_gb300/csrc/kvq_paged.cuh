@@ -223,6 +223,8 @@ struct SplitArgs {
     int fuse;                      // 1: the last CTA of a key joins its records (no merge kernel)
     int* arrived;                  // [key] records written; 0 between calls
     float2* stats;                 // [n_seq][T][Hq] reference (log2 units) and weight of 2^(s - reference), or NULL
+    float* kept;                   // [n_pages][Hkv][cells][kept_q][16] scores, where they are kept (launch_split_kept)
+    int kept_q;                    // queries of a KV head in this call
     long long max_keys;            // keys that the record area holds beside the CTAs' own
     float* part_o;                 // [slot][rec_rows][D]
     float* part_ml;                // [slot][rec_rows][2]  (max in log2 units, sum)
@@ -245,6 +247,7 @@ struct PlanEntry {
 int split_tile(int NB, bool bf16, int most_queries);
 int split_warps(int NB, int tile);
 cudaError_t launch_split(const SplitArgs& a, cudaStream_t s);
+cudaError_t launch_split_kept(const SplitArgs& a, cudaStream_t s);        // (tile 8; kvq_paged_decode_kept.cu)
 cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s);
 // The weights of a decode's queries onto the row scores (kvq_paged_scored.cu)
 struct ScoredArgs {
@@ -258,10 +261,12 @@ struct ScoredArgs {
     float decay;
     const float2* stats;           // as in SplitArgs
     float* scores;                 // [n_pages][Hkv][page_rows]
+    const float* kept;             // as in SplitArgs, of at most 8 queries a KV head
     int slices;                    // query tiles in shared memory at a time
     int sms;
 };
-cudaError_t launch_scored(const ScoredArgs& a, cudaStream_t s);
+cudaError_t launch_scored(const ScoredArgs& a, cudaStream_t s);           // from the keys
+cudaError_t launch_gains(const ScoredArgs& a, cudaStream_t s);            // from the scores that the decode kept
 
 // Eviction (kvq_paged_evict.cu)
 struct RowsArgs {

@@ -20,7 +20,8 @@ struct kvq_paged {
     int8_t* codes;
     float* scales;
     float* row_scores;
-    int n_axes;
+    float* kept;
+    int kept_q, n_axes;
     Freqs freqs;
 };
 
@@ -170,7 +171,7 @@ kvq_status check_evict(const kvq_paged* c, const int* tables, const int* lens, i
 }
 
 kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start, const int* prefix_len, int n_groups,
-                  const int* lists, int keep, float2* stats, void* stream) {
+                  const int* lists, int keep, float2* stats, float* kept, void* stream) {
     kvq_status st = check_query(c, q);
     if (st != KVQ_OK) return st;
     if (!q->out || !aligned16(q->out)) return fail(KVQ_EINVAL, "out is NULL or not 16-byte aligned");
@@ -219,6 +220,8 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
     a.arrived = reinterpret_cast<int*>(c->ws + c->off_arrived);
     a.fuse = n_groups == 0;
     a.stats = stats;
+    a.kept = kept;
+    a.kept_q = own;
     a.part_ml = reinterpret_cast<float*>(c->ws + c->off_ml);
     a.part_o = reinterpret_cast<float*>(c->ws + c->off_o);
     a.tile_rows = prefix_rows_of(a.g.NB());
@@ -232,7 +235,7 @@ kvq_status decode(kvq_paged* c, const kvq_paged_query* q, const int* group_start
         e = launch_prefix(a, s);
         if (e != cudaSuccess) return cuda_fail(e, "paged decode prefix kernel");
     }
-    e = launch_split(a, s);
+    e = kept ? launch_split_kept(a, s) : launch_split(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode split kernel");
     if (!a.fuse) e = launch_merge(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode merge kernel");
@@ -367,6 +370,8 @@ kvq_status kvq_paged_alloc(const kvq_paged_config* cfg, void* pool, void* bounds
     c->freqs = f;
     c->n_axes = 1;
     c->row_scores = nullptr;
+    c->kept = nullptr;
+    c->kept_q = 0;
     *out = c;
     return KVQ_OK;
 }
@@ -431,7 +436,7 @@ kvq_status kvq_paged_bounds(kvq_paged* c, const int* tables, const int* lens, in
 }
 
 kvq_status kvq_paged_decode(kvq_paged* c, const kvq_paged_query* a, void* stream) {
-    return decode(c, a, nullptr, nullptr, 0, nullptr, 0, nullptr, stream);
+    return decode(c, a, nullptr, nullptr, 0, nullptr, 0, nullptr, nullptr, stream);
 }
 
 kvq_status kvq_paged_decode_shared(kvq_paged* c, const kvq_paged_query* a, const int* group_start,
@@ -440,7 +445,7 @@ kvq_status kvq_paged_decode_shared(kvq_paged* c, const kvq_paged_query* a, const
     if (st != KVQ_OK) return st;
     if (!group_start || !prefix_len) return fail(KVQ_EINVAL, "group_start or prefix_len is NULL");
     if (n_groups < 1 || n_groups > a->n_seq) return fail(KVQ_EINVAL, "n_groups must be in [1, n_seq]");
-    return decode(c, a, group_start, prefix_len, n_groups, nullptr, 0, nullptr, stream);
+    return decode(c, a, group_start, prefix_len, n_groups, nullptr, 0, nullptr, nullptr, stream);
 }
 
 kvq_status kvq_paged_select(kvq_paged* c, const kvq_paged_query* a, int* pages, int keep, int n_first, int n_last,
@@ -482,13 +487,22 @@ kvq_status kvq_paged_decode_sparse(kvq_paged* c, const kvq_paged_query* a, const
     if ((long long)keep * c->cfg.page_rows > (1LL << 24)) return fail(KVQ_EINVAL, "keep * page_rows above 2^24");
     if (a->window != 0) return fail(KVQ_EINVAL, "listed pages take no window");
     if (a->n_seq * a->T > kMaxEntries) return fail(KVQ_ERANGE, "n_seq * T above %d", kMaxEntries);
-    return decode(c, a, nullptr, nullptr, 0, pages, keep, nullptr, stream);
+    return decode(c, a, nullptr, nullptr, 0, pages, keep, nullptr, nullptr, stream);
 }
 
 kvq_status kvq_paged_set_scores(kvq_paged* c, float* scores) {
     if (!c) return fail(KVQ_EINVAL, "cache is NULL");
     if (!aligned16(scores)) return fail(KVQ_EINVAL, "scores must be 16-byte aligned");
     c->row_scores = scores;
+    return KVQ_OK;
+}
+
+kvq_status kvq_paged_set_score_scratch(kvq_paged* c, float* scratch, int queries) {
+    if (!c) return fail(KVQ_EINVAL, "cache is NULL");
+    if (!aligned16(scratch)) return fail(KVQ_EINVAL, "scratch must be 16-byte aligned");
+    if (scratch && (queries < 1 || queries > 8)) return fail(KVQ_EINVAL, "queries=%d outside [1, 8]", queries);
+    c->kept = scratch;
+    c->kept_q = scratch ? queries : 0;
     return KVQ_OK;
 }
 
@@ -503,7 +517,11 @@ kvq_status kvq_paged_decode_scored(kvq_paged* c, const kvq_paged_query* q, float
         return fail(KVQ_EINVAL, "out must not overlap q");
     ScoredArgs a = {};
     a.stats = reinterpret_cast<float2*>(c->ws + c->off_stats);
-    st = decode(c, q, nullptr, nullptr, 0, nullptr, 0, const_cast<float2*>(a.stats), stream);
+    // scores kept by the decode where there is room for them and they are fewer bytes, written and
+    // read, than the keys again
+    const int own = q->n_q_heads / c->cfg.n_kv_heads * q->T;
+    if (own <= c->kept_q && 8 * own <= c->g.NB() * (c->g.fp8 ? 32 : 34)) a.kept = c->kept;
+    st = decode(c, q, nullptr, nullptr, 0, nullptr, 0, const_cast<float2*>(a.stats), const_cast<float*>(a.kept), stream);
     if (st != KVQ_OK) return st;
     a.g = c->g;
     a.q = q->q;
@@ -522,7 +540,8 @@ kvq_status kvq_paged_decode_scored(kvq_paged* c, const kvq_paged_query* q, float
     a.decay = decay;
     a.scores = c->row_scores;
     a.sms = c->num_sms;
-    cudaError_t e = launch_scored(a, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = a.kept ? launch_gains(a, s) : launch_scored(a, s);
     return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "row score kernel");
 }
 

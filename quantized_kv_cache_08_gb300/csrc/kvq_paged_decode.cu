@@ -44,10 +44,18 @@
 #include <algorithm>
 #include <type_traits>
 
+// Built a second time with KVQ_PAGED_KEEP (kvq_paged_decode_kept.cu): the split
+// kernel of tiles of 8 queries then keeps the scores that it works out, for
+// kvq_paged_decode_scored.  A translation unit of its own leaves this one's code as it is.
+#ifndef KVQ_PAGED_KEEP
+#define KVQ_PAGED_KEEP 0
+#endif
+
 namespace kvq {
 namespace paged {
 namespace {
 
+constexpr bool kKeep = KVQ_PAGED_KEEP;
 
 // Query tiles: 8 or 16 bf16 queries, or 8 or 16 of f32 in two parts
 enum Tile { kT8 = 0, kT16 = 1, kF32 = 2, kF32W = 3 };
@@ -129,7 +137,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* cell, int row0, const Rows& 
 template <int NB, bool F8, int TILE>
 __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int row0, const uint8_t* __restrict__ qs,
                                           const LaneRows<Acc<NB, F8, TILE>::NQ>& lr, int lane, const float (&zero)[4],
-                                          uint32_t magic, uint32_t exps, Acc<NB, F8, TILE>& acc) {
+                                          uint32_t magic, uint32_t exps, Acc<NB, F8, TILE>& acc, float* kept = nullptr) {
     constexpr bool HL = two_parts<TILE>();
     constexpr int NQ = Acc<NB, F8, TILE>::NQ;
     const int j = lane & 3;
@@ -211,6 +219,7 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
     }
     // ---- scale, cap, mask; the reference
     float top[NQ];
+    static_assert(!kKeep || NQ == 1, "scores are kept of tiles of 8 queries");
 #pragma unroll
     for (int r = 0; r < NQ; ++r) {
 #pragma unroll
@@ -233,6 +242,12 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
                 }
         }
         top[r] = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+    }
+    if constexpr (kKeep) {                                // (kept: this lane's query's 16 rows, NULL where there is none)
+        if (kept) {
+            *reinterpret_cast<float2*>(kept + 2 * j) = make_float2(sc[0][0], sc[0][1]);
+            *reinterpret_cast<float2*>(kept + 2 * j + 8) = make_float2(sc[1][0], sc[1][1]);
+        }
     }
     bool move = top[0] > acc.m[0] + kLazy;
     if (NQ == 2) move |= top[NQ - 1] > acc.m[NQ - 1] + kLazy;
@@ -622,6 +637,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
     __shared__ long long s_wsum[kWarps];
     __shared__ int s_ksum[kWarps];
     __shared__ int s_row0[kWarps][kMaxStages];        // first row of the cell in a stage, -1: none
+    __shared__ long long s_cell[kKeep ? kWarps : 1][kKeep ? kMaxStages : 1];      // which of the pool's cells it is
     __shared__ __align__(8) uint64_t s_bar[kWarps][kMaxStages];
     __shared__ int s_abort, s_last[groups_of<NB, TILE>()];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -716,6 +732,7 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             const bool there = pr.row0 >= 0 && pr.page >= 0 && pr.page < a.g.n_pages;
             if (pr.row0 >= 0 && !there) atomicExch(a.g.err, kErrCounter);
             s_row0[warp][st] = there ? pr.row0 : -1;
+            if constexpr (kKeep) s_cell[warp][st] = (long long)pr.page * (a.g.Hkv * a.g.cells_per_page()) + pr.off / CELL;
             if (there) {
                 dev::mbar_expect_tx(bar, CELL);
                 asm volatile(
@@ -875,7 +892,8 @@ __global__ void __launch_bounds__(warps_of<NB, TILE>() * 32, 1) split_kernel(con
             const bool there = wait_bounded(bar0 + 8u * st, phase, &s_abort, a.g.err);
             const int row0 = s_row0[warp][st];
             if (there && row0 >= 0 && row0 < lr.hi_max)
-                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, zero, magic, exps, acc);
+                take_cell<NB, F8, TILE>(a, ring_p + st * CELL, row0, qs, lr, lane, zero, magic, exps, acc,
+                                        kKeep && g < f.nq ? a.kept + (s_cell[kKeep ? warp : 0][kKeep ? st : 0] * a.kept_q + g) * 16 : nullptr);
             __syncwarp();
             if (there) produce(st);
             if (++st == stages) {
@@ -1120,10 +1138,15 @@ cudaError_t launch_split_t(const SplitArgs& a, cudaStream_t s) {
 
 template <int NB, bool F8>
 cudaError_t launch_split_f(const SplitArgs& a, cudaStream_t s) {
-    if constexpr (NB < 8)
-        if (!a.bf16 && a.tile == 16) return launch_split_t<NB, F8, kF32W>(a, s);
-    if (!a.bf16) return launch_split_t<NB, F8, kF32>(a, s);
-    return a.tile == 8 ? launch_split_t<NB, F8, kT8>(a, s) : launch_split_t<NB, F8, kT16>(a, s);
+    if constexpr (kKeep) {
+        if (a.tile != 8) return cudaErrorInvalidValue;
+        return a.bf16 ? launch_split_t<NB, F8, kT8>(a, s) : launch_split_t<NB, F8, kF32>(a, s);
+    } else {
+        if constexpr (NB < 8)
+            if (!a.bf16 && a.tile == 16) return launch_split_t<NB, F8, kF32W>(a, s);
+        if (!a.bf16) return launch_split_t<NB, F8, kF32>(a, s);
+        return a.tile == 8 ? launch_split_t<NB, F8, kT8>(a, s) : launch_split_t<NB, F8, kT16>(a, s);
+    }
 }
 
 template <int NB>
@@ -1133,6 +1156,15 @@ cudaError_t launch_split_nb(const SplitArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+#if KVQ_PAGED_KEEP
+cudaError_t launch_split_kept(const SplitArgs& a, cudaStream_t s) {
+    switch (a.g.NB()) {
+        case 2: return launch_split_nb<2>(a, s);
+        case 4: return launch_split_nb<4>(a, s);
+        default: return launch_split_nb<8>(a, s);
+    }
+}
+#else
 // f32 queries of head_dim 256 stay at 8: two parts of 16 leave few registers and
 // stages (16k rows, 4 KV heads of 8 x 4 queries, P d in two parts: 43 us, 8: 38),
 // where smaller heads gain (8 sequences of 16k rows, 8 KV heads of 128, 16 queries:
@@ -1165,6 +1197,8 @@ cudaError_t launch_merge(const SplitArgs& a, cudaStream_t s) {
         default: return launch_dependent(merge_kernel<8>, grid, 256, 0, s, a, a.tile);
     }
 }
+
+#endif
 
 }  // namespace paged
 }  // namespace kvq

@@ -440,6 +440,111 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
     }
 }
 
+// ------------------------------------------------------------ from kept scores
+
+constexpr int kGainThreads = 256;
+constexpr int kGainRows = 2;           // rows of a thread in an item
+
+// Rows of (sequence, KV head) pairs, a row a thread, kGainRows x kGainThreads an item: its
+// kept scores of NQ queries at most, their weights, and the row's score.
+template <int NQ>
+__global__ void __launch_bounds__(kGainThreads) gains_kernel(const __grid_constant__ ScoredArgs a) {
+    constexpr int kWarpsG = kGainThreads / 32, kItem = kGainRows * kGainThreads;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ long long s_sum[kWarpsG];
+    long long* plan = reinterpret_cast<long long*>(smem);                      // items before each sequence, of a KV head
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nq = a.hpk * a.T;
+    wait_for_earlier();
+    let_next_start();
+    auto first_row = [&](int len) {                        // (with nothing to fade, rows that a query sees)
+        return a.decay == 1.f && a.window > 0 ? max(0, len - a.T + 1 - a.window) & ~15 : 0;
+    };
+    auto items = [&](int e) {
+        const int len = a.lens[e];
+        if (len <= 0 || len > (long long)a.g.max_pages << a.g.page_shift) return 0;      // (reported by the decode)
+        return (len - first_row(len) + kItem - 1) / kItem;
+    };
+    {
+        const int per = (a.n_seq + kGainThreads - 1) / kGainThreads;
+        long long w = 0;
+        for (int i = 0; i < per; ++i) {
+            const int e = tid * per + i;
+            if (e < a.n_seq) {
+                plan[e] = w;
+                w += items(e);
+            }
+        }
+        long long wi = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, wi, o);
+            if (lane >= o) wi += y;
+        }
+        if (lane == 31) s_sum[warp] = wi;
+        __syncthreads();
+        long long base = wi - w;
+        for (int i = 0; i < warp; ++i) base += s_sum[i];
+        for (int i = 0; i < per; ++i)
+            if (tid * per + i < a.n_seq) plan[tid * per + i] += base;
+        if (tid == kGainThreads - 1) plan[a.n_seq] = base + w;
+        __syncthreads();
+    }
+    const long long U = plan[a.n_seq] * a.g.Hkv;
+    const int mask = a.g.page_rows - 1;
+    for (long long x = blockIdx.x; x < U; x += gridDim.x) {
+        int e = 0;
+        {
+            int hi = a.n_seq;
+            while (hi - e > 1) {
+                const int mid = (e + hi) >> 1;
+                if (plan[mid] * a.g.Hkv <= x) e = mid;
+                else hi = mid;
+            }
+        }
+        const long long in_e = x - plan[e] * a.g.Hkv, n_items = plan[e + 1] - plan[e];
+        const int kh = (int)(in_e / n_items), item = (int)(in_e - kh * n_items);
+        const int len = a.lens[e], r0 = first_row(len) + item * kItem + tid;
+        const int seen = a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;      // rows before it no query sees
+        const int* table = a.tables + (long long)e * a.g.max_pages;
+        long long at[kGainRows];                           // of the row's score, -1: none
+        float old[kGainRows], s[kGainRows][NQ];
+#pragma unroll
+        for (int i = 0; i < kGainRows; ++i) {
+            const int r = r0 + i * kGainThreads;
+            at[i] = -1;
+            old[i] = 0.f;
+            if (r >= len) continue;
+            const int page = table[r >> a.g.page_shift];
+            if (page < 0 || page >= a.g.n_pages) continue;
+            at[i] = ((long long)page * a.g.Hkv + kh) * a.g.page_rows + (r & mask);
+            if (a.decay > 0.f) old[i] = a.scores[at[i]];
+            const float* from = a.kept + (at[i] >> 4) * nq * 16 + (r & 15);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) s[i][q] = q < nq && r >= seen ? from[q * 16] : 0.f;
+        }
+        float gain[kGainRows] = {};
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            if (q >= nq) break;
+            const int t = q / a.hpk, h = kh * a.hpk + q - t * a.hpk;
+            const int hi = len - a.T + t + 1, lo = a.window > 0 ? max(0, hi - a.window) : 0;
+            if (hi <= lo) continue;
+            const float2 st = a.stats[((long long)e * a.T + t) * a.Hq + h];
+            if (!(st.y > 0.f && st.x > kNegInf && st.x < kInf)) continue;      // (one that is not finite adds nothing)
+#pragma unroll
+            for (int i = 0; i < kGainRows; ++i) {
+                const int r = r0 + i * kGainThreads;
+                const float p = ex2(__fadd_rn(s[i][q], -st.x)) * st.y;
+                gain[i] += r >= lo && r < hi ? p : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kGainRows; ++i)
+            if (at[i] >= 0) a.scores[at[i]] = a.decay > 0.f ? fmaf(a.decay, old[i], gain[i]) : gain[i];
+    }
+}
+
 template <int NB, bool F8, bool F32Q, bool MANY>
 cudaError_t launch_many(const ScoredArgs& a, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
@@ -470,6 +575,15 @@ cudaError_t launch_scored(const ScoredArgs& a, cudaStream_t s) {
         case 4: return launch_nb<4>(a, s);
         default: return launch_nb<8>(a, s);
     }
+}
+
+cudaError_t launch_gains(const ScoredArgs& a, cudaStream_t s) {
+    const size_t smem = (size_t)(a.n_seq + 1) * 8;
+    const dim3 grid((unsigned)(a.sms * 6));
+    const int nq = a.hpk * a.T;
+    if (nq <= 1) return launch_dependent(gains_kernel<1>, grid, kGainThreads, smem, s, a);
+    if (nq <= 4) return launch_dependent(gains_kernel<4>, grid, kGainThreads, smem, s, a);
+    return launch_dependent(gains_kernel<8>, grid, kGainThreads, smem, s, a);
 }
 
 }  // namespace paged

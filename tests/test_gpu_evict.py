@@ -65,6 +65,8 @@ def near(got, old, gain, decay):
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("D,Hkv,hpk,T,page,lens,kw", [
     (64, 2, 4, 1, 16, [1, 0, 33, 96], {}),
+    (64, 1, 8, 1, 16, [50, 16], {}),
+    (128, 2, 2, 4, 32, [3, 1100, 700], dict(window=90)),             # pages of many fragments, a window's front
     (128, 1, 1, 1, 32, [5, 190, 64], {}),
     (128, 3, 5, 3, 16, [2, 80, 3], dict(window=7)),                  # a sequence with positions below 0
     (256, 1, 8, 2, 64, [130, 17], dict(softcap=5.0)),
@@ -74,9 +76,13 @@ def near(got, old, gain, decay):
     (128, 1, 33, 4, 16, [90, 5], {}),
 ])
 @pytest.mark.parametrize("decay", [1.0, 0.0, 0.5])
-def test_scored_decode(fmt, dtype, D, Hkv, hpk, T, page, lens, kw, decay):
+@pytest.mark.parametrize("scratch", [True, False])
+def test_scored_decode(fmt, dtype, D, Hkv, hpk, T, page, lens, kw, decay, scratch):
+    if scratch and hpk * T > 8:
+        pytest.skip("no scratch for so many queries")
     n, mp = len(lens), max(2, -(-max(lens) // page))
-    p = PagedPair(n, Hkv, D, Hkv * hpk, page=page, max_pages=mp, fmt=fmt, max_t=T, seed=D + T, scores=True)
+    p = PagedPair(n, Hkv, D, Hkv * hpk, page=page, max_pages=mp, fmt=fmt, max_t=T, seed=D + T, scores=True, score_scratch=scratch)
+    assert (p.dev.scratch is not None) == scratch
     p.append(lens)
     for step, sink in enumerate((False, True)):
         before = torch.rand(p.dev.scores.shape, device="cuda")
@@ -102,12 +108,13 @@ def test_scored_decode(fmt, dtype, D, Hkv, hpk, T, page, lens, kw, decay):
     assert p.dev.device_error() == 0
 
 
-def test_weights_add_up_and_repeat():
+@pytest.mark.parametrize("scratch", [True, False])
+def test_weights_add_up_and_repeat(scratch):
     """Many sequences of very different lengths over all blocks: a query's weights sum to 1; two runs give the same bits."""
     need_gpu()
     n, Hkv, D, page, mp = 33, 4, 64, 64, 64
     lens = [1 + (i * 997) % 4096 for i in range(n)]
-    c = PagedKVCache(n * mp, page, Hkv, D, 4 * Hkv, max_seqs=n, max_pages=mp, scores=True)
+    c = PagedKVCache(n * mp, page, Hkv, D, 4 * Hkv, max_seqs=n, max_pages=mp, scores=True, score_scratch=scratch)
     tab = torch.randperm(n * mp, generator=torch.Generator().manual_seed(1)).view(n, mp).int().cuda()
     starts = i32(np.concatenate([[0], np.cumsum(lens)]).tolist())
     k = torch.randn(sum(lens), Hkv, D, device="cuda", dtype=BF)
@@ -151,11 +158,13 @@ def test_appended_rows_start_at_zero(fmt, counts, bounds):
 @pytest.mark.parametrize("fmt", [Q8, F8])
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("scale", [1e2, 1e4, 1e6, 1e12])
-def test_weights_of_large_scores_add_up(fmt, dtype, scale):
+@pytest.mark.parametrize("scratch", [True, False])
+def test_weights_of_large_scores_add_up(fmt, dtype, scale, scratch):
     """Scores of thousands and more: their steps in f32 are no small change of a weight any more, but weights are
     worked out from the same numbers as the softmax's sum, so that they add up to 1 a query: 2^-21 for the sum of 300 f32
     numbers either way, as much again for the product."""
-    p = PagedPair(2, 2, 128, 8, page=16, max_pages=20, fmt=fmt, scores=True)
+    p = PagedPair(2, 2, 128, 8, page=16, max_pages=20, fmt=fmt, max_t=1, scores=True, score_scratch=scratch)
+    assert (p.dev.scratch is not None) == scratch
     p.append([300, 33])
     out = p.dev.decode_scored(p.randn(2, 1, 8, 128, dtype=dtype).cuda(), p.tables, p.lens(), scale=scale)
     assert torch.isfinite(out).all()
@@ -164,8 +173,9 @@ def test_weights_of_large_scores_add_up(fmt, dtype, scale):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
-def test_queries_that_are_not_finite_add_nothing(dtype):
-    p = PagedPair(2, 1, 64, 4, page=16, max_pages=3, scores=True)
+@pytest.mark.parametrize("scratch", [True, False])
+def test_queries_that_are_not_finite_add_nothing(dtype, scratch):
+    p = PagedPair(2, 1, 64, 4, page=16, max_pages=3, max_t=1, scores=True, score_scratch=scratch)
     p.append([40, 20])
     q = p.randn(2, 1, 4, 64, dtype=dtype)
     bad = q.clone()
@@ -189,7 +199,8 @@ def test_queries_that_are_not_finite_add_nothing(dtype):
 
 def test_rows_of_garbage_behind_the_length_do_no_harm():
     """Bytes behind the length inside its cell are NaN scales and codes (the pool is filled with them)."""
-    p = PagedPair(3, 2, 128, 8, page=16, max_pages=2, scores=True)
+    p = PagedPair(3, 2, 128, 8, page=16, max_pages=2, max_t=1, scores=True)
+    p.dev.scratch.fill_(float("nan"))
     p.append([1, 17, 31])
     p.dev.scores.fill_(1.0)
     p.dev.decode_scored(p.randn(3, 1, 8, 128).cuda(), p.tables, p.lens())
@@ -621,6 +632,9 @@ def test_refusals():
         with pytest.raises(B.KvqError):
             B.kvq_paged_compact(p.dev.handle, at[0], at[1], 2, at[2], 2, at[3], at[4])
     B.kvq_paged_set_scores(p.dev.handle, buf.data_ptr())
+    for at, queries in ((4, 1), (0, 0), (0, 9), (0, -1)):
+        with pytest.raises(B.KvqError):
+            B.kvq_paged_set_score_scratch(p.dev.handle, buf.data_ptr() + at, queries)
     for bad in (dict(decay=-0.1), dict(decay=1.5), dict(decay=float("nan")), dict(out=q), dict(softcap=-1.0), dict(window=-1)):
         with pytest.raises((ValueError, B.KvqError)):
             p.dev.decode_scored(q, p.tables, lens, **bad)

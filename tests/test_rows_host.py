@@ -42,6 +42,7 @@ def test_null_arguments(L):
     for call in (
             lambda: B.kvq_paged_append_at(None, 16, 256, 16, 256, None, 0, None, 0, 0, 16, 16, 1, 1, None, 1, 16),
             lambda: B.kvq_paged_set_axes(None, [0], 1), lambda: B.kvq_paged_set_scores(None, 16),
+            lambda: B.kvq_paged_set_score_scratch(None, 16, 1),
             lambda: B.kvq_paged_decode_scored(None, q, 1.0), lambda: B.kvq_paged_select_rows(None, 16, 16, 1, 4, 0, 0, 16),
             lambda: B.kvq_paged_compact(None, 16, 16, 1, 16, 4, None, 16)):
         with pytest.raises(B.KvqError) as e:
