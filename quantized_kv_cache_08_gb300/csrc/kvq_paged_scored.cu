@@ -443,13 +443,13 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
 // ------------------------------------------------------------ from kept scores
 
 constexpr int kGainThreads = 256;
-constexpr int kGainRows = 2;           // rows of a thread in an item
+constexpr int kGainSets = 2;           // sets of four rows of a thread in an item
 
-// Rows of (sequence, KV head) pairs, a row a thread, kGainRows x kGainThreads an item: its
-// kept scores of NQ queries at most, their weights, and the row's score.
+// Rows of (sequence, KV head) pairs, four neighbours a load: their kept scores of NQ
+// queries at most, the weights, and the rows' scores.
 template <int NQ>
 __global__ void __launch_bounds__(kGainThreads) gains_kernel(const __grid_constant__ ScoredArgs a) {
-    constexpr int kWarpsG = kGainThreads / 32, kItem = kGainRows * kGainThreads;
+    constexpr int kWarpsG = kGainThreads / 32, kItem = 4 * kGainSets * kGainThreads;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ long long s_sum[kWarpsG];
     long long* plan = reinterpret_cast<long long*>(smem);                      // items before each sequence, of a KV head
@@ -504,26 +504,28 @@ __global__ void __launch_bounds__(kGainThreads) gains_kernel(const __grid_consta
         }
         const long long in_e = x - plan[e] * a.g.Hkv, n_items = plan[e + 1] - plan[e];
         const int kh = (int)(in_e / n_items), item = (int)(in_e - kh * n_items);
-        const int len = a.lens[e], r0 = first_row(len) + item * kItem + tid;
+        const int len = a.lens[e], r0 = first_row(len) + item * kItem + 4 * tid;
         const int seen = a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;      // rows before it no query sees
         const int* table = a.tables + (long long)e * a.g.max_pages;
-        long long at[kGainRows];                           // of the row's score, -1: none
-        float old[kGainRows], s[kGainRows][NQ];
+        long long at[kGainSets];                           // of the rows' scores, -1: none
+        float4 old[kGainSets], s[kGainSets][NQ], gain[kGainSets];
 #pragma unroll
-        for (int i = 0; i < kGainRows; ++i) {
-            const int r = r0 + i * kGainThreads;
-            at[i] = -1;
-            old[i] = 0.f;
-            if (r >= len) continue;
-            const int page = table[r >> a.g.page_shift];
-            if (page < 0 || page >= a.g.n_pages) continue;
-            at[i] = ((long long)page * a.g.Hkv + kh) * a.g.page_rows + (r & mask);
-            if (a.decay > 0.f) old[i] = a.scores[at[i]];
+        for (int i = 0; i < kGainSets; ++i) {
+            const int r = r0 + i * 4 * kGainThreads;
+            const int page = r < len ? table[r >> a.g.page_shift] : -1;
+            at[i] = page >= 0 && page < a.g.n_pages ? ((long long)page * a.g.Hkv + kh) * a.g.page_rows + (r & mask) : -1;
+        }
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kGainSets; ++i) {
+            const int r = r0 + i * 4 * kGainThreads;
+            const bool on = at[i] >= 0;
+            old[i] = on && a.decay > 0.f ? *reinterpret_cast<const float4*>(a.scores + at[i]) : none;
             const float* from = a.kept + (at[i] >> 4) * nq * 16 + (r & 15);
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) s[i][q] = q < nq && r >= seen ? from[q * 16] : 0.f;
+            for (int q = 0; q < NQ; ++q) s[i][q] = on && q < nq && r + 4 > seen ? __ldcs(reinterpret_cast<const float4*>(from + q * 16)) : none;
+            gain[i] = none;
         }
-        float gain[kGainRows] = {};
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             if (q >= nq) break;
@@ -532,16 +534,33 @@ __global__ void __launch_bounds__(kGainThreads) gains_kernel(const __grid_consta
             if (hi <= lo) continue;
             const float2 st = a.stats[((long long)e * a.T + t) * a.Hq + h];
             if (!(st.y > 0.f && st.x > kNegInf && st.x < kInf)) continue;      // (one that is not finite adds nothing)
+            auto add = [&](float& g, float score, int r) {
+                const float p = ex2(__fadd_rn(score, -st.x)) * st.y;
+                g += r >= lo && r < hi ? p : 0.f;
+            };
 #pragma unroll
-            for (int i = 0; i < kGainRows; ++i) {
-                const int r = r0 + i * kGainThreads;
-                const float p = ex2(__fadd_rn(s[i][q], -st.x)) * st.y;
-                gain[i] += r >= lo && r < hi ? p : 0.f;
+            for (int i = 0; i < kGainSets; ++i) {
+                const int r = r0 + i * 4 * kGainThreads;
+                add(gain[i].x, s[i][q].x, r);
+                add(gain[i].y, s[i][q].y, r + 1);
+                add(gain[i].z, s[i][q].z, r + 2);
+                add(gain[i].w, s[i][q].w, r + 3);
             }
         }
 #pragma unroll
-        for (int i = 0; i < kGainRows; ++i)
-            if (at[i] >= 0) a.scores[at[i]] = a.decay > 0.f ? fmaf(a.decay, old[i], gain[i]) : gain[i];
+        for (int i = 0; i < kGainSets; ++i) {
+            if (at[i] < 0) continue;
+            const int r = r0 + i * 4 * kGainThreads;
+            auto faded = [&](float o, float g) { return a.decay > 0.f ? fmaf(a.decay, o, g) : g; };
+            const float v[4] = {faded(old[i].x, gain[i].x), faded(old[i].y, gain[i].y), faded(old[i].z, gain[i].z), faded(old[i].w, gain[i].w)};
+            if (r + 4 <= len) {
+                *reinterpret_cast<float4*>(a.scores + at[i]) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (r + k < len) a.scores[at[i] + k] = v[k];
+            }
+        }
     }
 }
 
