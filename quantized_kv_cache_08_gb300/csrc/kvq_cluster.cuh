@@ -43,6 +43,16 @@ __device__ __forceinline__ int size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return (int)r;
 }
+// Before a block touches another's shared memory that one has to have started: all
+// threads arrive() at their start, and started() behind it, before the first store
+__device__ __forceinline__ void arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void started() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // every thread of every block of the cluster; what was written before it, to any of
 // their shared memories or to global memory, is seen behind it
 __device__ __forceinline__ void sync() {

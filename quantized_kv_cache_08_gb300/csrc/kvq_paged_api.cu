@@ -578,7 +578,7 @@ kvq_status kvq_paged_compact(kvq_paged* c, const int* tables, const int* lens, i
     if (tables_out == tables) return fail(KVQ_EINVAL, "tables_out must be NULL (in place) or hold other pages than tables");
     // (a sequence holds no more)
     const int most = std::min(keep, c->cfg.max_pages * c->cfg.page_rows);
-    if (c->cfg.bounds && (long long)n_seq * most * c->cfg.n_kv_heads > (1LL << 31))
+    if (c->cfg.bounds && (long long)n_seq * most * c->cfg.n_kv_heads > 0x7fffffffLL)
         return fail(KVQ_ERANGE, "n_seq * keep too large for one call");
     CompactArgs a = {};
     a.g = c->g;

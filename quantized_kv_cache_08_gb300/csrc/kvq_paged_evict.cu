@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
         for (int i = rank * kPick + tid; i < a.keep; i += C * kPick) out[i] = i < len ? i : -1;
         return;
     }
+    cluster::arrive();
     const int first = a.n_first, last = len - a.n_last;           // rows [first, last) compete
     const int per = (((len + C - 1) / C) + 15) & ~15;
     const int s0 = min(len, rank * per), s1 = min(len, s0 + per), m = s1 - s0;
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kPick) select_rows_kernel(const __grid_constan
         s_hi[warp] = hi;
     }
     __syncthreads();
+    cluster::started();
     if (warp < 2) {
         uint32_t v = warp ? 0u : 0xffffffffu;
         if (lane < kPickWarps) v = warp ? s_hi[lane] : s_lo[lane];

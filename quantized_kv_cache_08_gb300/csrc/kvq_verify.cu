@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = cluster::size(), rank = cluster::rank();
     const long long b = blockIdx.x / C;
+    cluster::arrive();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- the first draft that does not stand
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     u64 S = 0, first = 0, mine = 0;
     for (int mode = 0; mode < 2; ++mode) {
         sums(lo, hi);
+        if (mode == 0) cluster::started();
         if (tid < C) {
             u64 t = 0;
             for (int w = 0; w < kWarps; ++w) t += s_sum[w];
