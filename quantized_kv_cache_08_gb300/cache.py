@@ -467,9 +467,13 @@ class PagedKVCache:
         ascending, -1 behind the last."""
         n, tp, lp = self._batch(tables, lens)
         if rows is None:
-            rows = self._new((n, self.n_kv_heads, keep), torch.int32, stream)
-        self._call(self._lib.kvq_paged_select_rows, tp, lp, n, keep, n_first, n_last,
-                   self._ints(rows, (n, self.n_kv_heads, keep), "rows"), self._stream(stream))
+            rows = torch.empty((n, self.n_kv_heads, keep), dtype=_I32, device=self.device) if stream is None else \
+                self._new((n, self.n_kv_heads, keep), torch.int32, stream)
+            rp = rows.data_ptr()
+        else:
+            rp = self._ints(rows, (n, self.n_kv_heads, keep), "rows")
+        self._call(self._lib.kvq_paged_select_rows, tp, lp, n, keep, n_first, n_last, rp,
+                   _raw_stream(self.index) if stream is None else stream.cuda_stream)
         return rows
 
     def compact(self, tables, lens, rows, lens_out=None, tables_out=None, stream=None):
@@ -478,11 +482,15 @@ class PagedKVCache:
         lengths (lens_out, made if None; may be lens)."""
         n, tp, lp = self._batch(tables, lens)
         keep = rows.shape[-1]
-        if lens_out is None:
-            lens_out = self._new((n,), torch.int32, stream)
+        rp = self._ints(rows, (n, self.n_kv_heads, keep), "rows")
         to = None if tables_out is None else self._ints(tables_out, (n, self.max_pages), "tables_out")
-        self._call(self._lib.kvq_paged_compact, tp, lp, n, self._ints(rows, (n, self.n_kv_heads, keep), "rows"), keep, to,
-                   self._ints(lens_out, (n,), "lens_out"), self._stream(stream))
+        if lens_out is None:
+            lens_out = torch.empty_like(lens) if stream is None else self._new((n,), torch.int32, stream)
+            op = lens_out.data_ptr()
+        else:
+            op = self._ints(lens_out, (n,), "lens_out")
+        self._call(self._lib.kvq_paged_compact, tp, lp, n, rp, keep, to, op,
+                   _raw_stream(self.index) if stream is None else stream.cuda_stream)
         return lens_out
 
     def device_error(self, stream=None):
@@ -533,7 +541,7 @@ def verify(target, draft, tokens, uniform, lens=None, accept=None, next_tokens=N
 
     def make():
         with torch.cuda.stream(stream):
-            t = tokens.new_empty(n)
+            t = torch.empty(n, dtype=_I32, device=target.device)
         t.record_stream(torch.cuda.current_stream(target.device))
         return t
 
@@ -541,10 +549,10 @@ def verify(target, draft, tokens, uniform, lens=None, accept=None, next_tokens=N
     np_ = counts(next_tokens, "next_tokens") if next_tokens is not None else None
     lp = counts(lens, "lens") if lens is not None else None
     if accept is None:
-        accept = tokens.new_empty(n) if stream is None else make()
+        accept = torch.empty(n, dtype=_I32, device=target.device) if stream is None else make()
         ap = accept.data_ptr()
     if next_tokens is None:
-        next_tokens = tokens.new_empty(n) if stream is None else make()
+        next_tokens = torch.empty_like(accept) if stream is None else make()
         np_ = next_tokens.data_ptr()
     a = ctypes.byref(B.kvq_verify_args(target.data_ptr(), dp, tokens.data_ptr(), uniform.data_ptr(), code, n, T, V, ts, tr, ds,
                                        dr, ap, np_, lp))
