@@ -589,6 +589,34 @@ def test_two_caches_on_two_streams():
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("scratch", [True, False])
+@pytest.mark.parametrize("fmt", [Q8, F8])
+def test_pages_beyond_four_gigabytes(fmt, scratch):
+    """Pages at the end of a pool of more than 2^32 bytes give what pages at the front of a small one give."""
+    need_gpu()
+    n, Hkv, Hq, D, page, mp, keep = 2, 8, 8, 256, 256, 3, 300
+    g = torch.Generator().manual_seed(3)
+    k, v, q = (torch.randn(n, 700, Hkv, D, generator=g).cuda() for _ in range(3))
+    at = torch.arange(700).int().cuda().expand(n, 700).contiguous()
+    got = []
+    for n_pages in (8, 5000):
+        c = PagedKVCache(n_pages, page, Hkv, D, Hq, max_seqs=n, max_pages=mp, max_t=1, fmt=fmt, rope_dim=D, scores=True, score_scratch=scratch)
+        assert n_pages == 8 or c.pool.numel() > 1 << 32
+        last = (torch.arange(n * mp).view(n, mp).flip(0) + n_pages - 7).int().cuda()
+        lens = i32([700, 513])
+        c.append(k, v, last, i32([700, 700]), positions=at)
+        out = c.decode_scored(q[:, :1].contiguous(), last, lens)
+        scores = c.scores[last.long()].clone()
+        rows = c.select_rows(last, lens, keep, n_first=2, n_last=30)
+        new = c.compact(last, lens, rows)
+        ko, vo = torch.empty(n, keep, Hkv, D, device="cuda"), torch.empty(n, keep, Hkv, D, device="cuda")
+        c.read(last, new, ko, vo)
+        got.append((out, scores, rows, new, ko, vo))
+        assert c.device_error() == 0
+        del c
+    assert all(torch.equal(x, y) for x, y in zip(*got)) and got[0][3].tolist() == [keep, keep]
+
+
 def test_on_another_stream():
     p = PagedPair(2, 2, 64, 4, page=16, max_pages=4, scores=True)
     p.append([60, 35])
