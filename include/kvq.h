@@ -249,7 +249,8 @@ kvq_status kvq_truncate_device(kvq_cache* cache, const int* accept_d, int T, voi
  * any number >= 0, a row's elements side by side.  tokens: device int32
  * [n_seq][T - 1]; one outside [0, vocab) is no draft: the sequence's drafts end
  * there (its step may hold fewer than T - 1).  uniform: device f32 [n_seq][T] in [0, 1).
- * A probability that is not above 0 (NaN too) counts as 0, one above 1 as 1.
+ * A probability that is not above 0 (NaN too) counts as 0, one above 1 as 1, in
+ * the test of a draft as in the draw.
  *
  * Draft t stands while uniform[t] * q_t(tokens[t]) < p_t(tokens[t]) (the exact
  * products) and all before it stand.  With a the number that do:

@@ -164,8 +164,8 @@ def verify(target, draft, tokens, uniform):
     a, held = 0, False
     while a < T - 1 and 0 <= tokens[a] < V:
         held = True
-        qd = 1.0 if draft is None else draft[a, tokens[a]]
-        if not uniform[a] * qd < target[a, tokens[a]]:
+        qd = 1.0 if draft is None else clean(draft[a, tokens[a]])
+        if not uniform[a] * qd < clean(target[a, tokens[a]]):
             break
         a, held = a + 1, False
     w = p = units(target[a])

@@ -2,7 +2,7 @@
 //
 // Mathematics.  Draft d_t of a sequence stands while u_t q_t(d_t) < p_t(d_t); the
 // products of two f32 numbers are exact in f64, so the test is one of real
-// numbers.  At row a, the first whose draft falls or is none, the next token is
+// numbers; p and q are clean() first, as they are where they are summed.  At row a, the first whose draft falls or is none, the next token is
 // drawn from weights w_i = max(P_i - Q_i, 0) (P_i where no draft stood), P and Q
 // the probabilities in whole units of 2^-52: with S their sum it is the first i
 // whose running sum passes floor(S u).  Sums of whole numbers do not depend on
@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             if (t < a.T - 1) {
                 d = a.tokens[b * (a.T - 1) + t];
                 if (d >= 0 && d < a.vocab) {
-                    const float p = element<BF16>(a.target, b * a.target_seq + t * a.target_row + d);
-                    const float q = a.draft ? element<BF16>(a.draft, b * a.draft_seq + t * a.draft_row + d) : 1.f;
+                    const float p = clean(element<BF16>(a.target, b * a.target_seq + t * a.target_row + d));
+                    const float q = a.draft ? clean(element<BF16>(a.draft, b * a.draft_seq + t * a.draft_row + d)) : 1.f;
                     ok = (double)a.uniform[b * a.T + t] * (double)q < (double)p;
                 } else {
                     d = -1;
