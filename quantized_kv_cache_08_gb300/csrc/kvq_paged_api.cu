@@ -578,8 +578,6 @@ kvq_status kvq_paged_compact(kvq_paged* c, const int* tables, const int* lens, i
     if (tables_out == tables) return fail(KVQ_EINVAL, "tables_out must be NULL (in place) or hold other pages than tables");
     // (a sequence holds no more)
     const int most = std::min(keep, c->cfg.max_pages * c->cfg.page_rows);
-    if (c->cfg.bounds && (long long)n_seq * most * c->cfg.n_kv_heads > 0x7fffffffLL)
-        return fail(KVQ_ERANGE, "n_seq * keep too large for one call");
     CompactArgs a = {};
     a.g = c->g;
     a.tables = tables;
@@ -597,8 +595,14 @@ kvq_status kvq_paged_compact(kvq_paged* c, const int* tables, const int* lens, i
     cudaError_t e = launch_compact(a, c->num_sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "row compaction kernel");
     if (!c->cfg.bounds) return KVQ_OK;
-    const Rows r{a.tables_out, lens_out, nullptr, n_seq, most, n_seq * most};
-    return bounds_of(c, r, s);
+    // (rows times KV heads of one launch stay within 32 bits)
+    const int at_once = (int)std::max(1LL, 0x7fffffffLL / ((long long)most * c->cfg.n_kv_heads));
+    for (int i = 0; i < n_seq; i += at_once) {
+        const int n = std::min(at_once, n_seq - i);
+        st = bounds_of(c, Rows{a.tables_out + (size_t)i * c->cfg.max_pages, lens_out + i, nullptr, n, most, n * most}, s);
+        if (st != KVQ_OK) return st;
+    }
+    return KVQ_OK;
 }
 
 kvq_status kvq_paged_read_error(kvq_paged* c, int* err, void* stream) {

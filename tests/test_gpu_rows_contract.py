@@ -5,8 +5,9 @@ import numpy as np
 import pytest
 import torch
 
-from quantized_kv_cache_08_gb300.cache import verify
+from quantized_kv_cache_08_gb300.cache import PagedKVCache, verify
 from tests.kvq_testutil import need_gpu
+from tests.test_gpu_evict import i32
 from tests.test_rows_contract_host import ODD, odd_rows
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +25,37 @@ def test_probabilities_of_a_draft_that_are_none(dtype):
     accept, token = verify(t.to(dtype).cuda(), q.to(dtype).cuda(), k.cuda(), u.float().cuda())
     assert accept.tolist() == [2 if c[3] else 1 for c in ODD]
     assert token.tolist() == [6 if c[3] else 4 for c in ODD]
+
+
+# ------------------------------------------------------------------ eviction
+
+def test_a_move_of_many_rows_renews_its_bounds():
+    """n * keep * KV heads beyond 2^31: a list of a table's full length, sequences of 300 rows."""
+    need_gpu()
+    n, Hkv, D, page, mp, L = 17, 8, 64, 256, 65536, 300
+    keep = page * mp
+    assert n * keep * Hkv > 1 << 31
+    c = PagedKVCache(4 * n, page, Hkv, D, Hkv, max_seqs=n, max_pages=mp, bounds=True)
+    c.pool.zero_()
+    tables, into = (torch.zeros(n, mp, dtype=torch.int32, device="cuda") for _ in range(2))
+    tables[:, :2] = torch.arange(2 * n, dtype=torch.int32, device="cuda").view(n, 2)
+    into[:, :2] = torch.arange(2 * n, 4 * n, dtype=torch.int32, device="cuda").view(n, 2)
+    g = torch.Generator().manual_seed(7)
+    k = torch.randn(n, L, Hkv, D, generator=g).cuda()
+    lens = i32([L] * n)
+    c.append(k, k, tables, lens)
+    rows = torch.empty(n, Hkv, keep, dtype=torch.int32, device="cuda")     # (all of a list but its first rows is not read)
+    rows[:, :, :L] = torch.arange(L, dtype=torch.int32, device="cuda")
+    c.bounds.fill_(77)
+    want = c.bounds.clone()
+    new = c.compact(tables, lens, rows, tables_out=into)
+    assert new.tolist() == [L] * n
+    got = c.bounds.clone()
+    c.bounds.copy_(want)
+    c.update_bounds(into, new, L)
+    assert torch.equal(got, c.bounds) and not torch.equal(got, want)
+    ko, vo = (torch.empty(n, L, Hkv, D, device="cuda") for _ in range(2))
+    kn, vn = torch.empty_like(ko), torch.empty_like(vo)
+    c.read(tables, lens, ko, vo)
+    c.read(into, new, kn, vn)
+    assert torch.equal(ko, kn) and torch.equal(vo, vn) and c.device_error() == 0
