@@ -205,8 +205,9 @@ class PagedKVCache:
     whose rows are given positions on several axes.  scores: keep an attention score per row and KV head in
     `scores` (float32 [n_pages, Hkv, page_rows], zeros at first; scores_buf takes over an existing
     tensor), which `decode_scored` adds to, `select_rows` goes by and `compact`
-    moves; appended rows start at 0.  score_scratch: room beside it for the scores of up to 8 queries a KV head
-    (as many as max_q_heads and max_t allow, 4 bytes a row and query), which spares decode_scored a second pass over the keys."""
+    moves; appended rows start at 0.  score_scratch: room beside it for the scores of a call of up to
+    8 queries a KV head (or as many as max_q_heads, max_t and the keys' bytes allow; 4 bytes a row, KV head and query: 14 % of a
+    pool of head_dim 128 for 8), which spares such calls of decode_scored a second pass over the keys."""
 
     def __init__(self, n_pages, page_rows, n_kv_heads, head_dim, max_q_heads, max_seqs, max_pages, max_t=1,
                  fmt="q8_0/q5_1", rope_dim=0, rope_base=10000.0, rope_interleaved=False, rope_freq=None, bounds=False,
@@ -243,8 +244,10 @@ class PagedKVCache:
                     or not scores_buf.is_contiguous():
                 raise ValueError(f"scores_buf must be a contiguous float32 {list(shape)} tensor on {dev}")
             self.scores = scores_buf
-            queries = max_q_heads // n_kv_heads * max_t
-            if score_scratch and queries <= 8:
+            # (a call keeps at most 8 queries' scores, and only where they are fewer bytes than a row's keys)
+            key = head_dim // 32 * (32 if fmt == "e4m3" else 34)
+            queries = min(8, max_q_heads // n_kv_heads * max_t, (key - 1) // 8)
+            if score_scratch:
                 self.scratch = torch.empty(n_pages * n_kv_heads * page_rows * queries, dtype=torch.float32, device=dev)
         self.workspace = torch.empty(sz.workspace, dtype=torch.uint8, device=dev)
         if stream is not None:

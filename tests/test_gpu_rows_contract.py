@@ -7,11 +7,13 @@ import torch
 
 from quantized_kv_cache_08_gb300.cache import PagedKVCache, verify
 from tests.kvq_testutil import need_gpu
-from tests.test_gpu_evict import i32
+from tests.paged_testutil import PagedPair
+from tests.test_gpu_evict import gains, i32, near, scores_of
 from tests.test_rows_contract_host import ODD, odd_rows
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
+Q8, F8 = "q8_0/q5_1", "e4m3"
 
 
 # ------------------------------------------------------------------ verification
@@ -25,6 +27,35 @@ def test_probabilities_of_a_draft_that_are_none(dtype):
     accept, token = verify(t.to(dtype).cuda(), q.to(dtype).cuda(), k.cuda(), u.float().cuda())
     assert accept.tolist() == [2 if c[3] else 1 for c in ODD]
     assert token.tolist() == [6 if c[3] else 4 for c in ODD]
+
+
+# ------------------------------------------------------------------ room for kept scores
+
+@pytest.mark.parametrize("fmt,D,hpk,max_t,queries", [
+    (Q8, 128, 4, 1, 4), (Q8, 128, 4, 4, 8), (F8, 128, 2, 64, 8), (Q8, 64, 8, 1, 8), (F8, 256, 16, 1, 8),
+    (F8, 64, 8, 1, 7),                                   # (8 scores are as many bytes as a row's keys)
+    (F8, 64, 4, 4, 7),
+])
+def test_room_for_scores_is_what_a_call_can_use(fmt, D, hpk, max_t, queries):
+    """Room for 8 queries a KV head, or as many as a call can have, and a cache made for drafts keeps
+    the scores of its steps of few rows; calls of more leave the room as it is.  Scores are right either way."""
+    p = PagedPair(2, 2, D, 2 * hpk, page=16, max_pages=4, fmt=fmt, max_t=max_t, scores=True, seed=D)
+    assert p.dev.scratch.numel() == p.n_pages * 2 * 16 * queries
+    p.append([50, 7])
+    key = D * (32 if fmt == F8 else 34) // 32
+    for T in (1, 2, 3, 5):
+        if T > max_t:
+            break
+        p.dev.scratch.fill_(float("nan"))
+        p.dev.scores.zero_()
+        q = p.randn(2, T, 2 * hpk, D)
+        p.dev.decode_scored(q.cuda(), p.tables, p.lens())
+        kept = hpk * T <= 8 and 8 * hpk * T < key
+        assert bool((~torch.isnan(p.dev.scratch)).any()) == kept, T
+        gain = gains(p, q)
+        for b in range(2):
+            near(scores_of(p, b), np.zeros(gain[b].shape), gain[b], 1.0)
+    assert p.dev.device_error() == 0
 
 
 # ------------------------------------------------------------------ eviction
