@@ -217,7 +217,8 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
 #pragma unroll
             for (int i = 0; i < 2 * NQ; ++i) sc[t][i] = HL ? raw[i / 2 % QF][t][i & 1] + raw[i / 2 % QF][t][2 + (i & 1)] : raw[0][t][i];
     }
-    // ---- scale, cap, mask; the reference
+    // ---- scale, cap, mask; the reference.  (Products rounded before the reference is taken
+    // off, as where the row scores' weights are worked out from the keys: the same numbers)
     float top[NQ];
     static_assert(!kKeep || NQ == 1, "scores are kept of tiles of 8 queries");
 #pragma unroll
@@ -225,12 +226,12 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) sc[t][2 * r + i] *= lr.fac[r];
+            for (int i = 0; i < 2; ++i) sc[t][2 * r + i] = __fmul_rn(sc[t][2 * r + i], lr.fac[r]);
         if (a.softcap_b > 0.f) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) sc[t][2 * r + i] = a.softcap_b * tanhf(a.softcap_a * sc[t][2 * r + i]);
+                for (int i = 0; i < 2; ++i) sc[t][2 * r + i] = __fmul_rn(a.softcap_b, tanhf(__fmul_rn(a.softcap_a, sc[t][2 * r + i])));
         }
         if (edge) {
 #pragma unroll
@@ -284,7 +285,7 @@ __device__ __forceinline__ void take_cell(const SplitArgs& a, uint8_t* cell, int
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) sc[t][2 * r + i] = ex2(sc[t][2 * r + i] + c);
+            for (int i = 0; i < 2; ++i) sc[t][2 * r + i] = ex2(__fadd_rn(sc[t][2 * r + i], c));
         acc.l[r] += (sc[0][2 * r] + sc[0][2 * r + 1]) + (sc[1][2 * r] + sc[1][2 * r + 1]);
     }
     // ---- values

@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<NB, MANY>()) scored_kernel
                                         // (rounded before the reference is taken off, as in the decode: at scores of
                                         // thousands one rounding less would be another number than its sums hold)
                                         float v = __fmul_rn(sc[u][x][2 * r + i], f.x);
-                                        if (a.softcap_b > 0.f) v = __fmul_rn(a.softcap_b, tanhf(a.softcap_a * v));
+                                        if (a.softcap_b > 0.f) v = __fmul_rn(a.softcap_b, tanhf(__fmul_rn(a.softcap_a, v)));
                                         float p = ex2(__fadd_rn(v, f.y));
                                         if (edge) {
                                             const int at_row = row0 + 16 * x + g + 8 * r;
