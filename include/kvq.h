@@ -413,8 +413,8 @@ typedef struct kvq_paged_config {
 } kvq_paged_config;
 
 /* Device bytes the caller provides (each 16-byte aligned): pool, bounds (0
- * without cfg.bounds), workspace (the error word, decode partials, page
- * scores).  Pool bytes need no initial value. */
+ * without cfg.bounds), workspace (the error word, decode partials, 8 bytes a
+ * sequence, row and query head for kvq_paged_decode_scored, page scores).  Pool bytes need no initial value. */
 typedef struct kvq_paged_sizes {
     size_t pool, bounds, workspace;
     size_t page_bytes, cell_bytes;
@@ -564,15 +564,20 @@ kvq_status kvq_paged_set_scores(kvq_paged* cache, float* scores);
  * (its output is NaN) adds nothing.  Sums are f32 in a fixed order: two runs
  * give the same bits.  The pages of one call's sequences are their own: a page
  * in two tables of the call is written by both.  Rows of bad pages are left
- * out.  out must not overlap q.  Needs a buffer (kvq_paged_set_scores). */
+ * out.  out must not overlap q.  Needs a buffer (kvq_paged_set_scores).
+ * All T rows' queries count when the call runs: the weights of drafts that a
+ * verification lets fall afterwards stay in the scores of the rows they saw. */
 kvq_status kvq_paged_decode_scored(kvq_paged* cache, const kvq_paged_query* a, float decay, void* stream);
 
 /* Room for a scored decode's scores: device f32 [n_pages][Hkv][page_rows][queries],
  * 16-byte aligned, queries in [1, 8], kept until another (or NULL: none) takes its
  * place.  With it, calls of at most `queries` queries a KV head (n_q_heads / Hkv * T)
- * whose scores are fewer bytes than the keys keep them in the first pass, where
- * the second pass else works them out again from the keys: the same scores, at
- * half the extra time.  Its contents are the library's.  Enqueues nothing. */
+ * whose scores, 8 bytes a row and query written and read, are fewer than the keys'
+ * bytes keep them in the first pass, where the second pass else works them out
+ * again from the keys: the same weights, and the less extra time the fewer the
+ * queries (of 1 a third of it, of 8 of head_dim 64 all of it).  What it holds
+ * lives within a call: caches with as many rows of all KV heads, whose calls are in one
+ * stream's order, may have one together.  Enqueues nothing. */
 kvq_status kvq_paged_set_score_scratch(kvq_paged* cache, float* scratch, int queries);
 
 /* Choose the rows that stay.  rows: device int32 [n_seq][Hkv][keep] receives for
@@ -591,7 +596,7 @@ kvq_status kvq_paged_select_rows(kvq_paged* cache, const int* tables, const int*
  * bit, with its score where a buffer is set; with cfg.bounds the pages' key
  * bounds are renewed.  lens_out[b] = min(lens[b], keep) (lens_out may be lens).
  * The keys stay turned by the positions they were appended with: append the
- * next rows with kvq_paged_append_at.
+ * next rows with kvq_paged_append_at.  (Of a bad length lens_out is that length.)
  *   tables_out NULL: in place, into the sequence's own pages; what lies behind
  *     the new length is then free.  A page belongs to one sequence.
  *   tables_out (device int32 [n_seq][max_pages]): into other pages (of a sequence that

@@ -457,7 +457,8 @@ class PagedKVCache:
     def decode_scored(self, q, tables, lens, decay=1.0, sinks=None, scale=0.0, window=0, softcap=0.0, out=None,
                       stream=None):
         """decode, with the weights of each row added to its score: decay * score
-        + the sum over the T query rows and the queries of the KV head."""
+        + the sum over the T query rows and the queries of the KV head (those of
+        drafts that fall later too: nothing takes them off again)."""
         if not 0.0 <= decay <= 1.0:
             raise ValueError("decay must be in [0, 1]")
         out, a = self._query(q, tables, lens, sinks, scale, window, softcap, out, stream)

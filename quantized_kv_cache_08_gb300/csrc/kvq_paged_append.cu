@@ -17,7 +17,8 @@
 // at any position below 2^24, where p f in one fp32 product would be off by
 // p 2^-24 radians.  Positions are a row's index in its sequence, or given for each
 // row on up to four axes, of which each pair of elements has one; those angles are worked out
-// further (put_angle_at; 8k rows 54.9 us in all, by index 50.7).
+// further (put_angle_at; 8k rows 55.3 us in all, by index 51.0).  bf16 instances without
+// bounds spill 76 to 104 bytes a thread at their 64 registers.
 #include "kvq_paged.cuh"
 #include "kvq_quant.cuh"
 

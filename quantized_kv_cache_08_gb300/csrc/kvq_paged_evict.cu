@@ -23,9 +23,14 @@
 //
 // Measured.  Choosing: 131072 rows of 8 KV heads 20 us (4 MB: some 2 us each for the
 // load, a digit's counts and their exchange, twice, the masks and the writing), 4608 rows
-// 8, 32 sequences of up to 16384 22.  Moving: those 32 to 2000 rows each 70 us, for 291 MB
+// 8, 32 sequences of up to 16384 22 (of 16384 each 25).  These have tables as long as the longest sequence; keys
+// are held in shared memory for what a table can hold: with tables of 131072 rows 64 sequences of
+// 2000 take 23.6 where tables of 2048 take 16.8, and 32 of 16384 33.5 where 24.7.
+// Moving: those 32 to 2000 rows each 70 us, for 291 MB
 // of sectors read (a row in five stays, in sectors that it shares with others) and 115
-// written, 0.88 of the copy rate; 131072 rows of E4M3 heads of 64 to 16384 18.7, in place 29; 4608 to 4096 4.8 and 9.
+// written, 0.86 of the copy rate (91 MB reach memory within the kernel), in place 79; 131072 rows of E4M3 heads of 64 to 16384 18.8,
+// in place 29; 4608 to 4096 4.8 and 9.  A cache with page bounds has them renewed behind the
+// move, by a warp for each row that a sequence may keep, of which one a page has work: 250 us more for the 32.
 #include "kvq_cluster.cuh"
 #include "kvq_paged.cuh"
 
