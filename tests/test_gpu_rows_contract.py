@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from quantized_kv_cache_08_gb300 import _binding as B
 from quantized_kv_cache_08_gb300.cache import PagedKVCache, verify
 from tests.kvq_testutil import need_gpu
 from tests.paged_testutil import PagedPair
@@ -56,6 +57,32 @@ def test_room_for_scores_is_what_a_call_can_use(fmt, D, hpk, max_t, queries):
         for b in range(2):
             near(scores_of(p, b), np.zeros(gain[b].shape), gain[b], 1.0)
     assert p.dev.device_error() == 0
+
+
+def test_caches_of_one_stream_share_the_room():
+    """Two caches with one buffer for kept scores, their calls by turns: scores as with one each."""
+    need_gpu()
+    n, Hkv, D, page, mp, T = 5, 2, 128, 16, 80, 2
+    g = torch.Generator().manual_seed(11)
+    tab = torch.randperm(n * mp, generator=g).view(n, mp).int().cuda()
+    lens = i32([1280, 1, 700, 16, 999])
+    k = [torch.randn(n, 1280, Hkv, D, generator=g).cuda() for _ in range(2)]
+    q = [torch.randn(n, T, 4 * Hkv, D, generator=g).cuda() for _ in range(2)]
+    got = []
+    for shared in (False, True):
+        c = [PagedKVCache(n * mp, page, Hkv, D, 4 * Hkv, max_seqs=n, max_pages=mp, max_t=T, scores=True, score_scratch=not shared) for _ in range(2)]
+        room = torch.empty(n * mp * page * Hkv * 4 * T, device="cuda")
+        for x, y in zip(c, k):
+            x.append(y, y, tab, i32([1280] * n))
+            if shared:
+                B.kvq_paged_set_score_scratch(x.handle, room.data_ptr(), 4 * T)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for x, y in zip(c, q):
+                x.decode_scored(y, tab, lens)
+        got.append([x.scores.clone() for x in c])
+        assert all(x.device_error() == 0 for x in c)
+    assert all(torch.equal(x, y) for x, y in zip(*got))
 
 
 # ------------------------------------------------------------------ eviction
